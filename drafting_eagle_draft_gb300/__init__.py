@@ -38,11 +38,14 @@ EXPORTS = ("peagle_create", "peagle_draft", "peagle_catch_up", "peagle_verify_gr
            "peagle_set_timing", "peagle_read_timing", "peagle_read_pass_trace",
            "peagle_set_wait_limit", "peagle_set_pass_kernel",
            "peagle_decode_attention_static",
+           "peagle_append_kv_quant", "peagle_read_kv_quant",
+           "peagle_decode_attention_quant", "peagle_decode_attention_quant_workspace",
            "peagle_device_error_bits", "peagle_strerror", "peagle_destroy")
 STAGES = ("fc", "qkv", "attn", "oproj", "gate_up", "down", "lm_head", "norm", "small")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 
 
 class PeagleDims(ctypes.Structure):
@@ -75,6 +78,17 @@ class PeagleGrads(ctypes.Structure):
 
 class PeagleKV(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("capacity", _i32), ("batch", _i32)]
+
+
+class PeagleKVQuant(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("errors", _vp)] + \
+               [(n, _i32) for n in ("n_layers", "batch", "n_kv_heads", "capacity", "head_dim",
+                                    "block")]
+
+
+class PeagleKVRows(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("layer_stride", _i64), ("batch_stride", _i64),
+                ("token_stride", _i64), ("head_stride", _i64), ("dtype", _i32)]
 
 
 _LIB = None
@@ -116,6 +130,16 @@ def lib():
         L.peagle_set_pass_kernel.argtypes = [_vp, _i32]
         L.peagle_decode_attention_static.argtypes = [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
                                                      _i32, _vp, _vp, _vp]
+        L.peagle_append_kv_quant.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32, _i32, _vp, _vp,
+                                             _i32, ctypes.POINTER(PeagleKVRows), _i32, _i32, _vp]
+        L.peagle_read_kv_quant.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32, _i32, _vp, _vp,
+                                           ctypes.POINTER(PeagleKVRows), _i32, _vp]
+        L.peagle_decode_attention_quant.argtypes = [
+            ctypes.POINTER(PeagleKVQuant), _i32, _i32, _i32, _i32, _vp, _i32, _i64, _vp, _i32,
+            _i32, ctypes.c_float, _vp, _vp, _vp, _i64, _vp]
+        L.peagle_decode_attention_quant_workspace.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32,
+                                                              _i32, _i32]
+        L.peagle_decode_attention_quant_workspace.restype = _i64
         L.peagle_read_timing.argtypes = [_vp, _vp, _vp]
         L.peagle_read_pass_trace.argtypes = [_vp, _vp, _i32, _vp, _vp]
         L.peagle_read_pass_trace.restype = _i32
@@ -386,6 +410,157 @@ def peagle_decode_attention_static(batch, K, n_q_heads, n_kv_heads, head_dim, q,
                                                 _ptr(k_cache), _ptr(v_cache), int(capacity),
                                                 _ptr(seq_lens), _ptr(out), _stream_ptr(stream)),
            "peagle_decode_attention_static")
+
+
+def _refuse(what, why):
+    raise PeagleError(PEAGLE_ERR_INVALID, f"{what}: {why}")
+
+
+def _on(t, dev, dtype, what):
+    """The device pointer of a CUDA tensor on `dev` with the given type (else INVALID)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != dev:
+        _refuse(what, f"a tensor of {dtype} on {dev} is wanted, got {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
+    """PeagleKVQuant over the tensors of an 8-bit cache: k, v float8_e4m3fn (or uint8)
+    [n_layers, batch, n_kv_heads, capacity, head_dim], k_scale, v_scale float32
+    [n_layers, batch, n_kv_heads, capacity / block], errors an int32 tensor of one element or
+    None.  All contiguous and on one CUDA device; the struct keeps them alive."""
+    import torch
+
+    what = "kv_quant_struct"
+    if k.dim() != 5 or k_scale.dim() != 4 or not k_scale.shape[3] or \
+            k.shape[3] % k_scale.shape[3] or k.shape[:3] != k_scale.shape[:3]:
+        _refuse(what, f"codes {tuple(k.shape)} and scales {tuple(k_scale.shape)} do not fit")
+    for t, like, kinds in ((k, k, (torch.float8_e4m3fn, torch.uint8)),
+                           (v, k, (torch.float8_e4m3fn, torch.uint8)),
+                           (k_scale, k_scale, (torch.float32,)),
+                           (v_scale, k_scale, (torch.float32,))):
+        if t.dtype not in kinds or t.shape != like.shape or t.device != k.device or \
+                not t.is_contiguous():
+            _refuse(what, "contiguous codes in 8 bits and float32 scales of equal shapes on one "
+                          "device are wanted")
+    if errors is not None and (errors.numel() < 1 or not errors.is_contiguous()):
+        _refuse(what, "errors is one int32")
+    L, B, H, cap, hd = k.shape
+    st = PeagleKVQuant(k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+                       errors=_on(errors, k.device, torch.int32, what), n_layers=L, batch=B,
+                       n_kv_heads=H, capacity=cap, head_dim=hd, block=cap // k_scale.shape[3])
+    st._keep = (k, v, k_scale, v_scale, errors)
+    st._device = k.device
+    return st
+
+
+def _quant_call(kv, what, stream):
+    """The cache's device, which has to be the current CUDA device, and the stream."""
+    import torch
+
+    dev = kv._device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(what, f"the cache is on {dev}, which is not the current CUDA device")
+    if stream is None:
+        return dev, torch.cuda.current_stream().cuda_stream
+    return dev, _stream_ptr(stream)
+
+
+def _kv_rows(kv, layer, batch, k, v, n_max, dev, what, written):
+    """PeagleKVRows of k / v [n_layers, batch, n_max, n_kv_heads, head_dim] (layer >= 0: without
+    the first axis): float32 or bfloat16, any strides with the last axis contiguous."""
+    import torch
+
+    lead = (kv.n_layers,) if layer < 0 else ()
+    dt = k.dtype
+    if dt != torch.float32 and dt != torch.bfloat16:
+        _refuse(what, f"rows are float32 or bfloat16, got {dt}")
+    sh, sd = k.shape, k.stride()
+    if len(sh) != len(lead) + 4 or sh[:-4] != lead or sh[-4] < batch or sh[-3] < n_max or \
+            sh[-2] != kv.n_kv_heads or sh[-1] != kv.head_dim or v.shape != sh or \
+            v.stride() != sd or sd[-1] != 1:
+        _refuse(what, f"rows {tuple(sh)} / {tuple(v.shape)} (strides {sd} / {v.stride()}) do not "
+                      f"fit layer {layer}, batch {batch}, n_max {n_max}")
+    if written and any(n > 1 and s == 0 for n, s in zip(sh, sd)):
+        _refuse(what, "the rows to be written overlap")
+    return PeagleKVRows(k=_on(k, dev, dt, what), v=_on(v, dev, dt, what),
+                        layer_stride=sd[0] if lead else 0, batch_stride=sd[-4],
+                        token_stride=sd[-3], head_stride=sd[-2],
+                        dtype=PEAGLE_F32 if dt == torch.float32 else PEAGLE_BF16)
+
+
+def _lens(t, batch, dev, what):
+    import torch
+
+    if t is None:
+        return None
+    if t.numel() < batch or not t.is_contiguous():
+        _refuse(what, f"{batch} contiguous int32 are wanted")
+    return _on(t, dev, torch.int32, what)
+
+
+def peagle_append_kv_quant(kv: PeagleKVQuant, batch, seq_lens, n_commit, k_rows, v_rows, n_max,
+                           layer=-1, n_extra=0, advance=True, stream=None):
+    """Quantise rows into the 8-bit cache (include/peagle.h).  k_rows / v_rows: float32 or
+    bfloat16 [n_layers, batch, >= n_max, n_kv_heads, head_dim] (layer >= 0: without the first
+    axis), any strides with the last axis contiguous."""
+    what = "peagle_append_kv_quant"
+    dev, s = _quant_call(kv, what, stream)
+    rows = _kv_rows(kv, layer, batch, k_rows, v_rows, n_max, dev, what, False)
+    _check(lib().peagle_append_kv_quant(kv, layer, batch, _lens(seq_lens, batch, dev, what),
+                                        _lens(n_commit, batch, dev, what), n_extra, rows, n_max,
+                                        1 if advance else 0, s), what)
+
+
+def peagle_read_kv_quant(kv: PeagleKVQuant, batch, counts, out_k, out_v, n_max, layer=-1,
+                         starts=None, stream=None):
+    """Read slots of the 8-bit cache back into rows laid out like peagle_append_kv_quant's
+    (include/peagle.h)."""
+    what = "peagle_read_kv_quant"
+    dev, s = _quant_call(kv, what, stream)
+    rows = _kv_rows(kv, layer, batch, out_k, out_v, n_max, dev, what, True)
+    _check(lib().peagle_read_kv_quant(kv, layer, batch, _lens(starts, batch, dev, what),
+                                      _lens(counts, batch, dev, what), rows, n_max, s), what)
+
+
+def peagle_decode_attention_quant_workspace(kv: PeagleKVQuant, batch, K, n_q_heads) -> int:
+    """Bytes of workspace of peagle_decode_attention_quant (include/peagle.h)."""
+    n = lib().peagle_decode_attention_quant_workspace(kv, batch, K, n_q_heads)
+    if n < 0:
+        raise PeagleError(n, "peagle_decode_attention_quant_workspace")
+    return n
+
+
+def peagle_decode_attention_quant(kv: PeagleKVQuant, layer, batch, K, n_q_heads, q, seq_lens, out,
+                                  workspace, out_lse=None, causal=True, window=0, scale=None,
+                                  stream=None):
+    """Decode attention over one layer of the 8-bit cache (include/peagle.h).  q, out: float32 or
+    bfloat16 [batch * K, n_q_heads, head_dim], rows of q any stride; workspace: a contiguous
+    CUDA tensor; scale: 1 / sqrt(head_dim) when None."""
+    import torch
+
+    what = "peagle_decode_attention_quant"
+    dev, s = _quant_call(kv, what, stream)
+    hd, dt = kv.head_dim, q.dtype
+    shape = (batch * K, n_q_heads, hd)
+    if dt != torch.float32 and dt != torch.bfloat16:
+        _refuse(what, f"queries are float32 or bfloat16, got {dt}")
+    sd = q.stride()
+    if q.shape != shape or out.shape != shape or sd[2] != 1 or (n_q_heads > 1 and sd[1] != hd) or \
+            not out.is_contiguous() or (batch * K > 1 and sd[0] < n_q_heads * hd):
+        _refuse(what, f"q and out are {shape}, q's rows contiguous, out contiguous")
+    if out_lse is not None and (out_lse.shape != shape[:2] or not out_lse.is_contiguous()):
+        _refuse(what, f"out_lse is {shape[:2]}, contiguous")
+    if not workspace.is_contiguous() or workspace.device != dev:
+        _refuse(what, f"a contiguous workspace on {dev} is wanted")
+    _check(lib().peagle_decode_attention_quant(
+        kv, layer, batch, K, n_q_heads, _on(q, dev, dt, what),
+        PEAGLE_F32 if dt == torch.float32 else PEAGLE_BF16, sd[0] if batch * K > 1 else 0,
+        _lens(seq_lens, batch, dev, what), 1 if causal else 0, window,
+        hd ** -0.5 if scale is None else scale, _on(out, dev, dt, what),
+        _on(out_lse, dev, torch.float32, what), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s), what)
 
 
 def peagle_device_error_bits(ctx: Context) -> int:

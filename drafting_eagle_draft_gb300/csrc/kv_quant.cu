@@ -1,0 +1,344 @@
+// Writing and reading the 8-bit KV cache: peagle_append_kv_quant and peagle_read_kv_quant.
+//
+// The cache commit is part of every speculative round ("P-EAGLE: A Technical Deep Dive into
+// Parallel Speculative Decoding", section "Technical Architecture"); the 8-bit form with a
+// scale per block of slots is this library's.
+#include "kv_quant.cuh"
+
+namespace peagle {
+namespace kvq {
+
+struct RowsArgs {
+  char* k;
+  char* v;
+  int64_t layer, batch, token, head;  // strides in elements
+};
+
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int* errors;
+  int batch, heads, capacity;
+  int layer0;
+};
+
+// Row counts of a request and whether they fit; raises the error bits when `report`.
+__device__ __forceinline__ bool rows_fit(int at, int64_t n, int n_max, int capacity,
+                                         int* errors, bool report) {
+  if (n < 0 || n > n_max) {
+    if (report) raise_error(errors, PEAGLE_DEV_BAD_COMMIT);
+    return false;
+  }
+  if (at < 0 || at > capacity - n) {
+    if (report) raise_error(errors, PEAGLE_DEV_KV_OVERFLOW);
+    return false;
+  }
+  return true;
+}
+
+// 16 consecutive row elements as fp32 (16-byte aligned by the host's checks).
+__device__ __forceinline__ void load16(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+  }
+}
+__device__ __forceinline__ void load16(const bf16* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+// A CTA encodes one block of slots of one (layer, request, kv head), keys or values.
+//
+//   s = 2^e, the smallest with amax <= 448 s over the block's live values (448 = 1.75 x 2^8, so
+//   e = E - 8 for amax = 1.m x 2^E with 1.m <= 1.75, else E - 7);  code = round(x / s)
+//
+// Each thread holds 16 consecutive elements of one slot in registers: one pass over the rows
+// (two or four 16-byte loads), a maximum over the CTA, one 16-byte store.  Scaling by a power
+// of two is exact, so the only rounding is the conversion to e4m3; the committed slots of the
+// first block are read back (16 codes a thread) and stored again only if their scale changed.
+// Heads run fastest over the grid: the rows of one token lie side by side.
+template <int HD, int BLOCK, typename T>
+__global__ void __launch_bounds__(BLOCK* HD / 16)
+    append_quant_kernel(CacheArgs c, RowsArgs rows, const int* seq_lens, const int* n_commit,
+                        int n_extra, int n_max) {
+  pdl_enter();
+  constexpr int THREADS = BLOCK * HD / 16, WARPS = THREADS / 32;
+  __shared__ unsigned red[WARPS];
+  const int h = blockIdx.x % c.heads, rest = blockIdx.x / c.heads;
+  const bool value = rest & 1;
+  const int b = blockIdx.y, l = blockIdx.z;
+  const int at = seq_lens[b];
+  const int64_t n = (int64_t)(n_commit ? n_commit[b] : 0) + n_extra;
+  if (!rows_fit(at, n, n_max, c.capacity, c.errors,
+                blockIdx.x == 0 && l == 0 && threadIdx.x == 0))
+    return;
+  const int block = at / BLOCK + (rest >> 1);
+  if (n == 0 || (int64_t)block * BLOCK >= at + n) return;
+
+  const int t = threadIdx.x / (HD / 16), d = threadIdx.x % (HD / 16) * 16;
+  const int slot = block * BLOCK + t;
+  const bool old = slot < at, fresh = !old && slot < at + n;
+  const int64_t unit = ((int64_t)(c.layer0 + l) * c.batch + b) * c.heads + h;
+  uint8_t* code = (value ? c.v : c.k) + (unit * c.capacity + slot) * HD + d;
+  float* scale = (value ? c.v_scale : c.k_scale) + unit * (c.capacity / BLOCK) + block;
+
+  float x[16];
+  float was = 0.f;
+  if (fresh) {
+    const T* src = reinterpret_cast<const T*>(value ? rows.v : rows.k) + l * rows.layer +
+                   b * rows.batch + (int64_t)(slot - at) * rows.token + h * rows.head + d;
+    load16(src, x);
+  } else if (old) {
+    was = *scale;
+    const uint4 u = *reinterpret_cast<const uint4*>(code);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = cvt_e4m3x2_f32x2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+      x[2 * i] = f.x * was, x[2 * i + 1] = f.y * was;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+  }
+
+  // the largest finite magnitude, as bits (their order is the magnitudes' order)
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const unsigned m = __float_as_uint(x[i]) & 0x7fffffffu;
+    top = max(top, m < 0x7f800000u ? m : 0u);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) top = max(top, red[i]);
+
+  // adding 0x1fffff carries into the exponent when the fraction is above 1.75's
+  int e = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
+  e = top ? min(max(e, -40), 120) : 0;
+  const float s = __uint_as_float((unsigned)(127 + e) << 23);
+  const float inv = __uint_as_float((unsigned)(127 - e) << 23);
+  if (fresh || (old && s != was)) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = x[4 * i + j];
+        // (the conversion saturates: an infinity would become 448)
+        y[j] = fabsf(v) == INFINITY ? NAN : v * inv;
+      }
+      w[i] = (uint32_t)cvt_f32x2_e4m3x2(y[0], y[1]) | (uint32_t)cvt_f32x2_e4m3x2(y[2], y[3]) << 16;
+    }
+    *reinterpret_cast<uint4*>(code) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (threadIdx.x == 0) *scale = s;
+}
+
+__global__ void __launch_bounds__(256)
+    advance_kernel(int batch, int* seq_lens, const int* n_commit, int n_extra, int n_max,
+                   int capacity) {
+  pdl_enter();
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= batch) return;
+  const int at = seq_lens[b];
+  const int64_t n = (int64_t)(n_commit ? n_commit[b] : 0) + n_extra;
+  if (rows_fit(at, n, n_max, capacity, nullptr, false)) seq_lens[b] = at + (int)n;
+}
+
+// 16 bytes of row elements from 16 / sizeof(T) codes (packed, low byte first).
+__device__ __forceinline__ uint4 decode(const uint2 c, float s, const bf16*) {
+  uint32_t r[4];
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = cvt_e4m3x2_f32x2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f.x * s, f.y * s);
+    r[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ uint4 decode(const uint32_t c, float s, const float*) {
+  const float2 a = cvt_e4m3x2_f32x2((uint16_t)c), b = cvt_e4m3x2_f32x2((uint16_t)(c >> 16));
+  return make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s),
+                    __float_as_uint(b.y * s));
+}
+
+template <typename T>
+struct Codes;
+template <>
+struct Codes<bf16> {
+  typedef uint2 type;
+};
+template <>
+struct Codes<float> {
+  typedef uint32_t type;
+};
+
+constexpr int READ_THREADS = 256, READ_UNROLL = 4;
+
+// A CTA reads READ_THREADS x READ_UNROLL pieces of one (layer, request, kv head), keys or
+// values: a piece is 16 bytes of row elements, so every store is a full one and consecutive
+// threads' loads and stores are consecutive.
+template <int HD, typename T>
+__global__ void __launch_bounds__(READ_THREADS)
+    read_quant_kernel(CacheArgs c, RowsArgs rows, int block_shift, const int* starts,
+                      const int* counts, int n_max) {
+  pdl_enter();
+  typedef typename Codes<T>::type Code;
+  constexpr int E = 16 / sizeof(T), PER_ROW = HD / E;
+  const int h = blockIdx.x % c.heads, rest = blockIdx.x / c.heads;
+  const bool value = rest & 1;
+  const int b = blockIdx.y, l = blockIdx.z;
+  const int at = starts ? starts[b] : 0, n = counts[b];
+  if (!rows_fit(at, n, n_max, c.capacity, c.errors,
+                blockIdx.x == 0 && l == 0 && threadIdx.x == 0))
+    return;
+  const int64_t unit = ((int64_t)(c.layer0 + l) * c.batch + b) * c.heads + h;
+  const uint8_t* code = (value ? c.v : c.k) + (unit * c.capacity + at) * HD;
+  const float* scale = (value ? c.v_scale : c.k_scale) + unit * (c.capacity >> block_shift);
+  T* out = reinterpret_cast<T*>(value ? rows.v : rows.k) + l * rows.layer + b * rows.batch +
+           h * rows.head;
+  const int64_t first = (int64_t)(rest >> 1) * (READ_THREADS * READ_UNROLL) + threadIdx.x;
+  const int64_t end = (int64_t)n * PER_ROW;
+  Code got[READ_UNROLL];
+  float s[READ_UNROLL];
+#pragma unroll
+  for (int i = 0; i < READ_UNROLL; ++i) {
+    const int64_t p = first + i * READ_THREADS;
+    if (p < end) {
+      got[i] = __ldg(reinterpret_cast<const Code*>(code) + p);
+      s[i] = __ldg(scale + ((at + (int)(p / PER_ROW)) >> block_shift));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < READ_UNROLL; ++i) {
+    const int64_t p = first + i * READ_THREADS;
+    if (p < end)
+      *reinterpret_cast<uint4*>(out + (p / PER_ROW) * rows.token + (p % PER_ROW) * E) =
+          decode(got[i], s[i], (const T*)nullptr);
+  }
+}
+
+static int check_rows(const peagle_kv_rows* r) {
+  if (!r || !r->k || !r->v) return PEAGLE_ERR_INVALID;
+  if (r->dtype != PEAGLE_F32 && r->dtype != PEAGLE_BF16) return PEAGLE_ERR_UNSUPPORTED;
+  const int64_t e = r->dtype == PEAGLE_F32 ? 4 : 8;
+  if (!aligned(r->k, 16) || !aligned(r->v, 16) || r->layer_stride % e || r->batch_stride % e ||
+      r->token_stride % e || r->head_stride % e)
+    return PEAGLE_ERR_INVALID;
+  return PEAGLE_OK;
+}
+
+static CacheArgs cache_args(const peagle_kv_quant* kv, int layer) {
+  CacheArgs c;
+  c.k = (uint8_t*)kv->k, c.v = (uint8_t*)kv->v;
+  c.k_scale = kv->k_scale, c.v_scale = kv->v_scale, c.errors = kv->errors;
+  c.batch = kv->batch, c.heads = kv->n_kv_heads, c.capacity = kv->capacity;
+  c.layer0 = layer < 0 ? 0 : layer;
+  return c;
+}
+
+static RowsArgs rows_args(const peagle_kv_rows* r) {
+  return RowsArgs{(char*)r->k, (char*)r->v, r->layer_stride, r->batch_stride, r->token_stride,
+                  r->head_stride};
+}
+
+template <int HD, int BLOCK>
+static cudaError_t launch_append(int dtype, dim3 grid, cudaStream_t s, const CacheArgs& c,
+                                 const RowsArgs& r, const int* seq_lens, const int* n_commit,
+                                 int n_extra, int n_max) {
+  const dim3 threads(BLOCK * HD / 16);
+  return dtype == PEAGLE_F32
+             ? launch_pdl(append_quant_kernel<HD, BLOCK, float>, grid, threads, 0, s, c, r,
+                          seq_lens, n_commit, n_extra, n_max)
+             : launch_pdl(append_quant_kernel<HD, BLOCK, bf16>, grid, threads, 0, s, c, r,
+                          seq_lens, n_commit, n_extra, n_max);
+}
+
+}  // namespace kvq
+}  // namespace peagle
+
+using namespace peagle;
+using namespace peagle::kvq;
+
+extern "C" int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                                      int32_t* seq_lens, const int32_t* n_commit, int32_t n_extra,
+                                      const peagle_kv_rows* rows, int32_t n_max, int32_t advance,
+                                      void* stream) {
+  int rc = check_cache(kv, layer, batch);
+  if (rc != PEAGLE_OK) return rc;
+  rc = check_rows(rows);
+  if (rc != PEAGLE_OK) return rc;
+  if (!seq_lens || seq_lens == n_commit || n_max < 1 || n_max > (1 << 30) || n_extra < -n_max ||
+      n_extra > n_max || (advance != 0 && advance != 1))
+    return PEAGLE_ERR_INVALID;
+  cudaStream_t s = (cudaStream_t)stream;
+  // the blocks that n_max rows can touch, wherever the first of them starts
+  const int64_t blocks = ((int64_t)n_max + kv->block - 2) / kv->block + 1;
+  const int64_t gx = blocks * 2 * kv->n_kv_heads;
+  if (gx > INT32_MAX) return PEAGLE_ERR_INVALID;
+  const dim3 grid((unsigned)gx, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
+  const CacheArgs c = cache_args(kv, layer);
+  const RowsArgs r = rows_args(rows);
+  cudaError_t e = cudaErrorInvalidValue;
+#define PEAGLE_APPEND(HD, BLOCK)                                                          \
+  if (kv->head_dim == HD && kv->block == BLOCK)                                           \
+    e = launch_append<HD, BLOCK>(rows->dtype, grid, s, c, r, seq_lens, n_commit, n_extra, \
+                                 n_max);
+  PEAGLE_APPEND(64, 16)
+  PEAGLE_APPEND(64, 32)
+  PEAGLE_APPEND(64, 64)
+  PEAGLE_APPEND(64, 128)
+  PEAGLE_APPEND(128, 16)
+  PEAGLE_APPEND(128, 32)
+  PEAGLE_APPEND(128, 64)
+  PEAGLE_APPEND(128, 128)
+#undef PEAGLE_APPEND
+  if (e == cudaSuccess && advance)
+    e = launch_pdl(advance_kernel, dim3((unsigned)cdiv(batch, 256)), dim3(256), 0, s, batch,
+                   seq_lens, n_commit, n_extra, n_max, kv->capacity);
+  return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+extern "C" int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                                    const int32_t* starts, const int32_t* counts,
+                                    const peagle_kv_rows* out, int32_t n_max, void* stream) {
+  int rc = check_cache(kv, layer, batch);
+  if (rc != PEAGLE_OK) return rc;
+  rc = check_rows(out);
+  if (rc != PEAGLE_OK) return rc;
+  if (!counts || n_max < 1 || n_max > (1 << 30)) return PEAGLE_ERR_INVALID;
+  const bool f32 = out->dtype == PEAGLE_F32;
+  const int64_t pieces = (int64_t)n_max * kv->head_dim / (f32 ? 4 : 8);
+  const int64_t per = READ_THREADS * READ_UNROLL;
+  const int64_t gx = (pieces + per - 1) / per * 2 * kv->n_kv_heads;
+  if (gx > INT32_MAX) return PEAGLE_ERR_INVALID;
+  const dim3 grid((unsigned)gx, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
+  const CacheArgs c = cache_args(kv, layer);
+  const RowsArgs r = rows_args(out);
+  const int shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
+  auto launch = [&](void (*kernel)(CacheArgs, RowsArgs, int, const int*, const int*, int)) {
+    return launch_pdl(kernel, grid, dim3(READ_THREADS), 0, (cudaStream_t)stream, c, r, shift,
+                      starts, counts, n_max);
+  };
+  const cudaError_t e = kv->head_dim == 64
+                            ? launch(f32 ? read_quant_kernel<64, float> : read_quant_kernel<64, bf16>)
+                            : launch(f32 ? read_quant_kernel<128, float> : read_quant_kernel<128, bf16>);
+  return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}

@@ -410,6 +410,127 @@ int peagle_decode_attention_static(int32_t batch, int32_t K, int32_t n_q_heads,
                                    const void* k_cache, const void* v_cache, int32_t capacity,
                                    const int32_t* seq_lens, float* out, void* stream);
 
+/* Drafter KV cache in 8 bits (device, caller-owned).  The pages keep the drafter's cache in
+ * the weights' type ("P-EAGLE: A Technical Deep Dive into Parallel Speculative Decoding",
+ * section "Technical Architecture"); this form of it, for long contexts, many requests and
+ * parked ones, is the library's own.  A slot's value is code x scale: e4m3 codes, and one
+ * fp32 scale for each block of `block` slots of a (layer, request, kv head), keys and values
+ * each:
+ *   k, v              [n_layers][batch][n_kv_heads][capacity][head_dim], one byte an element
+ *   k_scale, v_scale  [n_layers][batch][n_kv_heads][capacity / block]
+ * Keys are stored after RoPE.  Request b's committed entries are slots 0 .. seq_lens[b]-1.
+ * peagle_append_kv_quant makes the scale of a block the smallest power of two s, within
+ * 2^-40 .. 2^120, with |x| <= 448 s for every finite live value x of the block (1 when they
+ * are all zero), so a value of a block whose largest is A is off by at most 2^-4 of itself or
+ * 2^-17.8 A (half the spacing of the smallest codes), whichever is more; the other calls take
+ * any positive finite scale.  NaN and infinite values are stored as NaN.  Codes and scales of
+ * slots that nothing was appended to are never used and need no initial value.
+ * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; block 16, 32, 64 or 128.
+ * capacity is a multiple of block; k and v are 16-byte aligned; n_layers and batch are at
+ * most 65535 (else PEAGLE_ERR_INVALID).
+ * The calls below need no context.  Errors that depend on device-resident values are OR-ed,
+ * as PEAGLE_DEV_* bits, into the device word `errors` (NULL: not reported), which the caller
+ * reads and clears. */
+typedef struct peagle_kv_quant {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* errors;
+  int32_t n_layers;
+  int32_t batch;
+  int32_t n_kv_heads;
+  int32_t capacity;
+  int32_t head_dim;
+  int32_t block;
+} peagle_kv_quant;
+
+/* Rows of keys and values in 16 or 32 bits (device): element d of request b's row t of kv
+ * head h of layer l is at k[l * layer_stride + b * batch_stride + t * token_stride +
+ * h * head_stride + d], v alike; strides count elements, any sign, multiples of 16 bytes;
+ * k and v are 16-byte aligned; dtype is a peagle_dtype.  The buffers of a peagle_kv are such
+ * rows (strides batch * nkv * capacity * hd, nkv * capacity * hd, hd, capacity * hd), so is
+ * the k_rows layout of peagle_append_kv. */
+typedef struct peagle_kv_rows {
+  void* k;
+  void* v;
+  int64_t layer_stride;
+  int64_t batch_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t dtype;
+} peagle_kv_rows;
+
+/* Quantise rows as they enter the 8-bit cache (the commit of peagle_append_kv, for this
+ * cache).  Request b's first n = n_commit[b] + n_extra rows (0 .. n_max; n_commit NULL counts
+ * as zeros) go to slots seq_lens[b] .. seq_lens[b] + n - 1.  Each block that they touch gets
+ * the scale of its live values, which are the new rows and, in the block that seq_lens[b]
+ * points into, the committed slots before it; those are encoded again when the scale changes
+ * (exactly, except for values that become smaller than the new scale's smallest codes).
+ * Slots from seq_lens[b] + n on keep their codes; what they held is dead once their block's
+ * scale has changed.
+ *   layer    the layer that `rows` holds (rows without a layer axis: layer_stride unused),
+ *            or -1: rows of every layer
+ *   rows     at least n_max rows a request are addressable; only the first n are read
+ *   advance  1: then set seq_lens[b] to seq_lens[b] + n (in place; n_commit is another
+ *            buffer); 0: leave it, for rows that may be dropped again (a draft block) or
+ *            for layers appended one by one
+ * A request with rows out of range (n outside 0 .. n_max: BAD_COMMIT; seq_lens[b] < 0 or
+ * seq_lens[b] + n > capacity: KV_OVERFLOW) is left unchanged. */
+int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                           int32_t* seq_lens, const int32_t* n_commit, int32_t n_extra,
+                           const peagle_kv_rows* rows, int32_t n_max, int32_t advance,
+                           void* stream);
+
+/* Read slots of the 8-bit cache back as 16- or 32-bit rows (a parked request that returns to
+ * a peagle_kv cache): row t of request b is slot starts[b] + t (starts NULL: 0), t <
+ * counts[b] (0 .. n_max); rows from counts[b] on are left as they are.  code x scale is
+ * rounded once to the rows' type (no rounding for the scales that peagle_append_kv_quant
+ * writes).  layer as above.  Rows of `out` do not overlap one another.  Out of range:
+ * counts[b] outside 0 .. n_max is BAD_COMMIT, starts[b] < 0 or starts[b] + counts[b] >
+ * capacity KV_OVERFLOW; that request's rows are left as they are. */
+int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                         const int32_t* starts, const int32_t* counts,
+                         const peagle_kv_rows* out, int32_t n_max, void* stream);
+
+/* Decode attention over the 8-bit cache, for one layer: for request b, draft row j (rows
+ * b*K + j) and query head h, softmax(scale q . k) . v over the slots of kv head
+ * h / (n_q_heads / n_kv_heads) that the row sees.
+ *   q, out    device [batch*K][n_q_heads][head_dim] of type dtype (peagle_dtype); consecutive
+ *             rows of q are q_stride elements apart (0: n_q_heads * head_dim), out is
+ *             contiguous; both 16-byte aligned, q_stride a multiple of 16 bytes.  q is taken
+ *             as already rotated.
+ *   seq_lens  device int32 [batch]
+ *   causal    1: row j sees the slots 0 .. seq_lens[b] + j (the draft block's rows are in the
+ *             cache, as after an append with advance = 0); 0: every row sees the slots
+ *             0 .. seq_lens[b] - 1 only
+ *   window    > 0: of those, only slots above seq_lens[b] + j - window; 0: all
+ *   scale     of the scores, finite (1 / sqrt(head_dim) as a rule)
+ *   out_lse   device fp32 [batch*K][n_q_heads]: the natural logarithm of the sum of
+ *             exp(scale q . k), by which the result joins with attention over other keys;
+ *             or NULL
+ *   workspace device memory of at least peagle_decode_attention_quant_workspace() bytes,
+ *             256-byte aligned, no initial value; calls that may overlap on the GPU (other
+ *             streams, graphs replayed at once) each have their own
+ * A row that sees no slot gives zeros (and -inf).  Values and scores of slots that a row does
+ * not see never reach it, NaN included.  fp32 accumulation, softmax and lse; bf16 queries
+ * enter exactly and softmax weights rounded to 11 bits, fp32 queries and their weights as
+ * two 11-bit parts (22 bits).  Results are the same on every call (no atomics).
+ * A request with seq_lens[b] < 0, or whose last row's slot is beyond the capacity, is
+ * skipped with KV_OVERFLOW; its rows are left as they are.
+ * Limits: K * n_q_heads / n_kv_heads <= 128 (else PEAGLE_ERR_UNSUPPORTED); a workspace that
+ * is too small is PEAGLE_ERR_CAPACITY. */
+int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                                  int32_t K, int32_t n_q_heads, const void* q, int32_t dtype,
+                                  int64_t q_stride, const int32_t* seq_lens, int32_t causal,
+                                  int32_t window, float scale, void* out, float* out_lse,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that peagle_decode_attention_quant needs for these sizes on the current
+ * device (for any layer, lengths and window), or a negative error. */
+int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant* kv, int32_t batch,
+                                                int32_t K, int32_t n_q_heads);
+
 /* Raw device error bits observed by the last peagle_status call. */
 int32_t peagle_device_error_bits(const peagle_ctx* ctx);
 
