@@ -3,12 +3,53 @@
 // The draft block's attention ("P-EAGLE: A Technical Deep Dive into Parallel Speculative
 // Decoding", section "2. The P-EAGLE Parallel Drafter": the K rows of a request attend over
 // the cache and the rows before them), reading codes and block scales.
+//
+// Mathematics.  With codes k, v and scales a, c of a slot's block, and everything in the log2
+// domain, s = (q . k) a scale log2(e), and
+//     out = sum_t 2^s_t c_t v_t / sum_t 2^s_t.
+// The kernel holds, for each row, a reference m and sums the weights w_t = 2^(s_t + log2 c_t - m):
+//     O = sum_t w_t v_t (codes, on the tensor cores),   l = sum_t w_t / c_t,   out = O / l,
+// so a value's scale rides in the exponential's argument and weights of quiet and loud blocks
+// alike lie where the tensor operand's 11 bits are.  m moves only when a weight would pass 2^LIM
+// (and O and l are scaled then), which after the first tiles is rare.  Sums and statistics are
+// fp32.
+//
+// Tensor work, all on m16n8k.. instructions with keys (then head dims) as the 16 rows and the
+// query rows as the 8 columns, because a decode batch has few query rows:
+//   S^T = K Q^T  bf16 queries are split exactly into two e4m3 parts (4 + 4 significant bits), so
+//                the codes enter as they are stored; e4m3 k32 instructions issue nearly twice as
+//                fast as f16 k16 ones (0.93 against 0.50 an SM and clock, measured) for twice the
+//                depth.  fp32 queries: two f16 parts, codes converted to f16 (exact).
+//   O^T = V^T P  f16: e4m3 would leave the weights 2^-9 of range.  A weight keeps 11 bits; for
+//                fp32 queries it is two f16 parts.
+// The contraction's order over head dims is free, so a lane takes 16 consecutive bytes of a
+// key for its K operand; the order of the output's head dims is free, so a lane takes 8 or 16
+// consecutive bytes of 4 keys for V^T and pairs them with byte permutes: no transposes in shared
+// memory.
+//
+// Work split.  A unit is a tile of 32 slots of one (request, kv head).  All units of the call,
+// in order, are cut into equal consecutive shares, one for each of CTAS CTAs (one an SM), so
+// ragged batches and single long requests fill the GPU alike.  Inside a CTA 8 / groups streams
+// of warps take the tiles of a (request, kv head) in turn (groups of warps share a stream's
+// tiles when there are more query rows than one warp's registers hold), each with its own
+// cp.async ring in shared memory that runs on across (request, kv head) boundaries.  At the end
+// of one its streams are joined in shared memory; one that lies whole in a CTA is written out,
+// pieces of one go to the workspace and the second kernel joins them.
 #include <math.h>
+
+#include <type_traits>
 
 #include "kv_quant.cuh"
 
 namespace peagle {
 namespace kvq {
+
+constexpr int CTAS = 152;      // GB300's SMs
+constexpr int WARPS = 8;
+constexpr int TILE = 32;       // slots a unit
+constexpr int MAX_ROWS = 128;  // query rows a kv head
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no slot
 
 struct AttnQuantArgs {
   const uint8_t* k;        // this layer's codes [batch slots][nkv][capacity][hd]
@@ -21,75 +62,964 @@ struct AttnQuantArgs {
   float* lse;
   const int* seq_lens;
   int* errors;
-  float* work;
-  int batch, K, nq, nkv, capacity, block_shift, causal, window;
-  float scale;
+  int4* desc;              // [CTAS]: request, kv head, last CTA of the piece chain (or -1)
+  float* work;             // [CTAS][2] slots of partial results
+  int batch, K, G, nkv, capacity, block_shift, causal, window;
+  int groups;              // warps that share a stream's tiles, each NT x 8 query rows
+  int stages;
+  float scale;             // of the scores, with log2(e)
 };
 
-// The slots [begin, end) that row j of a request of length len sees; empty when end <= begin.
-__device__ __forceinline__ void row_span(const AttnQuantArgs& a, int len, int j, int& begin,
-                                         int& end) {
-  end = a.causal ? len + j + 1 : len;
-  begin = a.window > 0 ? max(0, len + j - a.window + 1) : 0;
+// Slots [begin, end) that row j of a request of length len sees; empty when end <= begin.
+__device__ __forceinline__ int row_begin(const AttnQuantArgs& a, int len, int j) {
+  return a.window > 0 ? max(0, len + j - a.window + 1) : 0;
 }
-
+__device__ __forceinline__ int row_end(const AttnQuantArgs& a, int len, int j) {
+  return a.causal ? len + j + 1 : len;
+}
 __device__ __forceinline__ bool request_fits(const AttnQuantArgs& a, int len) {
   return len >= 0 && len <= a.capacity - (a.causal ? a.K : 0);
 }
+// Tiles [first, first + count) that some row of a request sees.
+__device__ __forceinline__ int request_tiles(const AttnQuantArgs& a, int len, int& first) {
+  first = 0;
+  if (!request_fits(a, len)) return 0;
+  const int lo = row_begin(a, len, 0), hi = row_end(a, len, a.K - 1);
+  if (hi <= lo) return 0;
+  first = lo / TILE;
+  return (hi + TILE - 1) / TILE - first;
+}
 
-// One warp per (request, draft row, query head); each lane keeps the running maximum, sum and
-// output of every 32nd slot.
-template <int HD, typename T>
-__global__ void __launch_bounds__(128) attn_quant_simple_kernel(AttnQuantArgs a) {
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most `pending` of the newest groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int pending) {
+  switch (pending) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+  }
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+  return v;
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of rows of HD bytes.  The chunks
+// of a 128-byte line are permuted by bits of the row so that both readers are free of bank
+// conflicts: a phase of the K operand's loads takes 4 chunks of rows 2i and 2i + 1, one of the
+// V operand's the same 2 chunks of rows 0, 2, 4, 6 (or 1, 3, 5, 7).
+template <int HD>
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
+  if (HD == 128) {
+    const int f = ((row ^ (row >> 2)) & 1) << 2 | (row & 2);
+    return (uint32_t)(row * 128 + ((chunk ^ f) << 4));
+  }
+  const int line = row >> 1;
+  return (uint32_t)(line * 128 + ((((row & 1) << 2 | chunk) ^ ((line & 3) << 1)) << 4));
+}
+
+// The exponent e of the smallest power of two with amax <= 448 2^e (amax as fp32 bits).
+__device__ __forceinline__ int e4m3_exponent(unsigned amax) {
+  const int e = (int)((amax + 0x1fffffu) >> 23) - 127 - 8;
+  return min(max(e, -100), 120);
+}
+__device__ __forceinline__ float power2(int e) {
+  return __uint_as_float((unsigned)(127 + e) << 23);
+}
+
+// Where a CTA's walk over the units stands: one (request, kv head).
+struct Segment {
+  int b, h, len;
+  int first_tile, tiles;
+  int at;  // of its first unit, relative to the CTA's share (negative: it began before)
+  __device__ __forceinline__ bool next(const AttnQuantArgs& a) {
+    at += tiles;
+    if (++h < a.nkv) return true;
+    h = 0;
+    do {
+      if (++b >= a.batch) return false;
+      len = a.seq_lens[b];
+      tiles = request_tiles(a, len, first_tile);
+    } while (!tiles);
+    return true;
+  }
+};
+
+// Query operands of one warp: NT x 8 rows of one (request, kv head), in registers.
+template <int HD, int NT, bool F32>
+struct Queries;
+
+template <int HD, int NT>
+struct Queries<HD, NT, false> {
+  static constexpr int STEPS = HD / 32;
+  uint32_t b[2][STEPS][NT][2];  // e4m3 parts, [part][k step][rows][register]
+  float scale[NT][2];           // of rows 2c and 2c + 1, with the scores' scale
+
+  __device__ __forceinline__ void load(const AttnQuantArgs& a, int req, int h, int row0,
+                                       int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + r;
+      float x[HD / 4];
+      unsigned top = 0;
+      if (row < a.K * a.G) {
+        const bf16* q = (const bf16*)a.q + ((int64_t)req * a.K + row / a.G) * a.q_stride +
+                        (int64_t)(h * a.G + row % a.G) * HD + 16 * c;
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + (i & 1) * 8));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool fine = top < 0x7f800000u;
+      const int e = fine ? e4m3_exponent(top) : 0;
+      const float inv = fine ? power2(-e) : 0.f;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float y0 = fine ? x[8 * s + 4 * i + 2 * j] * inv : 0.f;
+            const float y1 = fine ? x[8 * s + 4 * i + 2 * j + 1] * inv : 0.f;
+            const uint16_t p = cvt_f32x2_e4m3x2(y0, y1);
+            const float2 f = cvt_e4m3x2_f32x2(p);
+            hi |= (uint32_t)p << (16 * j);
+            lo |= (uint32_t)cvt_f32x2_e4m3x2(y0 - f.x, y1 - f.y) << (16 * j);
+          }
+          b[0][s][nt][i] = hi;
+          b[1][s][nt][i] = lo;
+        }
+      }
+      // a row that is not finite gives NaN
+      const float mine = fine ? power2(e) * a.scale : NAN;
+      scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+      scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+    }
+  }
+
+  // acc[nt] += the scores of 16 keys (rows 0 .. 15 from shared address k).  `off`: the lane's
+  // first chunk.
+  __device__ __forceinline__ void scores(float (*acc)[4], uint32_t k, uint32_t off) const {
+#pragma unroll
+    for (int half = 0; half < HD / 64; ++half) {
+      // (chunk c + 4 of a 128-byte row is chunk c with its bit 2 flipped)
+      const uint4 u = lds128(k + (off ^ (half * 64)));
+      const uint4 w = lds128(k + (off ^ (half * 64)) + 8 * HD);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_e4m3(acc[nt], u.x, w.x, u.y, w.y, b[p][2 * half][nt][0], b[p][2 * half][nt][1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_e4m3(acc[nt], u.z, w.z, u.w, w.w, b[p][2 * half + 1][nt][0],
+                   b[p][2 * half + 1][nt][1]);
+      }
+    }
+  }
+};
+
+template <int HD, int NT>
+struct Queries<HD, NT, true> {
+  static constexpr int STEPS = HD / 16;
+  uint32_t b[2][STEPS][NT][2];  // f16 parts
+  float scale[NT][2];
+
+  __device__ __forceinline__ void load(const AttnQuantArgs& a, int req, int h, int row0,
+                                       int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + r;
+      float x[HD / 4];
+      unsigned top = 0;
+      if (row < a.K * a.G) {
+        const float* q = (const float*)a.q + ((int64_t)req * a.K + row / a.G) * a.q_stride +
+                         (int64_t)(h * a.G + row % a.G) * HD + 16 * c;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(q + (i >> 2) * 64 + (i & 3) * 4));
+          x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool fine = top < 0x7f800000u;
+      // the largest element to 2^14 .. 2^15: the second part's last bit is then 2^-38 of it
+      const int e = fine ? min(max((int)(top >> 23) - 127 - 14, -100), 120) : 0;
+      const float inv = fine ? power2(-e) : 0.f;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float y0 = fine ? x[4 * s + 2 * i] * inv : 0.f;
+          const float y1 = fine ? x[4 * s + 2 * i + 1] * inv : 0.f;
+          const uint32_t hi = pack_f16(y0, y1);
+          const float2 f = unpack_f16(hi);
+          b[0][s][nt][i] = hi;
+          b[1][s][nt][i] = pack_f16(y0 - f.x, y1 - f.y);
+        }
+      }
+      const float mine = fine ? power2(e) * a.scale : NAN;
+      scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
+      scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+    }
+  }
+
+  __device__ __forceinline__ void scores(float (*acc)[4], uint32_t k, uint32_t off) const {
+#pragma unroll
+    for (int half = 0; half < HD / 64; ++half) {
+      const uint4 u4 = lds128(k + (off ^ (half * 64)));
+      const uint4 w4 = lds128(k + (off ^ (half * 64)) + 8 * HD);
+      const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t a0 = cvt_e4m3x2_f16x2((uint16_t)u[s]);
+        const uint32_t a2 = cvt_e4m3x2_f16x2((uint16_t)(u[s] >> 16));
+        const uint32_t a1 = cvt_e4m3x2_f16x2((uint16_t)w[s]);
+        const uint32_t a3 = cvt_e4m3x2_f16x2((uint16_t)(w[s] >> 16));
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(acc[nt], a0, a1, a2, a3, b[p][4 * half + s][nt][0], b[p][4 * half + s][nt][1]);
+      }
+    }
+  }
+};
+
+// NaN codes of a word: 0x80 in each such byte.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// One warp's running result over a (request, kv head): NT x 8 query rows.  O^T's fragment: head
+// dim r HD / 8 + 2 i (elements 0, 1) and the next one (2, 3), rows 2c (0, 2) and 2c + 1 (1, 3).
+template <int HD, int NT, bool F32>
+struct Running {
+  // 2^SHIFT is where the largest weight is put, 2^LIM what it may grow to (f16 ends at 2^16):
+  // far up, because weights below 2^-14 lose bits of their 11.  The second part of an fp32
+  // weight needs that range most.
+  static constexpr float SHIFT = F32 ? 13.f : 6.f, LIM = F32 ? 15.f : 14.f;
+  float o[HD / 16][NT][4];
+  float m[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = NO_REF;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.f;
+    }
+  }
+
+  // A tile of 32 slots from `slot` on.  edge: some row does not see some of it.
+  __device__ __forceinline__ void tile(const AttnQuantArgs& a, const Queries<HD, NT, F32>& q,
+                                       uint32_t k, uint32_t v, uint32_t scales, int slot,
+                                       bool edge, int len, int row0, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const uint32_t k_off = tile_offset<HD>(r, c);
+    float acc[2][NT][4];
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[sub][nt][j] = 0.f;
+      q.scores(acc[sub], k + sub * 16 * HD, k_off);
+    }
+    const uint4 sc = lds128(scales);
+    const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+    // (a half without any slot to see was filled with zeros)
+    const float vs[2] = {sc.z ? __uint_as_float(sc.z) : 1.f, sc.w ? __uint_as_float(sc.w) : 1.f};
+    const float lv[2] = {lg2(vs[0]), lg2(vs[1])};
+    unsigned seen = ~0u;  // bit (sub * NT + nt) * 4 + j: element j's slot is seen by its row
+    static_assert(2 * NT * 4 <= 32, "one bit an element");
+    if (edge) {
+      seen = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = min((row0 + nt * 8 + 2 * c + e) / a.G, a.K - 1);
+          const int lo = row_begin(a, len, j), hi = row_end(a, len, j);
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int t = slot + sub * 16 + y * 8 + r;
+              if (t >= lo && t < hi) seen |= 1u << ((sub * NT + nt) * 4 + 2 * y + e);
+            }
+        }
+      }
+    }
+    float x[2][NT][4];
+    bool again = true;
+    while (true) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f0 = q.scale[nt][0] * ks[sub], f1 = q.scale[nt][1] * ks[sub];
+          const float g0 = lv[sub] - m[nt][0], g1 = lv[sub] - m[nt][1];
+          float* w = x[sub][nt];
+          const float* s = acc[sub][nt];
+          w[0] = fmaf(s[0], f0, g0), w[1] = fmaf(s[1], f1, g1);
+          w[2] = fmaf(s[2], f0, g0), w[3] = fmaf(s[3], f1, g1);
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!(seen >> ((sub * NT + nt) * 4 + j) & 1)) w[j] = -INFINITY;
+          }
+          top = max3(top, w[0], w[1]);
+          top = max3(top, w[2], w[3]);
+        }
+      }
+      // (NaN passes no comparison: it reaches the weights as it is)
+      if (!again || !__any_sync(0xffffffffu, top > LIM)) break;
+      again = false;
+      raise(q, acc, ks, lv, seen);
+    }
+    const float rv[2] = {rcp(vs[0]), rcp(vs[1])};
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      uint32_t p[F32 ? 2 : 1][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* w = x[sub][nt];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = ex2(w[j]);
+        l[nt][0] = fmaf(w[0] + w[2], rv[sub], l[nt][0]);
+        l[nt][1] = fmaf(w[1] + w[3], rv[sub], l[nt][1]);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t hi = pack_f16(w[2 * y], w[2 * y + 1]);
+          p[0][nt][y] = transpose8(hi);
+          if (F32) {
+            const float2 f = unpack_f16(hi);
+            p[F32 ? 1 : 0][nt][y] = transpose8(pack_f16(w[2 * y] - f.x, w[2 * y + 1] - f.y));
+          }
+        }
+      }
+      values(p, v + sub * 16 * HD, edge, seen >> (sub * NT * 4), lane);
+    }
+  }
+
+  // Moves the references of the rows that a tile's scores pass, and scales what was summed.
+  __device__ __forceinline__ void raise(const Queries<HD, NT, F32>& q, float (*acc)[NT][4],
+                                        const float* ks, const float* lv, unsigned seen) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (seen >> ((sub * NT + nt) * 4 + 2 * y + e) & 1)
+              top = fmaxf(top, fmaf(acc[sub][nt][2 * y + e], q.scale[nt][e] * ks[sub], lv[sub]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float to = top - m[nt][e] > LIM ? top - SHIFT : m[nt][e];
+        const float f = ex2(m[nt][e] - to);
+        if (to != m[nt][e]) {
+          l[nt][e] *= f;
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) o[i][nt][e] *= f, o[i][nt][2 + e] *= f;
+          m[nt][e] = to;
+        }
+      }
+    }
+  }
+
+  // O^T += V^T P over 16 slots (rows 0 .. 15 from shared address v).
+  __device__ __forceinline__ void values(const uint32_t (*p)[NT][2], uint32_t v, bool edge,
+                                         unsigned seen, int lane) {
+    constexpr int WORDS = HD / 32;  // of a lane's bytes of one slot
+    const int r = lane >> 2, c = lane & 3;
+    uint32_t w[4][WORDS];  // slots 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int row = 2 * c + (s & 1);  // (8 rows further on the chunks are permuted alike)
+      if (HD == 128) {
+        const uint4 u = lds128(v + tile_offset<HD>(row, r) + (s >> 1) * 8 * HD);
+        w[s][0] = u.x, w[s][1] = u.y, w[s][WORDS - 2] = u.z, w[s][WORDS - 1] = u.w;
+      } else {
+        const uint2 u = lds64(v + tile_offset<HD>(row, r >> 1) + (r & 1) * 8 + (s >> 1) * 8 * HD);
+        w[s][0] = u.x, w[s][1] = u.y;
+      }
+    }
+    if (edge) {
+      // A slot that only some rows see may hold NaN; a zero weight does not keep it out of the
+      // other rows.  Its codes are cleared, and the rows that see it are made NaN by a product
+      // of the two 0 / 1 matrices "is NaN" and "is seen".
+      uint32_t bad = 0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) bad |= nan_codes(w[s][j]);
+      if (__any_sync(0xffffffffu, bad)) {
+        uint32_t one[4][WORDS];  // e4m3 1.0 where a code is NaN
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < WORDS; ++j) {
+            const uint32_t n = nan_codes(w[s][j]) >> 7;
+            one[s][j] = n * 0x38u;
+            w[s][j] &= ~(n * 0xffu);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const unsigned bits = seen >> (nt * 4);
+          const uint32_t b0 = transpose8((bits & 1 ? 0x3c00u : 0u) | (bits & 2 ? 0x3c000000u : 0u));
+          const uint32_t b1 = transpose8((bits & 4 ? 0x3c00u : 0u) | (bits & 8 ? 0x3c000000u : 0u));
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            float n[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t x[4];
+            operand(one, i, x);
+            mma_f16(n, x[0], x[1], x[2], x[3], b0, b1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n[j] > 0.f) o[i][nt][j] = NAN;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i) {
+      uint32_t x[4];
+      operand(w, i, x);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(o[i][nt], x[0], x[1], x[2], x[3], p[0][nt][0], p[0][nt][1]);
+        if (F32)
+          mma_f16(o[i][nt], x[0], x[1], x[2], x[3], p[F32 ? 1 : 0][nt][0], p[F32 ? 1 : 0][nt][1]);
+      }
+    }
+  }
+
+  // The V^T operand of head dims r HD / 8 + 2 i, + 1 from a lane's bytes of its four slots.
+  __device__ __forceinline__ static void operand(const uint32_t (*w)[HD / 32], int i,
+                                                 uint32_t* x) {
+    const unsigned sel = i & 1 ? 0x7362u : 0x5140u;  // bytes of two slots, side by side
+    const uint32_t a = __byte_perm(w[0][i >> 1], w[1][i >> 1], sel);
+    const uint32_t b = __byte_perm(w[2][i >> 1], w[3][i >> 1], sel);
+    x[0] = cvt_e4m3x2_f16x2((uint16_t)a), x[1] = cvt_e4m3x2_f16x2((uint16_t)(a >> 16));
+    x[2] = cvt_e4m3x2_f16x2((uint16_t)b), x[3] = cvt_e4m3x2_f16x2((uint16_t)(b >> 16));
+  }
+};
+
+// Two values of a row at consecutive head dims.
+__device__ __forceinline__ void store2(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+__device__ __forceinline__ void store2(bf16* p, float x, float y) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+}
+
+// A row's result: its address in out, whether the row exists, and 1 / l (0 for a row that has
+// seen nothing); writes its lse when `first`.
+template <typename T>
+__device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int h, int row,
+                                         float m, float l, bool first, float& inv) {
+  const bool none = m == NO_REF && l == 0.f;  // (a row of NaN scores has no reference either)
+  inv = none ? 0.f : 1.f / l;
+  const int64_t at = ((int64_t)req * a.K + row / a.G) * ((int64_t)a.nkv * a.G) + h * a.G + row % a.G;
+  if (first && a.lse) a.lse[at] = none ? -INFINITY : (m + log2f(l)) * LN2;
+  return (T*)a.out + at * hd;
+}
+
+// Sum over the CTA's threads of v before this one, and over all of them.
+__device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) red[wid] = x;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    const long long s = red[i];
+    if (i < wid) before += s;
+    total += s;
+  }
+  return before + x - v;
+}
+
+template <int HD, int NT, bool F32>
+__global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs a) {
+  typedef typename std::conditional<F32, float, bf16>::type T;
+  constexpr int STAGE = 2 * TILE * HD + 16;       // K, V, four scales
+  constexpr int FRAG = HD / 16 * NT * 4 * 32;     // floats of a warp's O^T
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long red[WARPS];
+  __shared__ long long found[2];
+  __shared__ int found_b;
+  __shared__ float row_m[WARPS][NT * 8], row_l[WARPS][NT * 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = a.groups, streams = WARPS / groups;
+  const int stream = warp / groups, group = warp % groups;
+  const int row0 = group * NT * 8;
   pdl_enter();
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= a.K * a.nq) return;
-  const int j = item / a.nq, h = item % a.nq, g = h / (a.nq / a.nkv);
-  const int len = a.seq_lens[b];
-  if (!request_fits(a, len)) {
-    if (item == 0 && lane == 0) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
-    return;
-  }
-  int begin, end;
-  row_span(a, len, j, begin, end);
-  const int64_t unit = (int64_t)b * a.nkv + g;
-  const int64_t row = (int64_t)b * a.K + j;
-  const T* q = (const T*)a.q + row * a.q_stride + (int64_t)h * HD;
-  float m = -INFINITY, sum = 0.f, o[HD];
-#pragma unroll
-  for (int d = 0; d < HD; ++d) o[d] = 0.f;
-  for (int t = begin + lane; t < end; t += 32) {
-    const uint8_t* k = a.k + (unit * a.capacity + t) * HD;
-    const uint8_t* v = a.v + (unit * a.capacity + t) * HD;
-    const int64_t at = unit * (a.capacity >> a.block_shift) + (t >> a.block_shift);
-    float x = 0.f;
-    for (int d = 0; d < HD; d += 2) {
-      const float2 f = cvt_e4m3x2_f32x2(*(const uint16_t*)(k + d));
-      x += ld(q + d) * f.x + ld(q + d + 1) * f.y;
+
+  // this CTA's share of the units, and the (request, kv head) in which it begins
+  Segment seg;
+  int n;  // units of the share
+  long long total = 0, share, lo;
+  {
+    long long units = 0, before = 0;
+    int first;
+    for (int b0 = 0; b0 < a.batch; b0 += WARPS * 32) {
+      const int b = b0 + threadIdx.x;
+      units = 0;
+      if (b < a.batch) {
+        const int len = a.seq_lens[b];
+        units = (long long)request_tiles(a, len, first) * a.nkv;
+        if (blockIdx.x == 0 && !request_fits(a, len)) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
+      }
+      long long part;
+      before = block_scan(units, red, part);
+      total += part;
     }
-    x *= a.k_scale[at] * a.scale;
-    const float top = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.f : expf(m - top), p = expf(x - top);
-    m = top;
-    sum = sum * keep + p;
-    const float w = p * a.v_scale[at];
-    for (int d = 0; d < HD; d += 2) {
-      const float2 f = cvt_e4m3x2_f32x2(*(const uint16_t*)(v + d));
-      o[d] = o[d] * keep + w * f.x;
-      o[d + 1] = o[d + 1] * keep + w * f.y;
+    share = (total + CTAS - 1) / CTAS;
+    // a share below 4 tiles leaves warps idle and makes pieces to join
+    share = share < 4 ? 4 : share;
+    lo = share * blockIdx.x;
+    if (lo >= total) {
+      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    n = (int)(total - lo < share ? total - lo : share);
+    long long base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += WARPS * 32) {
+      if (a.batch > WARPS * 32) {
+        const int b = b0 + threadIdx.x;
+        units = b < a.batch ? (long long)request_tiles(a, a.seq_lens[b], first) * a.nkv : 0;
+        long long part;
+        before = base + block_scan(units, red, part);
+        base += part;
+      }
+      if (units && lo >= before && lo < before + units) {
+        found[0] = before;
+        found_b = b0 + threadIdx.x;
+      }
+    }
+    __syncthreads();
+    seg.b = found_b;
+    seg.len = a.seq_lens[seg.b];
+    seg.tiles = request_tiles(a, seg.len, seg.first_tile);
+    const long long in = lo - found[0];
+    seg.h = (int)(in / seg.tiles);
+    seg.at = -(int)(in % seg.tiles);
+  }
+
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) +
+                        (uint32_t)(stream * a.stages) * STAGE;
+  float* joined = reinterpret_cast<float*>(smem + (size_t)streams * a.stages * STAGE);
+
+  // the stream's loads run ahead of its products, over (request, kv head) boundaries
+  Segment next = seg;
+  int next_u = max(next.at, 0) + stream, slot_in = 0;
+  bool more = true;
+  auto issue = [&]() {
+    while (more && next_u >= min(next.at + next.tiles, n)) {
+      more = next.at + next.tiles < n && next.next(a);
+      next_u = max(next.at, 0) + stream;
+    }
+    if (more) {
+      const int lo_slot = row_begin(a, next.len, 0), hi_slot = row_end(a, next.len, a.K - 1);
+      const int slot = (next.first_tile + next_u - next.at) * TILE;
+      const int64_t unit = (int64_t)next.b * a.nkv + next.h;
+      const uint8_t* k = a.k + (unit * a.capacity + slot) * HD;
+      const uint8_t* v = a.v + (unit * a.capacity + slot) * HD;
+      const uint32_t to = ring + slot_in * STAGE;
+      constexpr int CHUNKS = TILE * HD / 16;
+      const int step = 32 * groups;
+      for (int i = group * 32 + lane; i < CHUNKS; i += step) {
+        const int row = i / (HD / 16), t = slot + row;
+        const uint32_t off = tile_offset<HD>(row, i % (HD / 16));
+        const bool in = t >= lo_slot && t < hi_slot;
+        cp_async16(to + off, in ? k + i * 16 : a.k, in ? 16 : 0);
+        cp_async16(to + TILE * HD + off, in ? v + i * 16 : a.v, in ? 16 : 0);
+      }
+      if (group == 0 && lane < 4) {
+        const int t = slot + (lane & 1) * 16;
+        const bool in = t + 16 > lo_slot && t < hi_slot;
+        const float* s = (lane < 2 ? a.k_scale : a.v_scale) +
+                         unit * (a.capacity >> a.block_shift) + (t >> a.block_shift);
+        cp_async4(to + 2 * TILE * HD + lane * 4, in ? s : a.k_scale, in ? 4 : 0);
+      }
+      next_u += streams;
+    }
+    cp_async_commit();
+    if (++slot_in == a.stages) slot_in = 0;
+  };
+  for (int i = 0; i < a.stages - 1; ++i) issue();
+
+  Queries<HD, NT, F32> q;
+  Running<HD, NT, F32> run;
+  int slot_out = 0;
+  bool chained = false;
+  while (true) {
+    const int begin = max(seg.at, 0), end = min(seg.at + seg.tiles, n);
+    const int all_begin = row_begin(a, seg.len, a.K - 1), all_end = row_end(a, seg.len, 0);
+    q.load(a, seg.b, seg.h, row0, lane);
+    run.clear();
+    for (int u = begin + stream; u < end; u += streams) {
+      cp_async_wait(a.stages - 2);
+      if (groups > 1)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "r"(32 * groups) : "memory");
+      else
+        __syncwarp();
+      issue();
+      const uint32_t at = ring + slot_out * STAGE;
+      const int slot = (seg.first_tile + u - seg.at) * TILE;
+      const bool edge = slot < all_begin || slot + TILE > all_end;
+      run.tile(a, q, at, at + TILE * HD, at + 2 * TILE * HD, slot, edge, seg.len, row0, lane);
+      if (++slot_out == a.stages) slot_out = 0;
+    }
+
+    // join the streams: a common reference for every row, then their sums
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+          run.l[nt][e] += __shfl_xor_sync(0xffffffffu, run.l[nt][e], d);
+        if (r == 0) row_m[warp][nt * 8 + 2 * c + e] = run.m[nt][e];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = NO_REF;
+        for (int s = 0; s < streams; ++s)
+          top = fmaxf(top, row_m[s * groups + group][nt * 8 + 2 * c + e]);
+        const float f = ex2(run.m[nt][e] - top);
+        run.m[nt][e] = top;
+        run.l[nt][e] *= f;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) run.o[i][nt][e] *= f, run.o[i][nt][2 + e] *= f;
+        if (r == 0) row_l[warp][nt * 8 + 2 * c + e] = run.l[nt][e];
+      }
+    // two streams at a time add theirs to streams 0 and 1, then 1 to 0
+    for (int s = streams; s > 1;) {
+      const int give = s > 2 ? 2 : 1, from = s - give;
+      float4* buf = reinterpret_cast<float4*>(joined) +
+                    (size_t)((stream >= from ? stream - from : stream) * groups + group) * (FRAG / 4);
+      if (stream >= from && stream < s) {
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            buf[(i * NT + nt) * 32 + lane] = make_float4(run.o[i][nt][0], run.o[i][nt][1],
+                                                         run.o[i][nt][2], run.o[i][nt][3]);
+      }
+      __syncthreads();
+      if (stream < give) {
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float4 f = buf[(i * NT + nt) * 32 + lane];
+            run.o[i][nt][0] += f.x, run.o[i][nt][1] += f.y;
+            run.o[i][nt][2] += f.z, run.o[i][nt][3] += f.w;
+          }
+      }
+      s = from;
+      if (s > 1) __syncthreads();
+    }
+    if (streams == 1) __syncthreads();
+
+    if (stream == 0) {
+      const bool began = seg.at >= 0, ended = seg.at + seg.tiles <= n;
+      float* slot = a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
+                                 ((size_t)groups * NT * 8 * (HD + 2));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float inv[2];
+        T* out[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = row0 + nt * 8 + 2 * c + e;
+          float l = 0.f;
+          for (int s = 0; s < streams; ++s) l += row_l[s * groups + group][nt * 8 + 2 * c + e];
+          out[e] = nullptr;
+          if (began && ended) {
+            if (row < a.K * a.G)
+              out[e] = finish_row<T>(a, HD, seg.b, seg.h, row, run.m[nt][e], l, r == 0, inv[e]);
+          } else if (r == 0) {
+            slot[2 * row] = run.m[nt][e];
+            slot[2 * row + 1] = l;
+          }
+        }
+        if (began && ended) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (out[e])
+#pragma unroll
+              for (int i = 0; i < HD / 16; ++i)
+                store2(out[e] + r * (HD / 8) + 2 * i, run.o[i][nt][e] * inv[e],
+                       run.o[i][nt][2 + e] * inv[e]);
+        } else {
+          float4* o = reinterpret_cast<float4*>(slot + (size_t)groups * NT * 16);
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i)
+            o[((group * NT + nt) * (HD / 16) + i) * 32 + lane] =
+                make_float4(run.o[i][nt][0], run.o[i][nt][1], run.o[i][nt][2], run.o[i][nt][3]);
+        }
+      }
+      if (began && !ended) {
+        chained = true;
+        if (warp == 0 && lane == 0)
+          a.desc[blockIdx.x] =
+              make_int4(seg.b, seg.h, (int)((lo + seg.at + seg.tiles - 1) / share), 0);
+      }
+    }
+    if (seg.at + seg.tiles >= n) break;
+    seg.next(a);
+    __syncthreads();  // row_m, row_l and the joining buffers are free again
+  }
+  if (warp == 0 && lane == 0 && !chained) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  cp_async_wait(0);
+}
+
+// Joins the pieces of the (request, kv head)s that several CTAs worked on: block (c, z) takes the
+// one whose first piece CTA c holds, a warp 32 fragments of it (ntiles x HD / 16 of them in
+// all, cut into gridDim.y = HD / 16 parts) over a part of the pieces.  Also writes the rows of requests
+// that no row of which sees a slot.
+template <int HD, typename T>
+__global__ void __launch_bounds__(WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a, int ntiles) {
+  pdl_enter();
+  __shared__ float4 red_o[WARPS][32];
+  __shared__ float red_m[WARPS][8], red_l[WARPS][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.y == 0) {
+    for (int b = blockIdx.x; b < a.batch; b += CTAS) {
+      const int len = a.seq_lens[b];
+      int first;
+      if (!request_fits(a, len) || request_tiles(a, len, first)) continue;
+      const int64_t rows = (int64_t)a.K * a.nkv * a.G;
+      T* out = (T*)a.out + b * rows * HD;
+      for (int64_t i = threadIdx.x; i < rows * HD; i += WARPS * 32) st(out + i, 0.f);
+      if (a.lse)
+        for (int64_t i = threadIdx.x; i < rows; i += WARPS * 32) a.lse[b * rows + i] = -INFINITY;
     }
   }
-  const float top = warp_max(m);
-  const float f = m == -INFINITY ? 0.f : expf(m - top);
-  const float total = warp_sum(sum * f);
-  T* out = (T*)a.out + (row * a.nq + h) * HD;
-#pragma unroll
-  for (int d = 0; d < HD; ++d) {
-    const float x = warp_sum(o[d] * f);
-    if (lane == (d & 31)) st(out + d, end > begin ? x / total : 0.f);
+  const int4 d = a.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const int cols = ntiles * (HD / 16), per = cols / gridDim.y;  // 32 fragments each
+  const int parts = max(1, WARPS / per);                        // warps that share one
+  const int pieces = d.z - (int)blockIdx.x + 1;
+  const size_t slot = (size_t)ntiles * 8 * (HD + 2);
+  const int r = lane >> 2, c = lane & 3;
+  auto piece = [&](int p) {
+    return a.work + ((size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * slot;
+  };
+  for (int at = warp / parts; at < per; at += WARPS / parts) {
+    const int col = blockIdx.y * per + at, nt = col / (HD / 16), i = col % (HD / 16);
+    const int row = nt * 8 + 2 * c, part = warp % parts;
+    float m0 = NO_REF, m1 = NO_REF;
+#pragma unroll 4
+    for (int p = part; p < pieces; p += parts) {
+      const float4 f = *reinterpret_cast<const float4*>(piece(p) + 2 * row);
+      m0 = fmaxf(m0, f.x), m1 = fmaxf(m1, f.z);
+    }
+    float l0 = 0.f, l1 = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = part; p < pieces; p += parts) {
+      const float* s = piece(p);
+      const float4 f = *reinterpret_cast<const float4*>(s + 2 * row);
+      const float4 g = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
+      const float f0 = ex2(f.x - m0), f1 = ex2(f.z - m1);
+      l0 = fmaf(f.y, f0, l0), l1 = fmaf(f.w, f1, l1);
+      o.x = fmaf(g.x, f0, o.x), o.y = fmaf(g.y, f1, o.y);
+      o.z = fmaf(g.z, f0, o.z), o.w = fmaf(g.w, f1, o.w);
+    }
+    if (parts > 1) {
+      // (per <= WARPS / parts: every warp is in this loop once, or not at all)
+      red_o[warp][lane] = o;
+      if (r == 0) {
+        red_m[warp][2 * c] = m0, red_m[warp][2 * c + 1] = m1;
+        red_l[warp][2 * c] = l0, red_l[warp][2 * c + 1] = l1;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / parts), "r"(32 * parts) : "memory");
+      if (part) continue;
+      const float n0 = m0, n1 = m1;
+      for (int w = 1; w < parts; ++w) {
+        m0 = fmaxf(m0, red_m[warp + w][2 * c]);
+        m1 = fmaxf(m1, red_m[warp + w][2 * c + 1]);
+      }
+      float f0 = ex2(n0 - m0), f1 = ex2(n1 - m1);
+      l0 *= f0, l1 *= f1;
+      o = make_float4(o.x * f0, o.y * f1, o.z * f0, o.w * f1);
+      for (int w = 1; w < parts; ++w) {
+        f0 = ex2(red_m[warp + w][2 * c] - m0), f1 = ex2(red_m[warp + w][2 * c + 1] - m1);
+        const float4 g = red_o[warp + w][lane];
+        l0 = fmaf(red_l[warp + w][2 * c], f0, l0), l1 = fmaf(red_l[warp + w][2 * c + 1], f1, l1);
+        o.x = fmaf(g.x, f0, o.x), o.y = fmaf(g.y, f1, o.y);
+        o.z = fmaf(g.z, f0, o.z), o.w = fmaf(g.w, f1, o.w);
+      }
+    }
+    float inv;
+    if (row < a.K * a.G) {
+      T* out = finish_row<T>(a, HD, d.x, d.y, row, m0, l0, i == 0 && r == 0, inv);
+      store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
+    }
+    if (row + 1 < a.K * a.G) {
+      T* out = finish_row<T>(a, HD, d.x, d.y, row + 1, m1, l1, i == 0 && r == 0, inv);
+      store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
+    }
   }
-  if (a.lse && lane == 0) a.lse[row * a.nq + h] = end > begin ? top + logf(total) : -INFINITY;
+}
+
+// How the query rows of a kv head are laid over warps: groups of warps x NT tiles of 8 rows.
+// A warp's registers hold the queries and the outputs of NT tiles: 24 NT registers for
+// head_dim 64 (32 NT with fp32 queries), 48 NT (64 NT) for 128.
+struct Plan {
+  int nt, groups;
+  int ntiles() const { return nt * groups; }
+};
+static Plan plan_of(int hd, bool f32, int rows) {
+  const int tiles = cdiv(rows, 8), most = hd == 64 ? 4 : f32 ? 2 : 3;
+  Plan p;
+  for (p.groups = 1; cdiv(tiles, p.groups) > most; p.groups *= 2) {
+  }
+  p.nt = cdiv(tiles, p.groups);
+  return p;
+}
+
+static size_t slot_bytes(int hd, int ntiles) { return (size_t)ntiles * 8 * (hd + 2) * sizeof(float); }
+static int64_t work_bytes(int hd, int ntiles) {
+  return 4096 + (int64_t)CTAS * 2 * (int64_t)slot_bytes(hd, ntiles);
+}
+
+template <int HD, int NT, bool F32>
+static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
+  constexpr size_t STAGE = 2 * TILE * HD + 16, FRAG = (size_t)HD / 16 * NT * 4 * 32 * sizeof(float);
+  const int streams = WARPS / p.groups;
+  const size_t join = streams > 1 ? (size_t)(streams > 2 ? 2 : 1) * p.groups * FRAG : 0;
+  // up to 8 stages a stream, within the 227 KB of a CTA less its static arrays
+  const size_t room = 220 * 1024 - join;
+  a.groups = p.groups;
+  a.stages = (int)(room / (streams * STAGE));
+  a.stages = a.stages > 8 ? 8 : a.stages;
+  const size_t smem = streams * a.stages * STAGE + join;
+  cudaError_t e = smem_optin((const void*)attn_quant_kernel<HD, NT, F32>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_quant_kernel<HD, NT, F32>, dim3(CTAS), dim3(WARPS * 32), smem, s, a);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(CTAS, HD / 16);
+  return launch_pdl(attn_quant_join_kernel<HD, typename std::conditional<F32, float, bf16>::type>,
+                    grid, dim3(WARPS * 32), 0, s, a, p.ntiles());
 }
 
 }  // namespace kvq
@@ -103,7 +1033,8 @@ static int check_attention(const peagle_kv_quant* kv, int32_t batch, int32_t K,
   const int rc = check_cache(kv, 0, batch);
   if (rc != PEAGLE_OK) return rc;
   if (K < 1 || n_q_heads < 1 || n_q_heads % kv->n_kv_heads) return PEAGLE_ERR_INVALID;
-  if (K > 128 || K * (int64_t)(n_q_heads / kv->n_kv_heads) > 128) return PEAGLE_ERR_UNSUPPORTED;
+  if (K > MAX_ROWS || K * (int64_t)(n_q_heads / kv->n_kv_heads) > MAX_ROWS)
+    return PEAGLE_ERR_UNSUPPORTED;
   return PEAGLE_OK;
 }
 
@@ -112,7 +1043,11 @@ extern "C" int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant
                                                            int32_t n_q_heads) {
   const int rc = check_attention(kv, batch, K, n_q_heads);
   if (rc != PEAGLE_OK) return rc;
-  return 256;
+  const int rows = K * (n_q_heads / kv->n_kv_heads);
+  // (the larger of the two query types' plans)
+  const int a = plan_of(kv->head_dim, false, rows).ntiles();
+  const int b = plan_of(kv->head_dim, true, rows).ntiles();
+  return work_bytes(kv->head_dim, a > b ? a : b);
 }
 
 extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t layer,
@@ -132,27 +1067,40 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
       q_stride % (dtype == PEAGLE_F32 ? 4 : 8))
     return PEAGLE_ERR_INVALID;
   if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
+  const int hd = kv->head_dim;
+  const bool f32 = dtype == PEAGLE_F32;
   const int64_t unit = (int64_t)layer * kv->batch * kv->n_kv_heads;
   AttnQuantArgs a;
-  a.k = (const uint8_t*)kv->k + unit * kv->capacity * kv->head_dim;
-  a.v = (const uint8_t*)kv->v + unit * kv->capacity * kv->head_dim;
+  a.k = (const uint8_t*)kv->k + unit * kv->capacity * hd;
+  a.v = (const uint8_t*)kv->v + unit * kv->capacity * hd;
   a.k_scale = kv->k_scale + unit * (kv->capacity / kv->block);
   a.v_scale = kv->v_scale + unit * (kv->capacity / kv->block);
   a.q = q;
-  a.q_stride = q_stride ? q_stride : (int64_t)n_q_heads * kv->head_dim;
+  a.q_stride = q_stride ? q_stride : (int64_t)n_q_heads * hd;
   a.out = out, a.lse = out_lse, a.seq_lens = seq_lens, a.errors = kv->errors;
-  a.work = (float*)workspace;
-  a.batch = batch, a.K = K, a.nq = n_q_heads, a.nkv = kv->n_kv_heads, a.capacity = kv->capacity;
+  a.desc = (int4*)workspace;
+  a.work = (float*)((char*)workspace + 4096);
+  a.batch = batch, a.K = K, a.G = n_q_heads / kv->n_kv_heads, a.nkv = kv->n_kv_heads;
+  a.capacity = kv->capacity;
   a.block_shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
-  a.causal = causal, a.window = window, a.scale = scale;
-  const dim3 grid((unsigned)cdiv(K * n_q_heads, 4), (unsigned)batch);
-  auto launch = [&](void (*kernel)(AttnQuantArgs)) {
-    return launch_pdl(kernel, grid, dim3(128), 0, (cudaStream_t)stream, a);
-  };
-  const bool f32 = dtype == PEAGLE_F32;
-  const cudaError_t e =
-      kv->head_dim == 64
-          ? launch(f32 ? attn_quant_simple_kernel<64, float> : attn_quant_simple_kernel<64, bf16>)
-          : launch(f32 ? attn_quant_simple_kernel<128, float> : attn_quant_simple_kernel<128, bf16>);
+  a.causal = causal, a.window = window, a.scale = scale * LOG2E;
+  const Plan p = plan_of(hd, f32, K * a.G);
+  cudaError_t e = cudaErrorInvalidValue;
+#define PEAGLE_ATTN(HD, NT, F32) \
+  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32>(a, p, (cudaStream_t)stream);
+  PEAGLE_ATTN(64, 1, false)
+  PEAGLE_ATTN(64, 2, false)
+  PEAGLE_ATTN(64, 3, false)
+  PEAGLE_ATTN(64, 4, false)
+  PEAGLE_ATTN(64, 1, true)
+  PEAGLE_ATTN(64, 2, true)
+  PEAGLE_ATTN(64, 3, true)
+  PEAGLE_ATTN(64, 4, true)
+  PEAGLE_ATTN(128, 1, false)
+  PEAGLE_ATTN(128, 2, false)
+  PEAGLE_ATTN(128, 3, false)
+  PEAGLE_ATTN(128, 1, true)
+  PEAGLE_ATTN(128, 2, true)
+#undef PEAGLE_ATTN
   return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }

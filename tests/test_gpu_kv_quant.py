@@ -254,7 +254,9 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
     u = 2^-24 is half an fp32 step.  A score is a product of hd terms summed in fp32 in any
     order: (hd + 8) u S with S = scale sum |q k|; fp32 queries come as two 11-bit parts, which
     drop 2^-22 of an element, or of 2^-2 of the row's largest where an element is that small:
-    2^-22 S + 2^-24 scale max|q| sum |k|.  A score's error d moves the weights by 2 d relative
+    2^-22 S + 2^-24 scale max|q| sum |k|; bf16 queries as two e4m3 parts, whose last spacing of
+    2^-9 (half of it dropped) is at most 2^-10 / 224 of the row's largest.
+    A score's error d moves the weights by 2 d relative
     (numerator and sum).  The exponential's argument carries u of its size (|x| < 2^8 before a
     weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to 11 bits
     (2^-12 relative; 2^-22 for the two parts of fp32) or, below the smallest f16, to half of
@@ -277,6 +279,8 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
             d = (hd + 8) * u * S
             if f32:
                 d += 2.0 ** -22 * S + u * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
+            else:
+                d += 2.0 ** -10 / 224 * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
             d += 2.0 ** -15 + 2.0 ** -21 + 4 * u * S
             w, tiny = (2.0 ** -22, 2.0 ** -36) if f32 else (2.0 ** -12, 2.0 ** -25)
             to[r, h] = absolute[r, h] * (2 * d + w + 2 * (n + 64) * u) + \
@@ -299,13 +303,12 @@ def attend(c, layer, q, lens, K, causal=True, window=0, scale=None, stream=None,
     return out, lse
 
 
-def check_attention(c, layer, q, lens, K, causal=True, window=0, scale=None):
-    out, lse = attend(c, layer, q, lens, K, causal, window, scale)
-    assert c.err() == 0
+def check_result(c, layer, q, lens, K, causal, window, scale, out, lse):
     dtype = "f32" if q.dtype == torch.float32 else "bf16"
     q64 = q.double().cpu().numpy()
+    B = len(lens)
     (kc, ks), (vc, vs) = c.host("k"), c.host("v")
-    kval, vval = Q.values(kc[layer], ks[layer], c.block), Q.values(vc[layer], vs[layer], c.block)
+    kval, vval = (Q.values(x[layer, :B], y[layer, :B], c.block) for x, y in ((kc, ks), (vc, vs)))
     sc = q.shape[2] ** -0.5 if scale is None else scale
     want, wl, ab = Q.attention(q64, kval, vval, lens, K, causal, window, sc)
     to, tl = bounds(q64, kval, vval, vs[layer].max(-1), lens, K, causal, window, sc, want, wl, ab,
@@ -317,8 +320,14 @@ def check_attention(c, layer, q, lens, K, causal=True, window=0, scale=None):
     worst = np.max(np.abs(got - want) / np.where(to > 0, to, 1))
     assert worst <= 1, f"out: {worst:.3f} of the bound"
     if not none.all():
-        worst = np.max(np.abs(gl - wl)[~none] / tl[~none])
+        worst = np.max(np.abs(gl[~none] - wl[~none]) / tl[~none])
         assert worst <= 1, f"lse: {worst:.3f} of the bound"
+
+
+def check_attention(c, layer, q, lens, K, causal=True, window=0, scale=None):
+    out, lse = attend(c, layer, q, lens, K, causal, window, scale)
+    assert c.err() == 0
+    check_result(c, layer, q, lens, K, causal, window, scale, out, lse)
     return out, lse
 
 
@@ -469,19 +478,22 @@ def test_attention_requests_out_of_range_and_strided_queries():
     lens = [5, -1, cap - K, cap - K + 1, 2 ** 31 - 1]
     out, lse = attend(c, 0, q, lens, K)
     assert c.err() == m.PEAGLE_DEV_KV_OVERFLOW
-    ref, rl = attend(c, 0, q[:3 * K].contiguous(), [5, 0, cap - K], K)
-    for b in (0, 2):
-        assert torch.equal(out[b * K:(b + 1) * K], ref[b * K:(b + 1) * K])
-        assert torch.equal(lse[b * K:(b + 1) * K], rl[b * K:(b + 1) * K])
+    for b, n in ((0, 5), (2, cap - K)):
+        one = slice(b * K, (b + 1) * K)
+        at = Cache.__new__(Cache)  # request b alone
+        at.block, at.t = c.block, {k: t[:, b:b + 1] for k, t in c.t.items()}
+        check_result(at, 0, q[one], [n], K, True, 0, None, out[one], lse[one])
     for b in (1, 3, 4):
         assert (out[b * K:(b + 1) * K] == -7.0).all() and (lse[b * K:(b + 1) * K] == -7.0).all()
     out, _ = attend(c, 0, q, [5, 1, 2, cap - K + 1, cap], K, causal=False)  # the prefix alone fits
     assert c.err() == 0 and (out != -7.0).any(-1).all()
-    # without lse the output is the same
+    # without lse the output is the same, and so it is with contiguous queries
+    lens = [5, 0, cap - K]
+    ref, _ = attend(c, 0, q[:3 * K].contiguous(), lens, K)
     o2 = torch.empty(3 * K, nq, hd, dtype=torch.bfloat16, device="cuda")
     w = torch.empty(m.peagle_decode_attention_quant_workspace(c.kv, 3, K, nq), dtype=torch.uint8,
                     device="cuda")
-    m.peagle_decode_attention_quant(c.kv, 0, 3, K, nq, q[:3 * K], ints([5, 0, cap - K]), o2, w)
+    m.peagle_decode_attention_quant(c.kv, 0, 3, K, nq, q[:3 * K], ints(lens), o2, w)
     assert torch.equal(o2, ref)
 
 
