@@ -14,14 +14,14 @@
 // (and O and l are scaled then), which after the first tiles is rare.  Sums and statistics are
 // fp32.
 //
-// Tensor work, all on m16n8k.. instructions with keys (then head dims) as the 16 rows and the
-// query rows as the 8 columns, because a decode batch has few query rows:
-//   S^T = K Q^T  bf16 queries are split exactly into two e4m3 parts (4 + 4 significant bits), so
-//                the codes enter as they are stored; e4m3 k32 instructions issue nearly twice as
-//                fast as f16 k16 ones (0.93 against 0.50 an SM and clock, measured) for twice the
-//                depth.  fp32 queries: two f16 parts, codes converted to f16 (exact).
-//   O^T = V^T P  f16: e4m3 would leave the weights 2^-9 of range.  A weight keeps 11 bits; for
-//                fp32 queries it is two f16 parts.
+// Tensor work: m16n8k16 with f16 operands, keys (then head dims) as the 16 rows and the query
+// rows as the 8 columns, because a decode batch has few query rows.  Codes become f16 exactly
+// (one conversion instruction for two); the e4m3 form of the instruction is no faster here, it
+// runs as conversions and f16 products (0.43 an SM and clock measured with changing operands,
+// for twice the depth of an f16 one at 0.48).
+//   S^T = K Q^T  bf16 queries, each row scaled by a power of two, are exact in f16; fp32 queries
+//                come as two f16 parts.
+//   O^T = V^T P  a weight keeps 11 bits; for fp32 queries it is two f16 parts.
 // The contraction's order over head dims is free, so a lane takes 16 consecutive bytes of a
 // key for its K operand; the order of the output's head dims is free, so a lane takes 8 or 16
 // consecutive bytes of 4 keys for V^T and pairs them with byte permutes: no transposes in shared
@@ -123,14 +123,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ void mma_e4m3(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -140,10 +132,20 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// The first product of a sum: zeros as C, which take no registers.
+__device__ __forceinline__ void mma_f16_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// (the remaining 4 - bytes are zeros)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
@@ -190,11 +192,6 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
   return (uint32_t)(line * 128 + ((((row & 1) << 2 | chunk) ^ ((line & 3) << 1)) << 4));
 }
 
-// The exponent e of the smallest power of two with amax <= 448 2^e (amax as fp32 bits).
-__device__ __forceinline__ int e4m3_exponent(unsigned amax) {
-  const int e = (int)((amax + 0x1fffffu) >> 23) - 127 - 8;
-  return min(max(e, -100), 120);
-}
 __device__ __forceinline__ float power2(int e) {
   return __uint_as_float((unsigned)(127 + e) << 23);
 }
@@ -217,150 +214,100 @@ struct Segment {
   }
 };
 
-// Query operands of one warp: NT x 8 rows of one (request, kv head), in registers.
+// Query operands.  prepare() makes the operands of one tile of 8 rows in shared memory (a warp;
+// the CTA's warps share the tiles of a (request, kv head)), load() takes NT tiles' into a warp's
+// registers, scores() multiplies 16 keys by them.
+// 16 consecutive query elements of a row at head dims 16c and, for head_dim 128, 64 + 16c;
+// the row's largest magnitude as bits.
+template <int HD, typename T>
+__device__ __forceinline__ unsigned load_query(const AttnQuantArgs& a, int req, int h, int row,
+                                               int c, float* x) {
+  unsigned top = 0;
+  if (row < a.K * a.G) {
+    const int j = row / a.G;
+    const T* q = (const T*)a.q + ((int64_t)req * a.K + j) * a.q_stride +
+                 (int64_t)(h * a.G + row - j * a.G) * HD + 16 * c;
+    constexpr int E = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < HD / 4 / E; ++i) {
+      const uint4 u =
+          __ldg(reinterpret_cast<const uint4*>(q + (i * E / 16) * 64 + i * E % 16));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (sizeof(T) == 2) {
+          x[E * i + 2 * k] = __uint_as_float(w[k] << 16);
+          x[E * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+          x[E * i + k] = __uint_as_float(w[k]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+}
+
 template <int HD, int NT, bool F32>
-struct Queries;
+struct Queries {
+  static constexpr int STEPS = HD / 16, PARTS = F32 ? 2 : 1;
+  static constexpr int TILE_BYTES = PARTS * STEPS * 32 * 8;
+  uint32_t b[PARTS][STEPS][NT][2];  // [part][k step][rows][register]
+  float scale[NT][2];               // of rows 2c and 2c + 1, with the scores' scale
 
-template <int HD, int NT>
-struct Queries<HD, NT, false> {
-  static constexpr int STEPS = HD / 32;
-  uint32_t b[2][STEPS][NT][2];  // e4m3 parts, [part][k step][rows][register]
-  float scale[NT][2];           // of rows 2c and 2c + 1, with the scores' scale
+  __device__ __forceinline__ static void prepare(const AttnQuantArgs& a, int req, int h, int tile,
+                                                 int lane, uint2* to, float* scales) {
+    float x[HD / 4];
+    typedef typename std::conditional<F32, float, bf16>::type T;
+    const unsigned top = load_query<HD, T>(a, req, h, tile * 8 + (lane >> 2), lane & 3, x);
+    const bool fine = top < 0x7f800000u;
+    // the largest element to 2^14 .. 2^15: f16's last bit is then 2^-38 of it
+    const int e = fine ? min(max((int)(top >> 23) - 127 - 14, -100), 120) : 0;
+    const float inv = power2(-e);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      uint32_t part[PARTS][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float y0 = x[4 * s + 2 * i] * inv, y1 = x[4 * s + 2 * i + 1] * inv;
+        part[0][i] = pack_f16(y0, y1);
+        const float2 f = unpack_f16(part[0][i]);
+        if (F32) part[PARTS - 1][i] = pack_f16(y0 - f.x, y1 - f.y);
+      }
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        to[(p * STEPS + s) * 32 + lane] = make_uint2(part[p][0], part[p][1]);
+    }
+    // a row that is not finite gives NaN
+    if ((lane & 3) == 0) scales[lane >> 2] = fine ? power2(e) * a.scale : NAN;
+  }
 
-  __device__ __forceinline__ void load(const AttnQuantArgs& a, int req, int h, int row0,
-                                       int lane) {
-    const int r = lane >> 2, c = lane & 3;
+  __device__ __forceinline__ void load(const uint2* from, const float* scales, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + r;
-      float x[HD / 4];
-      unsigned top = 0;
-      if (row < a.K * a.G) {
-        const bf16* q = (const bf16*)a.q + ((int64_t)req * a.K + row / a.G) * a.q_stride +
-                        (int64_t)(h * a.G + row % a.G) * HD + 16 * c;
 #pragma unroll
-        for (int i = 0; i < HD / 32; ++i) {
-          const uint4 u = __ldg(reinterpret_cast<const uint4*>(q + (i >> 1) * 64 + (i & 1) * 8));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-          }
+        for (int s = 0; s < STEPS; ++s) {
+          const uint2 u = from[nt * (TILE_BYTES / 8) + (p * STEPS + s) * 32 + lane];
+          b[p][s][nt][0] = u.x, b[p][s][nt][1] = u.y;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const bool fine = top < 0x7f800000u;
-      const int e = fine ? e4m3_exponent(top) : 0;
-      const float inv = fine ? power2(-e) : 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float y0 = fine ? x[8 * s + 4 * i + 2 * j] * inv : 0.f;
-            const float y1 = fine ? x[8 * s + 4 * i + 2 * j + 1] * inv : 0.f;
-            const uint16_t p = cvt_f32x2_e4m3x2(y0, y1);
-            const float2 f = cvt_e4m3x2_f32x2(p);
-            hi |= (uint32_t)p << (16 * j);
-            lo |= (uint32_t)cvt_f32x2_e4m3x2(y0 - f.x, y1 - f.y) << (16 * j);
-          }
-          b[0][s][nt][i] = hi;
-          b[1][s][nt][i] = lo;
-        }
-      }
-      // a row that is not finite gives NaN
-      const float mine = fine ? power2(e) * a.scale : NAN;
-      scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
-      scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+      const float2 f = reinterpret_cast<const float2*>(scales)[nt * 4 + (lane & 3)];
+      scale[nt][0] = f.x, scale[nt][1] = f.y;
     }
   }
 
-  // acc[nt] += the scores of 16 keys (rows 0 .. 15 from shared address k).  `off`: the lane's
+  // acc[nt] = the scores of 16 keys (rows 0 .. 15 from shared address k).  `off`: the lane's
   // first chunk.
   __device__ __forceinline__ void scores(float (*acc)[4], uint32_t k, uint32_t off) const {
 #pragma unroll
     for (int half = 0; half < HD / 64; ++half) {
       // (chunk c + 4 of a 128-byte row is chunk c with its bit 2 flipped)
-      const uint4 u = lds128(k + (off ^ (half * 64)));
-      const uint4 w = lds128(k + (off ^ (half * 64)) + 8 * HD);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_e4m3(acc[nt], u.x, w.x, u.y, w.y, b[p][2 * half][nt][0], b[p][2 * half][nt][1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_e4m3(acc[nt], u.z, w.z, u.w, w.w, b[p][2 * half + 1][nt][0],
-                   b[p][2 * half + 1][nt][1]);
-      }
-    }
-  }
-};
-
-template <int HD, int NT>
-struct Queries<HD, NT, true> {
-  static constexpr int STEPS = HD / 16;
-  uint32_t b[2][STEPS][NT][2];  // f16 parts
-  float scale[NT][2];
-
-  __device__ __forceinline__ void load(const AttnQuantArgs& a, int req, int h, int row0,
-                                       int lane) {
-    const int r = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + r;
-      float x[HD / 4];
-      unsigned top = 0;
-      if (row < a.K * a.G) {
-        const float* q = (const float*)a.q + ((int64_t)req * a.K + row / a.G) * a.q_stride +
-                         (int64_t)(h * a.G + row % a.G) * HD + 16 * c;
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(q + (i >> 2) * 64 + (i & 3) * 4));
-          x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const bool fine = top < 0x7f800000u;
-      // the largest element to 2^14 .. 2^15: the second part's last bit is then 2^-38 of it
-      const int e = fine ? min(max((int)(top >> 23) - 127 - 14, -100), 120) : 0;
-      const float inv = fine ? power2(-e) : 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float y0 = fine ? x[4 * s + 2 * i] * inv : 0.f;
-          const float y1 = fine ? x[4 * s + 2 * i + 1] * inv : 0.f;
-          const uint32_t hi = pack_f16(y0, y1);
-          const float2 f = unpack_f16(hi);
-          b[0][s][nt][i] = hi;
-          b[1][s][nt][i] = pack_f16(y0 - f.x, y1 - f.y);
-        }
-      }
-      const float mine = fine ? power2(e) * a.scale : NAN;
-      scale[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
-      scale[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
-    }
-  }
-
-  __device__ __forceinline__ void scores(float (*acc)[4], uint32_t k, uint32_t off) const {
-#pragma unroll
-    for (int half = 0; half < HD / 64; ++half) {
       const uint4 u4 = lds128(k + (off ^ (half * 64)));
       const uint4 w4 = lds128(k + (off ^ (half * 64)) + 8 * HD);
       const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -371,10 +318,15 @@ struct Queries<HD, NT, true> {
         const uint32_t a1 = cvt_e4m3x2_f16x2((uint16_t)w[s]);
         const uint32_t a3 = cvt_e4m3x2_f16x2((uint16_t)(w[s] >> 16));
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(acc[nt], a0, a1, a2, a3, b[p][4 * half + s][nt][0], b[p][4 * half + s][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (half == 0 && s == 0 && p == 0)
+              mma_f16_first(acc[nt], a0, a1, a2, a3, b[0][0][nt][0], b[0][0][nt][1]);
+            else
+              mma_f16(acc[nt], a0, a1, a2, a3, b[p][4 * half + s][nt][0],
+                      b[p][4 * half + s][nt][1]);
+          }
       }
     }
   }
@@ -389,17 +341,21 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 // dim r HD / 8 + 2 i (elements 0, 1) and the next one (2, 3), rows 2c (0, 2) and 2c + 1 (1, 3).
 template <int HD, int NT, bool F32>
 struct Running {
-  // 2^SHIFT is where the largest weight is put, 2^LIM what it may grow to (f16 ends at 2^16):
-  // far up, because weights below 2^-14 lose bits of their 11.  The second part of an fp32
-  // weight needs that range most.
-  static constexpr float SHIFT = F32 ? 13.f : 6.f, LIM = F32 ? 15.f : 14.f;
+  // 2^SHIFT is where the largest weight is put, 2^LIM what it may grow to before the reference
+  // moves (f16 ends at 2^16).  Room to grow saves moves: with the heavy-tailed scores of real
+  // keys 8 of a stream's first 32 tiles move some row's reference with 2^15 of it, 14 with 2^8.
+  // The price is at the other end, where weights below 2^-14 lose bits of their 11; the second
+  // part of an fp32 weight needs that range, so there the largest is put high.
+  static constexpr float SHIFT = F32 ? 13.f : 0.f, LIM = 15.f;
   float o[HD / 16][NT][4];
   float m[NT][2], l[NT][2];
+  unsigned started;  // bit 2 nt + e: the row has seen a slot (its m counts)
 
   __device__ __forceinline__ void clear() {
+    started = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = NO_REF;
+      m[nt][0] = m[nt][1] = 0.f;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i)
@@ -408,26 +364,32 @@ struct Running {
     }
   }
 
-  // A tile of 32 slots from `slot` on.  edge: some row does not see some of it.
+  // A tile of 32 slots from `slot` on.  edge: some row does not see some of it.  rows: each query
+  // row's draft row.
   __device__ __forceinline__ void tile(const AttnQuantArgs& a, const Queries<HD, NT, F32>& q,
                                        uint32_t k, uint32_t v, uint32_t scales, int slot,
-                                       bool edge, int len, int row0, int lane) {
+                                       bool edge, int len, const uint8_t* rows, int lane) {
     const int r = lane >> 2, c = lane & 3;
     const uint32_t k_off = tile_offset<HD>(r, c);
-    float acc[2][NT][4];
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[sub][nt][j] = 0.f;
-      q.scores(acc[sub], k + sub * 16 * HD, k_off);
-    }
     const uint4 sc = lds128(scales);
+    float x[2][NT][4];  // the scores, then the weights' exponents
+    q.scores(x[0], k, k_off);
+    q.scores(x[1], k + 16 * HD, k_off);
     const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
-    // (a half without any slot to see was filled with zeros)
+    // (16 slots without any to see come without scales)
     const float vs[2] = {sc.z ? __uint_as_float(sc.z) : 1.f, sc.w ? __uint_as_float(sc.w) : 1.f};
     const float lv[2] = {lg2(vs[0]), lg2(vs[1])};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const float f0 = q.scale[nt][0] * ks[sub], f1 = q.scale[nt][1] * ks[sub];
+        const float g0 = lv[sub] - m[nt][0], g1 = lv[sub] - m[nt][1];
+        float* w = x[sub][nt];
+        w[0] = fmaf(w[0], f0, g0), w[1] = fmaf(w[1], f1, g1);
+        w[2] = fmaf(w[2], f0, g0), w[3] = fmaf(w[3], f1, g1);
+      }
+    }
     unsigned seen = ~0u;  // bit (sub * NT + nt) * 4 + j: element j's slot is seen by its row
     static_assert(2 * NT * 4 <= 32, "one bit an element");
     if (edge) {
@@ -436,46 +398,31 @@ struct Running {
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = min((row0 + nt * 8 + 2 * c + e) / a.G, a.K - 1);
-          const int lo = row_begin(a, len, j), hi = row_end(a, len, j);
+          const int j = rows[nt * 8 + 2 * c + e];
+          const int lo = row_begin(a, len, j) - slot - r, hi = row_end(a, len, j) - slot - r;
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int t = slot + sub * 16 + y * 8 + r;
-              if (t >= lo && t < hi) seen |= 1u << ((sub * NT + nt) * 4 + 2 * y + e);
+              if (sub * 16 + y * 8 >= lo && sub * 16 + y * 8 < hi)
+                seen |= 1u << ((sub * NT + nt) * 4 + 2 * y + e);
+              else
+                x[sub][nt][2 * y + e] = -INFINITY;
             }
         }
       }
     }
-    float x[2][NT][4];
-    bool again = true;
-    while (true) {
-      float top = -INFINITY;
+    float top = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float f0 = q.scale[nt][0] * ks[sub], f1 = q.scale[nt][1] * ks[sub];
-          const float g0 = lv[sub] - m[nt][0], g1 = lv[sub] - m[nt][1];
-          float* w = x[sub][nt];
-          const float* s = acc[sub][nt];
-          w[0] = fmaf(s[0], f0, g0), w[1] = fmaf(s[1], f1, g1);
-          w[2] = fmaf(s[2], f0, g0), w[3] = fmaf(s[3], f1, g1);
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!(seen >> ((sub * NT + nt) * 4 + j) & 1)) w[j] = -INFINITY;
-          }
-          top = max3(top, w[0], w[1]);
-          top = max3(top, w[2], w[3]);
-        }
+        top = max3(top, x[sub][nt][0], x[sub][nt][1]);
+        top = max3(top, x[sub][nt][2], x[sub][nt][3]);
       }
-      // (NaN passes no comparison: it reaches the weights as it is)
-      if (!again || !__any_sync(0xffffffffu, top > LIM)) break;
-      again = false;
-      raise(q, acc, ks, lv, seen);
-    }
+    // (NaN passes no comparison: it reaches the weights as it is)
+    constexpr unsigned ALL = (1u << (2 * NT)) - 1;
+    if (__any_sync(0xffffffffu, top > LIM || started != ALL)) raise(x);
     const float rv[2] = {rcp(vs[0]), rcp(vs[1])};
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
@@ -501,30 +448,25 @@ struct Running {
     }
   }
 
-  // Moves the references of the rows that a tile's scores pass, and scales what was summed.
-  __device__ __forceinline__ void raise(const Queries<HD, NT, F32>& q, float (*acc)[NT][4],
-                                        const float* ks, const float* lv, unsigned seen) {
+  // Moves the references of the rows that a tile passes or starts, and scales what was summed.
+  __device__ __forceinline__ void raise(float (*x)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            if (seen >> ((sub * NT + nt) * 4 + 2 * y + e) & 1)
-              top = fmaxf(top, fmaf(acc[sub][nt][2 * y + e], q.scale[nt][e] * ks[sub], lv[sub]));
+        float top = fmaxf(max3(x[0][nt][e], x[0][nt][2 + e], x[1][nt][e]), x[1][nt][2 + e]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float to = top - m[nt][e] > LIM ? top - SHIFT : m[nt][e];
-        const float f = ex2(m[nt][e] - to);
-        if (to != m[nt][e]) {
-          l[nt][e] *= f;
+        const bool any = !(top == -INFINITY), had = started >> (2 * nt + e) & 1;
+        const float by = any && (top > LIM || !had) ? top - SHIFT : 0.f;
+        const float f = had ? ex2(-by) : 1.f;  // (nothing was summed before the first slot)
+        if (any) started |= 1u << (2 * nt + e);
+        m[nt][e] += by;
+        l[nt][e] *= f;
 #pragma unroll
-          for (int i = 0; i < HD / 16; ++i) o[i][nt][e] *= f, o[i][nt][2 + e] *= f;
-          m[nt][e] = to;
-        }
+        for (int sub = 0; sub < 2; ++sub) x[sub][nt][e] -= by, x[sub][nt][2 + e] -= by;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) o[i][nt][e] *= f, o[i][nt][2 + e] *= f;
       }
     }
   }
@@ -547,9 +489,9 @@ struct Running {
       }
     }
     if (edge) {
-      // A slot that only some rows see may hold NaN; a zero weight does not keep it out of the
-      // other rows.  Its codes are cleared, and the rows that see it are made NaN by a product
-      // of the two 0 / 1 matrices "is NaN" and "is seen".
+      // A slot that some row does not see may hold NaN, and a zero weight does not keep it out.
+      // Its codes are cleared, and the rows that see it are made NaN by a product of the two
+      // 0 / 1 matrices "is NaN" and "is seen".
       uint32_t bad = 0;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
@@ -615,16 +557,16 @@ __device__ __forceinline__ void store2(bf16* p, float x, float y) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
 }
 
-// A row's result: its address in out, whether the row exists, and 1 / l (0 for a row that has
-// seen nothing); writes its lse when `first`.
+// A row's result: its address in out and 1 / l (0 for a row that has seen nothing); writes its lse
+// when `first`.  at: the row's place among its request's rows and heads.
 template <typename T>
-__device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int h, int row,
-                                         float m, float l, bool first, float& inv) {
+__device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int at, float m,
+                                         float l, bool first, float& inv) {
   const bool none = m == NO_REF && l == 0.f;  // (a row of NaN scores has no reference either)
   inv = none ? 0.f : 1.f / l;
-  const int64_t at = ((int64_t)req * a.K + row / a.G) * ((int64_t)a.nkv * a.G) + h * a.G + row % a.G;
-  if (first && a.lse) a.lse[at] = none ? -INFINITY : (m + log2f(l)) * LN2;
-  return (T*)a.out + at * hd;
+  const int64_t to = (int64_t)req * a.K * (a.nkv * a.G) + at;
+  if (first && a.lse) a.lse[to] = none ? -INFINITY : (m + log2f(l)) * LN2;
+  return (T*)a.out + to * hd;
 }
 
 // Sum over the CTA's threads of v before this one, and over all of them.
@@ -660,10 +602,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
   __shared__ long long found[2];
   __shared__ int found_b;
   __shared__ float row_m[WARPS][NT * 8], row_l[WARPS][NT * 8];
+  __shared__ __align__(8) float row_scale[MAX_ROWS + 8];
+  __shared__ uint8_t row_j[MAX_ROWS + 8];  // each query row's draft row
+  __shared__ int row_at[MAX_ROWS + 8];     // and place among its request's rows and heads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = a.groups, streams = WARPS / groups;
   const int stream = warp / groups, group = warp % groups;
   const int row0 = group * NT * 8;
+  if (threadIdx.x < groups * NT * 8) {
+    const int j = min((int)threadIdx.x / a.G, a.K - 1);  // (past the last row: the last draft row)
+    row_j[threadIdx.x] = (uint8_t)j;
+    row_at[threadIdx.x] = j * (a.nkv * a.G) + (int)threadIdx.x - j * a.G;
+  }
   pdl_enter();
 
   // this CTA's share of the units, and the (request, kv head) in which it begins
@@ -721,43 +671,71 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
                         (uint32_t)(stream * a.stages) * STAGE;
   float* joined = reinterpret_cast<float*>(smem + (size_t)streams * a.stages * STAGE);
 
-  // the stream's loads run ahead of its products, over (request, kv head) boundaries
+  // The stream's loads run ahead of its products, over (request, kv head) boundaries.  A lane
+  // copies the same chunks of every tile: rows WARP_ROWS groups apart, whose places in a stage
+  // follow from two offsets (rows 4 apart are permuted differently, rows 8 apart alike).
+  constexpr int ROW_CHUNKS = HD / 16, WARP_ROWS = 32 / ROW_CHUNKS;
   Segment next = seg;
-  int next_u = max(next.at, 0) + stream, slot_in = 0;
+  int next_u = 0, next_end = 0, slot_in = 0;
+  const uint8_t *next_k = nullptr, *next_v = nullptr;
+  const float* next_scale = nullptr;
+  const int my_row = group * WARP_ROWS + lane / ROW_CHUNKS;
+  const uint32_t off_even = tile_offset<HD>(my_row, lane % ROW_CHUNKS);
+  const uint32_t off_odd = tile_offset<HD>(my_row + WARP_ROWS * groups, lane % ROW_CHUNKS) -
+                           WARP_ROWS * groups * HD;
   bool more = true;
+  auto enter = [&]() {  // the stream's first tile of segment `next`
+    next_u = max(next.at, 0) + stream;
+    next_end = min(next.at + next.tiles, n);
+    const int64_t unit = (int64_t)next.b * a.nkv + next.h;
+    const int64_t slot = (int64_t)(next.first_tile + next_u - next.at) * TILE;
+    const int64_t at = (unit * a.capacity + slot + my_row) * HD + lane % ROW_CHUNKS * 16;
+    next_k = a.k + at;
+    next_v = a.v + at;
+    next_scale = (lane < 2 ? a.k_scale : a.v_scale) + unit * (a.capacity >> a.block_shift);
+  };
   auto issue = [&]() {
-    while (more && next_u >= min(next.at + next.tiles, n)) {
+    while (more && next_u >= next_end) {
       more = next.at + next.tiles < n && next.next(a);
-      next_u = max(next.at, 0) + stream;
+      if (more) enter();
     }
     if (more) {
-      const int lo_slot = row_begin(a, next.len, 0), hi_slot = row_end(a, next.len, a.K - 1);
       const int slot = (next.first_tile + next_u - next.at) * TILE;
-      const int64_t unit = (int64_t)next.b * a.nkv + next.h;
-      const uint8_t* k = a.k + (unit * a.capacity + slot) * HD;
-      const uint8_t* v = a.v + (unit * a.capacity + slot) * HD;
       const uint32_t to = ring + slot_in * STAGE;
-      constexpr int CHUNKS = TILE * HD / 16;
-      const int step = 32 * groups;
-      for (int i = group * 32 + lane; i < CHUNKS; i += step) {
-        const int row = i / (HD / 16), t = slot + row;
-        const uint32_t off = tile_offset<HD>(row, i % (HD / 16));
-        const bool in = t >= lo_slot && t < hi_slot;
-        cp_async16(to + off, in ? k + i * 16 : a.k, in ? 16 : 0);
-        cp_async16(to + TILE * HD + off, in ? v + i * 16 : a.v, in ? 16 : 0);
+      if (slot + TILE <= a.capacity) {
+        for (int i = 0; i < TILE; i += 2 * WARP_ROWS * groups) {
+          const int by = WARP_ROWS * groups;
+          cp_async16(to + off_even + i * HD, next_k + i * HD);
+          cp_async16(to + TILE * HD + off_even + i * HD, next_v + i * HD);
+          if (i + by < TILE) {
+            cp_async16(to + off_odd + (i + by) * HD, next_k + (i + by) * HD);
+            cp_async16(to + TILE * HD + off_odd + (i + by) * HD, next_v + (i + by) * HD);
+          }
+        }
+      } else {  // a tile that the capacity ends in
+        for (int i = 0; i < TILE; i += WARP_ROWS * groups) {
+          const uint32_t off = tile_offset<HD>(my_row + i, lane % ROW_CHUNKS);
+          if (slot + my_row + i < a.capacity) {
+            cp_async16(to + off, next_k + i * HD);
+            cp_async16(to + TILE * HD + off, next_v + i * HD);
+          }
+        }
       }
       if (group == 0 && lane < 4) {
+        // (scales of blocks without a slot to see may be anything: zeros instead)
         const int t = slot + (lane & 1) * 16;
-        const bool in = t + 16 > lo_slot && t < hi_slot;
-        const float* s = (lane < 2 ? a.k_scale : a.v_scale) +
-                         unit * (a.capacity >> a.block_shift) + (t >> a.block_shift);
-        cp_async4(to + 2 * TILE * HD + lane * 4, in ? s : a.k_scale, in ? 4 : 0);
+        const bool in = t + 16 > row_begin(a, next.len, 0) && t < row_end(a, next.len, a.K - 1);
+        cp_async4(to + 2 * TILE * HD + lane * 4, in ? next_scale + (t >> a.block_shift) : a.k_scale,
+                  in ? 4 : 0);
       }
       next_u += streams;
+      next_k += (int64_t)streams * TILE * HD;
+      next_v += (int64_t)streams * TILE * HD;
     }
     cp_async_commit();
     if (++slot_in == a.stages) slot_in = 0;
   };
+  enter();
   for (int i = 0; i < a.stages - 1; ++i) issue();
 
   Queries<HD, NT, F32> q;
@@ -767,8 +745,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
   while (true) {
     const int begin = max(seg.at, 0), end = min(seg.at + seg.tiles, n);
     const int all_begin = row_begin(a, seg.len, a.K - 1), all_end = row_end(a, seg.len, 0);
-    q.load(a, seg.b, seg.h, row0, lane);
+    for (int t = warp; t < groups * NT; t += WARPS)
+      Queries<HD, NT, F32>::prepare(a, seg.b, seg.h, t, lane,
+                                    reinterpret_cast<uint2*>(joined) +
+                                        t * (Queries<HD, NT, F32>::TILE_BYTES / 8),
+                                    row_scale + t * 8);
     run.clear();
+    __syncthreads();
+    q.load(reinterpret_cast<const uint2*>(joined) +
+               group * NT * (Queries<HD, NT, F32>::TILE_BYTES / 8),
+           row_scale + row0, lane);
     for (int u = begin + stream; u < end; u += streams) {
       cp_async_wait(a.stages - 2);
       if (groups > 1)
@@ -779,7 +765,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
       const uint32_t at = ring + slot_out * STAGE;
       const int slot = (seg.first_tile + u - seg.at) * TILE;
       const bool edge = slot < all_begin || slot + TILE > all_end;
-      run.tile(a, q, at, at + TILE * HD, at + 2 * TILE * HD, slot, edge, seg.len, row0, lane);
+      run.tile(a, q, at, at + TILE * HD, at + 2 * TILE * HD, slot, edge, seg.len, row_j + row0, lane);
       if (++slot_out == a.stages) slot_out = 0;
     }
 
@@ -792,6 +778,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           run.l[nt][e] += __shfl_xor_sync(0xffffffffu, run.l[nt][e], d);
+        if (!(run.started >> (2 * nt + e) & 1)) run.m[nt][e] = NO_REF;
         if (r == 0) row_m[warp][nt * 8 + 2 * c + e] = run.m[nt][e];
       }
     __syncthreads();
@@ -854,7 +841,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
           out[e] = nullptr;
           if (began && ended) {
             if (row < a.K * a.G)
-              out[e] = finish_row<T>(a, HD, seg.b, seg.h, row, run.m[nt][e], l, r == 0, inv[e]);
+              out[e] = finish_row<T>(a, HD, seg.b, seg.h * a.G + row_at[row], run.m[nt][e], l,
+                                     r == 0, inv[e]);
           } else if (r == 0) {
             slot[2 * row] = run.m[nt][e];
             slot[2 * row + 1] = l;
@@ -970,12 +958,15 @@ __global__ void __launch_bounds__(WARPS * 32) attn_quant_join_kernel(AttnQuantAr
       }
     }
     float inv;
+    const int nq = a.nkv * a.G, j0 = row / a.G, j1 = (row + 1) / a.G;
     if (row < a.K * a.G) {
-      T* out = finish_row<T>(a, HD, d.x, d.y, row, m0, l0, i == 0 && r == 0, inv);
+      T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
+                             i == 0 && r == 0, inv);
       store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
     }
     if (row + 1 < a.K * a.G) {
-      T* out = finish_row<T>(a, HD, d.x, d.y, row + 1, m1, l1, i == 0 && r == 0, inv);
+      T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
+                             i == 0 && r == 0, inv);
       store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
     }
   }
@@ -1006,7 +997,10 @@ template <int HD, int NT, bool F32>
 static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
   constexpr size_t STAGE = 2 * TILE * HD + 16, FRAG = (size_t)HD / 16 * NT * 4 * 32 * sizeof(float);
   const int streams = WARPS / p.groups;
-  const size_t join = streams > 1 ? (size_t)(streams > 2 ? 2 : 1) * p.groups * FRAG : 0;
+  // the joining buffers, which also hold the prepared queries
+  size_t join = streams > 1 ? (size_t)(streams > 2 ? 2 : 1) * p.groups * FRAG : 0;
+  const size_t prepared = (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES;
+  join = join > prepared ? join : prepared;
   // up to 8 stages a stream, within the 227 KB of a CTA less its static arrays
   const size_t room = 220 * 1024 - join;
   a.groups = p.groups;

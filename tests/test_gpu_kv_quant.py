@@ -254,9 +254,7 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
     u = 2^-24 is half an fp32 step.  A score is a product of hd terms summed in fp32 in any
     order: (hd + 8) u S with S = scale sum |q k|; fp32 queries come as two 11-bit parts, which
     drop 2^-22 of an element, or of 2^-2 of the row's largest where an element is that small:
-    2^-22 S + 2^-24 scale max|q| sum |k|; bf16 queries as two e4m3 parts, whose last spacing of
-    2^-9 (half of it dropped) is at most 2^-10 / 224 of the row's largest.
-    A score's error d moves the weights by 2 d relative
+    2^-22 S + 2^-24 scale max|q| sum |k|.  A score's error d moves the weights by 2 d relative
     (numerator and sum).  The exponential's argument carries u of its size (|x| < 2^8 before a
     weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to 11 bits
     (2^-12 relative; 2^-22 for the two parts of fp32) or, below the smallest f16, to half of
@@ -279,8 +277,6 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
             d = (hd + 8) * u * S
             if f32:
                 d += 2.0 ** -22 * S + u * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
-            else:
-                d += 2.0 ** -10 / 224 * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
             d += 2.0 ** -15 + 2.0 ** -21 + 4 * u * S
             w, tiny = (2.0 ** -22, 2.0 ** -36) if f32 else (2.0 ** -12, 2.0 ** -25)
             to[r, h] = absolute[r, h] * (2 * d + w + 2 * (n + 64) * u) + \
