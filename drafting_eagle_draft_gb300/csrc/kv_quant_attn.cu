@@ -44,9 +44,14 @@
 namespace peagle {
 namespace kvq {
 
+#ifndef PEAGLE_W64
+#define PEAGLE_W64 8
+#define PEAGLE_MOST64 4
+#endif
 constexpr int CTAS = 152;      // GB300's SMs
-constexpr int WARPS = 8;
 constexpr int TILE = 32;       // slots a unit
+constexpr int ENTRY = 8;       // what a (request, kv head) costs besides its tiles, in tiles
+constexpr int JOIN_WARPS = 8;  // of the second kernel
 constexpr int MAX_ROWS = 128;  // query rows a kv head
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no slot
@@ -200,9 +205,11 @@ __device__ __forceinline__ float power2(int e) {
 struct Segment {
   int b, h, len;
   int first_tile, tiles;
-  int at;  // of its first unit, relative to the CTA's share (negative: it began before)
-  __device__ __forceinline__ bool next(const AttnQuantArgs& a) {
-    at += tiles;
+  int at;  // of its first tile, relative to the CTA's share (negative: it began before)
+  // The next one; false when it is not in the share of n any more.
+  __device__ __forceinline__ bool next(const AttnQuantArgs& a, int n) {
+    at += tiles + ENTRY;
+    if (at >= n) return false;
     if (++h < a.nkv) return true;
     h = 0;
     do {
@@ -217,41 +224,52 @@ struct Segment {
 // Query operands.  prepare() makes the operands of one tile of 8 rows in shared memory (a warp;
 // the CTA's warps share the tiles of a (request, kv head)), load() takes NT tiles' into a warp's
 // registers, scores() multiplies 16 keys by them.
-// 16 consecutive query elements of a row at head dims 16c and, for head_dim 128, 64 + 16c;
-// the row's largest magnitude as bits.
-template <int HD, typename T>
-__device__ __forceinline__ unsigned load_query(const AttnQuantArgs& a, int req, int h, int row,
-                                               int c, float* x) {
-  unsigned top = 0;
-  if (row < a.K * a.G) {
-    const int j = row / a.G;
-    const T* q = (const T*)a.q + ((int64_t)req * a.K + j) * a.q_stride +
-                 (int64_t)(h * a.G + row - j * a.G) * HD + 16 * c;
-    constexpr int E = 16 / sizeof(T);
+// A lane's query elements: 16 consecutive ones of row 8 tile + r at head dims 16c and, for
+// head_dim 128, 64 + 16c, as they are stored (zeros past the last row).
+template <int HD, bool F32>
+struct RawQuery {
+  static constexpr int E = F32 ? 4 : 8, N = HD / 4 / E;
+  uint4 u[N];
+
+  __device__ __forceinline__ void fetch(const AttnQuantArgs& a, int req, int h, int tile,
+                                        int lane) {
+    const int row = tile * 8 + (lane >> 2), c = lane & 3;
+    if (row < a.K * a.G) {
+      const int j = row / a.G;
+      const char* q = (const char*)a.q +
+                      (((int64_t)req * a.K + j) * a.q_stride +
+                       (int64_t)(h * a.G + row - j * a.G) * HD + 16 * c) * (F32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < HD / 4 / E; ++i) {
-      const uint4 u =
-          __ldg(reinterpret_cast<const uint4*>(q + (i * E / 16) * 64 + i * E % 16));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int i = 0; i < N; ++i)
+        u[i] = __ldg(reinterpret_cast<const uint4*>(
+            q + ((i * E / 16) * 64 + i * E % 16) * (F32 ? 4 : 2)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  // The elements, and the largest magnitude of the row as bits.
+  __device__ __forceinline__ unsigned elements(float* x) const {
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (sizeof(T) == 2) {
+        if (F32) {
+          x[E * i + k] = __uint_as_float(w[k]);
+        } else {
           x[E * i + 2 * k] = __uint_as_float(w[k] << 16);
           x[E * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        } else {
-          x[E * i + k] = __uint_as_float(w[k]);
         }
       }
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < HD / 4; ++i) x[i] = 0.f;
+    for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   }
-#pragma unroll
-  for (int i = 0; i < HD / 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-}
+};
 
 template <int HD, int NT, bool F32>
 struct Queries {
@@ -260,11 +278,10 @@ struct Queries {
   uint32_t b[PARTS][STEPS][NT][2];  // [part][k step][rows][register]
   float scale[NT][2];               // of rows 2c and 2c + 1, with the scores' scale
 
-  __device__ __forceinline__ static void prepare(const AttnQuantArgs& a, int req, int h, int tile,
+  __device__ __forceinline__ static void prepare(const RawQuery<HD, F32>& raw, float scale,
                                                  int lane, uint2* to, float* scales) {
     float x[HD / 4];
-    typedef typename std::conditional<F32, float, bf16>::type T;
-    const unsigned top = load_query<HD, T>(a, req, h, tile * 8 + (lane >> 2), lane & 3, x);
+    const unsigned top = raw.elements(x);
     const bool fine = top < 0x7f800000u;
     // the largest element to 2^14 .. 2^15: f16's last bit is then 2^-38 of it
     const int e = fine ? min(max((int)(top >> 23) - 127 - 14, -100), 120) : 0;
@@ -284,7 +301,7 @@ struct Queries {
         to[(p * STEPS + s) * 32 + lane] = make_uint2(part[p][0], part[p][1]);
     }
     // a row that is not finite gives NaN
-    if ((lane & 3) == 0) scales[lane >> 2] = fine ? power2(e) * a.scale : NAN;
+    if ((lane & 3) == 0) scales[lane >> 2] = fine ? power2(e) * scale : NAN;
   }
 
   __device__ __forceinline__ void load(const uint2* from, const float* scales, int lane) {
@@ -569,7 +586,8 @@ __device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req
   return (T*)a.out + to * hd;
 }
 
-// Sum over the CTA's threads of v before this one, and over all of them.
+// Sum over the W warps' threads of v before this one, and over all of them.
+template <int W>
 __device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   long long x = v;
@@ -584,7 +602,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
   long long before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) {
+  for (int i = 0; i < W; ++i) {
     const long long s = red[i];
     if (i < wid) before += s;
     total += s;
@@ -592,21 +610,28 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
   return before + x - v;
 }
 
-template <int HD, int NT, bool F32>
-__global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs a) {
+// Parts in which the warps' O^T go through the joining buffer.  At head_dim 128 parts leave room
+// for a third stage of the rings (NT 1 and 2; NT 3 has two either way).
+constexpr int join_passes(int hd, int nt, int w) { return hd == 64 ? 1 : nt == 2 ? 4 : 2; }
+
+// W: warps a CTA.
+template <int HD, int NT, bool F32, int W>
+__global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) {
   typedef typename std::conditional<F32, float, bf16>::type T;
-  constexpr int STAGE = 2 * TILE * HD + 16;       // K, V, four scales
-  constexpr int FRAG = HD / 16 * NT * 4 * 32;     // floats of a warp's O^T
+  typedef Queries<HD, NT, F32> Q;
+  constexpr int STAGE = 2 * TILE * HD + 16;  // K, V, four scales
+  constexpr int FRAG = HD / 16 * NT * 32;    // float4s of a warp's O^T
+  constexpr int PASSES = join_passes(HD, NT, W), PASS = FRAG / PASSES;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ long long red[WARPS];
-  __shared__ long long found[2];
+  __shared__ long long red[W];
+  __shared__ long long found;
   __shared__ int found_b;
-  __shared__ float row_m[WARPS][NT * 8], row_l[WARPS][NT * 8];
+  __shared__ __align__(8) float row_m[W][NT * 8], row_l[W][NT * 8];
   __shared__ __align__(8) float row_scale[MAX_ROWS + 8];
   __shared__ uint8_t row_j[MAX_ROWS + 8];  // each query row's draft row
   __shared__ int row_at[MAX_ROWS + 8];     // and place among its request's rows and heads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = a.groups, streams = WARPS / groups;
+  const int groups = a.groups, streams = W / groups;
   const int stream = warp / groups, group = warp % groups;
   const int row0 = group * NT * 8;
   if (threadIdx.x < groups * NT * 8) {
@@ -616,60 +641,63 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
   }
   pdl_enter();
 
-  // this CTA's share of the units, and the (request, kv head) in which it begins
+  // this CTA's share of the work, and the (request, kv head) in which it begins
   Segment seg;
-  int n;  // units of the share
+  int n;  // cost of the share
   long long total = 0, share, lo;
   {
-    long long units = 0, before = 0;
+    long long cost = 0, before = 0;
     int first;
-    for (int b0 = 0; b0 < a.batch; b0 += WARPS * 32) {
+    auto cost_of = [&](int b) {
+      const int tiles = b < a.batch ? request_tiles(a, a.seq_lens[b], first) : 0;
+      return tiles ? (long long)(tiles + ENTRY) * a.nkv : 0;
+    };
+    for (int b0 = 0; b0 < a.batch; b0 += W * 32) {
       const int b = b0 + threadIdx.x;
-      units = 0;
-      if (b < a.batch) {
-        const int len = a.seq_lens[b];
-        units = (long long)request_tiles(a, len, first) * a.nkv;
-        if (blockIdx.x == 0 && !request_fits(a, len)) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
-      }
+      cost = cost_of(b);
+      if (blockIdx.x == 0 && b < a.batch && !request_fits(a, a.seq_lens[b]))
+        raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
       long long part;
-      before = block_scan(units, red, part);
+      before = block_scan<W>(cost, red, part);
       total += part;
     }
     share = (total + CTAS - 1) / CTAS;
     // a share below 4 tiles leaves warps idle and makes pieces to join
     share = share < 4 ? 4 : share;
     lo = share * blockIdx.x;
-    if (lo >= total) {
-      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      return;
-    }
     n = (int)(total - lo < share ? total - lo : share);
     long long base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += WARPS * 32) {
-      if (a.batch > WARPS * 32) {
-        const int b = b0 + threadIdx.x;
-        units = b < a.batch ? (long long)request_tiles(a, a.seq_lens[b], first) * a.nkv : 0;
+    for (int b0 = 0; b0 < a.batch && lo < total; b0 += W * 32) {
+      if (a.batch > W * 32) {
+        cost = cost_of(b0 + threadIdx.x);
         long long part;
-        before = base + block_scan(units, red, part);
+        before = base + block_scan<W>(cost, red, part);
         base += part;
       }
-      if (units && lo >= before && lo < before + units) {
-        found[0] = before;
+      if (cost && lo >= before && lo < before + cost) {
+        found = before;
         found_b = b0 + threadIdx.x;
       }
     }
     __syncthreads();
-    seg.b = found_b;
-    seg.len = a.seq_lens[seg.b];
-    seg.tiles = request_tiles(a, seg.len, seg.first_tile);
-    const long long in = lo - found[0];
-    seg.h = (int)(in / seg.tiles);
-    seg.at = -(int)(in % seg.tiles);
+    if (lo < total) {
+      seg.b = found_b;
+      seg.len = a.seq_lens[seg.b];
+      seg.tiles = request_tiles(a, seg.len, seg.first_tile);
+      const long long in = lo - found;
+      seg.h = (int)(in / (seg.tiles + ENTRY));
+      seg.at = ENTRY - (int)(in % (seg.tiles + ENTRY));
+    }
+    if (lo >= total || seg.at >= n) {
+      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
   }
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) +
                         (uint32_t)(stream * a.stages) * STAGE;
-  float* joined = reinterpret_cast<float*>(smem + (size_t)streams * a.stages * STAGE);
+  uint2* prepared = reinterpret_cast<uint2*>(smem + (size_t)streams * a.stages * STAGE);
+  float4* joined = reinterpret_cast<float4*>(prepared + groups * NT * (Q::TILE_BYTES / 8));
 
   // The stream's loads run ahead of its products, over (request, kv head) boundaries.  A lane
   // copies the same chunks of every tile: rows WARP_ROWS groups apart, whose places in a stage
@@ -696,13 +724,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
   };
   auto issue = [&]() {
     while (more && next_u >= next_end) {
-      more = next.at + next.tiles < n && next.next(a);
+      more = next.next(a, n);
       if (more) enter();
     }
     if (more) {
       const int slot = (next.first_tile + next_u - next.at) * TILE;
       const uint32_t to = ring + slot_in * STAGE;
-      if (slot + TILE <= a.capacity) {
+      if (my_row >= TILE) {  // (more groups than the tile has rows for)
+      } else if (slot + TILE <= a.capacity) {
         for (int i = 0; i < TILE; i += 2 * WARP_ROWS * groups) {
           const int by = WARP_ROWS * groups;
           cp_async16(to + off_even + i * HD, next_k + i * HD);
@@ -715,7 +744,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
       } else {  // a tile that the capacity ends in
         for (int i = 0; i < TILE; i += WARP_ROWS * groups) {
           const uint32_t off = tile_offset<HD>(my_row + i, lane % ROW_CHUNKS);
-          if (slot + my_row + i < a.capacity) {
+          if (my_row + i < TILE && slot + my_row + i < a.capacity) {
             cp_async16(to + off, next_k + i * HD);
             cp_async16(to + TILE * HD + off, next_v + i * HD);
           }
@@ -738,23 +767,23 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
   enter();
   for (int i = 0; i < a.stages - 1; ++i) issue();
 
-  Queries<HD, NT, F32> q;
+  RawQuery<HD, F32> raw;
+  if (warp < groups * NT) raw.fetch(a, seg.b, seg.h, warp, lane);
+  Q q;
   Running<HD, NT, F32> run;
+  const int r = lane >> 2, c = lane & 3;
   int slot_out = 0;
   bool chained = false;
   while (true) {
     const int begin = max(seg.at, 0), end = min(seg.at + seg.tiles, n);
     const int all_begin = row_begin(a, seg.len, a.K - 1), all_end = row_end(a, seg.len, 0);
-    for (int t = warp; t < groups * NT; t += WARPS)
-      Queries<HD, NT, F32>::prepare(a, seg.b, seg.h, t, lane,
-                                    reinterpret_cast<uint2*>(joined) +
-                                        t * (Queries<HD, NT, F32>::TILE_BYTES / 8),
-                                    row_scale + t * 8);
+    for (int t = warp; t < groups * NT; t += W) {
+      if (t >= W) raw.fetch(a, seg.b, seg.h, t, lane);
+      Q::prepare(raw, a.scale, lane, prepared + t * (Q::TILE_BYTES / 8), row_scale + t * 8);
+    }
     run.clear();
     __syncthreads();
-    q.load(reinterpret_cast<const uint2*>(joined) +
-               group * NT * (Queries<HD, NT, F32>::TILE_BYTES / 8),
-           row_scale + row0, lane);
+    q.load(prepared + group * NT * (Q::TILE_BYTES / 8), row_scale + row0, lane);
     for (int u = begin + stream; u < end; u += streams) {
       cp_async_wait(a.stages - 2);
       if (groups > 1)
@@ -765,12 +794,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
       const uint32_t at = ring + slot_out * STAGE;
       const int slot = (seg.first_tile + u - seg.at) * TILE;
       const bool edge = slot < all_begin || slot + TILE > all_end;
-      run.tile(a, q, at, at + TILE * HD, at + 2 * TILE * HD, slot, edge, seg.len, row_j + row0, lane);
+      run.tile(a, q, at, at + TILE * HD, at + 2 * TILE * HD, slot, edge, seg.len, row_j + row0,
+               lane);
       if (++slot_out == a.stages) slot_out = 0;
     }
 
+    // the next (request, kv head)'s queries arrive while this one's streams are joined
+    const Segment done = seg;
+    const bool last = !seg.next(a, n);
+    if (!last && warp < groups * NT) raw.fetch(a, seg.b, seg.h, warp, lane);
+
     // join the streams: a common reference for every row, then their sums
-    const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -790,92 +824,71 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
         for (int s = 0; s < streams; ++s)
           top = fmaxf(top, row_m[s * groups + group][nt * 8 + 2 * c + e]);
         const float f = ex2(run.m[nt][e] - top);
-        run.m[nt][e] = top;
-        run.l[nt][e] *= f;
+        if (r == 0) row_l[warp][nt * 8 + 2 * c + e] = run.l[nt][e] * f;
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) run.o[i][nt][e] *= f, run.o[i][nt][2 + e] *= f;
-        if (r == 0) row_l[warp][nt * 8 + 2 * c + e] = run.l[nt][e];
       }
-    // two streams at a time add theirs to streams 0 and 1, then 1 to 0
-    for (int s = streams; s > 1;) {
-      const int give = s > 2 ? 2 : 1, from = s - give;
-      float4* buf = reinterpret_cast<float4*>(joined) +
-                    (size_t)((stream >= from ? stream - from : stream) * groups + group) * (FRAG / 4);
-      if (stream >= from && stream < s) {
+    const bool began = done.at >= 0, whole = began && done.at + done.tiles <= n;
+    float* slot = a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
+                               ((size_t)groups * NT * 8 * (HD + 2));
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i)
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (pass) __syncthreads();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            buf[(i * NT + nt) * 32 + lane] = make_float4(run.o[i][nt][0], run.o[i][nt][1],
-                                                         run.o[i][nt][2], run.o[i][nt][3]);
-      }
+      for (int i = 0; i < HD / 16 / PASSES; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float* o = run.o[pass * (HD / 16 / PASSES) + i][nt];
+          joined[warp * PASS + (nt * (HD / 16 / PASSES) + i) * 32 + lane] =
+              make_float4(o[0], o[1], o[2], o[3]);
+        }
       __syncthreads();
-      if (stream < give) {
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float4 f = buf[(i * NT + nt) * 32 + lane];
-            run.o[i][nt][0] += f.x, run.o[i][nt][1] += f.y;
-            run.o[i][nt][2] += f.z, run.o[i][nt][3] += f.w;
-          }
-      }
-      s = from;
-      if (s > 1) __syncthreads();
-    }
-    if (streams == 1) __syncthreads();
-
-    if (stream == 0) {
-      const bool began = seg.at >= 0, ended = seg.at + seg.tiles <= n;
-      float* slot = a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
-                                 ((size_t)groups * NT * 8 * (HD + 2));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float inv[2];
-        T* out[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = row0 + nt * 8 + 2 * c + e;
-          float l = 0.f;
-          for (int s = 0; s < streams; ++s) l += row_l[s * groups + group][nt * 8 + 2 * c + e];
-          out[e] = nullptr;
-          if (began && ended) {
-            if (row < a.K * a.G)
-              out[e] = finish_row<T>(a, HD, seg.b, seg.h * a.G + row_at[row], run.m[nt][e], l,
-                                     r == 0, inv[e]);
-          } else if (r == 0) {
-            slot[2 * row] = run.m[nt][e];
-            slot[2 * row + 1] = l;
-          }
+      // each warp sums some of the fragments over the streams
+      for (int at = warp; at < groups * (PASS / 32); at += W) {
+        const int g = at / (PASS / 32), in = at % (PASS / 32);
+        const int nt = in / (HD / 16 / PASSES), i = pass * (HD / 16 / PASSES) + in % (HD / 16 / PASSES);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
+        for (int s = 0; s < streams; ++s) {
+          const int w = s * groups + g;
+          const float4 f = joined[w * PASS + in * 32 + lane];
+          const float2 l = *reinterpret_cast<const float2*>(&row_l[w][nt * 8 + 2 * c]);
+          const float2 m = *reinterpret_cast<const float2*>(&row_m[w][nt * 8 + 2 * c]);
+          o.x += f.x, o.y += f.y, o.z += f.z, o.w += f.w;
+          l0 += l.x, l1 += l.y;
+          m0 = fmaxf(m0, m.x), m1 = fmaxf(m1, m.y);
         }
-        if (began && ended) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (out[e])
-#pragma unroll
-              for (int i = 0; i < HD / 16; ++i)
-                store2(out[e] + r * (HD / 8) + 2 * i, run.o[i][nt][e] * inv[e],
-                       run.o[i][nt][2 + e] * inv[e]);
+        const int row = (g * NT + nt) * 8 + 2 * c;
+        if (whole) {
+          const int d = r * (HD / 8) + 2 * i;
+          float inv;
+          if (row < a.K * a.G) {
+            T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row], m0, l0,
+                                   i == 0 && r == 0, inv);
+            store2(out + d, o.x * inv, o.z * inv);
+          }
+          if (row + 1 < a.K * a.G) {
+            T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row + 1], m1, l1,
+                                   i == 0 && r == 0, inv);
+            store2(out + d, o.y * inv, o.w * inv);
+          }
         } else {
-          float4* o = reinterpret_cast<float4*>(slot + (size_t)groups * NT * 16);
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i)
-            o[((group * NT + nt) * (HD / 16) + i) * 32 + lane] =
-                make_float4(run.o[i][nt][0], run.o[i][nt][1], run.o[i][nt][2], run.o[i][nt][3]);
+          if (i == 0 && r == 0)
+            *reinterpret_cast<float4*>(slot + 2 * row) = make_float4(m0, l0, m1, l1);
+          reinterpret_cast<float4*>(
+              slot + (size_t)groups * NT * 16)[((g * NT + nt) * (HD / 16) + i) * 32 + lane] = o;
         }
       }
-      if (began && !ended) {
-        chained = true;
-        if (warp == 0 && lane == 0)
-          a.desc[blockIdx.x] =
-              make_int4(seg.b, seg.h, (int)((lo + seg.at + seg.tiles - 1) / share), 0);
-      }
     }
-    if (seg.at + seg.tiles >= n) break;
-    seg.next(a);
-    __syncthreads();  // row_m, row_l and the joining buffers are free again
+    if (began && !whole) {
+      chained = true;
+      if (threadIdx.x == 0)
+        a.desc[blockIdx.x] =
+            make_int4(done.b, done.h, (int)((lo + done.at + done.tiles - 1) / share), 0);
+    }
+    if (last) break;
   }
-  if (warp == 0 && lane == 0 && !chained) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !chained) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   cp_async_wait(0);
 }
 
@@ -884,10 +897,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_kernel(AttnQuantArgs
 // all, cut into gridDim.y = HD / 16 parts) over a part of the pieces.  Also writes the rows of requests
 // that no row of which sees a slot.
 template <int HD, typename T>
-__global__ void __launch_bounds__(WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a, int ntiles) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a, int ntiles) {
   pdl_enter();
-  __shared__ float4 red_o[WARPS][32];
-  __shared__ float red_m[WARPS][8], red_l[WARPS][8];
+  __shared__ float4 red_o[JOIN_WARPS][32];
+  __shared__ float red_m[JOIN_WARPS][8], red_l[JOIN_WARPS][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.y == 0) {
     for (int b = blockIdx.x; b < a.batch; b += CTAS) {
@@ -896,22 +909,22 @@ __global__ void __launch_bounds__(WARPS * 32) attn_quant_join_kernel(AttnQuantAr
       if (!request_fits(a, len) || request_tiles(a, len, first)) continue;
       const int64_t rows = (int64_t)a.K * a.nkv * a.G;
       T* out = (T*)a.out + b * rows * HD;
-      for (int64_t i = threadIdx.x; i < rows * HD; i += WARPS * 32) st(out + i, 0.f);
+      for (int64_t i = threadIdx.x; i < rows * HD; i += JOIN_WARPS * 32) st(out + i, 0.f);
       if (a.lse)
-        for (int64_t i = threadIdx.x; i < rows; i += WARPS * 32) a.lse[b * rows + i] = -INFINITY;
+        for (int64_t i = threadIdx.x; i < rows; i += JOIN_WARPS * 32) a.lse[b * rows + i] = -INFINITY;
     }
   }
   const int4 d = a.desc[blockIdx.x];
   if (d.x < 0) return;
   const int cols = ntiles * (HD / 16), per = cols / gridDim.y;  // 32 fragments each
-  const int parts = max(1, WARPS / per);                        // warps that share one
+  const int parts = max(1, JOIN_WARPS / per);                        // warps that share one
   const int pieces = d.z - (int)blockIdx.x + 1;
   const size_t slot = (size_t)ntiles * 8 * (HD + 2);
   const int r = lane >> 2, c = lane & 3;
   auto piece = [&](int p) {
     return a.work + ((size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * slot;
   };
-  for (int at = warp / parts; at < per; at += WARPS / parts) {
+  for (int at = warp / parts; at < per; at += JOIN_WARPS / parts) {
     const int col = blockIdx.y * per + at, nt = col / (HD / 16), i = col % (HD / 16);
     const int row = nt * 8 + 2 * c, part = warp % parts;
     float m0 = NO_REF, m1 = NO_REF;
@@ -933,7 +946,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_quant_join_kernel(AttnQuantAr
       o.z = fmaf(g.z, f0, o.z), o.w = fmaf(g.w, f1, o.w);
     }
     if (parts > 1) {
-      // (per <= WARPS / parts: every warp is in this loop once, or not at all)
+      // (per <= JOIN_WARPS / parts: every warp is in this loop once, or not at all)
       red_o[warp][lane] = o;
       if (r == 0) {
         red_m[warp][2 * c] = m0, red_m[warp][2 * c + 1] = m1;
@@ -980,7 +993,7 @@ struct Plan {
   int ntiles() const { return nt * groups; }
 };
 static Plan plan_of(int hd, bool f32, int rows) {
-  const int tiles = cdiv(rows, 8), most = hd == 64 ? 4 : f32 ? 2 : 3;
+  const int tiles = cdiv(rows, 8), most = hd == 64 ? PEAGLE_MOST64 : f32 ? 2 : 3;
   Plan p;
   for (p.groups = 1; cdiv(tiles, p.groups) > most; p.groups *= 2) {
   }
@@ -993,27 +1006,25 @@ static int64_t work_bytes(int hd, int ntiles) {
   return 4096 + (int64_t)CTAS * 2 * (int64_t)slot_bytes(hd, ntiles);
 }
 
-template <int HD, int NT, bool F32>
+template <int HD, int NT, bool F32, int W>
 static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
-  constexpr size_t STAGE = 2 * TILE * HD + 16, FRAG = (size_t)HD / 16 * NT * 4 * 32 * sizeof(float);
-  const int streams = WARPS / p.groups;
-  // the joining buffers, which also hold the prepared queries
-  size_t join = streams > 1 ? (size_t)(streams > 2 ? 2 : 1) * p.groups * FRAG : 0;
-  const size_t prepared = (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES;
-  join = join > prepared ? join : prepared;
+  constexpr size_t STAGE = 2 * TILE * HD + 16;
+  constexpr size_t JOIN = (size_t)W * HD * NT * 32 / join_passes(HD, NT, W);
+  const int streams = W / p.groups;
+  const size_t fixed = JOIN + (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES;
   // up to 8 stages a stream, within the 227 KB of a CTA less its static arrays
-  const size_t room = 220 * 1024 - join;
+  const size_t room = 221 * 1024 - fixed;
   a.groups = p.groups;
   a.stages = (int)(room / (streams * STAGE));
   a.stages = a.stages > 8 ? 8 : a.stages;
-  const size_t smem = streams * a.stages * STAGE + join;
-  cudaError_t e = smem_optin((const void*)attn_quant_kernel<HD, NT, F32>, smem);
+  const size_t smem = streams * a.stages * STAGE + fixed;
+  auto kernel = attn_quant_kernel<HD, NT, F32, W>;
+  cudaError_t e = smem_optin((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_quant_kernel<HD, NT, F32>, dim3(CTAS), dim3(WARPS * 32), smem, s, a);
+  e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  const dim3 grid(CTAS, HD / 16);
   return launch_pdl(attn_quant_join_kernel<HD, typename std::conditional<F32, float, bf16>::type>,
-                    grid, dim3(WARPS * 32), 0, s, a, p.ntiles());
+                    dim3(CTAS, HD / 16), dim3(JOIN_WARPS * 32), 0, s, a, p.ntiles());
 }
 
 }  // namespace kvq
@@ -1081,7 +1092,7 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   const Plan p = plan_of(hd, f32, K * a.G);
   cudaError_t e = cudaErrorInvalidValue;
 #define PEAGLE_ATTN(HD, NT, F32) \
-  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32>(a, p, (cudaStream_t)stream);
+  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, HD == 64 ? PEAGLE_W64 : 8>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)
   PEAGLE_ATTN(64, 2, false)
   PEAGLE_ATTN(64, 3, false)
