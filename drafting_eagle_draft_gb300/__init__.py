@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpeagle.so")
@@ -420,7 +421,7 @@ def _on(t, dev, dtype, what):
     """The device pointer of a CUDA tensor on `dev` with the given type (else INVALID)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != dev:
+    if t.dtype is not dtype or t.device != dev:
         _refuse(what, f"a tensor of {dtype} on {dev} is wanted, got {t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -430,8 +431,6 @@ def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
     [n_layers, batch, n_kv_heads, capacity, head_dim], k_scale, v_scale float32
     [n_layers, batch, n_kv_heads, capacity / block], errors an int32 tensor of one element or
     None.  All contiguous and on one CUDA device; the struct keeps them alive."""
-    import torch
-
     what = "kv_quant_struct"
     if k.dim() != 5 or k_scale.dim() != 4 or not k_scale.shape[3] or \
             k.shape[3] % k_scale.shape[3] or k.shape[:3] != k_scale.shape[:3]:
@@ -455,49 +454,51 @@ def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
     return st
 
 
-def _quant_call(kv, what, stream):
-    """The cache's device, which has to be the current CUDA device, and the stream."""
-    import torch
-
+def _quant_stream(kv, what, stream):
+    """The call's stream; the cache's device has to be the current CUDA device."""
+    cuda = torch.cuda
     dev = kv._device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+    if dev.type != "cuda" or dev.index != cuda.current_device():
         _refuse(what, f"the cache is on {dev}, which is not the current CUDA device")
     if stream is None:
-        return dev, torch.cuda.current_stream().cuda_stream
-    return dev, _stream_ptr(stream)
+        # (the current stream's handle without the Stream object around it: 0.1 of 2.9 us)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(dev.index) if raw else cuda.current_stream().cuda_stream
+    return _stream_ptr(stream)
 
 
-def _kv_rows(kv, layer, batch, k, v, n_max, dev, what, written):
+def _kv_rows(kv, layer, batch, k, v, n_max, what, written):
     """PeagleKVRows of k / v [n_layers, batch, n_max, n_kv_heads, head_dim] (layer >= 0: without
     the first axis): float32 or bfloat16, any strides with the last axis contiguous."""
-    import torch
-
-    lead = (kv.n_layers,) if layer < 0 else ()
-    dt = k.dtype
-    if dt != torch.float32 and dt != torch.bfloat16:
+    dt, sh, sd = k.dtype, k.shape, k.stride()
+    whole = layer < 0
+    if dt is torch.bfloat16:
+        code = PEAGLE_BF16
+    elif dt is torch.float32:
+        code = PEAGLE_F32
+    else:
         _refuse(what, f"rows are float32 or bfloat16, got {dt}")
-    sh, sd = k.shape, k.stride()
-    if len(sh) != len(lead) + 4 or sh[:-4] != lead or sh[-4] < batch or sh[-3] < n_max or \
-            sh[-2] != kv.n_kv_heads or sh[-1] != kv.head_dim or v.shape != sh or \
-            v.stride() != sd or sd[-1] != 1:
-        _refuse(what, f"rows {tuple(sh)} / {tuple(v.shape)} (strides {sd} / {v.stride()}) do not "
-                      f"fit layer {layer}, batch {batch}, n_max {n_max}")
+    if len(sh) != (5 if whole else 4) or v.shape != sh or v.stride() != sd:
+        _refuse(what, f"rows {tuple(sh)} and {tuple(v.shape)} (strides {sd}, {v.stride()}) are "
+                      f"not alike or not of {5 if whole else 4} axes")
+    if (whole and sh[0] != kv.n_layers) or sh[-4] < batch or sh[-3] < n_max or \
+            sh[-2] != kv.n_kv_heads or sh[-1] != kv.head_dim or sd[-1] != 1:
+        _refuse(what, f"rows {tuple(sh)} with strides {sd} do not fit layer {layer}, batch "
+                      f"{batch}, n_max {n_max}")
     if written and any(n > 1 and s == 0 for n, s in zip(sh, sd)):
         _refuse(what, "the rows to be written overlap")
-    return PeagleKVRows(k=_on(k, dev, dt, what), v=_on(v, dev, dt, what),
-                        layer_stride=sd[0] if lead else 0, batch_stride=sd[-4],
-                        token_stride=sd[-3], head_stride=sd[-2],
-                        dtype=PEAGLE_F32 if dt == torch.float32 else PEAGLE_BF16)
+    dev = kv._device
+    return PeagleKVRows(_on(k, dev, dt, what), _on(v, dev, dt, what), sd[0] if whole else 0,
+                        sd[-4], sd[-3], sd[-2], code)
 
 
 def _lens(t, batch, dev, what):
-    import torch
-
     if t is None:
         return None
-    if t.numel() < batch or not t.is_contiguous():
-        _refuse(what, f"{batch} contiguous int32 are wanted")
-    return _on(t, dev, torch.int32, what)
+    if t.dtype is not torch.int32 or t.device != dev or t.numel() < batch or \
+            not t.is_contiguous():
+        _refuse(what, f"{batch} contiguous int32 on {dev} are wanted")
+    return t.data_ptr()
 
 
 def peagle_append_kv_quant(kv: PeagleKVQuant, batch, seq_lens, n_commit, k_rows, v_rows, n_max,
@@ -506,11 +507,14 @@ def peagle_append_kv_quant(kv: PeagleKVQuant, batch, seq_lens, n_commit, k_rows,
     bfloat16 [n_layers, batch, >= n_max, n_kv_heads, head_dim] (layer >= 0: without the first
     axis), any strides with the last axis contiguous."""
     what = "peagle_append_kv_quant"
-    dev, s = _quant_call(kv, what, stream)
-    rows = _kv_rows(kv, layer, batch, k_rows, v_rows, n_max, dev, what, False)
-    _check(lib().peagle_append_kv_quant(kv, layer, batch, _lens(seq_lens, batch, dev, what),
-                                        _lens(n_commit, batch, dev, what), n_extra, rows, n_max,
-                                        1 if advance else 0, s), what)
+    s = _quant_stream(kv, what, stream)
+    rows = _kv_rows(kv, layer, batch, k_rows, v_rows, n_max, what, False)
+    dev = kv._device
+    rc = lib().peagle_append_kv_quant(kv, layer, batch, _lens(seq_lens, batch, dev, what),
+                                      _lens(n_commit, batch, dev, what), n_extra, rows, n_max,
+                                      1 if advance else 0, s)
+    if rc:
+        raise PeagleError(rc, what)
 
 
 def peagle_read_kv_quant(kv: PeagleKVQuant, batch, counts, out_k, out_v, n_max, layer=-1,
@@ -518,10 +522,13 @@ def peagle_read_kv_quant(kv: PeagleKVQuant, batch, counts, out_k, out_v, n_max, 
     """Read slots of the 8-bit cache back into rows laid out like peagle_append_kv_quant's
     (include/peagle.h)."""
     what = "peagle_read_kv_quant"
-    dev, s = _quant_call(kv, what, stream)
-    rows = _kv_rows(kv, layer, batch, out_k, out_v, n_max, dev, what, True)
-    _check(lib().peagle_read_kv_quant(kv, layer, batch, _lens(starts, batch, dev, what),
-                                      _lens(counts, batch, dev, what), rows, n_max, s), what)
+    s = _quant_stream(kv, what, stream)
+    rows = _kv_rows(kv, layer, batch, out_k, out_v, n_max, what, True)
+    dev = kv._device
+    rc = lib().peagle_read_kv_quant(kv, layer, batch, _lens(starts, batch, dev, what),
+                                    _lens(counts, batch, dev, what), rows, n_max, s)
+    if rc:
+        raise PeagleError(rc, what)
 
 
 def peagle_decode_attention_quant_workspace(kv: PeagleKVQuant, batch, K, n_q_heads) -> int:
@@ -538,29 +545,32 @@ def peagle_decode_attention_quant(kv: PeagleKVQuant, layer, batch, K, n_q_heads,
     """Decode attention over one layer of the 8-bit cache (include/peagle.h).  q, out: float32 or
     bfloat16 [batch * K, n_q_heads, head_dim], rows of q any stride; workspace: a contiguous
     CUDA tensor; scale: 1 / sqrt(head_dim) when None."""
-    import torch
-
     what = "peagle_decode_attention_quant"
-    dev, s = _quant_call(kv, what, stream)
-    hd, dt = kv.head_dim, q.dtype
-    shape = (batch * K, n_q_heads, hd)
-    if dt != torch.float32 and dt != torch.bfloat16:
+    s = _quant_stream(kv, what, stream)
+    dev, hd, dt, rows = kv._device, kv.head_dim, q.dtype, batch * K
+    shape = (rows, n_q_heads, hd)
+    if dt is torch.bfloat16:
+        code = PEAGLE_BF16
+    elif dt is torch.float32:
+        code = PEAGLE_F32
+    else:
         _refuse(what, f"queries are float32 or bfloat16, got {dt}")
     sd = q.stride()
     if q.shape != shape or out.shape != shape or sd[2] != 1 or (n_q_heads > 1 and sd[1] != hd) or \
-            not out.is_contiguous() or (batch * K > 1 and sd[0] < n_q_heads * hd):
+            not out.is_contiguous() or (rows > 1 and sd[0] < n_q_heads * hd):
         _refuse(what, f"q and out are {shape}, q's rows contiguous, out contiguous")
     if out_lse is not None and (out_lse.shape != shape[:2] or not out_lse.is_contiguous()):
         _refuse(what, f"out_lse is {shape[:2]}, contiguous")
     if not workspace.is_contiguous() or workspace.device != dev:
         _refuse(what, f"a contiguous workspace on {dev} is wanted")
-    _check(lib().peagle_decode_attention_quant(
-        kv, layer, batch, K, n_q_heads, _on(q, dev, dt, what),
-        PEAGLE_F32 if dt == torch.float32 else PEAGLE_BF16, sd[0] if batch * K > 1 else 0,
+    rc = lib().peagle_decode_attention_quant(
+        kv, layer, batch, K, n_q_heads, _on(q, dev, dt, what), code, sd[0] if rows > 1 else 0,
         _lens(seq_lens, batch, dev, what), 1 if causal else 0, window,
         hd ** -0.5 if scale is None else scale, _on(out, dev, dt, what),
         _on(out_lse, dev, torch.float32, what), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), s), what)
+        workspace.numel() * workspace.element_size(), s)
+    if rc:
+        raise PeagleError(rc, what)
 
 
 def peagle_device_error_bits(ctx: Context) -> int:

@@ -38,116 +38,155 @@ __device__ __forceinline__ bool rows_fit(int at, int64_t n, int n_max, int capac
   return true;
 }
 
-// 16 consecutive row elements as fp32 (16-byte aligned by the host's checks).
-__device__ __forceinline__ void load16(const float* p, float* x) {
+// 16 consecutive elements of a slot, as they were loaded: rows (16-byte aligned by the host's
+// checks) or codes.
+template <typename T>
+struct Piece {
+  static constexpr int N = sizeof(T);  // 16-byte words
+  uint4 u[N];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+    for (int i = 0; i < N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-}
-__device__ __forceinline__ void load16(const bf16* p, float* x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  // Element 4 w + j of the row's 32-bit words' elements.
+  __device__ __forceinline__ void elements(int w, float* x) const {
+    if (sizeof(T) == 4) {
+      const uint4 f = u[w % N];
+      x[0] = __uint_as_float(f.x), x[1] = __uint_as_float(f.y);
+      x[2] = __uint_as_float(f.z), x[3] = __uint_as_float(f.w);
+    } else {
+      const uint32_t a = w & 1 ? u[w / 2 % N].z : u[w / 2 % N].x;
+      const uint32_t b = w & 1 ? u[w / 2 % N].w : u[w / 2 % N].y;
+      x[0] = __uint_as_float(a << 16), x[1] = __uint_as_float(a & 0xffff0000u);
+      x[2] = __uint_as_float(b << 16), x[3] = __uint_as_float(b & 0xffff0000u);
     }
   }
+  // The elements of four codes, with their scale.
+  __device__ __forceinline__ static void decode(uint32_t c, float s, float* x) {
+    const float2 a = cvt_e4m3x2_f32x2((uint16_t)c), b = cvt_e4m3x2_f32x2((uint16_t)(c >> 16));
+    x[0] = a.x * s, x[1] = a.y * s, x[2] = b.x * s, x[3] = b.y * s;
+  }
+};
+
+__device__ __forceinline__ unsigned finite_bits(float x) {
+  const unsigned m = __float_as_uint(x) & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
 }
 
-// A CTA encodes one block of slots of one (layer, request, kv head), keys or values.
+// A CTA encodes U / 2 consecutive blocks of slots of one (layer, request, kv head), keys and
+// values: U units.
 //
 //   s = 2^e, the smallest with amax <= 448 s over the block's live values (448 = 1.75 x 2^8, so
 //   e = E - 8 for amax = 1.m x 2^E with 1.m <= 1.75, else E - 7);  code = round(x / s)
 //
-// Each thread holds 16 consecutive elements of one slot in registers: one pass over the rows
-// (two or four 16-byte loads), a maximum over the CTA, one 16-byte store.  Scaling by a power
-// of two is exact, so the only rounding is the conversion to e4m3; the committed slots of the
-// first block are read back (16 codes a thread) and stored again only if their scale changed.
-// Heads run fastest over the grid: the rows of one token lie side by side.
-template <int HD, int BLOCK, typename T>
+// Each thread holds 16 consecutive elements of one slot of every unit in registers, as loaded:
+// one pass over the rows (two or four 16-byte loads a unit), one exchange of maxima over the
+// CTA, one 16-byte store a unit.  Scaling by a power of two is exact, so the only rounding is the
+// conversion to e4m3; the committed slots of the first block are read back (16 codes a thread)
+// and stored again only if their scale changed.  Bound by memory for long rows, where U = 4
+// units in flight a CTA hide the chain length -> rows -> maximum -> codes; by latency for a draft
+// block, where U = 2 spreads the units over more CTAs.  Heads run fastest over the grid: the rows
+// of one token lie side by side.
+template <int HD, int BLOCK, int U, typename T>
 __global__ void __launch_bounds__(BLOCK* HD / 16)
     append_quant_kernel(CacheArgs c, RowsArgs rows, const int* seq_lens, const int* n_commit,
                         int n_extra, int n_max) {
   pdl_enter();
   constexpr int THREADS = BLOCK * HD / 16, WARPS = THREADS / 32;
-  __shared__ unsigned red[WARPS];
-  const int h = blockIdx.x % c.heads, rest = blockIdx.x / c.heads;
-  const bool value = rest & 1;
+  __shared__ unsigned red[U][WARPS];
+  const int h = blockIdx.x % c.heads;
   const int b = blockIdx.y, l = blockIdx.z;
   const int at = seq_lens[b];
   const int64_t n = (int64_t)(n_commit ? n_commit[b] : 0) + n_extra;
   if (!rows_fit(at, n, n_max, c.capacity, c.errors,
                 blockIdx.x == 0 && l == 0 && threadIdx.x == 0))
     return;
-  const int block = at / BLOCK + (rest >> 1);
-  if (n == 0 || (int64_t)block * BLOCK >= at + n) return;
+  const int first = at / BLOCK + (int)(blockIdx.x / c.heads) * (U / 2);
+  const int64_t end = at + n;  // (the first slot behind the rows)
+  if (n == 0 || (int64_t)first * BLOCK >= end) return;
 
   const int t = threadIdx.x / (HD / 16), d = threadIdx.x % (HD / 16) * 16;
-  const int slot = block * BLOCK + t;
-  const bool old = slot < at, fresh = !old && slot < at + n;
   const int64_t unit = ((int64_t)(c.layer0 + l) * c.batch + b) * c.heads + h;
-  uint8_t* code = (value ? c.v : c.k) + (unit * c.capacity + slot) * HD + d;
-  float* scale = (value ? c.v_scale : c.k_scale) + unit * (c.capacity / BLOCK) + block;
+  const int64_t row0 = l * rows.layer + b * rows.batch + h * rows.head + d;
+  // what this thread's slot of a unit is: a new row, a committed one, or neither
+  auto fresh = [&](int u) {
+    const int slot = (first + u / 2) * BLOCK + t;
+    return slot >= at && slot < end;
+  };
+  auto old = [&](int u) { return (first + u / 2) * BLOCK + t < at; };
+  auto code = [&](int u) {
+    return (u & 1 ? c.v : c.k) + (unit * c.capacity + (first + u / 2) * BLOCK + t) * HD + d;
+  };
+  auto scale = [&](int u) {
+    return (u & 1 ? c.v_scale : c.k_scale) + unit * (c.capacity / BLOCK) + first + u / 2;
+  };
 
-  float x[16];
-  float was = 0.f;
-  if (fresh) {
-    const T* src = reinterpret_cast<const T*>(value ? rows.v : rows.k) + l * rows.layer +
-                   b * rows.batch + (int64_t)(slot - at) * rows.token + h * rows.head + d;
-    load16(src, x);
-  } else if (old) {
-    was = *scale;
-    const uint4 u = *reinterpret_cast<const uint4*>(code);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  Piece<T> x[U];
+  float was[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = cvt_e4m3x2_f32x2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-      x[2 * i] = f.x * was, x[2 * i + 1] = f.y * was;
+  for (int u = 0; u < U; ++u) {
+    was[u] = 0.f;
+    if (fresh(u)) {
+      const int64_t row = (first + u / 2) * BLOCK + t - at;
+      x[u].load(reinterpret_cast<const T*>(u & 1 ? rows.v : rows.k) + row0 + row * rows.token);
+    } else if (u < 2 && old(u)) {
+      was[u] = *scale(u);
+      x[u].u[0] = *reinterpret_cast<const uint4*>(code(u));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
   }
+  auto elements = [&](int u, int w, float* y) {
+    if (u < 2 && old(u)) {
+      const uint4 q = x[u].u[0];
+      Piece<T>::decode(w == 0 ? q.x : w == 1 ? q.y : w == 2 ? q.z : q.w, was[u], y);
+    } else {
+      x[u].elements(w, y);
+    }
+  };
 
-  // the largest finite magnitude, as bits (their order is the magnitudes' order)
-  unsigned top = 0;
+  // the largest finite magnitudes, as bits (their order is the magnitudes' order)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const unsigned m = __float_as_uint(x[i]) & 0x7fffffffu;
-    top = max(top, m < 0x7f800000u ? m : 0u);
+  for (int u = 0; u < U; ++u) {
+    unsigned top = 0;
+    if (fresh(u) || (u < 2 && old(u))) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float y[4];
+        elements(u, w, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, finite_bits(y[j]));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) red[u][threadIdx.x >> 5] = top;
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) top = max(top, red[i]);
-
-  // adding 0x1fffff carries into the exponent when the fraction is above 1.75's
-  int e = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
-  e = top ? min(max(e, -40), 120) : 0;
-  const float s = __uint_as_float((unsigned)(127 + e) << 23);
-  const float inv = __uint_as_float((unsigned)(127 - e) << 23);
-  if (fresh || (old && s != was)) {
-    uint32_t w[4];
+  for (int u = 0; u < U; ++u) {
+    if ((int64_t)(first + u / 2) * BLOCK >= end) break;
+    unsigned top = red[u][threadIdx.x % WARPS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[4];
+    for (int o = WARPS / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // adding 0x1fffff carries into the exponent when the fraction is above 1.75's
+    int e = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
+    e = top ? min(max(e, -40), 120) : 0;
+    const float s = __uint_as_float((unsigned)(127 + e) << 23);
+    const float inv = __uint_as_float((unsigned)(127 - e) << 23);
+    if (fresh(u) || (u < 2 && old(u) && s != was[u])) {
+      uint32_t q[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = x[4 * i + j];
-        // (the conversion saturates: an infinity would become 448)
-        y[j] = fabsf(v) == INFINITY ? NAN : v * inv;
+      for (int w = 0; w < 4; ++w) {
+        float y[4];
+        elements(u, w, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // (the conversion saturates: an infinity would become 448)
+          y[j] = fabsf(y[j]) == INFINITY ? NAN : y[j] * inv;
+        q[w] = (uint32_t)cvt_f32x2_e4m3x2(y[0], y[1]) |
+               (uint32_t)cvt_f32x2_e4m3x2(y[2], y[3]) << 16;
       }
-      w[i] = (uint32_t)cvt_f32x2_e4m3x2(y[0], y[1]) | (uint32_t)cvt_f32x2_e4m3x2(y[2], y[3]) << 16;
+      *reinterpret_cast<uint4*>(code(u)) = make_uint4(q[0], q[1], q[2], q[3]);
     }
-    *reinterpret_cast<uint4*>(code) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (threadIdx.x == 0) *scale(u) = s;
   }
-  if (threadIdx.x == 0) *scale = s;
 }
 
 __global__ void __launch_bounds__(256)
@@ -260,15 +299,16 @@ static RowsArgs rows_args(const peagle_kv_rows* r) {
 }
 
 template <int HD, int BLOCK>
-static cudaError_t launch_append(int dtype, dim3 grid, cudaStream_t s, const CacheArgs& c,
-                                 const RowsArgs& r, const int* seq_lens, const int* n_commit,
-                                 int n_extra, int n_max) {
-  const dim3 threads(BLOCK * HD / 16);
-  return dtype == PEAGLE_F32
-             ? launch_pdl(append_quant_kernel<HD, BLOCK, float>, grid, threads, 0, s, c, r,
-                          seq_lens, n_commit, n_extra, n_max)
-             : launch_pdl(append_quant_kernel<HD, BLOCK, bf16>, grid, threads, 0, s, c, r,
-                          seq_lens, n_commit, n_extra, n_max);
+static cudaError_t launch_append(int dtype, int units, dim3 grid, cudaStream_t s,
+                                 const CacheArgs& c, const RowsArgs& r, const int* seq_lens,
+                                 const int* n_commit, int n_extra, int n_max) {
+  auto go = [&](void (*kernel)(CacheArgs, RowsArgs, const int*, const int*, int, int)) {
+    return launch_pdl(kernel, grid, dim3(BLOCK * HD / 16), 0, s, c, r, seq_lens, n_commit, n_extra,
+                      n_max);
+  };
+  if (dtype == PEAGLE_F32) return go(append_quant_kernel<HD, BLOCK, 2, float>);
+  return go(units == 2 ? append_quant_kernel<HD, BLOCK, 2, bf16>
+                       : append_quant_kernel<HD, BLOCK, 4, bf16>);
 }
 
 }  // namespace kvq
@@ -291,7 +331,9 @@ extern "C" int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, 
   cudaStream_t s = (cudaStream_t)stream;
   // the blocks that n_max rows can touch, wherever the first of them starts
   const int64_t blocks = ((int64_t)n_max + kv->block - 2) / kv->block + 1;
-  const int64_t gx = blocks * 2 * kv->n_kv_heads;
+  // (fp32 rows have as many bytes in flight with two units as bf16 ones with four)
+  const int units = blocks <= 4 || rows->dtype == PEAGLE_F32 ? 2 : 4;
+  const int64_t gx = (blocks + units / 2 - 1) / (units / 2) * kv->n_kv_heads;
   if (gx > INT32_MAX) return PEAGLE_ERR_INVALID;
   const dim3 grid((unsigned)gx, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
   const CacheArgs c = cache_args(kv, layer);
@@ -299,8 +341,8 @@ extern "C" int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, 
   cudaError_t e = cudaErrorInvalidValue;
 #define PEAGLE_APPEND(HD, BLOCK)                                                          \
   if (kv->head_dim == HD && kv->block == BLOCK)                                           \
-    e = launch_append<HD, BLOCK>(rows->dtype, grid, s, c, r, seq_lens, n_commit, n_extra, \
-                                 n_max);
+    e = launch_append<HD, BLOCK>(rows->dtype, units, grid, s, c, r, seq_lens, n_commit,  \
+                                 n_extra, n_max);
   PEAGLE_APPEND(64, 16)
   PEAGLE_APPEND(64, 32)
   PEAGLE_APPEND(64, 64)

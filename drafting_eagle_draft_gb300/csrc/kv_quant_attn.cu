@@ -51,7 +51,7 @@ namespace kvq {
 constexpr int CTAS = 152;      // GB300's SMs
 constexpr int TILE = 32;       // slots a unit
 constexpr int ENTRY = 8;       // what a (request, kv head) costs besides its tiles, in tiles
-constexpr int JOIN_WARPS = 8;  // of the second kernel
+constexpr int JOIN_WARPS = 4;  // of the second kernel
 constexpr int MAX_ROWS = 128;  // query rows a kv head
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no slot
@@ -893,15 +893,18 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 }
 
 // Joins the pieces of the (request, kv head)s that several CTAs worked on: block (c, z) takes the
-// one whose first piece CTA c holds, a warp 32 fragments of it (ntiles x HD / 16 of them in
-// all, cut into gridDim.y = HD / 16 parts) over a part of the pieces.  Also writes the rows of requests
-// that no row of which sees a slot.
+// one whose first piece CTA c holds, and of its ntiles x HD / 16 columns of 32 fragments the z-th
+// part; the block's warps split a column's pieces.  Bound by the latency of the pieces' loads
+// (they are in L2), so a warp has up to 8 of them in flight and goes over them once.  Also writes
+// the rows of requests no row of which sees a slot.
 template <int HD, typename T>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a, int ntiles) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a,
+                                                                          int ntiles) {
   pdl_enter();
   __shared__ float4 red_o[JOIN_WARPS][32];
-  __shared__ float red_m[JOIN_WARPS][8], red_l[JOIN_WARPS][8];
+  __shared__ float4 red_ml[JOIN_WARPS][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 d = a.desc[blockIdx.x];
   if (blockIdx.y == 0) {
     for (int b = blockIdx.x; b < a.batch; b += CTAS) {
       const int len = a.seq_lens[b];
@@ -914,74 +917,79 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
         for (int64_t i = threadIdx.x; i < rows; i += JOIN_WARPS * 32) a.lse[b * rows + i] = -INFINITY;
     }
   }
-  const int4 d = a.desc[blockIdx.x];
   if (d.x < 0) return;
-  const int cols = ntiles * (HD / 16), per = cols / gridDim.y;  // 32 fragments each
-  const int parts = max(1, JOIN_WARPS / per);                        // warps that share one
+  const int cols = ntiles * (HD / 16);
+  const int col0 = cols * blockIdx.y / gridDim.y, col1 = cols * (blockIdx.y + 1) / gridDim.y;
   const int pieces = d.z - (int)blockIdx.x + 1;
   const size_t slot = (size_t)ntiles * 8 * (HD + 2);
+  // (piece p > 0 is the head of CTA c + p's share: slot 0; the first is the tail of c's: slot 1)
+  const float* base = a.work + (size_t)blockIdx.x * 2 * slot;
   const int r = lane >> 2, c = lane & 3;
-  auto piece = [&](int p) {
-    return a.work + ((size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * slot;
-  };
-  for (int at = warp / parts; at < per; at += JOIN_WARPS / parts) {
-    const int col = blockIdx.y * per + at, nt = col / (HD / 16), i = col % (HD / 16);
-    const int row = nt * 8 + 2 * c, part = warp % parts;
-    float m0 = NO_REF, m1 = NO_REF;
-#pragma unroll 4
-    for (int p = part; p < pieces; p += parts) {
-      const float4 f = *reinterpret_cast<const float4*>(piece(p) + 2 * row);
-      m0 = fmaxf(m0, f.x), m1 = fmaxf(m1, f.z);
-    }
-    float l0 = 0.f, l1 = 0.f;
+  for (int col = col0; col < col1; ++col) {
+    const int nt = col / (HD / 16), i = col % (HD / 16), row = nt * 8 + 2 * c;
+    float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = part; p < pieces; p += parts) {
-      const float* s = piece(p);
-      const float4 f = *reinterpret_cast<const float4*>(s + 2 * row);
-      const float4 g = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
-      const float f0 = ex2(f.x - m0), f1 = ex2(f.z - m1);
-      l0 = fmaf(f.y, f0, l0), l1 = fmaf(f.w, f1, l1);
-      o.x = fmaf(g.x, f0, o.x), o.y = fmaf(g.y, f1, o.y);
-      o.z = fmaf(g.z, f0, o.z), o.w = fmaf(g.w, f1, o.w);
-    }
-    if (parts > 1) {
-      // (per <= JOIN_WARPS / parts: every warp is in this loop once, or not at all)
-      red_o[warp][lane] = o;
-      if (r == 0) {
-        red_m[warp][2 * c] = m0, red_m[warp][2 * c + 1] = m1;
-        red_l[warp][2 * c] = l0, red_l[warp][2 * c + 1] = l1;
+    constexpr int BATCH = 8;
+    for (int p0 = warp; p0 < pieces; p0 += BATCH * JOIN_WARPS) {
+      float4 f[BATCH], g[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int p = p0 + k * JOIN_WARPS;
+        const float* s = base + ((size_t)2 * p + (p == 0 ? 1 : 0)) * slot;
+        f[k] = make_float4(NO_REF, 0.f, NO_REF, 0.f);
+        g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < pieces) {
+          f[k] = *reinterpret_cast<const float4*>(s + 2 * row);
+          g[k] = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
+        }
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / parts), "r"(32 * parts) : "memory");
-      if (part) continue;
-      const float n0 = m0, n1 = m1;
-      for (int w = 1; w < parts; ++w) {
-        m0 = fmaxf(m0, red_m[warp + w][2 * c]);
-        m1 = fmaxf(m1, red_m[warp + w][2 * c + 1]);
-      }
-      float f0 = ex2(n0 - m0), f1 = ex2(n1 - m1);
-      l0 *= f0, l1 *= f1;
-      o = make_float4(o.x * f0, o.y * f1, o.z * f0, o.w * f1);
-      for (int w = 1; w < parts; ++w) {
-        f0 = ex2(red_m[warp + w][2 * c] - m0), f1 = ex2(red_m[warp + w][2 * c + 1] - m1);
-        const float4 g = red_o[warp + w][lane];
-        l0 = fmaf(red_l[warp + w][2 * c], f0, l0), l1 = fmaf(red_l[warp + w][2 * c + 1], f1, l1);
-        o.x = fmaf(g.x, f0, o.x), o.y = fmaf(g.y, f1, o.y);
-        o.z = fmaf(g.z, f0, o.z), o.w = fmaf(g.w, f1, o.w);
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) n0 = fmaxf(n0, f[k].x), n1 = fmaxf(n1, f[k].z);
+      float x0 = ex2(m0 - n0), x1 = ex2(m1 - n1);
+      l0 *= x0, l1 *= x1;
+      o = make_float4(o.x * x0, o.y * x1, o.z * x0, o.w * x1);
+      m0 = n0, m1 = n1;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        x0 = ex2(f[k].x - m0), x1 = ex2(f[k].z - m1);
+        l0 = fmaf(f[k].y, x0, l0), l1 = fmaf(f[k].w, x1, l1);
+        o.x = fmaf(g[k].x, x0, o.x), o.y = fmaf(g[k].y, x1, o.y);
+        o.z = fmaf(g[k].z, x0, o.z), o.w = fmaf(g[k].w, x1, o.w);
       }
     }
-    float inv;
-    const int nq = a.nkv * a.G, j0 = row / a.G, j1 = (row + 1) / a.G;
-    if (row < a.K * a.G) {
-      T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
-                             i == 0 && r == 0, inv);
-      store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
+    red_o[warp][lane] = o;
+    if (r == 0) red_ml[warp][c] = make_float4(m0, l0, m1, l1);
+    __syncthreads();
+    if (warp == (col - col0) % JOIN_WARPS) {
+      l0 = l1 = 0.f;
+      m0 = m1 = NO_REF;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < JOIN_WARPS; ++w)
+        m0 = fmaxf(m0, red_ml[w][c].x), m1 = fmaxf(m1, red_ml[w][c].z);
+#pragma unroll
+      for (int w = 0; w < JOIN_WARPS; ++w) {
+        const float4 f = red_ml[w][c], g = red_o[w][lane];
+        const float x0 = ex2(f.x - m0), x1 = ex2(f.z - m1);
+        l0 = fmaf(f.y, x0, l0), l1 = fmaf(f.w, x1, l1);
+        o.x = fmaf(g.x, x0, o.x), o.y = fmaf(g.y, x1, o.y);
+        o.z = fmaf(g.z, x0, o.z), o.w = fmaf(g.w, x1, o.w);
+      }
+      float inv;
+      const int nq = a.nkv * a.G, j0 = row / a.G, j1 = (row + 1) / a.G;
+      if (row < a.K * a.G) {
+        T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
+                               i == 0 && r == 0, inv);
+        store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
+      }
+      if (row + 1 < a.K * a.G) {
+        T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
+                               i == 0 && r == 0, inv);
+        store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
+      }
     }
-    if (row + 1 < a.K * a.G) {
-      T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
-                             i == 0 && r == 0, inv);
-      store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
-    }
+    if (col + 1 < col1) __syncthreads();
   }
 }
 
@@ -1024,7 +1032,8 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_quant_join_kernel<HD, typename std::conditional<F32, float, bf16>::type>,
-                    dim3(CTAS, HD / 16), dim3(JOIN_WARPS * 32), 0, s, a, p.ntiles());
+                    dim3(CTAS, cdiv(p.ntiles() * (HD / 16), 2)), dim3(JOIN_WARPS * 32), 0, s, a,
+                    p.ntiles());
 }
 
 }  // namespace kvq
