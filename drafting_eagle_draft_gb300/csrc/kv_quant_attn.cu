@@ -35,11 +35,7 @@
 // cp.async ring in shared memory that runs on across (request, kv head) boundaries.  At the end
 // of one its streams are joined in shared memory; one that lies whole in a CTA is written out,
 // pieces of one go to the workspace and the second kernel joins them.
-#include <math.h>
-
-#include <type_traits>
-
-#include "kv_quant.cuh"
+#include "kv_quant_attn.cuh"
 
 namespace peagle {
 namespace kvq {
@@ -48,81 +44,11 @@ namespace kvq {
 #define PEAGLE_W64 8
 #define PEAGLE_MOST64 4
 #endif
-constexpr int CTAS = 152;      // GB300's SMs
 constexpr int TILE = 32;       // slots a unit
 constexpr int ENTRY = 8;       // what a (request, kv head) costs besides its tiles, in tiles
 constexpr int JOIN_WARPS = 4;  // of the second kernel
-constexpr int MAX_ROWS = 128;  // query rows a kv head
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no slot
+typedef Segment<TILE, ENTRY> Seg;
 
-struct AttnQuantArgs {
-  const uint8_t* k;        // this layer's codes [batch slots][nkv][capacity][hd]
-  const uint8_t* v;
-  const float* k_scale;    // [batch slots][nkv][capacity / block]
-  const float* v_scale;
-  const void* q;
-  int64_t q_stride;
-  void* out;
-  float* lse;
-  const int* seq_lens;
-  int* errors;
-  int4* desc;              // [CTAS]: request, kv head, last CTA of the piece chain (or -1)
-  float* work;             // [CTAS][2] slots of partial results
-  int batch, K, G, nkv, capacity, block_shift, causal, window;
-  int groups;              // warps that share a stream's tiles, each NT x 8 query rows
-  int stages;
-  float scale;             // of the scores, with log2(e)
-};
-
-// Slots [begin, end) that row j of a request of length len sees; empty when end <= begin.
-__device__ __forceinline__ int row_begin(const AttnQuantArgs& a, int len, int j) {
-  return a.window > 0 ? max(0, len + j - a.window + 1) : 0;
-}
-__device__ __forceinline__ int row_end(const AttnQuantArgs& a, int len, int j) {
-  return a.causal ? len + j + 1 : len;
-}
-__device__ __forceinline__ bool request_fits(const AttnQuantArgs& a, int len) {
-  return len >= 0 && len <= a.capacity - (a.causal ? a.K : 0);
-}
-// Tiles [first, first + count) that some row of a request sees.
-__device__ __forceinline__ int request_tiles(const AttnQuantArgs& a, int len, int& first) {
-  first = 0;
-  if (!request_fits(a, len)) return 0;
-  const int lo = row_begin(a, len, 0), hi = row_end(a, len, a.K - 1);
-  if (hi <= lo) return 0;
-  first = lo / TILE;
-  return (hi + TILE - 1) / TILE - first;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t h) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -201,29 +127,6 @@ __device__ __forceinline__ float power2(int e) {
   return __uint_as_float((unsigned)(127 + e) << 23);
 }
 
-// Where a CTA's walk over the units stands: one (request, kv head).
-struct Segment {
-  int b, h, len;
-  int first_tile, tiles;
-  int at;  // of its first tile, relative to the CTA's share (negative: it began before)
-  // The next one; false when it is not in the share of n any more.
-  __device__ __forceinline__ bool next(const AttnQuantArgs& a, int n) {
-    at += tiles + ENTRY;
-    if (at >= n) return false;
-    if (++h < a.nkv) return true;
-    h = 0;
-    do {
-      if (++b >= a.batch) return false;
-      len = a.seq_lens[b];
-      tiles = request_tiles(a, len, first_tile);
-    } while (!tiles);
-    return true;
-  }
-};
-
-// Query operands.  prepare() makes the operands of one tile of 8 rows in shared memory (a warp;
-// the CTA's warps share the tiles of a (request, kv head)), load() takes NT tiles' into a warp's
-// registers, scores() multiplies 16 keys by them.
 // A lane's query elements: 16 consecutive ones of row 8 tile + r at head dims 16c and, for
 // head_dim 128, 64 + 16c, as they are stored (zeros past the last row).
 template <int HD, bool F32>
@@ -359,11 +262,12 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 template <int HD, int NT, bool F32>
 struct Running {
   // 2^SHIFT is where the largest weight is put, 2^LIM what it may grow to before the reference
-  // moves (f16 ends at 2^16).  Room to grow saves moves: with the heavy-tailed scores of real
-  // keys 8 of a stream's first 32 tiles move some row's reference with 2^15 of it, 14 with 2^8.
-  // The price is at the other end, where weights below 2^-14 lose bits of their 11; the second
-  // part of an fp32 weight needs that range, so there the largest is put high.
-  static constexpr float SHIFT = F32 ? 13.f : 0.f, LIM = 15.f;
+  // moves (f16 ends at 2^16).  Room to grow saves moves: a tile of heavy-tailed scores (tokens of
+  // lognormal size) moved some row's reference in 14 of a stream's first 32 tiles with 2^8 of it,
+  // in 5 with 2^19; normal scores hardly ever after the first tile.  The price is at the other
+  // end, where weights below 2^-14 lose bits of their 11; the second part of an fp32 weight needs
+  // that range, so there the largest is put high.
+  static constexpr float SHIFT = F32 ? 13.f : -4.f, LIM = 15.f;
   float o[HD / 16][NT][4];
   float m[NT][2], l[NT][2];
   unsigned started;  // bit 2 nt + e: the row has seen a slot (its m counts)
@@ -475,7 +379,8 @@ struct Running {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const bool any = !(top == -INFINITY), had = started >> (2 * nt + e) & 1;
-        const float by = any && (top > LIM || !had) ? top - SHIFT : 0.f;
+        // (rows below their limit move up too: that is room for later tiles)
+        const float by = !any ? 0.f : had ? fmaxf(top - SHIFT, 0.f) : top - SHIFT;
         const float f = had ? ex2(-by) : 1.f;  // (nothing was summed before the first slot)
         if (any) started |= 1u << (2 * nt + e);
         m[nt][e] += by;
@@ -566,50 +471,6 @@ struct Running {
   }
 };
 
-// Two values of a row at consecutive head dims.
-__device__ __forceinline__ void store2(float* p, float x, float y) {
-  *reinterpret_cast<float2*>(p) = make_float2(x, y);
-}
-__device__ __forceinline__ void store2(bf16* p, float x, float y) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
-}
-
-// A row's result: its address in out and 1 / l (0 for a row that has seen nothing); writes its lse
-// when `first`.  at: the row's place among its request's rows and heads.
-template <typename T>
-__device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int at, float m,
-                                         float l, bool first, float& inv) {
-  const bool none = m == NO_REF && l == 0.f;  // (a row of NaN scores has no reference either)
-  inv = none ? 0.f : 1.f / l;
-  const int64_t to = (int64_t)req * a.K * (a.nkv * a.G) + at;
-  if (first && a.lse) a.lse[to] = none ? -INFINITY : (m + log2f(l)) * LN2;
-  return (T*)a.out + to * hd;
-}
-
-// Sum over the W warps' threads of v before this one, and over all of them.
-template <int W>
-__device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) red[wid] = x;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const long long s = red[i];
-    if (i < wid) before += s;
-    total += s;
-  }
-  return before + x - v;
-}
-
 // Parts in which the warps' O^T go through the joining buffer.  At head_dim 128 parts leave room
 // for a third stage of the rings (NT 1 and 2; NT 3 has two either way).
 constexpr int join_passes(int hd, int nt, int w) { return hd == 64 ? 1 : nt == 2 ? 4 : 2; }
@@ -623,9 +484,6 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   constexpr int FRAG = HD / 16 * NT * 32;    // float4s of a warp's O^T
   constexpr int PASSES = join_passes(HD, NT, W), PASS = FRAG / PASSES;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ long long red[W];
-  __shared__ long long found;
-  __shared__ int found_b;
   __shared__ __align__(8) float row_m[W][NT * 8], row_l[W][NT * 8];
   __shared__ __align__(8) float row_scale[MAX_ROWS + 8];
   __shared__ uint8_t row_j[MAX_ROWS + 8];  // each query row's draft row
@@ -641,57 +499,13 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   }
   pdl_enter();
 
-  // this CTA's share of the work, and the (request, kv head) in which it begins
-  Segment seg;
-  int n;  // cost of the share
-  long long total = 0, share, lo;
-  {
-    long long cost = 0, before = 0;
-    int first;
-    auto cost_of = [&](int b) {
-      const int tiles = b < a.batch ? request_tiles(a, a.seq_lens[b], first) : 0;
-      return tiles ? (long long)(tiles + ENTRY) * a.nkv : 0;
-    };
-    for (int b0 = 0; b0 < a.batch; b0 += W * 32) {
-      const int b = b0 + threadIdx.x;
-      cost = cost_of(b);
-      if (blockIdx.x == 0 && b < a.batch && !request_fits(a, a.seq_lens[b]))
-        raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
-      long long part;
-      before = block_scan<W>(cost, red, part);
-      total += part;
-    }
-    share = (total + CTAS - 1) / CTAS;
-    // a share below 4 tiles leaves warps idle and makes pieces to join
-    share = share < 4 ? 4 : share;
-    lo = share * blockIdx.x;
-    n = (int)(total - lo < share ? total - lo : share);
-    long long base = 0;
-    for (int b0 = 0; b0 < a.batch && lo < total; b0 += W * 32) {
-      if (a.batch > W * 32) {
-        cost = cost_of(b0 + threadIdx.x);
-        long long part;
-        before = base + block_scan<W>(cost, red, part);
-        base += part;
-      }
-      if (cost && lo >= before && lo < before + cost) {
-        found = before;
-        found_b = b0 + threadIdx.x;
-      }
-    }
-    __syncthreads();
-    if (lo < total) {
-      seg.b = found_b;
-      seg.len = a.seq_lens[seg.b];
-      seg.tiles = request_tiles(a, seg.len, seg.first_tile);
-      const long long in = lo - found;
-      seg.h = (int)(in / (seg.tiles + ENTRY));
-      seg.at = ENTRY - (int)(in % (seg.tiles + ENTRY));
-    }
-    if (lo >= total || seg.at >= n) {
-      if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      return;
-    }
+  // a share below 4 tiles would leave warps idle and make pieces to join
+  Seg seg;
+  int n;
+  long long lo, share;
+  if (!find_share<W, TILE, ENTRY>(a, 4, seg, n, lo, share)) {
+    if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
   }
 
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) +
@@ -703,7 +517,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   // copies the same chunks of every tile: rows WARP_ROWS groups apart, whose places in a stage
   // follow from two offsets (rows 4 apart are permuted differently, rows 8 apart alike).
   constexpr int ROW_CHUNKS = HD / 16, WARP_ROWS = 32 / ROW_CHUNKS;
-  Segment next = seg;
+  Seg next = seg;
   int next_u = 0, next_end = 0, slot_in = 0;
   const uint8_t *next_k = nullptr, *next_v = nullptr;
   const float* next_scale = nullptr;
@@ -800,7 +614,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
     }
 
     // the next (request, kv head)'s queries arrive while this one's streams are joined
-    const Segment done = seg;
+    const Seg done = seg;
     const bool last = !seg.next(a, n);
     if (!last && warp < groups * NT) raw.fetch(a, seg.b, seg.h, warp, lane);
 
@@ -896,20 +710,21 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 // one whose first piece CTA c holds, and of its ntiles x HD / 16 columns of 32 fragments the z-th
 // part; the block's warps split a column's pieces.  Bound by the latency of the pieces' loads
 // (they are in L2), so a warp has up to 8 of them in flight and goes over them once.  Also writes
-// the rows of requests no row of which sees a slot.
-template <int HD, typename T>
+// the rows of requests no row of which sees a slot.  ROWS: outputs lie row by row, a lane's
+// float4 is four head dims of one row; else as fragments (struct Running).
+template <int HD, typename T, bool ROWS>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a,
                                                                           int ntiles) {
   pdl_enter();
   __shared__ float4 red_o[JOIN_WARPS][32];
-  __shared__ float4 red_ml[JOIN_WARPS][4];
+  __shared__ float4 red_ml[JOIN_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 d = a.desc[blockIdx.x];
   if (blockIdx.y == 0) {
     for (int b = blockIdx.x; b < a.batch; b += CTAS) {
       const int len = a.seq_lens[b];
       int first;
-      if (!request_fits(a, len) || request_tiles(a, len, first)) continue;
+      if (!request_fits(a, len) || request_tiles<TILE>(a, len, first)) continue;
       const int64_t rows = (int64_t)a.K * a.nkv * a.G;
       T* out = (T*)a.out + b * rows * HD;
       for (int64_t i = threadIdx.x; i < rows * HD; i += JOIN_WARPS * 32) st(out + i, 0.f);
@@ -926,7 +741,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
   const float* base = a.work + (size_t)blockIdx.x * 2 * slot;
   const int r = lane >> 2, c = lane & 3;
   for (int col = col0; col < col1; ++col) {
-    const int nt = col / (HD / 16), i = col % (HD / 16), row = nt * 8 + 2 * c;
+    const int nt = col / (HD / 16), i = col % (HD / 16);
+    const int row = ROWS ? (col * 32 + lane) / (HD / 4) : nt * 8 + 2 * c;
     float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int BATCH = 8;
@@ -939,7 +755,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
         f[k] = make_float4(NO_REF, 0.f, NO_REF, 0.f);
         g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < pieces) {
-          f[k] = *reinterpret_cast<const float4*>(s + 2 * row);
+          if (ROWS) {
+            const float2 x = *reinterpret_cast<const float2*>(s + 2 * row);
+            f[k] = make_float4(x.x, x.y, x.x, x.y);
+          } else {
+            f[k] = *reinterpret_cast<const float4*>(s + 2 * row);
+          }
           g[k] = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
         }
       }
@@ -959,7 +780,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
       }
     }
     red_o[warp][lane] = o;
-    if (r == 0) red_ml[warp][c] = make_float4(m0, l0, m1, l1);
+    red_ml[warp][lane] = make_float4(m0, l0, m1, l1);
     __syncthreads();
     if (warp == (col - col0) % JOIN_WARPS) {
       l0 = l1 = 0.f;
@@ -967,23 +788,34 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
       o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < JOIN_WARPS; ++w)
-        m0 = fmaxf(m0, red_ml[w][c].x), m1 = fmaxf(m1, red_ml[w][c].z);
+        m0 = fmaxf(m0, red_ml[w][lane].x), m1 = fmaxf(m1, red_ml[w][lane].z);
 #pragma unroll
       for (int w = 0; w < JOIN_WARPS; ++w) {
-        const float4 f = red_ml[w][c], g = red_o[w][lane];
+        const float4 f = red_ml[w][lane], g = red_o[w][lane];
         const float x0 = ex2(f.x - m0), x1 = ex2(f.z - m1);
         l0 = fmaf(f.y, x0, l0), l1 = fmaf(f.w, x1, l1);
         o.x = fmaf(g.x, x0, o.x), o.y = fmaf(g.y, x1, o.y);
         o.z = fmaf(g.z, x0, o.z), o.w = fmaf(g.w, x1, o.w);
       }
       float inv;
-      const int nq = a.nkv * a.G, j0 = row / a.G, j1 = (row + 1) / a.G;
-      if (row < a.K * a.G) {
+      const int nq = a.nkv * a.G;
+      if (ROWS) {
+        const int parts = a.heads / a.nkv, part = d.y % parts, of = part * a.part_rows + row;
+        if (row < a.part_rows && of < a.K * a.G) {
+          const int at = (col * 32 + lane) % (HD / 4) * 4, j = of / a.G;
+          T* out = finish_row<T>(a, HD, d.x, j * nq + d.y / parts * a.G + of - j * a.G, m0, l0,
+                                 at == 0, inv);
+          store2(out + at, o.x * inv, o.y * inv);
+          store2(out + at + 2, o.z * inv, o.w * inv);
+        }
+      }
+      const int j0 = row / a.G, j1 = (row + 1) / a.G;
+      if (!ROWS && row < a.K * a.G) {
         T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
                                i == 0 && r == 0, inv);
         store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
       }
-      if (row + 1 < a.K * a.G) {
+      if (!ROWS && row + 1 < a.K * a.G) {
         T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
                                i == 0 && r == 0, inv);
         store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
@@ -1031,9 +863,24 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_quant_join_kernel<HD, typename std::conditional<F32, float, bf16>::type>,
-                    dim3(CTAS, cdiv(p.ntiles() * (HD / 16), 2)), dim3(JOIN_WARPS * 32), 0, s, a,
-                    p.ntiles());
+  return launch_join(HD, F32, false, a, p.ntiles(), s);
+}
+
+cudaError_t launch_join(int hd, bool f32, bool rowmajor, const AttnQuantArgs& a, int ntiles,
+                        cudaStream_t s) {
+  // blocks of two columns each
+  auto go = [&](void (*kernel)(AttnQuantArgs, int)) {
+    return launch_pdl(kernel, dim3(CTAS, cdiv(ntiles * (hd / 16), 2)), dim3(JOIN_WARPS * 32), 0, s,
+                      a, ntiles);
+  };
+  if (rowmajor)
+    return go(hd == 64 ? attn_quant_join_kernel<64, bf16, true>
+                       : attn_quant_join_kernel<128, bf16, true>);
+  if (f32)
+    return go(hd == 64 ? attn_quant_join_kernel<64, float, false>
+                       : attn_quant_join_kernel<128, float, false>);
+  return go(hd == 64 ? attn_quant_join_kernel<64, bf16, false>
+                     : attn_quant_join_kernel<128, bf16, false>);
 }
 
 }  // namespace kvq
@@ -1058,10 +905,11 @@ extern "C" int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant
   const int rc = check_attention(kv, batch, K, n_q_heads);
   if (rc != PEAGLE_OK) return rc;
   const int rows = K * (n_q_heads / kv->n_kv_heads);
-  // (the larger of the two query types' plans)
+  // (the largest of the query types' plans)
   const int a = plan_of(kv->head_dim, false, rows).ntiles();
-  const int b = plan_of(kv->head_dim, true, rows).ntiles();
-  return work_bytes(kv->head_dim, a > b ? a : b);
+  const int b = plan_of(kv->head_dim, true, rows).ntiles(), c = attn_quant_tc_rows(rows) / 8;
+  const int most = a > b ? a : b;
+  return work_bytes(kv->head_dim, most > c ? most : c);
 }
 
 extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t layer,
@@ -1098,8 +946,12 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   a.capacity = kv->capacity;
   a.block_shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
   a.causal = causal, a.window = window, a.scale = scale * LOG2E;
+  a.heads = a.nkv, a.part_rows = K * a.G;
   const Plan p = plan_of(hd, f32, K * a.G);
   cudaError_t e = cudaErrorInvalidValue;
+  if (attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * a.capacity))
+    return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
+                                                                                    : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \
   if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, HD == 64 ? PEAGLE_W64 : 8>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)

@@ -514,10 +514,10 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  *             streams, graphs replayed at once) each have their own
  * A row that sees no slot gives zeros (and -inf).  Values and scores of slots that a row does
  * not see never reach it, NaN included.  fp32 accumulation, softmax and lse.  bf16 queries
- * enter exactly (down to 2^-38 of their row's largest element) and softmax weights rounded to
+ * enter exactly (down to 2^-31 of the largest element of their kv head's rows) and softmax weights rounded to
  * 11 bits, fp32 queries and their weights as two such parts (22 bits); weights x value scale
- * below 2^-14 of the row's largest lose bits, down to 2^-25 (fp32 queries: 2^-38).  Results
- * are the same on every call with the same lengths (no atomics).
+ * below 2^-10 of the row's largest lose bits, down to 2^-21 of it (fp32 queries: 2^-38).
+ * Results are the same on every call with the same lengths (no atomics).
  * A request with seq_lens[b] < 0, or whose last row's slot is beyond the capacity, is
  * skipped with KV_OVERFLOW; its rows are left as they are.
  * Limits: K * n_q_heads / n_kv_heads <= 128 (else PEAGLE_ERR_UNSUPPORTED); a workspace that

@@ -257,9 +257,9 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
     2^-22 S + 2^-24 scale max|q| sum |k|.  A score's error d moves the weights by 2 d relative
     (numerator and sum).  The exponential's argument carries u of its size (|x| < 2^8 before a
     weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to 11 bits
-    (2^-12 relative; 2^-22 for the two parts of fp32) or, below the smallest f16, to half of
-    2^-24 with the largest weight at least 1: n 2^-25 448 s over all slots (2^-36 for two
-    parts).  Sums over n slots: (n + 64) u.  Then half a step of the output's type."""
+    (2^-12 relative; 2^-22 for the two parts of fp32) or, below f16's normal values, to half
+    of 2^-24 where the largest weight x value scale of the row is at least 2^-4 (2^13 for fp32):
+    n 2^-21 448 s over all slots (2^-38), s the largest value scale.  Sums over n slots: (n + 64) u.  Then half a step of the output's type."""
     f32 = dtype == "f32"
     u = 2.0 ** -24
     BK, nq, hd = q.shape
@@ -278,7 +278,7 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
             if f32:
                 d += 2.0 ** -22 * S + u * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
             d += 2.0 ** -15 + 2.0 ** -21 + 4 * u * S
-            w, tiny = (2.0 ** -22, 2.0 ** -36) if f32 else (2.0 ** -12, 2.0 ** -25)
+            w, tiny = (2.0 ** -22, 2.0 ** -38) if f32 else (2.0 ** -12, 2.0 ** -21)
             to[r, h] = absolute[r, h] * (2 * d + w + 2 * (n + 64) * u) + \
                 n * tiny * 448.0 * vscale_max[b, h // G]
             tl[r, h] = d + (n + 64) * u + 4 * u * abs(lse[r, h])
