@@ -32,20 +32,23 @@ namespace {
 #ifndef PEAGLE_TC_SLOTS
 #define PEAGLE_TC_SLOTS 0
 #endif
-#ifndef PEAGLE_CW
-#define PEAGLE_CW 8
+#ifndef PEAGLE_CW64
+#define PEAGLE_CW64 4
+#endif
+#ifndef PEAGLE_CW128
+#define PEAGLE_CW128 4
 #endif
 constexpr int TT = 128;        // slots a tile
 constexpr int TC_ENTRY = 3;    // what a head costs besides its tiles, in tiles
-constexpr int NC = 16;         // query rows a softmax thread
+constexpr int NC = 32;         // query rows a softmax thread
 constexpr int TMEM_COLS = 256; // O in columns 0 .. 127, the scores' buffers at 128 and 192
 constexpr float SHIFT = -4.f, LIM = 15.f;  // see struct Running in kv_quant_attn.cu
 typedef Segment<TT, TC_ENTRY> TSeg;
 
-// A CTA for H x 16 query rows: its warps, in this order, and its shared memory.
+// A CTA for H x 32 query rows: its warps, in this order, and its shared memory.
 template <int HD, int H>
 struct Smem {
-  static constexpr int SOFT = 128 * H, CONV = 32 * PEAGLE_CW, LOAD_WARP = (SOFT + CONV) / 32;
+  static constexpr int SOFT = 128 * H, CONV = 32 * (HD == 64 ? PEAGLE_CW64 : PEAGLE_CW128), LOAD_WARP = (SOFT + CONV) / 32;
   static constexpr int MMA_WARP = LOAD_WARP + 1, WARPS = LOAD_WARP + 2;
   static constexpr int RP = NC * H;
   static constexpr int NK = HD == 64 ? 2 : 1;   // f16 key tiles, and query tiles
@@ -70,15 +73,14 @@ constexpr int DESCS = 16;
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// Whether x holds for any of the THREADS threads that meet at barrier ID.
-template <int ID, int THREADS>
-__device__ __forceinline__ bool any_of(bool x) {
+// Whether x holds for any of the threads that meet at the barrier.
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
   uint32_t y;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
-      : "r"((uint32_t)x), "n"(ID), "n"(THREADS)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
       : "memory");
   return y != 0;
 }
@@ -125,10 +127,10 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
   return w & ~((nan_bytes(w) >> 7) * 0xffu);
 }
 
-// Sums over the warp's lanes of NC = 16 values a lane: lanes i and i + 16 get the sum of v[i].
+// Sums over the warp's lanes of 32 values a lane: lane i gets the sum of v[i].
 __device__ __forceinline__ float scatter_sum(float* v, int lane) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = 16; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -136,7 +138,7 @@ __device__ __forceinline__ float scatter_sum(float* v, int lane) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+  return v[0];
 }
 
 template <int HD, int H>
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t raw_full[NR], raw_empty[NR], k_full[NK], v_full[2], s_full[2], s_empty[2],
-      p_full[2], pv_done[2], o_free, finished;
+      p_full[2], pv_done[2], head_in, o_free, finished;
   __shared__ uint32_t tmem_at;
   __shared__ volatile int s_abort;
   __shared__ __align__(16) TileDesc descs[DESCS];
@@ -183,6 +185,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       tc::mbar_init(&p_full[i], SOFT / 32);
       tc::mbar_init(&pv_done[i], 1);
     }
+    tc::mbar_init(&head_in, SOFT / 32);
     tc::mbar_init(&o_free, SOFT / 32);
     tc::mbar_init(&finished, 1);
     tc::fence_barrier_init();
@@ -195,8 +198,6 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_at;
-  auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(SOFT) : "memory"); };
-  auto soft_any = [&](bool x) { return any_of<1, SOFT>(x); };
   auto wait = [&](uint64_t* bar, int phase) {
     if (!tc::mbar_try_wait(bar, (uint32_t)phase & 1u))
       wait_long(bar, (uint32_t)phase & 1u, &s_abort, a.errors);
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       wait(&raw_full[r], t / NR);
       const TileDesc d = descs[t % DESCS];
       if (t >= NK) wait(&s_full[(t - NK) & 1], (t - NK) >> 1);
-      if (any_of<2, CONV>(s_abort)) break;  // (all converters or none: they meet at a barrier)
+      if (any_of(2, CONV, s_abort)) break;  // (all converters or none: they meet at a barrier)
       if (d.flags & FIRST) {
         // One power of two for the head's queries: the largest element to 2^14 .. 2^15.  bf16's 8
         // bits fit f16 down to 2^-31 of it.  Rows that are not finite are told apart and cleared.
@@ -427,8 +428,11 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
     }
   } else {
     // ---- softmax: this thread's slot of every tile, NC query rows from column col0 on
-    const int quarter = warp & 3, part16 = warp >> 2, col0 = part16 * NC;
-    const int key = quarter * 32 + lane;
+    const int quarter = warp & 3, part32 = warp >> 2, col0 = part32 * NC;
+    const int key = quarter * 32 + lane;  // (of this group's 128 threads too)
+    const int bar = 3 + part32;
+    auto group_any = [&](bool x) { return any_of(bar, 128, x); };
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); };
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float l[NC];
     bool pending = true, chained = false, stop = false;
@@ -437,15 +441,15 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       wait(&s_full[b], t >> 1);
       const TileDesc d = descs[t % DESCS];
       if (d.flags & FIRST) {
-        if (tid < RP) neg_ref[tid] = 0.f, has_slot[tid] = false;
+        if (key < NC) neg_ref[col0 + key] = 0.f, has_slot[col0 + key] = false;
 #pragma unroll
         for (int c = 0; c < NC; ++c) l[c] = 0.f;
         pending = true;
-        soft_sync();
+        group_sync();
       }
       tc::fence_after_sync();
       float x[NC];
-      tc::tmem_ld16(tmem + lanes + 128 + b * 64 + col0, x);
+      tc::tmem_ld32(tmem + lanes + 128 + b * 64 + col0, x);
       tc::tmem_ld_wait();
       const float vs = scales[t % DESCS][TT / 16 + key / 16];
       const float g = scales[t % DESCS][key / 16] * q_scale[d.head & 3], lv = lg2(vs), rv = rcp(vs);
@@ -478,8 +482,8 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       for (int c = 0; c < NC; c += 2) top4[c / 2 % 4] = max3(top4[c / 2 % 4], x[c], x[c + 1]);
       const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
       // (NaN passes no comparison: it reaches the weights as it is)
-      if (soft_any(top > LIM || pending || s_abort)) {
-        stop = soft_any(s_abort);
+      if (group_any(top > LIM || pending || s_abort)) {
+        stop = group_any(s_abort);
         if (stop) break;
         float mine = -INFINITY;
 #pragma unroll
@@ -487,44 +491,43 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
           const float y = warp_max_f32(x[c]);
           if (lane == c) mine = y;
         }
-        if (lane < NC) tops[quarter][col0 + lane] = mine;
-        soft_sync();
+        tops[quarter][col0 + lane] = mine;
+        group_sync();
         bool missing = false;
-        if (tid < RP) {
-          const float y = fmaxf(fmaxf(tops[0][tid], tops[1][tid]), fmaxf(tops[2][tid], tops[3][tid]));
-          const bool any = !(y == -INFINITY), had = has_slot[tid];
+        if (key < NC) {
+          const int c = col0 + key;
+          const float y = fmaxf(fmaxf(tops[0][c], tops[1][c]), fmaxf(tops[2][c], tops[3][c]));
+          const bool any = !(y == -INFINITY), had = has_slot[c];
           const float by = !any ? 0.f : had ? fmaxf(y - SHIFT, 0.f) : y - SHIFT;
-          factor[tid] = had ? ex2(-by) : 1.f;
-          moved[tid] = -by;
-          neg_ref[tid] -= by;
-          has_slot[tid] = had || any;
+          factor[c] = had ? ex2(-by) : 1.f;
+          moved[c] = -by;
+          neg_ref[c] -= by;
+          has_slot[c] = had || any;
           missing = !(had || any);
         }
-        pending = soft_any(missing);
-        if (!(d.flags & FIRST)) {
+        pending = group_any(missing);
+        if (!(d.flags & FIRST) && quarter == part32) {
+          // the group's rows are the lanes of this quarter of tensor memory
           wait(&pv_done[b ^ 1], (t - 1) >> 1);
           tc::fence_after_sync();
-          if (quarter * 32 < RP) {
-            const int row = quarter * 32 + lane;
-            const float f = row < RP ? factor[row] : 1.f;
+          const float f = factor[col0 + lane];
 #pragma unroll 1
-            for (int i = part16 * 16; i < HD; i += 16 * H) {
-              const uint32_t to = tmem + lanes + i;
-              float o[16];
-              tc::tmem_ld16(to, o);
-              tc::tmem_ld_wait();
+          for (int i = 0; i < HD; i += 16) {
+            const uint32_t to = tmem + lanes + i;
+            float o[16];
+            tc::tmem_ld16(to, o);
+            tc::tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= f;
-              asm volatile(
-                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                  "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to),
-                  "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]),
-                  "f"(o[7]), "f"(o[8]), "f"(o[9]), "f"(o[10]), "f"(o[11]), "f"(o[12]), "f"(o[13]),
-                  "f"(o[14]), "f"(o[15])
-                  : "memory");
-            }
-            tc::tmem_st_wait();
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            asm volatile(
+                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to),
+                "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]),
+                "f"(o[7]), "f"(o[8]), "f"(o[9]), "f"(o[10]), "f"(o[11]), "f"(o[12]), "f"(o[13]),
+                "f"(o[14]), "f"(o[15])
+                : "memory");
           }
+          tc::tmem_st_wait();
         }
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       uint8_t* to = sm + M::P + b * M::PB + key * 128;
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i)
-        *reinterpret_cast<uint4*>(to + ((part16 * (NC / 8) + i ^ (key & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(to + ((part32 * (NC / 8) + i ^ (key & 7)) << 4)) =
             make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
       fence_proxy_async_smem();
       tc::fence_before_sync();
@@ -555,10 +558,13 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       if (d.flags & LAST) {
         // ---- the head's result, or this CTA's piece of it
         const float sum = scatter_sum(l, lane);
-        if (lane < NC) sums[quarter][col0 + lane] = sum;
+        sums[quarter][col0 + lane] = sum;
         wait(&pv_done[b], t >> 1);
+        // (waits and not barriers between the groups: after an abort one may not come)
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&head_in);
+        wait(&head_in, d.head);
         tc::fence_after_sync();
-        soft_sync();
         const int row = quarter * 32 + lane;
         const bool began = d.flags & BEGAN, whole = d.flags & WHOLE;
         if (quarter * 32 < RP) {
@@ -572,14 +578,14 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
             m = has_slot[row] ? -neg_ref[row] : NO_REF;
             sum_l = sums[0][row] + sums[1][row] + sums[2][row] + sums[3][row];
             if (bad_row[d.head & 3][row] && has_slot[row]) sum_l = NAN;
-            if (!whole && part16 == 0) *reinterpret_cast<float2*>(work + 2 * row) = make_float2(m, sum_l);
+            if (!whole && part32 == 0) *reinterpret_cast<float2*>(work + 2 * row) = make_float2(m, sum_l);
           }
           if (whole && exists)
             out = finish_row<bf16>(a, HD, d.b, j * (a.nkv * a.G) + kvh * a.G + of - j * a.G, m, sum_l,
-                                   part16 == 0, inv);
+                                   part32 == 0, inv);
           const bool patch = nan_slots[d.head & 3] && exists;
 #pragma unroll 1
-          for (int i0 = part16 * 16; i0 < HD; i0 += 16 * H) {
+          for (int i0 = part32 * 16; i0 < HD; i0 += 16 * H) {
             float o[16];
             tc::tmem_ld16(tmem + lanes + i0, o);
             tc::tmem_ld_wait();
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&o_free);
-        soft_sync();  // (the references and sums are free again)
+        wait(&o_free, d.head);  // (the references and sums are free again)
       }
       if (d.flags & END) break;
     }
@@ -650,9 +656,9 @@ cudaError_t launch(const AttnQuantArgs& a, cudaStream_t s) {
   return launch_join(HD, false, true, a, NC * H / 8, s);
 }
 
-// Parts of at most 64 query rows, equal up to one row, in 2, 3 or 4 groups of 16.
+// Parts of at most 64 query rows, equal up to one row, in 1 or 2 groups of 32.
 int part_rows_of(int rows) { return cdiv(rows, cdiv(rows, 64)); }
-int groups_of(int rows) { return max(2, cdiv(part_rows_of(rows), NC)); }
+int groups_of(int rows) { return cdiv(part_rows_of(rows), NC); }
 
 }  // namespace
 
@@ -666,8 +672,8 @@ cudaError_t launch_attention_tc(int hd, int rows, AttnQuantArgs a, cudaStream_t 
   a.part_rows = part_rows_of(rows);
   a.heads = a.nkv * cdiv(rows, 64);
   const int h = groups_of(rows);
-  if (hd == 64) return h == 2 ? launch<64, 2>(a, s) : h == 3 ? launch<64, 3>(a, s) : launch<64, 4>(a, s);
-  return h == 2 ? launch<128, 2>(a, s) : h == 3 ? launch<128, 3>(a, s) : launch<128, 4>(a, s);
+  if (hd == 64) return h == 1 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);
+  return h == 1 ? launch<128, 1>(a, s) : launch<128, 2>(a, s);
 }
 
 }  // namespace kvq
