@@ -44,10 +44,16 @@ namespace kvq {
 #define PEAGLE_W64 8
 #define PEAGLE_MOST64 4
 #endif
+#ifndef PEAGLE_MOST128
+#define PEAGLE_MOST128 3
+#endif
 constexpr int TILE = 32;       // slots a unit
-constexpr int ENTRY = 8;       // what a (request, kv head) costs besides its tiles, in tiles
+#ifndef PEAGLE_ENTRY
+#define PEAGLE_ENTRY 32
+#endif
+constexpr int ENTRY = PEAGLE_ENTRY;       // what a (request, kv head) costs besides its tiles, in tiles
 constexpr int JOIN_WARPS = 4;  // of the second kernel
-typedef Segment<TILE, ENTRY> Seg;
+typedef Segment<TILE> Seg;
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -486,6 +492,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(8) float row_m[W][NT * 8], row_l[W][NT * 8];
   __shared__ __align__(8) float row_scale[MAX_ROWS + 8];
+  __shared__ float sum_m[MAX_ROWS + 8], sum_l[MAX_ROWS + 8];
   __shared__ uint8_t row_j[MAX_ROWS + 8];  // each query row's draft row
   __shared__ int row_at[MAX_ROWS + 8];     // and place among its request's rows and heads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -501,9 +508,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 
   // a share below 4 tiles would leave warps idle and make pieces to join
   Seg seg;
-  int n;
-  long long lo, share;
-  if (!find_share<W, TILE, ENTRY>(a, 4, seg, n, lo, share)) {
+  int n, lo, share;
+  if (!find_share<TILE, ENTRY>(a, 4, seg, n, lo, share)) {
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
     const bool last = !seg.next(a, n);
     if (!last && warp < groups * NT) raw.fetch(a, seg.b, seg.h, warp, lane);
 
-    // join the streams: a common reference for every row, then their sums
+    // join the streams: their references, sums and outputs by way of shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -626,53 +632,56 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           run.l[nt][e] += __shfl_xor_sync(0xffffffffu, run.l[nt][e], d);
-        if (!(run.started >> (2 * nt + e) & 1)) run.m[nt][e] = NO_REF;
-        if (r == 0) row_m[warp][nt * 8 + 2 * c + e] = run.m[nt][e];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = NO_REF;
-        for (int s = 0; s < streams; ++s)
-          top = fmaxf(top, row_m[s * groups + group][nt * 8 + 2 * c + e]);
-        const float f = ex2(run.m[nt][e] - top);
-        if (r == 0) row_l[warp][nt * 8 + 2 * c + e] = run.l[nt][e] * f;
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) run.o[i][nt][e] *= f, run.o[i][nt][2 + e] *= f;
+        if (r == 0) {
+          row_m[warp][nt * 8 + 2 * c + e] = run.started >> (2 * nt + e) & 1 ? run.m[nt][e] : NO_REF;
+          row_l[warp][nt * 8 + 2 * c + e] = run.l[nt][e];
+        }
       }
     const bool began = done.at >= 0, whole = began && done.at + done.tiles <= n;
     float* slot = a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
                                ((size_t)groups * NT * 8 * (HD + 2));
-#pragma unroll
+#pragma unroll 1
     for (int pass = 0; pass < PASSES; ++pass) {
       if (pass) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < HD / 16 / PASSES; ++i)
+      for (int i = 0; i < HD / 16; ++i)
+        if (i / (HD / 16 / PASSES) == pass)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float* o = run.o[pass * (HD / 16 / PASSES) + i][nt];
-          joined[warp * PASS + (nt * (HD / 16 / PASSES) + i) * 32 + lane] =
-              make_float4(o[0], o[1], o[2], o[3]);
-        }
+          for (int nt = 0; nt < NT; ++nt) {
+            const float* o = run.o[i][nt];
+            joined[warp * PASS + (nt * (HD / 16 / PASSES) + i % (HD / 16 / PASSES)) * 32 + lane] =
+                make_float4(o[0], o[1], o[2], o[3]);
+          }
       __syncthreads();
+      if (pass == 0) {
+        // each row's common reference and sum, and what each stream's output counts there
+        if (threadIdx.x < groups * NT * 8) {
+          const int g = threadIdx.x / (NT * 8), row = threadIdx.x % (NT * 8);
+          float m = NO_REF, l = 0.f;
+          for (int w = g; w < W; w += groups) m = fmaxf(m, row_m[w][row]);
+          for (int w = g; w < W; w += groups) {
+            const float f = ex2(row_m[w][row] - m);
+            l = fmaf(row_l[w][row], f, l);
+            row_m[w][row] = f;
+          }
+          sum_m[threadIdx.x] = m, sum_l[threadIdx.x] = l;
+        }
+        __syncthreads();
+      }
       // each warp sums some of the fragments over the streams
+#pragma unroll 1
       for (int at = warp; at < groups * (PASS / 32); at += W) {
         const int g = at / (PASS / 32), in = at % (PASS / 32);
         const int nt = in / (HD / 16 / PASSES), i = pass * (HD / 16 / PASSES) + in % (HD / 16 / PASSES);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
-        for (int s = 0; s < streams; ++s) {
-          const int w = s * groups + g;
-          const float4 f = joined[w * PASS + in * 32 + lane];
-          const float2 l = *reinterpret_cast<const float2*>(&row_l[w][nt * 8 + 2 * c]);
-          const float2 m = *reinterpret_cast<const float2*>(&row_m[w][nt * 8 + 2 * c]);
-          o.x += f.x, o.y += f.y, o.z += f.z, o.w += f.w;
-          l0 += l.x, l1 += l.y;
-          m0 = fmaxf(m0, m.x), m1 = fmaxf(m1, m.y);
+        for (int w = g; w < W; w += groups) {
+          const float4 x = joined[w * PASS + in * 32 + lane];
+          const float2 f = *reinterpret_cast<const float2*>(&row_m[w][nt * 8 + 2 * c]);
+          o.x = fmaf(x.x, f.x, o.x), o.y = fmaf(x.y, f.y, o.y);
+          o.z = fmaf(x.z, f.x, o.z), o.w = fmaf(x.w, f.y, o.w);
         }
         const int row = (g * NT + nt) * 8 + 2 * c;
+        const float m0 = sum_m[row], m1 = sum_m[row + 1], l0 = sum_l[row], l1 = sum_l[row + 1];
         if (whole) {
           const int d = r * (HD / 8) + 2 * i;
           float inv;
@@ -833,7 +842,7 @@ struct Plan {
   int ntiles() const { return nt * groups; }
 };
 static Plan plan_of(int hd, bool f32, int rows) {
-  const int tiles = cdiv(rows, 8), most = hd == 64 ? PEAGLE_MOST64 : f32 ? 2 : 3;
+  const int tiles = cdiv(rows, 8), most = hd == 64 ? PEAGLE_MOST64 : f32 ? 2 : PEAGLE_MOST128;
   Plan p;
   for (p.groups = 1; cdiv(tiles, p.groups) > most; p.groups *= 2) {
   }
@@ -929,6 +938,9 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
       q_stride % (dtype == PEAGLE_F32 ? 4 : 8))
     return PEAGLE_ERR_INVALID;
   if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
+  // (the walk over the tiles counts in 31 bits; a cache beyond that does not fit a GPU)
+  if ((int64_t)batch * kv->n_kv_heads * 2 * (kv->capacity / TILE + 2 + ENTRY) >= 1 << 30)
+    return PEAGLE_ERR_UNSUPPORTED;
   const int hd = kv->head_dim;
   const bool f32 = dtype == PEAGLE_F32;
   const int64_t unit = (int64_t)layer * kv->batch * kv->n_kv_heads;
@@ -949,7 +961,9 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   a.heads = a.nkv, a.part_rows = K * a.G;
   const Plan p = plan_of(hd, f32, K * a.G);
   cudaError_t e = cudaErrorInvalidValue;
-  if (attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * a.capacity))
+  // the slots that the call sees at most
+  const int64_t most = window > 0 && window < kv->capacity - K ? window + K : kv->capacity;
+  if (attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \

@@ -88,15 +88,15 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 // Where a CTA's walk over the tiles stands: one head of a request (a kv head, or a part of the
-// query rows of one), which costs ENTRY tiles besides its own.
-template <int TILE, int ENTRY>
+// query rows of one), which costs `entry` tiles besides its own.
+template <int TILE>
 struct Segment {
   int b, h, len;
-  int first_tile, tiles;
+  int first_tile, tiles, entry;
   int at;  // of its first tile, relative to the CTA's share (negative: it began before)
   // The next one; false when it is not in the share of n any more.
   __device__ __forceinline__ bool next(const AttnQuantArgs& a, int n) {
-    at += tiles + ENTRY;
+    at += tiles + entry;
     if (at >= n) return false;
     if (++h < a.heads) return true;
     h = 0;
@@ -109,79 +109,55 @@ struct Segment {
   }
 };
 
-// Sum over the W warps' threads of v before this one, and over all of them.
-template <int W>
-__device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  long long x = v;
+// This CTA's share of the call: `seg`, where it begins, its cost n, where it lies (lo) and how long
+// every share is.  False when it holds no tile.  A head's entry (its queries, the first tile's
+// references, the join of the streams) counts as up to ENTRY tiles.  Where a CTA has fewer tiles
+// than that, it counts as a share: then no CTA has to enter two heads, and no more CTAs than heads
+// stay idle.  Every warp finds the share for itself, a lane summing up consecutive requests, so
+// nothing waits on a barrier.  (The host has checked that all fits 31 bits.)
+template <int TILE, int ENTRY>
+__device__ __forceinline__ bool find_share(const AttnQuantArgs& a, int least, Segment<TILE>& seg,
+                                           int& n, int& lo, int& share) {
+  const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
+  const int b0 = min(lane * per, a.batch), b1 = min(b0 + per, a.batch);
+  int my_tiles = 0, my_requests = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int len = a.seq_lens[b];
+    int first;
+    const int tiles = request_tiles<TILE>(a, len, first);
+    my_tiles += tiles;
+    my_requests += tiles > 0;
+    if (blockIdx.x == 0 && threadIdx.x < 32 && !request_fits(a, len))
+      raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
+  }
+  const int all_tiles = __reduce_add_sync(0xffffffffu, my_tiles) * a.heads;
+  seg.entry = min(ENTRY, all_tiles / CTAS + 1);
+  const int mine = (my_tiles + my_requests * seg.entry) * a.heads;
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
   }
-  __syncthreads();
-  if (lane == 31) red[wid] = x;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const long long s = red[i];
-    if (i < wid) before += s;
-    total += s;
-  }
-  return before + x - v;
-}
-
-
-// This CTA's share of the call: `seg`, where it begins, its cost n, where it lies (lo) and how long
-// every share is.  False when it holds no tile.  All W x 32 threads.
-template <int W, int TILE, int ENTRY>
-__device__ __forceinline__ bool find_share(const AttnQuantArgs& a, int least, Segment<TILE, ENTRY>& seg,
-                                           int& n, long long& lo, long long& share) {
-  __shared__ long long red[W];
-  __shared__ long long found;
-  __shared__ int found_b;
-  long long total = 0, cost = 0, before = 0;
-  int first;
-  auto cost_of = [&](int b) {
-    const int tiles = b < a.batch ? request_tiles<TILE>(a, a.seq_lens[b], first) : 0;
-    return tiles ? (long long)(tiles + ENTRY) * a.heads : 0;
-  };
-  for (int b0 = 0; b0 < a.batch; b0 += W * 32) {
-    const int b = b0 + threadIdx.x;
-    cost = cost_of(b);
-    if (blockIdx.x == 0 && b < a.batch && !request_fits(a, a.seq_lens[b]))
-      raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
-    long long part;
-    before = block_scan<W>(cost, red, part);
-    total += part;
-  }
-  share = (total + CTAS - 1) / CTAS;
-  share = share < least ? least : share;
+  const int total = __shfl_sync(0xffffffffu, upto, 31);
+  share = max(least, (total + CTAS - 1) / CTAS);
   lo = share * blockIdx.x;
-  n = (int)(total - lo < share ? total - lo : share);
-  long long base = 0;
-  for (int b0 = 0; b0 < a.batch && lo < total; b0 += W * 32) {
-    if (a.batch > W * 32) {
-      cost = cost_of(b0 + threadIdx.x);
-      long long part;
-      before = base + block_scan<W>(cost, red, part);
-      base += part;
-    }
-    if (cost && lo >= before && lo < before + cost) {
-      found = before;
-      found_b = b0 + threadIdx.x;
-    }
-  }
-  __syncthreads();
-  if (lo >= total) return false;
-  seg.b = found_b;
-  seg.len = a.seq_lens[seg.b];
-  seg.tiles = request_tiles<TILE>(a, seg.len, seg.first_tile);
-  const long long in = lo - found;
-  seg.h = (int)(in / (seg.tiles + ENTRY));
-  seg.at = ENTRY - (int)(in % (seg.tiles + ENTRY));
+  n = min(share, total - lo);
+  if (n <= 0) return false;
+  const int who = __ffs(__ballot_sync(0xffffffffu, lo >= upto - mine && lo < upto)) - 1;
+  int before = __shfl_sync(0xffffffffu, upto - mine, who);
+  int cost;
+  seg.b = __shfl_sync(0xffffffffu, b0, who) - 1;
+  do {
+    seg.len = a.seq_lens[++seg.b];
+    seg.tiles = request_tiles<TILE>(a, seg.len, seg.first_tile);
+    cost = seg.tiles ? (seg.tiles + seg.entry) * a.heads : 0;
+    before += cost;
+  } while (lo >= before);
+  const int in = lo - (before - cost);
+  seg.h = in / (seg.tiles + seg.entry);
+  seg.at = seg.entry - (in - seg.h * (seg.tiles + seg.entry));
   return seg.at < n;
 }
 
@@ -199,9 +175,9 @@ template <typename T>
 __device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int at, float m,
                                          float l, bool first, float& inv) {
   const bool none = m == NO_REF && l == 0.f;  // (a row of NaN scores has no reference either)
-  inv = none ? 0.f : 1.f / l;
+  inv = none ? 0.f : rcp(l);
   const int64_t to = (int64_t)req * a.K * (a.nkv * a.G) + at;
-  if (first && a.lse) a.lse[to] = none ? -INFINITY : (m + log2f(l)) * LN2;
+  if (first && a.lse) a.lse[to] = none ? -INFINITY : (m + lg2(l)) * LN2;
   return (T*)a.out + to * hd;
 }
 

@@ -30,7 +30,7 @@ namespace kvq {
 namespace {
 
 #ifndef PEAGLE_TC_SLOTS
-#define PEAGLE_TC_SLOTS 0
+#define PEAGLE_TC_SLOTS (3 << 16)
 #endif
 #ifndef PEAGLE_CW64
 #define PEAGLE_CW64 4
@@ -39,11 +39,14 @@ namespace {
 #define PEAGLE_CW128 4
 #endif
 constexpr int TT = 128;        // slots a tile
-constexpr int TC_ENTRY = 3;    // what a head costs besides its tiles, in tiles
+#ifndef PEAGLE_TCE
+#define PEAGLE_TCE 3
+#endif
+constexpr int TC_ENTRY = PEAGLE_TCE;    // what a head costs besides its tiles, in tiles
 constexpr int NC = 32;         // query rows a softmax thread
 constexpr int TMEM_COLS = 256; // O in columns 0 .. 127, the scores' buffers at 128 and 192
 constexpr float SHIFT = -4.f, LIM = 15.f;  // see struct Running in kv_quant_attn.cu
-typedef Segment<TT, TC_ENTRY> TSeg;
+typedef Segment<TT> TSeg;
 
 // A CTA for H x 32 query rows: its warps, in this order, and its shared memory.
 template <int HD, int H>
@@ -169,8 +172,8 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
   pdl_enter();
   TSeg seg;
   int n;
-  long long lo, share;
-  if (!find_share<M::WARPS, TT, TC_ENTRY>(a, 2, seg, n, lo, share)) {
+  int lo, share;
+  if (!find_share<TT, TC_ENTRY>(a, 2, seg, n, lo, share)) {
     if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
@@ -663,7 +666,7 @@ int groups_of(int rows) { return cdiv(part_rows_of(rows), NC); }
 }  // namespace
 
 bool attn_quant_tc_takes(int hd, bool f32, int rows, int64_t slots) {
-  return !f32 && rows > 16 && slots >= PEAGLE_TC_SLOTS;
+  return !f32 && rows > (hd == 64 ? 48 : 32) && slots * cdiv(rows, 64) >= PEAGLE_TC_SLOTS;
 }
 
 int attn_quant_tc_rows(int rows) { return NC * groups_of(rows); }
