@@ -15,6 +15,13 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// Four codes: the low two and the high two.
+__device__ __forceinline__ void cvt_e4m3x4_f16x2(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
+}
 __device__ __forceinline__ float2 cvt_e4m3x2_f32x2(uint16_t c) {
   const uint32_t h = cvt_e4m3x2_f16x2(c);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

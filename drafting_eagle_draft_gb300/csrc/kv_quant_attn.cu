@@ -40,18 +40,9 @@
 namespace peagle {
 namespace kvq {
 
-#ifndef PEAGLE_W64
-#define PEAGLE_W64 8
-#define PEAGLE_MOST64 4
-#endif
-#ifndef PEAGLE_MOST128
-#define PEAGLE_MOST128 3
-#endif
+constexpr int W = 8;           // warps a CTA: two a scheduler, with 255 registers each
 constexpr int TILE = 32;       // slots a unit
-#ifndef PEAGLE_ENTRY
-#define PEAGLE_ENTRY 32
-#endif
-constexpr int ENTRY = PEAGLE_ENTRY;       // what a (request, kv head) costs besides its tiles, in tiles
+constexpr int ENTRY = 28;      // see find_share; 24 and 32 measured within 2 %, 8 up to 20 % slower
 constexpr int JOIN_WARPS = 4;  // of the second kernel
 typedef Segment<TILE> Seg;
 
@@ -239,10 +230,9 @@ struct Queries {
       const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const uint32_t a0 = cvt_e4m3x2_f16x2((uint16_t)u[s]);
-        const uint32_t a2 = cvt_e4m3x2_f16x2((uint16_t)(u[s] >> 16));
-        const uint32_t a1 = cvt_e4m3x2_f16x2((uint16_t)w[s]);
-        const uint32_t a3 = cvt_e4m3x2_f16x2((uint16_t)(w[s] >> 16));
+        uint32_t a0, a1, a2, a3;
+        cvt_e4m3x4_f16x2(u[s], a0, a2);
+        cvt_e4m3x4_f16x2(w[s], a1, a3);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p)
 #pragma unroll
@@ -472,23 +462,22 @@ struct Running {
     const unsigned sel = i & 1 ? 0x7362u : 0x5140u;  // bytes of two slots, side by side
     const uint32_t a = __byte_perm(w[0][i >> 1], w[1][i >> 1], sel);
     const uint32_t b = __byte_perm(w[2][i >> 1], w[3][i >> 1], sel);
-    x[0] = cvt_e4m3x2_f16x2((uint16_t)a), x[1] = cvt_e4m3x2_f16x2((uint16_t)(a >> 16));
-    x[2] = cvt_e4m3x2_f16x2((uint16_t)b), x[3] = cvt_e4m3x2_f16x2((uint16_t)(b >> 16));
+    cvt_e4m3x4_f16x2(a, x[0], x[1]);
+    cvt_e4m3x4_f16x2(b, x[2], x[3]);
   }
 };
 
 // Parts in which the warps' O^T go through the joining buffer.  At head_dim 128 parts leave room
 // for a third stage of the rings (NT 1 and 2; NT 3 has two either way).
-constexpr int join_passes(int hd, int nt, int w) { return hd == 64 ? 1 : nt == 2 ? 4 : 2; }
+constexpr int join_passes(int hd, int nt) { return hd == 64 ? 1 : nt == 2 ? 4 : 2; }
 
-// W: warps a CTA.
-template <int HD, int NT, bool F32, int W>
+template <int HD, int NT, bool F32>
 __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) {
   typedef typename std::conditional<F32, float, bf16>::type T;
   typedef Queries<HD, NT, F32> Q;
   constexpr int STAGE = 2 * TILE * HD + 16;  // K, V, four scales
   constexpr int FRAG = HD / 16 * NT * 32;    // float4s of a warp's O^T
-  constexpr int PASSES = join_passes(HD, NT, W), PASS = FRAG / PASSES;
+  constexpr int PASSES = join_passes(HD, NT), PASS = FRAG / PASSES;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(8) float row_m[W][NT * 8], row_l[W][NT * 8];
   __shared__ __align__(8) float row_scale[MAX_ROWS + 8];
@@ -836,13 +825,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
 
 // How the query rows of a kv head are laid over warps: groups of warps x NT tiles of 8 rows.
 // A warp's registers hold the queries and the outputs of NT tiles: 24 NT registers for
-// head_dim 64 (32 NT with fp32 queries), 48 NT (64 NT) for 128.
+// head_dim 64 (32 NT with fp32 queries), 48 NT (64 NT) for 128.  As many rows a warp as they hold:
+// each warp of a group converts the codes for itself.  24 rows over 65536 slots at head_dim 64 take
+// 134 us as one group of three tiles and 210 as two groups; 16 warps with half the registers and
+// two tiles each took 161 us where 8 with four took 124 (64 rows, a batch of 64).
 struct Plan {
   int nt, groups;
   int ntiles() const { return nt * groups; }
 };
 static Plan plan_of(int hd, bool f32, int rows) {
-  const int tiles = cdiv(rows, 8), most = hd == 64 ? PEAGLE_MOST64 : f32 ? 2 : PEAGLE_MOST128;
+  const int tiles = cdiv(rows, 8), most = hd == 64 ? 4 : f32 ? 2 : 3;
   Plan p;
   for (p.groups = 1; cdiv(tiles, p.groups) > most; p.groups *= 2) {
   }
@@ -855,10 +847,10 @@ static int64_t work_bytes(int hd, int ntiles) {
   return 4096 + (int64_t)CTAS * 2 * (int64_t)slot_bytes(hd, ntiles);
 }
 
-template <int HD, int NT, bool F32, int W>
+template <int HD, int NT, bool F32>
 static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
   constexpr size_t STAGE = 2 * TILE * HD + 16;
-  constexpr size_t JOIN = (size_t)W * HD * NT * 32 / join_passes(HD, NT, W);
+  constexpr size_t JOIN = (size_t)W * HD * NT * 32 / join_passes(HD, NT);
   const int streams = W / p.groups;
   const size_t fixed = JOIN + (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES;
   // up to 8 stages a stream, within the 227 KB of a CTA less its static arrays
@@ -867,7 +859,7 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   a.stages = (int)(room / (streams * STAGE));
   a.stages = a.stages > 8 ? 8 : a.stages;
   const size_t smem = streams * a.stages * STAGE + fixed;
-  auto kernel = attn_quant_kernel<HD, NT, F32, W>;
+  auto kernel = attn_quant_kernel<HD, NT, F32>;
   cudaError_t e = smem_optin((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
@@ -967,7 +959,7 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \
-  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, HD == 64 ? PEAGLE_W64 : 8>(a, p, (cudaStream_t)stream);
+  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)
   PEAGLE_ATTN(64, 2, false)
   PEAGLE_ATTN(64, 3, false)

@@ -185,7 +185,7 @@ __device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req
 // on.  rowmajor: how the pieces' outputs lie in the workspace.
 cudaError_t launch_join(int hd, bool f32, bool rowmajor, const AttnQuantArgs& a, int ntiles,
                         cudaStream_t s);
-// tcgen05 kernel, its shapes, and the workspace slot's rows (kv_quant_attn_tc.cu).
+// The tcgen05 kernel, the calls it takes, and the rows of its workspace slots (kv_quant_attn_tc.cu).
 bool attn_quant_tc_takes(int hd, bool f32, int rows, int64_t slots);
 int attn_quant_tc_rows(int rows);
 cudaError_t launch_attention_tc(int hd, int rows, AttnQuantArgs a, cudaStream_t s);

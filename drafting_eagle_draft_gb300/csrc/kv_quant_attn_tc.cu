@@ -14,13 +14,22 @@
 // the way from the copied tile to the operands' 128-byte swizzled layout: the 8-bit form of the
 // product would need the weights in 8 bits, as two parts of 4 bits for bf16's accuracy.
 //
-// Warps: 8 softmax (two halves of the query rows x four lane quarters of tensor memory), 4
-// converters, one that issues bulk copies of the codes into a ring, one that issues the products.
-// All of them walk the same tiles and hand over through mbarriers, with bounded waits.
+// Warps: 8 softmax (two groups, a half of the query rows each, x four lane quarters of tensor
+// memory), 4 converters, one that issues bulk copies of the codes into a ring, one that issues the
+// products.  All of them walk the same tiles and hand over through mbarriers, with bounded waits;
+// after one that ran out all leave, and the call's error word says so.
 //
 // The references move as in the warps' kernel: when some weight of a tile would pass 2^LIM, all rows
-// move up to the tile's maxima (one vote of the softmax warps a tile), and O is scaled in tensor
-// memory after the product before.
+// of the group move up to the tile's maxima (one vote of its 128 threads a tile), and O is scaled in
+// tensor memory after the product before: a group's rows are one quarter's lanes.
+//
+// What bounds it: the softmax warps' chain of a tile, about 2,600 cycles at 64 rows and head_dim 64
+// (the tile's bytes would take 700 at the copy rate, the two products 550), spread over loads from
+// tensor memory, 130 arithmetic instructions, the vote, exponentials, and stores with their proxy
+// fence; the tensor pipe is 12 % busy.  Two requests of 65536 slots at head_dim 128, 64 rows: 104 us,
+// 2.5 TB/s (37 % of the measured copy rate); the warps' kernel takes 151.  Tried and slower: groups
+// of 128 threads that each convert, multiply and weigh their own tiles (195 us for what takes 146),
+// the weights computed while the votes come in (123 for 108: the code leaves the instruction cache).
 #include "kv_quant_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -29,31 +38,23 @@ namespace kvq {
 
 namespace {
 
-#ifndef PEAGLE_TC_SLOTS
-#define PEAGLE_TC_SLOTS (3 << 16)
-#endif
-#ifndef PEAGLE_CW64
-#define PEAGLE_CW64 4
-#endif
-#ifndef PEAGLE_CW128
-#define PEAGLE_CW128 4
-#endif
 constexpr int TT = 128;        // slots a tile
-#ifndef PEAGLE_TCE
-#define PEAGLE_TCE 3
-#endif
-constexpr int TC_ENTRY = PEAGLE_TCE;    // what a head costs besides its tiles, in tiles
+constexpr int TC_ENTRY = 3;    // what a head costs besides its tiles, in tiles
 constexpr int NC = 32;         // query rows a softmax thread
 constexpr int TMEM_COLS = 256; // O in columns 0 .. 127, the scores' buffers at 128 and 192
 constexpr float SHIFT = -4.f, LIM = 15.f;  // see struct Running in kv_quant_attn.cu
 typedef Segment<TT> TSeg;
 
-// A CTA for H x 32 query rows: its warps, in this order, and its shared memory.
-template <int HD, int H>
+// A CTA's warps, in this order: softmax, converters, copies, products.  14 of them leave 128 registers
+// a thread; with 8 converters, or 16 softmax warps of 16 rows each, the same calls took 8 .. 20 %
+// longer.
+constexpr int SOFT = 256, CONV = 128, LOAD_WARP = (SOFT + CONV) / 32, MMA_WARP = LOAD_WARP + 1;
+constexpr int WARPS = LOAD_WARP + 2;
+constexpr int RP = 64;         // query rows of a part, padded: two groups of softmax warps
+
+// Shared memory of a CTA.
+template <int HD>
 struct Smem {
-  static constexpr int SOFT = 128 * H, CONV = 32 * (HD == 64 ? PEAGLE_CW64 : PEAGLE_CW128), LOAD_WARP = (SOFT + CONV) / 32;
-  static constexpr int MMA_WARP = LOAD_WARP + 1, WARPS = LOAD_WARP + 2;
-  static constexpr int RP = NC * H;
   static constexpr int NK = HD == 64 ? 2 : 1;   // f16 key tiles, and query tiles
   static constexpr int NR = HD == 64 ? 5 : 2;   // copied tiles
   static constexpr int F16 = TT * HD * 2, PB = TT * 128, QB = RP * HD * 2, RAW = 2 * TT * HD;
@@ -117,10 +118,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int lbo) {
 
 // 16 codes as 16 f16 values.
 __device__ __forceinline__ void convert16(uint4 c, uint4& lo, uint4& hi) {
-  lo.x = cvt_e4m3x2_f16x2((uint16_t)c.x), lo.y = cvt_e4m3x2_f16x2((uint16_t)(c.x >> 16));
-  lo.z = cvt_e4m3x2_f16x2((uint16_t)c.y), lo.w = cvt_e4m3x2_f16x2((uint16_t)(c.y >> 16));
-  hi.x = cvt_e4m3x2_f16x2((uint16_t)c.z), hi.y = cvt_e4m3x2_f16x2((uint16_t)(c.z >> 16));
-  hi.z = cvt_e4m3x2_f16x2((uint16_t)c.w), hi.w = cvt_e4m3x2_f16x2((uint16_t)(c.w >> 16));
+  cvt_e4m3x4_f16x2(c.x, lo.x, lo.y);
+  cvt_e4m3x4_f16x2(c.y, lo.z, lo.w);
+  cvt_e4m3x4_f16x2(c.z, hi.x, hi.y);
+  cvt_e4m3x4_f16x2(c.w, hi.z, hi.w);
 }
 // NaN codes of a word: 0x80 in each such byte.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
@@ -144,10 +145,10 @@ __device__ __forceinline__ float scatter_sum(float* v, int lane) {
   return v[0];
 }
 
-template <int HD, int H>
-__global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantArgs a) {
-  typedef Smem<HD, H> M;
-  constexpr int RP = M::RP, NK = M::NK, NR = M::NR, SOFT = M::SOFT, CONV = M::CONV;
+template <int HD>
+__global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantArgs a) {
+  typedef Smem<HD> M;
+  constexpr int NK = M::NK, NR = M::NR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t raw_full[NR], raw_empty[NR], k_full[NK], v_full[2], s_full[2], s_empty[2],
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
     tc::mbar_init(&finished, 1);
     tc::fence_barrier_init();
   }
-  if (warp == M::MMA_WARP) {
+  if (warp == MMA_WARP) {
     tc::tmem_alloc(&tmem_at, TMEM_COLS);
     tc::tmem_relinquish();
   }
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
       wait_long(bar, (uint32_t)phase & 1u, &s_abort, a.errors);
   };
 
-  if (warp == M::LOAD_WARP) {
+  if (warp == LOAD_WARP) {
     // ---- the walk over the share, bulk copies of the codes, and the scales
     const uint64_t policy = tc::policy_evict_first();
     int t = 0, head = 0, u = max(seg.at, 0);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
         tc::mbar_wait(&raw_full[x % NR], (uint32_t)(x / NR) & 1u, &never);
     }
     __syncwarp();
-  } else if (warp == M::MMA_WARP) {
+  } else if (warp == MMA_WARP) {
     // ---- the products
     if (lane == 0) {
       constexpr uint32_t id_s = (1u << 4) | (uint32_t)(RP >> 3) << 17 | (uint32_t)(TT >> 4) << 24;
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
                                    part32 == 0, inv);
           const bool patch = nan_slots[d.head & 3] && exists;
 #pragma unroll 1
-          for (int i0 = part32 * 16; i0 < HD; i0 += 16 * H) {
+          for (int i0 = part32 * 16; i0 < HD; i0 += 32) {
             float o[16];
             tc::tmem_ld16(tmem + lanes + i0, o);
             tc::tmem_ld_wait();
@@ -642,41 +643,46 @@ __global__ void __launch_bounds__(Smem<HD, H>::WARPS * 32, 1) attn_quant_tc_kern
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == M::MMA_WARP) {
+  if (warp == MMA_WARP) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
-template <int HD, int H>
+template <int HD>
 cudaError_t launch(const AttnQuantArgs& a, cudaStream_t s) {
-  const size_t smem = Smem<HD, H>::BYTES;
-  auto kernel = attn_quant_tc_kernel<HD, H>;
+  const size_t smem = Smem<HD>::BYTES;
+  auto kernel = attn_quant_tc_kernel<HD>;
   cudaError_t e = smem_optin((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(CTAS), dim3(Smem<HD, H>::WARPS * 32), smem, s, a);
+  e = launch_pdl(kernel, dim3(CTAS), dim3(WARPS * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  return launch_join(HD, false, true, a, NC * H / 8, s);
+  return launch_join(HD, false, true, a, RP / 8, s);
 }
-
-// Parts of at most 64 query rows, equal up to one row, in 1 or 2 groups of 32.
-int part_rows_of(int rows) { return cdiv(rows, cdiv(rows, 64)); }
-int groups_of(int rows) { return cdiv(part_rows_of(rows), NC); }
 
 }  // namespace
 
+// Where this kernel takes less time than the warps' one (us, this one against that one; slots = the
+// slots of all requests and kv heads):
+//   head_dim 128, 64 rows:  1048576 slots 105 / 149, 262144 41 / 49, 131072 35 / 32, 65536 26 / 25
+//   head_dim 128, 40 rows:  1048576 slots 102 / 122, 262144 39 / 46, 131072 35 / 30
+//   head_dim 64, 64 rows:   1048576 slots 81 / 88, 524288 50 / 54, 262144 34 / 34, 32768 20 / 16
+//   head_dim 64, 40 rows:   1048576 slots 80 / 72
+//   head_dim 64, 64 rows, 64 requests of 300 .. 4100 slots: 106 / 127
+// Its chain of a tile is longer (conversion, product, softmax, product), so it wants several tiles a
+// CTA; and below 33 rows half of its softmax threads would have none.
 bool attn_quant_tc_takes(int hd, bool f32, int rows, int64_t slots) {
-  return !f32 && rows > (hd == 64 ? 48 : 32) && slots * cdiv(rows, 64) >= PEAGLE_TC_SLOTS;
+  return !f32 && rows > (hd == 64 ? 48 : 32) && slots * cdiv(rows, RP) >= 3 << 16;
 }
 
-int attn_quant_tc_rows(int rows) { return NC * groups_of(rows); }
+// (more than 32 rows, whatever the slots; parts are equal up to one row)
+int attn_quant_tc_rows(int rows) { return rows > 32 ? RP : 0; }
 
 cudaError_t launch_attention_tc(int hd, int rows, AttnQuantArgs a, cudaStream_t s) {
-  a.part_rows = part_rows_of(rows);
-  a.heads = a.nkv * cdiv(rows, 64);
-  const int h = groups_of(rows);
-  if (hd == 64) return h == 1 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);
-  return h == 1 ? launch<128, 1>(a, s) : launch<128, 2>(a, s);
+  const int parts = cdiv(rows, RP);
+  a.part_rows = cdiv(rows, parts);
+  a.heads = a.nkv * parts;
+  return hd == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace kvq

@@ -358,6 +358,44 @@ def test_attention_matches_oracle(nq, nkv, hd, K, block, dtype):
     check_attention(c, 1, q, lens, K, scale=-0.05)
 
 
+# more than 48 (head_dim 128: 32) query rows a kv head and enough slots that the tcgen05 kernel runs:
+# whole and odd row counts, one and two parts of them, one and two kv heads
+MANY_ROWS = [(8, 1, 64, 7, 16, 28672), (16, 1, 64, 4, 32, 28672), (32, 2, 64, 4, 64, 14336),
+             (7, 1, 64, 16, 128, 14336), (11, 1, 128, 3, 16, 28672), (8, 1, 128, 5, 32, 28672),
+             (16, 2, 128, 8, 64, 14336), (9, 1, 128, 11, 128, 14336), (16, 1, 128, 8, 16, 14336)]
+
+
+@pytest.mark.parametrize("nq,nkv,hd,K,block,cap", MANY_ROWS)
+def test_attention_many_rows(nq, nkv, hd, K, block, cap):
+    # around the kernel's tiles of 128 slots
+    lens = [0, 1, 120, 128, 129, 517, 383]
+    c = Cache(1, len(lens), nkv, cap, hd, block, nq + hd + K, spread=4)
+    q = queries(len(lens), K, nq, hd, "bf16", K + nq)
+    check_attention(c, 0, q, lens, K)
+    check_attention(c, 0, q, lens, K, causal=False)
+    check_attention(c, 0, q, lens, K, causal=False, scale=-0.05)
+    # (a window keeps the slots that a call sees few; at 28,088 and more the tcgen05 kernel runs)
+    check_attention(c, 0, q, lens, K, window=max(2, K // 2))
+    # the end of the capacity
+    lens = [cap - K, cap - 100, cap - 129 - K, 5, 5, 5, 5]
+    check_attention(c, 0, q, lens, K)
+
+
+@pytest.mark.parametrize("hd,G,K", [(64, 16, 4), (128, 8, 5), (128, 16, 8)])
+def test_attention_many_rows_long_and_many(hd, G, K):
+    """Heads over several CTAs beside short ones; more heads than CTAs; a window in long contexts."""
+    lens = [16000, 3, 9000]
+    c = Cache(1, 3, 4, 16512, hd, 32, 5, spread=2)
+    q = queries(3, K, 4 * G, hd, "bf16", 77)
+    check_attention(c, 0, q, lens, K)
+    lens = [int(x) for x in np.random.default_rng(9).integers(0, 300, 300)]
+    lens[7] = 4000
+    c = Cache(1, 300, 1, 4096, hd, 16, 6, spread=2)
+    q = queries(300, K, G, hd, "bf16", 78)
+    check_attention(c, 0, q, lens, K)
+    check_attention(c, 0, q, lens, K, window=1000)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("nq,nkv,hd,K", [(8, 1, 64, 8), (4, 1, 128, 1), (16, 1, 128, 8)])
 def test_attention_long_context(nq, nkv, hd, K, dtype):
@@ -378,17 +416,21 @@ def test_attention_many_requests(hd, G, K, dtype):
     check_attention(c, 0, queries(300, K, 2 * G, hd, dtype, 78), lens, K)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("nq,hd,K", [(4, 64, 4), (2, 128, 8), (16, 64, 8)])
-def test_attention_unseen_slots_never_matter(nq, hd, K, dtype):
+@pytest.mark.parametrize("nq,hd,K,cap,dtype", [
+    (4, 64, 4, 160, "bf16"), (4, 64, 4, 160, "f32"), (2, 128, 8, 160, "bf16"),
+    (2, 128, 8, 160, "f32"), (16, 64, 8, 160, "bf16"), (16, 64, 8, 160, "f32"),
+    # tcgen05
+    (16, 64, 8, 24576, "bf16"), (8, 128, 5, 49152, "bf16"), (12, 128, 7, 24576, "bf16")])
+def test_attention_unseen_slots_never_matter(nq, hd, K, cap, dtype):
     """Every slot that no row sees, and every scale of such blocks, is NaN; slots that only some
     rows see (the draft block, the window's edge) hold NaN for the rows that do not see them."""
     m = pk()
     lens = [0, 7, 40, 129]
-    B, cap, block = len(lens), 160, 16
+    B, block = len(lens), 16
     c = Cache(1, B, 1, cap, hd, block, 21)
     q = queries(B, K, nq, hd, dtype, 22)
-    for causal, window in ((True, 0), (False, 0), (True, 9), (True, 50), (False, 30)):
+    wide = cap // 2  # the rows' last slots again, and one window that reaches all of them
+    for causal, window in ((True, 0), (False, 0), (True, 9), (True, 50), (False, 30), (True, wide)):
         want, wl = attend(c, 0, q, lens, K, causal, window)
         keep = {n: t.clone() for n, t in c.t.items()}
         for b, n in enumerate(lens):
@@ -431,24 +473,25 @@ def test_attention_unseen_slots_never_matter(nq, hd, K, dtype):
             c.t[n_].copy_(t)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_attention_scales_far_apart(dtype):
+@pytest.mark.parametrize("nq,cap,dtype", [(4, 416, "bf16"), (4, 416, "f32"), (32, 98304, "bf16")])
+def test_attention_scales_far_apart(nq, cap, dtype):
     """Blocks whose scales differ by 2^40, zero blocks among them, and any scale, not only powers
     of two; sharp and flat rows; large and tiny queries."""
-    lens, K, nq, hd, block = [400, 90], 2, 4, 64, 16
+    lens, K, hd, block = [400, 90], 2, 64, 16
     for seed, size in ((1, 1.0), (2, 30.0), (3, 1e-6)):
-        c = Cache(1, 2, 1, 416, hd, block, seed, spread=0)
+        c = Cache(1, 2, 1, cap, hd, block, seed, spread=0)
         r = np.random.default_rng(seed)
-        s = 2.0 ** r.uniform(-20, 20, (1, 2, 1, 416 // block))
+        s = 2.0 ** r.uniform(-20, 20, (1, 2, 1, cap // block))
         c.t["v_scale"].copy_(torch.from_numpy(s.astype(np.float32)))
         c.t["k_scale"].copy_(torch.from_numpy((2.0 ** r.uniform(-1, 1, s.shape)).astype(np.float32)))
         c.t["v"].view(torch.uint8)[0, :, :, 32:48] = 0
         check_attention(c, 0, queries(2, K, nq, hd, dtype, seed, size), lens, K)
 
 
-def test_attention_queries_that_are_not_finite():
-    lens, K, nq, hd = [50, 7], 2, 2, 64
-    c = Cache(1, 2, 1, 64, hd, 32, 4)
+@pytest.mark.parametrize("nq,cap", [(2, 64), (32, 98304)])
+def test_attention_queries_that_are_not_finite(nq, cap):
+    lens, K, hd = [50, 7], 2, 64
+    c = Cache(1, 2, 1, cap, hd, 32, 4)
     for dtype in ("bf16", "f32"):
         q = queries(2, K, nq, hd, dtype, 5)
         want, _ = attend(c, 0, q, lens, K)
@@ -465,11 +508,12 @@ def test_attention_queries_that_are_not_finite():
         check_attention(c, 0, p, lens, K)
 
 
-def test_attention_requests_out_of_range_and_strided_queries():
+@pytest.mark.parametrize("nq,cap", [(4, 96), (32, 19680)])
+def test_attention_requests_out_of_range_and_strided_queries(nq, cap):
     m = pk()
-    K, nq, hd, cap = 3, 4, 128, 96
+    K, hd = 3, 128
     c = Cache(1, 5, 2, cap, hd, 32, 30)
-    fused = queries(5, K, 8, hd, "bf16", 31)
+    fused = queries(5, K, 2 * nq, hd, "bf16", 31)
     q = fused[:, :nq]  # rows of a fused projection
     lens = [5, -1, cap - K, cap - K + 1, 2 ** 31 - 1]
     out, lse = attend(c, 0, q, lens, K)
@@ -610,11 +654,12 @@ def test_parked_request_resumes_the_draft_pass():
     assert np.array_equal(toks[ok], ref.tokens[ok])
 
 
-def test_captured_round_replays_on_new_inputs():
+@pytest.mark.parametrize("nq,cap,window", [(8, 160, 70), (16, 49152, 0)])
+def test_captured_round_replays_on_new_inputs(nq, cap, window):
     """append + attention + commit in one CUDA graph, replayed while lengths advance, beside an
     eager call with its own workspace on another stream."""
     m = pk()
-    L, B, H, nq, hd, K, block, cap = 1, 2, 2, 8, 128, 5, 32, 160
+    L, B, H, hd, K, block = 1, 2, 2, 128, 5, 32
     c, e = fresh(L, B, H, cap, hd, block), fresh(L, B, H, cap, hd, block)
     rows = torch.zeros(2, L, B, K, H, hd, dtype=torch.bfloat16, device="cuda")
     q = torch.zeros(B * K, nq, hd, dtype=torch.bfloat16, device="cuda")
@@ -625,7 +670,7 @@ def test_captured_round_replays_on_new_inputs():
 
     def step(c, sl, rows, q, n, out, work):
         m.peagle_append_kv_quant(c.kv, B, sl, None, rows[0], rows[1], K, n_extra=K, advance=False)
-        m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, q, sl, out, work, window=70)
+        m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, q, sl, out, work, window=window)
         m.peagle_append_kv_quant(c.kv, B, sl, n, rows[0], rows[1], K)
 
     side = torch.cuda.Stream()
