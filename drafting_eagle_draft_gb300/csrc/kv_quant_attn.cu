@@ -29,7 +29,7 @@
 //
 // Work split.  A unit is a tile of 32 slots of one (request, kv head).  All units of the call,
 // in order, are cut into equal consecutive shares, one for each of CTAS CTAs (one an SM), so
-// ragged batches and single long requests fill the GPU alike.  Inside a CTA 8 / groups streams
+// ragged batches and single long requests fill the GPU alike.  Inside a CTA W / groups streams
 // of warps take the tiles of a (request, kv head) in turn (groups of warps share a stream's
 // tiles when there are more query rows than one warp's registers hold), each with its own
 // cp.async ring in shared memory that runs on across (request, kv head) boundaries.  At the end
@@ -40,7 +40,6 @@
 namespace peagle {
 namespace kvq {
 
-constexpr int W = 8;           // warps a CTA: two a scheduler, with 255 registers each
 constexpr int TILE = 32;       // slots a unit
 constexpr int ENTRY = 28;      // see find_share; 24 and 32 measured within 2 %, 8 up to 20 % slower
 constexpr int JOIN_WARPS = 4;  // of the second kernel
@@ -467,11 +466,16 @@ struct Running {
   }
 };
 
+// Warps a CTA: as many as their registers allow, 8 with up to 255 or 12 with 168.  12 read 65536
+// slots at head_dim 64 in 93 us for 8 query rows (8 warps 99, 16 warps 89) and 99 for 16 (115, 149);
+// 24 rows no longer fit (199 for 134), nor does head_dim 128 gain (8 rows 93 for 94).
+constexpr int warps_of(int hd, int nt, bool f32) { return hd == 64 && nt <= 2 && !f32 ? 12 : 8; }
+
 // Parts in which the warps' O^T go through the joining buffer.  At head_dim 128 parts leave room
 // for a third stage of the rings (NT 1 and 2; NT 3 has two either way).
 constexpr int join_passes(int hd, int nt) { return hd == 64 ? 1 : nt == 2 ? 4 : 2; }
 
-template <int HD, int NT, bool F32>
+template <int HD, int NT, bool F32, int W>
 __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) {
   typedef typename std::conditional<F32, float, bf16>::type T;
   typedef Queries<HD, NT, F32> Q;
@@ -847,7 +851,7 @@ static int64_t work_bytes(int hd, int ntiles) {
   return 4096 + (int64_t)CTAS * 2 * (int64_t)slot_bytes(hd, ntiles);
 }
 
-template <int HD, int NT, bool F32>
+template <int HD, int NT, bool F32, int W>
 static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
   constexpr size_t STAGE = 2 * TILE * HD + 16;
   constexpr size_t JOIN = (size_t)W * HD * NT * 32 / join_passes(HD, NT);
@@ -859,7 +863,7 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   a.stages = (int)(room / (streams * STAGE));
   a.stages = a.stages > 8 ? 8 : a.stages;
   const size_t smem = streams * a.stages * STAGE + fixed;
-  auto kernel = attn_quant_kernel<HD, NT, F32>;
+  auto kernel = attn_quant_kernel<HD, NT, F32, W>;
   cudaError_t e = smem_optin((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
@@ -959,7 +963,7 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \
-  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32>(a, p, (cudaStream_t)stream);
+  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, warps_of(HD, NT, F32)>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)
   PEAGLE_ATTN(64, 2, false)
   PEAGLE_ATTN(64, 3, false)
