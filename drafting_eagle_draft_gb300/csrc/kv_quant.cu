@@ -46,7 +46,7 @@ struct Piece {
   uint4 u[N];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < N; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ uint32_t word(int i) const {
     const uint4 x = u[i / 4];
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(READ_THREADS)
   for (int i = 0; i < READ_UNROLL; ++i) {
     const int64_t p = first + i * READ_THREADS;
     if (p < end) {
-      got[i] = __ldg(reinterpret_cast<const Code*>(code) + p);
-      s[i] = __ldg(scale + ((at + (int)(p / PER_ROW)) >> block_shift));
+      got[i] = reinterpret_cast<const Code*>(code)[p];
+      s[i] = scale[(at + (int)(p / PER_ROW)) >> block_shift];
     }
   }
 #pragma unroll

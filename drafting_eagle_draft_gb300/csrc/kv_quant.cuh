@@ -1,5 +1,8 @@
 // The 8-bit KV cache (peagle_kv_quant): argument checks and the e4m3 conversions that its
 // kernels share (kv_quant.cu writes and reads the cache, kv_quant_attn.cu attends over it).
+//
+// The kernels start before the one ahead of them in the stream has ended (programmatic launch), so
+// nothing they read is constant over their lifetime: plain loads, none through the read-only path.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -140,8 +140,8 @@ struct RawQuery {
                        (int64_t)(h * a.G + row - j * a.G) * HD + 16 * c) * (F32 ? 4 : 2);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        u[i] = __ldg(reinterpret_cast<const uint4*>(
-            q + ((i * E / 16) * 64 + i * E % 16) * (F32 ? 4 : 2)));
+        u[i] = *reinterpret_cast<const uint4*>(
+            q + ((i * E / 16) * 64 + i * E % 16) * (F32 ? 4 : 2));
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) u[i] = make_uint4(0, 0, 0, 0);
@@ -502,7 +502,10 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   // a share below 4 tiles would leave warps idle and make pieces to join
   Seg seg;
   int n, lo, share;
-  if (!find_share<TILE, ENTRY>(a, 4, seg, n, lo, share)) {
+  if (a.direct) {
+    lo = share = 0;
+    if (!find_heads<HD, T>(a, seg, n)) return;
+  } else if (!find_share<TILE, ENTRY>(a, 4, seg, n, lo, share)) {
     if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
@@ -727,11 +730,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
       const int len = a.seq_lens[b];
       int first;
       if (!request_fits(a, len) || request_tiles<TILE>(a, len, first)) continue;
-      const int64_t rows = (int64_t)a.K * a.nkv * a.G;
-      T* out = (T*)a.out + b * rows * HD;
-      for (int64_t i = threadIdx.x; i < rows * HD; i += JOIN_WARPS * 32) st(out + i, 0.f);
-      if (a.lse)
-        for (int64_t i = threadIdx.x; i < rows; i += JOIN_WARPS * 32) a.lse[b * rows + i] = -INFINITY;
+      write_empty<HD, T>(a, b, 0, a.nkv);
     }
   }
   if (d.x < 0) return;
@@ -868,7 +867,7 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
   if (e != cudaSuccess) return e;
-  return launch_join(HD, F32, false, a, p.ntiles(), s);
+  return a.direct ? e : launch_join(HD, F32, false, a, p.ntiles(), s);
 }
 
 cudaError_t launch_join(int hd, bool f32, bool rowmajor, const AttnQuantArgs& a, int ntiles,
@@ -955,11 +954,14 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   a.block_shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
   a.causal = causal, a.window = window, a.scale = scale * LOG2E;
   a.heads = a.nkv, a.part_rows = K * a.G;
-  const Plan p = plan_of(hd, f32, K * a.G);
-  cudaError_t e = cudaErrorInvalidValue;
-  // the slots that the call sees at most
+  // the slots that a head sees at most
   const int64_t most = window > 0 && window < kv->capacity - K ? window + K : kv->capacity;
-  if (attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
+  const Plan p = plan_of(hd, f32, K * a.G);
+  // Heads of at most two rounds of a CTA's streams are not worth a second step: one token over 128
+  // slots of two kv heads takes 4.7 us in one launch and 9.8 in two (in a graph).
+  a.direct = (most / TILE + 2) * p.groups <= 16;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (!a.direct && attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \

@@ -35,6 +35,7 @@ struct AttnQuantArgs {
   int groups;              // warps that share a stream's tiles, each NT x 8 query rows
   int stages;
   int part_rows;           // query rows of a part
+  int direct;              // every head lies whole in one CTA (short caches): no second step
   float scale;             // of the scores, with log2(e)
 };
 
@@ -159,6 +160,43 @@ __device__ __forceinline__ bool find_share(const AttnQuantArgs& a, int least, Se
   seg.h = in / (seg.tiles + seg.entry);
   seg.at = seg.entry - (in - seg.h * (seg.tiles + seg.entry));
   return seg.at < n;
+}
+
+// The rows of heads [h, h + heads) of a request none of whose rows sees a slot: zeros and -inf.
+template <int HD, typename T>
+__device__ __forceinline__ void write_empty(const AttnQuantArgs& a, int req, int h, int heads) {
+  const int nq = a.nkv * a.G, n = heads * a.G;
+  for (int j = 0; j < a.K; ++j) {
+    const int64_t row = ((int64_t)req * a.K + j) * nq + h * a.G;
+    for (int i = threadIdx.x; i < n * HD; i += blockDim.x) st((T*)a.out + row * HD + i, 0.f);
+    if (a.lse)
+      for (int i = threadIdx.x; i < n; i += blockDim.x) a.lse[row + i] = -INFINITY;
+  }
+}
+
+// find_share for a direct call: equal numbers of consecutive heads, each of them whole.  Writes the
+// heads that see no slot.
+template <int HD, typename T, int TILE>
+__device__ __forceinline__ bool find_heads(const AttnQuantArgs& a, Segment<TILE>& seg, int& n) {
+  const int all = a.batch * a.heads, per = (all + CTAS - 1) / CTAS;
+  const int begin = min(per * (int)blockIdx.x, all), end = min(begin + per, all);
+  n = 0;
+  seg.entry = seg.at = 1;
+  for (int b = begin / a.heads; b * a.heads < end; ++b) {
+    const int h = max(begin - b * a.heads, 0), heads = min(end - b * a.heads, a.heads) - h;
+    const int len = a.seq_lens[b];
+    int first;
+    const int tiles = request_tiles<TILE>(a, len, first);
+    if (!request_fits(a, len)) {
+      if (threadIdx.x == 0) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
+    } else if (!tiles) {
+      write_empty<HD, T>(a, b, h, heads);
+    } else {
+      if (!n) seg.b = b, seg.h = h, seg.len = len, seg.tiles = tiles, seg.first_tile = first;
+      n += heads * (tiles + seg.entry);
+    }
+  }
+  return n > 0;
 }
 
 // Two values of a row at consecutive head dims.

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
           // (scales of blocks without a slot to see may be anything)
           const int x = d.slot + lane % (TT / 16) * 16;
           const bool in = x + 16 > any_begin && x < any_end;
-          scales[t % DESCS][lane] = in ? __ldg(from + (x >> a.block_shift)) : lane < 8 ? 0.f : 1.f;
+          scales[t % DESCS][lane] = in ? from[x >> a.block_shift] : lane < 8 ? 0.f : 1.f;
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&raw_full[r]);
@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
           raw[i] = make_uint4(0, 0, 0, 0);
           if (row < a.part_rows && of < a.K * a.G) {
             const int j = of / a.G;
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(
+            raw[i] = *reinterpret_cast<const uint4*>(
                 (const bf16*)a.q + ((int64_t)d.b * a.K + j) * a.q_stride +
-                (int64_t)(d.h / parts * a.G + of - j * a.G) * HD + id % (HD / 8) * 8));
+                (int64_t)(d.h / parts * a.G + of - j * a.G) * HD + id % (HD / 8) * 8);
           }
         }
         for (int i = ct; i < RP; i += CONV) bad_row[at][i] = 0;
