@@ -439,18 +439,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); };
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float l[NC];
-    bool pending = true, chained = false, stop = false;
+    bool pending, chained = false, stop = false;
+    auto new_head = [&]() {
+      if (key < NC) neg_ref[col0 + key] = 0.f, has_slot[col0 + key] = false;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      pending = true;
+      group_sync();
+    };
+    new_head();
     for (int t = 0; !stop; ++t) {
       const int b = t & 1;
       wait(&s_full[b], t >> 1);
+      // (of no meaning after an abort: nothing up to the vote that ends the loop then may make some of
+      // the group's threads meet at a barrier and not others)
       const TileDesc d = descs[t % DESCS];
-      if (d.flags & FIRST) {
-        if (key < NC) neg_ref[col0 + key] = 0.f, has_slot[col0 + key] = false;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] = 0.f;
-        pending = true;
-        group_sync();
-      }
       tc::fence_after_sync();
       float x[NC];
       tc::tmem_ld32(tmem + lanes + 128 + b * 64 + col0, x);
@@ -636,6 +639,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&o_free);
         wait(&o_free, d.head);  // (the references and sums are free again)
+        new_head();
       }
       if (d.flags & END) break;
     }
