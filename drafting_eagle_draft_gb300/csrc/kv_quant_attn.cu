@@ -952,6 +952,8 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   a.batch = batch, a.K = K, a.G = n_q_heads / kv->n_kv_heads, a.nkv = kv->n_kv_heads;
   a.capacity = kv->capacity;
   a.block_shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
+  // (a window that no row's slots reach the end of is none: the kernels add slots to it in 32 bits)
+  if (window > kv->capacity + K) window = 0;
   a.causal = causal, a.window = window, a.scale = scale * LOG2E;
   a.heads = a.nkv, a.part_rows = K * a.G;
   // the slots that a head sees at most

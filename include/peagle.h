@@ -422,8 +422,9 @@ int peagle_decode_attention_static(int32_t batch, int32_t K, int32_t n_q_heads,
  * peagle_append_kv_quant makes the scale of a block the smallest power of two s, within
  * 2^-40 .. 2^120, with |x| <= 448 s for every finite live value x of the block (1 when they
  * are all zero), so a value of a block whose largest is A is off by at most 2^-4 of itself or
- * 2^-17.8 A (half the spacing of the smallest codes), whichever is more; the other calls take
- * any positive finite scale.  NaN and infinite values are stored as NaN.  Codes and scales of
+ * 2^-17.8 A (half the spacing of the smallest codes), whichever is more (magnitudes from 1.9375
+ * x 2^127 on round up to 2^128, infinity); the other calls take any positive finite scale.  NaN
+ * and infinite values are stored as NaN.  Codes and scales of
  * slots that nothing was appended to are never used and need no initial value.
  * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; block 16, 32, 64 or 128.
  * capacity is a multiple of block; k and v are 16-byte aligned; n_layers and batch are at
@@ -513,23 +514,28 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  *             256-byte aligned, no initial value; calls that may overlap on the GPU (other
  *             streams, graphs replayed at once) each have their own
  * A row that sees no slot gives zeros (and -inf).  Values and scores of slots that a row does
- * not see never reach it, NaN included.  fp32 accumulation, softmax and lse.  bf16 queries
- * enter exactly (down to 2^-31 of the largest element of their kv head's rows) and softmax weights rounded to
- * 11 bits, fp32 queries and their weights as two such parts (22 bits); weights x value scale
- * below 2^-10 of the row's largest lose bits, down to 2^-21 of it (fp32 queries: 2^-38).
- * Results are the same on every call with the same lengths (no atomics).
+ * not see never reach it, NaN included; a row of q that is not finite gives NaN.  fp32
+ * accumulation, softmax and lse.  bf16 queries enter exactly (down to 2^-31 of the largest
+ * element of their kv head's rows) and softmax weights rounded to 11 bits, fp32 queries and
+ * their weights as two such parts (22 bits); weights x value scale below 2^-10 of the row's
+ * largest lose bits, down to 2^-21 of it (fp32 queries: 2^-38), and below 2^-120 of it the
+ * weight leaves the sum of weights too: the value scales that matter to a row lie within 2^100
+ * of one another.
+ * Results are the same on every call with the same lengths and sizes (no atomics).
  * A request with seq_lens[b] < 0, or whose last row's slot is beyond the capacity, is
- * skipped with KV_OVERFLOW; its rows are left as they are.
- * Limits: K * n_q_heads / n_kv_heads <= 128 (else PEAGLE_ERR_UNSUPPORTED); a workspace that
- * is too small is PEAGLE_ERR_CAPACITY. */
+ * skipped with KV_OVERFLOW; its rows are left as they are.  Waits inside the kernel are
+ * bounded; one that ran out raises TIMEOUT, and the call's results are not to be used.
+ * Limits: K * n_q_heads / n_kv_heads <= 128, and batch * n_kv_heads * (capacity / 32 + 30)
+ * < 2^29 (else PEAGLE_ERR_UNSUPPORTED); a workspace that is too small is
+ * PEAGLE_ERR_CAPACITY. */
 int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
                                   int32_t K, int32_t n_q_heads, const void* q, int32_t dtype,
                                   int64_t q_stride, const int32_t* seq_lens, int32_t causal,
                                   int32_t window, float scale, void* out, float* out_lse,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that peagle_decode_attention_quant needs for these sizes on the current
- * device (for any layer, lengths and window), or a negative error. */
+/* Bytes of workspace that peagle_decode_attention_quant needs for these sizes (for any layer,
+ * lengths and window), or a negative error. */
 int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant* kv, int32_t batch,
                                                 int32_t K, int32_t n_q_heads);
 

@@ -259,7 +259,8 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
     weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to 11 bits
     (2^-12 relative; 2^-22 for the two parts of fp32) or, below f16's normal values, to half
     of 2^-24 where the largest weight x value scale of the row is at least 2^-4 (2^13 for fp32):
-    n 2^-21 448 s over all slots (2^-38), s the largest value scale.  Sums over n slots: (n + 64) u.  Then half a step of the output's type."""
+    n 2^-21 448 s over all slots (2^-38), s the largest value scale.  Sums over n slots:
+    (n + 64) u.  Then half a step of the output's type."""
     f32 = dtype == "f32"
     u = 2.0 ** -24
     BK, nq, hd = q.shape
@@ -394,6 +395,22 @@ def test_attention_many_rows_long_and_many(hd, G, K):
     q = queries(300, K, G, hd, "bf16", 78)
     check_attention(c, 0, q, lens, K)
     check_attention(c, 0, q, lens, K, window=1000)
+
+
+# one launch, two, and the tcgen05 kernel
+@pytest.mark.parametrize("nq,cap", [(8, 160), (8, 2048), (32, 98304)])
+def test_attention_windows_that_reach_every_slot(nq, cap):
+    """The largest window that leaves a slot out, the smallest that leaves none, and the largest."""
+    K = 7
+    c = Cache(1, 2, 2, cap, 64, 32, 8, spread=2)
+    q = queries(2, K, nq, 64, "bf16", 79)
+    lens = [cap - K, 130]
+    for causal in (True, False):
+        out, lse = check_attention(c, 0, q, lens, K, causal=causal)
+        for window in (cap, cap + K, cap + K + 1, 2 ** 31 - 1):
+            got = check_attention(c, 0, q, lens, K, causal=causal, window=window)
+            assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+        check_attention(c, 0, q, lens, K, causal=causal, window=cap - 1)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

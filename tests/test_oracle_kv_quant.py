@@ -184,6 +184,10 @@ def test_attention_refuses(pk):
     assert call(dtype=7) == uns
     assert call(K=16, nq=18) == uns and call(K=129, nq=2) == uns
     assert call(batch=4) == cap
+    # (slots of a layer beyond what the walk over them counts)
+    big = _kv(pk, batch=65535, n_kv_heads=16, capacity=1 << 15)
+    assert L.peagle_decode_attention_quant(big, 0, 65535, 2, 16, A, pk.PEAGLE_BF16, 0, A, 1, 0,
+                                           0.125, A, None, A, 1 << 40, None) == uns
     need = L.peagle_decode_attention_quant_workspace(kv, 3, 2, 4)
     assert need > 0 and call(n=need - 1) == cap and call(n=0) == cap
 
