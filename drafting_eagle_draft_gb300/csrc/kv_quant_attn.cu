@@ -43,6 +43,7 @@ namespace kvq {
 constexpr int TILE = 32;       // slots a unit
 constexpr int ENTRY = 28;      // see find_share; 24 and 32 measured within 2 %, 8 up to 20 % slower
 constexpr int JOIN_WARPS = 4;  // of the second kernel
+constexpr int MAX_SPLIT = 8;   // CTAs of a cluster that share a head
 typedef Segment<TILE> Seg;
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -102,6 +103,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
 __device__ __forceinline__ uint2 lds64(uint32_t p) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+  return v;
+}
+
+// (an address that mapa_shared gave)
+__device__ __forceinline__ float4 ld_cluster(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(p)
+               : "memory");
   return v;
 }
 
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
   // a share below 4 tiles would leave warps idle and make pieces to join
   Seg seg;
   int n, lo, share;
-  if (a.direct) {
+  if (a.split) {
     lo = share = 0;
     if (!find_heads<HD, T>(a, seg, n)) return;
   } else if (!find_share<TILE, ENTRY>(a, 4, seg, n, lo, share)) {
@@ -514,6 +525,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
                         (uint32_t)(stream * a.stages) * STAGE;
   uint2* prepared = reinterpret_cast<uint2*>(smem + (size_t)streams * a.stages * STAGE);
   float4* joined = reinterpret_cast<float4*>(prepared + groups * NT * (Q::TILE_BYTES / 8));
+  float* piece = reinterpret_cast<float*>(joined + W * PASS);  // what the cluster's CTAs join
 
   // The stream's loads run ahead of its products, over (request, kv head) boundaries.  A lane
   // copies the same chunks of every tile: rows WARP_ROWS groups apart, whose places in a stage
@@ -634,8 +646,24 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
         }
       }
     const bool began = done.at >= 0, whole = began && done.at + done.tiles <= n;
-    float* slot = a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
-                               ((size_t)groups * NT * 8 * (HD + 2));
+    float* slot = a.split > 1 ? piece
+                              : a.work + ((size_t)blockIdx.x * 2 + (began ? 1 : 0)) *
+                                             ((size_t)groups * NT * 8 * (HD + 2));
+    // column i of the fragments of rows row and row + 1
+    auto write = [&](int row, int i, float m0, float l0, float m1, float l1, const float4& o) {
+      const int d = r * (HD / 8) + 2 * i;
+      float inv;
+      if (row < a.K * a.G) {
+        T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row], m0, l0,
+                               i == 0 && r == 0, inv);
+        store2(out + d, o.x * inv, o.z * inv);
+      }
+      if (row + 1 < a.K * a.G) {
+        T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row + 1], m1, l1,
+                               i == 0 && r == 0, inv);
+        store2(out + d, o.y * inv, o.w * inv);
+      }
+    };
 #pragma unroll 1
     for (int pass = 0; pass < PASSES; ++pass) {
       if (pass) __syncthreads();
@@ -678,19 +706,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
         }
         const int row = (g * NT + nt) * 8 + 2 * c;
         const float m0 = sum_m[row], m1 = sum_m[row + 1], l0 = sum_l[row], l1 = sum_l[row + 1];
-        if (whole) {
-          const int d = r * (HD / 8) + 2 * i;
-          float inv;
-          if (row < a.K * a.G) {
-            T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row], m0, l0,
-                                   i == 0 && r == 0, inv);
-            store2(out + d, o.x * inv, o.z * inv);
-          }
-          if (row + 1 < a.K * a.G) {
-            T* out = finish_row<T>(a, HD, done.b, done.h * a.G + row_at[row + 1], m1, l1,
-                                   i == 0 && r == 0, inv);
-            store2(out + d, o.y * inv, o.w * inv);
-          }
+        if (whole && a.split < 2) {
+          write(row, i, m0, l0, m1, l1, o);
         } else {
           if (i == 0 && r == 0)
             *reinterpret_cast<float4*>(slot + 2 * row) = make_float4(m0, l0, m1, l1);
@@ -699,7 +716,39 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
         }
       }
     }
-    if (began && !whole) {
+    if (a.split > 1) {
+      // the cluster's warps share the columns of the pieces, which they read in one another's memory
+      __syncwarp();
+      tc::cluster_sync();
+      for (int col = (int)tc::cluster_ctarank() * W + warp; col < groups * NT * (HD / 16); col += a.split * W) {
+        const int i = col % (HD / 16), row = col / (HD / 16) * 8 + 2 * c;
+        float4 f[MAX_SPLIT], g[MAX_SPLIT];
+        float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int p = 0; p < MAX_SPLIT; ++p) {
+          f[p] = make_float4(NO_REF, 0.f, NO_REF, 0.f);
+          g[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p < a.split) {
+            const uint32_t from = tc::mapa_shared(piece, p);
+            f[p] = ld_cluster(from + 8 * row);
+            g[p] = ld_cluster(from + 64 * groups * NT + 16 * (col * 32 + lane));
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < MAX_SPLIT; ++p) m0 = fmaxf(m0, f[p].x), m1 = fmaxf(m1, f[p].z);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < MAX_SPLIT; ++p) {
+          const float x0 = ex2(f[p].x - m0), x1 = ex2(f[p].z - m1);
+          l0 = fmaf(f[p].y, x0, l0), l1 = fmaf(f[p].w, x1, l1);
+          o.x = fmaf(g[p].x, x0, o.x), o.y = fmaf(g[p].y, x1, o.y);
+          o.z = fmaf(g[p].z, x0, o.z), o.w = fmaf(g[p].w, x1, o.w);
+        }
+        write(row, i, m0, l0, m1, l1, o);
+      }
+      __syncwarp();
+      tc::cluster_sync();  // (a CTA's memory is its own again, or may end)
+    } else if (began && !whole) {
       chained = true;
       if (threadIdx.x == 0)
         a.desc[blockIdx.x] =
@@ -707,7 +756,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
     }
     if (last) break;
   }
-  if (threadIdx.x == 0 && !chained) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !chained && !a.split) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   cp_async_wait(0);
 }
 
@@ -850,12 +899,27 @@ static int64_t work_bytes(int hd, int ntiles) {
   return 4096 + (int64_t)CTAS * 2 * (int64_t)slot_bytes(hd, ntiles);
 }
 
+// Clusters of CTAs as large as these that the GPU's GPCs hold at a time.
+static int clusters_of(int split) { return split == 1 ? CTAS : split == 2 ? 76 : split == 4 ? 36 : 15; }
+
+// The CTAs that share a head when the call is done in one step, or 0 when two steps take less time:
+// equal shares of the call's tiles and the kernel that joins their pieces.
+static int split_of(const Plan& p, int warps, int64_t heads, int64_t slots) {
+  const int64_t tiles = (slots / TILE + 2) * p.groups;
+  int split = MAX_SPLIT;
+  while (split > 1 && (heads > clusters_of(split) || tiles <= warps * split / 2)) split /= 2;
+  const int64_t per = (heads + clusters_of(split) - 1) / clusters_of(split);
+  const int64_t rounds = (tiles + warps * split - 1) / (warps * split);
+  return per * (rounds + 2) <= 6 + heads * tiles / (CTAS * warps) ? split : 0;
+}
+
 template <int HD, int NT, bool F32, int W>
 static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t s) {
   constexpr size_t STAGE = 2 * TILE * HD + 16;
   constexpr size_t JOIN = (size_t)W * HD * NT * 32 / join_passes(HD, NT);
   const int streams = W / p.groups;
-  const size_t fixed = JOIN + (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES;
+  const size_t fixed = JOIN + (size_t)p.ntiles() * Queries<HD, NT, F32>::TILE_BYTES +
+                       (a.split > 1 ? slot_bytes(HD, p.ntiles()) : 0);
   // up to 8 stages a stream, within the 227 KB of a CTA less its static arrays
   const size_t room = 221 * 1024 - fixed;
   a.groups = p.groups;
@@ -865,9 +929,25 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
   auto kernel = attn_quant_kernel<HD, NT, F32, W>;
   cudaError_t e = smem_optin((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
-  if (e != cudaSuccess) return e;
-  return a.direct ? e : launch_join(HD, F32, false, a, p.ntiles(), s);
+  if (!a.split) {
+    e = launch_pdl(kernel, dim3(CTAS), dim3(W * 32), smem, s, a);
+    return e == cudaSuccess ? launch_join(HD, F32, false, a, p.ntiles(), s) : e;
+  }
+  const int64_t heads = (int64_t)a.batch * a.heads, most = clusters_of(a.split);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((heads < most ? heads : most) * a.split));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_join(int hd, bool f32, bool rowmajor, const AttnQuantArgs& a, int ntiles,
@@ -959,11 +1039,9 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   // the slots that a head sees at most
   const int64_t most = window > 0 && window < kv->capacity - K ? window + K : kv->capacity;
   const Plan p = plan_of(hd, f32, K * a.G);
-  // Heads of at most two rounds of a CTA's streams are not worth a second step: one token over 128
-  // slots of two kv heads takes 4.7 us in one launch and 9.8 in two (in a graph).
-  a.direct = (most / TILE + 2) * p.groups <= 16;
+  a.split = split_of(p, warps_of(hd, p.nt, f32), (int64_t)batch * a.nkv, most);
   cudaError_t e = cudaErrorInvalidValue;
-  if (!a.direct && attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
+  if (!a.split && attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
 #define PEAGLE_ATTN(HD, NT, F32) \

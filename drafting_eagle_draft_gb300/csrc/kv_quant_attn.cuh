@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "kv_quant.cuh"
+#include "tc_ptx.cuh"
 
 namespace peagle {
 namespace kvq {
@@ -35,7 +36,8 @@ struct AttnQuantArgs {
   int groups;              // warps that share a stream's tiles, each NT x 8 query rows
   int stages;
   int part_rows;           // query rows of a part
-  int direct;              // every head lies whole in one CTA (short caches): no second step
+  int split;               // > 0: a cluster of that many CTAs (a power of two) takes whole heads,
+                           // and there is no second step
   float scale;             // of the scores, with log2(e)
 };
 
@@ -106,7 +108,15 @@ struct Segment {
       len = a.seq_lens[b];
       tiles = request_tiles<TILE>(a, len, first_tile);
     } while (!tiles);
+    cut(a);
     return true;
+  }
+  // Of a request's tiles those of this CTA of its cluster, none perhaps.
+  __device__ __forceinline__ void cut(const AttnQuantArgs& a) {
+    if (a.split < 2) return;
+    const int shift = __ffs(a.split) - 1, r = (int)tc::cluster_ctarank(), from = tiles * r >> shift;
+    tiles = (tiles * (r + 1) >> shift) - from;
+    first_tile += from;
   }
 };
 
@@ -174,26 +184,30 @@ __device__ __forceinline__ void write_empty(const AttnQuantArgs& a, int req, int
   }
 }
 
-// find_share for a direct call: equal numbers of consecutive heads, each of them whole.  Writes the
-// heads that see no slot.
+// find_share for a call in one step: equal numbers of consecutive heads a cluster, and of each head
+// this CTA's part.  Writes the heads that see no slot.
 template <int HD, typename T, int TILE>
 __device__ __forceinline__ bool find_heads(const AttnQuantArgs& a, Segment<TILE>& seg, int& n) {
-  const int all = a.batch * a.heads, per = (all + CTAS - 1) / CTAS;
-  const int begin = min(per * (int)blockIdx.x, all), end = min(begin + per, all);
+  const int shift = __ffs(a.split) - 1;
+  const int clusters = gridDim.x >> shift, all = a.batch * a.heads;
+  const int per = (all + clusters - 1) / clusters;
+  const int begin = min(per * (int)(blockIdx.x >> shift), all), end = min(begin + per, all);
+  const bool lead = a.split == 1 || (int)tc::cluster_ctarank() == 0;
   n = 0;
-  seg.entry = seg.at = 1;
+  seg.entry = 1, seg.at = 0;  // (the entry comes after the tiles here: a head without any counts too)
   for (int b = begin / a.heads; b * a.heads < end; ++b) {
     const int h = max(begin - b * a.heads, 0), heads = min(end - b * a.heads, a.heads) - h;
-    const int len = a.seq_lens[b];
-    int first;
-    const int tiles = request_tiles<TILE>(a, len, first);
-    if (!request_fits(a, len)) {
-      if (threadIdx.x == 0) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
-    } else if (!tiles) {
-      write_empty<HD, T>(a, b, h, heads);
+    Segment<TILE> x = seg;
+    x.b = b, x.h = h, x.len = a.seq_lens[b];
+    x.tiles = request_tiles<TILE>(a, x.len, x.first_tile);
+    if (!request_fits(a, x.len)) {
+      if (lead && threadIdx.x == 0) raise_error(a.errors, PEAGLE_DEV_KV_OVERFLOW);
+    } else if (!x.tiles) {
+      if (lead) write_empty<HD, T>(a, b, h, heads);
     } else {
-      if (!n) seg.b = b, seg.h = h, seg.len = len, seg.tiles = tiles, seg.first_tile = first;
-      n += heads * (tiles + seg.entry);
+      x.cut(a);
+      if (!n) seg = x;
+      n += heads * (x.tiles + seg.entry);
     }
   }
   return n > 0;

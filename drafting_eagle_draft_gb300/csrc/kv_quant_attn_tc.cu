@@ -31,7 +31,6 @@
 // of 128 threads that each convert, multiply and weigh their own tiles (195 us for what takes 146),
 // the weights computed while the votes come in (123 for 108: the code leaves the instruction cache).
 #include "kv_quant_attn.cuh"
-#include "tc_ptx.cuh"
 
 namespace peagle {
 namespace kvq {

@@ -42,6 +42,12 @@ class Cache:
         return (self.t[name].float().cpu().double().numpy(),
                 self.t[name + "_scale"].cpu().double().numpy())
 
+    def alone(self, b):
+        """Request b's part, for check_result."""
+        c = Cache.__new__(Cache)
+        c.block, c.t = self.block, {k: t[:, b:b + 1] for k, t in self.t.items()}
+        return c
+
     def err(self):
         e = int(self.errors.item())
         self.errors.zero_()
@@ -256,8 +262,11 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
     drop 2^-22 of an element, or of 2^-2 of the row's largest where an element is that small:
     2^-22 S + 2^-24 scale max|q| sum |k|.  A score's error d moves the weights by 2 d relative
     (numerator and sum).  The exponential's argument carries u of its size (|x| < 2^8 before a
-    weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to 11 bits
-    (2^-12 relative; 2^-22 for the two parts of fp32) or, below f16's normal values, to half
+    weight vanishes: 2^-16 absolute is 2^8 u) and the SFU 2^-21.  Weights are rounded to f16's 11
+    bits in the numerator and not in the sum: consecutive values with e = 2^k <= w < 2^(k+1) are
+    2^-10 e apart, so half a step is 2^-11 e <= 2^-11 w (one slot seen alone gets all of it: its
+    result is v round(w) / w).  fp32's second part holds the rest, at most 2^-11 w, to 11 bits
+    again: 2^-22 or, below f16's normal values, to half
     of 2^-24 where the largest weight x value scale of the row is at least 2^-4 (2^13 for fp32):
     n 2^-21 448 s over all slots (2^-38), s the largest value scale.  Sums over n slots:
     (n + 64) u.  Then half a step of the output's type."""
@@ -279,7 +288,7 @@ def bounds(q, kval, vval, vscale_max, lens, K, causal, window, scale, out, lse, 
             if f32:
                 d += 2.0 ** -22 * S + u * abs(scale) * np.abs(q[r, h]).max() * ak.sum(-1).max()
             d += 2.0 ** -15 + 2.0 ** -21 + 4 * u * S
-            w, tiny = (2.0 ** -22, 2.0 ** -38) if f32 else (2.0 ** -12, 2.0 ** -21)
+            w, tiny = (2.0 ** -22, 2.0 ** -38) if f32 else (2.0 ** -11, 2.0 ** -21)
             to[r, h] = absolute[r, h] * (2 * d + w + 2 * (n + 64) * u) + \
                 n * tiny * 448.0 * vscale_max[b, h // G]
             tl[r, h] = d + (n + 64) * u + 4 * u * abs(lse[r, h])
@@ -395,6 +404,31 @@ def test_attention_many_rows_long_and_many(hd, G, K):
     q = queries(300, K, G, hd, "bf16", 78)
     check_attention(c, 0, q, lens, K)
     check_attention(c, 0, q, lens, K, window=1000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,G,K", [(64, 1, 1), (64, 4, 3), (64, 8, 8), (128, 8, 1), (128, 4, 5),
+                                    (128, 16, 8)])
+@pytest.mark.parametrize("heads", [1, 3, 7, 20])
+def test_attention_heads_shared_by_clusters(hd, G, K, heads, dtype):
+    """Capacities at which several CTAs share a head in one launch: 8, 4, 2 and 1 of them, shares
+    without a tile, requests that are empty or do not fit beside others of the same cluster."""
+    m = pk()
+    lens = [2040, 0, 1, 33, 300]
+    c = Cache(1, 5, heads, 2048, hd, 32, heads + hd, spread=2)
+    q = queries(5, K, heads * G, hd, dtype, 80)
+    check_attention(c, 0, q, lens, K)
+    check_attention(c, 0, q, [5, 6, 2048, 640, 31], K, causal=False)
+    check_attention(c, 0, q, [1111, 1999, 2, 640, 0], K, window=100)
+    bad = [5, -1, 2049, 640, 700]
+    out, lse = attend(c, 0, q, bad, K)
+    assert c.err() == m.PEAGLE_DEV_KV_OVERFLOW
+    for b in range(5):
+        rows = slice(b * K, (b + 1) * K)
+        if b in (1, 2):
+            assert (out[rows] == -7.0).all() and (lse[rows] == -7.0).all()
+        else:
+            check_result(c.alone(b), 0, q[rows], [bad[b]], K, True, 0, None, out[rows], lse[rows])
 
 
 # one launch, two, and the tcgen05 kernel
@@ -537,9 +571,7 @@ def test_attention_requests_out_of_range_and_strided_queries(nq, cap):
     assert c.err() == m.PEAGLE_DEV_KV_OVERFLOW
     for b, n in ((0, 5), (2, cap - K)):
         one = slice(b * K, (b + 1) * K)
-        at = Cache.__new__(Cache)  # request b alone
-        at.block, at.t = c.block, {k: t[:, b:b + 1] for k, t in c.t.items()}
-        check_result(at, 0, q[one], [n], K, True, 0, None, out[one], lse[one])
+        check_result(c.alone(b), 0, q[one], [n], K, True, 0, None, out[one], lse[one])
     for b in (1, 3, 4):
         assert (out[b * K:(b + 1) * K] == -7.0).all() and (lse[b * K:(b + 1) * K] == -7.0).all()
     out, _ = attend(c, 0, q, [5, 1, 2, cap - K + 1, cap], K, causal=False)  # the prefix alone fits
