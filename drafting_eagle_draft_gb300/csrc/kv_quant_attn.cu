@@ -902,15 +902,30 @@ static int64_t work_bytes(int hd, int ntiles) {
 // Clusters of CTAs as large as these that the GPU's GPCs hold at a time.
 static int clusters_of(int split) { return split == 1 ? CTAS : split == 2 ? 76 : split == 4 ? 36 : 15; }
 
-// The CTAs that share a head when the call is done in one step, or 0 when two steps take less time:
-// equal shares of the call's tiles and the kernel that joins their pieces.
-static int split_of(const Plan& p, int warps, int64_t heads, int64_t slots) {
+// The CTAs that share a head when the call is done in one step, or 0 when two steps take less time
+// (equal shares of the call's tiles, and the kernel that joins their pieces).  As many CTAs as find
+// room, unless one does the head in a round of its warps.  Two steps spread long heads better, one
+// saves a launch, the way through the workspace and shares that lie over two heads; a round's cost
+// follows from its products.  us in one step / in two, at full capacity (shorter and ragged requests
+// favour the one step more: 16 heads of 20 fp32 rows over 61 and 1051 slots 13 / 19):
+//   slots a head:                              288        544        1056       2080       4128
+//   4 rows of head_dim 128, 8 heads         7.2 / 12.2  7.2 / 12.2  7.4 / 12.3  8.5 / 9.6  10.0 / 10.3
+//   20 rows of head_dim 128, 8 heads       10.6 / 18.2 10.8 / 18.3 11.5 / 18.7 13.6 / 13.4 15.9 / 14.8
+//   20 rows in fp32, 32 heads              11.3 / 19.6 12.8 / 15.9 14.9 / 20.4 20.4 / 23.7 29.3 / 32.9
+//   8 rows of head_dim 64, 16 heads         5.9 / 11.0  6.4 / 11.2  6.7 / 9.0   7.7 / 9.5   9.0 / 11.5
+//   64 rows of head_dim 64, 8 heads         9.0 / 15.9  9.2 / 16.1 10.3 / 16.1 11.6 / 12.5 14.2 / 13.8
+//   64 rows of head_dim 64, 72 heads       10.5 / 15.4 11.8 / 17.9 14.6 / 21.3 20.5 / 29.2 30.8 / 34.8
+static int split_of(int hd, bool f32, const Plan& p, int warps, int64_t heads, int64_t slots) {
   const int64_t tiles = (slots / TILE + 2) * p.groups;
-  int split = MAX_SPLIT;
-  while (split > 1 && (heads > clusters_of(split) || tiles <= warps * split / 2)) split /= 2;
-  const int64_t per = (heads + clusters_of(split) - 1) / clusters_of(split);
-  const int64_t rounds = (tiles + warps * split - 1) / (warps * split);
-  return per * (rounds + 2) <= 6 + heads * tiles / (CTAS * warps) ? split : 0;
+  int split = tiles <= warps ? 1 : MAX_SPLIT;
+  while (heads > clusters_of(split) && split > 1) split /= 2;
+  const int64_t per = (heads + clusters_of(split) - 1) / clusters_of(split);  // heads a cluster
+  const double round = hd / 64 * (p.nt * (f32 ? 2 : 1) + 2) / 5.;             // us, about
+  const double one = (double)tiles / (warps * split);                         // rounds a head
+  const double rounds = (double)per * (one + 2) - 2;
+  const double shares = (double)heads * (double)tiles / (CTAS * warps);
+  const double saved = .3 * p.ntiles() > 2.6 ? .3 * p.ntiles() : 2.6;
+  return (rounds - shares) * round <= saved ? split : 0;
 }
 
 template <int HD, int NT, bool F32, int W>
@@ -1039,11 +1054,15 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   // the slots that a head sees at most
   const int64_t most = window > 0 && window < kv->capacity - K ? window + K : kv->capacity;
   const Plan p = plan_of(hd, f32, K * a.G);
-  a.split = split_of(p, warps_of(hd, p.nt, f32), (int64_t)batch * a.nkv, most);
+  const int warps = warps_of(hd, p.nt, f32);
+  const int64_t heads = (int64_t)batch * a.nkv;
   cudaError_t e = cudaErrorInvalidValue;
-  if (!a.split && attn_quant_tc_takes(hd, f32, K * a.G, (int64_t)batch * a.nkv * most))
+  // (the tcgen05 kernel only where heads are more than two rounds of a CTA's warps)
+  a.split = 0;
+  if ((most / TILE + 2) * p.groups > 2 * warps && attn_quant_tc_takes(hd, f32, K * a.G, heads * most))
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
+  a.split = split_of(hd, f32, p, warps, heads, most);
 #define PEAGLE_ATTN(HD, NT, F32) \
   if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, warps_of(HD, NT, F32)>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)
