@@ -95,14 +95,20 @@ __device__ __forceinline__ unsigned finite(unsigned bits) { return bits < 0x7f80
 // token lie side by side.
 //
 // Long rows are bound by memory: U = 4 units in flight a CTA and 64 registers a thread (1024 threads
-// an SM) hide the chain length -> rows -> maximum -> codes.  Four prompts of 1001 .. 8192 bf16 tokens
-// in 4 layers of 8 heads of 128: 91.7 us, 4.9 TB/s of the bytes they cannot do without (73 % of the
-// measured copy rate); 99 with U = 2, 94 with 51 registers, 103 with 3 CTAs an SM.  A draft block is
-// bound by latency, and U = 2 spreads its units over more CTAs.
-template <int HD, int BLOCK, int U, typename T>
+// an SM) hide the chain length -> rows -> maximum -> codes.  Counts are on the device, so CTAs for the
+// longest request find the others ended: with LOOP a CTA goes on to the blocks `stride` further on, and
+// there are a quarter as many.  Four prompts of 1001 .. 8192 bf16 tokens in 4 layers of 8 heads of 128:
+// 80.6 us, 5.6 TB/s of the bytes they cannot do without (83 % of the measured copy rate), 87 without
+// LOOP; 16 such prompts 291 (91 %) and 343, four in fp32 115 (96 %) and 135.  (Before LOOP: 99 with
+// U = 2, 103 with 3 CTAs an SM.)  A draft block is bound by latency, and U = 2 spreads its units over
+// more CTAs.
+// APPEND_MANY: the CTAs, 16 rounds of those that an SM holds, from which on LOOP pays; one prompt of
+// 2048 tokens in 4 layers of 8 heads of 128 takes 17.8 us with it and 13.1 without.
+constexpr int APPEND_MANY = 16 * 4 * 152;
+template <int HD, int BLOCK, int U, bool LOOP, typename T>
 __global__ void __launch_bounds__(BLOCK* HD / 16, 1024 / (BLOCK * HD / 16))
     append_quant_kernel(CacheArgs c, RowsArgs rows, const int* seq_lens, const int* n_commit,
-                        int n_extra, int n_max) {
+                        int n_extra, int n_max, int stride) {
   pdl_enter();
   constexpr int THREADS = BLOCK * HD / 16, WARPS = THREADS / 32;
   __shared__ unsigned red[U][WARPS];
@@ -113,109 +119,112 @@ __global__ void __launch_bounds__(BLOCK* HD / 16, 1024 / (BLOCK * HD / 16))
   if (!rows_fit(at, n, n_max, c.capacity, c.errors,
                 blockIdx.x == 0 && l == 0 && threadIdx.x == 0))
     return;
-  const int first = at / BLOCK + (int)(blockIdx.x / c.heads) * (U / 2);
-  const int64_t end = at + n;  // (the first slot behind the rows)
-  if (n == 0 || (int64_t)first * BLOCK >= end) return;
+  if (n == 0) return;
+  const int end = at + (int)n, last = (end - 1) / BLOCK;  // the slot behind the rows, their last block
 
   const int t = threadIdx.x / (HD / 16), d = threadIdx.x % (HD / 16) * 16;
   const int64_t unit = ((int64_t)(c.layer0 + l) * c.batch + b) * c.heads + h;
   const int64_t row0 = l * rows.layer + b * rows.batch + h * rows.head + d;
-  // what this thread's slot of a unit is: a new row, a committed one, or neither
-  auto fresh = [&](int u) {
-    const int slot = (first + u / 2) * BLOCK + t;
-    return slot >= at && slot < end;
-  };
-  auto old = [&](int u) { return (first + u / 2) * BLOCK + t < at; };
-  auto code = [&](int u) {
-    return (u & 1 ? c.v : c.k) + (unit * c.capacity + (first + u / 2) * BLOCK + t) * HD + d;
-  };
-  auto scale = [&](int u) {
-    return (u & 1 ? c.v_scale : c.k_scale) + unit * (c.capacity / BLOCK) + first + u / 2;
-  };
+  for (int first = at / BLOCK + (int)(blockIdx.x / c.heads) * (U / 2); first <= last; first += stride) {
+    // what this thread's slot of a unit is: a new row, a committed one, or neither
+    auto fresh = [&](int u) {
+      const int slot = (first + u / 2) * BLOCK + t;
+      return slot >= at && slot < end;
+    };
+    auto old = [&](int u) { return (first + u / 2) * BLOCK + t < at; };
+    auto code = [&](int u) {
+      return (u & 1 ? c.v : c.k) + (unit * c.capacity + (first + u / 2) * BLOCK + t) * HD + d;
+    };
+    auto scale = [&](int u) {
+      return (u & 1 ? c.v_scale : c.k_scale) + unit * (c.capacity / BLOCK) + first + u / 2;
+    };
 
-  Piece<T> x[U];
-  float was[U];
+    Piece<T> x[U];
+    float was[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    was[u] = 0.f;
-    if (fresh(u)) {
-      const int64_t row = (first + u / 2) * BLOCK + t - at;
-      x[u].load(reinterpret_cast<const T*>(u & 1 ? rows.v : rows.k) + row0 + row * rows.token);
-    } else if (u < 2 && old(u)) {
-      was[u] = *scale(u);
-      x[u].u[0] = *reinterpret_cast<const uint4*>(code(u));
-    }
-  }
-  // Magnitudes as bits (their order is the magnitudes' order), the largest over the CTA.
-  auto cta_top = [&](int u, unsigned top) {
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) red[u][threadIdx.x >> 5] = top;
-  };
-  auto all_top = [&](int u) {
-    unsigned top = red[u][threadIdx.x % WARPS];
-#pragma unroll
-    for (int o = WARPS / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    return top;
-  };
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    unsigned top = 0;
-    if (fresh(u)) {
-      top = x[u].row_top();
-    } else if (u < 2 && old(u)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = x[u].code_pair(i, was[u]);
-        top = max(top, max(magnitude(f.x), magnitude(f.y)));
+    for (int u = 0; u < U; ++u) {
+      was[u] = 0.f;
+      if (fresh(u)) {
+        const int64_t row = (first + u / 2) * BLOCK + t - at;
+        x[u].load(reinterpret_cast<const T*>(u & 1 ? rows.v : rows.k) + row0 + row * rows.token);
+      } else if (u < 2 && old(u)) {
+        was[u] = *scale(u);
+        x[u].u[0] = *reinterpret_cast<const uint4*>(code(u));
       }
     }
-    cta_top(u, top);
-  }
-  __syncthreads();
+    // Magnitudes as bits (their order is the magnitudes' order), the largest over the CTA.
+    auto cta_top = [&](int u, unsigned top) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((threadIdx.x & 31) == 0) red[u][threadIdx.x >> 5] = top;
+    };
+    auto all_top = [&](int u) {
+      unsigned top = red[u][threadIdx.x % WARPS];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if ((int64_t)(first + u / 2) * BLOCK >= end) break;
-    unsigned top = all_top(u);
-    const bool special = top >= 0x7f800000u;
-    if (special) {  // (all of the CTA) infinities or NaN: once more without them
-      __syncthreads();
-      top = 0;
-      if (fresh(u) || (u < 2 && old(u))) {
+      for (int o = WARPS / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      return top;
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      unsigned top = 0;
+      if (fresh(u)) {
+        top = x[u].row_top();
+      } else if (u < 2 && old(u)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 f = fresh(u) ? x[u].row_pair(i) : x[u].code_pair(i, was[u]);
-          top = max(top, max(finite(magnitude(f.x)), finite(magnitude(f.y))));
+          const float2 f = x[u].code_pair(i, was[u]);
+          top = max(top, max(magnitude(f.x), magnitude(f.y)));
         }
       }
       cta_top(u, top);
-      __syncthreads();
-      top = all_top(u);
     }
-    // adding 0x1fffff carries into the exponent when the fraction is above 1.75's
-    int e = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
-    e = top ? min(max(e, -40), 120) : 0;
-    const float s = __uint_as_float((unsigned)(127 + e) << 23);
-    const float inv = __uint_as_float((unsigned)(127 - e) << 23);
-    if (fresh(u) || (u < 2 && old(u) && s != was[u])) {
-      uint32_t q[4];
+    __syncthreads();
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float2 y[2];
+    for (int u = 0; u < U; ++u) {
+      if (first + u / 2 > last) break;
+      unsigned top = all_top(u);
+      const bool special = top >= 0x7f800000u;
+      if (special) {  // (all of the CTA) infinities or NaN: once more without them
+        __syncthreads();
+        top = 0;
+        if (fresh(u) || (u < 2 && old(u))) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          y[j] = fresh(u) ? x[u].row_pair(2 * w + j) : x[u].code_pair(2 * w + j, was[u]);
-          y[j].x *= inv, y[j].y *= inv;
-          if (special) {  // (the conversion saturates: an infinity would become 448)
-            if (magnitude(y[j].x) == 0x7f800000u) y[j].x = NAN;
-            if (magnitude(y[j].y) == 0x7f800000u) y[j].y = NAN;
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = fresh(u) ? x[u].row_pair(i) : x[u].code_pair(i, was[u]);
+            top = max(top, max(finite(magnitude(f.x)), finite(magnitude(f.y))));
           }
         }
-        q[w] = (uint32_t)cvt_f32x2_e4m3x2(y[0].x, y[0].y) |
-               (uint32_t)cvt_f32x2_e4m3x2(y[1].x, y[1].y) << 16;
+        cta_top(u, top);
+        __syncthreads();
+        top = all_top(u);
       }
-      *reinterpret_cast<uint4*>(code(u)) = make_uint4(q[0], q[1], q[2], q[3]);
+      // adding 0x1fffff carries into the exponent when the fraction is above 1.75's
+      int e = (int)((top + 0x1fffffu) >> 23) - 127 - 8;
+      e = top ? min(max(e, -40), 120) : 0;
+      const float s = __uint_as_float((unsigned)(127 + e) << 23);
+      const float inv = __uint_as_float((unsigned)(127 - e) << 23);
+      if (fresh(u) || (u < 2 && old(u) && s != was[u])) {
+        uint32_t q[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          float2 y[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            y[j] = fresh(u) ? x[u].row_pair(2 * w + j) : x[u].code_pair(2 * w + j, was[u]);
+            y[j].x *= inv, y[j].y *= inv;
+            if (special) {  // (the conversion saturates: an infinity would become 448)
+              if (magnitude(y[j].x) == 0x7f800000u) y[j].x = NAN;
+              if (magnitude(y[j].y) == 0x7f800000u) y[j].y = NAN;
+            }
+          }
+          q[w] = (uint32_t)cvt_f32x2_e4m3x2(y[0].x, y[0].y) |
+                 (uint32_t)cvt_f32x2_e4m3x2(y[1].x, y[1].y) << 16;
+        }
+        *reinterpret_cast<uint4*>(code(u)) = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      if (threadIdx.x == 0) *scale(u) = s;
     }
-    if (threadIdx.x == 0) *scale(u) = s;
+    if (!LOOP) break;
+    __syncthreads();  // (red is free again)
   }
 }
 
@@ -260,15 +269,21 @@ struct Codes<float> {
 };
 
 constexpr int READ_THREADS = 256, READ_UNROLL = 4;
+// CTAs (8 an SM are in flight) from which on LOOP pays: there are a quarter as many then, and fewer
+// find their request shorter than the longest.  16 requests of 1024 .. 8192 slots in 4 layers of 8
+// heads of 128 take 266 us with it and 300 without, one of 4096 in 4 layers of 8 heads of 64 10.5 and
+// 9.7.
+constexpr int READ_MANY = 16 * 8 * 152;
 
-// A CTA reads READ_THREADS x READ_UNROLL pieces of one (layer, request, kv head), keys or
-// values: a piece is 16 bytes of row elements, so every store is a full one and consecutive
-// threads' loads and stores are consecutive.  Bound by memory: 16 requests of 1024 .. 8192 slots in
-// 4 layers of 8 heads of 128 to bf16 take 301 us, 6.0 TB/s (89 % of the measured copy rate).
-template <int HD, typename T>
+// A CTA reads READ_THREADS x READ_UNROLL pieces of one (layer, request, kv head), keys or values, and
+// with LOOP those `stride` rows further on too: a piece is 16 bytes of row elements, so every store is
+// a full one and consecutive threads' loads and stores are consecutive.  Bound by memory: 16 requests
+// of 1024 .. 8192 slots in 4 layers of 8 heads of 128 to bf16 take 264 us, 6.85 TB/s (101 % of the
+// measured copy rate).
+template <int HD, bool LOOP, typename T>
 __global__ void __launch_bounds__(READ_THREADS)
     read_quant_kernel(CacheArgs c, RowsArgs rows, int block_shift, const int* starts,
-                      const int* counts, int n_max) {
+                      const int* counts, int n_max, int stride) {
   pdl_enter();
   typedef typename Codes<T>::type Code;
   constexpr int E = 16 / sizeof(T), PER_ROW = HD / E;
@@ -284,24 +299,26 @@ __global__ void __launch_bounds__(READ_THREADS)
   const float* scale = (value ? c.v_scale : c.k_scale) + unit * (c.capacity >> block_shift);
   T* out = reinterpret_cast<T*>(value ? rows.v : rows.k) + l * rows.layer + b * rows.batch +
            h * rows.head;
-  const int64_t first = (int64_t)(rest >> 1) * (READ_THREADS * READ_UNROLL) + threadIdx.x;
-  const int64_t end = (int64_t)n * PER_ROW;
-  Code got[READ_UNROLL];
-  float s[READ_UNROLL];
+  // (a thread's pieces are ROWS rows apart, in the same column)
+  constexpr int ROWS = READ_THREADS / PER_ROW;
+  const int col = threadIdx.x % PER_ROW;
+  for (int64_t base = (rest >> 1) * (ROWS * READ_UNROLL); base < n; base += stride) {
+    const int row = (int)base + (int)threadIdx.x / PER_ROW;
+    const Code* from = reinterpret_cast<const Code*>(code) + (int64_t)row * PER_ROW + col;
+    Code got[READ_UNROLL];
+    float s[READ_UNROLL];
 #pragma unroll
-  for (int i = 0; i < READ_UNROLL; ++i) {
-    const int64_t p = first + i * READ_THREADS;
-    if (p < end) {
-      got[i] = reinterpret_cast<const Code*>(code)[p];
-      s[i] = scale[(at + (int)(p / PER_ROW)) >> block_shift];
+    for (int i = 0; i < READ_UNROLL; ++i) {
+      if (row + i * ROWS < n) {
+        got[i] = from[i * READ_THREADS];
+        s[i] = scale[(at + row + i * ROWS) >> block_shift];
+      }
     }
-  }
+    T* to = out + row * rows.token + col * E;
 #pragma unroll
-  for (int i = 0; i < READ_UNROLL; ++i) {
-    const int64_t p = first + i * READ_THREADS;
-    if (p < end)
-      *reinterpret_cast<uint4*>(out + (p / PER_ROW) * rows.token + (p % PER_ROW) * E) =
-          decode(got[i], s[i], (const T*)nullptr);
+    for (int i = 0; i < READ_UNROLL; ++i, to += ROWS * rows.token)
+      if (row + i * ROWS < n) *reinterpret_cast<uint4*>(to) = decode(got[i], s[i], (const T*)nullptr);
+    if (!LOOP) break;
   }
 }
 
@@ -330,16 +347,19 @@ static RowsArgs rows_args(const peagle_kv_rows* r) {
 }
 
 template <int HD, int BLOCK>
-static cudaError_t launch_append(int dtype, int units, dim3 grid, cudaStream_t s,
+static cudaError_t launch_append(int dtype, int units, bool loop, dim3 grid, cudaStream_t s,
                                  const CacheArgs& c, const RowsArgs& r, const int* seq_lens,
-                                 const int* n_commit, int n_extra, int n_max) {
-  auto go = [&](void (*kernel)(CacheArgs, RowsArgs, const int*, const int*, int, int)) {
+                                 const int* n_commit, int n_extra, int n_max, int stride) {
+  auto go = [&](void (*kernel)(CacheArgs, RowsArgs, const int*, const int*, int, int, int)) {
     return launch_pdl(kernel, grid, dim3(BLOCK * HD / 16), 0, s, c, r, seq_lens, n_commit, n_extra,
-                      n_max);
+                      n_max, stride);
   };
-  if (dtype == PEAGLE_F32) return go(append_quant_kernel<HD, BLOCK, 2, float>);
-  return go(units == 2 ? append_quant_kernel<HD, BLOCK, 2, bf16>
-                       : append_quant_kernel<HD, BLOCK, 4, bf16>);
+  if (dtype == PEAGLE_F32)
+    return go(loop ? append_quant_kernel<HD, BLOCK, 2, true, float>
+                   : append_quant_kernel<HD, BLOCK, 2, false, float>);
+  if (units == 2) return go(append_quant_kernel<HD, BLOCK, 2, false, bf16>);
+  return go(loop ? append_quant_kernel<HD, BLOCK, 4, true, bf16>
+                 : append_quant_kernel<HD, BLOCK, 4, false, bf16>);
 }
 
 }  // namespace kvq
@@ -360,21 +380,26 @@ extern "C" int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, 
       n_extra > n_max || (advance != 0 && advance != 1))
     return PEAGLE_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
+  const int layers = layer < 0 ? kv->n_layers : 1;
   // the blocks that n_max rows can touch, wherever the first of them starts
   const int64_t blocks = ((int64_t)n_max + kv->block - 2) / kv->block + 1;
   // more than a few blocks a request: four units a CTA (fp32 rows have as many bytes in flight with
   // two)
   const int units = blocks <= 4 || rows->dtype == PEAGLE_F32 ? 2 : 4;
-  const int64_t gx = (blocks + units / 2 - 1) / (units / 2) * kv->n_kv_heads;
+  int64_t ctas = (blocks + units / 2 - 1) / (units / 2);
+  const bool loop = blocks > 4 && ctas * kv->n_kv_heads * batch * layers > APPEND_MANY;
+  if (loop) ctas = (ctas + 3) / 4;
+  const int64_t gx = ctas * kv->n_kv_heads;
+  const int stride = (int)(ctas * (units / 2));
   if (gx > INT32_MAX) return PEAGLE_ERR_INVALID;
-  const dim3 grid((unsigned)gx, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
+  const dim3 grid((unsigned)gx, (unsigned)batch, (unsigned)layers);
   const CacheArgs c = cache_args(kv, layer);
   const RowsArgs r = rows_args(rows);
   cudaError_t e = cudaErrorInvalidValue;
 #define PEAGLE_APPEND(HD, BLOCK)                                                          \
   if (kv->head_dim == HD && kv->block == BLOCK)                                           \
-    e = launch_append<HD, BLOCK>(rows->dtype, units, grid, s, c, r, seq_lens, n_commit,  \
-                                 n_extra, n_max);
+    e = launch_append<HD, BLOCK>(rows->dtype, units, loop, grid, s, c, r, seq_lens, n_commit,  \
+                                 n_extra, n_max, stride);
   PEAGLE_APPEND(64, 16)
   PEAGLE_APPEND(64, 32)
   PEAGLE_APPEND(64, 64)
@@ -399,20 +424,35 @@ extern "C" int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, in
   if (rc != PEAGLE_OK) return rc;
   if (!counts || n_max < 1 || n_max > (1 << 30)) return PEAGLE_ERR_INVALID;
   const bool f32 = out->dtype == PEAGLE_F32;
+  // n_max rows' pieces; counts are on the device
   const int64_t pieces = (int64_t)n_max * kv->head_dim / (f32 ? 4 : 8);
   const int64_t per = READ_THREADS * READ_UNROLL;
-  const int64_t gx = (pieces + per - 1) / per * 2 * kv->n_kv_heads;
+  const int layers = layer < 0 ? kv->n_layers : 1;
+  int64_t ctas = (pieces + per - 1) / per;
+  const bool loop = ctas * 2 * kv->n_kv_heads * batch * layers > READ_MANY;
+  if (loop) ctas = (ctas + 3) / 4;
+  const int64_t gx = ctas * 2 * kv->n_kv_heads;
   if (gx > INT32_MAX) return PEAGLE_ERR_INVALID;
-  const dim3 grid((unsigned)gx, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
+  const dim3 grid((unsigned)gx, (unsigned)batch, (unsigned)layers);
   const CacheArgs c = cache_args(kv, layer);
   const RowsArgs r = rows_args(out);
   const int shift = kv->block == 16 ? 4 : kv->block == 32 ? 5 : kv->block == 64 ? 6 : 7;
-  auto launch = [&](void (*kernel)(CacheArgs, RowsArgs, int, const int*, const int*, int)) {
+  const int stride = (int)(ctas * (per * (f32 ? 4 : 8) / kv->head_dim));  // rows, about n_max
+  auto launch = [&](void (*kernel)(CacheArgs, RowsArgs, int, const int*, const int*, int, int)) {
     return launch_pdl(kernel, grid, dim3(READ_THREADS), 0, (cudaStream_t)stream, c, r, shift,
-                      starts, counts, n_max);
+                      starts, counts, n_max, stride);
   };
-  const cudaError_t e = kv->head_dim == 64
-                            ? launch(f32 ? read_quant_kernel<64, float> : read_quant_kernel<64, bf16>)
-                            : launch(f32 ? read_quant_kernel<128, float> : read_quant_kernel<128, bf16>);
+  cudaError_t e = cudaErrorInvalidValue;
+#define PEAGLE_READ(HD, LOOP, F32, T) \
+  if (kv->head_dim == HD && loop == LOOP && f32 == F32) e = launch(read_quant_kernel<HD, LOOP, T>);
+  PEAGLE_READ(64, false, false, bf16)
+  PEAGLE_READ(64, true, false, bf16)
+  PEAGLE_READ(64, false, true, float)
+  PEAGLE_READ(64, true, true, float)
+  PEAGLE_READ(128, false, false, bf16)
+  PEAGLE_READ(128, true, false, bf16)
+  PEAGLE_READ(128, false, true, float)
+  PEAGLE_READ(128, true, true, float)
+#undef PEAGLE_READ
   return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }

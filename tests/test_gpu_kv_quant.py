@@ -237,6 +237,36 @@ def test_read_matches_codes_times_scales(hd, block, dtype):
                 assert (got[:, b, :, n[b]:] == -7.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_ragged_calls_equal_their_layers(dtype):
+    """Calls so large that a CTA takes several parts of its request's rows, against calls for one
+    layer, which are not."""
+    m = pk()
+    L, B, H, hd, cap, block = 4, 20, 8, 64, 2048, 16
+    c, one = fresh(L, B, H, cap, hd, block), fresh(L, B, H, cap, hd, block)
+    n = [2000, 0, 1, 15, 16, 17, 33, 1999, 64, 500, 31, 1024, 1, 0, 1500, 100, 48, 49, 2000, 700]
+    at = [48, 5, 2047, 0, 16, 3, 31, 0, 1, 17, 0, 1000, 8, 9, 0, 100, 7, 47, 33, 1]
+    rows = [torch.randn(L, B, 2000, H, hd, device="cuda",
+                        generator=torch.Generator("cuda").manual_seed(i)).to(DT[dtype]) for i in (1, 2)]
+    sl, so = ints(at), ints(at)
+    m.peagle_append_kv_quant(c.kv, B, sl, ints(n), *rows, 2000)
+    for layer in range(L):
+        m.peagle_append_kv_quant(one.kv, B, so, ints(n), rows[0][layer], rows[1][layer], 2000,
+                                 layer=layer, advance=layer == L - 1)
+    assert c.err() == 0 and one.err() == 0 and torch.equal(sl, so)
+    for name in c.t:
+        assert torch.equal(c.t[name].view(torch.uint8), one.t[name].view(torch.uint8)), name
+    out = torch.full((2, 2, L, B, 2000, H, hd), -7.0, dtype=DT[dtype], device="cuda")
+    m.peagle_read_kv_quant(c.kv, B, ints(n), out[0, 0], out[0, 1], 2000, starts=ints(at))
+    for layer in range(L):
+        m.peagle_read_kv_quant(c.kv, B, ints(n), out[1, 0, layer], out[1, 1, layer], 2000,
+                               layer=layer, starts=ints(at))
+    assert c.err() == 0 and torch.equal(out[0], out[1])
+    for b in range(B):
+        assert (out[0, :, :, b, n[b]:] == -7.0).all()
+        assert not n[b] or (out[0, :, :, b, :n[b]] != -7.0).any(-1).all()
+
+
 def test_read_counts_out_of_range():
     m = pk()
     c = Cache(1, 3, 2, 64, 64, 16, 61)
