@@ -35,6 +35,9 @@
 // cp.async ring in shared memory that runs on across (request, kv head) boundaries.  At the end
 // of one its streams are joined in shared memory; one that lies whole in a CTA is written out,
 // pieces of one go to the workspace and the second kernel joins them.
+// Calls with short heads take one step instead: every (request, kv head) belongs to a cluster of
+// 1 .. 8 CTAs, which cut its tiles among them and join their results through one another's shared
+// memory (split_of).
 #include "kv_quant_attn.cuh"
 
 namespace peagle {
