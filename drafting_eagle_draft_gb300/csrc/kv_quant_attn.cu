@@ -45,7 +45,6 @@ namespace kvq {
 
 constexpr int TILE = 32;       // slots a unit
 constexpr int ENTRY = 28;      // see find_share; 24 and 32 measured within 2 %, 8 up to 20 % slower
-constexpr int JOIN_WARPS = 4;  // of the second kernel
 constexpr int MAX_SPLIT = 8;   // CTAs of a cluster that share a head
 typedef Segment<TILE> Seg;
 
@@ -765,17 +764,21 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 
 // Joins the pieces of the (request, kv head)s that several CTAs worked on: block (c, z) takes the
 // one whose first piece CTA c holds, and of its ntiles x HD / 16 columns of 32 fragments the z-th
-// part; the block's warps split a column's pieces.  Bound by the latency of the pieces' loads
-// (they are in L2), so a warp has up to 8 of them in flight and goes over them once.  Also writes
-// the rows of requests no row of which sees a slot.  ROWS: outputs lie row by row, a lane's
+// 4 / JOIN_WARPS; JOIN_WARPS warps split a column's pieces.  Bound by the latency of the pieces' loads
+// (they are in L2), so a warp has up to 8 of them in flight and goes over them once, and by the start
+// of the blocks that find nothing to join: four warps a block, whatever the split.  With 8 heads and
+// more (about 19 pieces a head at most) one warp a column takes less time, 20 query rows of 16 requests
+// 51.3 us with the first kernel for 54.9; one head of 16416 slots 10.2 with four for 16.9.  Also
+// writes the rows of requests no row of which sees a slot.  ROWS: outputs lie row by row, a lane's
 // float4 is four head dims of one row; else as fragments (struct Running).
-template <int HD, typename T, bool ROWS>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQuantArgs a,
-                                                                          int ntiles) {
+template <int HD, typename T, bool ROWS, int JOIN_WARPS>
+__global__ void __launch_bounds__(128) attn_quant_join_kernel(AttnQuantArgs a, int ntiles) {
   pdl_enter();
-  __shared__ float4 red_o[JOIN_WARPS][32];
-  __shared__ float4 red_ml[JOIN_WARPS][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int JOIN_COLS = 4 / JOIN_WARPS;
+  __shared__ float4 red_o[JOIN_COLS][JOIN_WARPS][32];
+  __shared__ float4 red_ml[JOIN_COLS][JOIN_WARPS][32];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % JOIN_WARPS;
+  const int sub = threadIdx.x / (32 * JOIN_WARPS);
   const int4 d = a.desc[blockIdx.x];
   if (blockIdx.y == 0) {
     for (int b = blockIdx.x; b < a.batch; b += CTAS) {
@@ -786,95 +789,92 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_quant_join_kernel(AttnQu
     }
   }
   if (d.x < 0) return;
-  const int cols = ntiles * (HD / 16);
-  const int col0 = cols * blockIdx.y / gridDim.y, col1 = cols * (blockIdx.y + 1) / gridDim.y;
+  const int col = blockIdx.y * JOIN_COLS + sub;  // (HD / 16 is a multiple of 4)
   const int pieces = d.z - (int)blockIdx.x + 1;
   const size_t slot = (size_t)ntiles * 8 * (HD + 2);
   // (piece p > 0 is the head of CTA c + p's share: slot 0; the first is the tail of c's: slot 1)
   const float* base = a.work + (size_t)blockIdx.x * 2 * slot;
   const int r = lane >> 2, c = lane & 3;
-  for (int col = col0; col < col1; ++col) {
-    const int nt = col / (HD / 16), i = col % (HD / 16);
-    const int row = ROWS ? (col * 32 + lane) / (HD / 4) : nt * 8 + 2 * c;
-    float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int BATCH = 8;
-    for (int p0 = warp; p0 < pieces; p0 += BATCH * JOIN_WARPS) {
-      float4 f[BATCH], g[BATCH];
+  const int nt = col / (HD / 16), i = col % (HD / 16);
+  const int row = ROWS ? (col * 32 + lane) / (HD / 4) : nt * 8 + 2 * c;
+  float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int BATCH = 8;
+  for (int p0 = warp; p0 < pieces; p0 += BATCH * JOIN_WARPS) {
+    float4 f[BATCH], g[BATCH];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int p = p0 + k * JOIN_WARPS;
-        const float* s = base + ((size_t)2 * p + (p == 0 ? 1 : 0)) * slot;
-        f[k] = make_float4(NO_REF, 0.f, NO_REF, 0.f);
-        g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p < pieces) {
-          if (ROWS) {
-            const float2 x = *reinterpret_cast<const float2*>(s + 2 * row);
-            f[k] = make_float4(x.x, x.y, x.x, x.y);
-          } else {
-            f[k] = *reinterpret_cast<const float4*>(s + 2 * row);
-          }
-          g[k] = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
+    for (int k = 0; k < BATCH; ++k) {
+      const int p = p0 + k * JOIN_WARPS;
+      const float* s = base + ((size_t)2 * p + (p == 0 ? 1 : 0)) * slot;
+      f[k] = make_float4(NO_REF, 0.f, NO_REF, 0.f);
+      g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < pieces) {
+        if (ROWS) {
+          const float2 x = *reinterpret_cast<const float2*>(s + 2 * row);
+          f[k] = make_float4(x.x, x.y, x.x, x.y);
+        } else {
+          f[k] = *reinterpret_cast<const float4*>(s + 2 * row);
         }
-      }
-      float n0 = m0, n1 = m1;
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) n0 = fmaxf(n0, f[k].x), n1 = fmaxf(n1, f[k].z);
-      float x0 = ex2(m0 - n0), x1 = ex2(m1 - n1);
-      l0 *= x0, l1 *= x1;
-      o = make_float4(o.x * x0, o.y * x1, o.z * x0, o.w * x1);
-      m0 = n0, m1 = n1;
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        x0 = ex2(f[k].x - m0), x1 = ex2(f[k].z - m1);
-        l0 = fmaf(f[k].y, x0, l0), l1 = fmaf(f[k].w, x1, l1);
-        o.x = fmaf(g[k].x, x0, o.x), o.y = fmaf(g[k].y, x1, o.y);
-        o.z = fmaf(g[k].z, x0, o.z), o.w = fmaf(g[k].w, x1, o.w);
+        g[k] = reinterpret_cast<const float4*>(s + (size_t)ntiles * 16)[col * 32 + lane];
       }
     }
-    red_o[warp][lane] = o;
-    red_ml[warp][lane] = make_float4(m0, l0, m1, l1);
+    float n0 = m0, n1 = m1;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) n0 = fmaxf(n0, f[k].x), n1 = fmaxf(n1, f[k].z);
+    float x0 = ex2(m0 - n0), x1 = ex2(m1 - n1);
+    l0 *= x0, l1 *= x1;
+    o = make_float4(o.x * x0, o.y * x1, o.z * x0, o.w * x1);
+    m0 = n0, m1 = n1;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      x0 = ex2(f[k].x - m0), x1 = ex2(f[k].z - m1);
+      l0 = fmaf(f[k].y, x0, l0), l1 = fmaf(f[k].w, x1, l1);
+      o.x = fmaf(g[k].x, x0, o.x), o.y = fmaf(g[k].y, x1, o.y);
+      o.z = fmaf(g[k].z, x0, o.z), o.w = fmaf(g[k].w, x1, o.w);
+    }
+  }
+  if (JOIN_WARPS > 1) {
+    red_o[sub][warp][lane] = o;
+    red_ml[sub][warp][lane] = make_float4(m0, l0, m1, l1);
     __syncthreads();
-    if (warp == (col - col0) % JOIN_WARPS) {
-      l0 = l1 = 0.f;
-      m0 = m1 = NO_REF;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp) return;
+    l0 = l1 = 0.f;
+    m0 = m1 = NO_REF;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < JOIN_WARPS; ++w)
-        m0 = fmaxf(m0, red_ml[w][lane].x), m1 = fmaxf(m1, red_ml[w][lane].z);
+    for (int w = 0; w < JOIN_WARPS; ++w)
+      m0 = fmaxf(m0, red_ml[sub][w][lane].x), m1 = fmaxf(m1, red_ml[sub][w][lane].z);
 #pragma unroll
-      for (int w = 0; w < JOIN_WARPS; ++w) {
-        const float4 f = red_ml[w][lane], g = red_o[w][lane];
-        const float x0 = ex2(f.x - m0), x1 = ex2(f.z - m1);
-        l0 = fmaf(f.y, x0, l0), l1 = fmaf(f.w, x1, l1);
-        o.x = fmaf(g.x, x0, o.x), o.y = fmaf(g.y, x1, o.y);
-        o.z = fmaf(g.z, x0, o.z), o.w = fmaf(g.w, x1, o.w);
-      }
-      float inv;
-      const int nq = a.nkv * a.G;
-      if (ROWS) {
-        const int parts = a.heads / a.nkv, part = d.y % parts, of = part * a.part_rows + row;
-        if (row < a.part_rows && of < a.K * a.G) {
-          const int at = (col * 32 + lane) % (HD / 4) * 4, j = of / a.G;
-          T* out = finish_row<T>(a, HD, d.x, j * nq + d.y / parts * a.G + of - j * a.G, m0, l0,
-                                 at == 0, inv);
-          store2(out + at, o.x * inv, o.y * inv);
-          store2(out + at + 2, o.z * inv, o.w * inv);
-        }
-      }
-      const int j0 = row / a.G, j1 = (row + 1) / a.G;
-      if (!ROWS && row < a.K * a.G) {
-        T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
-                               i == 0 && r == 0, inv);
-        store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
-      }
-      if (!ROWS && row + 1 < a.K * a.G) {
-        T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
-                               i == 0 && r == 0, inv);
-        store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
-      }
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+      const float4 f = red_ml[sub][w][lane], g = red_o[sub][w][lane];
+      const float x0 = ex2(f.x - m0), x1 = ex2(f.z - m1);
+      l0 = fmaf(f.y, x0, l0), l1 = fmaf(f.w, x1, l1);
+      o.x = fmaf(g.x, x0, o.x), o.y = fmaf(g.y, x1, o.y);
+      o.z = fmaf(g.z, x0, o.z), o.w = fmaf(g.w, x1, o.w);
     }
-    if (col + 1 < col1) __syncthreads();
+  }
+  float inv;
+  const int nq = a.nkv * a.G;
+  if (ROWS) {
+    const int parts = a.heads / a.nkv, part = d.y % parts, of = part * a.part_rows + row;
+    if (row < a.part_rows && of < a.K * a.G) {
+      const int at = (col * 32 + lane) % (HD / 4) * 4, j = of / a.G;
+      T* out = finish_row<T>(a, HD, d.x, j * nq + d.y / parts * a.G + of - j * a.G, m0, l0,
+                             at == 0, inv);
+      store2(out + at, o.x * inv, o.y * inv);
+      store2(out + at + 2, o.z * inv, o.w * inv);
+    }
+  }
+  const int j0 = row / a.G, j1 = (row + 1) / a.G;
+  if (!ROWS && row < a.K * a.G) {
+    T* out = finish_row<T>(a, HD, d.x, j0 * nq + d.y * a.G + row - j0 * a.G, m0, l0,
+                           i == 0 && r == 0, inv);
+    store2(out + r * (HD / 8) + 2 * i, o.x * inv, o.z * inv);
+  }
+  if (!ROWS && row + 1 < a.K * a.G) {
+    T* out = finish_row<T>(a, HD, d.x, j1 * nq + d.y * a.G + row + 1 - j1 * a.G, m1, l1,
+                           i == 0 && r == 0, inv);
+    store2(out + r * (HD / 8) + 2 * i, o.y * inv, o.w * inv);
   }
 }
 
@@ -970,19 +970,17 @@ static cudaError_t launch_attention(AttnQuantArgs a, const Plan& p, cudaStream_t
 
 cudaError_t launch_join(int hd, bool f32, bool rowmajor, const AttnQuantArgs& a, int ntiles,
                         cudaStream_t s) {
-  // blocks of two columns each
+  const bool many = (int64_t)a.batch * a.heads >= 8;
   auto go = [&](void (*kernel)(AttnQuantArgs, int)) {
-    return launch_pdl(kernel, dim3(CTAS, cdiv(ntiles * (hd / 16), 2)), dim3(JOIN_WARPS * 32), 0, s,
-                      a, ntiles);
+    return launch_pdl(kernel, dim3(CTAS, ntiles * (hd / 16) / (many ? 4 : 1)), dim3(128), 0, s, a,
+                      ntiles);
   };
-  if (rowmajor)
-    return go(hd == 64 ? attn_quant_join_kernel<64, bf16, true>
-                       : attn_quant_join_kernel<128, bf16, true>);
-  if (f32)
-    return go(hd == 64 ? attn_quant_join_kernel<64, float, false>
-                       : attn_quant_join_kernel<128, float, false>);
-  return go(hd == 64 ? attn_quant_join_kernel<64, bf16, false>
-                     : attn_quant_join_kernel<128, bf16, false>);
+#define PEAGLE_JOIN(HD, T, ROWS) \
+  go(many ? attn_quant_join_kernel<HD, T, ROWS, 1> : attn_quant_join_kernel<HD, T, ROWS, 4>)
+  if (rowmajor) return hd == 64 ? PEAGLE_JOIN(64, bf16, true) : PEAGLE_JOIN(128, bf16, true);
+  if (f32) return hd == 64 ? PEAGLE_JOIN(64, float, false) : PEAGLE_JOIN(128, float, false);
+  return hd == 64 ? PEAGLE_JOIN(64, bf16, false) : PEAGLE_JOIN(128, bf16, false);
+#undef PEAGLE_JOIN
 }
 
 }  // namespace kvq
