@@ -722,7 +722,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
       // the cluster's warps share the columns of the pieces, which they read in one another's memory
       __syncwarp();
       tc::cluster_sync();
-      for (int col = (int)tc::cluster_ctarank() * W + warp; col < groups * NT * (HD / 16); col += a.split * W) {
+      const int cols = groups * NT * (HD / 16);
+      for (int col = (int)tc::cluster_ctarank() * W + warp; col < cols; col += a.split * W) {
         const int i = col % (HD / 16), row = col / (HD / 16) * 8 + 2 * c;
         float4 f[MAX_SPLIT], g[MAX_SPLIT];
         float m0 = NO_REF, m1 = NO_REF, l0 = 0.f, l1 = 0.f;
@@ -907,17 +908,18 @@ static int clusters_of(int split) { return split == 1 ? CTAS : split == 2 ? 76 :
 
 // The CTAs that share a head when the call is done in one step, or 0 when two steps take less time
 // (equal shares of the call's tiles, and the kernel that joins their pieces).  As many CTAs as find
-// room, unless one does the head in a round of its warps.  Two steps spread long heads better, one
-// saves a launch, the way through the workspace and shares that lie over two heads; a round's cost
-// follows from its products.  us in one step / in two, at full capacity (shorter and ragged requests
-// favour the one step more: 16 heads of 20 fp32 rows over 61 and 1051 slots 13 / 19):
-//   slots a head:                              288        544        1056       2080       4128
-//   4 rows of head_dim 128, 8 heads         7.2 / 12.2  7.2 / 12.2  7.4 / 12.3  8.5 / 9.6  10.0 / 10.3
-//   20 rows of head_dim 128, 8 heads       10.6 / 18.2 10.8 / 18.3 11.5 / 18.7 13.6 / 13.4 15.9 / 14.8
-//   20 rows in fp32, 32 heads              11.3 / 19.6 12.8 / 15.9 14.9 / 20.4 20.4 / 23.7 29.3 / 32.9
-//   8 rows of head_dim 64, 16 heads         5.9 / 11.0  6.4 / 11.2  6.7 / 9.0   7.7 / 9.5   9.0 / 11.5
-//   64 rows of head_dim 64, 8 heads         9.0 / 15.9  9.2 / 16.1 10.3 / 16.1 11.6 / 12.5 14.2 / 13.8
-//   64 rows of head_dim 64, 72 heads       10.5 / 15.4 11.8 / 17.9 14.6 / 21.3 20.5 / 29.2 30.8 / 34.8
+// room, unless one does the head in a round of its warps.  Two steps spread long and ragged heads
+// better, one saves a launch, the way through the workspace and shares that lie over two heads; a
+// round's cost follows from its products.  us in one step / in two, requests at full capacity and, in
+// brackets, spread from none of it to all:
+//   slots a head:           544                       1056                      2080
+//   4 rows of 128, 8 heads  7.2 / 11.0                7.6 / 11.6                8.6 / 9.4
+//   20 rows of 128, 16      11.5 / 17.1 (10.7 / 17.1) 13.7 / 12.2 (11.6 / 17.0) 15.8 / 13.3 (13.4 / 12.2)
+//   20 fp32 rows of 128, 32 13.0 / 13.7 (11.3 / 17.4) 15.1 / 17.5 (13.3 / 13.7) 19.9 / 21.3 (17.1 / 15.8)
+//   8 rows of 64, 32        6.6 / 8.2 (6.5 / 10.3)    7.1 / 10.6 (6.9 / 8.2)    8.1 / 10.6 (7.9 / 10.6)
+//   64 rows of 64, 8        9.3 / 13.7                10.6 / 14.4               11.8 / 11.6
+//   64 rows of 64, 72       12.0 / 14.2 (11.0 / 14.4) 14.4 / 17.1 (13.3 / 14.8) 20.6 / 25.3 (18.1 / 17.1)
+//   (4128 slots: 9.9 / 10.3 for the first, 14.4 / 12.9 for 64 rows of 64, 8 heads)
 static int split_of(int hd, bool f32, const Plan& p, int warps, int64_t heads, int64_t slots) {
   const int64_t tiles = (slots / TILE + 2) * p.groups;
   int split = tiles <= warps ? 1 : MAX_SPLIT;
@@ -927,7 +929,7 @@ static int split_of(int hd, bool f32, const Plan& p, int warps, int64_t heads, i
   const double one = (double)tiles / (warps * split);                         // rounds a head
   const double rounds = (double)per * (one + 2) - 2;
   const double shares = (double)heads * (double)tiles / (CTAS * warps);
-  const double saved = .3 * p.ntiles() > 2.6 ? .3 * p.ntiles() : 2.6;
+  const double saved = .3 * p.ntiles() > 1.8 ? .3 * p.ntiles() : 1.8;
   return (rounds - shares) * round <= saved ? split : 0;
 }
 
@@ -1064,8 +1066,9 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
     return launch_attention_tc(hd, K * a.G, a, (cudaStream_t)stream) == cudaSuccess ? PEAGLE_OK
                                                                                     : PEAGLE_ERR_CUDA;
   a.split = split_of(hd, f32, p, warps, heads, most);
-#define PEAGLE_ATTN(HD, NT, F32) \
-  if (hd == HD && p.nt == NT && f32 == F32) e = launch_attention<HD, NT, F32, warps_of(HD, NT, F32)>(a, p, (cudaStream_t)stream);
+#define PEAGLE_ATTN(HD, NT, F32)                                                           \
+  if (hd == HD && p.nt == NT && f32 == F32)                                                \
+    e = launch_attention<HD, NT, F32, warps_of(HD, NT, F32)>(a, p, (cudaStream_t)stream);
   PEAGLE_ATTN(64, 1, false)
   PEAGLE_ATTN(64, 2, false)
   PEAGLE_ATTN(64, 3, false)
