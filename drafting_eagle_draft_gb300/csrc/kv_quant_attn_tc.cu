@@ -26,8 +26,8 @@
 // What bounds it: the softmax warps' chain of a tile, about 2,600 cycles at 64 rows and head_dim 64
 // (the tile's bytes would take 700 at the copy rate, the two products 550), spread over loads from
 // tensor memory, 130 arithmetic instructions, the vote, exponentials, and stores with their proxy
-// fence; the tensor pipe is 12 % busy.  Two requests of 65536 slots at head_dim 128, 64 rows: 104 us,
-// 2.5 TB/s (37 % of the measured copy rate); the warps' kernel takes 151.  Tried and slower: groups
+// fence; the tensor pipe is 12 % busy.  Two requests of 65536 slots at head_dim 128, 64 rows: 93 us,
+// 2.9 TB/s (43 % of the measured copy rate); the warps' kernel takes 158.  Tried and slower: groups
 // of 128 threads that each convert, multiply and weigh their own tiles (195 us for what takes 146),
 // the weights computed while the votes come in (123 for 108: the code leaves the instruction cache).
 #include "kv_quant_attn.cuh"
@@ -667,15 +667,16 @@ cudaError_t launch(const AttnQuantArgs& a, cudaStream_t s) {
 
 // Where this kernel takes less time than the warps' one (us, this one against that one; slots = the
 // slots of all requests and kv heads):
-//   head_dim 128, 64 rows:  1048576 slots 105 / 149, 262144 41 / 49, 131072 35 / 32, 65536 26 / 25
-//   head_dim 128, 40 rows:  1048576 slots 102 / 122, 262144 39 / 46, 131072 35 / 30
-//   head_dim 64, 64 rows:   1048576 slots 81 / 88, 524288 50 / 54, 262144 34 / 34, 32768 20 / 16
-//   head_dim 64, 40 rows:   1048576 slots 80 / 72
-//   head_dim 64, 64 rows, 64 requests of 300 .. 4100 slots: 106 / 127
+//   head_dim 128, 64 rows:  1048576 slots 93 / 158, 262144 37 / 53, 131072 27 / 33, 65536 21.5 / 23.6
+//   head_dim 128, 40 rows:  1048576 slots 92 / 141, 262144 36 / 48, 131072 26 / 29, 65536 20.6 / 21.6
+//   head_dim 64, 64 rows:   1048576 slots 76 / 83, 524288 45 / 48, 262144 29.4 / 29.7, 131072 22 / 21
+//   head_dim 64, 40 rows:   1048576 slots 76 / 72
+//   head_dim 64, 64 rows, 64 requests of 300 .. 4100 slots: 93 / 108
 // Its chain of a tile is longer (conversion, product, softmax, product), so it wants several tiles a
 // CTA; and below 33 rows half of its softmax threads would have none.
 bool attn_quant_tc_takes(int hd, bool f32, int rows, int64_t slots) {
-  return !f32 && rows > (hd == 64 ? 48 : 32) && slots * cdiv(rows, RP) >= 3 << 16;
+  return !f32 && rows > (hd == 64 ? 48 : 32) &&
+         slots * cdiv(rows, RP) >= (hd == 64 ? 3 : 1) << 16;
 }
 
 // (more than 32 rows, whatever the slots; parts are equal up to one row)
