@@ -733,7 +733,8 @@ def test_parked_request_resumes_the_draft_pass():
     assert np.array_equal(toks[ok], ref.tokens[ok])
 
 
-@pytest.mark.parametrize("nq,cap,window", [(8, 160, 70), (16, 49152, 0)])
+# one launch, clusters of 8 CTAs, two launches, the tcgen05 kernel
+@pytest.mark.parametrize("nq,cap,window", [(8, 160, 70), (8, 2048, 0), (8, 12288, 0), (16, 49152, 0)])
 def test_captured_round_replays_on_new_inputs(nq, cap, window):
     """append + attention + commit in one CUDA graph, replayed while lengths advance, beside an
     eager call with its own workspace on another stream."""
