@@ -269,13 +269,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 // dim r HD / 8 + 2 i (elements 0, 1) and the next one (2, 3), rows 2c (0, 2) and 2c + 1 (1, 3).
 template <int HD, int NT, bool F32>
 struct Running {
-  // 2^SHIFT is where the largest weight is put, 2^LIM what it may grow to before the reference
-  // moves (f16 ends at 2^16).  Room to grow saves moves: a tile of heavy-tailed scores (tokens of
-  // lognormal size) moved some row's reference in 14 of a stream's first 32 tiles with 2^8 of it,
-  // in 5 with 2^19; normal scores hardly ever after the first tile.  The price is at the other
-  // end, where weights below 2^-14 lose bits of their 11; the second part of an fp32 weight needs
-  // that range, so there the largest is put high.
-  static constexpr float SHIFT = F32 ? 13.f : -4.f, LIM = 15.f;
+  static constexpr float SHIFT = F32 ? SHIFT_F32 : SHIFT_BF16;
   float o[HD / 16][NT][4];
   float m[NT][2], l[NT][2];
   unsigned started;  // bit 2 nt + e: the row has seen a slot (its m counts)

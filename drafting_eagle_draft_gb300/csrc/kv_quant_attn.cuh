@@ -18,6 +18,18 @@ constexpr int MAX_ROWS = 128;  // query rows a kv head
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no slot
 
+// A reference puts the largest weight at 2^SHIFT, and it may grow to 2^LIM before the reference moves
+// (f16 ends at 2^16).  Below 2^-14 weights lose bits of their 11 and below 2^-25 all of them, while
+// the sum of weights keeps them: n slots lose at most n 2^-(25 + SHIFT) of the largest weight, 2^-14
+// for bf16 queries over 131072 slots, and all of it where one slot outweighs a long flat tail.  A
+// SHIFT of -4 (room for growth of 2^19) took 1 .. 8 % less time, but one slot 15 nats above
+// 32768 others of 256 times its value came out 72 % too small.  The price of 2^9 of room is that
+// references move more often: 64 requests of 300 .. 4100 slots with 64 query rows (tcgen05) 108.9 us
+// in a graph for 100.9, 16 of 1024 .. 8192 with 20 rows 53.2 for 51.2, long contexts the same.  (2^10:
+// 114.1 and 55.3; 2^13: 118.2 and 57.6.)  The second part of an fp32 weight needs the range below its
+// first, so there the largest is put at 2^13.
+constexpr float SHIFT_BF16 = 6.f, SHIFT_F32 = 13.f, LIM = 15.f;
+
 struct AttnQuantArgs {
   const uint8_t* k;        // this layer's codes [batch slots][nkv][capacity][hd]
   const uint8_t* v;

@@ -41,7 +41,7 @@ constexpr int TT = 128;        // slots a tile
 constexpr int TC_ENTRY = 3;    // what a head costs besides its tiles, in tiles
 constexpr int NC = 32;         // query rows a softmax thread
 constexpr int TMEM_COLS = 256; // O in columns 0 .. 127, the scores' buffers at 128 and 192
-constexpr float SHIFT = -4.f, LIM = 15.f;  // see struct Running in kv_quant_attn.cu
+constexpr float SHIFT = SHIFT_BF16;
 typedef Segment<TT> TSeg;
 
 // A CTA's warps, in this order: softmax, converters, copies, products.  14 of them leave 128 registers

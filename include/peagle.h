@@ -517,10 +517,10 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  * not see never reach it, NaN included; a row of q that is not finite gives NaN.  fp32
  * accumulation, softmax and lse.  bf16 queries enter exactly (down to 2^-31 of the largest
  * element of their kv head's rows) and softmax weights rounded to 11 bits, fp32 queries and
- * their weights as two such parts (22 bits); weights x value scale below 2^-10 of the row's
- * largest lose bits, down to 2^-21 of it (fp32 queries: 2^-38), and below 2^-120 of it the
- * weight leaves the sum of weights too: the value scales that matter to a row lie within 2^100
- * of one another.
+ * their weights as two such parts (22 bits); weights x value scale below 2^-20 of the row's
+ * largest lose bits, down to 2^-31 of it (fp32 queries: 2^-38), which over n slots adds up to at
+ * most n 2^-31 of that largest (fp32: n 2^-38); below 2^-120 of it the weight leaves the sum of
+ * weights too: the value scales that matter to a row lie within 2^100 of one another.
  * Results are the same on every call with the same lengths and sizes (no atomics).
  * A request with seq_lens[b] < 0, or whose last row's slot is beyond the capacity, is
  * skipped with KV_OVERFLOW; its rows are left as they are.  Waits inside the kernel are
