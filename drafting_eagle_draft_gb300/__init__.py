@@ -39,7 +39,8 @@ EXPORTS = ("peagle_create", "peagle_draft", "peagle_catch_up", "peagle_verify_gr
            "peagle_set_timing", "peagle_read_timing", "peagle_read_pass_trace",
            "peagle_set_wait_limit", "peagle_set_pass_kernel",
            "peagle_decode_attention_static",
-           "peagle_append_kv_quant", "peagle_read_kv_quant",
+           "peagle_append_kv_quant", "peagle_read_kv_quant", "peagle_save_kv_quant",
+           "peagle_restore_kv_quant", "peagle_save_kv_quant_bytes",
            "peagle_decode_attention_quant", "peagle_decode_attention_quant_workspace",
            "peagle_device_error_bits", "peagle_strerror", "peagle_destroy")
 STAGES = ("fc", "qkv", "attn", "oproj", "gate_up", "down", "lm_head", "norm", "small")
@@ -135,6 +136,10 @@ def lib():
                                              _i32, ctypes.POINTER(PeagleKVRows), _i32, _i32, _vp]
         L.peagle_read_kv_quant.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32, _i32, _vp, _vp,
                                            ctypes.POINTER(PeagleKVRows), _i32, _vp]
+        for f in (L.peagle_save_kv_quant, L.peagle_restore_kv_quant):
+            f.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32, _i32, _vp, _vp, _i64, _vp]
+        L.peagle_save_kv_quant_bytes.argtypes = [ctypes.POINTER(PeagleKVQuant)]
+        L.peagle_save_kv_quant_bytes.restype = _i64
         L.peagle_decode_attention_quant.argtypes = [
             ctypes.POINTER(PeagleKVQuant), _i32, _i32, _i32, _i32, _vp, _i32, _i64, _vp, _i32,
             _i32, ctypes.c_float, _vp, _vp, _vp, _i64, _vp]
@@ -530,6 +535,39 @@ def peagle_read_kv_quant(kv: PeagleKVQuant, batch, counts, out_k, out_v, n_max, 
                                     _lens(counts, batch, dev, what), rows, n_max, s)
     if rc:
         raise PeagleError(rc, what)
+
+
+def peagle_save_kv_quant_bytes(kv: PeagleKVQuant) -> int:
+    """Bytes of the buffer of peagle_save_kv_quant (include/peagle.h)."""
+    n = lib().peagle_save_kv_quant_bytes(kv)
+    if n < 0:
+        raise PeagleError(n, "peagle_save_kv_quant_bytes")
+    return n
+
+
+def _open_block(call, what, kv, batch, seq_lens, saved, layer, stream):
+    s = _quant_stream(kv, what, stream)
+    dev = kv._device
+    if not saved.is_contiguous() or saved.device != dev:
+        _refuse(what, f"a contiguous buffer on {dev} is wanted")
+    rc = call(kv, layer, batch, _lens(seq_lens, batch, dev, what), saved.data_ptr(),
+              saved.numel() * saved.element_size(), s)
+    if rc:
+        raise PeagleError(rc, what)
+
+
+def peagle_save_kv_quant(kv: PeagleKVQuant, batch, seq_lens, saved, layer=-1, stream=None):
+    """Keep the committed slots of each request's open block before rows are appended that may be
+    dropped again (include/peagle.h).  saved: a contiguous tensor of
+    peagle_save_kv_quant_bytes()."""
+    _open_block(lib().peagle_save_kv_quant, "peagle_save_kv_quant", kv, batch, seq_lens, saved,
+                layer, stream)
+
+
+def peagle_restore_kv_quant(kv: PeagleKVQuant, batch, seq_lens, saved, layer=-1, stream=None):
+    """Put back what peagle_save_kv_quant kept, at the same lengths (include/peagle.h)."""
+    _open_block(lib().peagle_restore_kv_quant, "peagle_restore_kv_quant", kv, batch, seq_lens,
+                saved, layer, stream)
 
 
 def peagle_decode_attention_quant_workspace(kv: PeagleKVQuant, batch, K, n_q_heads) -> int:

@@ -1,4 +1,5 @@
-// Writing and reading the 8-bit KV cache: peagle_append_kv_quant and peagle_read_kv_quant.
+// Writing and reading the 8-bit KV cache: peagle_append_kv_quant, peagle_read_kv_quant, and the
+// open block set aside and put back (peagle_save_kv_quant, peagle_restore_kv_quant).
 //
 // The cache commit is part of every speculative round ("P-EAGLE: A Technical Deep Dive into
 // Parallel Speculative Decoding", section "Technical Architecture"); the 8-bit form with a
@@ -239,6 +240,43 @@ __global__ void __launch_bounds__(256)
   if (rows_fit(at, n, n_max, capacity, nullptr, false)) seq_lens[b] = at + (int)n;
 }
 
+// The committed slots of each request's open block to `saved` or back, with the block's scale: codes
+// [k, v][layers][batch slots][heads][block][head_dim], then scales [k, v][layers][batch slots][heads].
+// A CTA takes one (layer, request, head)'s keys or values: 16 KB at most, so the call is bound by its
+// launch.
+template <bool RESTORE>
+__global__ void __launch_bounds__(128)
+    open_block_kernel(CacheArgs c, int layers, int block, int hd, const int* seq_lens, char* saved) {
+  pdl_enter();
+  const int h = blockIdx.x % c.heads, b = blockIdx.y, l = c.layer0 + blockIdx.z;
+  const bool value = blockIdx.x / c.heads;
+  const int at = seq_lens[b];
+  if (at < 0 || at > c.capacity) {
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+      raise_error(c.errors, PEAGLE_DEV_KV_OVERFLOW);
+    return;
+  }
+  const int n = at % block;
+  if (n == 0) return;
+  const int64_t unit = ((int64_t)l * c.batch + b) * c.heads + h;
+  const int64_t units = (int64_t)layers * c.batch * c.heads, kept = (value ? units : 0) + unit;
+  uint4* code = reinterpret_cast<uint4*>((value ? c.v : c.k) + (unit * c.capacity + at - n) * hd);
+  uint4* code_kept = reinterpret_cast<uint4*>(saved + kept * block * hd);
+  float* scale = (value ? c.v_scale : c.k_scale) + unit * (c.capacity / block) + at / block;
+  float* scale_kept = reinterpret_cast<float*>(saved + 2 * units * block * hd) + kept;
+  for (int i = threadIdx.x; i < n * hd / 16; i += 128)
+    if (RESTORE)
+      code[i] = code_kept[i];
+    else
+      code_kept[i] = code[i];
+  if (threadIdx.x == 0) {
+    if (RESTORE)
+      *scale = *scale_kept;
+    else
+      *scale_kept = *scale;
+  }
+}
+
 // 16 bytes of row elements from 16 / sizeof(T) codes (packed, low byte first).
 __device__ __forceinline__ uint4 decode(const uint2 c, float s, const bf16*) {
   uint32_t r[4];
@@ -413,6 +451,44 @@ extern "C" int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, 
     e = launch_pdl(advance_kernel, dim3((unsigned)cdiv(batch, 256)), dim3(256), 0, s, batch,
                    seq_lens, n_commit, n_extra, n_max, kv->capacity);
   return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+extern "C" int64_t peagle_save_kv_quant_bytes(const peagle_kv_quant* kv) {
+  const int rc = check_cache(kv, -1, 1);
+  if (rc != PEAGLE_OK) return rc;
+  const int64_t units = (int64_t)kv->n_layers * kv->batch * kv->n_kv_heads;
+  // (a cache of this many units fits no GPU, and the bytes no 63 bits)
+  if (units > (int64_t)1 << 40) return PEAGLE_ERR_UNSUPPORTED;
+  return 2 * units * ((int64_t)kv->block * kv->head_dim + (int64_t)sizeof(float));
+}
+
+template <bool RESTORE>
+static int open_block(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                      const int32_t* seq_lens, const void* saved, int64_t saved_bytes,
+                      void* stream) {
+  const int rc = check_cache(kv, layer, batch);
+  if (rc != PEAGLE_OK) return rc;
+  if (!seq_lens || !saved || !aligned(saved, 16)) return PEAGLE_ERR_INVALID;
+  const int64_t need = peagle_save_kv_quant_bytes(kv);
+  if (need < 0) return (int)need;
+  if (saved_bytes < need) return PEAGLE_ERR_CAPACITY;
+  const dim3 grid(2u * kv->n_kv_heads, (unsigned)batch, layer < 0 ? (unsigned)kv->n_layers : 1u);
+  const cudaError_t e =
+      launch_pdl(open_block_kernel<RESTORE>, grid, dim3(128), 0, (cudaStream_t)stream,
+                 cache_args(kv, layer), kv->n_layers, kv->block, kv->head_dim, seq_lens, (char*)saved);
+  return e == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+extern "C" int peagle_save_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                                    const int32_t* seq_lens, void* saved, int64_t saved_bytes,
+                                    void* stream) {
+  return open_block<false>(kv, layer, batch, seq_lens, saved, saved_bytes, stream);
+}
+
+extern "C" int peagle_restore_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                                       const int32_t* seq_lens, const void* saved,
+                                       int64_t saved_bytes, void* stream) {
+  return open_block<true>(kv, layer, batch, seq_lens, saved, saved_bytes, stream);
 }
 
 extern "C" int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,

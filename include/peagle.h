@@ -476,12 +476,36 @@ typedef struct peagle_kv_rows {
  *   advance  1: then set seq_lens[b] to seq_lens[b] + n (in place; n_commit is another
  *            buffer); 0: leave it, for rows that may be dropped again (a draft block) or
  *            for layers appended one by one
+ * Rows that are dropped again leave a trace: where they raised the scale of the block that
+ * seq_lens[b] points into, the committed slots before them were rounded to it, and the next
+ * append's smaller scale does not bring that back.  peagle_save_kv_quant before such an append
+ * and peagle_restore_kv_quant after it do.
  * A request with rows out of range (n outside 0 .. n_max: BAD_COMMIT; seq_lens[b] < 0 or
  * seq_lens[b] + n > capacity: KV_OVERFLOW) is left unchanged. */
 int peagle_append_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
                            int32_t* seq_lens, const int32_t* n_commit, int32_t n_extra,
                            const peagle_kv_rows* rows, int32_t n_max, int32_t advance,
                            void* stream);
+
+/* The committed slots of the block that each request's length points into, and that block's
+ * scales, kept aside before rows are appended that may be dropped again, and put back bit for
+ * bit when they are (or before the accepted ones are appended): the cache is then the one that
+ * never saw them.  A request whose length is a multiple of block has no such slots.
+ *   seq_lens  device int32 [batch], the same at both calls; a request with seq_lens[b] < 0 or
+ *             > capacity is skipped with KV_OVERFLOW
+ *   layer     as in peagle_append_kv_quant; calls for single layers share one buffer
+ *   saved     device memory of at least peagle_save_kv_quant_bytes() bytes, 16-byte aligned, no
+ *             initial value; a buffer that is too small is PEAGLE_ERR_CAPACITY */
+int peagle_save_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                         const int32_t* seq_lens, void* saved, int64_t saved_bytes,
+                         void* stream);
+int peagle_restore_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
+                            const int32_t* seq_lens, const void* saved, int64_t saved_bytes,
+                            void* stream);
+
+/* Bytes that peagle_save_kv_quant needs for this cache (2 x layers x requests x kv heads of
+ * block x head_dim codes and a scale), or a negative error. */
+int64_t peagle_save_kv_quant_bytes(const peagle_kv_quant* kv);
 
 /* Read slots of the 8-bit cache back as 16- or 32-bit rows (a parked request that returns to
  * a peagle_kv cache): row t of request b is slot starts[b] + t (starts NULL: 0), t <

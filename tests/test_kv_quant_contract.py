@@ -1,0 +1,55 @@
+"""What include/peagle.h promises of the 8-bit cache's host side, and of its values by the fp64
+oracle (no GPU)."""
+import numpy as np
+import pytest
+
+from oracle import kv_quant_oracle as Q
+from test_oracle_kv_quant import A, CACHE, _kv, pk  # noqa: F401 (pk: fixture)
+
+
+def test_a_dropped_draft_rounds_committed_slots_unless_they_are_restored():
+    """Why peagle_save_kv_quant is there: 8 committed rows, one draft row with an element of 3e4,
+    dropped, and a quiet row; against the cache that never saw the draft."""
+    r = np.random.default_rng(4)
+    block, hd = 32, 64
+    rows = r.standard_normal((1, 1, 8, 1, hd))
+    loud, quiet = r.standard_normal((2, 1, 1, 1, 1, hd))
+    loud[..., 5] = 3e4
+    empty = np.zeros((1, 1, 1, 64, hd)), np.ones((1, 1, 1, 2))
+    one = Q.append(*empty, block, [0], [8], rows)
+    never = Q.append(*one, block, [8], [1], quiet)
+    drafted = Q.append(*one, block, [8], [1], loud)
+    traced = Q.append(*drafted, block, [8], [1], quiet)
+    assert np.array_equal(traced[1], never[1])  # the scale comes back, the values do not
+    assert (traced[0] != never[0])[..., :8, :].mean() > 0.5
+    codes, scale = drafted[0].copy(), drafted[1].copy()  # restored: the open block's committed part
+    codes[..., :8, :], scale[..., 0] = one[0][..., :8, :], one[1][..., 0]
+    clean = Q.append(codes, scale, block, [8], [1], quiet)
+    assert np.array_equal(clean[0][..., :9, :], never[0][..., :9, :])
+    assert np.array_equal(clean[1], never[1])
+
+
+@pytest.mark.parametrize("kw,code", CACHE)
+def test_save_and_restore_refuse_a_bad_cache(pk, kw, code):  # noqa: F811
+    L, kv, code = pk.lib(), _kv(pk, **kw), getattr(pk, "PEAGLE_ERR_" + code)
+    for f in (L.peagle_save_kv_quant, L.peagle_restore_kv_quant):
+        assert f(kv, -1, 3, A, A, 1 << 50, None) == code
+    if kw != dict(batch=2):
+        assert L.peagle_save_kv_quant_bytes(kv) == code
+
+
+def test_save_and_restore_refuse(pk):  # noqa: F811
+    L, kv = pk.lib(), _kv(pk)
+    bad, cap = pk.PEAGLE_ERR_INVALID, pk.PEAGLE_ERR_CAPACITY
+    need = pk.peagle_save_kv_quant_bytes(kv)
+    assert need == 2 * 2 * 3 * 2 * (32 * 64 + 4)
+    for f in (L.peagle_save_kv_quant, L.peagle_restore_kv_quant):
+        for layer in (-2, 2):
+            assert f(kv, layer, 3, A, A, need, None) == bad
+        assert f(kv, -1, 0, A, A, need, None) == bad and f(kv, -1, 4, A, A, need, None) == cap
+        assert f(kv, -1, 3, None, A, need, None) == bad
+        assert f(kv, -1, 3, A, None, need, None) == bad
+        assert f(kv, -1, 3, A, A + 8, need, None) == bad
+        assert f(kv, -1, 3, A, A, need - 1, None) == cap and f(kv, 1, 3, A, A, 0, None) == cap
+    huge = _kv(pk, n_layers=65535, batch=65535, n_kv_heads=65535)
+    assert L.peagle_save_kv_quant_bytes(huge) == pk.PEAGLE_ERR_UNSUPPORTED
