@@ -421,9 +421,12 @@ int peagle_decode_attention_static(int32_t batch, int32_t K, int32_t n_q_heads,
  * Keys are stored after RoPE.  Request b's committed entries are slots 0 .. seq_lens[b]-1.
  * peagle_append_kv_quant makes the scale of a block the smallest power of two s, within
  * 2^-40 .. 2^120, with |x| <= 448 s for every finite live value x of the block (1 when they
- * are all zero), so a value of a block whose largest is A is off by at most 2^-4 of itself or
- * 2^-17.8 A (half the spacing of the smallest codes), whichever is more (magnitudes from 1.9375
- * x 2^127 on round up to 2^128, infinity); the other calls take any positive finite scale.  NaN
+ * are all zero).  A value that is encoded once is off by at most 2^-4 of itself or 2^-10 s (half
+ * the spacing of the smallest codes; 2^-17.8 A for a block whose largest is A >= 2^-32),
+ * whichever is more.  A later append that raises its block's scale to s encodes it again, which
+ * is exact down to 2^-6 s and adds at most 2^-10 s below: after any number of growing scales a
+ * value is off by at most 2^-4 of itself and 2^-9 s more (2^-16.8 A).  Magnitudes from 1.9375 x
+ * 2^127 on round up to 2^128, infinity.  The other calls take any positive finite scale.  NaN
  * and infinite values are stored as NaN.  Codes and scales of
  * slots that nothing was appended to are never used and need no initial value.
  * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; block 16, 32, 64 or 128.

@@ -7,7 +7,7 @@ import torch
 
 from oracle import kv_quant_oracle as Q
 from pe_helpers import pk
-from test_gpu_kv_quant import DT, Cache, attend, queries
+from test_gpu_kv_quant import DT, Cache, attend, fresh, ints, queries
 
 pytestmark = pytest.mark.gpu
 FP8 = torch.float8_e4m3fn
@@ -141,3 +141,28 @@ def test_scales_far_apart_within_what_rows_see(nq, cap, dtype):
         c.t["k_scale"].copy_(torch.from_numpy((2.0 ** r.uniform(-1, 1, s.shape)).astype(np.float32)))
         c.t["v"].view(torch.uint8)[0, :, :, 32:48] = 0
         check(c, 0, queries(2, K, nq, hd, dtype, seed, size), lens, K)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("grow", [0.3, 1.0, 2.7])
+def test_rows_appended_one_by_one_against_the_rows_themselves(grow, dtype):
+    """Each row raises its block's scale: against the rows, not against an oracle that encodes
+    again too.  2^-4 of a value for its first encoding, less than 2^-9 of the last scale for all
+    others (half a step of the smallest codes, 2^-10 s, with scales that at least double)."""
+    m = pk()
+    B, H, hd, block, n = 2, 2, 64, 32, 32
+    c = fresh(1, B, H, 64, hd, block)
+    g = torch.Generator("cuda").manual_seed(2)
+    size = 2.0 ** (grow * torch.arange(n, device="cuda"))
+    rows = [(torch.randn(1, B, n, H, hd, device="cuda", generator=g) * size[:, None, None]).to(DT[dtype])
+            for _ in "kv"]
+    sl = ints([0] * B)
+    for at in range(n):
+        m.peagle_append_kv_quant(c.kv, B, sl, None, rows[0][:, :, at:at + 1], rows[1][:, :, at:at + 1],
+                                 1, n_extra=1)
+        for name, x in zip("kv", rows):
+            x = x[:, :, :at + 1].double().transpose(2, 3)
+            s = c.t[name + "_scale"][..., :1, None].double()
+            got = c.t[name][:, :, :, :at + 1].double() * s
+            assert ((got - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9 * s).all(), (at, name)
+    assert c.err() == 0 and sl.tolist() == [n] * B

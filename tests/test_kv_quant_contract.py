@@ -53,3 +53,38 @@ def test_save_and_restore_refuse(pk):  # noqa: F811
         assert f(kv, -1, 3, A, A, need - 1, None) == cap and f(kv, 1, 3, A, A, 0, None) == cap
     huge = _kv(pk, n_layers=65535, batch=65535, n_kv_heads=65535)
     assert L.peagle_save_kv_quant_bytes(huge) == pk.PEAGLE_ERR_UNSUPPORTED
+
+
+def test_repeated_growth_keeps_the_documented_bound():
+    """A value is encoded again whenever its block's scale grows: 29.125 x 2^-9 beside 448 is 30 x
+    2^-9, beside 897 it is 32 x 2^-9, off by 1.4 times what one encoding would allow."""
+    block, hd = 16, 64
+    c = np.zeros((1, 1, 1, 16, hd)), np.ones((1, 1, 1, 1))
+    x = 29.125 * 2.0 ** -9
+    for at, top in enumerate((448.0, 449.0, 897.0)):
+        row = np.zeros((1, 1, 1, 1, hd))
+        row[..., 0], row[..., 1] = top, x
+        c = Q.append(*c, block, [at], [1], row)
+    err, s = abs(Q.values(*c, block)[0, 0, 0, 0, 1] - x), c[1].max()
+    assert max(2.0 ** -4 * x, 2.0 ** -10 * s) < err <= 2.0 ** -4 * x + 2.0 ** -9 * s
+    assert s * 2.0 ** -9 <= 2.0 ** -16.8 * 897.0
+
+
+@pytest.mark.parametrize("grow", [0.3, 1.0, 2.7])
+def test_rows_appended_one_by_one_against_the_rows_themselves(grow):
+    r = np.random.default_rng(int(10 * grow))
+    block, hd, n = 32, 64, 32
+    rows = r.standard_normal((1, 1, n, 2, hd)) * 2.0 ** (grow * np.arange(n))[:, None, None]
+    c = np.zeros((1, 1, 2, 32, hd)), np.ones((1, 1, 2, 1))
+    for at in range(n):
+        c = Q.append(*c, block, [at], [1], rows[:, :, at:at + 1])
+        x = np.swapaxes(rows[:, :, :at + 1], 2, 3)
+        err = np.abs(Q.values(*c, block)[..., :at + 1, :] - x)
+        assert (err <= 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * c[1][..., None]).all()
+
+
+def test_a_block_below_the_smallest_scale_keeps_half_of_its_spacing():
+    x = np.full((1, 1, 1, 1, 64), 2.0 ** -48)
+    codes, scale = Q.append(np.zeros((1, 1, 1, 16, 64)), np.ones((1, 1, 1, 1)), 16, [0], [1], x)
+    assert scale[0, 0, 0, 0] == 2.0 ** -40
+    assert (np.abs(codes[..., 0, :] * scale - 2.0 ** -48) <= 2.0 ** -50).all()
