@@ -346,7 +346,7 @@ struct Running {
     // (NaN passes no comparison: it reaches the weights as it is)
     constexpr unsigned ALL = (1u << (2 * NT)) - 1;
     if (__any_sync(0xffffffffu, top > LIM || started != ALL)) raise(x);
-    const float rv[2] = {rcp(vs[0]), rcp(vs[1])};
+    const float rv[2] = {inverse_scale(vs[0]), inverse_scale(vs[1])};
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
       uint32_t p[F32 ? 2 : 1][NT][2];

@@ -89,6 +89,11 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 1 / c of a value scale from 2^-124 to the largest float (rcp alone gives 0 for subnormal results;
+// below, where sums of w / c leave fp32 in any case, 2^124 stands for it).
+__device__ __forceinline__ float inverse_scale(float c) {
+  return rcp(fmaxf(c, 0x1p-124f) * 0.25f) * 0.25f;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -239,6 +244,7 @@ template <typename T>
 __device__ __forceinline__ T* finish_row(const AttnQuantArgs& a, int hd, int req, int at, float m,
                                          float l, bool first, float& inv) {
   const bool none = m == NO_REF && l == 0.f;  // (a row of NaN scores has no reference either)
+  if (l == INFINITY) l = NAN;  // (value scales so small that the sum of w / c left fp32)
   inv = none ? 0.f : rcp(l);
   const int64_t to = (int64_t)req * a.K * (a.nkv * a.G) + at;
   if (first && a.lse) a.lse[to] = none ? -INFINITY : (m + lg2(l)) * LN2;

@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
       tc::tmem_ld32(tmem + lanes + 128 + b * 64 + col0, x);
       tc::tmem_ld_wait();
       const float vs = scales[t % DESCS][TT / 16 + key / 16];
-      const float g = scales[t % DESCS][key / 16] * q_scale[d.head & 3], lv = lg2(vs), rv = rcp(vs);
+      const float g = scales[t % DESCS][key / 16] * q_scale[d.head & 3], lv = lg2(vs);
+      const float rv = inverse_scale(vs);
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s_empty[b]);

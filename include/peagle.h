@@ -426,8 +426,8 @@ int peagle_decode_attention_static(int32_t batch, int32_t K, int32_t n_q_heads,
  * whichever is more.  A later append that raises its block's scale to s encodes it again, which
  * is exact down to 2^-6 s and adds at most 2^-10 s below: after any number of growing scales a
  * value is off by at most 2^-4 of itself and 2^-9 s more (2^-16.8 A).  Magnitudes from 1.9375 x
- * 2^127 on round up to 2^128, infinity.  The other calls take any positive finite scale.  NaN
- * and infinite values are stored as NaN.  Codes and scales of
+ * 2^127 on round up to 2^128, infinity.  peagle_read_kv_quant takes any positive finite scale,
+ * the attention its own range.  NaN and infinite values are stored as NaN.  Codes and scales of
  * slots that nothing was appended to are never used and need no initial value.
  * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; block 16, 32, 64 or 128.
  * capacity is a multiple of block; k and v are 16-byte aligned; n_layers and batch are at
@@ -547,7 +547,10 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  * their weights as two such parts (22 bits); weights x value scale below 2^-20 of the row's
  * largest lose bits, down to 2^-31 of it (fp32 queries: 2^-38), which over n slots adds up to at
  * most n 2^-31 of that largest (fp32: n 2^-38); below 2^-120 of it the weight leaves the sum of
- * weights too: the value scales that matter to a row lie within 2^100 of one another.
+ * weights too: the value scales that matter to a row lie within 2^100 of one another.  Value
+ * scales are 2^-80 or more (below, a row whose sum of weights leaves fp32 gives NaN), key scales
+ * any positive finite ones that keep scale q . k within fp32; the largest element of a row of q
+ * counts as at least 2^-86.
  * Results are the same on every call with the same lengths and sizes (no atomics).
  * A request with seq_lens[b] < 0, or whose last row's slot is beyond the capacity, is
  * skipped with KV_OVERFLOW; its rows are left as they are.  Waits inside the kernel are

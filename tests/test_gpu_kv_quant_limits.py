@@ -166,3 +166,29 @@ def test_rows_appended_one_by_one_against_the_rows_themselves(grow, dtype):
             got = c.t[name][:, :, :, :at + 1].double() * s
             assert ((got - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -9 * s).all(), (at, name)
     assert c.err() == 0 and sl.tolist() == [n] * B
+
+
+# one launch, clusters, two launches, tcgen05
+SCALE_SHAPES = [("bf16", 4, 416), ("f32", 4, 416), ("bf16", 4, 2048), ("f32", 8, 12288),
+                ("bf16", 8, 12288), ("bf16", 32, 98304)]
+
+
+@pytest.mark.parametrize("dtype,nq,cap", SCALE_SHAPES)
+@pytest.mark.parametrize("scale", [2.0 ** -80, 2.0 ** -40, 2.0 ** 120, 2.0 ** 126, 2.0 ** 127,
+                                   3.4e38])
+def test_value_scales_at_both_ends_of_their_range(dtype, nq, cap, scale):
+    lens, K, hd = [400, 90], 2, 64
+    c = Cache(1, 2, 1, cap, hd, 16, 9, spread=0)
+    c.t["v"].view(torch.uint8).bitwise_and_(0xaf)  # (below 0.5: the results stay finite)
+    c.t["v_scale"].fill_(scale)
+    check(c, 0, queries(2, K, nq, hd, dtype, 12), lens, K)
+
+
+@pytest.mark.parametrize("dtype,nq,cap", SCALE_SHAPES)
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** -140, 2.0 ** -126])
+def test_value_scales_below_their_range_are_not_silent(dtype, nq, cap, scale):
+    lens, K, hd = [400, 90], 2, 64
+    c = Cache(1, 2, 1, cap, hd, 16, 9, spread=0)
+    c.t["v_scale"].fill_(scale)
+    out, lse = attend(c, 0, queries(2, K, nq, hd, dtype, 12), lens, K)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
