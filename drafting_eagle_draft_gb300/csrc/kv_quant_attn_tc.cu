@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
     if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
+  // (after a wait that ran out the softmax threads look at a descriptor, perhaps one not written yet,
+  // before the vote that ends their loop: its head picks a row of row_j)
+  if (tid < DESCS) descs[tid] = TileDesc{};
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < NR; ++i) tc::mbar_init(&raw_full[i], 1), tc::mbar_init(&raw_empty[i], CONV / 32);
