@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
       wait_long(bar, (uint32_t)phase & 1u, &s_abort, a.errors);
   };
 
+  int copied = 0;  // tiles that the copying warp issued
   if (warp == LOAD_WARP) {
     // ---- the walk over the share, bulk copies of the codes, and the scales
     const uint64_t policy = tc::policy_evict_first();
@@ -257,11 +258,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
       seg = next;
       u = seg.at;
     }
-    if (s_abort && lane == 0) {  // the copies in flight
-      volatile int never = 0;
-      for (int x = max(0, t - NR); x < t; ++x)
-        tc::mbar_wait(&raw_full[x % NR], (uint32_t)(x / NR) & 1u, &never);
-    }
+    copied = t;
     __syncwarp();
   } else if (warp == MMA_WARP) {
     // ---- the products
@@ -653,6 +650,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
   if (warp == MMA_WARP) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, TMEM_COLS);
+  }
+  if (warp == LOAD_WARP && lane == 0 && s_abort) {
+    // The copies in flight, whoever gave up and however long after the last of them was issued.
+    volatile int never = 0;
+    for (int x = max(0, copied - NR); x < copied; ++x)
+      tc::mbar_wait(&raw_full[x % NR], (uint32_t)(x / NR) & 1u, &never);
   }
 }
 
