@@ -42,6 +42,7 @@ EXPORTS = ("peagle_create", "peagle_draft", "peagle_catch_up", "peagle_verify_gr
            "peagle_append_kv_quant", "peagle_read_kv_quant", "peagle_save_kv_quant",
            "peagle_restore_kv_quant", "peagle_save_kv_quant_bytes",
            "peagle_decode_attention_quant", "peagle_decode_attention_quant_workspace",
+           "peagle_set_wait_limit_quant",
            "peagle_device_error_bits", "peagle_strerror", "peagle_destroy")
 STAGES = ("fc", "qkv", "attn", "oproj", "gate_up", "down", "lm_head", "norm", "small")
 
@@ -146,6 +147,7 @@ def lib():
         L.peagle_decode_attention_quant_workspace.argtypes = [ctypes.POINTER(PeagleKVQuant), _i32,
                                                               _i32, _i32]
         L.peagle_decode_attention_quant_workspace.restype = _i64
+        L.peagle_set_wait_limit_quant.argtypes = [ctypes.c_uint64, _i32]
         L.peagle_read_timing.argtypes = [_vp, _vp, _vp]
         L.peagle_read_pass_trace.argtypes = [_vp, _vp, _i32, _vp, _vp]
         L.peagle_read_pass_trace.restype = _i32
@@ -610,6 +612,13 @@ def peagle_decode_attention_quant(kv: PeagleKVQuant, layer, batch, K, n_q_heads,
         workspace.numel() * workspace.element_size(), s)
     if rc:
         raise PeagleError(rc, what)
+
+
+def peagle_set_wait_limit_quant(limit_ns: int, unreachable_wait: int = -1):
+    """Bound of the waits inside peagle_decode_attention_quant, and one that cannot succeed: the
+    failure-path drill (include/peagle.h); (0, -1) restores the defaults."""
+    _check(lib().peagle_set_wait_limit_quant(int(limit_ns), int(unreachable_wait)),
+           "peagle_set_wait_limit_quant")
 
 
 def peagle_device_error_bits(ctx: Context) -> int:

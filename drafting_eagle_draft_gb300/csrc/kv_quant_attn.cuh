@@ -51,6 +51,8 @@ struct AttnQuantArgs {
   int split;               // > 0: a cluster of that many CTAs (a power of two) takes whole heads,
                            // and there is no second step
   float scale;             // of the scores, with log2(e)
+  unsigned long long wait_ns;  // bound of the tcgen05 kernel's waits
+  int stall;               // the Wait whose barriers want one arrival more than come, or -1
 };
 
 // Slots [begin, end) that row j of a request of length len sees; empty when end <= begin.

@@ -30,6 +30,8 @@
 // 2.9 TB/s (43 % of the measured copy rate); the warps' kernel takes 158.  Tried and slower: groups
 // of 128 threads that each convert, multiply and weigh their own tiles (195 us for what takes 146),
 // the weights computed while the votes come in (123 for 108: the code leaves the instruction cache).
+#include <atomic>
+
 #include "kv_quant_attn.cuh"
 
 namespace peagle {
@@ -73,6 +75,14 @@ struct TileDesc {
 };
 enum { FIRST = 1, LAST = 2, BEGAN = 4, WHOLE = 8, END = 16 };
 constexpr int DESCS = 16;
+
+// The waits that peagle_set_wait_limit_quant can make unreachable (the copies' own completion is
+// not one of them: what is in flight has to be waited for).
+enum Wait { RAW_EMPTY, K_FULL, V_FULL, S_FULL, S_EMPTY, P_FULL, PV_DONE, HEAD_IN, O_FREE, WAITS };
+constexpr unsigned long long DEFAULT_WAIT_NS = 2000000000ull;
+std::atomic<unsigned long long> wait_limit{DEFAULT_WAIT_NS};
+std::atomic<int> unreachable{-1};
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -102,8 +112,8 @@ __device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
 
 // The end of a wait that does not succeed at once (out of line: the code of the loops stays small).
 __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                       int* errors) {
-  if (!tc::mbar_wait(bar, parity, abort)) {
+                                       int* errors, unsigned long long limit_ns) {
+  if (!tc::mbar_wait(bar, parity, abort, limit_ns)) {
     if (!*abort) raise_error(errors, PEAGLE_DEV_TIMEOUT);
     *abort = 1;
   }
@@ -182,17 +192,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
   if (tid < DESCS) descs[tid] = TileDesc{};
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < NR; ++i) tc::mbar_init(&raw_full[i], 1), tc::mbar_init(&raw_empty[i], CONV / 32);
-    for (int i = 0; i < NK; ++i) tc::mbar_init(&k_full[i], CONV / 32);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&v_full[i], CONV / 32);
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&s_empty[i], SOFT / 32);
-      tc::mbar_init(&p_full[i], SOFT / 32);
-      tc::mbar_init(&pv_done[i], 1);
+    auto init = [&](uint64_t* bar, int count, Wait w) { tc::mbar_init(bar, count + (a.stall == w)); };
+    for (int i = 0; i < NR; ++i) {
+      tc::mbar_init(&raw_full[i], 1);
+      init(&raw_empty[i], CONV / 32, RAW_EMPTY);
     }
-    tc::mbar_init(&head_in, SOFT / 32);
-    tc::mbar_init(&o_free, SOFT / 32);
+    for (int i = 0; i < NK; ++i) init(&k_full[i], CONV / 32, K_FULL);
+    for (int i = 0; i < 2; ++i) {
+      init(&v_full[i], CONV / 32, V_FULL);
+      init(&s_full[i], 1, S_FULL);
+      init(&s_empty[i], SOFT / 32, S_EMPTY);
+      init(&p_full[i], SOFT / 32, P_FULL);
+      init(&pv_done[i], 1, PV_DONE);
+    }
+    init(&head_in, SOFT / 32, HEAD_IN);
+    init(&o_free, SOFT / 32, O_FREE);
     tc::mbar_init(&finished, 1);
     tc::fence_barrier_init();
   }
@@ -206,7 +220,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
   const uint32_t tmem = tmem_at;
   auto wait = [&](uint64_t* bar, int phase) {
     if (!tc::mbar_try_wait(bar, (uint32_t)phase & 1u))
-      wait_long(bar, (uint32_t)phase & 1u, &s_abort, a.errors);
+      wait_long(bar, (uint32_t)phase & 1u, &s_abort, a.errors, a.wait_ns);
   };
 
   int copied = 0;  // tiles that the copying warp issued
@@ -693,8 +707,17 @@ cudaError_t launch_attention_tc(int hd, int rows, AttnQuantArgs a, cudaStream_t 
   const int parts = cdiv(rows, RP);
   a.part_rows = cdiv(rows, parts);
   a.heads = a.nkv * parts;
+  a.wait_ns = wait_limit.load(), a.stall = unreachable.load();
   return hd == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace kvq
 }  // namespace peagle
+
+extern "C" int peagle_set_wait_limit_quant(uint64_t limit_ns, int32_t unreachable_wait) {
+  using namespace peagle::kvq;
+  if (unreachable_wait < -1 || unreachable_wait >= WAITS) return PEAGLE_ERR_INVALID;
+  wait_limit.store(limit_ns ? (unsigned long long)limit_ns : DEFAULT_WAIT_NS);
+  unreachable.store(unreachable_wait);
+  return PEAGLE_OK;
+}

@@ -564,6 +564,17 @@ int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t layer, int3
                                   int32_t window, float scale, void* out, float* out_lse,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Failure-path drill of the waits inside peagle_decode_attention_quant (its tcgen05 kernel, which
+ * calls with many query rows and slots run; the others have none), as peagle_set_wait_limit is
+ * for the draft pass: a wait gives up after limit_ns nanoseconds (0: the default of 2 s), and
+ * unreachable_wait >= 0 names one that can never succeed, because its barrier wants one arrival
+ * more than come: 0 a stage of copied codes to be free again, 1 converted keys, 2 converted
+ * values, 3 scores, 4 scores to be read, 5 weights, 6 outputs added up, 7 a head's sums, 8 a head's
+ * outputs to be read; -1 none.  Every role then leaves, and the call sets TIMEOUT.  For the
+ * process's calls that follow (a captured graph keeps what held at its capture).  Returns
+ * PEAGLE_ERR_INVALID for another wait. */
+int peagle_set_wait_limit_quant(uint64_t limit_ns, int32_t unreachable_wait);
+
 /* Bytes of workspace that peagle_decode_attention_quant needs for these sizes (for any layer,
  * lengths and window), or a negative error. */
 int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant* kv, int32_t batch,

@@ -88,3 +88,11 @@ def test_a_block_below_the_smallest_scale_keeps_half_of_its_spacing():
     codes, scale = Q.append(np.zeros((1, 1, 1, 16, 64)), np.ones((1, 1, 1, 1)), 16, [0], [1], x)
     assert scale[0, 0, 0, 0] == 2.0 ** -40
     assert (np.abs(codes[..., 0, :] * scale - 2.0 ** -48) <= 2.0 ** -50).all()
+
+
+def test_wait_limit_refuses_an_unknown_wait(pk):  # noqa: F811
+    for w in (-2, 9, 1000):
+        with pytest.raises(pk.PeagleError) as e:
+            pk.peagle_set_wait_limit_quant(1000, w)
+        assert e.value.code == pk.PEAGLE_ERR_INVALID
+    pk.peagle_set_wait_limit_quant(0, -1)
