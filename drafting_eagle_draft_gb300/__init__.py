@@ -11,7 +11,6 @@ import ctypes
 import os
 
 import numpy as np
-import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpeagle.so")
@@ -433,12 +432,26 @@ def _on(t, dev, dtype, what):
     return t.data_ptr()
 
 
+# torch, once there is a cache of its tensors (the package's host calls do without it), and the
+# current stream's handle without the Stream object around it (0.1 us for 2.9)
+torch = None
+_raw_stream = None
+
+
+def _import_torch():
+    global torch, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
     """PeagleKVQuant over the tensors of an 8-bit cache: k, v float8_e4m3fn (or uint8)
     [n_layers, batch, n_kv_heads, capacity, head_dim], k_scale, v_scale float32
     [n_layers, batch, n_kv_heads, capacity / block], errors an int32 tensor of one element or
     None.  All contiguous and on one CUDA device; the struct keeps them alive."""
     what = "kv_quant_struct"
+    if torch is None:
+        _import_torch()
     if k.dim() != 5 or k_scale.dim() != 4 or not k_scale.shape[3] or \
             k.shape[3] % k_scale.shape[3] or k.shape[:3] != k_scale.shape[:3]:
         _refuse(what, f"codes {tuple(k.shape)} and scales {tuple(k_scale.shape)} do not fit")
@@ -459,10 +472,6 @@ def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
     st._keep = (k, v, k_scale, v_scale, errors)
     st._device = k.device
     return st
-
-
-# the current stream's handle without the Stream object around it (0.1 us for 2.9)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _quant_stream(kv, what, stream):

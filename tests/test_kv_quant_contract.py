@@ -1,5 +1,9 @@
 """What include/peagle.h promises of the 8-bit cache's host side, and of its values by the fp64
 oracle (no GPU)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -96,3 +100,16 @@ def test_wait_limit_refuses_an_unknown_wait(pk):  # noqa: F811
             pk.peagle_set_wait_limit_quant(1000, w)
         assert e.value.code == pk.PEAGLE_ERR_INVALID
     pk.peagle_set_wait_limit_quant(0, -1)
+
+
+def test_host_calls_work_without_torch(pk):  # noqa: F811
+    """The package imports, and its host-only calls answer, where torch cannot be imported."""
+    root = os.path.dirname(os.path.dirname(pk.LIB_PATH))
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import drafting_eagle_draft_gb300 as m\n"
+            "assert m.strerror(m.PEAGLE_ERR_CAPACITY) and m.lib().peagle_status(None) == m.PEAGLE_ERR_INVALID\n"
+            "kv = m.PeagleKVQuant(k=1 << 20, v=1 << 20, k_scale=1 << 20, v_scale=1 << 20, n_layers=1,\n"
+            "                     batch=1, n_kv_heads=1, capacity=64, head_dim=64, block=32)\n"
+            "assert m.peagle_decode_attention_quant_workspace(kv, 1, 1, 1) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
