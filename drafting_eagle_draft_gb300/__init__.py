@@ -86,6 +86,7 @@ class PeagleKVQuant(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("errors", _vp)] + \
                [(n, _i32) for n in ("n_layers", "batch", "n_kv_heads", "capacity", "head_dim",
                                     "block")]
+    _device = None  # of its tensors (kv_quant_struct)
 
 
 class PeagleKVRows(ctypes.Structure):
@@ -477,6 +478,8 @@ def kv_quant_struct(k, v, k_scale, v_scale, errors=None) -> PeagleKVQuant:
 def _quant_stream(kv, what, stream):
     """The call's stream; the cache's device has to be the current CUDA device."""
     dev = kv._device
+    if dev is None:
+        _refuse(what, "a cache that kv_quant_struct made is wanted")
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         _refuse(what, f"the cache is on {dev}, which is not the current CUDA device")
     if stream is None and _raw_stream is not None:

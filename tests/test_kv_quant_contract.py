@@ -113,3 +113,16 @@ def test_host_calls_work_without_torch(pk):  # noqa: F811
             "assert m.peagle_decode_attention_quant_workspace(kv, 1, 1, 1) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_a_cache_filled_by_hand_is_refused_by_the_tensor_calls(pk):  # noqa: F811
+    kv = _kv(pk)
+    for call in (lambda: pk.peagle_append_kv_quant(kv, 1, None, None, None, None, 1, stream=0),
+                 lambda: pk.peagle_read_kv_quant(kv, 1, None, None, None, 1, stream=0),
+                 lambda: pk.peagle_save_kv_quant(kv, 1, None, None, stream=0),
+                 lambda: pk.peagle_restore_kv_quant(kv, 1, None, None, stream=0),
+                 lambda: pk.peagle_decode_attention_quant(kv, 0, 1, 1, 1, None, None, None, None,
+                                                          stream=0)):
+        with pytest.raises(pk.PeagleError) as e:
+            call()
+        assert e.value.code == pk.PEAGLE_ERR_INVALID
