@@ -424,6 +424,16 @@ def _refuse(what, why):
     raise PeagleError(PEAGLE_ERR_INVALID, f"{what}: {why}")
 
 
+_END = 1 << 31
+
+
+def _refuse_wide(what, **ints):
+    """The C calls take 32 bits of a whole number: what passes them would come in as another."""
+    for name, x in ints.items():
+        if not -_END <= x < _END:
+            _refuse(what, f"{name} = {x} is beyond 32 bits")
+
+
 def _on(t, dev, dtype, what):
     """The device pointer of a CUDA tensor on `dev` with the given type (else INVALID)."""
     if t is None:
@@ -528,6 +538,9 @@ def peagle_append_kv_quant(kv: PeagleKVQuant, batch, seq_lens, n_commit, k_rows,
     axis), any strides with the last axis contiguous."""
     what = "peagle_append_kv_quant"
     s = _quant_stream(kv, what, stream)
+    if not (-_END <= layer < _END and -_END <= n_extra < _END and 0 < batch < _END and
+            0 < n_max < _END):
+        _refuse_wide(what, layer=layer, n_extra=n_extra, batch=batch, n_max=n_max)
     rows = _kv_rows(kv, layer, batch, k_rows, v_rows, n_max, what, False)
     dev = kv._device
     rc = lib().peagle_append_kv_quant(kv, layer, batch, _lens(seq_lens, batch, dev, what),
@@ -543,6 +556,8 @@ def peagle_read_kv_quant(kv: PeagleKVQuant, batch, counts, out_k, out_v, n_max, 
     (include/peagle.h)."""
     what = "peagle_read_kv_quant"
     s = _quant_stream(kv, what, stream)
+    if not (-_END <= layer < _END and 0 < batch < _END and 0 < n_max < _END):
+        _refuse_wide(what, layer=layer, batch=batch, n_max=n_max)
     rows = _kv_rows(kv, layer, batch, out_k, out_v, n_max, what, True)
     dev = kv._device
     rc = lib().peagle_read_kv_quant(kv, layer, batch, _lens(starts, batch, dev, what),
@@ -562,6 +577,7 @@ def peagle_save_kv_quant_bytes(kv: PeagleKVQuant) -> int:
 def _open_block(call, what, kv, batch, seq_lens, saved, layer, stream):
     s = _quant_stream(kv, what, stream)
     dev = kv._device
+    _refuse_wide(what, layer=layer, batch=batch)
     if not saved.is_contiguous() or saved.device != dev:
         _refuse(what, f"a contiguous buffer on {dev} is wanted")
     rc = call(kv, layer, batch, _lens(seq_lens, batch, dev, what), saved.data_ptr(),
@@ -586,6 +602,7 @@ def peagle_restore_kv_quant(kv: PeagleKVQuant, batch, seq_lens, saved, layer=-1,
 
 def peagle_decode_attention_quant_workspace(kv: PeagleKVQuant, batch, K, n_q_heads) -> int:
     """Bytes of workspace of peagle_decode_attention_quant (include/peagle.h)."""
+    _refuse_wide("peagle_decode_attention_quant_workspace", batch=batch, K=K, n_q_heads=n_q_heads)
     n = lib().peagle_decode_attention_quant_workspace(kv, batch, K, n_q_heads)
     if n < 0:
         raise PeagleError(n, "peagle_decode_attention_quant_workspace")
@@ -600,6 +617,9 @@ def peagle_decode_attention_quant(kv: PeagleKVQuant, layer, batch, K, n_q_heads,
     CUDA tensor; scale: 1 / sqrt(head_dim) when None."""
     what = "peagle_decode_attention_quant"
     s = _quant_stream(kv, what, stream)
+    if not (0 <= layer < _END and 0 <= window < _END and 0 < batch < _END and 0 < K < _END and
+            0 < n_q_heads < _END):
+        _refuse_wide(what, layer=layer, window=window, batch=batch, K=K, n_q_heads=n_q_heads)
     dev, hd, dt, rows = kv._device, kv.head_dim, q.dtype, batch * K
     shape = (rows, n_q_heads, hd)
     if dt is torch.bfloat16:
@@ -629,6 +649,7 @@ def peagle_decode_attention_quant(kv: PeagleKVQuant, layer, batch, K, n_q_heads,
 def peagle_set_wait_limit_quant(limit_ns: int, unreachable_wait: int = -1):
     """Bound of the waits inside peagle_decode_attention_quant, and one that cannot succeed: the
     failure-path drill (include/peagle.h); (0, -1) restores the defaults."""
+    _refuse_wide("peagle_set_wait_limit_quant", unreachable_wait=unreachable_wait)
     _check(lib().peagle_set_wait_limit_quant(int(limit_ns), int(unreachable_wait)),
            "peagle_set_wait_limit_quant")
 

@@ -192,3 +192,30 @@ def test_value_scales_below_their_range_are_not_silent(dtype, nq, cap, scale):
     c.t["v_scale"].fill_(scale)
     out, lse = attend(c, 0, queries(2, K, nq, hd, dtype, 12), lens, K)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def test_whole_numbers_beyond_32_bits_are_refused():
+    m = pk()
+    c = Cache(1, 2, 2, 64, 64, 32, 5)
+    before = {k: t.clone() for k, t in c.t.items()}
+    rows = torch.zeros(2, 1, 2, 4, 2, 64, device="cuda")
+    q, sl, wide = torch.zeros(2, 4, 64, device="cuda"), ints([3, 4]), 1 << 32
+    out, work = torch.full_like(q, -7.0), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    saved = torch.empty(m.peagle_save_kv_quant_bytes(c.kv), dtype=torch.uint8, device="cuda")
+    for call in (lambda: m.peagle_append_kv_quant(c.kv, 2, sl, None, *rows, 4, n_extra=wide + 1),
+                 lambda: m.peagle_append_kv_quant(c.kv, 2, sl, None, *rows[:, 0], 4, layer=wide, n_extra=1),
+                 lambda: m.peagle_append_kv_quant(c.kv, 1 - wide, sl, None, *rows, 4, n_extra=1),
+                 lambda: m.peagle_append_kv_quant(c.kv, 2, sl, None, *rows, 4 - wide, n_extra=1),
+                 lambda: m.peagle_read_kv_quant(c.kv, 2, sl, *rows[:, 0], 4, layer=wide),
+                 lambda: m.peagle_read_kv_quant(c.kv, 2 - wide, sl, *rows, 4),
+                 lambda: m.peagle_save_kv_quant(c.kv, 2, sl, saved, layer=wide),
+                 lambda: m.peagle_restore_kv_quant(c.kv, 1 - wide, sl, saved),
+                 lambda: m.peagle_decode_attention_quant(c.kv, wide, 2, 1, 4, q, sl, out, work),
+                 lambda: m.peagle_decode_attention_quant(c.kv, 0, 2, 1, 4, q, sl, out, work, window=wide + 2)):
+        with pytest.raises(m.PeagleError) as e:
+            call()
+        assert e.value.code == m.PEAGLE_ERR_INVALID
+    torch.cuda.synchronize()
+    assert sl.tolist() == [3, 4] and (out == -7.0).all() and not rows.any()
+    for k, t in c.t.items():
+        assert torch.equal(t.view(torch.uint8), before[k].view(torch.uint8))

@@ -126,3 +126,14 @@ def test_a_cache_filled_by_hand_is_refused_by_the_tensor_calls(pk):  # noqa: F81
         with pytest.raises(pk.PeagleError) as e:
             call()
         assert e.value.code == pk.PEAGLE_ERR_INVALID
+
+
+def test_whole_numbers_beyond_32_bits_are_refused(pk):  # noqa: F811
+    """ctypes passes their low 32 bits: 2^32 + 1 draft rows came in as one."""
+    kv = _kv(pk)
+    assert pk.peagle_decode_attention_quant_workspace(kv, 3, 2, 4) > 0
+    for args in ((3 + 2 ** 32, 2, 4), (3, 1 + 2 ** 32, 4), (3, 2, 4 - 2 ** 32)):
+        with pytest.raises(pk.PeagleError):
+            pk.peagle_decode_attention_quant_workspace(kv, *args)
+    with pytest.raises(pk.PeagleError):
+        pk.peagle_set_wait_limit_quant(0, 2 ** 32 - 1)
