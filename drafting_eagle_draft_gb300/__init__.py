@@ -508,8 +508,13 @@ def _kv_rows(kv, layer, batch, k, v, n_max, what, written):
         code = PEAGLE_F32
     else:
         _refuse(what, f"rows are float32 or bfloat16, got {dt}")
-    if len(sh) != (5 if whole else 4) or v.shape != sh or v.stride() != sd:
-        _refuse(what, f"rows {tuple(sh)} and {tuple(v.shape)} (strides {sd}, {v.stride()}) are "
+    vd = v.stride()
+    if vd != sd and v.shape == sh:
+        # (axes of one element have no stride to agree on: one token of a fused projection beside a
+        # contiguous one)
+        sd, vd = (tuple(0 if n == 1 else x for n, x in zip(sh[:-1], y)) + y[-1:] for y in (sd, vd))
+    if len(sh) != (5 if whole else 4) or v.shape != sh or vd != sd:
+        _refuse(what, f"rows {tuple(sh)} and {tuple(v.shape)} (strides {sd}, {vd}) are "
                       f"not alike or not of {5 if whole else 4} axes")
     if (whole and sh[0] != kv.n_layers) or sh[-4] < batch or sh[-3] < n_max or \
             sh[-2] != kv.n_kv_heads or sh[-1] != kv.head_dim or sd[-1] != 1:

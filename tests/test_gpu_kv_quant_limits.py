@@ -219,3 +219,27 @@ def test_whole_numbers_beyond_32_bits_are_refused():
     assert sl.tolist() == [3, 4] and (out == -7.0).all() and not rows.any()
     for k, t in c.t.items():
         assert torch.equal(t.view(torch.uint8), before[k].view(torch.uint8))
+
+
+def test_one_token_of_a_fused_projection_beside_a_contiguous_one():
+    """Keys and values whose strides differ along axes of one element only are alike."""
+    m = pk()
+    B, H, hd = 1, 2, 64
+    c, e = (Cache(1, B, H, 64, hd, 32, 5) for _ in "ce")
+    fused = torch.randn(B, 1, 3 * H, hd, device="cuda")
+    k, v = fused[:, :, :H], torch.randn(B, 1, H, hd, device="cuda")
+    assert k.stride() != v.stride()
+    for x, rows in ((c, (k, v)), (e, (k.contiguous(), v))):
+        m.peagle_append_kv_quant(x.kv, B, ints([5]), None, *rows, 1, layer=0, n_extra=1)
+    for name in c.t:
+        assert torch.equal(c.t[name].view(torch.uint8), e.t[name].view(torch.uint8))
+    out = torch.zeros(B, 1, 3 * H, hd, device="cuda")
+    one = torch.zeros(B, 1, H, hd, device="cuda")
+    m.peagle_read_kv_quant(c.kv, B, ints([1]), out[:, :, :H], one, 1, layer=0, starts=ints([5]))
+    for got, x in ((out[:, :, :H], k), (one, v)):
+        assert ((got - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -10 * 8).all() and got.any()
+    assert not out[:, :, H:].any() and c.err() == 0
+    with pytest.raises(m.PeagleError):  # two tokens: the strides matter
+        f = torch.randn(B, 2, 3 * H, hd, device="cuda")
+        m.peagle_append_kv_quant(c.kv, B, ints([5]), None, f[:, :, :H], f[:, :, :H].contiguous(), 2,
+                                 layer=0, n_extra=2)
