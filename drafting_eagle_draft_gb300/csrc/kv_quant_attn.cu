@@ -1018,7 +1018,7 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   const int64_t need = peagle_decode_attention_quant_workspace(kv, batch, K, n_q_heads);
   if (need < 0) return (int)need;
   if (layer < 0 || layer >= kv->n_layers || !q || !seq_lens || !out || !workspace ||
-      (causal != 0 && causal != 1) || window < 0 || !isfinite(scale))
+      (causal != 0 && causal != 1) || window < 0 || !isfinite(scale * LOG2E))
     return PEAGLE_ERR_INVALID;
   if (dtype != PEAGLE_F32 && dtype != PEAGLE_BF16) return PEAGLE_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(out_lse, 4) ||

@@ -533,7 +533,7 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  *             cache, as after an append with advance = 0); 0: every row sees the slots
  *             0 .. seq_lens[b] - 1 only
  *   window    > 0: of those, only slots above seq_lens[b] + j - window; 0: all
- *   scale     of the scores, finite (1 / sqrt(head_dim) as a rule)
+ *   scale     of the scores (1 / sqrt(head_dim) as a rule), finite also times log2(e)
  *   out_lse   device fp32 [batch*K][n_q_heads]: the natural logarithm of the sum of
  *             exp(scale q . k), by which the result joins with attention over other keys;
  *             or NULL

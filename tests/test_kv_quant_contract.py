@@ -137,3 +137,10 @@ def test_whole_numbers_beyond_32_bits_are_refused(pk):  # noqa: F811
             pk.peagle_decode_attention_quant_workspace(kv, *args)
     with pytest.raises(pk.PeagleError):
         pk.peagle_set_wait_limit_quant(0, 2 ** 32 - 1)
+
+
+def test_attention_refuses_a_scale_that_log2_e_makes_infinite(pk):  # noqa: F811
+    L, kv = pk.lib(), _kv(pk)
+    for scale in (2.5e38, -3e38):
+        assert L.peagle_decode_attention_quant(kv, 0, 3, 2, 4, A, pk.PEAGLE_BF16, 0, A, 1, 0, scale, A,
+                                               None, A, 1 << 40, None) == pk.PEAGLE_ERR_INVALID
