@@ -513,8 +513,8 @@ int64_t peagle_save_kv_quant_bytes(const peagle_kv_quant* kv);
 /* Read slots of the 8-bit cache back as 16- or 32-bit rows (a parked request that returns to
  * a peagle_kv cache): row t of request b is slot starts[b] + t (starts NULL: 0), t <
  * counts[b] (0 .. n_max); rows from counts[b] on are left as they are.  code x scale is
- * rounded once to the rows' type (no rounding for the scales that peagle_append_kv_quant
- * writes).  layer as above.  Rows of `out` do not overlap one another.  Out of range:
+ * computed in fp32 and rounded to the rows' type (both exact for the scales that
+ * peagle_append_kv_quant writes).  layer as above.  Rows of `out` do not overlap one another.  Out of range:
  * counts[b] outside 0 .. n_max is BAD_COMMIT, starts[b] < 0 or starts[b] + counts[b] >
  * capacity KV_OVERFLOW; that request's rows are left as they are. */
 int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
