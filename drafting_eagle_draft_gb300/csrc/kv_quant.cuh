@@ -36,6 +36,11 @@ __device__ __forceinline__ uint16_t cvt_f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// NaN codes of a word: 0x80 in each such byte.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 __device__ __forceinline__ void raise_error(int* err, unsigned bits) {
   if (err) atomicOr((unsigned*)err, bits);
 }

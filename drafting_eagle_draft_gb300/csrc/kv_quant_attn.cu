@@ -260,11 +260,6 @@ struct Queries {
   }
 };
 
-// NaN codes of a word: 0x80 in each such byte.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
 // One warp's running result over a (request, kv head): NT x 8 query rows.  O^T's fragment: head
 // dim r HD / 8 + 2 i (elements 0, 1) and the next one (2, 3), rows 2c (0, 2) and 2c + 1 (1, 3).
 template <int HD, int NT, bool F32>

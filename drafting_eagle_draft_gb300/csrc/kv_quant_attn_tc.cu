@@ -132,12 +132,8 @@ __device__ __forceinline__ void convert16(uint4 c, uint4& lo, uint4& hi) {
   cvt_e4m3x4_f16x2(c.z, hi.x, hi.y);
   cvt_e4m3x4_f16x2(c.w, hi.z, hi.w);
 }
-// NaN codes of a word: 0x80 in each such byte.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
-  return w & ~((nan_bytes(w) >> 7) * 0xffu);
+  return w & ~((nan_codes(w) >> 7) * 0xffu);
 }
 
 // Sums over the warp's lanes of 32 values a lane: lane i gets the sum of v[i].
@@ -187,9 +183,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
     if (tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // (after a wait that ran out the softmax threads look at a descriptor, perhaps one not written yet,
-  // before the vote that ends their loop: its head picks a row of row_j)
-  if (tid < DESCS) descs[tid] = TileDesc{};
   if (tid == 0) {
     s_abort = 0;
     auto init = [&](uint64_t* bar, int count, Wait w) { tc::mbar_init(bar, count + (a.stall == w)); };
@@ -427,7 +420,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
           if (x >= all_begin && x < all_end) continue;
           uint4* p = reinterpret_cast<uint4*>(const_cast<uint8_t*>(from) + src0 + i * CONV * 16);
           const uint4 w = *p;
-          if (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) {
+          if (nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)) {
             *p = make_uint4(without_nan(w.x), without_nan(w.y), without_nan(w.z), without_nan(w.w));
             nan = true;
           }
@@ -487,7 +480,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
         // the draft rows that see this thread's slot
         const int over = d.slot + key - d.len;
         const int j0 = a.causal ? over : over < 0 ? 0 : a.K, j1 = a.window > 0 ? over + a.window - 1 : a.K;
-        const uint32_t* rows = reinterpret_cast<const uint32_t*>(row_j + d.h % parts * RP + col0);
+        // (unsigned: in row_j whatever a descriptor that a wait ran out on holds)
+        const unsigned part = (unsigned)d.h % (unsigned)parts;
+        const uint32_t* rows = reinterpret_cast<const uint32_t*>(row_j + part * RP + col0);
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
           const uint32_t w = rows[c / 4];
@@ -625,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_quant_tc_kernel(AttnQuantA
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  if (nan_bytes(w[i / 4]) >> (8 * (i % 4)) & 0x80) o[i] = NAN;
+                  if (nan_codes(w[i / 4]) >> (8 * (i % 4)) & 0x80) o[i] = NAN;
               }
             }
             if (out) {
