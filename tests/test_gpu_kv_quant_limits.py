@@ -243,3 +243,21 @@ def test_one_token_of_a_fused_projection_beside_a_contiguous_one():
         f = torch.randn(B, 2, 3 * H, hd, device="cuda")
         m.peagle_append_kv_quant(c.kv, B, ints([5]), None, f[:, :, :H], f[:, :, :H].contiguous(), 2,
                                  layer=0, n_extra=2)
+
+
+def test_queries_and_output_side_by_side():
+    """An output directly before and behind the queries' span is apart from it."""
+    m = pk()
+    B, K, nq, hd = 2, 3, 4, 64
+    c = Cache(1, B, 2, 64, hd, 32, 5)
+    lens = [7, 40]
+    buf = torch.zeros(3, B * K, nq, hd, dtype=torch.bfloat16, device="cuda")
+    buf[1] = queries(B, K, nq, hd, "bf16", 3)
+    want, _ = attend(c, 0, buf[1].clone(), lens, K)
+    work = torch.empty(m.peagle_decode_attention_quant_workspace(c.kv, B, K, nq), dtype=torch.uint8,
+                       device="cuda")
+    for i in (0, 2):
+        m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, buf[1], ints(lens), buf[i], work)
+        assert torch.equal(buf[i], want)
+    with pytest.raises(m.PeagleError):
+        m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, buf[1], ints(lens), buf[1], work)

@@ -144,3 +144,17 @@ def test_attention_refuses_a_scale_that_log2_e_makes_infinite(pk):  # noqa: F811
     for scale in (2.5e38, -3e38):
         assert L.peagle_decode_attention_quant(kv, 0, 3, 2, 4, A, pk.PEAGLE_BF16, 0, A, 1, 0, scale, A,
                                                None, A, 1 << 40, None) == pk.PEAGLE_ERR_INVALID
+
+
+def test_attention_refuses_an_output_over_its_queries(pk):  # noqa: F811
+    L, kv, row = pk.lib(), _kv(pk), 4 * 64 * 2  # six rows of four heads of 64, bf16
+    bad = pk.PEAGLE_ERR_INVALID
+
+    def call(out, stride=0):
+        return L.peagle_decode_attention_quant(kv, 0, 3, 2, 4, A, pk.PEAGLE_BF16, stride, A, 1, 0, 0.125,
+                                               out, None, A, 1 << 40, None)
+
+    for out in (A, A + 16, A + 6 * row - 16, A - 6 * row + 16):
+        assert call(out) == bad
+    # three halves of a row apart, and half a row backwards
+    assert call(A + 8 * row, 3 * 4 * 64 // 2) == bad and call(A - 5 * row, -4 * 64 // 2) == bad
