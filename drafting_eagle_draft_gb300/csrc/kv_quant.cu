@@ -498,7 +498,7 @@ extern "C" int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, in
   if (rc != PEAGLE_OK) return rc;
   rc = check_rows(out);
   if (rc != PEAGLE_OK) return rc;
-  if (!counts || n_max < 1 || n_max > (1 << 30)) return PEAGLE_ERR_INVALID;
+  if (!counts || out->k == out->v || n_max < 1 || n_max > (1 << 30)) return PEAGLE_ERR_INVALID;
   const bool f32 = out->dtype == PEAGLE_F32;
   // n_max rows' pieces; counts are on the device
   const int64_t pieces = (int64_t)n_max * kv->head_dim / (f32 ? 4 : 8);

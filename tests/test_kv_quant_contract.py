@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import kv_quant_oracle as Q
-from test_oracle_kv_quant import A, CACHE, _kv, pk  # noqa: F401 (pk: fixture)
+from test_oracle_kv_quant import A, CACHE, _kv, _rows, pk  # noqa: F401 (pk: fixture)
 
 
 def test_a_dropped_draft_rounds_committed_slots_unless_they_are_restored():
@@ -158,3 +158,8 @@ def test_attention_refuses_an_output_over_its_queries(pk):  # noqa: F811
         assert call(out) == bad
     # three halves of a row apart, and half a row backwards
     assert call(A + 8 * row, 3 * 4 * 64 // 2) == bad and call(A - 5 * row, -4 * 64 // 2) == bad
+
+
+def test_read_refuses_keys_and_values_into_the_same_rows(pk):  # noqa: F811
+    assert pk.lib().peagle_read_kv_quant(_kv(pk), -1, 3, None, A, _rows(pk), 4,
+                                         None) == pk.PEAGLE_ERR_INVALID
