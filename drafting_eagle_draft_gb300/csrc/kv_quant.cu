@@ -99,10 +99,12 @@ __device__ __forceinline__ unsigned finite(unsigned bits) { return bits < 0x7f80
 // an SM) hide the chain length -> rows -> maximum -> codes.  Counts are on the device, so CTAs for the
 // longest request find the others ended: with LOOP a CTA goes on to the blocks `stride` further on, and
 // there are a quarter as many.  Four prompts of 1001 .. 8192 bf16 tokens in 4 layers of 8 heads of 128:
-// 80.6 us, 5.6 TB/s of the bytes they cannot do without (83 % of the measured copy rate), 87 without
-// LOOP; 16 such prompts 291 (91 %) and 343, four in fp32 115 (96 %) and 135.  (Before LOOP: 99 with
+// 78.8 us, 5.7 TB/s of the bytes they cannot do without (84 % of the measured copy rate), 85 without
+// LOOP; 16 such prompts 290 (92 %) and 343, four in fp32 114 (97 %) and 134.  (Before LOOP: 99 with
 // U = 2, 103 with 3 CTAs an SM.)  A draft block is bound by latency, and U = 2 spreads its units over
-// more CTAs.
+// more CTAs.  A few rows of many requests are bound by the waves of CTAs: 1 .. 6 rows of 16 requests
+// in 4 layers of 8 heads of 128, blocks of 64, are 1024 CTAs of 512 threads, 304 of them at a time,
+// and each second one returns after it has read a length (7.6 us in a graph).
 // APPEND_MANY: the CTAs, 16 rounds of those that an SM holds, from which on LOOP pays; one prompt of
 // 2048 tokens in 4 layers of 8 heads of 128 takes 17.8 us with it and 13.1 without.
 constexpr int APPEND_MANY = 16 * 4 * 152;
@@ -309,15 +311,16 @@ struct Codes<float> {
 constexpr int READ_THREADS = 256, READ_UNROLL = 4;
 // CTAs (8 an SM are in flight) from which on LOOP pays: there are a quarter as many then, and fewer
 // find their request shorter than the longest.  16 requests of 1024 .. 8192 slots in 4 layers of 8
-// heads of 128 take 266 us with it and 300 without, one of 4096 in 4 layers of 8 heads of 64 10.5 and
-// 9.7.
+// heads of 128 take 264 us with it and 269 without, to fp32 446 and 474; one of 4096 in 4 layers of 8
+// heads of 64 10.5 and 9.7.
 constexpr int READ_MANY = 16 * 8 * 152;
 
 // A CTA reads READ_THREADS x READ_UNROLL pieces of one (layer, request, kv head), keys or values, and
 // with LOOP those `stride` rows further on too: a piece is 16 bytes of row elements, so every store is
 // a full one and consecutive threads' loads and stores are consecutive.  Bound by memory: 16 requests
-// of 1024 .. 8192 slots in 4 layers of 8 heads of 128 to bf16 take 264 us, 6.85 TB/s (101 % of the
-// measured copy rate).
+// of 1024 .. 8192 slots in 4 layers of 8 heads of 128 to bf16 take 264 us, 6.86 TB/s (101 % of the
+// measured copy rate), to fp32 446 us (100 %); 4096 slots of one in 4 layers of 8 heads of 64 9.7 us
+// (76 %) and 15.1 (82 %) in a graph.
 template <int HD, bool LOOP, typename T>
 __global__ void __launch_bounds__(READ_THREADS)
     read_quant_kernel(CacheArgs c, RowsArgs rows, int block_shift, const int* starts,

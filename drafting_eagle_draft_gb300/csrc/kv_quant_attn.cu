@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_quant_kernel(AttnQuantArgs a) 
 // (they are in L2), so a warp has up to 8 of them in flight and goes over them once, and by the start
 // of the blocks that find nothing to join: four warps a block, whatever the split.  With 8 heads and
 // more (about 19 pieces a head at most) one warp a column takes less time, 20 query rows of 16 requests
-// 51.3 us with the first kernel for 54.9; one head of 16416 slots 10.2 with four for 16.9.  Also
+// 53.1 us with the first kernel for 57.0; one head of 16416 slots 10.4 with four for 16.1.  Also
 // writes the rows of requests no row of which sees a slot.  ROWS: outputs lie row by row, a lane's
 // float4 is four head dims of one row; else as fragments (struct Running).
 template <int HD, typename T, bool ROWS, int JOIN_WARPS>

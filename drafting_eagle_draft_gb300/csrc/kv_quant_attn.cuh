@@ -24,8 +24,8 @@ constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no s
 // for bf16 queries over 131072 slots, and all of it where one slot outweighs a long flat tail.  A
 // SHIFT of -4 (room for growth of 2^19) took 1 .. 8 % less time, but one slot 15 nats above
 // 32768 others of 256 times its value came out 72 % too small.  The price of 2^9 of room is that
-// references move more often: 64 requests of 300 .. 4100 slots with 64 query rows (tcgen05) 108.9 us
-// in a graph for 100.9, 16 of 1024 .. 8192 with 20 rows 53.2 for 51.2, long contexts the same.  (2^10:
+// references move more often: 64 requests of 300 .. 4100 slots with 64 query rows (tcgen05) 109.2 us
+// in a graph for 100.9, 16 of 1024 .. 8192 with 20 rows 53.1 for 51.2, long contexts the same.  (2^10:
 // 114.1 and 55.3; 2^13: 118.2 and 57.6.)  The second part of an fp32 weight needs the range below its
 // first, so there the largest is put at 2^13.
 constexpr float SHIFT_BF16 = 6.f, SHIFT_F32 = 13.f, LIM = 15.f;

@@ -514,9 +514,9 @@ int64_t peagle_save_kv_quant_bytes(const peagle_kv_quant* kv);
  * a peagle_kv cache): row t of request b is slot starts[b] + t (starts NULL: 0), t <
  * counts[b] (0 .. n_max); rows from counts[b] on are left as they are.  code x scale is
  * computed in fp32 and rounded to the rows' type (both exact for the scales that
- * peagle_append_kv_quant writes).  layer as above.  Rows of `out` do not overlap one another, nor keys values.  Out of range:
- * counts[b] outside 0 .. n_max is BAD_COMMIT, starts[b] < 0 or starts[b] + counts[b] >
- * capacity KV_OVERFLOW; that request's rows are left as they are. */
+ * peagle_append_kv_quant writes).  layer as above.  Rows of `out` do not overlap one another,
+ * nor keys values.  Out of range: counts[b] outside 0 .. n_max is BAD_COMMIT, starts[b] < 0 or
+ * starts[b] + counts[b] > capacity KV_OVERFLOW; that request's rows are left as they are. */
 int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch,
                          const int32_t* starts, const int32_t* counts,
                          const peagle_kv_rows* out, int32_t n_max, void* stream);
