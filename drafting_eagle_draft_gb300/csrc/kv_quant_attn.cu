@@ -1027,9 +1027,11 @@ extern "C" int peagle_decode_attention_quant(const peagle_kv_quant* kv, int32_t 
   const bool f32 = dtype == PEAGLE_F32;
   // (out is written while other heads' queries are still to be read)
   const int64_t size = f32 ? 4 : 2, row = (int64_t)n_q_heads * hd * size, rows = (int64_t)batch * K;
-  const int64_t last = (rows - 1) * (q_stride ? q_stride * size : row);
-  const intptr_t q0 = (intptr_t)q + (last < 0 ? last : 0), q1 = (intptr_t)q + (last < 0 ? 0 : last) + row;
-  if (q0 < (intptr_t)out + rows * row && (intptr_t)out < q1) return PEAGLE_ERR_INVALID;
+  const int64_t step = q_stride ? q_stride * size : row, apart = step < 0 ? -step : step;
+  const int64_t to = (int64_t)(intptr_t)out;
+  const int64_t q0 = (int64_t)(intptr_t)q + (step < 0 ? (rows - 1) * step : 0);
+  const int64_t first = to - row < q0 ? 0 : (to - row - q0) / apart + 1;  // row that ends behind `to`
+  if (first < rows && q0 + first * apart < to + rows * row) return PEAGLE_ERR_INVALID;
   const int64_t unit = (int64_t)layer * kv->batch * kv->n_kv_heads;
   AttnQuantArgs a;
   a.k = (const uint8_t*)kv->k + unit * kv->capacity * hd;

@@ -21,8 +21,8 @@ constexpr float NO_REF = -3.0e38f;  // the reference of a row that has seen no s
 // A reference puts the largest weight at 2^SHIFT, and it may grow to 2^LIM before the reference moves
 // (f16 ends at 2^16).  Below 2^-14 weights lose bits of their 11 and below 2^-25 all of them, while
 // the sum of weights keeps them: n slots lose at most n 2^-(25 + SHIFT) of the largest weight, 2^-14
-// for bf16 queries over 131072 slots, and all of it where one slot outweighs a long flat tail.  A
-// SHIFT of -4 (room for growth of 2^19) took 1 .. 8 % less time, but one slot 15 nats above
+// for bf16 queries over 131072 slots.  Where one slot outweighs a long flat tail, that is the tail's
+// share: a SHIFT of -4 (room for growth of 2^19) took 1 .. 8 % less time, but one slot 15 nats above
 // 32768 others of 256 times its value came out 72 % too small.  The price of 2^9 of room is that
 // references move more often: 64 requests of 300 .. 4100 slots with 64 query rows (tcgen05) 109.2 us
 // in a graph for 100.9, 16 of 1024 .. 8192 with 20 rows 53.1 for 51.2, long contexts the same.  (2^10:

@@ -526,7 +526,7 @@ int peagle_read_kv_quant(const peagle_kv_quant* kv, int32_t layer, int32_t batch
  * h / (n_q_heads / n_kv_heads) that the row sees.
  *   q, out    device [batch*K][n_q_heads][head_dim] of type dtype (peagle_dtype); consecutive
  *             rows of q are q_stride elements apart (0: n_q_heads * head_dim), out is
- *             contiguous and lies outside of the span of q's rows; both 16-byte aligned,
+ *             contiguous and apart from q's rows; both 16-byte aligned,
  *             q_stride a multiple of 16 bytes.  q is taken as already rotated.
  *   seq_lens  device int32 [batch]
  *   causal    1: row j sees the slots 0 .. seq_lens[b] + j (the draft block's rows are in the

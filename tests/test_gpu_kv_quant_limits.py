@@ -261,3 +261,12 @@ def test_queries_and_output_side_by_side():
         assert torch.equal(buf[i], want)
     with pytest.raises(m.PeagleError):
         m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, buf[1], ints(lens), buf[1], work)
+    # rows so far apart that an output lies between two of them
+    far = torch.zeros(B * K, 1 + B * K, nq, hd, dtype=torch.bfloat16, device="cuda")
+    far[:, 0] = buf[1]
+    for i in range(B * K):
+        m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, far[:, 0], ints(lens), far[i, 1:], work)
+        assert torch.equal(far[i, 1:], want) and torch.equal(far[:, 0], buf[1])
+    for out in (far.flatten(0, 1)[2:2 + B * K], far.flatten(0, 1)[B * K:2 * B * K]):
+        with pytest.raises(m.PeagleError):
+            m.peagle_decode_attention_quant(c.kv, 0, B, K, nq, far[:, 0], ints(lens), out, work)
