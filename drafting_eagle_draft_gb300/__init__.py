@@ -42,6 +42,7 @@ EXPORTS = ("peagle_create", "peagle_draft", "peagle_catch_up", "peagle_verify_gr
            "peagle_restore_kv_quant", "peagle_save_kv_quant_bytes",
            "peagle_decode_attention_quant", "peagle_decode_attention_quant_workspace",
            "peagle_set_wait_limit_quant",
+           "peagle_sample", "peagle_verify_sample", "peagle_verify_sample_workspace",
            "peagle_device_error_bits", "peagle_strerror", "peagle_destroy")
 STAGES = ("fc", "qkv", "attn", "oproj", "gate_up", "down", "lm_head", "norm", "small")
 
@@ -93,6 +94,15 @@ class PeagleKVRows(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("layer_stride", _i64), ("batch_stride", _i64),
                 ("token_stride", _i64), ("head_stride", _i64), ("dtype", _i32)]
 
+
+class PeagleSampling(ctypes.Structure):
+    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp),
+                ("rows_per", _i32)]
+    _device = None  # of its arrays, and how many rows they serve (sampling_struct)
+    _entries = None
+
+
+DIST_BYTES = 32  # of a peagle_dist
 
 _LIB = None
 
@@ -148,6 +158,13 @@ def lib():
                                                               _i32, _i32]
         L.peagle_decode_attention_quant_workspace.restype = _i64
         L.peagle_set_wait_limit_quant.argtypes = [ctypes.c_uint64, _i32]
+        L.peagle_sample.argtypes = [ctypes.POINTER(PeagleSampling), _i32, _i32, _vp, _i32, _i64,
+                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+        L.peagle_verify_sample.argtypes = [_i32, _i32, _vp, ctypes.POINTER(PeagleSampling), _i32,
+                                           _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _vp, _i64, _vp]
+        L.peagle_verify_sample_workspace.argtypes = [_i32, _i32, _i32]
+        L.peagle_verify_sample_workspace.restype = _i64
         L.peagle_read_timing.argtypes = [_vp, _vp, _vp]
         L.peagle_read_pass_trace.argtypes = [_vp, _vp, _i32, _vp, _vp]
         L.peagle_read_pass_trace.restype = _i32
@@ -657,6 +674,139 @@ def peagle_set_wait_limit_quant(limit_ns: int, unreachable_wait: int = -1):
     _refuse_wide("peagle_set_wait_limit_quant", unreachable_wait=unreachable_wait)
     _check(lib().peagle_set_wait_limit_quant(int(limit_ns), int(unreachable_wait)),
            "peagle_set_wait_limit_quant")
+
+
+def sampling_struct(temperature=None, top_k=None, top_p=None, min_p=None,
+                    rows_per=1) -> PeagleSampling:
+    """PeagleSampling over contiguous CUDA tensors of one length (int32 top_k, float32 the others;
+    None: off), an entry for each `rows_per` consecutive rows; the struct keeps them alive."""
+    what = "sampling_struct"
+    if torch is None:
+        _import_torch()
+    if not 0 < rows_per < _END:
+        _refuse(what, f"rows_per = {rows_per}")
+    st = PeagleSampling(rows_per=rows_per)
+    for name, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p),
+                    ("min_p", min_p)):
+        if t is None:
+            continue
+        if st._device is None:
+            st._device, st._entries = t.device, t.numel()
+        if not t.is_contiguous() or t.numel() != st._entries:
+            _refuse(what, "contiguous tensors of one length are wanted")
+        setattr(st, name, _on(t, st._device, torch.int32 if name == "top_k" else torch.float32,
+                              what))
+    st._keep = (temperature, top_k, top_p, min_p)
+    return st
+
+
+def sample_dist(rows, device):
+    """A buffer of `rows` records (peagle_dist) for peagle_sample and peagle_verify_sample."""
+    if torch is None:
+        _import_torch()
+    return torch.zeros(rows, DIST_BYTES, dtype=torch.uint8, device=device)
+
+
+def _flat(t, count, dev, dtype, what, name, optional=False):
+    """The pointer of a contiguous tensor of at least `count` elements."""
+    if t is None:
+        if optional:
+            return None
+        _refuse(what, f"{name} is wanted")
+    if t.dtype is not dtype or t.device != dev or t.numel() < count or not t.is_contiguous():
+        _refuse(what, f"{name}: {count} contiguous {dtype} on {dev} are wanted")
+    return t.data_ptr()
+
+
+def _logit_rows(logits, how, what, stream):
+    """The stream, and dtype, rows, vocab and row stride of a block of logits [rows, vocab]."""
+    if torch is None:
+        _import_torch()
+    dt, dev, sh, sd = logits.dtype, logits.device, logits.shape, logits.stride()
+    if dt is torch.float32:
+        code = PEAGLE_F32
+    elif dt is torch.bfloat16:
+        code = PEAGLE_BF16
+    else:
+        _refuse(what, f"logits are float32 or bfloat16, got {dt}")
+    if len(sh) != 2 or (sh[1] > 1 and sd[1] != 1) or (sh[0] > 1 and sd[0] < sh[1]):
+        _refuse(what, f"logits are [rows, vocab], a row contiguous; got {tuple(sh)}, strides {sd}")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(what, f"the logits are on {dev}, which is not the current CUDA device")
+    if how is not None and how._device is not None and (
+            how._device != dev or how._entries * how.rows_per < sh[0]):
+        _refuse(what, f"the settings serve {how._entries * how.rows_per} rows on {how._device}")
+    if stream is None and _raw_stream is not None:
+        s = _raw_stream(dev.index)
+    else:
+        s = _stream_ptr(stream)
+    return s, dev, code, sh[0], sh[1], sd[0] if sh[0] > 1 else 0
+
+
+def peagle_sample(how, logits, uniforms, out_tokens, d2t=None, out_prob=None, out_dist=None,
+                  errors=None, stream=None):
+    """Draw a token from each row of logits (include/peagle.h).  how: a sampling_struct, or None;
+    logits: float32 or bfloat16 [rows, vocab], rows contiguous; uniforms, out_prob float32 [rows],
+    out_tokens int32 [rows], d2t int32 [vocab]; out_dist: sample_dist(rows, device)."""
+    what = "peagle_sample"
+    s, dev, code, rows, vocab, stride = _logit_rows(logits, how, what, stream)
+    i32, f32 = torch.int32, torch.float32
+    rc = lib().peagle_sample(
+        how, rows, vocab, logits.data_ptr(), code, stride,
+        _flat(uniforms, rows, dev, f32, what, "uniforms"),
+        _flat(d2t, vocab, dev, i32, what, "d2t", True),
+        _flat(out_tokens, rows, dev, i32, what, "out_tokens"),
+        _flat(out_prob, rows, dev, f32, what, "out_prob", True),
+        _flat(out_dist, rows * DIST_BYTES, dev, torch.uint8, what, "out_dist", True),
+        _flat(errors, 1, dev, i32, what, "errors", True), s)
+    if rc:
+        raise PeagleError(rc, what)
+
+
+def peagle_verify_sample_workspace(batch, K, vocab) -> int:
+    """Bytes of workspace of peagle_verify_sample (include/peagle.h)."""
+    _refuse_wide("peagle_verify_sample_workspace", batch=batch, K=K, vocab=vocab)
+    n = lib().peagle_verify_sample_workspace(batch, K, vocab)
+    if n < 0:
+        raise PeagleError(n, "peagle_verify_sample_workspace")
+    return n
+
+
+def peagle_verify_sample(batch, K, draft_tokens, how, target_logits, u_accept, u_bonus,
+                         out_accept_len, out_bonus, workspace, draft_logits=None, draft_dist=None,
+                         d2t=None, out_accept_prob=None, errors=None, stream=None):
+    """Accept sampled drafts or replace them (include/peagle.h).  target_logits: float32 or
+    bfloat16 [batch * (K + 1), vocab]; draft_logits float32 [batch * K, draft_vocab] with
+    draft_dist, the records that peagle_sample left, or neither (drafts that were not drawn)."""
+    what = "peagle_verify_sample"
+    s, dev, code, rows, vocab, stride = _logit_rows(target_logits, how, what, stream)
+    _refuse_wide(what, batch=batch, K=K)
+    if rows != batch * (K + 1):
+        _refuse(what, f"target_logits has {rows} rows, not batch * (K + 1) = {batch * (K + 1)}")
+    i32, f32, drafts, dv = torch.int32, torch.float32, batch * K, 0
+    if (draft_logits is None) != (draft_dist is None):
+        _refuse(what, "draft_logits and draft_dist belong together")
+    if draft_logits is not None:
+        if draft_logits.dim() != 2 or draft_logits.shape[0] != drafts:
+            _refuse(what, f"draft_logits is [{drafts}, draft_vocab]")
+        dv = draft_logits.shape[1]
+    if not workspace.is_contiguous() or workspace.device != dev:
+        _refuse(what, f"a contiguous workspace on {dev} is wanted")
+    rc = lib().peagle_verify_sample(
+        batch, K, _flat(draft_tokens, drafts, dev, i32, what, "draft_tokens"), how, vocab,
+        target_logits.data_ptr(), code, stride, dv,
+        _flat(draft_logits, drafts * dv, dev, f32, what, "draft_logits", True),
+        _flat(draft_dist, drafts * DIST_BYTES, dev, torch.uint8, what, "draft_dist", True),
+        _flat(d2t, dv, dev, i32, what, "d2t", True),
+        _flat(u_accept, drafts, dev, f32, what, "u_accept"),
+        _flat(u_bonus, batch, dev, f32, what, "u_bonus"),
+        _flat(out_accept_len, batch, dev, i32, what, "out_accept_len"),
+        _flat(out_bonus, batch, dev, i32, what, "out_bonus"),
+        _flat(out_accept_prob, drafts, dev, f32, what, "out_accept_prob", True),
+        _flat(errors, 1, dev, i32, what, "errors", True), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s)
+    if rc:
+        raise PeagleError(rc, what)
 
 
 def peagle_device_error_bits(ctx: Context) -> int:

@@ -1,0 +1,569 @@
+// Sampling from rows of logits with temperature, top-k, top-p and min-p (peagle_sample), and the
+// records of the rows' distributions that stochastic verification reads.
+//
+// A cluster of 1, 2, 4 or 8 CTAs takes a row.  Each CTA brings its chunk of the row into shared memory
+// once (asynchronous 16-byte copies; the largest logit is found as they arrive) and all further
+// passes run there:
+//   cut       only with top-k or top-p: a histogram of the chunk over y = (x - M) log2(e) / T in steps
+//             of 1/8, counts and weights (16-bit parts of the weights, so that 32-bit additions
+//             hold), summed over the cluster; the bin in which the k-th token, or the top_p-th part
+//             of the mass, lies is gathered into a list and ranked, or divided again by the logits'
+//             own order while it holds more than LIST tokens
+//   sums      the kept tokens' weights, a sum for each warp's span of the row
+//   locate    the span in which u S falls, divided again over one CTA's warps
+// Sums are whole numbers (sample.cuh), so nothing depends on their order.
+#include "sample.cuh"
+
+namespace peagle {
+namespace smp {
+
+namespace {
+
+constexpr int BINS = THREADS;  // one a thread in the cluster's sum
+constexpr int LIST = 256;
+
+struct Args {
+  const void* logits;
+  int64_t stride;
+  int vocab, chunk;  // chunk: logits a CTA
+  const float* temperature;
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  int rows_per;
+  const float* u;  // NULL: records only
+  const int* d2t;
+  int* token;
+  float* prob;
+  peagle_dist* dist;
+  int* errors;
+};
+
+struct Shared {
+  union {
+    uint4 hist[BINS];    // count, and three 16-bit parts of the weights
+    struct {             // (of a bin that is not divided again)
+      u64 list[LIST];    // key and index of the boundary bin's tokens: this CTA's
+      u64 all[LIST];     // the cluster's
+      u64 weight[LIST];
+    };
+  };
+  u64 red64[WARPS];
+  uint32_t red32[WARPS];
+  Locate find;
+  uint32_t top, bad;     // this CTA's largest key, and whether it holds a NaN or +inf
+  uint32_t count, low, high;  // of the list; smallest and largest key in the boundary bin
+  uint32_t first;        // lowest index of the largest logit
+  // what one thread finds for all
+  int bin;
+  uint32_t before_n, in_n;
+  u64 before_w, in_w;
+  uint32_t least;        // the border: tokens below it are cut
+  int last;
+  u64 kept_w;            // weights above it
+  int first_bin;         // the bin over y that the last cut went through, and what lies before it
+  u64 first_before;
+};
+
+template <typename T>
+struct Row {
+  const T* x;  // this CTA's chunk, in shared memory
+  int n, base;
+};
+
+template <typename T>
+__device__ __forceinline__ void see(T raw, float& top, bool& bad) {
+  const float x = to_f32(raw);
+  top = fmaxf(top, x);
+  bad |= !(x < INFINITY);
+}
+
+// Until at most `left` groups of this thread's copies are in flight.
+__device__ __forceinline__ void wait_copies(int left) {
+  if (left == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Copies n logits from src into shared memory at the same place within 16 bytes, and finds the
+// largest and whether one is not a number (or +inf).
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* src, T* dst, int n, float& top, bool& bad) {
+  constexpr int PER = 16 / sizeof(T), GROUPS = 4;
+  const int tid = threadIdx.x;
+  const int phase = (int)(((uintptr_t)src & 15) / sizeof(T));
+  const int head = min(n, phase ? PER - phase : 0);
+  const int vecs = (n - head) / PER, tail = n - head - vecs * PER;
+  const int per = ((vecs + GROUPS - 1) / GROUPS + THREADS - 1) / THREADS * THREADS;
+  const T* s = src + head;
+  T* d = dst + head;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(d + v * PER)),
+                   "l"(s + v * PER)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  if (tid < head) see(dst[tid] = src[tid], top, bad);
+  if (tid < tail) see(d[vecs * PER + tid] = s[vecs * PER + tid], top, bad);
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    wait_copies(GROUPS - 1 - g);
+    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS) {
+      T piece[PER];
+      *reinterpret_cast<uint4*>(piece) = *reinterpret_cast<const uint4*>(d + v * PER);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) see(piece[k], top, bad);
+    }
+  }
+}
+
+__device__ __forceinline__ int bin_of(float x, const Scale& s) {
+  const float y = exponent(x, s);
+  return y > -(BINS - 1) / 8.f ? (int)(y * -8.f) : BINS - 1;
+}
+
+// Adds up the cluster's histograms; thread t gets bin t.
+__device__ __forceinline__ void merge_bins(Shared& sh, int ctas, uint32_t& n, u64& w) {
+  n = 0;
+  w = 0;
+  for (int c = 0; c < ctas; ++c) {
+    const uint4 h = remote_u128(&sh.hist[threadIdx.x], c);
+    n += h.x;
+    w += (u64)h.y + ((u64)h.z << 16) + ((u64)h.w << 32);
+  }
+}
+
+// Finds the first bin at which the running count reaches `want_n` (by_count), or the running weight
+// want_w, and what lies before and in it (into sh; the last bin if none does).
+__device__ __forceinline__ void find_bin(Shared& sh, uint32_t n, u64 w, bool by_count, uint32_t want_n,
+                                         u64 want_w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  u64 wi = warp_scan64(w, lane);
+  uint32_t ni = (uint32_t)warp_scan64(n, lane);
+  __syncthreads();
+  if (lane == 31) {
+    sh.red64[warp] = wi;
+    sh.red32[warp] = ni;
+  }
+  __syncthreads();
+  for (int k = 0; k < warp; ++k) {
+    wi += sh.red64[k];
+    ni += sh.red32[k];
+  }
+  const bool reached = by_count ? ni >= want_n : wi >= want_w;
+  const bool before = by_count ? ni - n >= want_n : wi - w >= want_w;
+  if ((reached && !before) || (tid == BINS - 1 && !reached)) {
+    sh.bin = tid;
+    sh.before_n = ni - n;
+    sh.before_w = wi - w;
+    sh.in_n = n;
+    sh.in_w = w;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void add_bin(uint4* h, u64 w, bool weigh) {
+  atomicAdd(&h->x, 1u);
+  if (weigh && w) {
+    atomicAdd(&h->y, (uint32_t)w & 0xffffu);
+    atomicAdd(&h->z, (uint32_t)(w >> 16) & 0xffffu);
+    atomicAdd(&h->w, (uint32_t)(w >> 32));
+  }
+}
+
+// Cuts the row's order (larger logits first, then lower indices): keeps the first want_n tokens
+// (by_count), or the shortest prefix whose weights reach want_w.  n, w: the merged histogram over
+// y of the tokens that are kept so far (sh.least, sh.last).  Leaves the border in sh.least and
+// sh.last and the kept weights in sh.kept_w.
+template <typename T>
+__device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& tab, int ctas, bool weigh,
+                    bool by_count, uint32_t want_n, u64 want_w, uint32_t n, u64 w) {
+  const int tid = threadIdx.x;
+  find_bin(sh, n, w, by_count, want_n, want_w);
+  const int bin = sh.bin;
+  const uint32_t old_least = sh.least;
+  const int old_last = sh.last;
+  uint32_t before_n = sh.before_n, in_n = sh.in_n;
+  u64 before_w = sh.before_w;
+  if (tid == 0) {
+    sh.first_bin = bin;
+    sh.first_before = before_w;
+  }
+  uint32_t low = 0, high = 0xffffffffu;  // the boundary set: bin, and keys low .. high
+  bool ranged = false;
+  while (true) {
+    const bool listed = in_n <= LIST;
+    const bool divide = !listed && ranged;
+    const int shift = divide ? max(0, 32 - __clz(high - low) - 9) : 0;
+    if (divide && low == high) break;  // equal logits
+    __syncthreads();
+    cluster_barrier();  // (the buffers below are read no more)
+    if (tid == 0) {
+      sh.count = 0;
+      sh.low = 0xffffffffu;
+      sh.high = 0;
+    }
+    if (divide) sh.hist[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    uint32_t lo = 0xffffffffu, hi = 0;
+    for (int i = tid & ~31; i < row.n; i += THREADS) {
+      const int at = i + (tid & 31);
+      const float x = at < row.n ? to_f32(row.x[at]) : -INFINITY;
+      const uint32_t key = order_key(x);
+      const bool in = at < row.n && bin_of(x, s) == bin && key >= low && key <= high &&
+                      kept(key, row.base + at, old_least, old_last);
+      if (!__any_sync(0xffffffffu, in)) continue;
+      const u64 wx = divide && weigh ? weight(x, s, tab) : 0;
+      if (in) {
+        lo = min(lo, key);
+        hi = max(hi, key);
+        if (listed)
+          sh.list[atomicAdd(&sh.count, 1u)] = (u64)key << 32 | (0xffffffffu - (uint32_t)(row.base + at));
+        else if (divide)
+          add_bin(&sh.hist[(high - key) >> shift], wx, weigh);
+        else
+          atomicAdd(&sh.count, 1u);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if ((tid & 31) == 0) {
+      atomicMin(&sh.low, lo);
+      atomicMax(&sh.high, hi);
+    }
+    __syncthreads();
+    cluster_barrier();
+    if (listed) {
+      // every CTA has the whole list, and ranks it
+      int at = 0;
+      for (int c = 0; c < ctas; ++c) {
+        const int m = (int)remote_u32(&sh.count, c);
+        if (tid < m) sh.all[at + tid] = remote_u64(&sh.list[tid], c);
+        at += m;
+      }
+      __syncthreads();
+      const u64 me = tid < at ? sh.all[tid] : 0;
+      u64 mine = 0;
+      if (weigh && tid < ((at + 31) & ~31)) {
+        const uint32_t key = (uint32_t)(me >> 32);
+        mine = weight(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab);
+        if (tid < at) sh.weight[tid] = mine;
+      }
+      __syncthreads();
+      if (tid < at) {
+        uint32_t rank = 0;
+        u64 above = 0;
+        for (int k = 0; k < at; ++k) {
+          const bool more = sh.all[k] > me;
+          rank += more;
+          if (weigh) above += more ? sh.weight[k] : 0;
+        }
+        // the last that is kept: it is, and the next is not (the first always is)
+        const bool is = by_count ? before_n + rank < want_n : before_w + above < want_w;
+        const bool next = by_count ? before_n + rank + 1 < want_n : before_w + above + mine < want_w;
+        if ((is || rank == 0) && (!next || rank == at - 1)) {
+          sh.least = (uint32_t)(me >> 32);
+          sh.last = (int)(0xffffffffu - (uint32_t)me);
+          sh.kept_w = before_w + above + mine;
+        }
+      }
+      __syncthreads();
+      return;
+    }
+    if (!divide) {  // the bin's own range of logits, to be divided
+      low = 0xffffffffu;
+      high = in_n = 0;
+      for (int c = 0; c < ctas; ++c) {
+        in_n += remote_u32(&sh.count, c);
+        low = min(low, remote_u32(&sh.low, c));
+        high = max(high, remote_u32(&sh.high, c));
+      }
+      ranged = true;
+      continue;
+    }
+    merge_bins(sh, ctas, n, w);
+    find_bin(sh, n, w, by_count, by_count ? want_n - before_n : 0, by_count ? 0 : want_w - before_w);
+    high -= (uint32_t)sh.bin << shift;
+    low = max(low, high - ((1u << shift) - 1u));
+    before_n += sh.before_n;
+    before_w += sh.before_w;
+    in_n = sh.in_n;
+  }
+  // in_n > LIST equal logits: so many of them, the lowest indices first
+  const float x = __uint_as_float(low & 0x80000000u ? low & 0x7fffffffu : ~low);
+  const u64 each = weigh ? weight(x, s, tab) : 0;
+  uint32_t m;
+  if (by_count) {
+    m = want_n - before_n;
+  } else {
+    const u64 rest = want_w > before_w ? want_w - before_w : 0;
+    m = each ? (uint32_t)min((u64)in_n, (rest + each - 1) / each) : in_n;
+  }
+  m = max(1u, min(m, in_n));
+  const auto tie = [&](int i) -> u64 {
+    return i < row.n && order_key(to_f32(row.x[i])) == low &&
+           kept(low, row.base + i, old_least, old_last);
+  };
+  sum_spans(sh.find, row.n, tie);
+  __syncthreads();
+  cluster_barrier();
+  const int at = locate(sh.find, ctas, row.n, (u64)(m - 1), tie);
+  if (at >= 0 && (tid & 31) == 0) {
+    sh.first = (uint32_t)(row.base + at);
+  }
+  __syncthreads();
+  cluster_barrier();
+  if (tid == 0) {
+    sh.least = low;
+    sh.last = (int)remote_u32(&sh.first, sh.find.cta);
+    sh.kept_w = before_w + each * m;
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
+  extern __shared__ uint4 dynamic[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
+  const int r = blockIdx.x / ctas, set = r / a.rows_per;
+  const int frac = frac_bits(a.vocab);
+
+  const float temperature = a.temperature ? a.temperature[set] : 1.f;
+  const int top_k = a.top_k ? a.top_k[set] : 0;
+  const float top_p = a.top_p ? a.top_p[set] : 1.f;
+  const float min_p = a.min_p ? a.min_p[set] : 0.f;
+
+  Row<T> row;
+  row.base = rank * a.chunk;
+  row.n = max(0, min(a.chunk, a.vocab - row.base));
+  const T* src = static_cast<const T*>(a.logits) + (int64_t)r * a.stride + row.base;
+  T* chunk = reinterpret_cast<T*>(reinterpret_cast<char*>(dynamic) + ((uintptr_t)src & 15));
+  row.x = chunk;
+  float top = -INFINITY;
+  bool bad = false;
+  load_chunk(src, chunk, row.n, top, bad);
+  top = warp_max(top);
+  bad = __any_sync(0xffffffffu, bad);
+  if (tid == 0) {
+    sh.top = 0;
+    sh.bad = 0;
+    sh.first = 0xffffffffu;
+    sh.least = 0;
+    sh.last = 0x7fffffff;
+  }
+  sh.hist[tid] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  if (lane == 0) {
+    atomicMax(&sh.top, order_key(top));
+    if (bad) sh.bad = 1;
+  }
+  __syncthreads();
+  cluster_barrier();
+  uint32_t top_key = 0, any_bad = 0;
+  for (int c = 0; c < ctas; ++c) {
+    top_key = max(top_key, remote_u32(&sh.top, c));
+    any_bad |= remote_u32(&sh.bad, c);
+  }
+  top = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
+  const bool whole = !any_bad && top > -INFINITY && temperature >= 0.f;
+  if (!whole) {  // no distribution
+    if (rank == 0 && tid == 0) {
+      if (a.token) a.token[r] = -1;
+      if (a.prob) a.prob[r] = NAN;
+      if (a.dist) a.dist[r] = {0ull, NAN, temperature, 0xffffffffu, -1, -1, a.vocab};
+      raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_BAD_ROW);
+    }
+    cluster_barrier();
+    return;
+  }
+  if (temperature < COLD) {  // the largest logit alone, the lowest index of it
+    uint32_t first = 0xffffffffu;
+    for (int i = tid; i < row.n && first == 0xffffffffu; i += THREADS)
+      if (order_key(to_f32(row.x[i])) == top_key) first = row.base + i;
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) atomicMin(&sh.first, first);
+    __syncthreads();
+    cluster_barrier();
+    if (rank == 0 && tid == 0) {
+      for (int c = 0; c < ctas; ++c) first = min(first, remote_u32(&sh.first, c));
+      if (a.token) a.token[r] = (int)first + (a.d2t ? a.d2t[first] : 0);
+      if (a.prob) a.prob[r] = 1.f;
+      if (a.dist) a.dist[r] = {1ull << frac, top, 0.f, top_key, (int)first, (int)first, a.vocab};
+    }
+    cluster_barrier();
+    return;
+  }
+
+  const Scale s = make_scale(top, temperature, frac);
+  const Table tab = load_table();
+  const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
+  if (by_k || by_p) {
+    u64 sum = 0;
+    for (int i = tid & ~31; i < row.n; i += THREADS) {
+      const int at = i + lane;
+      const float x = at < row.n ? to_f32(row.x[at]) : -INFINITY;
+      const u64 w = by_p ? weight(x, s, tab) : 0;
+      sum += w;
+      if (at < row.n) add_bin(&sh.hist[bin_of(x, s)], w, by_p);
+    }
+    __syncthreads();
+    cluster_barrier();
+    uint32_t n;
+    u64 w;
+    merge_bins(sh, ctas, n, w);
+    u64 mass = 0;
+    if (by_k) {
+      cut(sh, row, s, tab, ctas, by_p, true, (uint32_t)top_k, 0, n, w);
+      mass = sh.kept_w;
+    } else {
+      find_bin(sh, n, w, false, 0, ~0ull);
+      mass = sh.before_w + sh.in_w;
+    }
+    if (by_p) {
+      if (by_k) {
+        // what the first cut left of the bins
+        if (tid > sh.first_bin) n = 0, w = 0;
+        if (tid == sh.first_bin) w = mass - sh.first_before;
+      }
+      const double want = ceil((double)fmaxf(top_p, 0.f) * (double)mass);
+      const u64 want_w = max(1ull, min(mass, (u64)want));
+      cut(sh, row, s, tab, ctas, true, false, 0, want_w, n, w);
+    }
+  }
+  uint32_t least = sh.least;
+  int last = sh.last;
+  if (min_p > 0.f) {
+    const float x = __double2float_ru((double)top + (double)temperature * log((double)fminf(min_p, 1.f)));
+    const uint32_t key = order_key(fminf(x, top));
+    if (key > least) {
+      least = key;
+      last = 0x7fffffff;
+    }
+  }
+  const auto weigh = [&](int i) -> u64 {
+    const float x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
+    const bool in = i < row.n && kept(order_key(x), row.base + i, least, last);
+    if (!__any_sync(0xffffffffu, in)) return 0;
+    const u64 w = weight(x, s, tab);
+    return in ? w : 0;
+  };
+  sum_spans(sh.find, row.n, weigh);
+  __syncthreads();
+  cluster_barrier();
+  const u64 total = total_of(sh.find, ctas);
+  peagle_dist d = {total, top, temperature, least, last, -1, a.vocab};
+  if (!a.u) {
+    if (rank == 0 && tid == 0) a.dist[r] = d;
+  } else {
+    const double u = a.u[r];
+    const double want = fmax(u, 0.0) * (double)total;  // (0 for a NaN)
+    const u64 target = want < (double)total ? min((u64)want, total - 1) : total - 1;
+    const int at = locate(sh.find, ctas, row.n, target, weigh);
+    if (at >= 0 && lane == 0) {
+      const int i = row.base + at;
+      d.index = i;
+      if (a.token) a.token[r] = i + (a.d2t ? a.d2t[i] : 0);
+      if (a.prob)
+        a.prob[r] = (float)(weight64(to_f32(row.x[at]), top, temperature) * (double)(1ull << frac) / (double)total);
+      if (a.dist) a.dist[r] = d;
+    }
+  }
+  cluster_barrier();  // (the others read this CTA's sums)
+}
+
+template <typename T>
+int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
+  const size_t bytes = (size_t)a.chunk * sizeof(T) + 32;
+  if (smem_optin((const void*)sample_kernel<T>, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+// CTAs a row: as many as keep the GPU's 2 x 152 places busy once, but at least 2048 logits each, and
+// at most CHUNK bytes of them, so that two CTAs fit an SM.
+constexpr int CHUNK = 100 << 10, PLACES = 304;
+int cluster_of(int rows, int vocab, int size) {
+  int c = 1;
+  while (c < MAX_CLUSTER && ((int64_t)vocab * size > (int64_t)CHUNK * c ||
+                             (rows * 2 * c <= PLACES && vocab >= 4096 * c)))
+    c *= 2;
+  return c;
+}
+
+}  // namespace
+
+int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* logits, int dtype,
+                int64_t row_stride, const float* u, const int* d2t, int* token, float* prob,
+                peagle_dist* dist, int* errors, cudaStream_t st) {
+  Args a = {};
+  const int size = dtype == PEAGLE_F32 ? 4 : 2;
+  const int ctas = cluster_of(rows, vocab, size);
+  a.logits = logits;
+  a.stride = row_stride ? row_stride : vocab;
+  a.vocab = vocab;
+  a.chunk = cdiv(cdiv(vocab, ctas), 8) * 8;
+  if (how) {
+    a.temperature = how->temperature;
+    a.top_k = how->top_k;
+    a.top_p = how->top_p;
+    a.min_p = how->min_p;
+  }
+  a.rows_per = how && how->rows_per ? how->rows_per : 1;
+  a.u = u;
+  a.d2t = d2t;
+  a.token = token;
+  a.prob = prob;
+  a.dist = dist;
+  a.errors = errors;
+  return dtype == PEAGLE_F32 ? launch<float>(a, rows, ctas, st) : launch<bf16>(a, rows, ctas, st);
+}
+
+// What both calls refuse of a block of logits.
+int check_rows(const peagle_sampling* how, int64_t rows, int vocab, const void* logits, int dtype,
+               int64_t row_stride) {
+  if (!logits || rows < 1 || vocab < 1 || (dtype != PEAGLE_F32 && dtype != PEAGLE_BF16))
+    return PEAGLE_ERR_INVALID;
+  if ((uintptr_t)logits % (dtype == PEAGLE_F32 ? 4 : 2)) return PEAGLE_ERR_INVALID;
+  if (row_stride && row_stride < vocab) return PEAGLE_ERR_INVALID;
+  if (how) {
+    if (how->rows_per < 0) return PEAGLE_ERR_INVALID;
+    if (((uintptr_t)how->temperature | (uintptr_t)how->top_k | (uintptr_t)how->top_p |
+         (uintptr_t)how->min_p) % 4)
+      return PEAGLE_ERR_INVALID;
+  }
+  if (vocab > MAX_VOCAB || rows > MAX_ROWS) return PEAGLE_ERR_UNSUPPORTED;
+  return PEAGLE_OK;
+}
+
+}  // namespace smp
+}  // namespace peagle
+
+extern "C" int peagle_sample(const peagle_sampling* how, int32_t rows, int32_t vocab,
+                             const void* logits, int32_t dtype, int64_t row_stride,
+                             const float* uniforms, const int32_t* d2t, int32_t* out_tokens,
+                             float* out_prob, peagle_dist* out_dist, int32_t* errors,
+                             void* stream) {
+  const int rc = peagle::smp::check_rows(how, rows, vocab, logits, dtype, row_stride);
+  if (rc != PEAGLE_OK) return rc;
+  if (!uniforms || !out_tokens || (uintptr_t)uniforms % 4 || (uintptr_t)d2t % 4 ||
+      (uintptr_t)out_tokens % 4 || (uintptr_t)out_prob % 4 || (uintptr_t)out_dist % 8 ||
+      (uintptr_t)errors % 4)
+    return PEAGLE_ERR_INVALID;
+  return peagle::smp::sample_rows(how, rows, vocab, logits, dtype, row_stride, uniforms, d2t,
+                                  out_tokens, out_prob, out_dist, errors, (cudaStream_t)stream);
+}

@@ -1,0 +1,255 @@
+// What sampling and stochastic verification share: the weight of a logit, the order of logits, the
+// record of a row's distribution, and the walk of a cluster over one row.
+//
+// A row's distribution is p_i = w_i / S over the kept tokens, w_i = exp((x_i - M) / T) with M the
+// row's largest logit.  A sampled token is a whole number: it has to be the same whatever the
+// cluster's size, the order of a sum or the lanes of a warp.  So weights are whole numbers
+// too: round(w 2^F) with F as large as 64 bits allow for the vocabulary (46 at 201088), their sums
+// are exact, and the weight itself is computed to about 2^-37 of its value (fp32 would put about one
+// row in 30,000 on the other side of a border).
+#pragma once
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace peagle {
+namespace smp {
+
+typedef unsigned long long u64;
+
+// Host side (sample.cu).  u NULL: the rows' records only.
+int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* logits, int dtype,
+                int64_t row_stride, const float* u, const int* d2t, int* token, float* prob,
+                peagle_dist* dist, int* errors, cudaStream_t st);
+int check_rows(const peagle_sampling* how, int64_t rows, int vocab, const void* logits, int dtype,
+               int64_t row_stride);
+
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int MAX_VOCAB = 262144, MAX_ROWS = 1 << 24;
+constexpr int MAX_CLUSTER = 8;
+
+// Fraction bits of the weights: vocab * 2^F stays below 2^64.
+__host__ __device__ __forceinline__ int frac_bits(int vocab) {
+  int top = 0;
+  while ((vocab >> top) > 1) ++top;
+  return 63 - top < 50 ? 63 - top : 50;
+}
+
+// Logits in their order as unsigned numbers; -0 and +0 are equal.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// A temperature below this counts as 0 (the largest logit alone): 1 / T stays far inside fp32.
+constexpr float COLD = 0x1p-60f;
+
+// log2(e) / T in two floats.
+struct Scale {
+  float top, ch, cl;
+  int shift;  // 62 - F
+};
+__device__ __forceinline__ Scale make_scale(float top, float temperature, int frac) {
+  Scale s;
+  const double c = 1.4426950408889634074 / (double)temperature;
+  s.top = top;
+  s.ch = (float)c;
+  s.cl = (float)(c - (double)s.ch);
+  s.shift = 62 - frac;
+  return s;
+}
+
+// (x - M) log2(e) / T, rounded: monotone in x.
+__device__ __forceinline__ float exponent(float x, const Scale& s) { return (x - s.top) * s.ch; }
+
+// 2^(i/32) 2^62, rounded; lane i of a warp holds entry i.
+__device__ const u64 POW2_32[32] = {
+    0x4000000000000000ull, 0x4166c34c5615d0ecull, 0x42d561b3e6243d8aull, 0x444c0740496d4294ull,
+    0x45cae0f1f545eb73ull, 0x47521cc5a2e6a9e0ull, 0x48e1e9b9d588e19bull, 0x4a7a77d47f7b84b1ull,
+    0x4c1bf828c6dc54b8ull, 0x4dc69cdceaa72a9cull, 0x4f7a993048d088d7ull, 0x513821818624b40cull,
+    0x52ff6b54d8a89c75ull, 0x54d0ad5a753e077cull, 0x56ac1f752150a563ull, 0x5891fac0e95612c8ull,
+    0x5a827999fcef3242ull, 0x5c7dd7a3b17dcf75ull, 0x5e8451cfac061b5full, 0x6096266533384a2bull,
+    0x62b39508aa836d6full, 0x64dcdec3371793d1ull, 0x6712460a8fc24072ull, 0x69540ec8f895722dull,
+    0x6ba27e656b4eb57aull, 0x6dfddbcbed791babull, 0x70666f76154a7089ull, 0x72dc8373be41a454ull,
+    0x75606373ee921c97ull, 0x77f25ccdee6d7ae6ull, 0x7a92be8a92436616ull, 0x7d41d96db915019dull};
+
+// ln 2 in two floats; the series' further terms are ln(2)^n / n!.
+constexpr float LN2 = 0x1.62e430p-1f, LN2_LO = -0x1.05c610p-29f;
+
+struct Table {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Table load_table() {
+  const u64 t = POW2_32[threadIdx.x & 31];
+  return {(uint32_t)t, (uint32_t)(t >> 32)};
+}
+
+// round(2^y 2^F), y = (x - M) log2(e) / T: x - M and y are sums of two floats, y = j/32 + g,
+// 2^y = 2^(j/32) (1 + p) with p = 2^g - 1 by its series, |g| <= 1/64, in units of 2^-37; the product
+// and the shift are on whole numbers.  Exactly 2^F at x = M.  The warp's 32 lanes call it together.
+__device__ __forceinline__ u64 weight(float x, const Scale& s, const Table& t) {
+  const float dh = x - s.top, back = dh - x;
+  const float dl = (x - (dh - back)) - (s.top + back);
+  const float ph = dh * s.ch;
+  const float pl = fmaf(dh, s.ch, -ph) + fmaf(dh, s.cl, dl * s.ch);
+  const float far = 393216.f;  // 1.5 2^18: its last place is 1/32
+  const float k = ph + far;
+  const int j = __float_as_int(k) - __float_as_int(far);
+  const float r = ph - (k - far);
+  const float g = r + pl, gl = pl - (g - r);
+  const float c = fmaf(g, fmaf(g, fmaf(g, 0.0013333558f, 0.0096181291f), 0.055504109f), 0.24022651f);
+  const float hh = fmaf(g, c, LN2), hl = fmaf(g, c, LN2 - hh) + LN2_LO;
+  const float qh = g * hh;
+  const float ql = fmaf(g, hh, -qh) + fmaf(g, hl, gl * hh);
+  const int p = __float2int_rn(qh * 0x1p37f) + __float2int_rn(ql * 0x1p37f);
+  const uint32_t lo = __shfl_sync(0xffffffffu, t.lo, j & 31);
+  const uint32_t hi = __shfl_sync(0xffffffffu, t.hi, j & 31);
+  u64 w = ((u64)hi << 32) | lo;
+  w += (u64)(((long long)(int)hi * p) >> 5);
+  const int n = s.shift - (j >> 5);  // >= 12
+  if (!(ph > -62.f) || n > 62) return 0;  // (-inf and NaN too)
+  return (w + (1ull << (n - 1))) >> n;
+}
+
+// The same weight in 64 bits, relative to M's (for a probability that is returned or compared).
+__device__ __forceinline__ double weight64(float x, float top, float temperature) {
+  return exp(((double)x - (double)top) / (double)temperature);
+}
+
+__device__ __forceinline__ bool kept(uint32_t key, int i, uint32_t least, int last) {
+  return key > least || (key == least && i <= last);
+}
+
+// ---- cluster -------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the row's CTAs.
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  tc::cluster_sync();
+}
+__device__ __forceinline__ u64 remote_u64(const u64* p, int rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(tc::mapa_shared(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(tc::mapa_shared(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 remote_u128(const uint4* p, int rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(tc::mapa_shared(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void remote_store(uint32_t* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::mapa_shared(p, rank)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// Where a running sum over a row passes a target.  The row's CTAs hold consecutive chunks of n
+// elements each (n differs in the last ones), a CTA's warps consecutive spans of its chunk.
+struct Locate {
+  u64 sums[WARPS];       // of the warps' spans
+  u64 fine[WARPS];       // of the chosen span's parts
+  u64 total, before;     // of the row; before the chosen span
+  int cta, warp;         // of the span
+};
+
+__device__ __forceinline__ int span_of(int n) { return (n + THREADS - 1) / THREADS * 32; }
+
+// Sums f(i) over this CTA's warps' spans (every lane calls f; f is 0 from n on).
+template <typename F>
+__device__ __forceinline__ void sum_spans(Locate& l, int n, F f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, span = span_of(n);
+  u64 sum = 0;
+  const int end = min(n, (warp + 1) * span);
+  for (int i = warp * span; i < end; i += 32) sum += f(i + lane);
+  sum = warp_sum64(sum);
+  if (lane == 0) l.sums[warp] = sum;
+}
+
+// After a cluster barrier behind sum_spans: the row's total, in every thread of the cluster.
+__device__ __forceinline__ u64 total_of(Locate& l, int ctas) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    u64 v = 0;
+    for (int i = lane; i < ctas * WARPS; i += 32) v += remote_u64(&l.sums[i % WARPS], i / WARPS);
+    v = warp_sum64(v);
+    if (lane == 0) l.total = v;
+  }
+  __syncthreads();
+  return l.total;
+}
+
+// The first element at which the running sum of f passes target (< total): its place in this CTA's
+// chunk, in every lane of one warp of the CTA that holds it; -1 everywhere else.
+template <typename F>
+__device__ __forceinline__ int locate(Locate& l, int ctas, int n, u64 target, F f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    u64 v[MAX_CLUSTER * WARPS / 32], mine = 0;
+#pragma unroll
+    for (int k = 0; k < MAX_CLUSTER * WARPS / 32; ++k) {
+      const int i = lane * (MAX_CLUSTER * WARPS / 32) + k;
+      v[k] = i < ctas * WARPS ? remote_u64(&l.sums[i % WARPS], i / WARPS) : 0;
+      mine += v[k];
+    }
+    u64 run = warp_scan64(mine, lane) - mine;
+#pragma unroll
+    for (int k = 0; k < MAX_CLUSTER * WARPS / 32; ++k) {
+      if (run <= target && target < run + v[k]) {
+        const int i = lane * (MAX_CLUSTER * WARPS / 32) + k;
+        l.cta = i / WARPS;
+        l.warp = i % WARPS;
+        l.before = run;
+      }
+      run += v[k];
+    }
+  }
+  __syncthreads();
+  if (l.cta != (int)tc::cluster_ctarank()) return -1;
+  const int span = span_of(n), first = l.warp * span, end = min(n, first + span);
+  const int part = (span / 32 + WARPS - 1) / WARPS * 32;
+  u64 sum = 0;
+  for (int i = first + warp * part; i < min(end, first + (warp + 1) * part); i += 32)
+    sum += f(i + lane);
+  sum = warp_sum64(sum);
+  if (lane == 0) l.fine[warp] = sum;
+  __syncthreads();
+  u64 run = l.before;
+  int w = 0;
+  while (w < WARPS - 1 && run + l.fine[w] <= target) run += l.fine[w++];
+  if (warp != w) return -1;
+  for (int i = first + w * part; i < min(end, first + (w + 1) * part); i += 32) {
+    const u64 v = f(i + lane);
+    const u64 up = warp_scan64(v, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, run + up > target);
+    if (hit) return i + __ffs(hit) - 1;
+    run += __shfl_sync(0xffffffffu, up, 31);
+  }
+  return -1;  // (not reached: target < total)
+}
+
+}  // namespace smp
+}  // namespace peagle

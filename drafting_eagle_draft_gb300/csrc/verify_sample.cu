@@ -1,0 +1,284 @@
+// Verification of sampled drafts (peagle_verify_sample).
+//
+// Two launches.  The first leaves the records of the target's batch (K+1) rows (sample.cu: the rows'
+// one reading from memory).  In the second a cluster takes a request: its drafts are accepted or
+// not from K logits and records, and the bonus token is drawn from r_i = max(p_i - q_i, 0) over the
+// row of the first rejected one, which is mostly still in the L2 cache.
+//
+// q lives in the draft vocabulary: the cluster's CTAs share out the draft row, and write each kept
+// entry's index (plus 1) to its target token's place in the shared memory of the CTA that has that
+// token's chunk.  p and q are whole numbers of 2^-63: weight x 2^127 / total, whose top 64 bits one
+// multiplication gives.
+#include "sample.cuh"
+
+namespace peagle {
+namespace smp {
+
+namespace {
+
+struct Args {
+  int K, vocab, draft_vocab, chunk, draft_chunk;
+  const int* tokens;
+  const void* target;
+  int64_t stride;
+  const float* draft;
+  const peagle_dist* draft_dist;
+  const peagle_dist* target_dist;
+  const int* d2t;
+  const float* u_accept;
+  const float* u_bonus;
+  int* accept_len;
+  int* bonus;
+  float* accept_prob;
+  int* errors;
+};
+
+// A row's probabilities as whole numbers of 2^-63.
+struct Probs {
+  Scale s;
+  uint32_t least;
+  int last;
+  bool cold;
+  int up;   // total's leading zeros
+  u64 inv;  // 2^127 / (total 2^up), rounded down
+};
+__device__ __forceinline__ Probs make_probs(const peagle_dist& d, int frac) {
+  Probs p;
+  p.cold = d.temperature < COLD;
+  p.s = make_scale(d.top, p.cold ? 1.f : d.temperature, frac);
+  p.least = d.least;
+  p.last = d.last;
+  p.up = __clzll((long long)d.total);
+  p.inv = (u64)((((unsigned __int128)1 << 127) - 1) / (d.total << p.up));
+  return p;
+}
+// Of a logit at index i; every lane of the warp calls it, with in = false where there is none.
+__device__ __forceinline__ u64 prob_of(float x, int i, bool in, const Probs& p, int frac, const Table& t) {
+  in = in && kept(order_key(x), i, p.least, p.last);
+  if (!__any_sync(0xffffffffu, in)) return 0;
+  const u64 w = p.cold ? 1ull << frac : weight(x, p.s, t);
+  return in ? __umul64hi(w << p.up, p.inv) : 0;
+}
+// In 64 bits, for the comparison of a draft.
+__device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, int frac) {
+  if (!kept(order_key(x), i, d.least, d.last) || x == -INFINITY) return 0.0;
+  const double w = d.temperature < COLD ? 1.0 : weight64(x, d.top, d.temperature);
+  return w * (double)(1ull << frac) / (double)d.total;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
+  extern __shared__ uint32_t from[];  // of this CTA's target tokens: the draft entry, plus 1
+  __shared__ Locate find;
+  __shared__ int accepted;
+  __shared__ bool drafted;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
+  const int b = blockIdx.x / ctas;
+  const int frac = frac_bits(a.vocab), draft_frac = frac_bits(a.draft_vocab);
+  const int base = rank * a.chunk, n = max(0, min(a.chunk, a.vocab - base));
+  const T* rows = static_cast<const T*>(a.target) + (int64_t)b * (a.K + 1) * a.stride;
+  const peagle_dist* pd = a.target_dist + (int64_t)b * (a.K + 1);
+  const peagle_dist* qd = a.draft_dist ? a.draft_dist + (int64_t)b * a.K : nullptr;
+
+  if (a.draft)
+    for (int i = tid; i < n; i += THREADS) from[i] = 0;
+
+  // the drafts: every CTA finds the same
+  if (tid < 32) {
+    int m = a.K;
+    bool fine = true;  // at m: the draft is a token that q gave
+    for (int j0 = 0; j0 < a.K; j0 += 32) {
+      const int j = j0 + lane;
+      bool ok = true, good = true;
+      if (j < a.K) {
+        const int x = a.tokens[b * a.K + j];
+        const peagle_dist p = pd[j];
+        unsigned bits = 0;
+        double pr = 0.0, qr = 1.0;
+        if (x < 0 || x >= a.vocab) bits = PEAGLE_DEV_BAD_TOKEN;
+        if (p.total == 0) bits |= PEAGLE_DEV_BAD_ROW;
+        if (qd) {
+          const peagle_dist q = qd[j];
+          if (q.total == 0) {
+            bits |= PEAGLE_DEV_BAD_ROW;
+          } else if (q.vocab != a.draft_vocab || q.index < 0 || q.index >= a.draft_vocab ||
+                     q.index + (a.d2t ? a.d2t[q.index] : 0) != x) {
+            bits |= PEAGLE_DEV_BAD_TOKEN;
+          } else {
+            qr = prob64(a.draft[((int64_t)b * a.K + j) * a.draft_vocab + q.index], q.index, q, draft_frac);
+          }
+        }
+        if (!bits) pr = prob64(to_f32(rows[(int64_t)j * a.stride + x]), x, p, frac);
+        good = !bits;
+        const double u = a.u_accept[b * a.K + j];
+        ok = good && u * qr < pr;
+        if (rank == 0) {
+          if (a.accept_prob)
+            a.accept_prob[b * a.K + j] = pr > 0.0 ? (float)fmin(1.0, pr / qr) : 0.f;
+          raise_error(reinterpret_cast<unsigned*>(a.errors), bits);
+        }
+      }
+      const unsigned no = __ballot_sync(0xffffffffu, !ok);
+      if (no && m == a.K) {
+        const int at = __ffs(no) - 1;
+        m = j0 + at;
+        fine = __shfl_sync(0xffffffffu, (int)good, at);
+      }
+    }
+    if (lane == 0) {
+      accepted = m;
+      drafted = m < a.K && fine;
+      if (rank == 0) a.accept_len[b] = m;
+    }
+  }
+  __syncthreads();
+  cluster_barrier();  // (the places in `from` are clear everywhere)
+  const int m = accepted;
+  const peagle_dist p = pd[m];
+  if (p.total == 0) {
+    if (rank == 0 && tid == 0) {
+      a.bonus[b] = -1;
+      raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_BAD_ROW);
+    }
+    return;
+  }
+  const bool with_q = drafted && a.draft;
+  const int only = drafted && !a.draft ? a.tokens[b * a.K + m] : -1;  // q = 1 there
+  const Table tab = load_table();
+  const Probs pp = make_probs(p, frac);
+  Probs qq = pp;
+  const float* draft = nullptr;
+  if (with_q) {
+    const peagle_dist q = qd[m];
+    qq = make_probs(q, draft_frac);
+    draft = a.draft + ((int64_t)b * a.K + m) * a.draft_vocab;
+    const int end = min(a.draft_vocab, (rank + 1) * a.draft_chunk);
+    for (int d = rank * a.draft_chunk + tid; d < end; d += THREADS) {
+      if (!kept(order_key(draft[d]), d, qq.least, qq.last)) continue;
+      const int t = d + (a.d2t ? a.d2t[d] : 0);
+      if (t >= 0 && t < a.vocab) remote_store(&from[t % a.chunk], t / a.chunk, d + 1);
+    }
+    __syncthreads();
+  }
+  cluster_barrier();
+  const T* row = rows + (int64_t)m * a.stride + base;
+  bool use_q = with_q || only >= 0;
+  const auto rest = [&](int i) -> u64 {
+    const bool in = i < n;
+    const u64 mine = prob_of(in ? to_f32(row[i]) : 0.f, base + i, in, pp, frac, tab);
+    if (!use_q) return mine;
+    if (!with_q) return base + i == only ? 0 : mine;
+    if (!__any_sync(0xffffffffu, mine != 0)) return 0;
+    const uint32_t d = in ? from[i] : 0;
+    const u64 theirs = prob_of(d ? draft[d - 1] : 0.f, (int)d - 1, d != 0, qq, draft_frac, tab);
+    return mine > theirs ? mine - theirs : 0;
+  };
+  sum_spans(find, n, rest);
+  __syncthreads();
+  cluster_barrier();
+  u64 total = total_of(find, ctas);
+  if (total == 0) {  // (the same everywhere) the drafter left nothing: p itself
+    cluster_barrier();
+    use_q = false;
+    sum_spans(find, n, rest);
+    __syncthreads();
+    cluster_barrier();
+    total = total_of(find, ctas);
+  }
+  const double want = fmax((double)a.u_bonus[b], 0.0) * (double)total;  // (0 for a NaN)
+  const u64 target = want < (double)total ? min((u64)want, total - 1) : total - 1;
+  const int at = locate(find, ctas, n, target, rest);
+  if (at >= 0 && lane == 0) a.bonus[b] = base + at;
+  cluster_barrier();  // (the others read this CTA's sums)
+}
+
+template <typename T>
+int launch(const Args& a, int batch, int ctas, cudaStream_t st) {
+  const size_t bytes = a.draft ? (size_t)a.chunk * 4 : 0;
+  if (smem_optin((const void*)verify_kernel<T>, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)batch * ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+int64_t check_sizes(int64_t batch, int K, int vocab) {
+  if (batch < 1 || K < 1 || vocab < 1) return PEAGLE_ERR_INVALID;
+  if (K > 64) return PEAGLE_ERR_CAPACITY;
+  if (vocab > MAX_VOCAB || batch * (K + 1) > MAX_ROWS) return PEAGLE_ERR_UNSUPPORTED;
+  return batch * (K + 1) * (int64_t)sizeof(peagle_dist);
+}
+
+}  // namespace
+}  // namespace smp
+}  // namespace peagle
+
+extern "C" int64_t peagle_verify_sample_workspace(int32_t batch, int32_t K, int32_t vocab) {
+  return peagle::smp::check_sizes(batch, K, vocab);
+}
+
+extern "C" int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* draft_tokens,
+                                    const peagle_sampling* how, int32_t vocab,
+                                    const void* target_logits, int32_t dtype,
+                                    int64_t target_stride, int32_t draft_vocab,
+                                    const float* draft_logits, const peagle_dist* draft_dist,
+                                    const int32_t* d2t, const float* u_accept,
+                                    const float* u_bonus, int32_t* out_accept_len,
+                                    int32_t* out_bonus, float* out_accept_prob, int32_t* errors,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+  using namespace peagle;
+  const int64_t need = smp::check_sizes(batch, K, vocab);
+  if (need < 0) return (int)need;
+  int rc = smp::check_rows(how, (int64_t)batch * (K + 1), vocab, target_logits, dtype, target_stride);
+  if (rc != PEAGLE_OK) return rc;
+  if (!draft_tokens || !u_accept || !u_bonus || !out_accept_len || !out_bonus || !workspace ||
+      (draft_logits == nullptr) != (draft_dist == nullptr))
+    return PEAGLE_ERR_INVALID;
+  if (((uintptr_t)draft_tokens | (uintptr_t)u_accept | (uintptr_t)u_bonus | (uintptr_t)d2t |
+       (uintptr_t)out_accept_len | (uintptr_t)out_bonus | (uintptr_t)out_accept_prob |
+       (uintptr_t)errors | (uintptr_t)draft_logits) % 4 ||
+      (uintptr_t)draft_dist % 8 || (uintptr_t)workspace % 16)
+    return PEAGLE_ERR_INVALID;
+  if (draft_logits && draft_vocab < 1) return PEAGLE_ERR_INVALID;
+  if (draft_logits && draft_vocab > smp::MAX_VOCAB) return PEAGLE_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
+  const cudaStream_t st = (cudaStream_t)stream;
+  peagle_dist* dist = static_cast<peagle_dist*>(workspace);
+  rc = smp::sample_rows(how, batch * (K + 1), vocab, target_logits, dtype, target_stride, nullptr,
+                        nullptr, nullptr, nullptr, dist, nullptr, st);
+  if (rc != PEAGLE_OK) return rc;
+  smp::Args a = {};
+  // a request's second step is a chain of short passes over one row: the whole cluster, but for
+  // rows of a few thousand tokens
+  int ctas = 1;
+  while (ctas < smp::MAX_CLUSTER && vocab >= 2048 * ctas) ctas *= 2;
+  a.K = K;
+  a.vocab = vocab;
+  a.draft_vocab = draft_logits ? draft_vocab : 1;
+  a.chunk = cdiv(vocab, ctas);
+  a.draft_chunk = cdiv(a.draft_vocab, ctas);
+  a.tokens = draft_tokens;
+  a.target = target_logits;
+  a.stride = target_stride ? target_stride : vocab;
+  a.draft = draft_logits;
+  a.draft_dist = draft_dist;
+  a.target_dist = dist;
+  a.d2t = d2t;
+  a.u_accept = u_accept;
+  a.u_bonus = u_bonus;
+  a.accept_len = out_accept_len;
+  a.bonus = out_bonus;
+  a.accept_prob = out_accept_prob;
+  a.errors = errors;
+  return dtype == PEAGLE_F32 ? smp::launch<float>(a, batch, ctas, st)
+                             : smp::launch<bf16>(a, batch, ctas, st);
+}

@@ -580,6 +580,100 @@ int peagle_set_wait_limit_quant(uint64_t limit_ns, int32_t unreachable_wait);
 int64_t peagle_decode_attention_quant_workspace(const peagle_kv_quant* kv, int32_t batch,
                                                 int32_t K, int32_t n_q_heads);
 
+/* Sampling at a temperature.  The pages draft and verify greedily ("EAGLE-4", section "EAGLE-4
+ * overview"); the calls below run the same round for requests that are sampled: peagle_sample draws
+ * tokens from logits, peagle_verify_sample accepts or replaces drafts so that what comes out is
+ * distributed as the target's own samples.  The settings are device arrays with one entry for each
+ * `rows_per` consecutive rows (0 counts as 1: one a row; K for a request's draft rows, K + 1 for its
+ * target rows).  NULL arrays: temperature 1, the filters off.
+ *   temperature  T >= 0; below 2^-60 the row is greedy (its largest logit, the lowest index of it)
+ *   top_k        keeps the k largest logits, the lower indices of equal ones (<= 0: all)
+ *   top_p        of those, keeps the shortest prefix, by the same order, whose probability reaches
+ *                top_p of theirs, at least one (>= 1 or NaN: all)
+ *   min_p        of those, keeps the ones with at least min_p times the largest probability (<= 0 or
+ *                NaN: all; above 1 counts as 1)
+ * The kept tokens' probabilities are w_i / (sum of w), w_i = exp((x_i - max x) / T). */
+typedef struct peagle_sampling {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t rows_per;
+} peagle_sampling;
+
+/* The distribution of a row, as peagle_sample leaves it for peagle_verify_sample: the largest
+ * logit, the temperature (0: greedy), the border of the kept tokens (their smallest logit's order
+ * key, and the highest kept index of logits equal to it), the sum of their weights as a whole
+ * number, the row's length, and the index that was sampled.  A row without a distribution has total 0
+ * and index -1. */
+typedef struct peagle_dist {
+  uint64_t total;
+  float top;
+  float temperature;
+  uint32_t least;
+  int32_t last;
+  int32_t index;
+  int32_t vocab;
+} peagle_dist;
+
+/* Draw one token from each row of logits (the drafter's out_logits, or the target's).
+ *   logits     device [rows][vocab] of type dtype (peagle_dtype), consecutive rows row_stride
+ *              elements apart (0: vocab; at least vocab); any alignment of whole elements
+ *   uniforms   device fp32 [rows]: random numbers in [0, 1).  Row r's token is the first index at
+ *              which the running sum of the kept probabilities, in the order of the indices, passes
+ *              uniforms[r] (below 0 or NaN counts as 0, 1 and more as just below 1)
+ *   d2t        device int32 [vocab] draft->target offsets, or NULL
+ *   out_tokens device int32 [rows]: index + d2t[index]
+ *   out_prob   device fp32 [rows]: the token's probability; or NULL
+ *   out_dist   device [rows]: the rows' records; or NULL
+ *   errors     device word as in peagle_kv_quant; or NULL
+ * Logits of -inf have no probability.  A row that holds a NaN or +inf or nothing but -inf, or whose
+ * temperature is negative or NaN, has no distribution: its token is -1 and its probability NaN, and
+ * it sets BAD_ROW.  Weights are computed to about 2^-37 and added up as whole numbers: the same
+ * inputs give the same tokens whatever the number of rows, their strides and the GPU's order of
+ * work.  A weight below 2^-46 (vocab 201088; 2^-50 at 8192 and less) of the largest may count as
+ * nothing.
+ * Needs no context and no workspace.  Limits (else PEAGLE_ERR_UNSUPPORTED): vocab <= 262144, rows <=
+ * 2^24. */
+int peagle_sample(const peagle_sampling* how, int32_t rows, int32_t vocab, const void* logits,
+                  int32_t dtype, int64_t row_stride, const float* uniforms, const int32_t* d2t,
+                  int32_t* out_tokens, float* out_prob, peagle_dist* out_dist, int32_t* errors,
+                  void* stream);
+
+/* Verification of sampled drafts ("EAGLE-4 overview" has the greedy form, peagle_verify_greedy): for
+ * each request the longest prefix of accepted drafts, plus one bonus token.  With p_j the target's
+ * distribution after j drafts (its settings `how`) and q_j the one that draft j was drawn from,
+ * draft j (token x) is accepted iff u_accept[b, j] q_j(x) < p_j(x).  The bonus token is drawn, as
+ * peagle_sample draws, from max(p_m - q_m, 0) where m < K drafts are accepted (from p_m should that
+ * be nothing) and from p_K where all are.  Whatever the drafter, out comes the target's distribution.
+ *   draft_tokens   device int32 [batch, K], target vocabulary
+ *   target_logits  device [batch * (K+1)][vocab], type dtype, rows target_stride elements apart
+ *   draft_logits   device fp32 [batch * K][draft_vocab] (contiguous), draft_dist their records and
+ *                  d2t their offsets (distinct ids; NULL: the identity), as they went through
+ *                  peagle_sample, whose out_tokens are draft_tokens; or both NULL: drafts that were
+ *                  not drawn (peagle_draft's own tokens), q_j(x) = 1
+ *   u_accept       device fp32 [batch, K], u_bonus device fp32 [batch]: random numbers in [0, 1)
+ *   out_accept_len device int32 [batch]: m in 0..K; out_bonus device int32 [batch]
+ *   out_accept_prob device fp32 [batch, K]: min(1, p_j(x) / q_j(x)) of every draft, also behind a
+ *                  rejected one; or NULL
+ *   workspace      device memory of at least peagle_verify_sample_workspace() bytes, 16-byte
+ *                  aligned, no initial value; calls that may overlap on the GPU each have their own
+ * A draft token outside the vocabulary, or that is not its record's (BAD_TOKEN), and one whose record
+ * or target row has no distribution (BAD_ROW), is rejected with probability 0; the bonus is then
+ * drawn from p_m, or -1 where that row has no distribution.
+ * Needs no context.  1 <= K <= 64; limits as for peagle_sample, batch * (K+1) <= 2^24; a workspace
+ * that is too small is PEAGLE_ERR_CAPACITY. */
+int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* draft_tokens,
+                         const peagle_sampling* how, int32_t vocab, const void* target_logits,
+                         int32_t dtype, int64_t target_stride, int32_t draft_vocab,
+                         const float* draft_logits, const peagle_dist* draft_dist,
+                         const int32_t* d2t, const float* u_accept, const float* u_bonus,
+                         int32_t* out_accept_len, int32_t* out_bonus, float* out_accept_prob,
+                         int32_t* errors, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that peagle_verify_sample needs, or a negative error. */
+int64_t peagle_verify_sample_workspace(int32_t batch, int32_t K, int32_t vocab);
+
 /* Raw device error bits observed by the last peagle_status call. */
 int32_t peagle_device_error_bits(const peagle_ctx* ctx);
 

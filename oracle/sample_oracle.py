@@ -1,0 +1,94 @@
+"""fp64 oracle of sampling at a temperature and of the verification of sampled drafts.
+
+Plain numpy on the definitions in include/peagle.h (peagle_sampling, peagle_sample and
+peagle_verify_sample); no code of the CUDA path.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+COLD = 2.0 ** -60  # temperatures below it are greedy
+
+
+def order(x):
+    """Indices by size, larger first, the lower index of equal ones first."""
+    return np.argsort(-np.asarray(x, np.float64), kind="stable")
+
+
+def distribution(x, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """The probabilities of one row of logits, or None where it has no distribution."""
+    x = np.asarray(x, np.float64)
+    if np.isnan(x).any() or not x.max() < np.inf or x.max() == -np.inf or not temperature >= 0:
+        return None
+    by_size = order(x)
+    if temperature < COLD:
+        p = np.zeros(len(x))
+        p[by_size[0]] = 1.0
+        return p
+    y = (x[by_size] - x[by_size[0]]) / np.float64(temperature)
+    w = np.exp(y)
+    n = len(x)
+    if 0 < top_k < n:
+        n = int(top_k)
+    if top_p < 1.0:
+        before = np.concatenate([[0.0], np.cumsum(w[:n])[:-1]])
+        n = max(1, int((before < max(top_p, 0.0) * w[:n].sum()).sum()))
+    if min_p > 0.0:
+        # (w >= min_p by the exponents: exp rounds y = -1e-40 up to the largest weight itself)
+        n = int((y[:n] >= np.log(np.float64(min(min_p, 1.0)))).sum())
+    p = np.zeros(len(x))
+    p[by_size[:n]] = w[:n] / w[:n].sum()
+    return p
+
+
+def pick(p, u):
+    """The first index at which the running sum passes u of the whole."""
+    c = np.cumsum(p)
+    u = 0.0 if not u > 0 else float(u)
+    last = int(np.nonzero(p)[0][-1])
+    return min(int(np.searchsorted(c, u * c[-1], side="right")), last)
+
+
+def sample(x, u, d2t=None, **settings):
+    """(token, probability, index)."""
+    p = distribution(x, **settings)
+    if p is None:
+        return -1, np.nan, -1
+    i = pick(p, u)
+    return i + (0 if d2t is None else int(d2t[i])), p[i], i
+
+
+def left_over(p, q):
+    """What the bonus token is drawn from: max(p - q, 0), or p where that is nothing."""
+    r = np.maximum(p - q, 0.0)
+    return r if r.sum() > 0 else p
+
+
+def verify(tokens, p, q, u_accept, u_bonus):
+    """One request: draft tokens [K] (target vocabulary), p [K + 1] and q [K] distributions over the
+    target vocabulary (None: none).  Returns (accepted, bonus, accept probabilities)."""
+    K = len(tokens)
+    prob, ok, good = np.zeros(K), np.zeros(K, bool), np.zeros(K, bool)
+    for j, x in enumerate(tokens):
+        good[j] = p[j] is not None and q[j] is not None and 0 <= x < len(p[j])
+        if good[j]:
+            a, b = p[j][x], q[j][x]
+            prob[j] = min(1.0, a / b) if a > 0 else 0.0
+            ok[j] = u_accept[j] * b < a
+    m = int(np.argmin(ok)) if not ok.all() else K
+    if p[m] is None:
+        return m, -1, prob
+    r = p[m]
+    if m < K and good[m]:
+        r = left_over(p[m], q[m])
+    return m, pick(r, u_bonus), prob
+
+
+def spread(q, d2t, vocab):
+    """A draft-vocabulary distribution over the target's vocabulary."""
+    if q is None:
+        return None
+    out = np.zeros(vocab)
+    ids = np.arange(len(q)) + (0 if d2t is None else np.asarray(d2t, np.int64))
+    out[ids] = q
+    return out
