@@ -43,6 +43,8 @@ EXPORTS = ("peagle_create", "peagle_draft", "peagle_catch_up", "peagle_verify_gr
            "peagle_decode_attention_quant", "peagle_decode_attention_quant_workspace",
            "peagle_set_wait_limit_quant",
            "peagle_sample", "peagle_verify_sample", "peagle_verify_sample_workspace",
+           "peagle_decode_attention_shared", "peagle_decode_attention_shared_workspace",
+           "peagle_set_wait_limit_shared",
            "peagle_device_error_bits", "peagle_strerror", "peagle_destroy")
 STAGES = ("fc", "qkv", "attn", "oproj", "gate_up", "down", "lm_head", "norm", "small")
 
@@ -165,6 +167,12 @@ def lib():
                                            _vp, _vp, _vp, _vp, _i64, _vp]
         L.peagle_verify_sample_workspace.argtypes = [_i32, _i32, _i32]
         L.peagle_verify_sample_workspace.restype = _i64
+        L.peagle_decode_attention_shared.argtypes = (
+            [_i32] * 6 + [_vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, ctypes.c_float,
+                          _vp, _vp, _vp, _vp, _i64, _vp])
+        L.peagle_decode_attention_shared_workspace.argtypes = [_i32] * 8
+        L.peagle_decode_attention_shared_workspace.restype = _i64
+        L.peagle_set_wait_limit_shared.argtypes = [ctypes.c_uint64, _i32]
         L.peagle_read_timing.argtypes = [_vp, _vp, _vp]
         L.peagle_read_pass_trace.argtypes = [_vp, _vp, _i32, _vp, _vp]
         L.peagle_read_pass_trace.restype = _i32
@@ -807,6 +815,85 @@ def peagle_verify_sample(batch, K, draft_tokens, how, target_logits, u_accept, u
         workspace.numel() * workspace.element_size(), s)
     if rc:
         raise PeagleError(rc, what)
+
+
+def _shared_sizes(what, batch, K, q, prefix_k, k):
+    """dtype, query heads, kv heads, head_dim and the capacities of a shared attention call."""
+    if torch is None:
+        _import_torch()
+    _refuse_wide(what, batch=batch, K=K)
+    dt = q.dtype
+    if dt is torch.bfloat16:
+        code = PEAGLE_BF16
+    elif dt is torch.float32:
+        code = PEAGLE_F32
+    else:
+        _refuse(what, f"queries are float32 or bfloat16, got {dt}")
+    qs, ps, ks = q.shape, prefix_k.shape, k.shape
+    if len(qs) != 3 or len(ps) != 3 or len(ks) != 4 or qs[0] != batch * K or ks[0] < batch or \
+            ks[1] != ps[0] or ps[2] != qs[2] or ks[3] != qs[2]:
+        _refuse(what, f"q {tuple(qs)}, prefix {tuple(ps)} and cache {tuple(ks)} do not fit batch {batch}, "
+                      f"K {K}")
+    return code, qs[1], ps[0], qs[2], ps[1], ks[2]
+
+
+def peagle_decode_attention_shared_workspace(batch, K, q, prefix_k, k_cache) -> int:
+    """Bytes of workspace of peagle_decode_attention_shared for tensors of these shapes and types
+    (include/peagle.h)."""
+    what = "peagle_decode_attention_shared_workspace"
+    code, nq, nkv, hd, pcap, cap = _shared_sizes(what, batch, K, q, prefix_k, k_cache)
+    n = lib().peagle_decode_attention_shared_workspace(code, batch, K, nq, nkv, hd, pcap, cap)
+    if n < 0:
+        raise PeagleError(n, what)
+    return n
+
+
+def peagle_decode_attention_shared(batch, K, q, prefix_k, prefix_v, prefix_len, k_cache, v_cache,
+                                   seq_lens, out, workspace, out_lse=None, causal=True, scale=None,
+                                   errors=None, stream=None):
+    """Decode attention over a prefix that the batch shares and the requests' own slots
+    (include/peagle.h).  q, out: float32 or bfloat16 [batch * K, n_q_heads, head_dim], rows of q any
+    stride; prefix_k, prefix_v [n_kv_heads, prefix_capacity, head_dim] and k_cache, v_cache [>= batch,
+    n_kv_heads, capacity, head_dim] of q's type, contiguous; prefix_len int32 [1]; scale:
+    1 / sqrt(head_dim) when None."""
+    what = "peagle_decode_attention_shared"
+    code, nq, nkv, hd, pcap, cap = _shared_sizes(what, batch, K, q, prefix_k, k_cache)
+    dev, dt, rows, sd = q.device, q.dtype, batch * K, q.stride()
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(what, f"q is on {dev}, which is not the current CUDA device")
+    if prefix_v.shape != prefix_k.shape or v_cache.shape != k_cache.shape or not (
+            prefix_k.is_contiguous() and prefix_v.is_contiguous() and k_cache.is_contiguous() and
+            v_cache.is_contiguous()):
+        _refuse(what, "keys and values are contiguous and of equal shapes")
+    if out.shape != q.shape or sd[2] != 1 or (nq > 1 and sd[1] != hd) or not out.is_contiguous() or \
+            (rows > 1 and sd[0] < nq * hd):
+        _refuse(what, "q's rows are contiguous and apart, out is contiguous and of q's shape")
+    if out_lse is not None and (out_lse.shape != q.shape[:2] or not out_lse.is_contiguous()):
+        _refuse(what, f"out_lse is {tuple(q.shape[:2])}, contiguous")
+    if not workspace.is_contiguous() or workspace.device != dev:
+        _refuse(what, f"a contiguous workspace on {dev} is wanted")
+    if stream is None and _raw_stream is not None:
+        s = _raw_stream(dev.index)
+    else:
+        s = _stream_ptr(stream)
+    rc = lib().peagle_decode_attention_shared(
+        code, batch, K, nq, nkv, hd, _on(q, dev, dt, what), sd[0] if rows > 1 else 0,
+        _on(prefix_k, dev, dt, what), _on(prefix_v, dev, dt, what), pcap,
+        _lens(prefix_len, 1, dev, what), _on(k_cache, dev, dt, what), _on(v_cache, dev, dt, what), cap,
+        _lens(seq_lens, batch, dev, what), 1 if causal else 0, hd ** -0.5 if scale is None else scale,
+        _on(out, dev, dt, what), _on(out_lse, dev, torch.float32, what),
+        _flat(errors, 1, dev, torch.int32, what, "errors", True), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s)
+    if rc:
+        raise PeagleError(rc, what)
+
+
+def peagle_set_wait_limit_shared(limit_ns: int, unreachable_wait: int = -1):
+    """Bound of the waits inside peagle_decode_attention_shared, and one that cannot succeed: the
+    failure-path drill (include/peagle.h); (0, -1) restores the defaults."""
+    _refuse_wide("peagle_set_wait_limit_shared", unreachable_wait=unreachable_wait)
+    _check(lib().peagle_set_wait_limit_shared(int(limit_ns), int(unreachable_wait)),
+           "peagle_set_wait_limit_shared")
 
 
 def peagle_device_error_bits(ctx: Context) -> int:

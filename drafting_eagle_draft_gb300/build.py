@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libpeagle.so")
 SOURCES = ["peagle_api.cu", "kernels.cu", "gemm_tc.cu", "pass_kernel.cu", "masked_attn_tc.cu",
            "train_kernels.cu", "train_attn_mma.cu", "train_attn_tc.cu", "gemm_tf32.cu",
            "kv_quant.cu", "kv_quant_attn.cu", "kv_quant_attn_tc.cu",
-           "sample.cu", "verify_sample.cu"]
+           "sample.cu", "verify_sample.cu", "shared_attn.cu", "shared_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr"]

@@ -1,0 +1,292 @@
+// Decode attention over a shared prefix and each request's own slots
+// (peagle_decode_attention_shared): entry point, the fp32 kernel and the join.
+//
+// For one kv head the rows of the whole batch, batch x K x (heads a kv head), are the rows of one
+// product with the prefix, so that its keys and values are read once for a tile of rows and not
+// once for each request; a request's own slots meet its K x (heads a kv head) rows only.  Either
+// part is cut along its slots into pieces, each with its own reference and sum, and a second
+// kernel joins a row's pieces.
+//
+// fp32 (fma): a CTA takes 32 rows of a kv head and a piece of the slots, in tiles of 64.  A warp
+// has 8 rows; for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
+// shared memory), for the outputs head_dim / 32 dims.  What bounds it is shared memory: as many
+// wavefronts of loads as cycles of products.
+#include "shared_attn.cuh"
+
+namespace peagle {
+namespace sha {
+
+namespace {
+
+constexpr int ROWS = 32, KEYS = 64, SIMT_THREADS = 128, RW = 8;  // RW: rows a warp
+constexpr float LOG2E = 1.44269504f;
+
+// Pieces of a row: `shared` of the prefix, then `own`.
+struct Pieces {
+  int shared, own;
+};
+
+// piece p of row x of head h: [piece][batch * K * nq] statistics, then as many rows of hd
+__device__ __forceinline__ size_t part_at(const Args& a, int piece, int row, int head) {
+  return ((size_t)piece * a.batch * a.K + row) * a.nq + head;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(SIMT_THREADS) simt_kernel(Args a, Pieces pc) {
+  constexpr int KS = HD + 4, DL = HD / 32;
+  extern __shared__ float smem[];
+  float* sq = smem;                // [ROWS][HD]
+  float* sk = sq + ROWS * HD;      // [KEYS][KS]
+  float* sv = sk + KEYS * KS;      // [KEYS][HD]
+  float* sp = sv + KEYS * HD;      // [ROWS][KEYS]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  const int all = a.batch * a.K * a.G, mine = a.K * a.G;
+  const int shared_tiles = cdiv(all, ROWS), own_tiles = cdiv(mine, ROWS);
+  int x = blockIdx.x, slots, first_row, rows, piece, pieces, b = -1;
+  const float *k, *v;
+  if (x < shared_tiles * pc.shared) {
+    piece = x / shared_tiles;
+    pieces = pc.shared;
+    first_row = x % shared_tiles * ROWS;
+    rows = min(ROWS, all - first_row);
+    slots = prefix_of(a);
+    k = static_cast<const float*>(a.pk) + (size_t)h * a.pcap * HD;
+    v = static_cast<const float*>(a.pv) + (size_t)h * a.pcap * HD;
+  } else {
+    x -= shared_tiles * pc.shared;
+    b = x % a.batch;
+    x /= a.batch;
+    piece = x / own_tiles;
+    pieces = pc.own;
+    first_row = x % own_tiles * ROWS;
+    rows = min(ROWS, mine - first_row);
+    slots = slots_of(a, b);
+    k = static_cast<const float*>(a.k) + ((size_t)b * a.nkv + h) * a.cap * HD;
+    v = static_cast<const float*>(a.v) + ((size_t)b * a.nkv + h) * a.cap * HD;
+  }
+  if (slots < 0) return;  // (the join sees it too)
+  const int tiles = cdiv(slots, KEYS);
+  const int t0 = (int)((int64_t)tiles * piece / pieces), t1 = (int)((int64_t)tiles * (piece + 1) / pieces);
+
+  // rows of this warp: row in the request (or batch), q row and head, limit
+  const int base = b < 0 ? 0 : b * a.K;
+  for (int i = tid; i < ROWS * HD / 4; i += SIMT_THREADS) {
+    const int r = i / (HD / 4), d = i % (HD / 4) * 4, at = first_row + r;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows)
+      y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (int64_t)(base + at / a.G) * a.q_stride +
+                                           (size_t)(h * a.G + at % a.G) * HD + d);
+    *reinterpret_cast<float4*>(sq + r * HD + d) = y;
+  }
+  const float qs = a.scale * LOG2E;
+  float m[RW], l[RW], o[RW][DL];
+  int limit[RW];
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) o[r][d] = 0.f;
+    const int at = first_row + warp * RW + r;
+    limit[r] = warp * RW + r < rows ? (b < 0 ? slots : limit_of(a, slots, at / a.G)) : 0;
+  }
+  for (int t = t0; t < t1; ++t) {
+    __syncthreads();
+    for (int i = tid; i < KEYS * HD / 4; i += SIMT_THREADS) {
+      const int s = i / (HD / 4), d = i % (HD / 4) * 4;
+      float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+      if (t * KEYS + s < slots) {
+        kk = *reinterpret_cast<const float4*>(k + (size_t)(t * KEYS + s) * HD + d);
+        vv = *reinterpret_cast<const float4*>(v + (size_t)(t * KEYS + s) * HD + d);
+      }
+      *reinterpret_cast<float4*>(sk + s * KS + d) = kk;
+      *reinterpret_cast<float4*>(sv + s * HD + d) = vv;
+    }
+    __syncthreads();
+    if (warp * RW >= rows) continue;
+    float s0[RW] = {}, s1[RW] = {};
+#pragma unroll 4
+    for (int d = 0; d < HD; d += 4) {
+      const float4 ka = *reinterpret_cast<const float4*>(sk + lane * KS + d);
+      const float4 kb = *reinterpret_cast<const float4*>(sk + (lane + 32) * KS + d);
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const float4 y = *reinterpret_cast<const float4*>(sq + (warp * RW + r) * HD + d);
+        s0[r] = fmaf(y.x, ka.x, fmaf(y.y, ka.y, fmaf(y.z, ka.z, fmaf(y.w, ka.w, s0[r]))));
+        s1[r] = fmaf(y.x, kb.x, fmaf(y.y, kb.y, fmaf(y.z, kb.z, fmaf(y.w, kb.w, s1[r]))));
+      }
+    }
+    bool edge = false;
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      const int seen = limit[r] - t * KEYS;
+      edge |= seen < KEYS;
+      s0[r] = lane < seen ? s0[r] * qs : -INFINITY;
+      s1[r] = lane + 32 < seen ? s1[r] * qs : -INFINITY;
+      const float top = fmaxf(m[r], warp_max(fmaxf(s0[r], s1[r])));
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float c = exp2f(m[r] - ref);
+      s0[r] = exp2f(s0[r] - ref);
+      s1[r] = exp2f(s1[r] - ref);
+      l[r] = l[r] * c + (s0[r] + s1[r]);  // (of this lane's slots)
+#pragma unroll
+      for (int d = 0; d < DL; ++d) o[r][d] *= c;
+      m[r] = top;
+      sp[(warp * RW + r) * KEYS + lane] = s0[r];
+      sp[(warp * RW + r) * KEYS + lane + 32] = s1[r];
+    }
+    __syncwarp();
+    const float* w = sp + warp * RW * KEYS;
+    const float* vd = sv + lane * DL;
+    if (!edge) {
+#pragma unroll 2
+      for (int s = 0; s < KEYS; s += 4) {
+        float y[4][DL];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int d = 0; d < DL; ++d) y[i][d] = vd[(s + i) * HD + d];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          const float4 p = *reinterpret_cast<const float4*>(w + r * KEYS + s);
+#pragma unroll
+          for (int d = 0; d < DL; ++d)
+            o[r][d] = fmaf(p.x, y[0][d], fmaf(p.y, y[1][d], fmaf(p.z, y[2][d], fmaf(p.w, y[3][d], o[r][d]))));
+        }
+      }
+    } else {  // a value that a row does not see is no part of its sum, NaN or not
+      for (int s = 0; s < KEYS; ++s)
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+          if (t * KEYS + s < limit[r])
+#pragma unroll
+            for (int d = 0; d < DL; ++d) o[r][d] = fmaf(w[r * KEYS + s], vd[s * HD + d], o[r][d]);
+    }
+  }
+  Stat* stat = reinterpret_cast<Stat*>(a.part);
+  float* sums = a.part + 2 * part_at(a, pc.shared + pc.own, 0, 0);
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const int at = first_row + warp * RW + r;
+    const float total = warp_sum(l[r]);
+    if (warp * RW + r >= rows) continue;
+    const size_t i = part_at(a, b < 0 ? piece : pc.shared + piece, base + at / a.G, h * a.G + at % a.G);
+    if (lane == 0) stat[i] = {m[r], total};
+#pragma unroll
+    for (int d = 0; d < DL; ++d) sums[i * HD + lane * DL + d] = o[r][d];
+  }
+}
+
+// Joins the pieces of a row and head; a warp each.
+template <int HD>
+__global__ void __launch_bounds__(256) simt_join_kernel(Args a, Pieces pc) {
+  constexpr int DL = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = (int)(x / a.nq), head = (int)(x % a.nq);
+  if (row >= a.batch * a.K) return;
+  if (prefix_of(a) < 0 || slots_of(a, row / a.K) < 0) {
+    if (lane == 0) raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_KV_OVERFLOW);
+    return;
+  }
+  const Stat* stat = reinterpret_cast<const Stat*>(a.part);
+  const float* sums = a.part + 2 * part_at(a, pc.shared + pc.own, 0, 0);
+  float m = -INFINITY, l = 0.f, o[DL] = {};
+  for (int p = 0; p < pc.shared + pc.own; ++p) {
+    const size_t i = part_at(a, p, row, head);
+    const Stat s = stat[i];
+    if (s.l == 0.f) continue;
+    const float top = fmaxf(m, s.m), c = exp2f(m - top), w = exp2f(s.m - top);
+    l = l * c + s.l * w;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) o[d] = fmaf(o[d], c, w * sums[i * HD + lane * DL + d]);
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float* out = static_cast<float*>(a.out) + ((size_t)row * a.nq + head) * HD + lane * DL;
+#pragma unroll
+  for (int d = 0; d < DL; ++d) out[d] = o[d] * inv;
+  if (a.lse && lane == 0) a.lse[(size_t)row * a.nq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+}
+
+// Pieces, so that the CTAs fill the GPU's 304 places a few times, of at least two tiles each.
+Pieces simt_pieces(int batch, int K, int G, int nkv, int pcap, int cap) {
+  const auto cut = [](int64_t ctas, int slots) {
+    const int64_t most = slots / (2 * KEYS) + 1, want = (4 * 304 + ctas - 1) / ctas;
+    return (int)(want < most ? want : most);
+  };
+  const int64_t shared = (int64_t)cdiv(batch * K * G, ROWS) * nkv;
+  const int64_t own = (int64_t)batch * cdiv(K * G, ROWS) * nkv;
+  return {cut(shared, pcap), cut(own, cap)};
+}
+
+template <int HD>
+int launch_simt(const Args& a, cudaStream_t st) {
+  const Pieces pc = simt_pieces(a.batch, a.K, a.G, a.nkv, a.pcap, a.cap);
+  const size_t smem = (ROWS * HD + KEYS * (HD + 4) + KEYS * HD + ROWS * KEYS) * sizeof(float);
+  if (smem_optin((const void*)simt_kernel<HD>, smem) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  const int64_t ctas = (int64_t)cdiv(a.batch * a.K * a.G, ROWS) * pc.shared +
+                       (int64_t)a.batch * cdiv(a.K * a.G, ROWS) * pc.own;
+  simt_kernel<HD><<<dim3((unsigned)ctas, a.nkv), SIMT_THREADS, smem, st>>>(a, pc);
+  const int64_t warps = (int64_t)a.batch * a.K * a.nq;
+  simt_join_kernel<HD><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a, pc);
+  return cudaGetLastError() == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+}
+
+int64_t workspace(int dtype, int64_t batch, int K, int nq, int nkv, int hd, int pcap, int cap) {
+  if (batch < 1 || K < 1 || nq < 1 || nkv < 1 || pcap < 1 || cap < 1 || nq % nkv ||
+      (dtype != PEAGLE_F32 && dtype != PEAGLE_BF16))
+    return PEAGLE_ERR_INVALID;
+  const int64_t G = nq / nkv;
+  if ((hd != 64 && hd != 128) || K * G > 128 || nkv > 65535 || batch * K * nq > MAX_ROWS ||
+      pcap > MAX_SLOTS || cap > MAX_SLOTS)
+    return PEAGLE_ERR_UNSUPPORTED;
+  if (dtype == PEAGLE_BF16) return tc_workspace(batch, K, (int)G, nkv, hd);
+  const Pieces pc = simt_pieces((int)batch, K, (int)G, nkv, pcap, cap);
+  return (pc.shared + pc.own) * batch * K * nq * (hd + 2) * 4;
+}
+
+}  // namespace
+}  // namespace sha
+}  // namespace peagle
+
+extern "C" int64_t peagle_decode_attention_shared_workspace(int32_t dtype, int32_t batch, int32_t K,
+                                                            int32_t n_q_heads, int32_t n_kv_heads,
+                                                            int32_t head_dim, int32_t prefix_capacity,
+                                                            int32_t capacity) {
+  return peagle::sha::workspace(dtype, batch, K, n_q_heads, n_kv_heads, head_dim, prefix_capacity, capacity);
+}
+
+extern "C" int peagle_decode_attention_shared(int32_t dtype, int32_t batch, int32_t K, int32_t n_q_heads,
+                                              int32_t n_kv_heads, int32_t head_dim, const void* q,
+                                              int64_t q_stride, const void* prefix_k, const void* prefix_v,
+                                              int32_t prefix_capacity, const int32_t* prefix_len,
+                                              const void* k_cache, const void* v_cache, int32_t capacity,
+                                              const int32_t* seq_lens, int32_t causal, float scale, void* out,
+                                              float* out_lse, int32_t* errors, void* workspace,
+                                              int64_t workspace_bytes, void* stream) {
+  using namespace peagle;
+  const int64_t need =
+      sha::workspace(dtype, batch, K, n_q_heads, n_kv_heads, head_dim, prefix_capacity, capacity);
+  if (need < 0) return (int)need;
+  const int size = dtype == PEAGLE_F32 ? 4 : 2;
+  const int64_t row = (int64_t)n_q_heads * head_dim, rows = (int64_t)batch * K;
+  if (!q_stride) q_stride = row;
+  if (!q || !prefix_k || !prefix_v || !prefix_len || !k_cache || !v_cache || !seq_lens || !out || !workspace ||
+      q_stride < row || q_stride * size % 16 || (causal != 0 && causal != 1) || !(fabsf(scale * sha::LOG2E) <= 3.4e38f))
+    return PEAGLE_ERR_INVALID;
+  if (((uintptr_t)q | (uintptr_t)prefix_k | (uintptr_t)prefix_v | (uintptr_t)k_cache | (uintptr_t)v_cache |
+       (uintptr_t)out) % 16 ||
+      ((uintptr_t)prefix_len | (uintptr_t)seq_lens | (uintptr_t)out_lse | (uintptr_t)errors) % 4 ||
+      (uintptr_t)workspace % 256)
+    return PEAGLE_ERR_INVALID;
+  const char *o = (const char*)out, *i = (const char*)q;
+  if (o < i + ((rows - 1) * q_stride + row) * size && i < o + rows * row * size) return PEAGLE_ERR_INVALID;
+  if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
+  const sha::Args a = {q, q_stride, prefix_k, prefix_v, prefix_len, k_cache, v_cache, seq_lens, batch, K,
+                       n_q_heads, n_kv_heads, n_q_heads / n_kv_heads, prefix_capacity, capacity, causal, scale,
+                       out, out_lse, errors, (float*)workspace};
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PEAGLE_F32) return head_dim == 64 ? sha::launch_simt<64>(a, st) : sha::launch_simt<128>(a, st);
+  return sha::launch_tc(a, head_dim, st);
+}

@@ -1,0 +1,720 @@
+// Decode attention over a shared prefix and each request's own slots, bf16, on the 5th-generation
+// tensor cores (entry point and what is computed: shared_attn.cu).
+//
+// Units.  A kv head's rows of the whole batch meet the prefix in tiles of 128 rows, two tiles at a
+// time where there are two (a pair: both use the same key and value tiles); a request's rows meet
+// its own slots alone.  A unit is such rows x all of their slots, in tiles of 128 slots.  The tiles
+// of all units, a pair's counted twice, and ENTRY more for each unit, are dealt to the 152 CTAs in
+// equal shares: a CTA's share is a piece of one unit, some whole ones and a piece of another.  Each
+// piece leaves its sums in the workspace, in a place of its unit (the piece with the first tile) or
+// of its CTA (a continued unit, one a CTA at most), and the join adds them up.
+//
+// A CTA has two groups of 128 softmax threads, a thread a row, and one thread each that issues
+// copies and products.  For a pair the groups have a row tile each; otherwise both have the same
+// rows and take alternate slot tiles.  Per tile and group
+//   S = Q K^T   tcgen05.mma M = 128 rows, N = 128 slots, into the group's columns of tensor memory
+//   softmax     the thread reads its row of S, raises its reference only when the row's maximum
+//               passes it by 2^8 (the weights then stay within 2^8 and the row of O is scaled in
+//               place, rarely), and stores the weights as bf16 over the scores
+//   O += P V    tcgen05.mma with P from tensor memory and V as it lies (MN-major)
+// While one group is in its softmax the products of the other run.  Weights are rounded to bf16
+// (2^-8 of each, as the draft pass does: the value operand is bf16, and both operands have one
+// type); their sum is that of the unrounded ones, in fp32.
+//
+// Values that a row does not see never reach it: slots behind the last visible one are cleared in
+// shared memory before the product, and in the slots that only some rows see (a draft block) values
+// that are not finite are cleared and added to the rows that see them at the end.
+#include <atomic>
+
+#include <cuda.h>
+
+#include "shared_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace peagle {
+namespace sha {
+
+namespace {
+
+constexpr int TT = 128;      // slots a tile, rows a tile
+constexpr int CTAS = 152;
+constexpr int ENTRY = 3;     // what a unit costs besides its tiles, in tiles
+constexpr int MIN_SHARE = 4; // (of at least 2: a share between two others then has a tile of a pair)
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
+constexpr float LOG2E = 1.44269504f;
+constexpr float LAZY = 8.f;
+
+template <int HD>
+struct Smem {
+  static constexpr int QB = TT * HD * 2;    // a row tile's queries
+  static constexpr int SLOT = TT * HD * 2;  // a tile's keys, or its values
+  static constexpr int RING = HD == 64 ? 10 : 5;
+  static constexpr int BYTES = 2 * QB + RING * SLOT + 1024;  // (aligned to 1024)
+};
+
+// The waits that peagle_set_wait_limit_shared can make unreachable.
+enum Wait { SLOT_FREE, Q_FULL, S_FULL, P_FULL, O_FULL, WAITS };
+constexpr unsigned long long DEFAULT_WAIT_NS = 2000000000ull;
+std::atomic<unsigned long long> wait_limit{DEFAULT_WAIT_NS};
+std::atomic<int> unreachable{-1};
+
+// Row slots of the workspace: prefix units of 2 x 128, own units of 2 x KG, CTAs of 2 x 128.
+struct Layout {
+  int units;           // of the prefix
+  int64_t own, cta;    // first row slot of each kind
+  int64_t rows;
+  int64_t header;      // bytes of the plan: the share, and each request's first cost
+};
+__host__ __device__ inline Layout layout_of(int64_t batch, int K, int G, int nkv) {
+  Layout l;
+  const int64_t tiles = (batch * K * G + TT - 1) / TT;
+  l.units = (int)((tiles + 1) / 2 * nkv);
+  l.own = (int64_t)l.units * 2 * TT;
+  l.cta = l.own + batch * nkv * 2 * K * G;
+  l.rows = l.cta + (int64_t)CTAS * 2 * TT;
+  l.header = ((batch + 1) * 8 + 255) / 256 * 256;
+  return l;
+}
+
+// Costs of the call, the same in every CTA and in the join.
+struct Costs {
+  int tiles;         // of the prefix
+  int pairs;         // of a kv head
+  int pair, single;  // cost of a unit
+  int64_t head, prefix;
+};
+__device__ __forceinline__ Costs costs_of(const Args& a, int prefix) {
+  Costs c;
+  c.tiles = cdiv(prefix, TT);
+  const int rows = cdiv(a.batch * a.K * a.G, TT);
+  c.pairs = rows / 2;
+  c.pair = c.tiles ? 2 * c.tiles + ENTRY : 0;
+  c.single = c.tiles && (rows & 1) ? c.tiles + ENTRY : 0;
+  c.head = (int64_t)c.pairs * c.pair + c.single;
+  c.prefix = c.head * a.nkv;
+  return c;
+}
+__device__ __forceinline__ int own_cost(const Args& a, int b) {
+  const int n = slots_of(a, b);
+  return n > 0 ? cdiv(n, TT) + ENTRY : 0;
+}
+
+// Tiles of a unit that begins at `start` (in cost) with `step` a tile, from cost `at` on.
+__device__ __forceinline__ int tile_from(int64_t at, int64_t start, int step, int tiles) {
+  const int64_t d = at - start - ENTRY;
+  if (d <= 0) return 0;
+  const int64_t t = step == 2 ? (d + 1) >> 1 : d;
+  return t < tiles ? (int)t : tiles;
+}
+
+struct Unit {
+  int b;        // request, or -1: the prefix
+  int h;
+  int row;      // first row: of the kv head's rows in the batch, or of the request's
+  int rows;     // of both groups' tiles together
+  bool pair;
+  int slots;    // that its last row sees
+  int t0, t1;   // this CTA's tiles
+  int64_t place;  // its own row slots in the workspace
+  int stride;     // of the groups' places in them
+};
+
+// Walks a CTA's units.
+struct Walk {
+  int64_t begin, end, start;  // the share; of the unit that comes next
+  int prefix;                 // slots
+  int u, b, h;                // next prefix unit of head h, or (u < 0) request b's head h
+};
+
+template <typename L>
+__device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const L& l, Walk& w, Unit& x) {
+  while (w.start < w.end) {
+    const int64_t start = w.start;
+    int tiles, step;
+    if (w.u >= 0) {
+      x.b = -1;
+      x.h = w.h;
+      x.pair = w.u < c.pairs;
+      x.row = w.u * 2 * TT;
+      x.rows = min(2 * TT, a.batch * a.K * a.G - x.row);
+      x.slots = w.prefix;
+      tiles = c.tiles;
+      step = x.pair ? 2 : 1;
+      x.place = (int64_t)(w.h * (l.units / a.nkv) + w.u) * 2 * TT;
+      x.stride = TT;
+      w.start += x.pair ? c.pair : c.single;
+      if (++w.u == l.units / a.nkv) {
+        w.u = 0;
+        if (++w.h == a.nkv) {
+          w.u = -1;
+          w.h = w.b = 0;
+        }
+      }
+    } else {
+      if (w.b >= a.batch) return false;
+      x.b = w.b;
+      x.h = w.h;
+      x.pair = false;
+      x.row = 0;
+      x.rows = a.K * a.G;
+      x.slots = slots_of(a, w.b);
+      tiles = x.slots > 0 ? cdiv(x.slots, TT) : 0;
+      step = 1;
+      x.place = l.own + ((int64_t)w.b * a.nkv + w.h) * 2 * a.K * a.G;
+      x.stride = a.K * a.G;
+      w.start += tiles ? tiles + ENTRY : 0;
+      if (++w.h == a.nkv) {
+        w.h = 0;
+        ++w.b;
+      }
+    }
+    x.t0 = tile_from(w.begin, start, step, tiles);
+    x.t1 = tile_from(w.end, start, step, tiles);
+    if (x.t0 < x.t1) return true;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* errors,
+                                       unsigned long long limit_ns) {
+  if (tc::mbar_wait(bar, parity, abort, limit_ns)) return true;
+  if (!*abort) raise_error(reinterpret_cast<unsigned*>(errors), PEAGLE_DEV_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int lbo) {
+  return (tc::smem_desc_sw128(addr) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(lbo >> 4) << 16;
+}
+// D (+)= A B with A in tensor memory: two 16-bit elements a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 16-byte chunk c of row r of a 128-byte-swizzled tile
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+struct Barriers {
+  uint64_t full[10], empty[10];  // ring slots
+  uint64_t q[2], s[2], p[2], o[2];
+  uint64_t end;
+};
+
+// Ring entries of a piece of n tiles, in order: K 0, K 1, V 0, K 2, V 1, ...
+__device__ __forceinline__ int key_entry(int t) { return t ? 2 * t - 1 : 0; }
+__device__ __forceinline__ int value_entry(int t, int n) { return min(n, t + 2) + t; }
+
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1)
+    shared_attn_kernel(const __grid_constant__ CUtensorMap prefix_k, const __grid_constant__ CUtensorMap prefix_v,
+                       const __grid_constant__ CUtensorMap own_k, const __grid_constant__ CUtensorMap own_v, Args a,
+                       unsigned long long limit_ns, int never) {
+  typedef Smem<HD> M;
+  constexpr int RING = M::RING, HALVES = HD / 64;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = sm + 2 * M::QB;
+  __shared__ Barriers bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_b;
+  __shared__ unsigned long long s_total;
+  __shared__ long long s_start;
+  __shared__ int s_odd[2][2];  // whether a group met a draft value that is not finite; by its units in turn
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
+  tc::pdl_launch_dependents();
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_total = 0;
+    const auto count = [&](int kind, int n) { return (uint32_t)(n + (never == kind)); };
+    for (int i = 0; i < RING; ++i) {
+      tc::mbar_init(&bar.full[i], 1);
+      tc::mbar_init(&bar.empty[i], count(SLOT_FREE, 1));
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&bar.q[w], count(Q_FULL, TT));
+      tc::mbar_init(&bar.s[w], count(S_FULL, 1));
+      tc::mbar_init(&bar.p[w], count(P_FULL, TT));
+      tc::mbar_init(&bar.o[w], count(O_FULL, 1));
+    }
+    tc::mbar_init(&bar.end, 1);
+    s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&prefix_k);
+    tc::tma_prefetch_desc(&prefix_v);
+    tc::tma_prefetch_desc(&own_k);
+    tc::tma_prefetch_desc(&own_v);
+  }
+  if (warp == MMA_WARP) {
+    tc::tmem_alloc(&s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  const int prefix = prefix_of(a);
+  const Costs c = costs_of(a, max(prefix, 0));
+  unsigned long long mine = 0;
+  if (prefix >= 0)
+    for (int b = tid; b < a.batch; b += THREADS) mine += own_cost(a, b);
+  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0 && mine) atomicAdd(&s_total, mine * a.nkv);
+  __syncthreads();
+  const int64_t total = prefix >= 0 ? c.prefix + (int64_t)s_total : 0;
+  const int64_t share = max((int64_t)MIN_SHARE, (total + CTAS - 1) / CTAS);
+  Walk walk;
+  walk.begin = blockIdx.x * share;
+  walk.end = min(total, walk.begin + share);
+  walk.prefix = prefix;
+  if (warp == 0) {
+    // the request that the share begins in; CTA 0 leaves every request's first cost for the join
+    long long* plan = reinterpret_cast<long long*>(a.part);
+    if (blockIdx.x == 0 && lane == 0) plan[0] = share;
+    int64_t run = c.prefix;
+    int b0 = a.batch;
+    int64_t at = total;
+    for (int b = 0; b < a.batch && (blockIdx.x == 0 || b0 == a.batch); b += 32) {
+      const int64_t x = b + lane < a.batch && prefix >= 0 ? (int64_t)own_cost(a, b + lane) * a.nkv : 0;
+      int64_t sum = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const int64_t first = run + sum - x;
+      if (blockIdx.x == 0 && b + lane < a.batch) plan[1 + b + lane] = first;
+      const unsigned in = __ballot_sync(0xffffffffu, x > 0 && first + x > walk.begin);
+      if (in && b0 == a.batch) {
+        b0 = b + __ffs(in) - 1;
+        at = __shfl_sync(0xffffffffu, first, __ffs(in) - 1);
+      }
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      s_b = b0;
+      s_start = at;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  if (walk.begin < c.prefix) {
+    walk.h = (int)(walk.begin / c.head);
+    const int64_t rest = walk.begin - walk.h * c.head;
+    walk.u = min((int)(rest / c.pair), c.pairs);
+    if (c.pair == 0) walk.u = 0;
+    walk.start = walk.h * c.head + (int64_t)walk.u * c.pair;
+    walk.b = 0;
+  } else {
+    walk.u = -1;
+    walk.b = s_b;
+    walk.start = s_start;
+    walk.h = 0;
+    if (s_b < a.batch && walk.begin > walk.start) {
+      const int cost = own_cost(a, s_b);
+      walk.h = (int)((walk.begin - walk.start) / cost);
+      walk.start += (int64_t)walk.h * cost;
+    }
+  }
+  volatile int* abort = &s_abort;
+  const auto wait = [&](uint64_t* b, uint32_t parity) {
+    return tc::mbar_try_wait(b, parity) || wait_long(b, parity, abort, a.errors, limit_ns);
+  };
+  Unit x;
+
+  if (warp == LOAD_WARP) {
+    if (lane == 0) {
+      const uint64_t keep = tc::policy_evict_last(), once = tc::policy_evict_first();
+      int it = 0;
+      bool on = true;
+      while (on && next_unit(a, c, l, walk, x)) {
+        const bool shared = x.b < 0;
+        const int z = shared ? x.h : x.b * a.nkv + x.h;
+        // (a prefix that several row tiles read again stays in the cache)
+        const uint64_t policy = shared && l.units > a.nkv ? keep : once;
+        const int n = x.t1 - x.t0;
+        const auto load = [&](const CUtensorMap* map, int t) {
+          const int slot = it % RING;
+          if (it >= RING && !wait(&bar.empty[slot], (uint32_t)(it / RING - 1) & 1)) return false;
+          tc::mbar_expect_tx(&bar.full[slot], M::SLOT);
+#pragma unroll
+          for (int half = 0; half < HALVES; ++half)
+            tc::tma_load_3d(ring + slot * M::SLOT + half * TT * 128, map, half * 64, (x.t0 + t) * TT, z,
+                            &bar.full[slot], policy);
+          ++it;
+          return true;
+        };
+        const CUtensorMap* mk = shared ? &prefix_k : &own_k;
+        const CUtensorMap* mv = shared ? &prefix_v : &own_v;
+        on = load(mk, 0);
+        for (int t = 0; on && t < n; ++t) {
+          if (t + 1 < n) on = load(mk, t + 1);
+          on = on && load(mv, t);
+        }
+      }
+      // no CTA ends with a copy in flight (those before the last RING are done: their slots were free)
+      for (int i = max(0, it - RING); i < it; ++i) {
+        const unsigned long long t0 = tc::globaltimer();
+        while (!tc::mbar_try_wait(&bar.full[i % RING], (uint32_t)(i / RING) & 1) &&
+               tc::globaltimer() - t0 < DEFAULT_WAIT_NS) {
+        }
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    if (lane == 0) {
+      const uint32_t base = tc::smem_u32(sm), rings = tc::smem_u32(ring);
+      const uint32_t idS = tc::idesc_bf16(TT, TT), idO = tc::idesc_bf16(TT, HD) | (1u << 16);
+      uint32_t it = 0, nq[2] = {}, np[2] = {};
+      bool on = true;
+      while (on && next_unit(a, c, l, walk, x)) {
+        const int n = x.t1 - x.t0;
+        const int count[2] = {x.pair ? n : (n + 1) / 2, x.pair ? n : n / 2};
+        // S of group w's step i
+        const auto scores = [&](int w, int i) {
+          const int t = x.pair ? i : 2 * i + w;
+          const uint32_t e = it + key_entry(t), slot = e % RING;
+          if (!wait(&bar.full[slot], (e / RING) & 1)) return false;
+          tc::fence_after_sync();
+          const uint64_t dq = operand_desc(base + w * M::QB, 16), dk = operand_desc(rings + slot * M::SLOT, 16);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            tc::mma_bf16(tmem + w * TT, dq + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2,
+                         dk + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2, idS, k > 0);
+          tc::mma_commit(&bar.s[w]);
+          if (!x.pair || w == 1) tc::mma_commit(&bar.empty[slot]);
+          return true;
+        };
+        for (int w = 0; on && w < 2; ++w)
+          if (count[w]) on = wait(&bar.q[w], nq[w]++ & 1) && scores(w, 0);
+        for (int i = 0; on && i < count[0]; ++i)
+          for (int w = 0; on && w < 2; ++w) {
+            if (i >= count[w]) continue;
+            const int t = x.pair ? i : 2 * i + w;
+            const uint32_t e = it + value_entry(t, n), slot = e % RING;
+            on = wait(&bar.p[w], np[w]++ & 1) && wait(&bar.full[slot], (e / RING) & 1);
+            if (!on) break;
+            tc::fence_after_sync();
+            const uint64_t dv = operand_desc(rings + slot * M::SLOT, TT * 128);
+#pragma unroll
+            for (int k = 0; k < TT / 16; ++k)
+              mma_bf16_ts(tmem + 2 * TT + w * HD, tmem + w * TT + k * 8, dv + k * (16 * 128 >> 4), idO,
+                          i > 0 || k > 0);
+            if (!x.pair || w == 1) tc::mma_commit(&bar.empty[slot]);
+            if (i + 1 < count[w])
+              on = scores(w, i + 1);
+            else
+              tc::mma_commit(&bar.o[w]);
+          }
+        it += 2 * n;
+      }
+    }
+  } else {
+    const int w = warp >> 2, r = tid & (TT - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + w * TT, tO = tmem + lanes + 2 * TT + w * HD;
+    const float qs = fmaxf(fabsf(a.scale) * LOG2E, 0x1p-126f);
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    Stat* stat = reinterpret_cast<Stat*>(reinterpret_cast<char*>(a.part) + l.header);
+    float* sums = reinterpret_cast<float*>(stat + l.rows);
+    uint32_t it = 0, ns = 0, no = 0;
+    bool on = true;
+    while (on && next_unit(a, c, l, walk, x)) {
+      const int n = x.t1 - x.t0, count = x.pair ? n : (n + 1 - w) / 2;
+      const uint32_t first = it;
+      it += 2 * n;
+      if (!count) continue;
+      const int at = x.pair ? w * TT + r : r;  // of the unit's rows
+      const bool in = at < x.rows;
+      const bool live = (at & ~31) < x.rows;   // any row of the warp
+      const int rr = x.row + at, bk = (x.b < 0 ? 0 : x.b * a.K) + rr / a.G, head = x.h * a.G + rr % a.G;
+      {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (int64_t)bk * a.q_stride +
+                                                        (size_t)head * HD);
+        uint8_t* to = sm + w * M::QB;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          uint4 y = in ? q[i] : make_uint4(0, 0, 0, 0);
+          y.x ^= flip, y.y ^= flip, y.z ^= flip, y.w ^= flip;
+          *reinterpret_cast<uint4*>(to + (i / 8) * TT * 128 + sw128(r, i % 8)) = y;
+        }
+        fence_proxy_async_smem();
+        tc::mbar_arrive(&bar.q[w]);
+      }
+      const int all = x.b < 0 ? x.slots : limit_of(a, x.slots, 0);  // slots that every row sees
+      const int limit = x.b < 0 ? x.slots : limit_of(a, x.slots, min(rr / a.G, a.K - 1));
+      float m = -INFINITY, sum = 0.f;
+      for (int i = 0; i < count; ++i) {
+        const int t = x.pair ? i : 2 * i + w, slot0 = (x.t0 + t) * TT;
+        on = __all_sync(0xffffffffu, wait(&bar.s[w], ns++ & 1));
+        if (!on) break;
+        tc::fence_after_sync();
+        const bool edge = slot0 + TT > all;
+        if (live) {
+          float s[TT];
+#pragma unroll
+          for (int k = 0; k < TT; k += 32) tc::tmem_ld32(tS + k, s + k);
+          tc::tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+              if (slot0 + k >= limit) s[k] = -INFINITY;
+          }
+          float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k < TT; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * qs;
+          float scale = 1.f;
+          if (mx > m + LAZY || (m == -INFINITY && mx > -INFINITY)) {
+            scale = m == -INFINITY ? 0.f : ex2(m - mx);
+            m = mx;
+          }
+          const float ref = m == -INFINITY ? 0.f : -m;
+          float add[4] = {};
+          float packed[TT / 2];
+#pragma unroll
+          for (int k = 0; k < TT; k += 2) {
+            const float p0 = ex2(fmaf(s[k], qs, ref)), p1 = ex2(fmaf(s[k + 1], qs, ref));
+            add[(k >> 1) & 3] += p0 + p1;
+            packed[k / 2] = __uint_as_float(pack2(p0, p1));
+          }
+          sum = sum * scale + ((add[0] + add[1]) + (add[2] + add[3]));
+          if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
+#pragma unroll
+            for (int k = 0; k < HD; k += 32) {
+              float o[32];
+              tc::tmem_ld32(tO + k, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int d = 0; d < 32; ++d) o[d] *= scale;
+              tc::tmem_st32(tO + k, o);
+            }
+          }
+          tc::tmem_st32(tS, packed);
+          tc::tmem_st32(tS + 32, packed + 32);
+          tc::tmem_st_wait();
+        }
+        if (edge) {
+          // this thread's slot of the values: behind every row's limit, or seen by some rows
+          const uint32_t e = first + value_entry(t, n);
+          on = __all_sync(0xffffffffu, wait(&bar.full[e % RING], (e / RING) & 1));
+          if (!on) break;
+          uint8_t* v = ring + e % RING * M::SLOT;
+          if (slot0 + r >= x.slots) {
+#pragma unroll
+            for (int k = 0; k < HD / 8; ++k)
+              *reinterpret_cast<uint4*>(v + (k / 8) * TT * 128 + sw128(r, k % 8)) = make_uint4(0, 0, 0, 0);
+          } else if (slot0 + r >= all) {
+            for (int k = 0; k < HD / 8; ++k) {
+              uint4* p = reinterpret_cast<uint4*>(v + (k / 8) * TT * 128 + sw128(r, k % 8));
+              uint32_t y[4] = {p->x, p->y, p->z, p->w};
+              bool odd = false;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                if ((y[d] & 0x7f80u) == 0x7f80u) y[d] &= 0xffff0000u, odd = true;
+                if ((y[d] & 0x7f800000u) == 0x7f800000u) y[d] &= 0xffffu, odd = true;
+              }
+              if (odd) {
+                *p = make_uint4(y[0], y[1], y[2], y[3]);
+                *(volatile int*)&s_odd[w][no & 1] = 1;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bar.p[w]);
+      }
+      if (!on) break;
+      on = __all_sync(0xffffffffu, wait(&bar.o[w], no & 1));
+      if (!on) break;
+      tc::fence_after_sync();
+      // every thread of the group is behind its last unit, whose flag serves the next one
+      const bool odd = *(volatile int*)&s_odd[w][no & 1];
+      if (r == 0) *(volatile int*)&s_odd[w][~no & 1] = 0;
+      ++no;
+      if (live) {
+        float o[HD];
+#pragma unroll
+        for (int k = 0; k < HD; k += 32) tc::tmem_ld32(tO + k, o + k);
+        tc::tmem_ld_wait();
+        if (in && odd) {
+          const bf16* v = static_cast<const bf16*>(a.v) + ((size_t)x.b * a.nkv + x.h) * a.cap * HD;
+          for (int slot = all; slot < limit; ++slot) {
+            const int t = slot / TT - x.t0;
+            if (t < 0 || t >= n || (t & 1) != w) continue;  // another group's, or CTA's
+#pragma unroll
+            for (int d = 0; d < HD; ++d) {
+              const float y = __bfloat162float(v[(size_t)slot * HD + d]);
+              if (!(fabsf(y) < INFINITY)) o[d] += y;
+            }
+          }
+        }
+        if (in) {
+          const int64_t place = (x.t0 ? l.cta + (int64_t)blockIdx.x * 2 * TT + w * TT : x.place + w * x.stride) + r;
+          stat[place] = {m, sum};
+          float4* to = reinterpret_cast<float4*>(sums + place * HD);
+#pragma unroll
+          for (int d = 0; d < HD; d += 4) to[d / 4] = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+        }
+      }
+      tc::fence_before_sync();
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    if (lane == 0) {
+      // products that were issued and not waited for (after a wait that ran out) end first
+      tc::mma_commit(&bar.end);
+      const unsigned long long t0 = tc::globaltimer();
+      while (!tc::mbar_try_wait(&bar.end, 0) && tc::globaltimer() - t0 < DEFAULT_WAIT_NS) {
+      }
+    }
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins a row's pieces; a warp a row and head.
+template <int HD>
+__global__ void __launch_bounds__(256) shared_join_kernel(Args a) {
+  constexpr int DL = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = (int)(i / a.nq), head = (int)(i % a.nq);
+  tc::pdl_wait();
+  if (row >= a.batch * a.K) return;
+  const int prefix = prefix_of(a), b = row / a.K, slots = prefix < 0 ? -1 : slots_of(a, b);
+  if (slots < 0) {
+    if (lane == 0) raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_KV_OVERFLOW);
+    return;
+  }
+  const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
+  const Costs c = costs_of(a, prefix);
+  const long long* plan = reinterpret_cast<const long long*>(a.part);
+  const int64_t share = plan[0];
+  const Stat* stat = reinterpret_cast<const Stat*>(reinterpret_cast<const char*>(a.part) + l.header);
+  const float* sums = reinterpret_cast<const float*>(stat + l.rows);
+  const int h = head / a.G, g = head % a.G;
+  float m = -INFINITY, total = 0.f, o[DL] = {};
+  const auto add = [&](int64_t place) {
+    const Stat s = stat[place];
+    if (s.l == 0.f) return;
+    const float top = fmaxf(m, s.m), x = exp2f(m - top), y = exp2f(s.m - top);
+    total = total * x + s.l * y;
+    const float* from = sums + place * HD + lane * DL;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) o[d] = fmaf(o[d], x, y * from[d]);
+    m = top;
+  };
+  // a unit's pieces: group `w`'s sums of each, or both groups' where they share the rows
+  const auto unit = [&](int64_t start, int tiles, bool pair, int w, int64_t place, int stride, int r) {
+    const int step = pair ? 2 : 1;
+    const int64_t c0 = (start + ENTRY) / share, c1 = (start + ENTRY + (int64_t)(tiles - 1) * step) / share;
+    for (int64_t k = c0; k <= c1; ++k) {
+      const int n = tile_from((k + 1) * share, start, step, tiles) - tile_from(k * share, start, step, tiles);
+      const int64_t at = k == c0 ? place : l.cta + k * 2 * TT;
+      const int by = k == c0 ? stride : TT;
+      if (pair) {
+        add(at + w * by + r);
+      } else {
+        add(at + r);
+        if (n > 1) add(at + by + r);
+      }
+    }
+  };
+  if (c.tiles) {
+    const int rr = row * a.G + g, u = rr / (2 * TT), r = rr % (2 * TT);
+    unit(h * c.head + (int64_t)u * c.pair, c.tiles, u < c.pairs, r / TT, (int64_t)(h * (l.units / a.nkv) + u) * 2 * TT,
+         TT, r % TT);
+  }
+  if (slots > 0) {
+    const int tiles = cdiv(slots, TT);
+    unit(plan[1 + b] + (int64_t)h * (tiles + ENTRY), tiles, false, 0, l.own + ((int64_t)b * a.nkv + h) * 2 * a.K * a.G,
+         a.K * a.G, (row % a.K) * a.G + g);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  bf16* out = static_cast<bf16*>(a.out) + ((size_t)row * a.nq + head) * HD + lane * DL;
+#pragma unroll
+  for (int d = 0; d < DL; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack2(o[d] * inv, o[d + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(size_t)row * a.nq + head] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718f;
+}
+
+typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                           const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                           CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+  static const Encode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (Encode)f;
+  }();
+  return fn;
+}
+
+// [heads][capacity][hd], boxes of 64 dims x 128 slots; slots from the capacity on read as zeros.
+bool tile_map(CUtensorMap* out, const void* base, int hd, int capacity, int64_t heads) {
+  const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)capacity, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)capacity * hd * 2};
+  const cuuint32_t box[3] = {64, TT, 1}, one[3] = {1, 1, 1};
+  const Encode f = encoder();
+  return f && f(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD>
+int launch(const Args& a, cudaStream_t st) {
+  CUtensorMap pk, pv, k, v;
+  if (!tile_map(&pk, a.pk, HD, a.pcap, a.nkv) || !tile_map(&pv, a.pv, HD, a.pcap, a.nkv) ||
+      !tile_map(&k, a.k, HD, a.cap, (int64_t)a.batch * a.nkv) || !tile_map(&v, a.v, HD, a.cap, (int64_t)a.batch * a.nkv))
+    return PEAGLE_ERR_CUDA;
+  if (smem_optin((const void*)shared_attn_kernel<HD>, Smem<HD>::BYTES) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, a, wait_limit.load(), unreachable.load());
+  if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
+  const int64_t warps = (int64_t)a.batch * a.K * a.nq;
+  return launch_pdl(shared_join_kernel<HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a) == cudaSuccess
+             ? PEAGLE_OK
+             : PEAGLE_ERR_CUDA;
+}
+
+}  // namespace
+
+int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd) {
+  const Layout l = layout_of(batch, K, G, nkv);
+  return l.header + l.rows * (hd + 2) * 4;
+}
+
+int launch_tc(const Args& a, int hd, cudaStream_t st) { return hd == 64 ? launch<64>(a, st) : launch<128>(a, st); }
+
+}  // namespace sha
+}  // namespace peagle
+
+extern "C" int peagle_set_wait_limit_shared(uint64_t limit_ns, int32_t unreachable_wait) {
+  using namespace peagle::sha;
+  if (unreachable_wait < -1 || unreachable_wait >= WAITS) return PEAGLE_ERR_INVALID;
+  wait_limit = limit_ns ? limit_ns : DEFAULT_WAIT_NS;
+  unreachable = unreachable_wait;
+  return PEAGLE_OK;
+}

@@ -674,6 +674,61 @@ int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* draft_tokens,
 /* Bytes of workspace that peagle_verify_sample needs, or a negative error. */
 int64_t peagle_verify_sample_workspace(int32_t batch, int32_t K, int32_t vocab);
 
+/* Decode attention of a batch whose requests share a long prefix (several samples of one prompt),
+ * for one layer: for request b, draft row j (rows b*K + j) and query head h, softmax(scale q . k) . v
+ * over the prefix's slots and, behind them, the request's own.  The prefix is read once for the
+ * whole batch.  The pages have no counterpart: peagle_draft's cache holds every request whole.
+ *   dtype    of q, out and both caches (peagle_dtype)
+ *   q, out   device [batch*K][n_q_heads][head_dim]; consecutive rows of q are q_stride elements apart
+ *            (0: n_q_heads * head_dim), a multiple of 16 bytes; out is contiguous and apart from q's
+ *            rows; both 16-byte aligned.  q and the keys are taken as already rotated.
+ *   prefix_k, prefix_v  device [n_kv_heads][prefix_capacity][head_dim], 16-byte aligned: one layer of a
+ *            peagle_kv of one request
+ *   prefix_len  device int32 [1]: slots 0 .. prefix_len - 1 are seen by every row
+ *   k_cache, v_cache  device [batch][n_kv_heads][capacity][head_dim], 16-byte aligned: one layer of a
+ *            peagle_kv that holds what follows the prefix
+ *   seq_lens device int32 [batch]: slots of each request's own cache
+ *   causal   1: row j sees the own slots 0 .. seq_lens[b] + j (the draft block's rows are in the
+ *            cache); 0: every row sees 0 .. seq_lens[b] - 1
+ *   scale    of the scores (1 / sqrt(head_dim) as a rule), finite also times log2(e)
+ *   out_lse  device fp32 [batch*K][n_q_heads]: the natural logarithm of the sum of exp(scale q . k); or
+ *            NULL
+ *   errors   device word as in peagle_kv_quant; or NULL
+ *   workspace  device memory of at least peagle_decode_attention_shared_workspace() bytes, 256-byte
+ *            aligned, no initial value; calls that may overlap on the GPU each have their own
+ * A row that sees no slot gives zeros (and -inf).  What lies in slots that a row does not see never
+ * reaches it, NaN included; a value that is not finite in a slot that it does see makes that dim of
+ * the row not finite.  fp32 scores, softmax, accumulation and lse; softmax weights of bf16 calls are
+ * rounded to bf16, as in the draft pass.  Results are the same on every call with the same lengths
+ * and sizes (no atomics).
+ * prefix_len outside 0 .. prefix_capacity, or a request with seq_lens[b] < 0 or whose last row's slot is
+ * beyond the capacity: KV_OVERFLOW, and the rows concerned are left as they are.  Waits inside the
+ * kernel are bounded; one that ran out raises TIMEOUT, and the call's results are not to be used.
+ * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; K * n_q_heads / n_kv_heads <= 128; batch * K *
+ * n_q_heads, prefix_capacity and capacity <= 2^24; n_kv_heads <= 65535.  A workspace that is too small is
+ * PEAGLE_ERR_CAPACITY. */
+int peagle_decode_attention_shared(int32_t dtype, int32_t batch, int32_t K, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim, const void* q,
+                                   int64_t q_stride, const void* prefix_k, const void* prefix_v,
+                                   int32_t prefix_capacity, const int32_t* prefix_len,
+                                   const void* k_cache, const void* v_cache, int32_t capacity,
+                                   const int32_t* seq_lens, int32_t causal, float scale, void* out,
+                                   float* out_lse, int32_t* errors, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that peagle_decode_attention_shared needs, or a negative error. */
+int64_t peagle_decode_attention_shared_workspace(int32_t dtype, int32_t batch, int32_t K,
+                                                 int32_t n_q_heads, int32_t n_kv_heads,
+                                                 int32_t head_dim, int32_t prefix_capacity,
+                                                 int32_t capacity);
+
+/* Failure-path drill of the waits inside peagle_decode_attention_shared's bf16 kernel, as
+ * peagle_set_wait_limit_quant is for the 8-bit cache: a wait gives up after limit_ns nanoseconds (0: the
+ * default of 2 s), and unreachable_wait >= 0 names one that can never succeed: 0 a copied tile's place to
+ * be free again, 1 queries, 2 scores, 3 weights, 4 outputs added up; -1 none.  For the process's calls
+ * that follow.  Returns PEAGLE_ERR_INVALID for another wait. */
+int peagle_set_wait_limit_shared(uint64_t limit_ns, int32_t unreachable_wait);
+
 /* Raw device error bits observed by the last peagle_status call. */
 int32_t peagle_device_error_bits(const peagle_ctx* ctx);
 
