@@ -3,14 +3,18 @@
 //
 // A cluster of 1, 2, 4 or 8 CTAs takes a row.  Each CTA brings its chunk of the row into shared memory
 // once (asynchronous 16-byte copies; the largest logit is found as they arrive) and all further
-// passes run there:
-//   cut       only with top-k or top-p: a histogram of the chunk over y = (x - M) log2(e) / T in steps
-//             of 1/8, counts and weights (16-bit parts of the weights, so that 32-bit additions
-//             hold), summed over the cluster; the bin in which the k-th token, or the top_p-th part
-//             of the mass, lies is gathered into a list and ranked, or divided again by the logits'
-//             own order while it holds more than LIST tokens
-//   sums      the kept tokens' weights, a sum for each warp's span of the row
-//   locate    the span in which u S falls, divided again over one CTA's warps
+// passes run there.
+//   short   most filtered rows keep few tokens, and a bound below which none is kept costs one
+//           comparison a logit: the k-th largest of the threads' own maxima for top-k, and for top-p
+//           w >= (1 - p) S / (2 vocab) (all that lies below has less than (1 - p) S).  The tokens
+//           above it, up to LIST of them, go to the row's first CTA, which sorts them, cuts the
+//           order by k, p and min_p, sorts what is left by index and picks.
+//   long    otherwise the border is found over the whole row: a histogram over y = (x - M) log2(e) / T
+//           in steps of 1/8, counts and weights (16-bit parts of the weights, so that 32-bit
+//           additions hold), summed over the cluster; the bin in which the k-th token, or the top_p-th
+//           part of the mass, lies is gathered and ranked, or divided again by the logits' own order
+//           while it holds more than RANK tokens.  Then the kept tokens' weights are summed up for
+//           each warp's span of the row, and the span in which u S falls is divided again.
 // Sums are whole numbers (sample.cuh), so nothing depends on their order.
 #include "sample.cuh"
 
@@ -20,7 +24,7 @@ namespace smp {
 namespace {
 
 constexpr int BINS = THREADS;  // one a thread in the cluster's sum
-constexpr int LIST = 256;
+constexpr int RANK = 256;
 
 struct Args {
   const void* logits;
@@ -36,22 +40,24 @@ struct Args {
   int* token;
   float* prob;
   peagle_dist* dist;
+  RowList list;  // (with u NULL) the kept tokens of short rows
   int* errors;
 };
 
 struct Shared {
   union {
     uint4 hist[BINS];    // count, and three 16-bit parts of the weights
-    struct {             // (of a bin that is not divided again)
-      u64 list[LIST];    // key and index of the boundary bin's tokens: this CTA's
+    struct {
+      u64 list[LIST];    // key and index of tokens: this CTA's
       u64 all[LIST];     // the cluster's
-      u64 weight[LIST];
     };
   };
+  u64 weight[LIST];
   u64 red64[WARPS];
   uint32_t red32[WARPS];
   Locate find;
-  uint32_t top, bad;     // this CTA's largest key, and whether it holds a NaN or +inf
+  uint32_t top;          // this CTA's largest key (all ones: a NaN)
+  u64 sum;               // this CTA's weights
   uint32_t count, low, high;  // of the list; smallest and largest key in the boundary bin
   uint32_t first;        // lowest index of the largest logit
   // what one thread finds for all
@@ -71,11 +77,24 @@ struct Row {
   int n, base;
 };
 
-template <typename T>
-__device__ __forceinline__ void see(T raw, float& top, bool& bad) {
-  const float x = to_f32(raw);
-  top = fmaxf(top, x);
-  bad |= !(x < INFINITY);
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // bf16
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest of 16 bytes of logits and `top`, or NaN.
+__device__ __forceinline__ float top_of(uint4 v, float top, float) {
+  return max_nan(max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                         max_nan(__uint_as_float(v.z), __uint_as_float(v.w))), top);
+}
+__device__ __forceinline__ float top_of(uint4 v, float top, bf16) {
+  const uint32_t m = max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w));
+  return max_nan(max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)), top);
 }
 
 // Until at most `left` groups of this thread's copies are in flight.
@@ -87,9 +106,9 @@ __device__ __forceinline__ void wait_copies(int left) {
 }
 
 // Copies n logits from src into shared memory at the same place within 16 bytes, and finds the
-// largest and whether one is not a number (or +inf).
+// largest (NaN if one is).
 template <typename T>
-__device__ __forceinline__ void load_chunk(const T* src, T* dst, int n, float& top, bool& bad) {
+__device__ __forceinline__ void load_chunk(const T* src, T* dst, int n, float& top) {
   constexpr int PER = 16 / sizeof(T), GROUPS = 4;
   const int tid = threadIdx.x;
   const int phase = (int)(((uintptr_t)src & 15) / sizeof(T));
@@ -106,17 +125,32 @@ __device__ __forceinline__ void load_chunk(const T* src, T* dst, int n, float& t
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  if (tid < head) see(dst[tid] = src[tid], top, bad);
-  if (tid < tail) see(d[vecs * PER + tid] = s[vecs * PER + tid], top, bad);
+  if (tid < head) top = max_nan(top, to_f32(dst[tid] = src[tid]));
+  if (tid < tail) top = max_nan(top, to_f32(d[vecs * PER + tid] = s[vecs * PER + tid]));
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
     wait_copies(GROUPS - 1 - g);
-    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS) {
-      T piece[PER];
-      *reinterpret_cast<uint4*>(piece) = *reinterpret_cast<const uint4*>(d + v * PER);
-#pragma unroll
-      for (int k = 0; k < PER; ++k) see(piece[k], top, bad);
-    }
+    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS)
+      top = top_of(*reinterpret_cast<const uint4*>(d + v * PER), top, T());
+  }
+}
+
+// Calls f(x, place) for the logits at least `floor` of a chunk that load_chunk brought.
+template <typename T, typename F>
+__device__ __forceinline__ void above(const T* chunk, int n, float floor, F f) {
+  constexpr int PER = 16 / sizeof(T);
+  const int tid = threadIdx.x, phase = (int)((tc::smem_u32(chunk) & 15) / sizeof(T));
+  const int head = min(n, phase ? PER - phase : 0), vecs = (n - head) / PER, tail = n - head - vecs * PER;
+  const auto one = [&](int i) {
+    const float x = to_f32(chunk[i]);
+    if (x >= floor) f(x, i);
+  };
+  if (tid < head) one(tid);
+  if (tid < tail) one(head + vecs * PER + tid);
+  for (int v = tid; v < vecs; v += THREADS) {
+    const uint4 y = *reinterpret_cast<const uint4*>(chunk + head + v * PER);
+    if (top_of(y, -INFINITY, T()) >= floor)
+      for (int k = 0; k < PER; ++k) one(head + v * PER + k);
   }
 }
 
@@ -195,7 +229,7 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
   uint32_t low = 0, high = 0xffffffffu;  // the boundary set: bin, and keys low .. high
   bool ranged = false;
   while (true) {
-    const bool listed = in_n <= LIST;
+    const bool listed = in_n <= RANK;
     const bool divide = !listed && ranged;
     const int shift = divide ? max(0, 32 - __clz(high - low) - 9) : 0;
     if (divide && low == high) break;  // equal logits
@@ -292,7 +326,7 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
     before_w += sh.before_w;
     in_n = sh.in_n;
   }
-  // in_n > LIST equal logits: so many of them, the lowest indices first
+  // in_n > RANK equal logits: so many of them, the lowest indices first
   const float x = __uint_as_float(low & 0x80000000u ? low & 0x7fffffffu : ~low);
   const u64 each = weigh ? weight(x, s, tab) : 0;
   uint32_t m;
@@ -324,10 +358,95 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
   __syncthreads();
 }
 
+// The weights before which a token is kept: top_p of the mass, at least the first token's.
+__device__ __forceinline__ u64 part_of(float top_p, u64 mass) {
+  const double want = ceil((double)fmaxf(top_p, 0.f) * (double)mass);
+  return max(1ull, min(mass, (u64)want));
+}
+
+// Sorts a number of each of the first `size` threads (a power of two), the largest first.
+__device__ __forceinline__ u64 sort_down(u64 v, int size, u64* buf) {
+  const int tid = threadIdx.x;
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      u64 o;
+      if (j >= 32) {
+        __syncthreads();
+        buf[tid] = v;
+        __syncthreads();
+        o = buf[tid ^ j];
+      } else {
+        o = __shfl_xor_sync(0xffffffffu, v, j);
+      }
+      if (((tid & j) == 0) == ((tid & k) == 0 || k == size) ? o > v : o < v) v = o;
+    }
+  return v;
+}
+__device__ __forceinline__ int size_for(int n) { return n < 2 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// One CTA's end of a short row: n candidates (sh.all) that hold every kept token.  mass: of the whole
+// row, unless it is the first top_k candidates' (mine).
+__device__ __forceinline__ void finish(Shared& sh, const Args& a, int r, int n, const Scale& s, const Table& tab,
+                                       float top, float temperature, int frac, int top_k, bool by_p, float top_p,
+                                       u64 mass, bool mine, uint32_t min_key) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  u64 me = tid < n ? sh.all[tid] : 0;
+  me = sort_down(me, size_for(n), sh.list);
+  const uint32_t key = (uint32_t)(me >> 32);
+  const int index = (int)(0xffffffffu - (uint32_t)me);
+  u64 w = 0;
+  if ((tid & ~31) < n) w = weight(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab);
+  const bool first = tid < n && tid < top_k;
+  if (!first) w = 0;
+  u64 all;
+  const u64 run = block_scan(w, sh.red64, all);
+  const u64 want = by_p ? part_of(top_p, mine ? all : mass) : ~0ull;
+  const bool in = first && run - w < want, keep = in && key >= min_key;
+  sh.weight[tid] = w;
+  sh.all[tid] = me;
+  const int cut = __syncthreads_count(in), m = __syncthreads_count(keep);
+  if (tid == cut - 1) {
+    sh.least = max(key, min_key);
+    sh.last = key >= min_key ? index : 0x7fffffff;
+  }
+  if (tid == m - 1) sh.kept_w = run;
+  // by index
+  const u64 order = sort_down(keep ? ~((u64)index << 16 | tid) : 0, size_for(m), sh.list);
+  __syncthreads();
+  const u64 total = sh.kept_w;
+  const int i = (int)(~order >> 16), from = (int)(~order & 0xffff);
+  w = tid < m ? sh.weight[from] : 0;
+  peagle_dist d = {total, top, temperature, sh.least, sh.last, -1, a.vocab};
+  if (!a.u) {
+    if (tid == 0) {
+      a.dist[r] = d;
+      if (a.list.count) a.list.count[r] = m;
+    }
+    if (a.list.count && tid < m) {
+      a.list.index[(int64_t)r * LIST + tid] = i;
+      a.list.weight[(int64_t)r * LIST + tid] = w;
+    }
+    return;
+  }
+  const u64 target = target_of(a.u[r], total);
+  const u64 up = block_scan(w, sh.red64, all);
+  if (up - w <= target && target < up) {
+    const uint32_t k = (uint32_t)(sh.all[from] >> 32);
+    d.index = i;
+    if (a.token) a.token[r] = i + (a.d2t ? a.d2t[i] : 0);
+    if (a.prob)
+      a.prob[r] = (float)(weight64(__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), top, temperature) *
+                          (double)(1ull << frac) / (double)total);
+    if (a.dist) a.dist[r] = d;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   extern __shared__ uint4 dynamic[];
   __shared__ Shared sh;
+  tc::pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
   const int r = blockIdx.x / ctas, set = r / a.rows_per;
@@ -345,37 +464,33 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   T* chunk = reinterpret_cast<T*>(reinterpret_cast<char*>(dynamic) + ((uintptr_t)src & 15));
   row.x = chunk;
   float top = -INFINITY;
-  bool bad = false;
-  load_chunk(src, chunk, row.n, top, bad);
-  top = warp_max(top);
-  bad = __any_sync(0xffffffffu, bad);
+  load_chunk(src, chunk, row.n, top);
+  const float mine = top;  // this thread's own
+  uint32_t key = top == top ? order_key(top) : 0xffffffffu;
+  key = __reduce_max_sync(0xffffffffu, key);
   if (tid == 0) {
     sh.top = 0;
-    sh.bad = 0;
+    sh.sum = 0;
+    sh.count = 0;
     sh.first = 0xffffffffu;
     sh.least = 0;
     sh.last = 0x7fffffff;
   }
   sh.hist[tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  if (lane == 0) {
-    atomicMax(&sh.top, order_key(top));
-    if (bad) sh.bad = 1;
-  }
+  if (lane == 0) atomicMax(&sh.top, key);
   __syncthreads();
   cluster_barrier();
-  uint32_t top_key = 0, any_bad = 0;
-  for (int c = 0; c < ctas; ++c) {
-    top_key = max(top_key, remote_u32(&sh.top, c));
-    any_bad |= remote_u32(&sh.bad, c);
-  }
+  uint32_t top_key = 0;
+  for (int c = 0; c < ctas; ++c) top_key = max(top_key, remote_u32(&sh.top, c));
   top = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
-  const bool whole = !any_bad && top > -INFINITY && temperature >= 0.f;
+  const bool whole = top > -INFINITY && top < INFINITY && temperature >= 0.f;  // (top: NaN if any is)
   if (!whole) {  // no distribution
     if (rank == 0 && tid == 0) {
       if (a.token) a.token[r] = -1;
       if (a.prob) a.prob[r] = NAN;
       if (a.dist) a.dist[r] = {0ull, NAN, temperature, 0xffffffffu, -1, -1, a.vocab};
+      if (a.list.count) a.list.count[r] = 0;
       raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_BAD_ROW);
     }
     cluster_barrier();
@@ -394,6 +509,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
       if (a.token) a.token[r] = (int)first + (a.d2t ? a.d2t[first] : 0);
       if (a.prob) a.prob[r] = 1.f;
       if (a.dist) a.dist[r] = {1ull << frac, top, 0.f, top_key, (int)first, (int)first, a.vocab};
+      if (a.list.count) {
+        a.list.count[r] = 1;
+        a.list.index[(int64_t)r * LIST] = (int)first;
+        a.list.weight[(int64_t)r * LIST] = 1ull << frac;
+      }
     }
     cluster_barrier();
     return;
@@ -402,48 +522,93 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   const Scale s = make_scale(top, temperature, frac);
   const Table tab = load_table();
   const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
+  uint32_t min_key = 0;
+  if (min_p > 0.f) {
+    const float x = __double2float_ru((double)top + (double)temperature * log((double)fminf(min_p, 1.f)));
+    min_key = order_key(fminf(x, top));
+  }
   if (by_k || by_p) {
-    u64 sum = 0;
+    // a logit that no kept token is below
+    float floor = -INFINITY;
+    u64 mass = 0;
+    if (a.vocab > LIST) {
+      if (by_k) {
+        if (mine > -INFINITY) atomicAdd(&sh.hist[bin_of(mine, s)].x, 1u);
+        __syncthreads();
+        cluster_barrier();
+        uint32_t n;
+        u64 w;
+        merge_bins(sh, ctas, n, w);
+        find_bin(sh, n, w, true, (uint32_t)top_k, 0);
+        if (sh.bin < BINS - 1)  // (else: fewer threads than k)
+          floor = __double2float_rd((double)top - (sh.bin + 1) / 8.0 / (double)s.ch * (1 + 1e-6));
+      } else {
+        u64 sum = 0;
+        for (int i = tid & ~31; i < row.n; i += THREADS)
+          sum += weight(i + lane < row.n ? to_f32(row.x[i + lane]) : -INFINITY, s, tab);
+        sum = warp_sum64(sum);
+        if (lane == 0) atomicAdd(&sh.sum, sum);
+        __syncthreads();
+        cluster_barrier();
+        for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
+        const double rest = (1.0 - (double)fmaxf(top_p, 0.f)) * (double)mass / (double)(1ull << frac);
+        floor = __double2float_rd((double)top + (double)temperature * log(rest / (2.0 * a.vocab)));
+      }
+      cluster_barrier();  // (the histogram's place holds the list)
+    }
+    above(chunk, row.n, floor, [&](float x, int i) {
+      const uint32_t at = atomicAdd(&sh.count, 1u);
+      if (at < LIST) sh.list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(row.base + i));
+    });
+    __syncthreads();
+    cluster_barrier();
+    int n = 0;
+    for (int c = 0; c < ctas; ++c) {
+      const int m = (int)remote_u32(&sh.count, c);
+      if (rank == 0 && n + m <= LIST && tid < m) sh.all[n + tid] = remote_u64(&sh.list[tid], c);
+      n += m;
+    }
+    cluster_barrier();
+    if (n <= LIST) {
+      if (rank == 0) finish(sh, a, r, n, s, tab, top, temperature, frac, by_k ? top_k : LIST, by_p, top_p, mass, by_k || a.vocab <= LIST, min_key);
+      return;
+    }
+    if (tid == 0) sh.count = 0;
+    sh.hist[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
     for (int i = tid & ~31; i < row.n; i += THREADS) {
       const int at = i + lane;
       const float x = at < row.n ? to_f32(row.x[at]) : -INFINITY;
       const u64 w = by_p ? weight(x, s, tab) : 0;
-      sum += w;
       if (at < row.n) add_bin(&sh.hist[bin_of(x, s)], w, by_p);
     }
     __syncthreads();
     cluster_barrier();
-    uint32_t n;
+    uint32_t tokens;
     u64 w;
-    merge_bins(sh, ctas, n, w);
-    u64 mass = 0;
+    merge_bins(sh, ctas, tokens, w);
     if (by_k) {
-      cut(sh, row, s, tab, ctas, by_p, true, (uint32_t)top_k, 0, n, w);
+      cut(sh, row, s, tab, ctas, by_p, true, (uint32_t)top_k, 0, tokens, w);
       mass = sh.kept_w;
     } else {
-      find_bin(sh, n, w, false, 0, ~0ull);
+      find_bin(sh, tokens, w, false, 0, ~0ull);
       mass = sh.before_w + sh.in_w;
     }
     if (by_p) {
       if (by_k) {
         // what the first cut left of the bins
-        if (tid > sh.first_bin) n = 0, w = 0;
+        if (tid > sh.first_bin) tokens = 0, w = 0;
         if (tid == sh.first_bin) w = mass - sh.first_before;
       }
-      const double want = ceil((double)fmaxf(top_p, 0.f) * (double)mass);
-      const u64 want_w = max(1ull, min(mass, (u64)want));
-      cut(sh, row, s, tab, ctas, true, false, 0, want_w, n, w);
+      const u64 want_w = part_of(top_p, mass);
+      cut(sh, row, s, tab, ctas, true, false, 0, want_w, tokens, w);
     }
   }
   uint32_t least = sh.least;
   int last = sh.last;
-  if (min_p > 0.f) {
-    const float x = __double2float_ru((double)top + (double)temperature * log((double)fminf(min_p, 1.f)));
-    const uint32_t key = order_key(fminf(x, top));
-    if (key > least) {
-      least = key;
-      last = 0x7fffffff;
-    }
+  if (min_key > least) {
+    least = min_key;
+    last = 0x7fffffff;
   }
   const auto weigh = [&](int i) -> u64 {
     const float x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
@@ -458,11 +623,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   const u64 total = total_of(sh.find, ctas);
   peagle_dist d = {total, top, temperature, least, last, -1, a.vocab};
   if (!a.u) {
-    if (rank == 0 && tid == 0) a.dist[r] = d;
+    if (rank == 0 && tid == 0) {
+      a.dist[r] = d;
+      if (a.list.count) a.list.count[r] = -1;
+    }
   } else {
-    const double u = a.u[r];
-    const double want = fmax(u, 0.0) * (double)total;  // (0 for a NaN)
-    const u64 target = want < (double)total ? min((u64)want, total - 1) : total - 1;
+    const u64 target = target_of(a.u[r], total);
     const int at = locate(sh.find, ctas, row.n, target, weigh);
     if (at >= 0 && lane == 0) {
       const int i = row.base + at;
@@ -509,7 +675,7 @@ int cluster_of(int rows, int vocab, int size) {
 
 int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* logits, int dtype,
                 int64_t row_stride, const float* u, const int* d2t, int* token, float* prob,
-                peagle_dist* dist, int* errors, cudaStream_t st) {
+                peagle_dist* dist, const RowList* list, int* errors, cudaStream_t st) {
   Args a = {};
   const int size = dtype == PEAGLE_F32 ? 4 : 2;
   const int ctas = cluster_of(rows, vocab, size);
@@ -529,6 +695,7 @@ int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* log
   a.token = token;
   a.prob = prob;
   a.dist = dist;
+  if (list) a.list = *list;
   a.errors = errors;
   return dtype == PEAGLE_F32 ? launch<float>(a, rows, ctas, st) : launch<bf16>(a, rows, ctas, st);
 }
@@ -565,5 +732,5 @@ extern "C" int peagle_sample(const peagle_sampling* how, int32_t rows, int32_t v
       (uintptr_t)errors % 4)
     return PEAGLE_ERR_INVALID;
   return peagle::smp::sample_rows(how, rows, vocab, logits, dtype, row_stride, uniforms, d2t,
-                                  out_tokens, out_prob, out_dist, errors, (cudaStream_t)stream);
+                                  out_tokens, out_prob, out_dist, nullptr, errors, (cudaStream_t)stream);
 }

@@ -17,10 +17,18 @@ namespace smp {
 
 typedef unsigned long long u64;
 
-// Host side (sample.cu).  u NULL: the rows' records only.
+// The kept tokens of rows that keep few: their indices in rising order, and weights, [rows][LIST].
+constexpr int LIST = 512;
+struct RowList {
+  int* count;  // [rows]: -1 where a row keeps too many
+  int* index;
+  u64* weight;
+};
+
+// Host side (sample.cu).  u NULL: the rows' records, and lists, only.
 int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* logits, int dtype,
                 int64_t row_stride, const float* u, const int* d2t, int* token, float* prob,
-                peagle_dist* dist, int* errors, cudaStream_t st);
+                peagle_dist* dist, const RowList* list, int* errors, cudaStream_t st);
 int check_rows(const peagle_sampling* how, int64_t rows, int vocab, const void* logits, int dtype,
                int64_t row_stride);
 
@@ -120,6 +128,12 @@ __device__ __forceinline__ bool kept(uint32_t key, int i, uint32_t least, int la
   return key > least || (key == least && i <= last);
 }
 
+// Where the running sum has to pass, of `total`, for a random number u.
+__device__ __forceinline__ u64 target_of(float u, u64 total) {
+  const double want = fmax((double)u, 0.0) * (double)total;  // (0 for a NaN)
+  return want < (double)total ? min((u64)want, total - 1) : total - 1;
+}
+
 // ---- cluster -------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
@@ -163,6 +177,22 @@ __device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {  // inclusive
   for (int o = 1; o < 32; o <<= 1) {
     const u64 x = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// Inclusive sums over the CTA's threads; the whole in `all`.
+__device__ __forceinline__ u64 block_scan(u64 v, u64* red, u64& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan64(v, lane);
+  __syncthreads();
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) {
+    if (k < warp) v += red[k];
+    all += red[k];
   }
   return v;
 }

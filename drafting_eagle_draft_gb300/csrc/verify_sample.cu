@@ -1,11 +1,13 @@
 // Verification of sampled drafts (peagle_verify_sample).
 //
-// Two launches.  The first leaves the records of the target's batch (K+1) rows (sample.cu: the rows'
-// one reading from memory).  In the second a cluster takes a request: its drafts are accepted or
-// not from K logits and records, and the bonus token is drawn from r_i = max(p_i - q_i, 0) over the
-// row of the first rejected one, which is mostly still in the L2 cache.
+// Two launches.  The first leaves the records of the target's batch (K+1) rows, and the kept tokens
+// of those that keep at most LIST (sample.cu: the rows' one reading from memory).  In the second a
+// cluster takes a request: its drafts are accepted or not from K logits and records, and the bonus
+// token is drawn from r_i = max(p_i - q_i, 0) over the row of the first rejected one.  Where that row
+// has a list, the first CTA does it alone: it looks the draft row's kept tokens up in the list.
+// Else all of them walk the row, which is mostly still in the L2 cache.
 //
-// q lives in the draft vocabulary: the cluster's CTAs share out the draft row, and write each kept
+// q lives in the draft vocabulary.  In the long form the cluster's CTAs share out the draft row, and write each kept
 // entry's index (plus 1) to its target token's place in the shared memory of the CTA that has that
 // token's chunk.  p and q are whole numbers of 2^-63: weight x 2^127 / total, whose top 64 bits one
 // multiplication gives.
@@ -24,6 +26,7 @@ struct Args {
   const float* draft;
   const peagle_dist* draft_dist;
   const peagle_dist* target_dist;
+  RowList list;
   const int* d2t;
   const float* u_accept;
   const float* u_bonus;
@@ -66,12 +69,39 @@ __device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, i
   return w * (double)(1ull << frac) / (double)d.total;
 }
 
+// Calls f(d) for the entries of a draft row that q keeps.
+template <typename F>
+__device__ __forceinline__ void kept_entries(const float* draft, int n, const Probs& q, F f) {
+  const auto one = [&](float x, int d) {
+    if (kept(order_key(x), d, q.least, q.last)) f(d);
+  };
+  if ((uintptr_t)draft % 16 == 0) {
+    const float4* v = reinterpret_cast<const float4*>(draft);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n / 4; i += THREADS) {
+      const float4 x = v[i];
+      one(x.x, 4 * i);
+      one(x.y, 4 * i + 1);
+      one(x.z, 4 * i + 2);
+      one(x.w, 4 * i + 3);
+    }
+    if (threadIdx.x < (n & 3)) one(draft[(n & ~3) + threadIdx.x], (n & ~3) + threadIdx.x);
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += THREADS) one(draft[i], i);
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
+__global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   extern __shared__ uint32_t from[];  // of this CTA's target tokens: the draft entry, plus 1
   __shared__ Locate find;
   __shared__ int accepted;
   __shared__ bool drafted;
+  __shared__ u64 red[WARPS];
+  __shared__ int tokens[LIST];    // of a list
+  __shared__ uint32_t match[LIST];  // the draft entry of each, plus 1
+  tc::pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
   const int b = blockIdx.x / ctas;
@@ -80,9 +110,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
   const T* rows = static_cast<const T*>(a.target) + (int64_t)b * (a.K + 1) * a.stride;
   const peagle_dist* pd = a.target_dist + (int64_t)b * (a.K + 1);
   const peagle_dist* qd = a.draft_dist ? a.draft_dist + (int64_t)b * a.K : nullptr;
-
-  if (a.draft)
-    for (int i = tid; i < n; i += THREADS) from[i] = 0;
 
   // the drafts: every CTA finds the same
   if (tid < 32) {
@@ -133,7 +160,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
     }
   }
   __syncthreads();
-  cluster_barrier();  // (the places in `from` are clear everywhere)
   const int m = accepted;
   const peagle_dist p = pd[m];
   if (p.total == 0) {
@@ -150,18 +176,57 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
   Probs qq = pp;
   const float* draft = nullptr;
   if (with_q) {
-    const peagle_dist q = qd[m];
-    qq = make_probs(q, draft_frac);
+    qq = make_probs(qd[m], draft_frac);
     draft = a.draft + ((int64_t)b * a.K + m) * a.draft_vocab;
-    const int end = min(a.draft_vocab, (rank + 1) * a.draft_chunk);
-    for (int d = rank * a.draft_chunk + tid; d < end; d += THREADS) {
+  }
+  const int64_t target_row = (int64_t)b * (a.K + 1) + m;
+  const int listed = a.list.count ? a.list.count[target_row] : -1;
+  if (listed >= 0) {
+    if (rank) return;
+    const bool in = tid < listed;
+    const int mine = in ? a.list.index[target_row * LIST + tid] : 0x7fffffff;
+    const u64 pi = in ? __umul64hi(a.list.weight[target_row * LIST + tid] << pp.up, pp.inv) : 0;
+    u64 ri = mine == only ? 0 : pi;
+    if (with_q) {
+      tokens[tid] = mine;
+      match[tid] = 0;
+      __syncthreads();
+      kept_entries(draft, a.draft_vocab, qq, [&](int d) {
+        const int t = d + (a.d2t ? a.d2t[d] : 0);
+        int lo = 0;
+#pragma unroll
+        for (int step = LIST / 2; step > 0; step /= 2)
+          if (tokens[lo + step] <= t) lo += step;
+        if (tokens[lo] == t && lo < listed) match[lo] = d + 1;
+      });
+      __syncthreads();
+      const uint32_t d = match[tid];
+      const u64 qi = prob_of(d ? draft[d - 1] : 0.f, (int)d - 1, d != 0, qq, draft_frac, tab);
+      ri = pi > qi ? pi - qi : 0;
+    }
+    u64 total;
+    u64 up = block_scan(ri, red, total);
+    if (total == 0) {  // the drafter left nothing: p itself
+      ri = pi;
+      up = block_scan(ri, red, total);
+    }
+    const u64 target = target_of(a.u_bonus[b], total);
+    if (up - ri <= target && target < up) a.bonus[b] = mine;
+    return;
+  }
+  if (with_q) {
+    for (int i = tid; i < n; i += THREADS) from[i] = 0;
+    __syncthreads();
+    cluster_barrier();
+    const int first = rank * a.draft_chunk, end = min(a.draft_vocab, first + a.draft_chunk);
+    for (int d = first + tid; d < end; d += THREADS) {
       if (!kept(order_key(draft[d]), d, qq.least, qq.last)) continue;
       const int t = d + (a.d2t ? a.d2t[d] : 0);
       if (t >= 0 && t < a.vocab) remote_store(&from[t % a.chunk], t / a.chunk, d + 1);
     }
     __syncthreads();
+    cluster_barrier();
   }
-  cluster_barrier();
   const T* row = rows + (int64_t)m * a.stride + base;
   bool use_q = with_q || only >= 0;
   const auto rest = [&](int i) -> u64 {
@@ -186,8 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify_kernel(Args a) {
     cluster_barrier();
     total = total_of(find, ctas);
   }
-  const double want = fmax((double)a.u_bonus[b], 0.0) * (double)total;  // (0 for a NaN)
-  const u64 target = want < (double)total ? min((u64)want, total - 1) : total - 1;
+  const u64 target = target_of(a.u_bonus[b], total);
   const int at = locate(find, ctas, n, target, rest);
   if (at >= 0 && lane == 0) a.bonus[b] = base + at;
   cluster_barrier();  // (the others read this CTA's sums)
@@ -202,20 +266,26 @@ int launch(const Args& a, int batch, int ctas, cudaStream_t st) {
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }
+
+// Rows up to which the workspace holds their lists (100 MB of them).
+constexpr int64_t LISTED = 16384, LIST_BYTES = LIST * 12 + 16;
 
 int64_t check_sizes(int64_t batch, int K, int vocab) {
   if (batch < 1 || K < 1 || vocab < 1) return PEAGLE_ERR_INVALID;
   if (K > 64) return PEAGLE_ERR_CAPACITY;
   if (vocab > MAX_VOCAB || batch * (K + 1) > MAX_ROWS) return PEAGLE_ERR_UNSUPPORTED;
-  return batch * (K + 1) * (int64_t)sizeof(peagle_dist);
+  const int64_t rows = batch * (K + 1);
+  return rows * (int64_t)sizeof(peagle_dist) + (rows <= LISTED ? rows * LIST_BYTES : 0);
 }
 
 }  // namespace
@@ -252,9 +322,16 @@ extern "C" int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* dra
   if (draft_logits && draft_vocab > smp::MAX_VOCAB) return PEAGLE_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
   const cudaStream_t st = (cudaStream_t)stream;
+  const int64_t rows = (int64_t)batch * (K + 1);
   peagle_dist* dist = static_cast<peagle_dist*>(workspace);
+  smp::RowList list = {};
+  if (rows <= smp::LISTED) {
+    list.weight = reinterpret_cast<smp::u64*>(dist + rows);
+    list.index = reinterpret_cast<int*>(list.weight + rows * smp::LIST);
+    list.count = list.index + rows * smp::LIST;
+  }
   rc = smp::sample_rows(how, batch * (K + 1), vocab, target_logits, dtype, target_stride, nullptr,
-                        nullptr, nullptr, nullptr, dist, nullptr, st);
+                        nullptr, nullptr, nullptr, dist, &list, nullptr, st);
   if (rc != PEAGLE_OK) return rc;
   smp::Args a = {};
   // a request's second step is a chain of short passes over one row: the whole cluster, but for
@@ -272,6 +349,7 @@ extern "C" int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* dra
   a.draft = draft_logits;
   a.draft_dist = draft_dist;
   a.target_dist = dist;
+  a.list = list;
   a.d2t = d2t;
   a.u_accept = u_accept;
   a.u_bonus = u_bonus;

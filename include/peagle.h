@@ -602,8 +602,8 @@ typedef struct peagle_sampling {
 } peagle_sampling;
 
 /* The distribution of a row, as peagle_sample leaves it for peagle_verify_sample: the largest
- * logit, the temperature (0: greedy), the border of the kept tokens (their smallest logit's order
- * key, and the highest kept index of logits equal to it), the sum of their weights as a whole
+ * logit, the temperature (0: greedy), a border of the kept tokens (an order key, and the highest kept
+ * index of logits that have it; larger logits are kept), the sum of their weights as a whole
  * number, the row's length, and the index that was sampled.  A row without a distribution has total 0
  * and index -1. */
 typedef struct peagle_dist {

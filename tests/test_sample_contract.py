@@ -10,7 +10,7 @@ SAMPLE = dict(how=None, rows=3, vocab=100, logits=A, dtype=0, stride=0, u=A, d2t
               dist=A, errors=A)
 VERIFY = dict(batch=2, K=3, tokens=A, how=None, vocab=100, target=A, dtype=1, stride=0, dv=50, draft=A,
               dist=A, d2t=A, u_accept=A, u_bonus=A, acc=A, bonus=A, prob=A, errors=A, work=A,
-              bytes=8 * 32)
+              bytes=8 * (32 + 512 * 12 + 16))
 
 
 def _how(pk, **kw):  # noqa: F811
@@ -49,7 +49,7 @@ def test_settings_are_refused(pk, kw):  # noqa: F811
     (dict(vocab=0), "INVALID"), (dict(vocab=262145), "UNSUPPORTED"), (dict(dv=0), "INVALID"),
     (dict(dv=262145), "UNSUPPORTED"), (dict(dtype=3), "INVALID"), (dict(stride=99), "INVALID"),
     (dict(draft=None), "INVALID"), (dict(dist=None), "INVALID"), (dict(draft=A + 2), "INVALID"),
-    (dict(dist=A + 4), "INVALID"), (dict(work=A + 8), "INVALID"), (dict(bytes=255), "CAPACITY"),
+    (dict(dist=A + 4), "INVALID"), (dict(work=A + 8), "INVALID"), (dict(bytes=8 * (32 + 512 * 12 + 16) - 1), "CAPACITY"),
     (dict(batch=1 << 23), "UNSUPPORTED"), (dict(target=None), "INVALID"), (dict(target=A + 1), "INVALID"),
     *[({k: None}, "INVALID") for k in ("tokens", "u_accept", "u_bonus", "acc", "bonus", "work")],
     *[({k: A + 2}, "INVALID") for k in ("tokens", "u_accept", "u_bonus", "acc", "bonus", "prob", "errors",
@@ -61,7 +61,9 @@ def test_verify_refuses(pk, kw, code):  # noqa: F811
 
 def test_workspace_sizes(pk):  # noqa: F811
     f = pk.lib().peagle_verify_sample_workspace
-    assert f(2, 3, 100) == 8 * 32 and f(1, 64, 262144) == 65 * 32
+    row = 32 + 512 * 12 + 16  # a record, and a list of up to 512 tokens
+    assert f(2, 3, 100) == 8 * row and f(1, 64, 262144) == 65 * row
+    assert f(8192, 1, 100) == 16384 * row and f(8193, 1, 100) == 16386 * 32  # no lists
     assert f(0, 3, 100) == f(1, 0, 100) == f(1, 1, 0) == pk.PEAGLE_ERR_INVALID
     assert f(1, 65, 100) == pk.PEAGLE_ERR_CAPACITY and f(1, 1, 262145) == pk.PEAGLE_ERR_UNSUPPORTED
     with pytest.raises(pk.PeagleError, match="32 bits"):
