@@ -48,12 +48,13 @@ struct Shared {
   union {
     uint4 hist[BINS];    // count, and three 16-bit parts of the weights
     struct {
-      u64 list[LIST];    // key and index of tokens: this CTA's
-      u64 all[LIST];     // the cluster's
+      u64 all[LIST];     // the cluster's list
+      u64 weight[LIST];
     };
   };
-  u64 weight[LIST];
+  u64 list[LIST];        // key and index of tokens: this CTA's
   u64 red64[WARPS];
+  float ch, cl, th, tl;  // log2(e) / T and T ln(min_p), two floats each
   uint32_t red32[WARPS];
   Locate find;
   uint32_t top;          // this CTA's largest key (all ones: a NaN)
@@ -105,37 +106,50 @@ __device__ __forceinline__ void wait_copies(int left) {
   if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Copies n logits from src into shared memory at the same place within 16 bytes, and finds the
-// largest (NaN if one is).
+// A chunk on its way into shared memory, at the same place within 16 bytes as in global memory.
 template <typename T>
-__device__ __forceinline__ void load_chunk(const T* src, T* dst, int n, float& top) {
-  constexpr int PER = 16 / sizeof(T), GROUPS = 4;
+struct Copies {
+  static constexpr int PER = 16 / sizeof(T), GROUPS = 4;
+  int vecs, per;
+  T* to;
+};
+template <typename T>
+__device__ __forceinline__ Copies<T> start_copies(const T* src, T* dst, int n, float& top) {
+  typedef Copies<T> C;
   const int tid = threadIdx.x;
   const int phase = (int)(((uintptr_t)src & 15) / sizeof(T));
-  const int head = min(n, phase ? PER - phase : 0);
-  const int vecs = (n - head) / PER, tail = n - head - vecs * PER;
-  const int per = ((vecs + GROUPS - 1) / GROUPS + THREADS - 1) / THREADS * THREADS;
+  const int head = min(n, phase ? C::PER - phase : 0);
+  C c;
+  c.vecs = (n - head) / C::PER;
+  c.per = ((c.vecs + C::GROUPS - 1) / C::GROUPS + THREADS - 1) / THREADS * THREADS;
+  c.to = dst + head;
+  const int tail = n - head - c.vecs * C::PER;
   const T* s = src + head;
-  T* d = dst + head;
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(d + v * PER)),
-                   "l"(s + v * PER)
+  for (int g = 0; g < C::GROUPS; ++g) {
+    for (int v = g * c.per + tid; v < min(c.vecs, (g + 1) * c.per); v += THREADS)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(c.to + v * C::PER)),
+                   "l"(s + v * C::PER)
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   if (tid < head) top = max_nan(top, to_f32(dst[tid] = src[tid]));
-  if (tid < tail) top = max_nan(top, to_f32(d[vecs * PER + tid] = s[vecs * PER + tid]));
+  if (tid < tail) top = max_nan(top, to_f32(c.to[c.vecs * C::PER + tid] = s[c.vecs * C::PER + tid]));
+  return c;
+}
+// Waits for this thread's copies, and finds their largest logit (NaN if one is).
+template <typename T>
+__device__ __forceinline__ void await_copies(const Copies<T>& c, float& top) {
+  typedef Copies<T> C;
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    wait_copies(GROUPS - 1 - g);
-    for (int v = g * per + tid; v < min(vecs, (g + 1) * per); v += THREADS)
-      top = top_of(*reinterpret_cast<const uint4*>(d + v * PER), top, T());
+  for (int g = 0; g < C::GROUPS; ++g) {
+    wait_copies(C::GROUPS - 1 - g);
+    for (int v = g * c.per + threadIdx.x; v < min(c.vecs, (g + 1) * c.per); v += THREADS)
+      top = top_of(*reinterpret_cast<const uint4*>(c.to + v * C::PER), top, T());
   }
 }
 
-// Calls f(x, place) for the logits at least `floor` of a chunk that load_chunk brought.
+// Calls f(x, place) for the logits at least `floor` of a chunk that these copies brought.
 template <typename T, typename F>
 __device__ __forceinline__ void above(const T* chunk, int n, float floor, F f) {
   constexpr int PER = 16 / sizeof(T);
@@ -152,6 +166,12 @@ __device__ __forceinline__ void above(const T* chunk, int n, float floor, F f) {
     if (top_of(y, -INFINITY, T()) >= floor)
       for (int k = 0; k < PER; ++k) one(head + v * PER + k);
   }
+}
+
+// A logit below every x whose exponent is y (< 0) or more: y / c, and what fp32 rounds of it and of
+// x - M (2^-24 each).
+__device__ __forceinline__ float below(const Scale& s, float y) {
+  return (s.top + y / s.ch * 1.00001f) - fabsf(s.top) * 1e-6f;
 }
 
 __device__ __forceinline__ int bin_of(float x, const Scale& s) {
@@ -360,8 +380,10 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
 
 // The weights before which a token is kept: top_p of the mass, at least the first token's.
 __device__ __forceinline__ u64 part_of(float top_p, u64 mass) {
-  const double want = ceil((double)fmaxf(top_p, 0.f) * (double)mass);
-  return max(1ull, min(mass, (u64)want));
+  bool more;
+  if (!(top_p > 0.f)) return 1;
+  const u64 want = part(mass, top_p, more) + more;
+  return max(1ull, min(mass, want));
 }
 
 // Sorts a number of each of the first `size` threads (a power of two), the largest first.
@@ -386,7 +408,7 @@ __device__ __forceinline__ int size_for(int n) { return n < 2 ? 1 : 1 << (32 - _
 
 // One CTA's end of a short row: n candidates (sh.all) that hold every kept token.  mass: of the whole
 // row, unless it is the first top_k candidates' (mine).
-__device__ __forceinline__ void finish(Shared& sh, const Args& a, int r, int n, const Scale& s, const Table& tab,
+__device__ __forceinline__ void finish(Shared& sh, uint2* raws, const Args& a, int r, int n, const Scale& s, const Table& tab,
                                        float top, float temperature, int frac, int top_k, bool by_p, float top_p,
                                        u64 mass, bool mine, uint32_t min_key) {
   const int tid = threadIdx.x;
@@ -395,8 +417,13 @@ __device__ __forceinline__ void finish(Shared& sh, const Args& a, int r, int n, 
   me = sort_down(me, size_for(n), sh.list);
   const uint32_t key = (uint32_t)(me >> 32);
   const int index = (int)(0xffffffffu - (uint32_t)me);
-  u64 w = 0;
-  if ((tid & ~31) < n) w = weight(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab);
+  u64 w = 0, raw = 0;
+  int down = 63;
+  if ((tid & ~31) < n) {
+    if (!weight_raw(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab, raw, down)) down = 63;
+    w = down > 62 ? 0 : (raw + (1ull << (down - 1))) >> down;
+  }
+  raws[tid] = make_uint2((uint32_t)(raw >> 31), (uint32_t)down);  // 32 bits of a weight
   const bool first = tid < n && tid < top_k;
   if (!first) w = 0;
   u64 all;
@@ -404,7 +431,6 @@ __device__ __forceinline__ void finish(Shared& sh, const Args& a, int r, int n, 
   const u64 want = by_p ? part_of(top_p, mine ? all : mass) : ~0ull;
   const bool in = first && run - w < want, keep = in && key >= min_key;
   sh.weight[tid] = w;
-  sh.all[tid] = me;
   const int cut = __syncthreads_count(in), m = __syncthreads_count(keep);
   if (tid == cut - 1) {
     sh.least = max(key, min_key);
@@ -432,12 +458,10 @@ __device__ __forceinline__ void finish(Shared& sh, const Args& a, int r, int n, 
   const u64 target = target_of(a.u[r], total);
   const u64 up = block_scan(w, sh.red64, all);
   if (up - w <= target && target < up) {
-    const uint32_t k = (uint32_t)(sh.all[from] >> 32);
+    const uint2 x = raws[from];
     d.index = i;
     if (a.token) a.token[r] = i + (a.d2t ? a.d2t[i] : 0);
-    if (a.prob)
-      a.prob[r] = (float)(weight64(__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), top, temperature) *
-                          (double)(1ull << frac) / (double)total);
+    if (a.prob) a.prob[r] = (float)ratio64(x.x, (int)x.y - 31, total);
     if (a.dist) a.dist[r] = d;
   }
 }
@@ -464,7 +488,12 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   T* chunk = reinterpret_cast<T*>(reinterpret_cast<char*>(dynamic) + ((uintptr_t)src & 15));
   row.x = chunk;
   float top = -INFINITY;
-  load_chunk(src, chunk, row.n, top);
+  const Copies<T> copies = start_copies(src, chunk, row.n, top);
+  if (tid == THREADS - 32 && temperature > 0.f) {
+    split(1.4426950408889634074 / (double)temperature, sh.ch, sh.cl);
+    if (min_p > 0.f) split((double)temperature * log((double)fminf(min_p, 1.f)), sh.th, sh.tl);
+  }
+  await_copies(copies, top);
   const float mine = top;  // this thread's own
   uint32_t key = top == top ? order_key(top) : 0xffffffffu;
   key = __reduce_max_sync(0xffffffffu, key);
@@ -519,13 +548,14 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
     return;
   }
 
-  const Scale s = make_scale(top, temperature, frac);
+  const Scale s = {top, sh.ch, sh.cl, 62 - frac};
   const Table tab = load_table();
   const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
   uint32_t min_key = 0;
-  if (min_p > 0.f) {
-    const float x = __double2float_ru((double)top + (double)temperature * log((double)fminf(min_p, 1.f)));
-    min_key = order_key(fminf(x, top));
+  if (min_p > 0.f) {  // the smallest fp32 number that is at least M + T ln(min_p)
+    const float x = top + sh.th, back = x - top;
+    const float rest = ((top - (x - back)) + (sh.th - back)) + sh.tl;
+    min_key = order_key(rest > 0.f ? fminf(nextafterf(x, INFINITY), top) : x);
   }
   if (by_k || by_p) {
     // a logit that no kept token is below
@@ -541,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
         merge_bins(sh, ctas, n, w);
         find_bin(sh, n, w, true, (uint32_t)top_k, 0);
         if (sh.bin < BINS - 1)  // (else: fewer threads than k)
-          floor = __double2float_rd((double)top - (sh.bin + 1) / 8.0 / (double)s.ch * (1 + 1e-6));
+          floor = below(s, -(sh.bin + 1) * 0.125f);
       } else {
         u64 sum = 0;
         for (int i = tid & ~31; i < row.n; i += THREADS)
@@ -551,10 +581,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
         __syncthreads();
         cluster_barrier();
         for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
-        const double rest = (1.0 - (double)fmaxf(top_p, 0.f)) * (double)mass / (double)(1ull << frac);
-        floor = __double2float_rd((double)top + (double)temperature * log(rest / (2.0 * a.vocab)));
+        const float rest = (1.f - fmaxf(top_p, 0.f)) * ((float)mass * exp2f((float)-frac));
+        floor = below(s, log2f(rest / (2.f * a.vocab)) - 0.01f);
       }
-      cluster_barrier();  // (the histogram's place holds the list)
     }
     above(chunk, row.n, floor, [&](float x, int i) {
       const uint32_t at = atomicAdd(&sh.count, 1u);
@@ -568,11 +597,15 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
       if (rank == 0 && n + m <= LIST && tid < m) sh.all[n + tid] = remote_u64(&sh.list[tid], c);
       n += m;
     }
-    cluster_barrier();
+    cluster_arrive();  // (the lists have been read)
     if (n <= LIST) {
-      if (rank == 0) finish(sh, a, r, n, s, tab, top, temperature, frac, by_k ? top_k : LIST, by_p, top_p, mass, by_k || a.vocab <= LIST, min_key);
+      if (rank == 0)
+        finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, n, s, tab, top, temperature, frac, by_k ? top_k : LIST, by_p, top_p, mass, by_k || a.vocab <= LIST, min_key);
+      __syncthreads();
+      cluster_wait();
       return;
     }
+    cluster_wait();
     if (tid == 0) sh.count = 0;
     sh.hist[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -630,13 +663,17 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   } else {
     const u64 target = target_of(a.u[r], total);
     const int at = locate(sh.find, ctas, row.n, target, weigh);
-    if (at >= 0 && lane == 0) {
-      const int i = row.base + at;
-      d.index = i;
-      if (a.token) a.token[r] = i + (a.d2t ? a.d2t[i] : 0);
-      if (a.prob)
-        a.prob[r] = (float)(weight64(to_f32(row.x[at]), top, temperature) * (double)(1ull << frac) / (double)total);
-      if (a.dist) a.dist[r] = d;
+    if (at >= 0) {  // (all lanes of one warp)
+      u64 raw;
+      int down;
+      weight_raw(to_f32(row.x[at]), s, tab, raw, down);
+      if (lane == 0) {
+        const int i = row.base + at;
+        d.index = i;
+        if (a.token) a.token[r] = i + (a.d2t ? a.d2t[i] : 0);
+        if (a.prob) a.prob[r] = (float)ratio64(raw, down, total);
+        if (a.dist) a.dist[r] = d;
+      }
     }
   }
   cluster_barrier();  // (the others read this CTA's sums)
@@ -644,7 +681,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
 
 template <typename T>
 int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
-  const size_t bytes = (size_t)a.chunk * sizeof(T) + 32;
+  // (the row's place holds `finish`'s numbers at the end)
+  const size_t bytes = max((size_t)a.chunk * sizeof(T) + 32, LIST * sizeof(uint2));
   if (smem_optin((const void*)sample_kernel<T>, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * ctas);

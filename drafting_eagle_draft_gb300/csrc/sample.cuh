@@ -52,17 +52,20 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 // A temperature below this counts as 0 (the largest logit alone): 1 / T stays far inside fp32.
 constexpr float COLD = 0x1p-60f;
 
-// log2(e) / T in two floats.
+// log2(e) / T in two floats.  (64-bit arithmetic is slow here: where a whole CTA wants a number that
+// needs it, one thread computes it.)
 struct Scale {
   float top, ch, cl;
   int shift;  // 62 - F
 };
+__device__ __forceinline__ void split(double x, float& hi, float& lo) {
+  hi = (float)x;
+  lo = (float)(x - (double)hi);
+}
 __device__ __forceinline__ Scale make_scale(float top, float temperature, int frac) {
   Scale s;
-  const double c = 1.4426950408889634074 / (double)temperature;
+  split(1.4426950408889634074 / (double)temperature, s.ch, s.cl);
   s.top = top;
-  s.ch = (float)c;
-  s.cl = (float)(c - (double)s.ch);
   s.shift = 62 - frac;
   return s;
 }
@@ -92,10 +95,11 @@ __device__ __forceinline__ Table load_table() {
   return {(uint32_t)t, (uint32_t)(t >> 32)};
 }
 
-// round(2^y 2^F), y = (x - M) log2(e) / T: x - M and y are sums of two floats, y = j/32 + g,
+// 2^y 2^F = raw 2^-n, y = (x - M) log2(e) / T: x - M and y are sums of two floats, y = j/32 + g,
 // 2^y = 2^(j/32) (1 + p) with p = 2^g - 1 by its series, |g| <= 1/64, in units of 2^-37; the product
-// and the shift are on whole numbers.  Exactly 2^F at x = M.  The warp's 32 lanes call it together.
-__device__ __forceinline__ u64 weight(float x, const Scale& s, const Table& t) {
+// is on whole numbers, raw in 2^62 .. 2^63.  False below 2^-900 (-inf and NaN too).  The warp's 32
+// lanes call it together.
+__device__ __forceinline__ bool weight_raw(float x, const Scale& s, const Table& t, u64& raw, int& n) {
   const float dh = x - s.top, back = dh - x;
   const float dl = (x - (dh - back)) - (s.top + back);
   const float ph = dh * s.ch;
@@ -112,16 +116,39 @@ __device__ __forceinline__ u64 weight(float x, const Scale& s, const Table& t) {
   const int p = __float2int_rn(qh * 0x1p37f) + __float2int_rn(ql * 0x1p37f);
   const uint32_t lo = __shfl_sync(0xffffffffu, t.lo, j & 31);
   const uint32_t hi = __shfl_sync(0xffffffffu, t.hi, j & 31);
-  u64 w = ((u64)hi << 32) | lo;
-  w += (u64)(((long long)(int)hi * p) >> 5);
-  const int n = s.shift - (j >> 5);  // >= 12
-  if (!(ph > -62.f) || n > 62) return 0;  // (-inf and NaN too)
-  return (w + (1ull << (n - 1))) >> n;
+  raw = (((u64)hi << 32) | lo) + (u64)(((long long)(int)hi * p) >> 5);
+  n = s.shift - (j >> 5);  // >= 12
+  return ph > -900.f;
+}
+// round(2^y 2^F); exactly 2^F at x = M.
+__device__ __forceinline__ u64 weight(float x, const Scale& s, const Table& t) {
+  u64 raw;
+  int n;
+  if (!weight_raw(x, s, t, raw, n) || n > 62) return 0;
+  return (raw + (1ull << (n - 1))) >> n;
+}
+// raw 2^-n / total, for one that is returned or compared: 64-bit arithmetic, for a few threads.
+__device__ __forceinline__ double ratio64(u64 raw, int n, u64 total) {
+  return (double)raw / (double)total * __hiloint2double((1023 - n) << 20, 0);
 }
 
-// The same weight in 64 bits, relative to M's (for a probability that is returned or compared).
-__device__ __forceinline__ double weight64(float x, float top, float temperature) {
-  return exp(((double)x - (double)top) / (double)temperature);
+// f t, 0 < f < 1, rounded down; `more`: something was dropped.
+__device__ __forceinline__ u64 part(u64 t, float f, bool& more) {
+  const uint32_t b = __float_as_uint(f), e = b >> 23;
+  const u64 m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int down = 150 - (int)max(e, 1u);  // f = m 2^-down, 24 or more
+  const u64 hi = __umul64hi(t, m), lo = t * m;
+  if (down < 64) {
+    more = (lo << (64 - down)) != 0;
+    return hi << (64 - down) | lo >> down;
+  }
+  const int rest = down - 64;  // hi has 24 bits
+  if (rest > 24) {
+    more = (lo | hi) != 0;
+    return 0;
+  }
+  more = lo != 0 || (hi & ((1ull << rest) - 1)) != 0;
+  return hi >> rest;
 }
 
 __device__ __forceinline__ bool kept(uint32_t key, int i, uint32_t least, int last) {
@@ -130,8 +157,9 @@ __device__ __forceinline__ bool kept(uint32_t key, int i, uint32_t least, int la
 
 // Where the running sum has to pass, of `total`, for a random number u.
 __device__ __forceinline__ u64 target_of(float u, u64 total) {
-  const double want = fmax((double)u, 0.0) * (double)total;  // (0 for a NaN)
-  return want < (double)total ? min((u64)want, total - 1) : total - 1;
+  bool more;
+  if (!(u > 0.f)) return 0;  // (a NaN too)
+  return u < 1.f ? part(total, u, more) : total - 1;
 }
 
 // ---- cluster -------------------------------------------------------------------------
@@ -141,9 +169,17 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 // Every thread of the row's CTAs.
-__device__ __forceinline__ void cluster_barrier() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  tc::cluster_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive();
+  cluster_wait();
 }
 __device__ __forceinline__ u64 remote_u64(const u64* p, int rank) {
   u64 v;

@@ -62,11 +62,15 @@ __device__ __forceinline__ u64 prob_of(float x, int i, bool in, const Probs& p, 
   const u64 w = p.cold ? 1ull << frac : weight(x, p.s, t);
   return in ? __umul64hi(w << p.up, p.inv) : 0;
 }
-// In 64 bits, for the comparison of a draft.
-__device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, int frac) {
-  if (!kept(order_key(x), i, d.least, d.last) || x == -INFINITY) return 0.0;
-  const double w = d.temperature < COLD ? 1.0 : weight64(x, d.top, d.temperature);
-  return w * (double)(1ull << frac) / (double)d.total;
+// In 64 bits, for the comparison of a draft; every lane of the warp calls it, each with its own row.
+__device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, int frac, const Table& t) {
+  const bool cold = d.temperature < COLD;
+  const Scale s = make_scale(d.top, cold ? 1.f : d.temperature, frac);
+  u64 raw;
+  int n;
+  const bool any = weight_raw(x, s, t, raw, n);
+  if (d.total == 0 || !kept(order_key(x), i, d.least, d.last)) return 0.0;
+  return cold ? 1.0 : any ? ratio64(raw, n, d.total) : 0.0;
 }
 
 // Calls f(d) for the entries of a draft row that q keeps.
@@ -99,6 +103,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   __shared__ int accepted;
   __shared__ bool drafted;
   __shared__ u64 red[WARPS];
+  __shared__ Probs probs[2];      // p and q
   __shared__ int tokens[LIST];    // of a list
   __shared__ uint32_t match[LIST];  // the draft entry of each, plus 1
   tc::pdl_wait();
@@ -111,6 +116,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   const peagle_dist* pd = a.target_dist + (int64_t)b * (a.K + 1);
   const peagle_dist* qd = a.draft_dist ? a.draft_dist + (int64_t)b * a.K : nullptr;
 
+  const Table tab = load_table();
   // the drafts: every CTA finds the same
   if (tid < 32) {
     int m = a.K;
@@ -118,33 +124,35 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
     for (int j0 = 0; j0 < a.K; j0 += 32) {
       const int j = j0 + lane;
       bool ok = true, good = true;
-      if (j < a.K) {
-        const int x = a.tokens[b * a.K + j];
-        const peagle_dist p = pd[j];
-        unsigned bits = 0;
-        double pr = 0.0, qr = 1.0;
-        if (x < 0 || x >= a.vocab) bits = PEAGLE_DEV_BAD_TOKEN;
-        if (p.total == 0) bits |= PEAGLE_DEV_BAD_ROW;
-        if (qd) {
-          const peagle_dist q = qd[j];
-          if (q.total == 0) {
-            bits |= PEAGLE_DEV_BAD_ROW;
-          } else if (q.vocab != a.draft_vocab || q.index < 0 || q.index >= a.draft_vocab ||
-                     q.index + (a.d2t ? a.d2t[q.index] : 0) != x) {
-            bits |= PEAGLE_DEV_BAD_TOKEN;
-          } else {
-            qr = prob64(a.draft[((int64_t)b * a.K + j) * a.draft_vocab + q.index], q.index, q, draft_frac);
-          }
-        }
-        if (!bits) pr = prob64(to_f32(rows[(int64_t)j * a.stride + x]), x, p, frac);
-        good = !bits;
+      const bool in = j < a.K;
+      const peagle_dist none = {0ull, 0.f, 1.f, 0xffffffffu, -1, -1, 0};
+      const int x = in ? a.tokens[b * a.K + j] : 0;
+      const peagle_dist p = in ? pd[j] : none, q = in && qd ? qd[j] : none;
+      unsigned bits = 0;
+      if (x < 0 || x >= a.vocab) bits = PEAGLE_DEV_BAD_TOKEN;
+      if (p.total == 0) bits |= PEAGLE_DEV_BAD_ROW;
+      if (qd) {
+        if (q.total == 0)
+          bits |= PEAGLE_DEV_BAD_ROW;
+        else if (q.vocab != a.draft_vocab || q.index < 0 || q.index >= a.draft_vocab ||
+                 q.index + (a.d2t ? a.d2t[q.index] : 0) != x)
+          bits |= PEAGLE_DEV_BAD_TOKEN;
+      }
+      good = in && !bits;
+      const float px = good ? to_f32(rows[(int64_t)j * a.stride + x]) : 0.f;
+      const float qx = good && qd ? a.draft[((int64_t)b * a.K + j) * a.draft_vocab + q.index] : 0.f;
+      double pr = prob64(px, x, p, frac, tab), qr = 1.0;
+      if (qd) qr = prob64(qx, q.index, q, draft_frac, tab);
+      if (!good) pr = 0.0;
+      if (in) {
         const double u = a.u_accept[b * a.K + j];
         ok = good && u * qr < pr;
         if (rank == 0) {
-          if (a.accept_prob)
-            a.accept_prob[b * a.K + j] = pr > 0.0 ? (float)fmin(1.0, pr / qr) : 0.f;
+          if (a.accept_prob) a.accept_prob[b * a.K + j] = pr > 0.0 ? (float)fmin(1.0, pr / qr) : 0.f;
           raise_error(reinterpret_cast<unsigned*>(a.errors), bits);
         }
+      } else {
+        good = true;
       }
       const unsigned no = __ballot_sync(0xffffffffu, !ok);
       if (no && m == a.K) {
@@ -171,14 +179,11 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   }
   const bool with_q = drafted && a.draft;
   const int only = drafted && !a.draft ? a.tokens[b * a.K + m] : -1;  // q = 1 there
-  const Table tab = load_table();
-  const Probs pp = make_probs(p, frac);
-  Probs qq = pp;
-  const float* draft = nullptr;
-  if (with_q) {
-    qq = make_probs(qd[m], draft_frac);
-    draft = a.draft + ((int64_t)b * a.K + m) * a.draft_vocab;
-  }
+  if (tid == 0) probs[0] = make_probs(p, frac);
+  if (tid == 32 && with_q) probs[1] = make_probs(qd[m], draft_frac);
+  const float* draft = with_q ? a.draft + ((int64_t)b * a.K + m) * a.draft_vocab : nullptr;
+  __syncthreads();
+  const Probs pp = probs[0], qq = probs[with_q];
   const int64_t target_row = (int64_t)b * (a.K + 1) + m;
   const int listed = a.list.count ? a.list.count[target_row] : -1;
   if (listed >= 0) {
