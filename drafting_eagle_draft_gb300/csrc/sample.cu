@@ -25,6 +25,7 @@ namespace {
 
 constexpr int BINS = THREADS;  // one a thread in the cluster's sum
 constexpr int RANK = 256;
+constexpr float LOWEST = -3.402823466e38f;
 
 struct Args {
   const void* logits;
@@ -59,7 +60,7 @@ struct Shared {
   Locate find;
   uint32_t top;          // this CTA's largest key (all ones: a NaN)
   u64 sum;               // this CTA's weights
-  uint32_t count, low, high;  // of the list; smallest and largest key in the boundary bin
+  uint32_t count;        // of the list
   uint32_t first;        // lowest index of the largest logit
   // what one thread finds for all
   int bin;
@@ -68,8 +69,9 @@ struct Shared {
   uint32_t least;        // the border: tokens below it are cut
   int last;
   u64 kept_w;            // weights above it
-  int first_bin;         // the bin over y that the last cut went through, and what lies before it
-  u64 first_before;
+  uint32_t floor;        // order key below which this CTA's list leaves tokens out
+  int n;                 // of the row's list; -1: too many
+  int bin0, bin1;        // where the border lies
 };
 
 template <typename T>
@@ -161,6 +163,7 @@ __device__ __forceinline__ void above(const T* chunk, int n, float floor, F f) {
   };
   if (tid < head) one(tid);
   if (tid < tail) one(head + vecs * PER + tid);
+#pragma unroll 4
   for (int v = tid; v < vecs; v += THREADS) {
     const uint4 y = *reinterpret_cast<const uint4*>(chunk + head + v * PER);
     if (top_of(y, -INFINITY, T()) >= floor)
@@ -219,6 +222,16 @@ __device__ __forceinline__ void find_bin(Shared& sh, uint32_t n, u64 w, bool by_
   __syncthreads();
 }
 
+// Keys low .. high in BINS parts: the width of one, as a shift.
+__device__ __forceinline__ int key_shift(uint32_t low, uint32_t high) { return max(0, 32 - __clz(high - low) - 9); }
+// The keys that the bins from bin0 to bin1 can hold.
+__device__ __forceinline__ uint32_t lowest_key(const Scale& s, int bin1) {
+  return bin1 == BINS - 1 ? 0u : order_key(below(s, -(bin1 + 1) * 0.125f));
+}
+__device__ __forceinline__ uint32_t highest_key(const Scale& s, int bin0) {
+  return order_key(fminf(s.top, (s.top - bin0 * 0.125f / s.ch * 0.99999f) + fabsf(s.top) * 1e-6f));
+}
+
 __device__ __forceinline__ void add_bin(uint4* h, u64 w, bool weigh) {
   atomicAdd(&h->x, 1u);
   if (weigh && w) {
@@ -229,67 +242,60 @@ __device__ __forceinline__ void add_bin(uint4* h, u64 w, bool weigh) {
 }
 
 // Cuts the row's order (larger logits first, then lower indices): keeps the first want_n tokens
-// (by_count), or the shortest prefix whose weights reach want_w.  n, w: the merged histogram over
-// y of the tokens that are kept so far (sh.least, sh.last).  Leaves the border in sh.least and
-// sh.last and the kept weights in sh.kept_w.
+// (by_count), or the shortest prefix whose weights reach want_w.  The border lies among the in_n tokens
+// in the bins bin0 .. bin1 over y, of those that are kept so far (sh.least, sh.last); before_n tokens,
+// or weights before_w, lie before them; their keys are low .. high.  filled: their histogram over the
+// keys is in place.  Leaves the border in sh.least and sh.last.
 template <typename T>
-__device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& tab, int ctas, bool weigh,
-                    bool by_count, uint32_t want_n, u64 want_w, uint32_t n, u64 w) {
+__device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& tab, int ctas, bool by_count,
+                    uint32_t want_n, u64 want_w, int bin0, int bin1, uint32_t before_n, u64 before_w, uint32_t in_n,
+                    uint32_t low, uint32_t high, bool filled) {
   const int tid = threadIdx.x;
-  find_bin(sh, n, w, by_count, want_n, want_w);
-  const int bin = sh.bin;
+  const bool weigh = !by_count;
   const uint32_t old_least = sh.least;
   const int old_last = sh.last;
-  uint32_t before_n = sh.before_n, in_n = sh.in_n;
-  u64 before_w = sh.before_w;
-  if (tid == 0) {
-    sh.first_bin = bin;
-    sh.first_before = before_w;
-  }
-  uint32_t low = 0, high = 0xffffffffu;  // the boundary set: bin, and keys low .. high
-  bool ranged = false;
+  uint32_t n;
+  u64 w;
   while (true) {
-    const bool listed = in_n <= RANK;
-    const bool divide = !listed && ranged;
-    const int shift = divide ? max(0, 32 - __clz(high - low) - 9) : 0;
-    if (divide && low == high) break;  // equal logits
+    const bool listed = !filled && in_n <= RANK;
+    const int shift = key_shift(low, high);
+    if (!listed && low == high) break;  // equal logits
+    if (!filled) {
     __syncthreads();
     cluster_barrier();  // (the buffers below are read no more)
-    if (tid == 0) {
-      sh.count = 0;
-      sh.low = 0xffffffffu;
-      sh.high = 0;
-    }
-    if (divide) sh.hist[tid] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sh.count = 0;
+    if (!listed) sh.hist[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    uint32_t lo = 0xffffffffu, hi = 0;
-    for (int i = tid & ~31; i < row.n; i += THREADS) {
-      const int at = i + (tid & 31);
-      const float x = at < row.n ? to_f32(row.x[at]) : -INFINITY;
-      const uint32_t key = order_key(x);
-      const bool in = at < row.n && bin_of(x, s) == bin && key >= low && key <= high &&
-                      kept(key, row.base + at, old_least, old_last);
-      if (!__any_sync(0xffffffffu, in)) continue;
-      const u64 wx = divide && weigh ? weight(x, s, tab) : 0;
-      if (in) {
-        lo = min(lo, key);
-        hi = max(hi, key);
-        if (listed)
-          sh.list[atomicAdd(&sh.count, 1u)] = (u64)key << 32 | (0xffffffffu - (uint32_t)(row.base + at));
-        else if (divide)
-          add_bin(&sh.hist[(high - key) >> shift], wx, weigh);
-        else
-          atomicAdd(&sh.count, 1u);
+    for (int i = tid & ~31; i < row.n; i += 4 * THREADS) {
+      float x[4];
+      bool is[4], any = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = i + k * THREADS + (tid & 31);
+        x[k] = at < row.n ? to_f32(row.x[at]) : -INFINITY;
+        const uint32_t key = order_key(x[k]);
+        const int bin = bin_of(x[k], s);
+        any |= is[k] = at < row.n && bin >= bin0 && bin <= bin1 && key >= low && key <= high &&
+                       kept(key, row.base + at, old_least, old_last);
       }
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if ((tid & 31) == 0) {
-      atomicMin(&sh.low, lo);
-      atomicMax(&sh.high, hi);
+      if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (!__any_sync(0xffffffffu, is[k])) continue;
+        const u64 wx = !listed && weigh ? weight(x[k], s, tab) : 0;
+        if (!is[k]) continue;
+        const uint32_t key = order_key(x[k]);
+        if (listed)
+          sh.list[atomicAdd(&sh.count, 1u)] =
+              (u64)key << 32 | (0xffffffffu - (uint32_t)(row.base + i + k * THREADS + (tid & 31)));
+        else
+          add_bin(&sh.hist[(high - key) >> shift], wx, weigh);
+      }
     }
     __syncthreads();
     cluster_barrier();
+    }
+    filled = false;
     if (listed) {
       // every CTA has the whole list, and ranks it
       int at = 0;
@@ -321,22 +327,10 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
         if ((is || rank == 0) && (!next || rank == at - 1)) {
           sh.least = (uint32_t)(me >> 32);
           sh.last = (int)(0xffffffffu - (uint32_t)me);
-          sh.kept_w = before_w + above + mine;
         }
       }
       __syncthreads();
       return;
-    }
-    if (!divide) {  // the bin's own range of logits, to be divided
-      low = 0xffffffffu;
-      high = in_n = 0;
-      for (int c = 0; c < ctas; ++c) {
-        in_n += remote_u32(&sh.count, c);
-        low = min(low, remote_u32(&sh.low, c));
-        high = max(high, remote_u32(&sh.high, c));
-      }
-      ranged = true;
-      continue;
     }
     merge_bins(sh, ctas, n, w);
     find_bin(sh, n, w, by_count, by_count ? want_n - before_n : 0, by_count ? 0 : want_w - before_w);
@@ -357,9 +351,12 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
     m = each ? (uint32_t)min((u64)in_n, (rest + each - 1) / each) : in_n;
   }
   m = max(1u, min(m, in_n));
-  const auto tie = [&](int i) -> u64 {
-    return i < row.n && order_key(to_f32(row.x[i])) == low &&
-           kept(low, row.base + i, old_least, old_last);
+  const auto tie = [&](auto count, int i) -> u64 {
+    u64 sum = 0;
+#pragma unroll
+    for (int k = 0; k < decltype(count)::value; ++k, i += 32)
+      sum += i < row.n && order_key(to_f32(row.x[i])) == low && kept(low, row.base + i, old_least, old_last);
+    return sum;
   };
   sum_spans(sh.find, row.n, tie);
   __syncthreads();
@@ -373,7 +370,6 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
   if (tid == 0) {
     sh.least = low;
     sh.last = (int)remote_u32(&sh.first, sh.find.cta);
-    sh.kept_w = before_w + each * m;
   }
   __syncthreads();
 }
@@ -466,6 +462,45 @@ __device__ __forceinline__ void finish(Shared& sh, uint2* raws, const Args& a, i
   }
 }
 
+// The first and last bin over y in which the running weight can reach `want`, `rest` being left behind
+// it (both in units of the largest weight), from the bins' counts: thread t has bin t's.
+__device__ __forceinline__ void border_bins(Shared& sh, uint32_t n, float want, float rest) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* red = reinterpret_cast<float*>(sh.red64);
+  const float high = (float)n * exp2f(-0.125f * tid);
+  const float low = tid == BINS - 1 ? 0.f : high * 0.917004f;  // 2^(-1/8)
+  float up[2] = {high, low}, all[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, up[k], o);
+      if (lane >= o) up[k] += x;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = up[k];
+    __syncthreads();
+    all[k] = 0.f;
+    for (int j = 0; j < WARPS; ++j) {
+      if (j < warp) up[k] += red[j];
+      all[k] += red[j];
+    }
+  }
+  // (sums of 512 numbers in fp32: 1 % is far more than they and the bins' edges are off by)
+  const bool can = up[0] * 1.01f >= want && (all[1] - up[1]) * 0.99f - all[1] * 1e-5f <= rest;
+  const bool must = up[1] * 0.99f >= want || (all[0] - up[0]) * 1.01f + all[0] * 1e-5f <= rest;
+  if (tid == 0) {
+    sh.bin0 = BINS - 1;
+    sh.bin1 = BINS - 1;
+  }
+  __syncthreads();
+  if (can) atomicMin(&sh.bin0, tid);
+  if (must) atomicMin(&sh.bin1, tid);
+  __syncthreads();
+  if (tid == 0) sh.bin0 = min(sh.bin0, sh.bin1);
+  __syncthreads();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   extern __shared__ uint4 dynamic[];
@@ -509,6 +544,28 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   __syncthreads();
   if (lane == 0) atomicMax(&sh.top, key);
   __syncthreads();
+  const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
+  const bool small = a.vocab <= LIST;
+  // With top-k every CTA lists its chunk's first tokens before the row's largest is known: four standard
+  // deviations and some more than its part of k, down to a border that as many threads' maxima reach.
+  const int mine_k = ctas == 1 ? top_k : min(top_k, top_k / ctas + 4 * (int)sqrtf((float)top_k / ctas) + 8);
+  const bool list_k = by_k && !small && mine_k <= THREADS * 7 / 8 && temperature >= COLD;
+  if (list_k) {
+    const uint32_t k = sh.top;
+    const Scale own = {__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), sh.ch, sh.cl, 0};
+    if (mine > -INFINITY) atomicAdd(&sh.hist[bin_of(mine, own)].x, 1u);
+    __syncthreads();
+    find_bin(sh, sh.hist[tid].x, 0, true, (uint32_t)mine_k, 0);
+    // (with fewer threads than mine_k that have a token at all: every token)
+    const float floor = sh.bin < BINS - 1 ? fmaxf(below(own, -(sh.bin + 1) * 0.125f), LOWEST) : LOWEST;
+    above(chunk, row.n, floor, [&](float x, int i) {
+      if (*(volatile uint32_t*)&sh.count > LIST) return;
+      const uint32_t at = atomicAdd(&sh.count, 1u);
+      if (at < LIST) sh.list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(row.base + i));
+    });
+    if (tid == 0) sh.floor = order_key(floor);
+    __syncthreads();
+  }
   cluster_barrier();
   uint32_t top_key = 0;
   for (int c = 0; c < ctas; ++c) top_key = max(top_key, remote_u32(&sh.top, c));
@@ -550,91 +607,189 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
 
   const Scale s = {top, sh.ch, sh.cl, 62 - frac};
   const Table tab = load_table();
-  const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
   uint32_t min_key = 0;
   if (min_p > 0.f) {  // the smallest fp32 number that is at least M + T ln(min_p)
     const float x = top + sh.th, back = x - top;
     const float rest = ((top - (x - back)) + (sh.th - back)) + sh.tl;
     min_key = order_key(rest > 0.f ? fminf(nextafterf(x, INFINITY), top) : x);
   }
+  bool certain = false;  // find.sums holds what lies before the border's bins
   if (by_k || by_p) {
-    // a logit that no kept token is below
-    float floor = -INFINITY;
     u64 mass = 0;
-    if (a.vocab > LIST) {
-      if (by_k) {
-        if (mine > -INFINITY) atomicAdd(&sh.hist[bin_of(mine, s)].x, 1u);
-        __syncthreads();
-        cluster_barrier();
-        uint32_t n;
-        u64 w;
-        merge_bins(sh, ctas, n, w);
-        find_bin(sh, n, w, true, (uint32_t)top_k, 0);
-        if (sh.bin < BINS - 1)  // (else: fewer threads than k)
-          floor = below(s, -(sh.bin + 1) * 0.125f);
-      } else {
-        u64 sum = 0;
-        for (int i = tid & ~31; i < row.n; i += THREADS)
-          sum += weight(i + lane < row.n ? to_f32(row.x[i + lane]) : -INFINITY, s, tab);
-        sum = warp_sum64(sum);
-        if (lane == 0) atomicAdd(&sh.sum, sum);
-        __syncthreads();
-        cluster_barrier();
-        for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
-        const float rest = (1.f - fmaxf(top_p, 0.f)) * ((float)mass * exp2f((float)-frac));
-        floor = below(s, log2f(rest / (2.f * a.vocab)) - 0.01f);
+    if (!list_k && !small && !by_k) {
+      // S, and on the way the tokens that top_p can keep if S is 1
+      const float floor = fmaxf(below(s, log2f((1.f - fmaxf(top_p, 0.f)) / (2.f * a.vocab)) - 0.01f), LOWEST);
+      u64 sum = 0;
+      for (int i = (tid & ~31) * 4 + lane; i < row.n + lane; i += 4 * THREADS) {
+        float x[4];
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = i + 32 * k < row.n ? to_f32(row.x[i + 32 * k]) : -INFINITY;
+          any |= x[k] >= floor;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += weight(x[k], s, tab);
+        // (a list that is too long already gets no more: thousands of additions to one number take a while)
+        if (!__any_sync(0xffffffffu, any && *(volatile uint32_t*)&sh.count <= LIST)) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned who = __ballot_sync(0xffffffffu, x[k] >= floor);
+          if (!who) continue;
+          uint32_t at = 0;
+          if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+          if (x[k] >= floor && at < LIST)
+            sh.list[at] = (u64)order_key(x[k]) << 32 | (0xffffffffu - (uint32_t)(row.base + i + 32 * k));
+        }
       }
-    }
-    above(chunk, row.n, floor, [&](float x, int i) {
-      const uint32_t at = atomicAdd(&sh.count, 1u);
-      if (at < LIST) sh.list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(row.base + i));
-    });
-    __syncthreads();
-    cluster_barrier();
-    int n = 0;
-    for (int c = 0; c < ctas; ++c) {
-      const int m = (int)remote_u32(&sh.count, c);
-      if (rank == 0 && n + m <= LIST && tid < m) sh.all[n + tid] = remote_u64(&sh.list[tid], c);
-      n += m;
-    }
-    cluster_arrive();  // (the lists have been read)
-    if (n <= LIST) {
-      if (rank == 0)
-        finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, n, s, tab, top, temperature, frac, by_k ? top_k : LIST, by_p, top_p, mass, by_k || a.vocab <= LIST, min_key);
+      sum = warp_sum64(sum);
+      if (lane == 0) atomicAdd(&sh.sum, sum);
       __syncthreads();
-      cluster_wait();
-      return;
+      cluster_barrier();
+      for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
+    } else if (small) {
+      if (tid < row.n)
+        sh.list[tid] = (u64)order_key(to_f32(row.x[tid])) << 32 | (0xffffffffu - (uint32_t)tid);
+      if (tid == 0) sh.count = row.n;
+      __syncthreads();
     }
-    cluster_wait();
-    if (tid == 0) sh.count = 0;
+    if (list_k || small || !by_k) {
+      // the row's first CTA collects the lists, as far down as all of them are whole
+      if (rank == 0) {
+        uint32_t floor = 0;
+        if (list_k)
+          for (int c = 0; c < ctas; ++c) floor = max(floor, remote_u32(&sh.floor, c));
+        else if (!small)
+          floor = order_key(below(s, log2f((1.f - fmaxf(top_p, 0.f)) * ((float)mass * exp2f((float)-frac)) /
+                                           (2.f * a.vocab)) - 0.01f));
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+        bool whole = true;
+        for (int c = 0; c < ctas; ++c) {
+          const uint32_t m = remote_u32(&sh.count, c);
+          whole = whole && m <= LIST;
+          const u64 x = whole && tid < m ? remote_u64(&sh.list[tid], c) : 0;
+          if (x && (uint32_t)(x >> 32) >= floor) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < LIST) sh.all[at] = x;
+          }
+        }
+        __syncthreads();
+        if (tid == 0 && (!whole || sh.n > LIST || (list_k && sh.n < top_k && floor > order_key(LOWEST)))) sh.n = -1;
+        __syncthreads();
+      }
+      cluster_arrive();  // (the lists have been read)
+      if (rank == 0 && sh.n >= 0)
+        finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, sh.n, s, tab, top, temperature, frac,
+               by_k ? top_k : LIST, by_p, top_p, mass, by_k || small, min_key);
+      cluster_wait();
+      const int n = (int)remote_u32(reinterpret_cast<uint32_t*>(&sh.n), 0);
+      if (n >= 0 && rank) return;  // (the first CTA's wait is for those that are still there)
+      cluster_barrier();
+      if (n >= 0) return;
+    }
+    // long: counts over y
     sh.hist[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid & ~31; i < row.n; i += THREADS) {
-      const int at = i + lane;
-      const float x = at < row.n ? to_f32(row.x[at]) : -INFINITY;
-      const u64 w = by_p ? weight(x, s, tab) : 0;
-      if (at < row.n) add_bin(&sh.hist[bin_of(x, s)], w, by_p);
-    }
+#pragma unroll 4
+    for (int i = tid; i < row.n; i += THREADS) atomicAdd(&sh.hist[bin_of(to_f32(row.x[i]), s)].x, 1u);
     __syncthreads();
     cluster_barrier();
     uint32_t tokens;
     u64 w;
     merge_bins(sh, ctas, tokens, w);
     if (by_k) {
-      cut(sh, row, s, tab, ctas, by_p, true, (uint32_t)top_k, 0, tokens, w);
-      mass = sh.kept_w;
-    } else {
-      find_bin(sh, tokens, w, false, 0, ~0ull);
-      mass = sh.before_w + sh.in_w;
+      find_bin(sh, tokens, 0, true, (uint32_t)top_k, 0);
+      const int bin = sh.bin;
+      const uint32_t before = sh.before_n;
+      cut(sh, row, s, tab, ctas, true, (uint32_t)top_k, 0, bin, bin, before, 0, sh.in_n, lowest_key(s, bin),
+          highest_key(s, bin), false);
+      tokens = tid < bin ? tokens : tid == bin ? (uint32_t)top_k - before : 0;
+      if (by_p) {  // the kept tokens' weights
+        const uint32_t least = sh.least;
+        const int last = sh.last;
+        sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
+          return weights(count, i0, s, tab, [&](int i, float& x) {
+            x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
+            return i < row.n && kept(order_key(x), row.base + i, least, last);
+          });
+        });
+        __syncthreads();
+        cluster_barrier();
+        mass = total_of(sh.find, ctas);
+      }
     }
     if (by_p) {
-      if (by_k) {
-        // what the first cut left of the bins
-        if (tid > sh.first_bin) tokens = 0, w = 0;
-        if (tid == sh.first_bin) w = mass - sh.first_before;
+      const u64 want = part_of(top_p, mass);
+      // A bin's weights are its count times 2^(-t/8) .. 2^(-(t+1)/8) of the largest: where the border
+      // can lie, by what comes before it and by what comes after it
+      border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
+      const uint32_t least = sh.least;
+      const int last = sh.last;
+      int bin0 = sh.bin0, bin1 = sh.bin1;
+      u64 had;  // what this warp's span has before the border's bins
+      while (true) {
+        // what lies before those bins, by the warps' spans, and a histogram over the keys in them
+        const uint32_t low = lowest_key(s, bin1), high = highest_key(s, bin0);
+        const int shift = key_shift(low, high);
+        cluster_barrier();  // (the histogram is read no more)
+        sh.hist[tid] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
+          constexpr int N = decltype(count)::value;
+          float x[N];
+          int bin[N];
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int i = i0 + 32 * k;
+            x[k] = i < row.n ? to_f32(row.x[i]) : -INFINITY;
+            bin[k] = i < row.n && kept(order_key(x[k]), row.base + i, least, last) ? bin_of(x[k], s) : BINS;
+            any |= bin[k] <= bin1;
+          }
+          if (!__any_sync(0xffffffffu, any)) return 0;
+          u64 sum = 0, wx[N];
+#pragma unroll
+          for (int k = 0; k < N; ++k) wx[k] = weight(x[k], s, tab);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            if (bin[k] < bin0)
+              sum += wx[k];
+            else if (bin[k] <= bin1)
+              add_bin(&sh.hist[(high - order_key(x[k])) >> shift], wx[k], true);
+          }
+          return sum;
+        });
+        __syncthreads();
+        cluster_barrier();
+        const u64 before = total_of(sh.find, ctas);
+        had = lane == 0 ? sh.find.sums[tid >> 5] : 0;
+        merge_bins(sh, ctas, tokens, w);
+        find_bin(sh, tokens, w, true, 0xffffffffu, 0);  // all of them
+        const uint32_t in_n = sh.before_n + sh.in_n;
+        const u64 there = sh.before_w + sh.in_w;
+        if ((before < want && before + there >= want) || (bin0 == 0 && bin1 == BINS - 1)) {
+          cut(sh, row, s, tab, ctas, false, 0, want, bin0, bin1, 0, before, in_n, low, high, true);
+          break;
+        }
+        bin0 = 0;  // (not reached: the bounds hold but for roundings that they allow for)
+        bin1 = BINS - 1;
       }
-      const u64 want_w = part_of(top_p, mass);
-      cut(sh, row, s, tab, ctas, true, false, 0, want_w, tokens, w);
+      certain = min_key <= sh.least;
+      if (certain) {  // and the kept ones of the border's bins
+        const uint32_t new_least = sh.least;
+        const int new_last = sh.last;
+        __syncthreads();
+        sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
+          return weights(count, i0, s, tab, [&](int i, float& x) {
+            x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
+            const int bin = bin_of(x, s);
+            return i < row.n && bin >= bin0 && bin <= bin1 && kept(order_key(x), row.base + i, new_least, new_last);
+          });
+        });
+        if (lane == 0) sh.find.sums[tid >> 5] += had;
+      }
     }
   }
   uint32_t least = sh.least;
@@ -643,14 +798,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
     least = min_key;
     last = 0x7fffffff;
   }
-  const auto weigh = [&](int i) -> u64 {
-    const float x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
-    const bool in = i < row.n && kept(order_key(x), row.base + i, least, last);
-    if (!__any_sync(0xffffffffu, in)) return 0;
-    const u64 w = weight(x, s, tab);
-    return in ? w : 0;
+  const auto weigh = [&](auto count, int i0) -> u64 {
+    return weights(count, i0, s, tab, [&](int i, float& x) {
+      x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
+      return i < row.n && kept(order_key(x), row.base + i, least, last);
+    });
   };
-  sum_spans(sh.find, row.n, weigh);
+  if (!certain) sum_spans(sh.find, row.n, weigh);
   __syncthreads();
   cluster_barrier();
   const u64 total = total_of(sh.find, ctas);
@@ -679,10 +833,19 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   cluster_barrier();  // (the others read this CTA's sums)
 }
 
+// CTAs a row: as many as keep the GPU's 2 x 152 places busy once, but at least 2048 logits each, and
+// at most CHUNK bytes of them, so that two CTAs fit an SM.
+constexpr int CHUNK = 100 << 10, PLACES = 304;
+constexpr size_t ALONE = 112 << 10;
+
 template <typename T>
 int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
   // (the row's place holds `finish`'s numbers at the end)
-  const size_t bytes = max((size_t)a.chunk * sizeof(T) + 32, LIST * sizeof(uint2));
+  size_t bytes = max((size_t)a.chunk * sizeof(T) + 32, LIST * sizeof(uint2));
+  // Few rows: an SM for each CTA (a cluster's CTAs share SMs while others are idle), where all clusters fit
+  // at once: 15 of 8 do, 36 of 4.  (16 rows of 201088: 131 us as two waves of 8, 105 sharing SMs.)
+  const int most = ctas == 8 ? 15 : ctas == 4 ? 36 : PLACES / 2 / ctas;
+  if (rows <= most) bytes = max(bytes, ALONE);
   if (smem_optin((const void*)sample_kernel<T>, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * ctas);
@@ -698,9 +861,6 @@ int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }
 
-// CTAs a row: as many as keep the GPU's 2 x 152 places busy once, but at least 2048 logits each, and
-// at most CHUNK bytes of them, so that two CTAs fit an SM.
-constexpr int CHUNK = 100 << 10, PLACES = 304;
 int cluster_of(int rows, int vocab, int size) {
   int c = 1;
   while (c < MAX_CLUSTER && ((int64_t)vocab * size > (int64_t)CHUNK * c ||

@@ -125,7 +125,7 @@ __device__ __forceinline__ u64 weight(float x, const Scale& s, const Table& t) {
   u64 raw;
   int n;
   if (!weight_raw(x, s, t, raw, n) || n > 62) return 0;
-  return (raw + (1ull << (n - 1))) >> n;
+  return ((raw >> (n - 1)) + 1) >> 1;
 }
 // raw 2^-n / total, for one that is returned or compared: 64-bit arithmetic, for a few threads.
 __device__ __forceinline__ double ratio64(u64 raw, int n, u64 total) {
@@ -233,6 +233,23 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64* red, u64& all) {
   return v;
 }
 
+// The weights of the elements i, i + 32, .. that in(i, x) takes (and gives the logit of).
+template <typename N, typename F>
+__device__ __forceinline__ u64 weights(N, int i, const Scale& s, const Table& t, F in) {
+  float x[N::value];
+  bool is[N::value], any = false;
+#pragma unroll
+  for (int k = 0; k < N::value; ++k) any |= is[k] = in(i + 32 * k, x[k]);
+  if (!__any_sync(0xffffffffu, any)) return 0;
+  u64 sum = 0;
+#pragma unroll
+  for (int k = 0; k < N::value; ++k) {
+    const u64 w = weight(x[k], s, t);
+    sum += is[k] ? w : 0;
+  }
+  return sum;
+}
+
 // Where a running sum over a row passes a target.  The row's CTAs hold consecutive chunks of n
 // elements each (n differs in the last ones), a CTA's warps consecutive spans of its chunk.
 struct Locate {
@@ -242,15 +259,25 @@ struct Locate {
   int cta, warp;         // of the span
 };
 
-__device__ __forceinline__ int span_of(int n) { return (n + THREADS - 1) / THREADS * 32; }
+__device__ __forceinline__ int span_of(int n) { return (n + 4 * THREADS - 1) / (4 * THREADS) * 128; }
 
-// Sums f(i) over this CTA's warps' spans (every lane calls f; f is 0 from n on).
+// A number of elements that a lane takes at once, 32 apart: a weight is a chain of 50 operations, and four of
+// them side by side keep a scheduler with four warps busy.
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+typedef Count<1> One;
+typedef Count<4> Four;
+
+// Sums f over this CTA's warps' spans: f(count, i) is the sum over i, i + 32, .. of `count` elements
+// (every lane calls it; from n on they are 0).
 template <typename F>
 __device__ __forceinline__ void sum_spans(Locate& l, int n, F f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, span = span_of(n);
   u64 sum = 0;
   const int end = min(n, (warp + 1) * span);
-  for (int i = warp * span; i < end; i += 32) sum += f(i + lane);
+  for (int i = warp * span; i < end; i += 128) sum += f(Four(), i + lane);
   sum = warp_sum64(sum);
   if (lane == 0) l.sums[warp] = sum;
 }
@@ -299,7 +326,7 @@ __device__ __forceinline__ int locate(Locate& l, int ctas, int n, u64 target, F 
   const int part = (span / 32 + WARPS - 1) / WARPS * 32;
   u64 sum = 0;
   for (int i = first + warp * part; i < min(end, first + (warp + 1) * part); i += 32)
-    sum += f(i + lane);
+    sum += f(One(), i + lane);
   sum = warp_sum64(sum);
   if (lane == 0) l.fine[warp] = sum;
   __syncthreads();
@@ -308,7 +335,7 @@ __device__ __forceinline__ int locate(Locate& l, int ctas, int n, u64 target, F 
   while (w < WARPS - 1 && run + l.fine[w] <= target) run += l.fine[w++];
   if (warp != w) return -1;
   for (int i = first + w * part; i < min(end, first + (w + 1) * part); i += 32) {
-    const u64 v = f(i + lane);
+    const u64 v = f(One(), i + lane);
     const u64 up = warp_scan64(v, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, run + up > target);
     if (hit) return i + __ffs(hit) - 1;

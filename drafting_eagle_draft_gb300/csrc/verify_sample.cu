@@ -55,13 +55,24 @@ __device__ __forceinline__ Probs make_probs(const peagle_dist& d, int frac) {
   p.inv = (u64)((((unsigned __int128)1 << 127) - 1) / (d.total << p.up));
   return p;
 }
-// Of a logit at index i; every lane of the warp calls it, with in = false where there is none.
-__device__ __forceinline__ u64 prob_of(float x, int i, bool in, const Probs& p, int frac, const Table& t) {
-  in = in && kept(order_key(x), i, p.least, p.last);
-  if (!__any_sync(0xffffffffu, in)) return 0;
-  const u64 w = p.cold ? 1ull << frac : weight(x, p.s, t);
-  return in ? __umul64hi(w << p.up, p.inv) : 0;
+// Of logits at indices; every lane of the warp calls it, with in = false where there is none.
+template <int N>
+__device__ __forceinline__ void probs_of(const float (&x)[N], const int (&i)[N], const bool (&in)[N], const Probs& p,
+                                         int frac, const Table& t, u64 (&out)[N]) {
+  bool is[N], any = false;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    out[k] = 0;
+    any |= is[k] = in[k] && kept(order_key(x[k]), i[k], p.least, p.last);
+  }
+  if (!__any_sync(0xffffffffu, any)) return;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const u64 w = p.cold ? 1ull << frac : weight(x[k], p.s, t);
+    if (is[k]) out[k] = __umul64hi(w << p.up, p.inv);
+  }
 }
+
 // In 64 bits, for the comparison of a draft; every lane of the warp calls it, each with its own row.
 __device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, int frac, const Table& t) {
   const bool cold = d.temperature < COLD;
@@ -206,8 +217,12 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
       });
       __syncthreads();
       const uint32_t d = match[tid];
-      const u64 qi = prob_of(d ? draft[d - 1] : 0.f, (int)d - 1, d != 0, qq, draft_frac, tab);
-      ri = pi > qi ? pi - qi : 0;
+      const float x[1] = {d ? draft[d - 1] : 0.f};
+      const int at[1] = {(int)d - 1};
+      const bool is[1] = {d != 0};
+      u64 qi[1];
+      probs_of(x, at, is, qq, draft_frac, tab, qi);
+      ri = pi > qi[0] ? pi - qi[0] : 0;
     }
     u64 total;
     u64 up = block_scan(ri, red, total);
@@ -234,15 +249,39 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   }
   const T* row = rows + (int64_t)m * a.stride + base;
   bool use_q = with_q || only >= 0;
-  const auto rest = [&](int i) -> u64 {
-    const bool in = i < n;
-    const u64 mine = prob_of(in ? to_f32(row[i]) : 0.f, base + i, in, pp, frac, tab);
-    if (!use_q) return mine;
-    if (!with_q) return base + i == only ? 0 : mine;
-    if (!__any_sync(0xffffffffu, mine != 0)) return 0;
-    const uint32_t d = in ? from[i] : 0;
-    const u64 theirs = prob_of(d ? draft[d - 1] : 0.f, (int)d - 1, d != 0, qq, draft_frac, tab);
-    return mine > theirs ? mine - theirs : 0;
+  const auto rest = [&](auto count, int i0) -> u64 {
+    constexpr int N = decltype(count)::value;
+    float x[N];
+    int at[N];
+    bool in[N], any = false;
+    u64 mine[N], theirs[N], sum = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + 32 * k;
+      in[k] = i < n;
+      x[k] = in[k] ? to_f32(row[i]) : 0.f;
+      at[k] = base + i;
+    }
+    probs_of(x, at, in, pp, frac, tab, mine);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (use_q && at[k] == only) mine[k] = 0;
+      sum += mine[k];
+      any |= mine[k] != 0;
+    }
+    if (!use_q || !with_q || !__any_sync(0xffffffffu, any)) return sum;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t d = in[k] ? from[i0 + 32 * k] : 0;
+      in[k] = d != 0;
+      at[k] = (int)d - 1;
+      x[k] = d ? draft[d - 1] : 0.f;
+    }
+    probs_of(x, at, in, qq, draft_frac, tab, theirs);
+    sum = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum += mine[k] > theirs[k] ? mine[k] - theirs[k] : 0;
+    return sum;
   };
   sum_spans(find, n, rest);
   __syncthreads();
