@@ -4,17 +4,18 @@
 // A cluster of 1, 2, 4 or 8 CTAs takes a row.  Each CTA brings its chunk of the row into shared memory
 // once (asynchronous 16-byte copies; the largest logit is found as they arrive) and all further
 // passes run there.
-//   short   most filtered rows keep few tokens, and a bound below which none is kept costs one
-//           comparison a logit: the k-th largest of the threads' own maxima for top-k, and for top-p
-//           w >= (1 - p) S / (2 vocab) (all that lies below has less than (1 - p) S).  The tokens
-//           above it, up to LIST of them, go to the row's first CTA, which sorts them, cuts the
-//           order by k, p and min_p, sorts what is left by index and picks.
-//   long    otherwise the border is found over the whole row: a histogram over y = (x - M) log2(e) / T
-//           in steps of 1/8, counts and weights (16-bit parts of the weights, so that 32-bit
-//           additions hold), summed over the cluster; the bin in which the k-th token, or the top_p-th
-//           part of the mass, lies is gathered and ranked, or divided again by the logits' own order
-//           while it holds more than RANK tokens.  Then the kept tokens' weights are summed up for
-//           each warp's span of the row, and the span in which u S falls is divided again.
+//   short   Most filtered rows keep few tokens, and a bound below which none is kept costs one
+//           comparison a logit.  With top-k a CTA takes it from its threads' own maxima, so that its part
+//           of the first k, and some more, are above it.  With top-p alone the weights are added up
+//           first, and counted over y = (x - M) log2(e) / T in steps of 1/8: the counts bound what lies
+//           before a bin and behind it, and so the bins that the border can be in.  The tokens above,
+//           up to LIST of them, go to the row's first CTA, which sorts them, cuts the order by k, p
+//           and min_p, sorts what is left by index and picks.
+//   long    Otherwise the border is found over the whole row.  The bins that it can be in are divided by
+//           the logits' own order, counts and weights (in 16-bit parts, so that 32-bit additions hold)
+//           summed over the cluster, until RANK tokens are left, which are ranked; what lies before
+//           those bins is added up on the way for each warp's span of the row, and the span in which
+//           u S falls is divided again.
 // Sums are whole numbers (sample.cuh), so nothing depends on their order.
 #include "sample.cuh"
 
@@ -463,7 +464,8 @@ __device__ __forceinline__ void finish(Shared& sh, uint2* raws, const Args& a, i
 }
 
 // The first and last bin over y in which the running weight can reach `want`, `rest` being left behind
-// it (both in units of the largest weight), from the bins' counts: thread t has bin t's.
+// it (both in units of the largest weight), from the bins' counts (thread t has bin t's): a bin's
+// weights are between 2^(-(t+1)/8) and 2^(-t/8) each.
 __device__ __forceinline__ void border_bins(Shared& sh, uint32_t n, float want, float rest) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* red = reinterpret_cast<float*>(sh.red64);
@@ -615,54 +617,54 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   }
   bool certain = false;  // find.sums holds what lies before the border's bins
   if (by_k || by_p) {
-    u64 mass = 0;
-    if (!list_k && !small && !by_k) {
-      // S, and on the way the tokens that top_p can keep if S is 1
-      const float floor = fmaxf(below(s, log2f((1.f - fmaxf(top_p, 0.f)) / (2.f * a.vocab)) - 0.01f), LOWEST);
+    u64 mass = 0, w = 0, want = 0;
+    uint32_t tokens = 0;      // thread t: in bin t over y
+    bool listed = list_k || small;
+    uint32_t floor = 0;       // key from which the lists are wanted
+    if (small) {
+      if (tid < row.n)
+        sh.list[tid] = (u64)order_key(to_f32(row.x[tid])) << 32 | (0xffffffffu - (uint32_t)tid);
+      if (tid == 0) sh.count = row.n;
+      __syncthreads();
+    } else if (!by_k) {
+      // S and the counts over y, from which follow the bins that the border can lie in
       u64 sum = 0;
       for (int i = (tid & ~31) * 4 + lane; i < row.n + lane; i += 4 * THREADS) {
         float x[4];
-        bool any = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           x[k] = i + 32 * k < row.n ? to_f32(row.x[i + 32 * k]) : -INFINITY;
-          any |= x[k] >= floor;
+          if (i + 32 * k < row.n) atomicAdd(&sh.hist[bin_of(x[k], s)].x, 1u);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum += weight(x[k], s, tab);
-        // (a list that is too long already gets no more: thousands of additions to one number take a while)
-        if (!__any_sync(0xffffffffu, any && *(volatile uint32_t*)&sh.count <= LIST)) continue;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const unsigned who = __ballot_sync(0xffffffffu, x[k] >= floor);
-          if (!who) continue;
-          uint32_t at = 0;
-          if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
-          at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-          if (x[k] >= floor && at < LIST)
-            sh.list[at] = (u64)order_key(x[k]) << 32 | (0xffffffffu - (uint32_t)(row.base + i + 32 * k));
-        }
       }
       sum = warp_sum64(sum);
       if (lane == 0) atomicAdd(&sh.sum, sum);
       __syncthreads();
       cluster_barrier();
       for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
-    } else if (small) {
-      if (tid < row.n)
-        sh.list[tid] = (u64)order_key(to_f32(row.x[tid])) << 32 | (0xffffffffu - (uint32_t)tid);
-      if (tid == 0) sh.count = row.n;
-      __syncthreads();
+      merge_bins(sh, ctas, tokens, w);
+      want = part_of(top_p, mass);
+      border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
+      const int bin1 = sh.bin1;
+      find_bin(sh, tid <= bin1 ? tokens : 0, 0, true, 0xffffffffu, 0);
+      if (sh.before_n + sh.in_n <= LIST) {
+        listed = true;
+        floor = lowest_key(s, bin1);
+        above(chunk, row.n, bin1 == BINS - 1 ? LOWEST : below(s, -(bin1 + 1) * 0.125f), [&](float x, int i) {
+          if (bin_of(x, s) > bin1) return;
+          sh.list[atomicAdd(&sh.count, 1u)] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(row.base + i));
+        });
+        __syncthreads();
+        cluster_barrier();
+      }
     }
-    if (list_k || small || !by_k) {
-      // the row's first CTA collects the lists, as far down as all of them are whole
+    if (listed) {
+      // the row's first CTA collects the lists, with top-k as far down as all of them are whole
       if (rank == 0) {
-        uint32_t floor = 0;
         if (list_k)
           for (int c = 0; c < ctas; ++c) floor = max(floor, remote_u32(&sh.floor, c));
-        else if (!small)
-          floor = order_key(below(s, log2f((1.f - fmaxf(top_p, 0.f)) * ((float)mass * exp2f((float)-frac)) /
-                                           (2.f * a.vocab)) - 0.01f));
         if (tid == 0) sh.n = 0;
         __syncthreads();
         bool whole = true;
@@ -684,22 +686,21 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
         finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, sh.n, s, tab, top, temperature, frac,
                by_k ? top_k : LIST, by_p, top_p, mass, by_k || small, min_key);
       cluster_wait();
+      if (!list_k && rank) return;  // (the first CTA's wait is for those that are still there)
       const int n = (int)remote_u32(reinterpret_cast<uint32_t*>(&sh.n), 0);
-      if (n >= 0 && rank) return;  // (the first CTA's wait is for those that are still there)
+      if (n >= 0 && rank) return;
       cluster_barrier();
       if (n >= 0) return;
     }
-    // long: counts over y
-    sh.hist[tid] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < row.n; i += THREADS) atomicAdd(&sh.hist[bin_of(to_f32(row.x[i]), s)].x, 1u);
-    __syncthreads();
-    cluster_barrier();
-    uint32_t tokens;
-    u64 w;
-    merge_bins(sh, ctas, tokens, w);
+    // long
     if (by_k) {
+      sh.hist[tid] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+#pragma unroll 4
+      for (int i = tid; i < row.n; i += THREADS) atomicAdd(&sh.hist[bin_of(to_f32(row.x[i]), s)].x, 1u);
+      __syncthreads();
+      cluster_barrier();
+      merge_bins(sh, ctas, tokens, w);
       find_bin(sh, tokens, 0, true, (uint32_t)top_k, 0);
       const int bin = sh.bin;
       const uint32_t before = sh.before_n;
@@ -718,13 +719,11 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
         __syncthreads();
         cluster_barrier();
         mass = total_of(sh.find, ctas);
+        want = part_of(top_p, mass);
+        border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
       }
     }
     if (by_p) {
-      const u64 want = part_of(top_p, mass);
-      // A bin's weights are its count times 2^(-t/8) .. 2^(-(t+1)/8) of the largest: where the border
-      // can lie, by what comes before it and by what comes after it
-      border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
       const uint32_t least = sh.least;
       const int last = sh.last;
       int bin0 = sh.bin0, bin1 = sh.bin1;
