@@ -241,7 +241,7 @@ int64_t workspace(int dtype, int64_t batch, int K, int nq, int nkv, int hd, int 
   if ((hd != 64 && hd != 128) || K * G > 128 || nkv > 65535 || batch * K * nq > MAX_ROWS ||
       pcap > MAX_SLOTS || cap > MAX_SLOTS)
     return PEAGLE_ERR_UNSUPPORTED;
-  if (dtype == PEAGLE_BF16) return tc_workspace(batch, K, (int)G, nkv, hd);
+  if (dtype == PEAGLE_BF16) return tc_workspace(batch, K, (int)G, nkv, hd, pcap, cap);
   const Pieces pc = simt_pieces((int)batch, K, (int)G, nkv, pcap, cap);
   return (pc.shared + pc.own) * batch * K * nq * (hd + 2) * 4;
 }

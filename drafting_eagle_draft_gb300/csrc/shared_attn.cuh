@@ -28,7 +28,7 @@ struct Args {
 };
 
 // The bf16 kernels (shared_attn_tc.cu).
-int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd);
+int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd, int pcap, int cap);
 int launch_tc(const Args& a, int hd, cudaStream_t st);
 
 // Slots of the prefix, or -1 where it does not fit.

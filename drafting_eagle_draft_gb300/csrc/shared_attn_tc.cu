@@ -40,7 +40,7 @@ constexpr int TT = 128;      // slots a tile, rows a tile
 constexpr int CTAS = 152;
 constexpr int ENTRY = 3;     // what a unit costs besides its tiles, in tiles
 constexpr int MIN_SHARE = 4; // (of at least 2: a share between two others then has a tile of a pair)
-constexpr int LOAD_WARP = 8, MMA_WARP = 9, THREADS = 320;
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, THREADS = 352;  // (a warp of products for each group)
 constexpr float LOG2E = 1.44269504f;
 constexpr float LAZY = 8.f;
 
@@ -49,30 +49,37 @@ struct Smem {
   static constexpr int QB = TT * HD * 2;    // a row tile's queries
   static constexpr int SLOT = TT * HD * 2;  // a tile's keys, or its values
   static constexpr int RING = HD == 64 ? 10 : 5;
+  // Tensor memory: the groups' scores, their outputs, and, where there is room, their weights: then the
+  // scores of the next tile are computed while the weights are.  Else the weights lie over the scores.
+  static constexpr bool AHEAD = HD == 64;
+  static constexpr int O = 2 * TT, P = AHEAD ? 2 * TT + 2 * HD : 0, PW = AHEAD ? TT / 2 : TT;
   static constexpr int BYTES = 2 * QB + RING * SLOT + 1024;  // (aligned to 1024)
 };
 
 // The waits that peagle_set_wait_limit_shared can make unreachable.
-enum Wait { SLOT_FREE, Q_FULL, S_FULL, P_FULL, O_FULL, WAITS };
+enum Wait { SLOT_FREE, Q_FULL, S_FULL, P_FULL, PV_DONE, S_FREE, WAITS };
 constexpr unsigned long long DEFAULT_WAIT_NS = 2000000000ull;
 std::atomic<unsigned long long> wait_limit{DEFAULT_WAIT_NS};
 std::atomic<int> unreachable{-1};
 
+// A row tile is as many whole draft rows (all heads of the kv head) as fit 128.
+__host__ __device__ inline int draft_rows(int G) { return TT / G; }
+
 // Row slots of the workspace: prefix units of 2 x 128, own units of 2 x KG, CTAs of 2 x 128.
 struct Layout {
-  int units;           // of the prefix
+  int per;             // prefix units of a kv head
   int64_t own, cta;    // first row slot of each kind
   int64_t rows;
   int64_t header;      // bytes of the plan: the share, and each request's first cost
 };
 __host__ __device__ inline Layout layout_of(int64_t batch, int K, int G, int nkv) {
   Layout l;
-  const int64_t tiles = (batch * K * G + TT - 1) / TT;
-  l.units = (int)((tiles + 1) / 2 * nkv);
-  l.own = (int64_t)l.units * 2 * TT;
+  const int64_t tiles = (batch * K + draft_rows(G) - 1) / draft_rows(G);
+  l.per = (int)((tiles + 1) / 2);
+  l.own = (int64_t)l.per * nkv * 2 * TT;
   l.cta = l.own + batch * nkv * 2 * K * G;
-  l.rows = l.cta + (int64_t)CTAS * 2 * TT;
-  l.header = ((batch + 1) * 8 + 255) / 256 * 256;
+  l.rows = (l.cta + (int64_t)CTAS * 2 * TT + 3) / 4 * 4;  // (the sums behind 8 bytes a row start at 32)
+  l.header = ((batch + 1) * 4 + 255) / 256 * 256;
   return l;
 }
 
@@ -81,16 +88,16 @@ struct Costs {
   int tiles;         // of the prefix
   int pairs;         // of a kv head
   int pair, single;  // cost of a unit
-  int64_t head, prefix;
+  int head, prefix;
 };
 __device__ __forceinline__ Costs costs_of(const Args& a, int prefix) {
   Costs c;
   c.tiles = cdiv(prefix, TT);
-  const int rows = cdiv(a.batch * a.K * a.G, TT);
+  const int rows = cdiv(a.batch * a.K, draft_rows(a.G));
   c.pairs = rows / 2;
   c.pair = c.tiles ? 2 * c.tiles + ENTRY : 0;
   c.single = c.tiles && (rows & 1) ? c.tiles + ENTRY : 0;
-  c.head = (int64_t)c.pairs * c.pair + c.single;
+  c.head = c.pairs * c.pair + c.single;
   c.prefix = c.head * a.nkv;
   return c;
 }
@@ -100,50 +107,57 @@ __device__ __forceinline__ int own_cost(const Args& a, int b) {
 }
 
 // Tiles of a unit that begins at `start` (in cost) with `step` a tile, from cost `at` on.
-__device__ __forceinline__ int tile_from(int64_t at, int64_t start, int step, int tiles) {
-  const int64_t d = at - start - ENTRY;
+__device__ __forceinline__ int tile_from(int at, int start, int step, int tiles) {
+  const int d = at - start - ENTRY;
   if (d <= 0) return 0;
-  const int64_t t = step == 2 ? (d + 1) >> 1 : d;
-  return t < tiles ? (int)t : tiles;
+  return min(step == 2 ? (d + 1) >> 1 : d, tiles);
 }
 
 struct Unit {
   int b;        // request, or -1: the prefix
   int h;
-  int row;      // first row: of the kv head's rows in the batch, or of the request's
-  int rows;     // of both groups' tiles together
+  int row;      // first draft row, of the batch's
   bool pair;
   int slots;    // that its last row sees
   int t0, t1;   // this CTA's tiles
   int64_t place;  // its own row slots in the workspace
   int stride;     // of the groups' places in them
+  uint32_t entry; // ring entries before it
 };
+// Group w's part in it: tiles, first draft row, number of MMA rows.
+__device__ __forceinline__ int tiles_of(const Unit& x, int w) {
+  return x.pair ? x.t1 - x.t0 : (x.t1 - x.t0 + 1 - w) / 2;
+}
+__device__ __forceinline__ int row_of(const Args& a, const Unit& x, int w) {
+  return x.row + (x.pair ? w * draft_rows(a.G) : 0);
+}
+__device__ __forceinline__ int rows_of(const Args& a, const Unit& x, int w) {
+  return x.b < 0 ? min(draft_rows(a.G), a.batch * a.K - row_of(a, x, w)) * a.G : a.K * a.G;
+}
 
 // Walks a CTA's units.
 struct Walk {
-  int64_t begin, end, start;  // the share; of the unit that comes next
-  int prefix;                 // slots
-  int u, b, h;                // next prefix unit of head h, or (u < 0) request b's head h
+  int begin, end, start;  // the share; of the unit that comes next
+  int prefix;             // slots
+  int u, b, h;            // next prefix unit of head h, or (u < 0) request b's head h
 };
 
-template <typename L>
-__device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const L& l, Walk& w, Unit& x) {
+__device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const Layout& l, Walk& w, Unit& x) {
   while (w.start < w.end) {
-    const int64_t start = w.start;
+    const int start = w.start;
     int tiles, step;
     if (w.u >= 0) {
       x.b = -1;
       x.h = w.h;
       x.pair = w.u < c.pairs;
-      x.row = w.u * 2 * TT;
-      x.rows = min(2 * TT, a.batch * a.K * a.G - x.row);
+      x.row = w.u * 2 * draft_rows(a.G);
       x.slots = w.prefix;
       tiles = c.tiles;
       step = x.pair ? 2 : 1;
-      x.place = (int64_t)(w.h * (l.units / a.nkv) + w.u) * 2 * TT;
+      x.place = (int64_t)(w.h * l.per + w.u) * 2 * TT;
       x.stride = TT;
       w.start += x.pair ? c.pair : c.single;
-      if (++w.u == l.units / a.nkv) {
+      if (++w.u == l.per) {
         w.u = 0;
         if (++w.h == a.nkv) {
           w.u = -1;
@@ -155,8 +169,7 @@ __device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const L
       x.b = w.b;
       x.h = w.h;
       x.pair = false;
-      x.row = 0;
-      x.rows = a.K * a.G;
+      x.row = w.b * a.K;
       x.slots = slots_of(a, w.b);
       tiles = x.slots > 0 ? cdiv(x.slots, TT) : 0;
       step = 1;
@@ -178,7 +191,7 @@ __device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const L
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* errors,
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* errors,
                                        unsigned long long limit_ns) {
   if (tc::mbar_wait(bar, parity, abort, limit_ns)) return true;
   if (!*abort) raise_error(reinterpret_cast<unsigned*>(errors), PEAGLE_DEV_TIMEOUT);
@@ -188,13 +201,54 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
 __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, int lbo) {
   return (tc::smem_desc_sw128(addr) & ~((uint64_t)0x3fff << 16)) | (uint64_t)(lbo >> 4) << 16;
 }
-// D (+)= A B with A in tensor memory: two 16-bit elements a column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Products and commits are issued by one elected lane of a warp that runs converged: the operands then
+// reach the instruction's uniform registers with less ado than from a lone thread's.
+// D (+)= A B, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with A in tensor memory: two 16-bit elements a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+// Until the loads from tensor memory are in; their 32 registers are used behind it.
+__device__ __forceinline__ void ld_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+// 32 lanes x 16 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
       : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -212,91 +266,102 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 
 
 struct Barriers {
   uint64_t full[10], empty[10];  // ring slots
-  uint64_t q[2], s[2], p[2], o[2];
+  uint64_t q[2], s[2], read[2], p[2], pv[2], unit[2];  // of the groups
   uint64_t end;
 };
 
-// Ring entries of a piece of n tiles, in order: K 0, K 1, V 0, K 2, V 1, ...
-__device__ __forceinline__ int key_entry(int t) { return t ? 2 * t - 1 : 0; }
-__device__ __forceinline__ int value_entry(int t, int n) { return min(n, t + 2) + t; }
+// Ring entries of a piece of n tiles, in the order in which the products take them: `ahead` tiles of
+// keys, then values and the further keys in turn.
+__device__ __forceinline__ int key_entry(int t, int ahead) { return t < ahead ? t : 2 * t - ahead + 1; }
+__device__ __forceinline__ int value_entry(int t, int ahead, int n) { return min(n, t + ahead) + t; }
 
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
     shared_attn_kernel(const __grid_constant__ CUtensorMap prefix_k, const __grid_constant__ CUtensorMap prefix_v,
-                       const __grid_constant__ CUtensorMap own_k, const __grid_constant__ CUtensorMap own_v, Args a,
+                       const __grid_constant__ CUtensorMap own_k, const __grid_constant__ CUtensorMap own_v, const __grid_constant__ CUtensorMap queries, Args a,
                        unsigned long long limit_ns, int never) {
   typedef Smem<HD> M;
   constexpr int RING = M::RING, HALVES = HD / 64;
+  constexpr bool AHEAD = M::AHEAD;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = sm + 2 * M::QB;
   __shared__ Barriers bar;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_b;
-  __shared__ unsigned long long s_total;
-  __shared__ long long s_start;
+  __shared__ int s_abort, s_b, s_issued;
+  __shared__ int s_total, s_start;
   __shared__ int s_odd[2][2];  // whether a group met a draft value that is not finite; by its units in turn
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
+  // What the walks read, and each softmax group's own walk (its first thread's): not in registers.
+  __shared__ Layout l;
+  __shared__ Costs c;
+  __shared__ Walk s_walk[2];
+  __shared__ Unit s_unit[2][2];
+  __shared__ bool s_more[2][2];
   tc::pdl_launch_dependents();
 
+  const int prefix = prefix_of(a);
+  if (tid == 32) {
+    l = layout_of(a.batch, a.K, a.G, a.nkv);
+    c = costs_of(a, max(prefix, 0));
+  }
   if (tid == 0) {
     s_abort = 0;
     s_total = 0;
     const auto count = [&](int kind, int n) { return (uint32_t)(n + (never == kind)); };
     for (int i = 0; i < RING; ++i) {
       tc::mbar_init(&bar.full[i], 1);
-      tc::mbar_init(&bar.empty[i], count(SLOT_FREE, 1));
+      tc::mbar_init(&bar.empty[i], count(SLOT_FREE, 2));
     }
     for (int w = 0; w < 2; ++w) {
-      tc::mbar_init(&bar.q[w], count(Q_FULL, TT));
+      tc::mbar_init(&bar.q[w], count(Q_FULL, 1));
       tc::mbar_init(&bar.s[w], count(S_FULL, 1));
       tc::mbar_init(&bar.p[w], count(P_FULL, TT));
-      tc::mbar_init(&bar.o[w], count(O_FULL, 1));
+      tc::mbar_init(&bar.pv[w], count(PV_DONE, 1));
+      tc::mbar_init(&bar.read[w], count(S_FREE, TT));
+      tc::mbar_init(&bar.unit[w], 1);
     }
-    tc::mbar_init(&bar.end, 1);
+    tc::mbar_init(&bar.end, 2);
+    s_issued = 0;
     s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&prefix_k);
     tc::tma_prefetch_desc(&prefix_v);
     tc::tma_prefetch_desc(&own_k);
     tc::tma_prefetch_desc(&own_v);
+    tc::tma_prefetch_desc(&queries);
   }
   if (warp == MMA_WARP) {
     tc::tmem_alloc(&s_tmem, 512);
     tc::tmem_relinquish();
   }
-  const int prefix = prefix_of(a);
-  const Costs c = costs_of(a, max(prefix, 0));
-  unsigned long long mine = 0;
+  int mine = 0;
   if (prefix >= 0)
     for (int b = tid; b < a.batch; b += THREADS) mine += own_cost(a, b);
   __syncthreads();
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0 && mine) atomicAdd(&s_total, mine * a.nkv);
   __syncthreads();
-  const int64_t total = prefix >= 0 ? c.prefix + (int64_t)s_total : 0;
-  const int64_t share = max((int64_t)MIN_SHARE, (total + CTAS - 1) / CTAS);
+  const int total = prefix >= 0 ? c.prefix + s_total : 0;
+  const int share = max(MIN_SHARE, (total + CTAS - 1) / CTAS);
   Walk walk;
   walk.begin = blockIdx.x * share;
   walk.end = min(total, walk.begin + share);
   walk.prefix = prefix;
   if (warp == 0) {
     // the request that the share begins in; CTA 0 leaves every request's first cost for the join
-    long long* plan = reinterpret_cast<long long*>(a.part);
+    int* plan = reinterpret_cast<int*>(a.part);
     if (blockIdx.x == 0 && lane == 0) plan[0] = share;
-    int64_t run = c.prefix;
-    int b0 = a.batch;
-    int64_t at = total;
+    int run = c.prefix, b0 = a.batch, at = total;
     for (int b = 0; b < a.batch && (blockIdx.x == 0 || b0 == a.batch); b += 32) {
-      const int64_t x = b + lane < a.batch && prefix >= 0 ? (int64_t)own_cost(a, b + lane) * a.nkv : 0;
-      int64_t sum = x;
+      const int x = b + lane < a.batch && prefix >= 0 ? own_cost(a, b + lane) * a.nkv : 0;
+      int sum = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
       }
-      const int64_t first = run + sum - x;
+      const int first = run + sum - x;
       if (blockIdx.x == 0 && b + lane < a.batch) plan[1 + b + lane] = first;
       const unsigned in = __ballot_sync(0xffffffffu, x > 0 && first + x > walk.begin);
       if (in && b0 == a.batch) {
@@ -315,11 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
   if (walk.begin < c.prefix) {
-    walk.h = (int)(walk.begin / c.head);
-    const int64_t rest = walk.begin - walk.h * c.head;
-    walk.u = min((int)(rest / c.pair), c.pairs);
-    if (c.pair == 0) walk.u = 0;
-    walk.start = walk.h * c.head + (int64_t)walk.u * c.pair;
+    walk.h = walk.begin / c.head;
+    walk.u = min((walk.begin - walk.h * c.head) / c.pair, c.pairs);
+    walk.start = walk.h * c.head + walk.u * c.pair;
     walk.b = 0;
   } else {
     walk.u = -1;
@@ -328,8 +391,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     walk.h = 0;
     if (s_b < a.batch && walk.begin > walk.start) {
       const int cost = own_cost(a, s_b);
-      walk.h = (int)((walk.begin - walk.start) / cost);
-      walk.start += (int64_t)walk.h * cost;
+      walk.h = (walk.begin - walk.start) / cost;
+      walk.start += walk.h * cost;
     }
   }
   volatile int* abort = &s_abort;
@@ -347,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool shared = x.b < 0;
         const int z = shared ? x.h : x.b * a.nkv + x.h;
         // (a prefix that several row tiles read again stays in the cache)
-        const uint64_t policy = shared && l.units > a.nkv ? keep : once;
+        const uint64_t policy = shared && l.per > 1 ? keep : once;
         const int n = x.t1 - x.t0;
         const auto load = [&](const CUtensorMap* map, int t) {
           const int slot = it % RING;
@@ -358,14 +421,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tma_load_3d(ring + slot * M::SLOT + half * TT * 128, map, half * 64, (x.t0 + t) * TT, z,
                             &bar.full[slot], policy);
           ++it;
+          *(volatile int*)&s_issued = it;
           return true;
         };
         const CUtensorMap* mk = shared ? &prefix_k : &own_k;
         const CUtensorMap* mv = shared ? &prefix_v : &own_v;
-        on = load(mk, 0);
+        const int ahead = (x.pair ? 1 : 2) * (AHEAD ? 2 : 1);
+        for (int t = 0; on && t < min(ahead, n); ++t) on = load(mk, t);
         for (int t = 0; on && t < n; ++t) {
-          if (t + 1 < n) on = load(mk, t + 1);
-          on = on && load(mv, t);
+          on = load(mv, t);
+          if (on && t + ahead < n) on = load(mk, t + ahead);
         }
       }
       // no CTA ends with a copy in flight (those before the last RING are done: their slots were free)
@@ -376,150 +441,261 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else if (warp == MMA_WARP) {
-    if (lane == 0) {
-      const uint32_t base = tc::smem_u32(sm), rings = tc::smem_u32(ring);
-      const uint32_t idS = tc::idesc_bf16(TT, TT), idO = tc::idesc_bf16(TT, HD) | (1u << 16);
-      uint32_t it = 0, nq[2] = {}, np[2] = {};
-      bool on = true;
-      while (on && next_unit(a, c, l, walk, x)) {
-        const int n = x.t1 - x.t0;
-        const int count[2] = {x.pair ? n : (n + 1) / 2, x.pair ? n : n / 2};
-        // S of group w's step i
-        const auto scores = [&](int w, int i) {
-          const int t = x.pair ? i : 2 * i + w;
-          const uint32_t e = it + key_entry(t), slot = e % RING;
-          if (!wait(&bar.full[slot], (e / RING) & 1)) return false;
-          tc::fence_after_sync();
-          const uint64_t dq = operand_desc(base + w * M::QB, 16), dk = operand_desc(rings + slot * M::SLOT, 16);
-#pragma unroll
-          for (int k = 0; k < HD / 16; ++k)
-            tc::mma_bf16(tmem + w * TT, dq + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2,
-                         dk + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2, idS, k > 0);
-          tc::mma_commit(&bar.s[w]);
-          if (!x.pair || w == 1) tc::mma_commit(&bar.empty[slot]);
-          return true;
-        };
-        for (int w = 0; on && w < 2; ++w)
-          if (count[w]) on = wait(&bar.q[w], nq[w]++ & 1) && scores(w, 0);
-        for (int i = 0; on && i < count[0]; ++i)
-          for (int w = 0; on && w < 2; ++w) {
-            if (i >= count[w]) continue;
-            const int t = x.pair ? i : 2 * i + w;
-            const uint32_t e = it + value_entry(t, n), slot = e % RING;
-            on = wait(&bar.p[w], np[w]++ & 1) && wait(&bar.full[slot], (e / RING) & 1);
-            if (!on) break;
-            tc::fence_after_sync();
-            const uint64_t dv = operand_desc(rings + slot * M::SLOT, TT * 128);
-#pragma unroll
-            for (int k = 0; k < TT / 16; ++k)
-              mma_bf16_ts(tmem + 2 * TT + w * HD, tmem + w * TT + k * 8, dv + k * (16 * 128 >> 4), idO,
-                          i > 0 || k > 0);
-            if (!x.pair || w == 1) tc::mma_commit(&bar.empty[slot]);
-            if (i + 1 < count[w])
-              on = scores(w, i + 1);
-            else
-              tc::mma_commit(&bar.o[w]);
+  } else if (warp >= MMA_WARP) {
+    const int w = warp - MMA_WARP;
+    const uint32_t rings = tc::smem_u32(ring);
+    const uint32_t idS = tc::idesc_bf16(TT, TT) | (a.scale < 0.f ? 1u << 13 : 0u);  // (-Q)
+    const uint32_t idO = tc::idesc_bf16(TT, HD) | (1u << 16);
+    const uint64_t dq0 = operand_desc(tc::smem_u32(sm), 16), dk0 = operand_desc(rings, 16);
+    const uint64_t dv0 = operand_desc(rings, TT * 128);
+    // An entry is here.  (A slot's barrier tells an entry from the one a turn before and no more: a group
+    // that has no part in many units in a row would take an older one for its own.)
+    const auto here = [&](uint32_t e) {
+      const volatile int* issued = &s_issued;
+      if (*issued <= (int)e) {
+        const unsigned long long t0 = tc::globaltimer();
+        while (*issued <= (int)e && !*abort) {
+          if (tc::globaltimer() - t0 > limit_ns) {
+            raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_TIMEOUT);
+            *abort = 1;
           }
-        it += 2 * n;
+          __nanosleep(32);
+        }
+        if (*abort) return false;
+      }
+      return wait(&bar.full[e % RING], (e / RING) & 1);
+    };
+    const auto all_of = [](bool b) { return __all_sync(0xffffffffu, b) != 0; };
+    uint32_t it = 0, next = 0, nq = 0, ns = 0, np = 0, nr = 0, asked = 0;
+    // The group's next unit; `next` counts the ring entries before it.
+    const auto advance = [&](Unit& u) {
+      while (next_unit(a, c, l, walk, u)) {
+        if (tiles_of(u, w)) return true;
+        next += 2 * (u.t1 - u.t0);
+      }
+      return false;
+    };
+    // Its queries, by one copy for 64 dims: whole draft rows of the kv head's heads.
+    const auto ask_queries = [&](const Unit& u) {
+      if (lane == 0) {
+        tc::mbar_expect_tx(&bar.q[w], HALVES * 128 * draft_rows(a.G) * a.G);
+#pragma unroll
+        for (int half = 0; half < HALVES; ++half)
+          tc::tma_load_3d(sm + w * M::QB + half * TT * 128, &queries, half * 64, u.h * a.G, row_of(a, u, w), &bar.q[w],
+                          tc::policy_evict_first());
+      }
+      __syncwarp();
+      ++asked;
+    };
+    Unit y;
+    bool on = true, more = advance(x);
+    if (more) ask_queries(x);
+    while (on && more) {
+      it = next;
+      const int n = x.t1 - x.t0, count = tiles_of(x, w), ahead = (x.pair ? 1 : 2) * (AHEAD ? 2 : 1);
+      const bool pair = x.pair;
+      next += 2 * n;
+      more = advance(y);
+      // an entry is free when both groups are done with it, or the one that takes it twice over
+      const auto taken = [&](uint32_t slot) {
+        commit(&bar.empty[slot]);
+        if (!pair) commit(&bar.empty[slot]);
+      };
+      const auto scores = [&](int i) {
+        const uint32_t e = it + key_entry(pair ? i : 2 * i + w, ahead), slot = e % RING;
+        on = all_of(here(e));
+        if (!on) return;
+        tc::fence_after_sync();
+        const uint64_t dq = dq0 + w * (M::QB >> 4), dk = dk0 + slot * (M::SLOT >> 4);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          mma_ss(tmem + w * TT, dq + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2,
+                 dk + (k / 4) * (TT * 128 >> 4) + (k % 4) * 2, idS, k > 0);
+        commit(&bar.s[w]);
+        ++ns;
+        taken(slot);
+      };
+      on = all_of(wait(&bar.q[w], nq++ & 1));
+      if (on) scores(0);
+      for (int i = 0; on && i < count; ++i) {
+        if (AHEAD && i + 1 < count) {
+          on = all_of(wait(&bar.read[w], nr++ & 1));
+          if (on) scores(i + 1);
+          if (!on) break;
+        }
+        if (i + 1 == count && more) {  // the last scores are there: their queries' place is free
+          on = all_of(wait(&bar.s[w], (ns - 1) & 1));
+          if (!on) break;
+          ask_queries(y);
+        }
+        const uint32_t e = it + value_entry(pair ? i : 2 * i + w, ahead, n), slot = e % RING;
+        on = all_of(wait(&bar.p[w], np++ & 1) && here(e));
+        if (!on) break;
+        tc::fence_after_sync();
+        const uint64_t dv = dv0 + slot * (M::SLOT >> 4);
+#pragma unroll
+        for (int k = 0; k < TT / 16; ++k)
+          mma_ts(tmem + M::O + w * HD, tmem + M::P + w * M::PW + k * 8, dv + k * (16 * 128 >> 4), idO, i > 0 || k > 0);
+        commit(&bar.pv[w]);
+        taken(slot);
+        if (!AHEAD && i + 1 < count) scores(i + 1);
+      }
+      x = y;
+    }
+    if (asked > nq) {  // (after a wait that ran out: no CTA ends with a copy in flight)
+      const unsigned long long t0 = tc::globaltimer();
+      while (!tc::mbar_try_wait(&bar.q[w], (asked - 1) & 1) && tc::globaltimer() - t0 < limit_ns) {
       }
     }
   } else {
     const int w = warp >> 2, r = tid & (TT - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + w * TT, tO = tmem + lanes + 2 * TT + w * HD;
+    const uint32_t tS = tmem + lanes + w * TT, tO = tmem + lanes + M::O + w * HD, tP = tmem + lanes + M::P + w * M::PW;
     const float qs = fmaxf(fabsf(a.scale) * LOG2E, 0x1p-126f);
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     Stat* stat = reinterpret_cast<Stat*>(reinterpret_cast<char*>(a.part) + l.header);
     float* sums = reinterpret_cast<float*>(stat + l.rows);
-    uint32_t it = 0, ns = 0, no = 0;
-    bool on = true;
-    while (on && next_unit(a, c, l, walk, x)) {
-      const int n = x.t1 - x.t0, count = x.pair ? n : (n + 1 - w) / 2;
-      const uint32_t first = it;
-      it += 2 * n;
-      if (!count) continue;
-      const int at = x.pair ? w * TT + r : r;  // of the unit's rows
-      const bool in = at < x.rows;
-      const bool live = (at & ~31) < x.rows;   // any row of the warp
-      const int rr = x.row + at, bk = (x.b < 0 ? 0 : x.b * a.K) + rr / a.G, head = x.h * a.G + rr % a.G;
-      {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + (int64_t)bk * a.q_stride +
-                                                        (size_t)head * HD);
-        uint8_t* to = sm + w * M::QB;
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          uint4 y = in ? q[i] : make_uint4(0, 0, 0, 0);
-          y.x ^= flip, y.y ^= flip, y.z ^= flip, y.w ^= flip;
-          *reinterpret_cast<uint4*>(to + (i / 8) * TT * 128 + sw128(r, i % 8)) = y;
-        }
-        fence_proxy_async_smem();
-        tc::mbar_arrive(&bar.q[w]);
-      }
+    uint32_t ns = 0, npv = 0, units = 0;
+    // The group's unit number k, by its first thread, for all.
+    const auto advance = [&](uint32_t k, uint32_t entry) {
+      if (r) return;
+      Unit u;
+      bool more;
+      while ((more = next_unit(a, c, l, s_walk[w], u)) && !tiles_of(u, w)) entry += 2 * (u.t1 - u.t0);
+      u.entry = entry;
+      s_unit[w][k & 1] = u;  // (all threads of the group are behind unit k - 2: they gave its weights)
+      s_more[w][k & 1] = more;
+      tc::mbar_arrive(&bar.unit[w]);
+    };
+    if (r == 0) s_walk[w] = walk;
+    advance(0, 0);
+    bool on = __all_sync(0xffffffffu, wait(&bar.unit[w], 0)), more = on && s_more[w][0];
+    while (on && more) {
+      const Unit x = s_unit[w][units & 1];
+      const int n = x.t1 - x.t0, count = tiles_of(x, w), ahead = (x.pair ? 1 : 2) * (AHEAD ? 2 : 1);
+      advance(units + 1, x.entry + 2 * n);
+      const int rows = rows_of(a, x, w);
+      const bool in = r < rows;
+      const bool live = (r & ~31) < rows;   // any row of the warp
       const int all = x.b < 0 ? x.slots : limit_of(a, x.slots, 0);  // slots that every row sees
-      const int limit = x.b < 0 ? x.slots : limit_of(a, x.slots, min(rr / a.G, a.K - 1));
+      const int limit = x.b < 0 ? x.slots : limit_of(a, x.slots, min(r / a.G, a.K - 1));
       float m = -INFINITY, sum = 0.f;
       for (int i = 0; i < count; ++i) {
         const int t = x.pair ? i : 2 * i + w, slot0 = (x.t0 + t) * TT;
         on = __all_sync(0xffffffffu, wait(&bar.s[w], ns++ & 1));
         if (!on) break;
         tc::fence_after_sync();
+        if (i + 1 == count) {  // (before its weights: the one after is not given sooner)
+          on = __all_sync(0xffffffffu, wait(&bar.unit[w], ~units & 1));
+          if (!on) break;
+          more = s_more[w][~units & 1];
+        }
         const bool edge = slot0 + TT > all;
-        if (live) {
-          float s[TT];
-#pragma unroll
-          for (int k = 0; k < TT; k += 32) tc::tmem_ld32(tS + k, s + k);
-          tc::tmem_ld_wait();
+        const int seen = limit - slot0;
+        float scale = 1.f;
+        // The row comes in four parts, the next one on its way while one is used; twice, for the maximum and
+        // for the weights: 64 registers, and code that stays in the instruction cache (a row of 128
+        // registers, unrolled, took a third longer).
+        const auto parts = [&](auto use, auto last) {
+          float u[32], v[32];
+          tc::tmem_ld32(tS, u);
+          ld_wait(u);
+#pragma unroll 1
+          for (int c = 0; c < TT; c += 64) {
+            tc::tmem_ld32(tS + c + 32, v);
+            use(u, c);
+            ld_wait(v);
+            if (c == 0)
+              tc::tmem_ld32(tS + 64, u);
+            else
+              last();
+            use(v, c + 32);
+            ld_wait(u);
+          }
+        };
+        const auto mask = [&](float (&u)[32], int c) {
           if (edge) {
 #pragma unroll
-            for (int k = 0; k < TT; ++k)
-              if (slot0 + k >= limit) s[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if (c + k >= seen) u[k] = -INFINITY;
           }
-          float top[4] = {s[0], s[1], s[2], s[3]};
+        };
+        if (live) {
+          float top = -INFINITY;
+          parts(
+              [&](float (&u)[32], int c) {
+                mask(u, c);
+                float t0 = fmaxf(u[0], u[1]), t1 = fmaxf(u[2], u[3]);
 #pragma unroll
-          for (int k = 4; k < TT; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * qs;
-          float scale = 1.f;
+                for (int k = 4; k < 32; k += 4) {
+                  t0 = fmaxf(fmaxf(t0, u[k]), u[k + 1]);
+                  t1 = fmaxf(fmaxf(t1, u[k + 2]), u[k + 3]);
+                }
+                top = fmaxf(fmaxf(top, t0), t1);
+              },
+              [] {});
+          const float mx = top * qs;
           if (mx > m + LAZY || (m == -INFINITY && mx > -INFINITY)) {
             scale = m == -INFINITY ? 0.f : ex2(m - mx);
             m = mx;
           }
-          const float ref = m == -INFINITY ? 0.f : -m;
-          float add[4] = {};
-          float packed[TT / 2];
-#pragma unroll
-          for (int k = 0; k < TT; k += 2) {
-            const float p0 = ex2(fmaf(s[k], qs, ref)), p1 = ex2(fmaf(s[k + 1], qs, ref));
-            add[(k >> 1) & 3] += p0 + p1;
-            packed[k / 2] = __uint_as_float(pack2(p0, p1));
-          }
-          sum = sum * scale + ((add[0] + add[1]) + (add[2] + add[3]));
+          sum *= scale;
+        }
+        if (i > 0) {  // the last product has been added up
+          on = __all_sync(0xffffffffu, wait(&bar.pv[w], npv++ & 1));
+          if (!on) break;
+          tc::fence_after_sync();
+        }
+        if (live) {
           if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
-#pragma unroll
-            for (int k = 0; k < HD; k += 32) {
-              float o[32];
-              tc::tmem_ld32(tO + k, o);
+#pragma unroll 1
+            for (int k = 0; k < HD; k += 16) {
+              float o[16];
+              tc::tmem_ld16(tO + k, o);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int d = 0; d < 32; ++d) o[d] *= scale;
-              tc::tmem_st32(tO + k, o);
+              for (int d = 0; d < 16; ++d) o[d] *= scale;
+              tmem_st16(tO + k, o);
             }
           }
-          tc::tmem_st32(tS, packed);
-          tc::tmem_st32(tS + 32, packed + 32);
+          const float ref = m == -INFINITY ? 0.f : -m;
+          parts(
+              [&](float (&u)[32], int c) {
+                mask(u, c);
+                float a0 = 0.f, a1 = 0.f, packed[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                  const float p0 = ex2(fmaf(u[k], qs, ref)), p1 = ex2(fmaf(u[k + 1], qs, ref));
+                  const float p2 = ex2(fmaf(u[k + 2], qs, ref)), p3 = ex2(fmaf(u[k + 3], qs, ref));
+                  a0 += p0 + p1;
+                  a1 += p2 + p3;
+                  packed[k / 2] = __uint_as_float(pack2(p0, p1));
+                  packed[k / 2 + 1] = __uint_as_float(pack2(p2, p3));
+                }
+                sum += a0 + a1;
+                tmem_st16(tP + c / 2, packed);
+              },
+              [&] {
+                if (AHEAD) {
+                  tc::fence_before_sync();
+                  if (i + 1 < count) tc::mbar_arrive(&bar.read[w]);
+                }
+              });
           tc::tmem_st_wait();
+        } else if (AHEAD && i + 1 < count) {
+          tc::mbar_arrive(&bar.read[w]);
         }
         if (edge) {
           // this thread's slot of the values: behind every row's limit, or seen by some rows
-          const uint32_t e = first + value_entry(t, n);
+          const uint32_t e = x.entry + value_entry(t, ahead, n);
           on = __all_sync(0xffffffffu, wait(&bar.full[e % RING], (e / RING) & 1));
           if (!on) break;
           uint8_t* v = ring + e % RING * M::SLOT;
           if (slot0 + r >= x.slots) {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < HD / 8; ++k)
               *reinterpret_cast<uint4*>(v + (k / 8) * TT * 128 + sw128(r, k % 8)) = make_uint4(0, 0, 0, 0);
           } else if (slot0 + r >= all) {
+#pragma unroll 1
             for (int k = 0; k < HD / 8; ++k) {
               uint4* p = reinterpret_cast<uint4*>(v + (k / 8) * TT * 128 + sw128(r, k % 8));
               uint32_t y[4] = {p->x, p->y, p->z, p->w};
@@ -531,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
               if (odd) {
                 *p = make_uint4(y[0], y[1], y[2], y[3]);
-                *(volatile int*)&s_odd[w][no & 1] = 1;
+                *(volatile int*)&s_odd[w][units & 1] = 1;
               }
             }
           }
@@ -541,50 +717,54 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::mbar_arrive(&bar.p[w]);
       }
       if (!on) break;
-      on = __all_sync(0xffffffffu, wait(&bar.o[w], no & 1));
+      on = __all_sync(0xffffffffu, wait(&bar.pv[w], npv++ & 1));
       if (!on) break;
       tc::fence_after_sync();
       // every thread of the group is behind its last unit, whose flag serves the next one
-      const bool odd = *(volatile int*)&s_odd[w][no & 1];
-      if (r == 0) *(volatile int*)&s_odd[w][~no & 1] = 0;
-      ++no;
+      const bool odd = *(volatile int*)&s_odd[w][units & 1];
+      if (r == 0) *(volatile int*)&s_odd[w][~units & 1] = 0;
+      ++units;
       if (live) {
-        float o[HD];
+        const int64_t place = (x.t0 ? l.cta + (int64_t)blockIdx.x * 2 * TT + w * TT : x.place + w * x.stride) + r;
+        if (in) stat[place] = {m, sum};
+        float* to = sums + place * HD;
+#pragma unroll 1
+        for (int k = 0; k < HD; k += 32) {
+          float o[32];
+          tc::tmem_ld32(tO + k, o);
+          ld_wait(o);
+          if (in) {
 #pragma unroll
-        for (int k = 0; k < HD; k += 32) tc::tmem_ld32(tO + k, o + k);
-        tc::tmem_ld_wait();
+            for (int d = 0; d < 32; d += 8)
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + k + d), "f"(o[d]),
+                           "f"(o[d + 1]), "f"(o[d + 2]), "f"(o[d + 3]), "f"(o[d + 4]), "f"(o[d + 5]), "f"(o[d + 6]),
+                           "f"(o[d + 7])
+                           : "memory");
+          }
+        }
         if (in && odd) {
           const bf16* v = static_cast<const bf16*>(a.v) + ((size_t)x.b * a.nkv + x.h) * a.cap * HD;
           for (int slot = all; slot < limit; ++slot) {
             const int t = slot / TT - x.t0;
             if (t < 0 || t >= n || (t & 1) != w) continue;  // another group's, or CTA's
-#pragma unroll
+#pragma unroll 1
             for (int d = 0; d < HD; ++d) {
-              const float y = __bfloat162float(v[(size_t)slot * HD + d]);
-              if (!(fabsf(y) < INFINITY)) o[d] += y;
+              const float z = __bfloat162float(v[(size_t)slot * HD + d]);
+              if (!(fabsf(z) < INFINITY)) to[d] += z;
             }
           }
-        }
-        if (in) {
-          const int64_t place = (x.t0 ? l.cta + (int64_t)blockIdx.x * 2 * TT + w * TT : x.place + w * x.stride) + r;
-          stat[place] = {m, sum};
-          float4* to = reinterpret_cast<float4*>(sums + place * HD);
-#pragma unroll
-          for (int d = 0; d < HD; d += 4) to[d / 4] = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
         }
       }
       tc::fence_before_sync();
     }
   }
+  // products that were issued and not waited for (after a wait that ran out) end before their memory goes
+  if (warp >= MMA_WARP) commit(&bar.end);
   __syncwarp();
   __syncthreads();
   if (warp == MMA_WARP) {
-    if (lane == 0) {
-      // products that were issued and not waited for (after a wait that ran out) end first
-      tc::mma_commit(&bar.end);
-      const unsigned long long t0 = tc::globaltimer();
-      while (!tc::mbar_try_wait(&bar.end, 0) && tc::globaltimer() - t0 < DEFAULT_WAIT_NS) {
-      }
+    const unsigned long long t0 = tc::globaltimer();
+    while (!tc::mbar_try_wait(&bar.end, 0) && tc::globaltimer() - t0 < DEFAULT_WAIT_NS) {
     }
     __syncwarp();
     tc::fence_after_sync();
@@ -608,8 +788,8 @@ __global__ void __launch_bounds__(256) shared_join_kernel(Args a) {
   }
   const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
   const Costs c = costs_of(a, prefix);
-  const long long* plan = reinterpret_cast<const long long*>(a.part);
-  const int64_t share = plan[0];
+  const int* plan = reinterpret_cast<const int*>(a.part);
+  const int share = plan[0];
   const Stat* stat = reinterpret_cast<const Stat*>(reinterpret_cast<const char*>(a.part) + l.header);
   const float* sums = reinterpret_cast<const float*>(stat + l.rows);
   const int h = head / a.G, g = head % a.G;
@@ -625,12 +805,12 @@ __global__ void __launch_bounds__(256) shared_join_kernel(Args a) {
     m = top;
   };
   // a unit's pieces: group `w`'s sums of each, or both groups' where they share the rows
-  const auto unit = [&](int64_t start, int tiles, bool pair, int w, int64_t place, int stride, int r) {
+  const auto unit = [&](int start, int tiles, bool pair, int w, int64_t place, int stride, int r) {
     const int step = pair ? 2 : 1;
-    const int64_t c0 = (start + ENTRY) / share, c1 = (start + ENTRY + (int64_t)(tiles - 1) * step) / share;
-    for (int64_t k = c0; k <= c1; ++k) {
+    const int c0 = (start + ENTRY) / share, c1 = (start + ENTRY + (tiles - 1) * step) / share;
+    for (int k = c0; k <= c1; ++k) {
       const int n = tile_from((k + 1) * share, start, step, tiles) - tile_from(k * share, start, step, tiles);
-      const int64_t at = k == c0 ? place : l.cta + k * 2 * TT;
+      const int64_t at = k == c0 ? place : l.cta + (int64_t)k * 2 * TT;
       const int by = k == c0 ? stride : TT;
       if (pair) {
         add(at + w * by + r);
@@ -641,13 +821,13 @@ __global__ void __launch_bounds__(256) shared_join_kernel(Args a) {
     }
   };
   if (c.tiles) {
-    const int rr = row * a.G + g, u = rr / (2 * TT), r = rr % (2 * TT);
-    unit(h * c.head + (int64_t)u * c.pair, c.tiles, u < c.pairs, r / TT, (int64_t)(h * (l.units / a.nkv) + u) * 2 * TT,
-         TT, r % TT);
+    const int per = draft_rows(a.G), tile = row / per, u = tile / 2;
+    unit(h * c.head + u * c.pair, c.tiles, u < c.pairs, tile & 1, (int64_t)(h * l.per + u) * 2 * TT, TT,
+         row % per * a.G + g);
   }
   if (slots > 0) {
     const int tiles = cdiv(slots, TT);
-    unit(plan[1 + b] + (int64_t)h * (tiles + ENTRY), tiles, false, 0, l.own + ((int64_t)b * a.nkv + h) * 2 * a.K * a.G,
+    unit(plan[1 + b] + h * (tiles + ENTRY), tiles, false, 0, l.own + ((int64_t)b * a.nkv + h) * 2 * a.K * a.G,
          a.K * a.G, (row % a.K) * a.G + g);
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
@@ -684,14 +864,25 @@ bool tile_map(CUtensorMap* out, const void* base, int hd, int capacity, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [draft rows][heads][hd], boxes of 64 dims x a kv head's heads x a row tile's draft rows.
+bool query_map(CUtensorMap* out, const Args& a, int hd) {
+  const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)a.nq, (cuuint64_t)a.batch * a.K};
+  const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)draft_rows(a.G)}, one[3] = {1, 1, 1};
+  const Encode f = encoder();
+  return f && f(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD>
 int launch(const Args& a, cudaStream_t st) {
-  CUtensorMap pk, pv, k, v;
+  CUtensorMap pk, pv, k, v, q;
   if (!tile_map(&pk, a.pk, HD, a.pcap, a.nkv) || !tile_map(&pv, a.pv, HD, a.pcap, a.nkv) ||
-      !tile_map(&k, a.k, HD, a.cap, (int64_t)a.batch * a.nkv) || !tile_map(&v, a.v, HD, a.cap, (int64_t)a.batch * a.nkv))
+      !tile_map(&k, a.k, HD, a.cap, (int64_t)a.batch * a.nkv) || !tile_map(&v, a.v, HD, a.cap, (int64_t)a.batch * a.nkv) || !query_map(&q, a, HD))
     return PEAGLE_ERR_CUDA;
   if (smem_optin((const void*)shared_attn_kernel<HD>, Smem<HD>::BYTES) != cudaSuccess) return PEAGLE_ERR_CUDA;
-  shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, a, wait_limit.load(), unreachable.load());
+  shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, q, a, wait_limit.load(), unreachable.load());
   if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
   const int64_t warps = (int64_t)a.batch * a.K * a.nq;
   return launch_pdl(shared_join_kernel<HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a) == cudaSuccess
@@ -701,7 +892,11 @@ int launch(const Args& a, cudaStream_t st) {
 
 }  // namespace
 
-int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd) {
+int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd, int pcap, int cap) {
+  const int64_t tiles = (batch * K + draft_rows(G) - 1) / draft_rows(G);
+  // the costs are counted in 32 bits
+  if (tiles * nkv * (pcap / TT + 1 + ENTRY) + batch * nkv * (cap / TT + 1 + ENTRY) >= 1 << 29)
+    return PEAGLE_ERR_UNSUPPORTED;
   const Layout l = layout_of(batch, K, G, nkv);
   return l.header + l.rows * (hd + 2) * 4;
 }

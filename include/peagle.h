@@ -705,7 +705,8 @@ int64_t peagle_verify_sample_workspace(int32_t batch, int32_t K, int32_t vocab);
  * beyond the capacity: KV_OVERFLOW, and the rows concerned are left as they are.  Waits inside the
  * kernel are bounded; one that ran out raises TIMEOUT, and the call's results are not to be used.
  * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; K * n_q_heads / n_kv_heads <= 128; batch * K *
- * n_q_heads, prefix_capacity and capacity <= 2^24; n_kv_heads <= 65535.  A workspace that is too small is
+ * n_q_heads, prefix_capacity and capacity <= 2^24; n_kv_heads <= 65535; for bf16, row tiles of 128 x slot
+ * tiles of 128 (all requests' capacities among them, each with 4 more) < 2^29.  A workspace that is too small is
  * PEAGLE_ERR_CAPACITY. */
 int peagle_decode_attention_shared(int32_t dtype, int32_t batch, int32_t K, int32_t n_q_heads,
                                    int32_t n_kv_heads, int32_t head_dim, const void* q,
@@ -725,7 +726,7 @@ int64_t peagle_decode_attention_shared_workspace(int32_t dtype, int32_t batch, i
 /* Failure-path drill of the waits inside peagle_decode_attention_shared's bf16 kernel, as
  * peagle_set_wait_limit_quant is for the 8-bit cache: a wait gives up after limit_ns nanoseconds (0: the
  * default of 2 s), and unreachable_wait >= 0 names one that can never succeed: 0 a copied tile's place to
- * be free again, 1 queries, 2 scores, 3 weights, 4 outputs added up; -1 none.  For the process's calls
+ * be free again, 1 queries, 2 scores, 3 weights, 4 outputs added up, 5 scores read (head_dim 64); -1 none.  For the process's calls
  * that follow.  Returns PEAGLE_ERR_INVALID for another wait. */
 int peagle_set_wait_limit_shared(uint64_t limit_ns, int32_t unreachable_wait);
 

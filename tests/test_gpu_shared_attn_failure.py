@@ -10,11 +10,13 @@ from test_gpu_shared_attn import Call
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("wait", range(5))
+@pytest.mark.parametrize("wait", range(6))
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("shape", ["pairs", "long", "many"])
 def test_a_wait_that_runs_out(shape, hd, wait):
     m = pk()
+    if wait == 5 and hd == 128:
+        pytest.skip("scores are read before their weights are stored over them: no wait of its own")
     if shape == "pairs":
         c = Call("bf16", 9, 8, 16, 2, hd, 100000, [10 * i for i in range(9)])
     elif shape == "long":

@@ -53,7 +53,7 @@ def test_workspace_is_exactly_what_is_wanted(pk):  # noqa: F811
 
 
 def test_the_wait_drill_refuses_other_waits(pk):  # noqa: F811
-    for wait in (-2, 5):
+    for wait in (-2, 6):
         assert pk.lib().peagle_set_wait_limit_shared(0, wait) == pk.PEAGLE_ERR_INVALID
     with pytest.raises(pk.PeagleError):
         pk.peagle_set_wait_limit_shared(0, 1 << 33)
