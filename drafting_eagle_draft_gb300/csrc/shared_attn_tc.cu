@@ -24,6 +24,7 @@
 // Values that a row does not see never reach it: slots behind the last visible one are cleared in
 // shared memory before the product, and in the slots that only some rows see (a draft block) values
 // that are not finite are cleared and added to the rows that see them at the end.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -38,7 +39,7 @@ namespace {
 
 constexpr int TT = 128;      // slots a tile, rows a tile
 constexpr int CTAS = 152;
-constexpr int ENTRY = 3;     // what a unit costs besides its tiles, in tiles
+constexpr int ENTRY = 4;     // what a unit costs besides its tiles, in tiles
 constexpr int MIN_SHARE = 4; // (of at least 2: a share between two others then has a tile of a pair)
 constexpr int LOAD_WARP = 8, MMA_WARP = 9, THREADS = 352;  // (a warp of products for each group)
 constexpr float LOG2E = 1.44269504f;
@@ -278,7 +279,7 @@ __device__ __forceinline__ int value_entry(int t, int ahead, int n) { return min
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
     shared_attn_kernel(const __grid_constant__ CUtensorMap prefix_k, const __grid_constant__ CUtensorMap prefix_v,
-                       const __grid_constant__ CUtensorMap own_k, const __grid_constant__ CUtensorMap own_v, const __grid_constant__ CUtensorMap queries, Args a,
+                       const __grid_constant__ CUtensorMap own_k, const __grid_constant__ CUtensorMap own_v, const __grid_constant__ CUtensorMap queries, Args a, Layout l,
                        unsigned long long limit_ns, int never) {
   typedef Smem<HD> M;
   constexpr int RING = M::RING, HALVES = HD / 64;
@@ -293,7 +294,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int s_odd[2][2];  // whether a group met a draft value that is not finite; by its units in turn
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // What the walks read, and each softmax group's own walk (its first thread's): not in registers.
-  __shared__ Layout l;
   __shared__ Costs c;
   __shared__ Walk s_walk[2];
   __shared__ Unit s_unit[2][2];
@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int prefix = prefix_of(a);
   if (tid == 32) {
-    l = layout_of(a.batch, a.K, a.G, a.nkv);
     c = costs_of(a, max(prefix, 0));
   }
   if (tid == 0) {
@@ -772,70 +771,92 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins a row's pieces; a warp a row and head.
+// Joins the pieces of a request's rows and a kv head; a warp a row and head, several in turn.
 template <int HD>
-__global__ void __launch_bounds__(256) shared_join_kernel(Args a) {
+__global__ void __launch_bounds__(256) shared_join_kernel(Args a, Layout l) {
   constexpr int DL = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int row = (int)(i / a.nq), head = (int)(i % a.nq);
+  const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y, rows = a.K * a.G;
   tc::pdl_wait();
-  if (row >= a.batch * a.K) return;
-  const int prefix = prefix_of(a), b = row / a.K, slots = prefix < 0 ? -1 : slots_of(a, b);
+  const int prefix = prefix_of(a), slots = prefix < 0 ? -1 : slots_of(a, b);
   if (slots < 0) {
-    if (lane == 0) raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_KV_OVERFLOW);
+    if (threadIdx.x == 0) raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_KV_OVERFLOW);
     return;
   }
-  const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
   const Costs c = costs_of(a, prefix);
   const int* plan = reinterpret_cast<const int*>(a.part);
-  const int share = plan[0];
+  const int share = plan[0], per = draft_rows(a.G);
   const Stat* stat = reinterpret_cast<const Stat*>(reinterpret_cast<const char*>(a.part) + l.header);
   const float* sums = reinterpret_cast<const float*>(stat + l.rows);
-  const int h = head / a.G, g = head % a.G;
-  float m = -INFINITY, total = 0.f, o[DL] = {};
-  const auto add = [&](int64_t place) {
-    const Stat s = stat[place];
-    if (s.l == 0.f) return;
-    const float top = fmaxf(m, s.m), x = exp2f(m - top), y = exp2f(s.m - top);
-    total = total * x + s.l * y;
-    const float* from = sums + place * HD + lane * DL;
-#pragma unroll
-    for (int d = 0; d < DL; ++d) o[d] = fmaf(o[d], x, y * from[d]);
-    m = top;
+  // A unit's pieces: of each CTA that has one, and of both groups where they share the rows.
+  struct Span {
+    int start, tiles, first, pieces, w, stride;
+    bool pair;
+    int64_t place;  // the unit's own row slots
   };
-  // a unit's pieces: group `w`'s sums of each, or both groups' where they share the rows
-  const auto unit = [&](int start, int tiles, bool pair, int w, int64_t place, int stride, int r) {
-    const int step = pair ? 2 : 1;
-    const int c0 = (start + ENTRY) / share, c1 = (start + ENTRY + (tiles - 1) * step) / share;
-    for (int k = c0; k <= c1; ++k) {
-      const int n = tile_from((k + 1) * share, start, step, tiles) - tile_from(k * share, start, step, tiles);
-      const int64_t at = k == c0 ? place : l.cta + (int64_t)k * 2 * TT;
-      const int by = k == c0 ? stride : TT;
-      if (pair) {
-        add(at + w * by + r);
-      } else {
-        add(at + r);
-        if (n > 1) add(at + by + r);
-      }
+  const auto span_of = [&](int start, int tiles, bool pair, int w, int64_t place, int stride) {
+    Span x = {start, tiles, (start + ENTRY) / share, 0, w, stride, pair, place};
+    const int last = (start + ENTRY + (tiles - 1) * (pair ? 2 : 1)) / share;
+    if (tiles) x.pieces = (last - x.first + 1) * (pair ? 1 : 2);
+    return x;
+  };
+  const int own_tiles = slots > 0 ? cdiv(slots, TT) : 0;
+  const Span own = span_of(own_tiles ? plan[1 + b] + h * (own_tiles + ENTRY) : 0, own_tiles, false, 0,
+                           l.own + ((int64_t)b * a.nkv + h) * 2 * rows, rows);
+  Span shared = {};
+  int tile = -1, pieces = 0;
+  int64_t place = 0;  // of piece `lane`, but for the row in it; -1: it has none
+  // Piece i of the row: the prefix unit's, then the own unit's.
+  const auto piece = [&](int i) -> int64_t {
+    if (i >= pieces) return -1;
+    const bool mine = i >= shared.pieces;
+    const Span& x = mine ? own : shared;
+    if (mine) i -= shared.pieces;
+    const int k = x.first + (x.pair ? i : i >> 1), w = x.pair ? x.w : i & 1, step = x.pair ? 2 : 1;
+    const int n = tile_from((k + 1) * share, x.start, step, x.tiles) - tile_from(k * share, x.start, step, x.tiles);
+    if (!x.pair && n <= w) return -1;
+    return k == x.first ? x.place + w * x.stride : l.cta + (int64_t)k * 2 * TT + w * TT;
+  };
+  for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.z * 8) {
+    const int j = r / a.G, g = r - j * a.G, row = b * a.K + j, t = row / per;
+    if (t != tile) {
+      tile = t;
+      const int u = t / 2;
+      shared = span_of(h * c.head + u * c.pair, c.tiles, u < c.pairs, t & 1, (int64_t)(h * l.per + u) * 2 * TT, TT);
+      pieces = shared.pieces + own.pieces;
+      place = piece(lane);
     }
-  };
-  if (c.tiles) {
-    const int per = draft_rows(a.G), tile = row / per, u = tile / 2;
-    unit(h * c.head + u * c.pair, c.tiles, u < c.pairs, tile & 1, (int64_t)(h * l.per + u) * 2 * TT, TT,
-         row % per * a.G + g);
-  }
-  if (slots > 0) {
-    const int tiles = cdiv(slots, TT);
-    unit(plan[1 + b] + h * (tiles + ENTRY), tiles, false, 0, l.own + ((int64_t)b * a.nkv + h) * 2 * a.K * a.G,
-         a.K * a.G, (row % a.K) * a.G + g);
-  }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  bf16* out = static_cast<bf16*>(a.out) + ((size_t)row * a.nq + head) * HD + lane * DL;
+    const int in_tile = (row - t * per) * a.G + g;
+    float m = -INFINITY, total = 0.f, o[DL] = {};
+    for (int base = 0; base < pieces; base += 32) {
+      // a lane a piece: all of their statistics at once
+      int64_t at = base ? piece(base + lane) : place;
+      Stat mine = {-INFINITY, 0.f};
+      if (at >= 0) mine = stat[at += base + lane < shared.pieces ? in_tile : r];
+      const float top = fmaxf(m, warp_max(mine.m));
+      const float old = top == -INFINITY ? 1.f : exp2f(m - top);
+      const float weight = mine.l == 0.f ? 0.f : exp2f(mine.m - top);
+      total = total * old + warp_sum(mine.l == 0.f ? 0.f : mine.l * weight);
 #pragma unroll
-  for (int d = 0; d < DL; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack2(o[d] * inv, o[d + 1] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(size_t)row * a.nq + head] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718f;
+      for (int d = 0; d < DL; ++d) o[d] *= old;
+      const unsigned any = __ballot_sync(0xffffffffu, mine.l != 0.f);
+      const int end = 32 - __clz(any);
+#pragma unroll 4
+      for (int i = 0; i < end; ++i) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, i);
+        const float y = __shfl_sync(0xffffffffu, weight, i);
+        if (!(any >> i & 1)) continue;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[d] = fmaf(y, sums[from * HD + lane * DL + d], o[d]);
+      }
+      m = top;
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const size_t head = (size_t)row * a.nq + h * a.G + g;
+    bf16* out = static_cast<bf16*>(a.out) + head * HD + lane * DL;
+#pragma unroll
+    for (int d = 0; d < DL; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack2(o[d] * inv, o[d + 1] * inv);
+    if (a.lse && lane == 0) a.lse[head] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718f;
+  }
 }
 
 typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -882,10 +903,14 @@ int launch(const Args& a, cudaStream_t st) {
       !tile_map(&k, a.k, HD, a.cap, (int64_t)a.batch * a.nkv) || !tile_map(&v, a.v, HD, a.cap, (int64_t)a.batch * a.nkv) || !query_map(&q, a, HD))
     return PEAGLE_ERR_CUDA;
   if (smem_optin((const void*)shared_attn_kernel<HD>, Smem<HD>::BYTES) != cudaSuccess) return PEAGLE_ERR_CUDA;
-  shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, q, a, wait_limit.load(), unreachable.load());
+  const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
+  shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, q, a, l, wait_limit.load(), unreachable.load());
   if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
-  const int64_t warps = (int64_t)a.batch * a.K * a.nq;
-  return launch_pdl(shared_join_kernel<HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a) == cudaSuccess
+  // A warp takes one row where all of them fit the GPU at once, else several: it finds their pieces once.
+  const int64_t blocks = (int64_t)a.batch * a.nkv;
+  const int most = (a.K * a.G + 7) / 8;
+  const int z = (int)std::min<int64_t>(most, std::max<int64_t>(1, CTAS * 8 / blocks));
+  return launch_pdl(shared_join_kernel<HD>, dim3(a.batch, a.nkv, z), dim3(256), 0, st, a, l) == cudaSuccess
              ? PEAGLE_OK
              : PEAGLE_ERR_CUDA;
 }
