@@ -285,7 +285,7 @@ extern "C" int peagle_decode_attention_shared(int32_t dtype, int32_t batch, int3
   if (workspace_bytes < need) return PEAGLE_ERR_CAPACITY;
   const sha::Args a = {q, q_stride, prefix_k, prefix_v, prefix_len, k_cache, v_cache, seq_lens, batch, K,
                        n_q_heads, n_kv_heads, n_q_heads / n_kv_heads, prefix_capacity, capacity, causal, scale,
-                       out, out_lse, errors, (float*)workspace};
+                       out, out_lse, errors, (float*)workspace, 0};
   const cudaStream_t st = (cudaStream_t)stream;
   if (dtype == PEAGLE_F32) return head_dim == 64 ? sha::launch_simt<64>(a, st) : sha::launch_simt<128>(a, st);
   return sha::launch_tc(a, head_dim, st);

@@ -25,11 +25,12 @@ struct Args {
   float* lse;
   int* errors;
   float* part;  // workspace
+  int entry;    // (bf16) what a unit costs besides its tiles
 };
 
 // The bf16 kernels (shared_attn_tc.cu).
 int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd, int pcap, int cap);
-int launch_tc(const Args& a, int hd, cudaStream_t st);
+int launch_tc(Args a, int hd, cudaStream_t st);
 
 // Slots of the prefix, or -1 where it does not fit.
 __device__ __forceinline__ int prefix_of(const Args& a) {

@@ -4,7 +4,7 @@
 // Units.  A kv head's rows of the whole batch meet the prefix in tiles of 128 rows, two tiles at a
 // time where there are two (a pair: both use the same key and value tiles); a request's rows meet
 // its own slots alone.  A unit is such rows x all of their slots, in tiles of 128 slots.  The tiles
-// of all units, a pair's counted twice, and ENTRY more for each unit, are dealt to the 152 CTAs in
+// of all units, a pair's counted twice, and some more for each unit, are dealt to the 152 CTAs in
 // equal shares: a CTA's share is a piece of one unit, some whole ones and a piece of another.  Each
 // piece leaves its sums in the workspace, in a place of its unit (the piece with the first tile) or
 // of its CTA (a continued unit, one a CTA at most), and the join adds them up.
@@ -39,11 +39,10 @@ namespace {
 
 constexpr int TT = 128;      // slots a tile, rows a tile
 constexpr int CTAS = 152;
-constexpr int ENTRY = 4;     // what a unit costs besides its tiles, in tiles
 constexpr int MIN_SHARE = 4; // (of at least 2: a share between two others then has a tile of a pair)
 constexpr int LOAD_WARP = 8, MMA_WARP = 9, THREADS = 352;  // (a warp of products for each group)
 constexpr float LOG2E = 1.44269504f;
-constexpr float LAZY = 8.f;
+constexpr float LAZY = 8.f, FAR = 32.f;  // log2
 
 template <int HD>
 struct Smem {
@@ -96,20 +95,20 @@ __device__ __forceinline__ Costs costs_of(const Args& a, int prefix) {
   c.tiles = cdiv(prefix, TT);
   const int rows = cdiv(a.batch * a.K, draft_rows(a.G));
   c.pairs = rows / 2;
-  c.pair = c.tiles ? 2 * c.tiles + ENTRY : 0;
-  c.single = c.tiles && (rows & 1) ? c.tiles + ENTRY : 0;
+  c.pair = c.tiles ? 2 * c.tiles + a.entry : 0;
+  c.single = c.tiles && (rows & 1) ? c.tiles + a.entry : 0;
   c.head = c.pairs * c.pair + c.single;
   c.prefix = c.head * a.nkv;
   return c;
 }
 __device__ __forceinline__ int own_cost(const Args& a, int b) {
   const int n = slots_of(a, b);
-  return n > 0 ? cdiv(n, TT) + ENTRY : 0;
+  return n > 0 ? cdiv(n, TT) + a.entry : 0;
 }
 
-// Tiles of a unit that begins at `start` (in cost) with `step` a tile, from cost `at` on.
+// Tiles of a unit whose first is at `start` (in cost), `step` each, before cost `at`.
 __device__ __forceinline__ int tile_from(int at, int start, int step, int tiles) {
-  const int d = at - start - ENTRY;
+  const int d = at - start;
   if (d <= 0) return 0;
   return min(step == 2 ? (d + 1) >> 1 : d, tiles);
 }
@@ -176,14 +175,14 @@ __device__ __forceinline__ bool next_unit(const Args& a, const Costs& c, const L
       step = 1;
       x.place = l.own + ((int64_t)w.b * a.nkv + w.h) * 2 * a.K * a.G;
       x.stride = a.K * a.G;
-      w.start += tiles ? tiles + ENTRY : 0;
+      w.start += tiles ? tiles + a.entry : 0;
       if (++w.h == a.nkv) {
         w.h = 0;
         ++w.b;
       }
     }
-    x.t0 = tile_from(w.begin, start, step, tiles);
-    x.t1 = tile_from(w.end, start, step, tiles);
+    x.t0 = tile_from(w.begin, start + a.entry, step, tiles);
+    x.t1 = tile_from(w.end, start + a.entry, step, tiles);
     if (x.t0 < x.t1) return true;
   }
   return false;
@@ -577,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool live = (r & ~31) < rows;   // any row of the warp
       const int all = x.b < 0 ? x.slots : limit_of(a, x.slots, 0);  // slots that every row sees
       const int limit = x.b < 0 ? x.slots : limit_of(a, x.slots, min(r / a.G, a.K - 1));
-      float m = -INFINITY, sum = 0.f;
+      float m = -INFINITY, raise = -INFINITY, sum = 0.f, before;
       for (int i = 0; i < count; ++i) {
         const int t = x.pair ? i : 2 * i + w, slot0 = (x.t0 + t) * TT;
         on = __all_sync(0xffffffffu, wait(&bar.s[w], ns++ & 1));
@@ -590,10 +589,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const bool edge = slot0 + TT > all;
         const int seen = limit - slot0;
-        float scale = 1.f;
-        // The row comes in four parts, the next one on its way while one is used; twice, for the maximum and
-        // for the weights: 64 registers, and code that stays in the instruction cache (a row of 128
-        // registers, unrolled, took a third longer).
+        // The row comes in four parts, the next one on its way while one is used: 64 registers, and code that
+        // stays in the instruction cache (a row of 128 registers, unrolled, took a third longer).
         const auto parts = [&](auto use, auto last) {
           float u[32], v[32];
           tc::tmem_ld32(tS, u);
@@ -606,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (c == 0)
               tc::tmem_ld32(tS + 64, u);
             else
-              last();
+              last(v);
             use(v, c + 32);
             ld_wait(u);
           }
@@ -618,33 +615,21 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (c + k >= seen) u[k] = -INFINITY;
           }
         };
-        if (live) {
-          float top = -INFINITY;
-          parts(
-              [&](float (&u)[32], int c) {
-                mask(u, c);
-                float t0 = fmaxf(u[0], u[1]), t1 = fmaxf(u[2], u[3]);
+        const auto largest = [](const float (&u)[32], float top) {
+          float t0 = fmaxf(u[0], u[1]), t1 = fmaxf(u[2], u[3]);
 #pragma unroll
-                for (int k = 4; k < 32; k += 4) {
-                  t0 = fmaxf(fmaxf(t0, u[k]), u[k + 1]);
-                  t1 = fmaxf(fmaxf(t1, u[k + 2]), u[k + 3]);
-                }
-                top = fmaxf(fmaxf(top, t0), t1);
-              },
-              [] {});
-          const float mx = top * qs;
-          if (mx > m + LAZY || (m == -INFINITY && mx > -INFINITY)) {
-            scale = m == -INFINITY ? 0.f : ex2(m - mx);
-            m = mx;
+          for (int k = 4; k < 32; k += 4) {
+            t0 = fmaxf(fmaxf(t0, u[k]), u[k + 1]);
+            t1 = fmaxf(fmaxf(t1, u[k + 2]), u[k + 3]);
           }
+          return fmaxf(fmaxf(top, t0), t1);
+        };
+        // O and the sum at reference `to` (the whole warp, each lane with its own)
+        const auto move = [&](float to) {
+          const float scale = to > m && m > -INFINITY ? ex2(m - to) : 1.f;
+          m = fmaxf(m, to);
           sum *= scale;
-        }
-        if (i > 0) {  // the last product has been added up
-          on = __all_sync(0xffffffffu, wait(&bar.pv[w], npv++ & 1));
-          if (!on) break;
-          tc::fence_after_sync();
-        }
-        if (live) {
+          before *= scale;
           if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
 #pragma unroll 1
             for (int k = 0; k < HD; k += 16) {
@@ -656,29 +641,69 @@ __global__ void __launch_bounds__(THREADS, 1)
               tmem_st16(tO + k, o);
             }
           }
-          const float ref = m == -INFINITY ? 0.f : -m;
-          parts(
-              [&](float (&u)[32], int c) {
-                mask(u, c);
-                float a0 = 0.f, a1 = 0.f, packed[16];
+        };
+        if (i > 0) {  // the last product has been added up
+          on = __all_sync(0xffffffffu, wait(&bar.pv[w], npv++ & 1));
+          if (!on) break;
+          tc::fence_after_sync();
+        }
+        if (live) {
+          // The weights are taken at the reference that the tiles before have left, and the maximum with them: a
+          // reference that is too low by less than 2^FAR costs no bit (bf16 and fp32 reach 2^127), and moves
+          // behind the tile.  Only a unit's first tile, one that passes 2^FAR, and the form without a tile
+          // ahead (its weights lie over the scores) look for the maximum first.
+          before = sum;
+          bool look = i == 0 || !AHEAD;
+          if (!look) move(raise);
+          while (true) {
+            float top = -INFINITY;
+            if (look) {
+              parts(
+                  [&](float (&u)[32], int c) {
+                    mask(u, c);
+                    top = largest(u, top);
+                  },
+                  [](float (&)[32]) {});
+              top *= qs;
+              move(top > m + LAZY || m == -INFINITY ? top : m);
+              sum = before;
+              top = -INFINITY;
+            }
+            const float ref = m == -INFINITY ? 0.f : -m;
+            bool again = false;
+            parts(
+                [&](float (&u)[32], int c) {
+                  mask(u, c);
+                  if (AHEAD) top = largest(u, top);
+                  float a0 = 0.f, a1 = 0.f, packed[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                  const float p0 = ex2(fmaf(u[k], qs, ref)), p1 = ex2(fmaf(u[k + 1], qs, ref));
-                  const float p2 = ex2(fmaf(u[k + 2], qs, ref)), p3 = ex2(fmaf(u[k + 3], qs, ref));
-                  a0 += p0 + p1;
-                  a1 += p2 + p3;
-                  packed[k / 2] = __uint_as_float(pack2(p0, p1));
-                  packed[k / 2 + 1] = __uint_as_float(pack2(p2, p3));
-                }
-                sum += a0 + a1;
-                tmem_st16(tP + c / 2, packed);
-              },
-              [&] {
-                if (AHEAD) {
+                  for (int k = 0; k < 32; k += 4) {
+                    const float p0 = ex2(fmaf(u[k], qs, ref)), p1 = ex2(fmaf(u[k + 1], qs, ref));
+                    const float p2 = ex2(fmaf(u[k + 2], qs, ref)), p3 = ex2(fmaf(u[k + 3], qs, ref));
+                    a0 += p0 + p1;
+                    a1 += p2 + p3;
+                    packed[k / 2] = __uint_as_float(pack2(p0, p1));
+                    packed[k / 2 + 1] = __uint_as_float(pack2(p2, p3));
+                  }
+                  sum += a0 + a1;
+                  tmem_st16(tP + c / 2, packed);
+                },
+                [&](float (&v)[32]) {
+                  if (!AHEAD) return;
+                  if (!look) {
+                    mask(v, 96);
+                    const float t = largest(v, top) * qs;
+                    again = __any_sync(0xffffffffu, t > m + FAR || (m == -INFINITY && t > -INFINITY));
+                  }
                   tc::fence_before_sync();
-                  if (i + 1 < count) tc::mbar_arrive(&bar.read[w]);
-                }
-              });
+                  if (!again && i + 1 < count) tc::mbar_arrive(&bar.read[w]);
+                });
+            if (!again) {
+              raise = top * qs > m + LAZY ? top * qs : m;
+              break;
+            }
+            look = true;
+          }
           tc::tmem_st_wait();
         } else if (AHEAD && i + 1 < count) {
           tc::mbar_arrive(&bar.read[w]);
@@ -789,18 +814,19 @@ __global__ void __launch_bounds__(256) shared_join_kernel(Args a, Layout l) {
   const float* sums = reinterpret_cast<const float*>(stat + l.rows);
   // A unit's pieces: of each CTA that has one, and of both groups where they share the rows.
   struct Span {
-    int start, tiles, first, pieces, w, stride;
+    int start, tiles, first, pieces, w, stride;  // (start: of its first tile)
     bool pair;
     int64_t place;  // the unit's own row slots
   };
   const auto span_of = [&](int start, int tiles, bool pair, int w, int64_t place, int stride) {
-    Span x = {start, tiles, (start + ENTRY) / share, 0, w, stride, pair, place};
-    const int last = (start + ENTRY + (tiles - 1) * (pair ? 2 : 1)) / share;
+    start += a.entry;
+    Span x = {start, tiles, start / share, 0, w, stride, pair, place};
+    const int last = (start + (tiles - 1) * (pair ? 2 : 1)) / share;
     if (tiles) x.pieces = (last - x.first + 1) * (pair ? 1 : 2);
     return x;
   };
   const int own_tiles = slots > 0 ? cdiv(slots, TT) : 0;
-  const Span own = span_of(own_tiles ? plan[1 + b] + h * (own_tiles + ENTRY) : 0, own_tiles, false, 0,
+  const Span own = span_of(own_tiles ? plan[1 + b] + h * (own_tiles + a.entry) : 0, own_tiles, false, 0,
                            l.own + ((int64_t)b * a.nkv + h) * 2 * rows, rows);
   Span shared = {};
   int tile = -1, pieces = 0;
@@ -920,13 +946,19 @@ int launch(const Args& a, cudaStream_t st) {
 int64_t tc_workspace(int64_t batch, int K, int G, int nkv, int hd, int pcap, int cap) {
   const int64_t tiles = (batch * K + draft_rows(G) - 1) / draft_rows(G);
   // the costs are counted in 32 bits
-  if (tiles * nkv * (pcap / TT + 1 + ENTRY) + batch * nkv * (cap / TT + 1 + ENTRY) >= 1 << 29)
+  if (tiles * nkv * (pcap / TT + 6) + batch * nkv * (cap / TT + 6) >= 1 << 29)
     return PEAGLE_ERR_UNSUPPORTED;
   const Layout l = layout_of(batch, K, G, nkv);
   return l.header + l.rows * (hd + 2) * 4;
 }
 
-int launch_tc(const Args& a, int hd, cudaStream_t st) { return hd == 64 ? launch<64>(a, st) : launch<128>(a, st); }
+int launch_tc(Args a, int hd, cudaStream_t st) {
+  // What a unit costs besides its tiles, in tiles (64 requests of 64 rows over 8192 slots and up to 1023 of
+  // their own, head_dim 64: 212, 200, 186, 200 us at 3, 4, 5, 6; 16 tokens over 131071, head_dim 128: 118,
+  // 123, 125, 131).
+  a.entry = hd == 64 ? 5 : 3;
+  return hd == 64 ? launch<64>(a, st) : launch<128>(a, st);
+}
 
 }  // namespace sha
 }  // namespace peagle
