@@ -24,7 +24,6 @@
 // Values that a row does not see never reach it: slots behind the last visible one are cleared in
 // shared memory before the product, and in the slots that only some rows see (a draft block) values
 // that are not finite are cleared and added to the rows that see them at the end.
-#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -796,8 +795,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the pieces of a request's rows and a kv head; a warp a row and head, several in turn.
-template <int HD>
+// Joins the pieces of a request's rows and a kv head.  A warp takes JOIN rows at a time, of one row tile, so
+// that their loads are in flight together; PARTS = 8: the eight warps of a CTA share out one row's pieces.
+template <int HD, int JOIN, int PARTS>
 __global__ void __launch_bounds__(256) shared_join_kernel(Args a, Layout l) {
   constexpr int DL = HD / 32;
   const int lane = threadIdx.x & 31, b = blockIdx.x, h = blockIdx.y, rows = a.K * a.G;
@@ -842,46 +842,122 @@ __global__ void __launch_bounds__(256) shared_join_kernel(Args a, Layout l) {
     if (!x.pair && n <= w) return -1;
     return k == x.first ? x.place + w * x.stride : l.cta + (int64_t)k * 2 * TT + w * TT;
   };
-  for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.z * 8) {
-    const int j = r / a.G, g = r - j * a.G, row = b * a.K + j, t = row / per;
-    if (t != tile) {
-      tile = t;
-      const int u = t / 2;
-      shared = span_of(h * c.head + u * c.pair, c.tiles, u < c.pairs, t & 1, (int64_t)(h * l.per + u) * 2 * TT, TT);
-      pieces = shared.pieces + own.pieces;
-      place = piece(lane);
-    }
-    const int in_tile = (row - t * per) * a.G + g;
-    float m = -INFINITY, total = 0.f, o[DL] = {};
-    for (int base = 0; base < pieces; base += 32) {
-      // a lane a piece: all of their statistics at once
-      int64_t at = base ? piece(base + lane) : place;
-      Stat mine = {-INFINITY, 0.f};
-      if (at >= 0) mine = stat[at += base + lane < shared.pieces ? in_tile : r];
-      const float top = fmaxf(m, warp_max(mine.m));
-      const float old = top == -INFINITY ? 1.f : exp2f(m - top);
-      const float weight = mine.l == 0.f ? 0.f : exp2f(mine.m - top);
-      total = total * old + warp_sum(mine.l == 0.f ? 0.f : mine.l * weight);
-#pragma unroll
-      for (int d = 0; d < DL; ++d) o[d] *= old;
-      const unsigned any = __ballot_sync(0xffffffffu, mine.l != 0.f);
-      const int end = 32 - __clz(any);
-#pragma unroll 4
-      for (int i = 0; i < end; ++i) {
-        const int64_t from = __shfl_sync(0xffffffffu, at, i);
-        const float y = __shfl_sync(0xffffffffu, weight, i);
-        if (!(any >> i & 1)) continue;
-#pragma unroll
-        for (int d = 0; d < DL; ++d) o[d] = fmaf(y, sums[from * HD + lane * DL + d], o[d]);
+  __shared__ float s_o[PARTS][HD], s_m[PARTS], s_l[PARTS];
+  const int warp = threadIdx.x >> 5, part = PARTS > 1 ? warp : 0;
+  for (int r0 = PARTS > 1 ? blockIdx.z : (blockIdx.z * 8 + warp) * JOIN; r0 < rows;
+       r0 += PARTS > 1 ? rows : gridDim.z * 8 * JOIN) {
+    for (int r = r0, some; r < min(r0 + JOIN, rows); r += some) {
+      const int first = b * rows + r, t = first / (per * a.G), in_tile = first - t * per * a.G;
+      some = min(min(r0 + JOIN, rows) - r, per * a.G - in_tile);
+      if (t != tile) {
+        tile = t;
+        const int u = t / 2;
+        shared = span_of(h * c.head + u * c.pair, c.tiles, u < c.pairs, t & 1, (int64_t)(h * l.per + u) * 2 * TT, TT);
+        pieces = shared.pieces + own.pieces;
+        place = piece(lane * PARTS + part);
       }
-      m = top;
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const size_t head = (size_t)row * a.nq + h * a.G + g;
-    bf16* out = static_cast<bf16*>(a.out) + head * HD + lane * DL;
+      float m[JOIN], total[JOIN], o[JOIN][DL];
 #pragma unroll
-    for (int d = 0; d < DL; d += 2) *reinterpret_cast<uint32_t*>(out + d) = pack2(o[d] * inv, o[d + 1] * inv);
-    if (a.lse && lane == 0) a.lse[head] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718f;
+      for (int k = 0; k < JOIN; ++k) {
+        m[k] = -INFINITY;
+        total[k] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[k][d] = 0.f;
+      }
+      for (int base = 0; base < pieces; base += 32 * PARTS) {
+        // a lane a piece: all of their statistics at once
+        const int mine_i = base + lane * PARTS + part;
+        int64_t at = base ? piece(mine_i) : place;
+        const bool has = at >= 0;
+        at = has ? at + (mine_i < shared.pieces ? in_tile : r) : 0;
+        Stat mine[JOIN];
+        float weight[JOIN];
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k) {
+          mine[k] = {-INFINITY, 0.f};
+          if (has && k < some) mine[k] = stat[at + k];
+        }
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k) {
+          const float top = fmaxf(m[k], warp_max(mine[k].m));
+          const float old = top == -INFINITY ? 1.f : exp2f(m[k] - top);
+          const bool any = mine[k].l != 0.f;
+          weight[k] = any ? exp2f(mine[k].m - top) : 0.f;
+          total[k] = total[k] * old + warp_sum(any ? mine[k].l * weight[k] : 0.f);
+          m[k] = top;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) o[k][d] *= old;
+        }
+        const unsigned all = __ballot_sync(0xffffffffu, has);
+        const int end = 32 - __clz(all);
+        constexpr int DEEP = 8 / JOIN;  // pieces whose loads go out together
+        for (int i0 = 0; i0 < end; i0 += DEEP) {
+          float x[DEEP][JOIN][DL];
+#pragma unroll
+          for (int i = 0; i < DEEP; ++i) {
+            const int64_t from = __shfl_sync(0xffffffffu, at, (i0 + i) & 31);
+            const bool is = i0 + i < end && (all >> ((i0 + i) & 31) & 1);
+            const float* v = sums + from * HD + lane * DL;
+#pragma unroll
+            for (int k = 0; k < JOIN; ++k) {
+              if (DL == 2) {
+                const float2 y = is && k < some ? *reinterpret_cast<const float2*>(v + k * HD) : make_float2(0.f, 0.f);
+                x[i][k][0] = y.x, x[i][k][1] = y.y;
+              } else {
+                const float4 y = is && k < some ? *reinterpret_cast<const float4*>(v + k * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[i][k][0] = y.x, x[i][k][1] = y.y, x[i][k][DL - 2] = y.z, x[i][k][DL - 1] = y.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+            for (int k = 0; k < JOIN; ++k) {
+              const float y = __shfl_sync(0xffffffffu, weight[k], (i0 + i) & 31);
+              const float n = __shfl_sync(0xffffffffu, mine[k].l, (i0 + i) & 31);
+#pragma unroll
+              for (int d = 0; d < DL; ++d) o[k][d] = i0 + i < end && n != 0.f ? fmaf(y, x[i][k][d], o[k][d]) : o[k][d];
+            }
+        }
+      }
+      if (PARTS > 1) {  // the warps' parts
+        if (lane == 0) {
+          s_m[part] = m[0];
+          s_l[part] = total[0];
+        }
+#pragma unroll
+        for (int d = 0; d < DL; ++d) s_o[part][lane * DL + d] = o[0][d];
+        __syncthreads();
+        if (warp) return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) top = fmaxf(top, s_m[i]);
+        m[0] = top;
+        total[0] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) o[0][d] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+          if (s_l[i] == 0.f) continue;
+          const float y = exp2f(s_m[i] - top);
+          total[0] += y * s_l[i];
+#pragma unroll
+          for (int d = 0; d < DL; ++d) o[0][d] = fmaf(y, s_o[i][lane * DL + d], o[0][d]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < JOIN; ++k) {
+        if (k >= some) continue;
+        const float inv = total[k] == 0.f ? 0.f : 1.f / total[k];
+        const int j = (r + k) / a.G;
+        const size_t head = (size_t)(b * a.K + j) * a.nq + h * a.G + (r + k - j * a.G);
+        bf16* out = static_cast<bf16*>(a.out) + head * HD + lane * DL;
+#pragma unroll
+        for (int d = 0; d < DL; d += 2)
+          *reinterpret_cast<uint32_t*>(out + d) = pack2(o[k][d] * inv, o[k][d + 1] * inv);
+        if (a.lse && lane == 0) a.lse[head] = total[k] == 0.f ? -INFINITY : (m[k] + log2f(total[k])) * 0.69314718f;
+      }
+    }
   }
 }
 
@@ -932,13 +1008,15 @@ int launch(const Args& a, cudaStream_t st) {
   const Layout l = layout_of(a.batch, a.K, a.G, a.nkv);
   shared_attn_kernel<HD><<<CTAS, THREADS, Smem<HD>::BYTES, st>>>(pk, pv, k, v, q, a, l, wait_limit.load(), unreachable.load());
   if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
-  // A warp takes one row where all of them fit the GPU at once, else several: it finds their pieces once.
-  const int64_t blocks = (int64_t)a.batch * a.nkv;
-  const int most = (a.K * a.G + 7) / 8;
-  const int z = (int)std::min<int64_t>(most, std::max<int64_t>(1, CTAS * 8 / blocks));
-  return launch_pdl(shared_join_kernel<HD>, dim3(a.batch, a.nkv, z), dim3(256), 0, st, a, l) == cudaSuccess
-             ? PEAGLE_OK
-             : PEAGLE_ERR_CUDA;
+  // The join: few rows have many pieces each.  (512 rows of 38 pieces: 9 us by CTAs, 26 by warps; 2048 of 17:
+  // 7 by warps, 17 by CTAs.)
+  const int rows = a.K * a.G;
+  const int64_t all = (int64_t)a.batch * a.nkv * rows;
+  const dim3 grid(a.batch, a.nkv, all <= CTAS * 4 ? rows : all <= CTAS * 16 ? (rows + 7) / 8 : (rows + 31) / 32);
+  const auto join = all <= CTAS * 4    ? shared_join_kernel<HD, 1, 8>
+                    : all <= CTAS * 16 ? shared_join_kernel<HD, 1, 1>
+                                       : shared_join_kernel<HD, 4, 1>;
+  return launch_pdl(join, grid, dim3(256), 0, st, a, l) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }
 
 }  // namespace
