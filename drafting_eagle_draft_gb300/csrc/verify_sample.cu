@@ -4,8 +4,8 @@
 // of those that keep at most LIST (sample.cu: the rows' one reading from memory).  In the second a
 // cluster takes a request: its drafts are accepted or not from K logits and records, and the bonus
 // token is drawn from r_i = max(p_i - q_i, 0) over the row of the first rejected one.  Where that row
-// has a list, the first CTA does it alone: it looks the draft row's kept tokens up in the list.
-// Else all of them walk the row, which is mostly still in the L2 cache.
+// has a list, the CTAs share out the draft row, look its tokens up in the list, and the first one draws.
+// Else all of them walk the target row, which is mostly still in the L2 cache.
 //
 // q lives in the draft vocabulary.  In the long form the cluster's CTAs share out the draft row, and write each kept
 // entry's index (plus 1) to its target token's place in the shared memory of the CTA that has that
@@ -84,27 +84,37 @@ __device__ __forceinline__ double prob64(float x, int i, const peagle_dist& d, i
   return cold ? 1.0 : any ? ratio64(raw, n, d.total) : 0.0;
 }
 
-// Calls f(d) for the entries of a draft row that q keeps.
+// The entries `done` .. n - 1 of a draft row with the ids that they stand for, four at a time: f(x, id, d).
+// A thread's loads go out together for DEEP fours.  (done: a multiple of 4)
 template <typename F>
-__device__ __forceinline__ void kept_entries(const float* draft, int n, const Probs& q, F f) {
-  const auto one = [&](float x, int d) {
-    if (kept(order_key(x), d, q.least, q.last)) f(d);
-  };
-  if ((uintptr_t)draft % 16 == 0) {
+__device__ __forceinline__ void draft_entries(const float* draft, const int* d2t, int done, int n, F f) {
+  constexpr int DEEP = 4;
+  if (((uintptr_t)draft | (uintptr_t)d2t) % 16 == 0) {
     const float4* v = reinterpret_cast<const float4*>(draft);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n / 4; i += THREADS) {
-      const float4 x = v[i];
-      one(x.x, 4 * i);
-      one(x.y, 4 * i + 1);
-      one(x.z, 4 * i + 2);
-      one(x.w, 4 * i + 3);
+    const int4* o = reinterpret_cast<const int4*>(d2t);
+    const int first = done / 4;
+    done = max(done, n & ~3);
+    for (int i0 = first + threadIdx.x; i0 < n / 4; i0 += DEEP * THREADS) {
+      float4 x[DEEP];
+      int4 t[DEEP];
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k) {
+        const int i = min(i0 + k * THREADS, n / 4 - 1);
+        x[k] = v[i];
+        t[k] = d2t ? o[i] : make_int4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k) {
+        const int d = 4 * (i0 + k * THREADS);
+        if (d >= done) break;
+        f(x[k].x, d + t[k].x, d);
+        f(x[k].y, d + 1 + t[k].y, d + 1);
+        f(x[k].z, d + 2 + t[k].z, d + 2);
+        f(x[k].w, d + 3 + t[k].w, d + 3);
+      }
     }
-    if (threadIdx.x < (n & 3)) one(draft[(n & ~3) + threadIdx.x], (n & ~3) + threadIdx.x);
-  } else {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += THREADS) one(draft[i], i);
   }
+  for (int d = done + threadIdx.x; d < n; d += THREADS) f(draft[d], d + (d2t ? d2t[d] : 0), d);
 }
 
 template <typename T>
@@ -117,6 +127,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   __shared__ Probs probs[2];      // p and q
   __shared__ int tokens[LIST];    // of a list
   __shared__ uint32_t match[LIST];  // the draft entry of each, plus 1
+  __shared__ uint32_t bits[LIST];   // of the ids in the list, by their lowest 14 bits
   tc::pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
@@ -198,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
   const int64_t target_row = (int64_t)b * (a.K + 1) + m;
   const int listed = a.list.count ? a.list.count[target_row] : -1;
   if (listed >= 0) {
-    if (rank) return;
+    if (rank && !with_q) return;
     const bool in = tid < listed;
     const int mine = in ? a.list.index[target_row * LIST + tid] : 0x7fffffff;
     const u64 pi = in ? __umul64hi(a.list.weight[target_row * LIST + tid] << pp.up, pp.inv) : 0;
@@ -206,16 +217,26 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(Args a) {
     if (with_q) {
       tokens[tid] = mine;
       match[tid] = 0;
+      bits[tid] = 0;
       __syncthreads();
-      kept_entries(draft, a.draft_vocab, qq, [&](int d) {
-        const int t = d + (a.d2t ? a.d2t[d] : 0);
+      if (in) atomicOr(&bits[mine / 32 % LIST], 1u << mine % 32);
+      __syncthreads();
+      cluster_barrier();  // (the first CTA's matches are clear)
+      // An id is looked for in the list only if its bit of 16384 is set: one in thirty that is not there.
+      // The cluster shares the row out; the matches go to its first CTA.
+      const int from_d = rank * a.draft_chunk, end_d = min(a.draft_vocab, from_d + a.draft_chunk);
+      draft_entries(draft, a.d2t, from_d, end_d, [&](float x, int t, int d) {
+        if (!(bits[t / 32 & (LIST - 1)] >> (t & 31) & 1)) return;
+        if (!kept(order_key(x), d, qq.least, qq.last)) return;
         int lo = 0;
-#pragma unroll
+#pragma unroll 1
         for (int step = LIST / 2; step > 0; step /= 2)
           if (tokens[lo + step] <= t) lo += step;
-        if (tokens[lo] == t && lo < listed) match[lo] = d + 1;
+        if (tokens[lo] == t && lo < listed) remote_store(&match[lo], 0, d + 1);
       });
       __syncthreads();
+      cluster_barrier();
+      if (rank) return;
       const uint32_t d = match[tid];
       const float x[1] = {d ? draft[d - 1] : 0.f};
       const int at[1] = {(int)d - 1};
@@ -386,7 +407,7 @@ extern "C" int peagle_verify_sample(int32_t batch, int32_t K, const int32_t* dra
   a.vocab = vocab;
   a.draft_vocab = draft_logits ? draft_vocab : 1;
   a.chunk = cdiv(vocab, ctas);
-  a.draft_chunk = cdiv(a.draft_vocab, ctas);
+  a.draft_chunk = cdiv(cdiv(a.draft_vocab, ctas), 4) * 4;
   a.tokens = draft_tokens;
   a.target = target_logits;
   a.stride = target_stride ? target_stride : vocab;
