@@ -31,7 +31,7 @@ constexpr float LOWEST = -3.402823466e38f;
 struct Args {
   const void* logits;
   int64_t stride;
-  int vocab, chunk;  // chunk: logits a CTA
+  int rows, vocab, chunk;  // chunk: logits a CTA
   const float* temperature;
   const int* top_k;
   const float* top_p;
@@ -73,6 +73,8 @@ struct Shared {
   uint32_t floor;        // order key below which this CTA's list leaves tokens out
   int n;                 // of the row's list; -1: too many
   int bin0, bin1;        // where the border lies
+  uint32_t lowest, highest;  // keys of the threads' largest; of a list
+  uint32_t left;         // (rows passed by) this CTA's row is not finished
 };
 
 template <typename T>
@@ -81,6 +83,9 @@ struct Row {
   int n, base;
 };
 
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -152,11 +157,11 @@ __device__ __forceinline__ void await_copies(const Copies<T>& c, float& top) {
   }
 }
 
-// Calls f(x, place) for the logits at least `floor` of a chunk that these copies brought.
+// Calls f(x, place) for the logits at least `floor` of a chunk.
 template <typename T, typename F>
 __device__ __forceinline__ void above(const T* chunk, int n, float floor, F f) {
   constexpr int PER = 16 / sizeof(T);
-  const int tid = threadIdx.x, phase = (int)((tc::smem_u32(chunk) & 15) / sizeof(T));
+  const int tid = threadIdx.x, phase = (int)(((uintptr_t)chunk & 15) / sizeof(T));
   const int head = min(n, phase ? PER - phase : 0), vecs = (n - head) / PER, tail = n - head - vecs * PER;
   const auto one = [&](int i) {
     const float x = to_f32(chunk[i]);
@@ -225,6 +230,38 @@ __device__ __forceinline__ void find_bin(Shared& sh, uint32_t n, u64 w, bool by_
 
 // Keys low .. high in BINS parts: the width of one, as a shift.
 __device__ __forceinline__ int key_shift(uint32_t low, uint32_t high) { return max(0, 32 - __clz(high - low) - 9); }
+// The largest border that leaves k of the cluster's keys (PER a thread; 0: none) at it or above, but for an
+// eighth of k more; the lowest finite key if there are fewer.  All keys are low .. high.  By the order alone: one
+// logit far above the others would push those out of any bins that are laid over the weights.
+template <int PER>
+__device__ uint32_t border_key(Shared& sh, int ctas, const uint32_t (&key)[PER], uint32_t low, uint32_t high,
+                               uint32_t k) {
+  const int tid = threadIdx.x;
+  uint32_t before = 0;
+  while (low <= high) {
+    const int shift = key_shift(low, high);
+    __syncthreads();
+    if (ctas > 1) cluster_barrier();  // (the bins are read no more)
+    sh.hist[tid].x = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] && key[i] >= low && key[i] <= high) atomicAdd(&sh.hist[(high - key[i]) >> shift].x, 1u);
+    __syncthreads();
+    if (ctas > 1) cluster_barrier();
+    uint32_t n = 0;
+    for (int c = 0; c < ctas; ++c) n += ctas > 1 ? remote_u32(&sh.hist[tid].x, c) : sh.hist[tid].x;
+    find_bin(sh, n, 0, true, k - before, 0);
+    if (before + sh.before_n + sh.in_n < k) break;
+    before += sh.before_n;
+    high -= (uint32_t)sh.bin << shift;
+    const uint32_t width = (1u << shift) - 1;
+    if (high - low > width) low = high - width;
+    if (shift == 0 || before + sh.in_n <= k + k / 8 + 8) return low;
+  }
+  return order_key(LOWEST);
+}
+
 // The keys that the bins from bin0 to bin1 can hold.
 __device__ __forceinline__ uint32_t lowest_key(const Scale& s, int bin1) {
   return bin1 == BINS - 1 ? 0u : order_key(below(s, -(bin1 + 1) * 0.125f));
@@ -262,39 +299,39 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
     const int shift = key_shift(low, high);
     if (!listed && low == high) break;  // equal logits
     if (!filled) {
-    __syncthreads();
-    cluster_barrier();  // (the buffers below are read no more)
-    if (tid == 0) sh.count = 0;
-    if (!listed) sh.hist[tid] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for (int i = tid & ~31; i < row.n; i += 4 * THREADS) {
-      float x[4];
-      bool is[4], any = false;
+      __syncthreads();
+      cluster_barrier();  // (the buffers below are read no more)
+      if (tid == 0) sh.count = 0;
+      if (!listed) sh.hist[tid] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      for (int i = tid & ~31; i < row.n; i += 4 * THREADS) {
+        float x[4];
+        bool is[4], any = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int at = i + k * THREADS + (tid & 31);
-        x[k] = at < row.n ? to_f32(row.x[at]) : -INFINITY;
-        const uint32_t key = order_key(x[k]);
-        const int bin = bin_of(x[k], s);
-        any |= is[k] = at < row.n && bin >= bin0 && bin <= bin1 && key >= low && key <= high &&
-                       kept(key, row.base + at, old_least, old_last);
-      }
-      if (!__any_sync(0xffffffffu, any)) continue;
+        for (int k = 0; k < 4; ++k) {
+          const int at = i + k * THREADS + (tid & 31);
+          x[k] = at < row.n ? to_f32(row.x[at]) : -INFINITY;
+          const uint32_t key = order_key(x[k]);
+          const int bin = bin_of(x[k], s);
+          any |= is[k] = at < row.n && bin >= bin0 && bin <= bin1 && key >= low && key <= high &&
+                         kept(key, row.base + at, old_least, old_last);
+        }
+        if (!__any_sync(0xffffffffu, any)) continue;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (!__any_sync(0xffffffffu, is[k])) continue;
-        const u64 wx = !listed && weigh ? weight(x[k], s, tab) : 0;
-        if (!is[k]) continue;
-        const uint32_t key = order_key(x[k]);
-        if (listed)
-          sh.list[atomicAdd(&sh.count, 1u)] =
-              (u64)key << 32 | (0xffffffffu - (uint32_t)(row.base + i + k * THREADS + (tid & 31)));
-        else
-          add_bin(&sh.hist[(high - key) >> shift], wx, weigh);
+        for (int k = 0; k < 4; ++k) {
+          if (!__any_sync(0xffffffffu, is[k])) continue;
+          const u64 wx = !listed && weigh ? weight(x[k], s, tab) : 0;
+          if (!is[k]) continue;
+          const uint32_t key = order_key(x[k]);
+          if (listed)
+            sh.list[atomicAdd(&sh.count, 1u)] =
+                (u64)key << 32 | (0xffffffffu - (uint32_t)(row.base + i + k * THREADS + (tid & 31)));
+          else
+            add_bin(&sh.hist[(high - key) >> shift], wx, weigh);
+        }
       }
-    }
-    __syncthreads();
-    cluster_barrier();
+      __syncthreads();
+      cluster_barrier();
     }
     filled = false;
     if (listed) {
@@ -310,7 +347,7 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
       u64 mine = 0;
       if (weigh && tid < ((at + 31) & ~31)) {
         const uint32_t key = (uint32_t)(me >> 32);
-        mine = weight(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab);
+        mine = weight(key_logit(key), s, tab);
         if (tid < at) sh.weight[tid] = mine;
       }
       __syncthreads();
@@ -342,7 +379,7 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
     in_n = sh.in_n;
   }
   // in_n > RANK equal logits: so many of them, the lowest indices first
-  const float x = __uint_as_float(low & 0x80000000u ? low & 0x7fffffffu : ~low);
+  const float x = key_logit(low);
   const u64 each = weigh ? weight(x, s, tab) : 0;
   uint32_t m;
   if (by_count) {
@@ -417,7 +454,7 @@ __device__ __forceinline__ void finish(Shared& sh, uint2* raws, const Args& a, i
   u64 w = 0, raw = 0;
   int down = 63;
   if ((tid & ~31) < n) {
-    if (!weight_raw(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key), s, tab, raw, down)) down = 63;
+    if (!weight_raw(key_logit(key), s, tab, raw, down)) down = 63;
     w = down > 62 ? 0 : (raw + (1ull << (down - 1))) >> down;
   }
   raws[tid] = make_uint2((uint32_t)(raw >> 31), (uint32_t)down);  // 32 bits of a weight
@@ -503,84 +540,253 @@ __device__ __forceinline__ void border_bins(Shared& sh, uint32_t n, float want, 
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
-  extern __shared__ uint4 dynamic[];
-  __shared__ Shared sh;
-  tc::pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank();
-  const int r = blockIdx.x / ctas, set = r / a.rows_per;
-  const int frac = frac_bits(a.vocab);
-
-  const float temperature = a.temperature ? a.temperature[set] : 1.f;
-  const int top_k = a.top_k ? a.top_k[set] : 0;
-  const float top_p = a.top_p ? a.top_p[set] : 1.f;
-  const float min_p = a.min_p ? a.min_p[set] : 0.f;
-
-  Row<T> row;
-  row.base = rank * a.chunk;
-  row.n = max(0, min(a.chunk, a.vocab - row.base));
-  const T* src = static_cast<const T*>(a.logits) + (int64_t)r * a.stride + row.base;
-  T* chunk = reinterpret_cast<T*>(reinterpret_cast<char*>(dynamic) + ((uintptr_t)src & 15));
-  row.x = chunk;
-  float top = -INFINITY;
-  const Copies<T> copies = start_copies(src, chunk, row.n, top);
-  if (tid == THREADS - 32 && temperature > 0.f) {
-    split(1.4426950408889634074 / (double)temperature, sh.ch, sh.cl);
-    if (min_p > 0.f) split((double)temperature * log((double)fminf(min_p, 1.f)), sh.th, sh.tl);
+// The threads' largest logits (NaN if one is): the CTA's, in sh.top, and the lowest of them, in sh.lowest.
+__device__ __forceinline__ void join_tops(Shared& sh, float top) {
+  const uint32_t key = top == top ? order_key(top) : 0xffffffffu;
+  const uint32_t high = __reduce_max_sync(0xffffffffu, key);
+  const uint32_t low = __reduce_min_sync(0xffffffffu, top > -INFINITY ? key : 0xffffffffu);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&sh.top, high);
+    atomicMin(&sh.lowest, low);
   }
-  await_copies(copies, top);
-  const float mine = top;  // this thread's own
-  uint32_t key = top == top ? order_key(top) : 0xffffffffu;
-  key = __reduce_max_sync(0xffffffffu, key);
+  __syncthreads();
+}
+// After it: the border that k threads' largest logits reach.
+__device__ __forceinline__ uint32_t thread_border(Shared& sh, float top, int k) {
+  const uint32_t key[1] = {top > -INFINITY ? order_key(top) : 0u};
+  return border_key(sh, 1, key, sh.lowest, sh.top, (uint32_t)k);
+}
+
+// ---- many rows: a CTA a row, which passes by once ---------------------------------------
+// The row is not kept: a thread's 16-byte pieces come through a ring of its own, STREAM deep.  With top-k the
+// first STREAM pieces' maxima give a border, the tokens above it are listed as they pass, and the border rises
+// with the list: the list's k-th token is one of the row's first k or above them.
+constexpr int STREAM = 8, STREAM_LIST = 2048, STREAM_FULL = 768, ALONE_K = THREADS * 7 / 8;
+constexpr size_t STREAM_BYTES = STREAM * THREADS * 16 + STREAM_LIST * 8;
+
+// Raises the border to the list's k-th token or little below it, and drops what is below; its size in sh.count.
+__device__ __forceinline__ float raise_border(Shared& sh, u64* list, int k, float floor) {
+  const int tid = threadIdx.x;
+  constexpr int PER = STREAM_LIST / THREADS;
+  __syncthreads();
+  const int n = (int)sh.count;
+  u64 mine[PER];
+  uint32_t key[PER], top = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    mine[i] = tid + i * THREADS < n ? list[tid + i * THREADS] : 0;
+    key[i] = (uint32_t)(mine[i] >> 32);
+    top = max(top, key[i]);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
   if (tid == 0) {
+    sh.highest = 0;
+    sh.count = 0;
+  }
+  __syncthreads();
+  if ((tid & 31) == 0) atomicMax(&sh.highest, top);
+  __syncthreads();
+  floor = fmaxf(floor, key_logit(border_key(sh, 1, key, order_key(floor), sh.highest, (uint32_t)k)));
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (mine[i] && key_logit(key[i]) >= floor) list[atomicAdd(&sh.count, 1u)] = mine[i];
+  __syncthreads();
+  return floor;
+}
+
+// Passes over a row: the thread's largest logit (NaN if one is), and, where k > 0, the list (its size in
+// sh.count, STREAM_LIST + 1 and more: it was not enough).
+template <typename T>
+__device__ __forceinline__ void pass_by(Shared& sh, uint4* ring, const T* src, int n, int k, float& top) {
+  constexpr int PER = 16 / sizeof(T);
+  const int tid = threadIdx.x;
+  u64* list = reinterpret_cast<u64*>(ring + STREAM * THREADS);
+  const int phase = (int)(((uintptr_t)src & 15) / sizeof(T));
+  const int head = min(n, phase ? PER - phase : 0), vecs = (n - head) / PER, tail = n - head - vecs * PER;
+  const T* s = src + head;
+  const auto ask = [&](int i) {
+    const int v = tid + i * THREADS;
+    if (v < vecs)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(ring + i % STREAM * THREADS + tid)),
+                   "l"(s + (int64_t)v * PER)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < STREAM; ++i) ask(i);
+  const int at = tid < head ? tid : tid >= 32 && tid - 32 < tail ? head + vecs * PER + tid - 32 : -1;
+  const float edge = at >= 0 ? to_f32(src[at]) : -INFINITY;
+  top = max_nan(top, edge);
+  float floor = LOWEST;
+  const auto add = [&](float x, int i) {
+    const uint32_t at = atomicAdd(&sh.count, 1u);
+    if (at < STREAM_LIST) list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)i);
+  };
+  if (k) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    float mine = edge;
+#pragma unroll
+    for (int i = 0; i < STREAM; ++i)
+      if (tid + i * THREADS < vecs) mine = top_of(ring[i * THREADS + tid], mine, T());
+    join_tops(sh, mine);
+    floor = key_logit(thread_border(sh, mine, k));
+    if (edge >= floor) add(edge, at);
+  }
+  const int turns = (vecs + THREADS - 1) / THREADS;
+  for (int i = 0; i < turns; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STREAM - 1) : "memory");
+    const int v = tid + i * THREADS;
+    if (v < vecs) {
+      const uint4 y = ring[i % STREAM * THREADS + tid];
+      const float most = top_of(y, -INFINITY, T());
+      top = max_nan(top, most);
+      if (k && most >= floor) {
+        const uint32_t word[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const float x = sizeof(T) == 4 ? __uint_as_float(word[j % 4])
+                                         : __uint_as_float(j & 1 ? word[j / 2 % 4] & 0xffff0000u : word[j / 2 % 4] << 16);
+          if (x >= floor) add(x, head + v * PER + j);
+        }
+      }
+    }
+    ask(i + STREAM);
+    if (k && i % STREAM == STREAM - 1) {
+      if (__syncthreads_or(*(volatile uint32_t*)&sh.count > STREAM_FULL)) {
+        if (sh.count > STREAM_LIST) {
+          k = 0;  // (the same everywhere)
+        } else {
+          floor = raise_border(sh, list, k, floor);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if (k && sh.count > LIST && sh.count <= STREAM_LIST) raise_border(sh, list, k, floor);
+}
+
+struct Set {
+  float temperature, top_p, min_p;
+  int top_k;
+};
+__device__ __forceinline__ Set settings(const Args& a, int r) {
+  const int set = r / a.rows_per;
+  return {a.temperature ? a.temperature[set] : 1.f, a.top_p ? a.top_p[set] : 1.f, a.min_p ? a.min_p[set] : 0.f,
+          a.top_k ? a.top_k[set] : 0};
+}
+__device__ __forceinline__ void reset(Shared& sh) {
+  if (threadIdx.x == 0) {
     sh.top = 0;
+    sh.lowest = 0xffffffffu;
     sh.sum = 0;
     sh.count = 0;
     sh.first = 0xffffffffu;
     sh.least = 0;
     sh.last = 0x7fffffff;
   }
-  sh.hist[tid] = make_uint4(0, 0, 0, 0);
+  sh.hist[threadIdx.x] = make_uint4(0, 0, 0, 0);
+}
+// The settings' numbers that need 64 bits (by one thread, while the row is on its way).
+__device__ __forceinline__ void scalars(Shared& sh, const Set& set) {
+  if (threadIdx.x == THREADS - 32 && set.temperature > 0.f) {
+    split(1.4426950408889634074 / (double)set.temperature, sh.ch, sh.cl);
+    if (set.min_p > 0.f) split((double)set.temperature * log((double)fminf(set.min_p, 1.f)), sh.th, sh.tl);
+  }
+}
+// The smallest fp32 number that is at least M + T ln(min_p), as a key.
+__device__ __forceinline__ uint32_t least_of(const Shared& sh, float top, float min_p) {
+  if (!(min_p > 0.f)) return 0;
+  const float x = top + sh.th, back = x - top;
+  const float rest = ((top - (x - back)) + (sh.th - back)) + sh.tl;
+  return order_key(rest > 0.f ? fminf(nextafterf(x, INFINITY), top) : x);
+}
+__device__ __forceinline__ bool has_distribution(float top, float temperature) {  // (top: NaN if any is)
+  return top > -INFINITY && top < INFINITY && temperature >= 0.f;
+}
+__device__ __forceinline__ void refuse(const Args& a, int r, float temperature) {  // (one thread)
+  if (a.token) a.token[r] = -1;
+  if (a.prob) a.prob[r] = NAN;
+  if (a.dist) a.dist[r] = {0ull, NAN, temperature, 0xffffffffu, -1, -1, a.vocab};
+  if (a.list.count) a.list.count[r] = 0;
+  raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_BAD_ROW);
+}
+// A row with top-k by this CTA alone; false: the list was too short for it.
+template <typename T>
+__device__ __forceinline__ bool sample_alone(const Args& a, Shared& sh, uint4* dynamic, int r) {
+  const int tid = threadIdx.x;
+  const Set set = settings(a, r);
+  if (!(set.top_k > 0 && set.top_k < a.vocab && set.top_k <= ALONE_K && set.temperature >= COLD)) return false;
+  reset(sh);
+  scalars(sh, set);
   __syncthreads();
-  if (lane == 0) atomicMax(&sh.top, key);
-  __syncthreads();
+  float top = -INFINITY;
+  pass_by(sh, dynamic, static_cast<const T*>(a.logits) + (int64_t)r * a.stride, a.vocab, set.top_k, top);
+  join_tops(sh, top);
+  top = key_logit(sh.top);
+  if (!has_distribution(top, set.temperature)) {
+    if (tid == 0) refuse(a, r, set.temperature);
+    return true;
+  }
+  const int n = (int)min(sh.count, LIST + 1u);
+  if (n > LIST) return false;
+  const int frac = frac_bits(a.vocab);
+  const Scale s = {top, sh.ch, sh.cl, 62 - frac};
+  const u64* list = reinterpret_cast<const u64*>(dynamic + STREAM * THREADS);
+  if (tid < n) sh.all[tid] = list[tid];
+  finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, n, s, load_table(), top, set.temperature, frac, set.top_k,
+         set.top_p < 1.f, set.top_p, 0, true, least_of(sh, top, set.min_p));
+  return true;
+}
+
+// A row by the cluster.  LEAVE: its CTAs may end when they are done.
+template <typename T, bool LEAVE>
+__device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4* dynamic, int r, int ctas, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int frac = frac_bits(a.vocab);
+  const Set set = settings(a, r);
+  const float temperature = set.temperature, top_p = set.top_p;
+  const int top_k = set.top_k;
+
+  Row<T> row;
+  row.base = rank * a.chunk;
+  row.n = max(0, min(a.chunk, a.vocab - row.base));
+  const T* src = static_cast<const T*>(a.logits) + (int64_t)r * a.stride + row.base;
   const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
   const bool small = a.vocab <= LIST;
   // With top-k every CTA lists its chunk's first tokens before the row's largest is known: four standard
   // deviations and some more than its part of k, down to a border that as many threads' maxima reach.
   const int mine_k = ctas == 1 ? top_k : min(top_k, top_k / ctas + 4 * (int)sqrtf((float)top_k / ctas) + 8);
-  const bool list_k = by_k && !small && mine_k <= THREADS * 7 / 8 && temperature >= COLD;
+  const bool list_k = by_k && !small && top_k <= ALONE_K && temperature >= COLD;
+  reset(sh);
+  T* chunk = reinterpret_cast<T*>(reinterpret_cast<char*>(dynamic) + ((uintptr_t)src & 15));
+  float top = -INFINITY;
+  const Copies<T> copies = start_copies(src, chunk, row.n, top);
+  scalars(sh, set);
+  await_copies(copies, top);
+  row.x = chunk;
+  const float mine = top;  // this thread's own
+  join_tops(sh, top);
   if (list_k) {
-    const uint32_t k = sh.top;
-    const Scale own = {__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), sh.ch, sh.cl, 0};
-    if (mine > -INFINITY) atomicAdd(&sh.hist[bin_of(mine, own)].x, 1u);
-    __syncthreads();
-    find_bin(sh, sh.hist[tid].x, 0, true, (uint32_t)mine_k, 0);
     // (with fewer threads than mine_k that have a token at all: every token)
-    const float floor = sh.bin < BINS - 1 ? fmaxf(below(own, -(sh.bin + 1) * 0.125f), LOWEST) : LOWEST;
+    const uint32_t border = thread_border(sh, mine, mine_k);
+    const float floor = key_logit(border);
     above(chunk, row.n, floor, [&](float x, int i) {
       if (*(volatile uint32_t*)&sh.count > LIST) return;
       const uint32_t at = atomicAdd(&sh.count, 1u);
       if (at < LIST) sh.list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(row.base + i));
     });
-    if (tid == 0) sh.floor = order_key(floor);
+    if (tid == 0) sh.floor = border;
     __syncthreads();
   }
   cluster_barrier();
   uint32_t top_key = 0;
   for (int c = 0; c < ctas; ++c) top_key = max(top_key, remote_u32(&sh.top, c));
-  top = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
-  const bool whole = top > -INFINITY && top < INFINITY && temperature >= 0.f;  // (top: NaN if any is)
-  if (!whole) {  // no distribution
-    if (rank == 0 && tid == 0) {
-      if (a.token) a.token[r] = -1;
-      if (a.prob) a.prob[r] = NAN;
-      if (a.dist) a.dist[r] = {0ull, NAN, temperature, 0xffffffffu, -1, -1, a.vocab};
-      if (a.list.count) a.list.count[r] = 0;
-      raise_error(reinterpret_cast<unsigned*>(a.errors), PEAGLE_DEV_BAD_ROW);
-    }
+  top = key_logit(top_key);
+  if (!has_distribution(top, temperature)) {
+    if (rank == 0 && tid == 0) refuse(a, r, temperature);
     cluster_barrier();
     return;
   }
@@ -609,12 +815,7 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
 
   const Scale s = {top, sh.ch, sh.cl, 62 - frac};
   const Table tab = load_table();
-  uint32_t min_key = 0;
-  if (min_p > 0.f) {  // the smallest fp32 number that is at least M + T ln(min_p)
-    const float x = top + sh.th, back = x - top;
-    const float rest = ((top - (x - back)) + (sh.th - back)) + sh.tl;
-    min_key = order_key(rest > 0.f ? fminf(nextafterf(x, INFINITY), top) : x);
-  }
+  const uint32_t min_key = least_of(sh, top, set.min_p);
   bool certain = false;  // find.sums holds what lies before the border's bins
   if (by_k || by_p) {
     u64 mass = 0, w = 0, want = 0;
@@ -661,10 +862,21 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
       }
     }
     if (listed) {
-      // the row's first CTA collects the lists, with top-k as far down as all of them are whole
+      // the row's first CTA collects the lists, with top-k as far down as all of them are whole, and, where
+      // that may be too much, no further than the k-th token or little below it
+      if (list_k) {
+        uint32_t n = 0;
+        for (int c = 0; c < ctas; ++c) {
+          floor = max(floor, remote_u32(&sh.floor, c));
+          n += remote_u32(&sh.count, c);
+        }
+        if (n > LIST) {
+          const uint32_t key[1] = {tid < min(sh.count, (uint32_t)LIST) ? (uint32_t)(sh.list[tid] >> 32) : 0u};
+          floor = max(floor, border_key(sh, ctas, key, floor, top_key, (uint32_t)top_k));
+          cluster_barrier();
+        }
+      }
       if (rank == 0) {
-        if (list_k)
-          for (int c = 0; c < ctas; ++c) floor = max(floor, remote_u32(&sh.floor, c));
         if (tid == 0) sh.n = 0;
         __syncthreads();
         bool whole = true;
@@ -686,9 +898,9 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
         finish(sh, reinterpret_cast<uint2*>(dynamic), a, r, sh.n, s, tab, top, temperature, frac,
                by_k ? top_k : LIST, by_p, top_p, mass, by_k || small, min_key);
       cluster_wait();
-      if (!list_k && rank) return;  // (the first CTA's wait is for those that are still there)
+      if (LEAVE && !list_k && rank) return;  // (the first CTA's wait is for those that are still there)
       const int n = (int)remote_u32(reinterpret_cast<uint32_t*>(&sh.n), 0);
-      if (n >= 0 && rank) return;
+      if (LEAVE && n >= 0 && rank) return;
       cluster_barrier();
       if (n >= 0) return;
     }
@@ -832,22 +1044,60 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
   cluster_barrier();  // (the others read this CTA's sums)
 }
 
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 2) sample_kernel(Args a) {
+  extern __shared__ uint4 dynamic[];
+  __shared__ Shared sh;
+  tc::pdl_launch_dependents();
+  const int ctas = (int)cluster_size();
+  sample_together<T, true>(a, sh, dynamic, blockIdx.x / ctas, ctas, (int)tc::cluster_ctarank());
+}
+
+// As many rows at a time as the cluster has CTAs: each passes by one, then all of them take those that are
+// left.  (Rows in a line often have the same settings: a cluster's are far apart.)
+template <typename T>
+__global__ void __launch_bounds__(THREADS, 2) sample_many_kernel(Args a) {
+  extern __shared__ uint4 dynamic[];
+  __shared__ Shared sh;
+  tc::pdl_launch_dependents();
+  const int ctas = (int)cluster_size(), rank = (int)tc::cluster_ctarank(), clusters = gridDim.x / ctas;
+  for (int64_t first = blockIdx.x / ctas; first < a.rows; first += (int64_t)clusters * ctas) {
+    const int64_t r = first + (int64_t)rank * clusters;
+    const bool left = r < a.rows && !sample_alone<T>(a, sh, dynamic, (int)r);
+    if (threadIdx.x == 0) sh.left = left;
+    __syncthreads();
+    cluster_barrier();
+    uint32_t which = 0;
+    for (int c = 0; c < ctas; ++c) which |= remote_u32(&sh.left, c) << c;
+    for (; which; which &= which - 1) {
+      cluster_barrier();  // (the row before is read no more)
+      sample_together<T, false>(a, sh, dynamic, (int)first + (__ffs(which) - 1) * clusters, ctas, rank);
+    }
+    cluster_barrier();
+  }
+}
+
 // CTAs a row: as many as keep the GPU's 2 x 152 places busy once, but at least 2048 logits each, and
 // at most CHUNK bytes of them, so that two CTAs fit an SM.
 constexpr int CHUNK = 100 << 10, PLACES = 304;
 constexpr size_t ALONE = 112 << 10;
 
 template <typename T>
-int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
+int launch(const Args& a, int rows, int ctas, bool many, cudaStream_t st) {
   // (the row's place holds `finish`'s numbers at the end)
   size_t bytes = max((size_t)a.chunk * sizeof(T) + 32, LIST * sizeof(uint2));
   // Few rows: an SM for each CTA (a cluster's CTAs share SMs while others are idle), where all clusters fit
   // at once: 15 of 8 do, 36 of 4.  (16 rows of 201088: 131 us as two waves of 8, 105 sharing SMs.)
   const int most = ctas == 8 ? 15 : ctas == 4 ? 36 : PLACES / 2 / ctas;
-  if (rows <= most) bytes = max(bytes, ALONE);
-  if (smem_optin((const void*)sample_kernel<T>, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  if (many)
+    bytes = max(bytes, STREAM_BYTES);
+  else if (rows <= most)
+    bytes = max(bytes, ALONE);
+  const auto kernel = many ? sample_many_kernel<T> : sample_kernel<T>;
+  if (smem_optin((const void*)kernel, bytes) != cudaSuccess) return PEAGLE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * ctas);
+  // (many: as many clusters as fit at once)
+  cfg.gridDim = dim3((unsigned)(many && ctas > 1 ? min(rows, 2 * most) : rows) * ctas);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
@@ -857,7 +1107,7 @@ int launch(const Args& a, int rows, int ctas, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
 }
 
 int cluster_of(int rows, int vocab, int size) {
@@ -876,8 +1126,11 @@ int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* log
   Args a = {};
   const int size = dtype == PEAGLE_F32 ? 4 : 2;
   const int ctas = cluster_of(rows, vocab, size);
+  // Top-k, where not all rows run at once or a row has one CTA anyway.
+  const bool many = how && how->top_k && vocab > 8 * LIST && (ctas == 1 || (int64_t)rows * ctas > PLACES);
   a.logits = logits;
   a.stride = row_stride ? row_stride : vocab;
+  a.rows = rows;
   a.vocab = vocab;
   a.chunk = cdiv(cdiv(vocab, ctas), 8) * 8;
   if (how) {
@@ -894,7 +1147,7 @@ int sample_rows(const peagle_sampling* how, int rows, int vocab, const void* log
   a.dist = dist;
   if (list) a.list = *list;
   a.errors = errors;
-  return dtype == PEAGLE_F32 ? launch<float>(a, rows, ctas, st) : launch<bf16>(a, rows, ctas, st);
+  return dtype == PEAGLE_F32 ? launch<float>(a, rows, ctas, many, st) : launch<bf16>(a, rows, ctas, many, st);
 }
 
 // What both calls refuse of a block of logits.
