@@ -580,11 +580,9 @@ __device__ __forceinline__ float raise_border(Shared& sh, u64* list, int k, floa
     top = max(top, key[i]);
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  if (tid == 0) {
-    sh.highest = 0;
-    sh.count = 0;
-  }
+  if (tid == 0) sh.highest = 0;
   __syncthreads();
+  if (tid == 0) sh.count = 0;  // (every thread has read it)
   if ((tid & 31) == 0) atomicMax(&sh.highest, top);
   __syncthreads();
   floor = fmaxf(floor, key_logit(border_key(sh, 1, key, order_key(floor), sh.highest, (uint32_t)k)));
