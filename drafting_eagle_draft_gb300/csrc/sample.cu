@@ -603,24 +603,20 @@ __device__ __forceinline__ void pass_by(Shared& sh, uint4* ring, const T* src, i
   const int phase = (int)(((uintptr_t)src & 15) / sizeof(T));
   const int head = min(n, phase ? PER - phase : 0), vecs = (n - head) / PER, tail = n - head - vecs * PER;
   const T* s = src + head;
-  const auto ask = [&](int i) {
+  const auto ask = [&](int slot, int i) {
     const int v = tid + i * THREADS;
     if (v < vecs)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(ring + i % STREAM * THREADS + tid)),
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(ring + slot * THREADS + tid)),
                    "l"(s + (int64_t)v * PER)
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < STREAM; ++i) ask(i);
+  for (int i = 0; i < STREAM; ++i) ask(i, i);
   const int at = tid < head ? tid : tid >= 32 && tid - 32 < tail ? head + vecs * PER + tid - 32 : -1;
   const float edge = at >= 0 ? to_f32(src[at]) : -INFINITY;
   top = max_nan(top, edge);
   float floor = LOWEST;
-  const auto add = [&](float x, int i) {
-    const uint32_t at = atomicAdd(&sh.count, 1u);
-    if (at < STREAM_LIST) list[at] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)i);
-  };
   if (k) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     float mine = edge;
@@ -629,31 +625,43 @@ __device__ __forceinline__ void pass_by(Shared& sh, uint4* ring, const T* src, i
       if (tid + i * THREADS < vecs) mine = top_of(ring[i * THREADS + tid], mine, T());
     join_tops(sh, mine);
     floor = key_logit(thread_border(sh, mine, k));
-    if (edge >= floor) add(edge, at);
+    if (edge >= floor) list[atomicAdd(&sh.count, 1u)] = (u64)order_key(edge) << 32 | (0xffffffffu - (uint32_t)at);
   }
   const int turns = (vecs + THREADS - 1) / THREADS;
-  for (int i = 0; i < turns; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(STREAM - 1) : "memory");
-    const int v = tid + i * THREADS;
-    if (v < vecs) {
-      const uint4 y = ring[i % STREAM * THREADS + tid];
-      const float most = top_of(y, -INFINITY, T());
-      top = max_nan(top, most);
-      if (k && most >= floor) {
-        const uint32_t word[4] = {y.x, y.y, y.z, y.w};
+  for (int i0 = 0; i0 < turns; i0 += STREAM) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const float x = sizeof(T) == 4 ? __uint_as_float(word[j % 4])
-                                         : __uint_as_float(j & 1 ? word[j / 2 % 4] & 0xffff0000u : word[j / 2 % 4] << 16);
-          if (x >= floor) add(x, head + v * PER + j);
+    for (int j = 0; j < STREAM; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STREAM - 1) : "memory");
+      const uint4* at = ring + j * THREADS + tid;
+      const int v = tid + (i0 + j) * THREADS;
+      if (v < vecs) {
+        const uint4 y = *at;
+        const float most = top_of(y, -INFINITY, T());
+        top = max_nan(top, most);
+        if (most >= floor) {
+          const uint32_t word[4] = {y.x, y.y, y.z, y.w};
+          uint32_t hits = 0;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const float x = __uint_as_float(sizeof(T) == 4 ? word[e % 4]
+                                            : e & 1 ? word[e / 2 % 4] & 0xffff0000u : word[e / 2 % 4] << 16);
+            hits |= x >= floor ? 1u << e : 0u;
+          }
+          uint32_t to = atomicAdd(&sh.count, (uint32_t)__popc(hits));
+          for (; hits; hits &= hits - 1, ++to) {
+            const int e = __ffs(hits) - 1;
+            const float x = to_f32(reinterpret_cast<const T*>(at)[e]);
+            if (to < STREAM_LIST) list[to] = (u64)order_key(x) << 32 | (0xffffffffu - (uint32_t)(head + v * PER + e));
+          }
         }
       }
+      ask(j, i0 + j + STREAM);
     }
-    ask(i + STREAM);
-    if (k && i % STREAM == STREAM - 1) {
+    if (k) {
       if (__syncthreads_or(*(volatile uint32_t*)&sh.count > STREAM_FULL)) {
         if (sh.count > STREAM_LIST) {
           k = 0;  // (the same everywhere)
+          floor = INFINITY;
         } else {
           floor = raise_border(sh, list, k, floor);
         }
