@@ -96,3 +96,13 @@ def test_oracle_is_attention_over_both_and_joins():
         assert np.allclose(got, out, rtol=0, atol=1e-12)
     none, ln, _ = S.attention(q, p, pv, 0, k, v, [0, 0], K, False)
     assert not none.any() and (ln == -np.inf).all()
+
+
+def test_work_beyond_31_bits_is_refused(pk):  # noqa: F811
+    """What a bf16 call divides among CTAs is counted in 32 bits; a call that is larger is refused, by the
+    workspace's size too, and one that is not is taken."""
+    size, call = pk.lib().peagle_decode_attention_shared_workspace, pk.lib().peagle_decode_attention_shared
+    most = dict(dtype=1, batch=4096, K=8, nq=64, nkv=64, hd=64, pcap=1 << 24, cap=1 << 20)
+    assert size(*most.values()) == pk.PEAGLE_ERR_UNSUPPORTED
+    assert call(*{**CALL, **most, "out": 1 << 60}.values(), None) == pk.PEAGLE_ERR_UNSUPPORTED
+    assert size(*{**most, "batch": 64}.values()) > 0 and size(*{**most, "dtype": 0}.values()) > 0
