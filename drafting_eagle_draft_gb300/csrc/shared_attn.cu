@@ -10,7 +10,8 @@
 // fp32 (fma): a CTA takes 32 rows of a kv head and a piece of the slots, in tiles of 64.  A warp
 // has 8 rows; for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
 // shared memory), for the outputs head_dim / 32 dims.  What bounds it is shared memory: as many
-// wavefronts of loads as cycles of products.
+// wavefronts of loads as cycles of products.  (2 requests of 10 rows x 2 kv heads of 64 over 128 shared and 16
+// own slots: 13.8 us in two launches, of which no more than 4 are the work.)
 #include "shared_attn.cuh"
 
 namespace peagle {

@@ -9,17 +9,28 @@
 // piece leaves its sums in the workspace, in a place of its unit (the piece with the first tile) or
 // of its CTA (a continued unit, one a CTA at most), and the join adds them up.
 //
-// A CTA has two groups of 128 softmax threads, a thread a row, and one thread each that issues
-// copies and products.  For a pair the groups have a row tile each; otherwise both have the same
-// rows and take alternate slot tiles.  Per tile and group
+// A CTA has two groups of 128 softmax threads, a thread a row, a warp that issues copies (keys, values and
+// queries by tensor maps) and a warp of products for each group: 352 threads.  For a pair the groups have a row
+// tile each; otherwise both have the same rows and take alternate slot tiles.  Per tile and group
 //   S = Q K^T   tcgen05.mma M = 128 rows, N = 128 slots, into the group's columns of tensor memory
-//   softmax     the thread reads its row of S, raises its reference only when the row's maximum
-//               passes it by 2^8 (the weights then stay within 2^8 and the row of O is scaled in
-//               place, rarely), and stores the weights as bf16 over the scores
+//   softmax     one pass over the thread's row of S: weights 2^(s - m) at the reference m that the tiles before
+//               left, as bf16 into tensor memory, with the row's maximum on the way.  A maximum up to 2^8 above m
+//               leaves it; up to 2^32 above it m moves after the tile (the row of O is scaled in place); beyond
+//               that, and in a row's first tile, the weights are computed again.  2^8 to 2^32 are far inside
+//               what bf16 weights, fp32 sums and O hold.
 //   O += P V    tcgen05.mma with P from tensor memory and V as it lies (MN-major)
-// While one group is in its softmax the products of the other run.  Weights are rounded to bf16
-// (2^-8 of each, as the draft pass does: the value operand is bf16, and both operands have one
-// type); their sum is that of the unrounded ones, in fp32.
+// At head_dim 64 the weights have columns of their own and the scores of the next tile are computed while this
+// one's weights are; at 128 tensor memory is full and they lie over the scores.  Weights are rounded to bf16
+// (2^-8 of each, as the draft pass does: the value operand is bf16, and both operands have one type); their sum
+// is that of the unrounded ones, in fp32.
+//
+// What bounds it.  64 rows x 8 kv heads of 64, 64 requests over 8192 shared slots and up to 1023 of their own:
+// 182 us, 73 GFLOP (38 us of products, 58 of exponentials at the unit's rate): a pair's tile takes 2.1 us, the
+// chain score -> weights -> product of its two groups, and the join about 20.  Measured on the way: products by
+// one thread of one warp 223; scores in two passes (maximum, then weights) 200; 252 without queries by tensor
+// copies and with one warp of products.  One token of 16 requests over 131071 slots at head_dim 128: 98 us, 605
+// MB, 89 at the rate of a copy.  4 requests over 4096: 21 us, of which 2.5 pass before the first tile (plan,
+// descriptors, the first copies) and 5 in the join's launch.
 //
 // Values that a row does not see never reach it: slots behind the last visible one are cleared in
 // shared memory before the product, and in the slots that only some rows see (a draft block) values

@@ -11,6 +11,12 @@
 // entry's index (plus 1) to its target token's place in the shared memory of the CTA that has that
 // token's chunk.  p and q are whole numbers of 2^-63: weight x 2^127 / total, whose top 64 bits one
 // multiplication gives.
+//
+// What bounds it.  One request, 8 drafts, 201088 target and 32000 draft tokens: 37 us, of which 20 are the
+// first launch; the second is a chain of a cluster's passes (accept, the rejected row's record, the draft row's
+// lookup, one draw).  The lookup is shared out and asks a bit a token first (16384 bits, hashed): by one CTA with
+// a binary search for each token it was 59 us.  64 requests of the same: 102 us for 240 MB (35 at the
+// rate of a copy), 87 of them the first launch.
 #include "sample.cuh"
 
 namespace peagle {
