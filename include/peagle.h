@@ -699,15 +699,16 @@ int64_t peagle_verify_sample_workspace(int32_t batch, int32_t K, int32_t vocab);
  * A row that sees no slot gives zeros (and -inf).  What lies in slots that a row does not see never
  * reaches it, NaN included; a value that is not finite in a slot that it does see makes that dim of
  * the row not finite.  fp32 scores, softmax, accumulation and lse; softmax weights of bf16 calls are
- * rounded to bf16, as in the draft pass.  Results are the same on every call with the same lengths
- * and sizes (no atomics).
+ * rounded to bf16, as in the draft pass.  Values up to 2^70 in size (fp32 calls: 2^102) cannot overflow
+ * on the way, larger ones may.  Results are the same on every call with the same lengths and sizes (no
+ * atomics).
  * prefix_len outside 0 .. prefix_capacity, or a request with seq_lens[b] < 0 or whose last row's slot is
  * beyond the capacity: KV_OVERFLOW, and the rows concerned are left as they are.  Waits inside the
  * kernel are bounded; one that ran out raises TIMEOUT, and the call's results are not to be used.
  * Limits (else PEAGLE_ERR_UNSUPPORTED): head_dim 64 or 128; K * n_q_heads / n_kv_heads <= 128; batch * K *
  * n_q_heads, prefix_capacity and capacity <= 2^24; n_kv_heads <= 65535; for bf16, row tiles of 128 x slot
- * tiles of 128 (all requests' capacities among them, each with 4 more) < 2^29.  A workspace that is too small is
- * PEAGLE_ERR_CAPACITY. */
+ * tiles of 128 (all requests' capacities among them, each with 6 more) < 2^29.  A workspace that is too
+ * small is PEAGLE_ERR_CAPACITY. */
 int peagle_decode_attention_shared(int32_t dtype, int32_t batch, int32_t K, int32_t n_q_heads,
                                    int32_t n_kv_heads, int32_t head_dim, const void* q,
                                    int64_t q_stride, const void* prefix_k, const void* prefix_v,
@@ -726,8 +727,8 @@ int64_t peagle_decode_attention_shared_workspace(int32_t dtype, int32_t batch, i
 /* Failure-path drill of the waits inside peagle_decode_attention_shared's bf16 kernel, as
  * peagle_set_wait_limit_quant is for the 8-bit cache: a wait gives up after limit_ns nanoseconds (0: the
  * default of 2 s), and unreachable_wait >= 0 names one that can never succeed: 0 a copied tile's place to
- * be free again, 1 queries, 2 scores, 3 weights, 4 outputs added up, 5 scores read (head_dim 64); -1 none.  For the process's calls
- * that follow.  Returns PEAGLE_ERR_INVALID for another wait. */
+ * be free again, 1 queries, 2 scores, 3 weights, 4 outputs added up, 5 scores read (head_dim 64); -1 none.  For the
+ * process's calls that follow.  Returns PEAGLE_ERR_INVALID for another wait. */
 int peagle_set_wait_limit_shared(uint64_t limit_ns, int32_t unreachable_wait);
 
 /* Raw device error bits observed by the last peagle_status call. */

@@ -205,15 +205,29 @@ def test_verify_long_and_short_rows_side_by_side():
 # ------------------------------------------------------------------ attention: references that jump
 
 JUMPS = {"rising": [0, 4, 30, 60], "falling": [60, 30, 4, 0], "far": [0, 50, 0, 110], "low first": [-90, 0, 0, 0],
-         "up and down": [0, 12, -40, 12, 24, -100, 36, 70, 0]}
+         "steps": [0, 20, 41, 20, 62, 82, 60, 103], "up and down": [0, 12, -40, 12, 24, -100, 36, 70, 0]}
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("jumps", sorted(JUMPS))
+@pytest.mark.parametrize("jumps", sorted(set(JUMPS) - {"steps"}))
 @pytest.mark.parametrize("prefix,lens", [(1100, [3, 200]), (0, [700, 1000, 0])])
 def test_scores_that_jump_between_tiles(prefix, lens, jumps, hd, dtype):
     """Every row's scores step by up to 110 (2^159) from one stretch of 128 slots to the next."""
+    check(jumping(dtype, hd, prefix, lens, jumps))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_large_values_while_scores_jump(hd, dtype):
+    """Weights up to 2^32 meet values of 2^68 and some more before the reference follows."""
+    c = jumping(dtype, hd, 1100, [3, 200], "steps")
+    for t in (c.pv, c.v):
+        t.mul_(2.0 ** 68)
+    check(c)
+
+
+def jumping(dtype, hd, prefix, lens, jumps):
     c = Call(dtype, len(lens), 4, 8, 2, hd, prefix, lens)
     way = torch.zeros(hd, device="cuda", dtype=c.q.dtype)
     way[::2] = 1.0
@@ -225,4 +239,4 @@ def test_scores_that_jump_between_tiles(prefix, lens, jumps, hd, dtype):
         if n:
             add = torch.tensor([steps[i // 128 % len(steps)] for i in range(n)], device="cuda") * unit
             t += (add[:, None] * way.float()).to(t.dtype)
-    check(c)
+    return c
