@@ -69,7 +69,7 @@ struct Shared {
   uint32_t red32[WARPS];
   Locate find;
   uint32_t top;          // this CTA's largest key (all ones: a NaN)
-  u64 sum;               // this CTA's weights
+  uint32_t heads, tails; // tokens before the border's bins, and behind them
   uint32_t count;        // of the list
   uint32_t first;        // lowest index of the largest logit
   // what one thread finds for all
@@ -421,6 +421,46 @@ __device__ void cut(Shared& sh, const Row<T>& row, const Scale& s, const Table& 
   __syncthreads();
 }
 
+// Sums f over the logits of this warp's span that take(i, x) wants, 32 of them at a time: a weight is 60
+// instructions and the question whether it is wanted 20.  buf: 64 numbers for each warp.  f(x, in): every lane
+// calls it.
+template <typename T, typename Take, typename F>
+__device__ __forceinline__ u64 sum_wanted(float* buf, const Row<T>& row, Take take, F f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, span = span_of(row.n);
+  const int end = min(row.n, (warp + 1) * span);
+  buf += warp * 64;
+  int from = 0, have = 0;
+  u64 sum = 0;
+  for (int i = warp * span; i < end; i += 128) {
+    float x[4];
+    bool is[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = i + 32 * k + lane;
+      x[k] = at < end ? to_f32(row.x[at]) : -INFINITY;
+      is[k] = at < end && take(at, x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t all = __ballot_sync(0xffffffffu, is[k]);
+      if (is[k]) buf[(from + have + __popc(all & ((1u << lane) - 1))) & 63] = x[k];
+      have += __popc(all);
+      if (have < 32) continue;  // (the same in the whole warp)
+      __syncwarp();
+      sum += f(buf[(from + lane) & 63], true);
+      __syncwarp();
+      from ^= 32;
+      have -= 32;
+    }
+  }
+  if (have) {
+    __syncwarp();
+    sum += f(lane < have ? buf[(from + lane) & 63] : -INFINITY, lane < have);
+    __syncwarp();
+  }
+  return warp_sum64(sum);
+}
+
 // The weights before which a token is kept: top_p of the mass, at least the first token's.
 __device__ __forceinline__ u64 part_of(float top_p, u64 mass) {
   bool more;
@@ -696,7 +736,8 @@ __device__ __forceinline__ void reset(Shared& sh) {
   if (threadIdx.x == 0) {
     sh.top = 0;
     sh.lowest = 0xffffffffu;
-    sh.sum = 0;
+    sh.heads = 0;
+    sh.tails = 0;
     sh.count = 0;
     sh.first = 0xffffffffu;
     sh.least = 0;
@@ -844,22 +885,22 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
       __syncthreads();
     } else if (!by_k) {
       // S and the counts over y, from which follow the bins that the border can lie in
-      u64 sum = 0;
-      for (int i = (tid & ~31) * 4 + lane; i < row.n + lane; i += 4 * THREADS) {
-        float x[4];
+      sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
+        constexpr int N = decltype(count)::value;
+        float x[N];
+        u64 sum = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[k] = i + 32 * k < row.n ? to_f32(row.x[i + 32 * k]) : -INFINITY;
-          if (i + 32 * k < row.n) atomicAdd(&sh.hist[bin_of(x[k], s)].x, 1u);
+        for (int k = 0; k < N; ++k) {
+          x[k] = i0 + 32 * k < row.n ? to_f32(row.x[i0 + 32 * k]) : -INFINITY;
+          if (i0 + 32 * k < row.n) atomicAdd(&sh.hist[bin_of(x[k], s)].x, 1u);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum += weight(x[k], s, tab);
-      }
-      sum = warp_sum64(sum);
-      if (lane == 0) atomicAdd(&sh.sum, sum);
+        for (int k = 0; k < N; ++k) sum += weight(x[k], s, tab);
+        return sum;
+      });
       __syncthreads();
       cluster_barrier();
-      for (int c = 0; c < ctas; ++c) mass += remote_u64(&sh.sum, c);
+      mass = total_of(sh.find, ctas);
       merge_bins(sh, ctas, tokens, w);
       want = part_of(top_p, mass);
       border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
@@ -954,7 +995,20 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
       const uint32_t least = sh.least;
       const int last = sh.last;
       int bin0 = sh.bin0, bin1 = sh.bin1;
-      u64 had;  // what this warp's span has before the border's bins
+      float* buf = reinterpret_cast<float*>(sh.list);
+      const int warp = tid >> 5;
+      // what this warp's span has in all, and before the border's bins: that itself, or what is not behind
+      // them, whichever are fewer tokens
+      const u64 whole = sh.find.sums[warp];
+      u64 had;
+      const uint32_t heads = __reduce_add_sync(0xffffffffu, tid < bin0 ? tokens : 0);
+      const uint32_t tails = __reduce_add_sync(0xffffffffu, tid > bin1 ? tokens : 0);
+      if (lane == 0) {
+        atomicAdd(&sh.heads, heads);
+        atomicAdd(&sh.tails, tails);
+      }
+      __syncthreads();
+      bool behind = sh.tails < sh.heads;
       while (true) {
         // what lies before those bins, by the warps' spans, and a histogram over the keys in them
         const uint32_t low = lowest_key(s, bin1), high = highest_key(s, bin0);
@@ -962,35 +1016,25 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
         cluster_barrier();  // (the histogram is read no more)
         sh.hist[tid] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
-          constexpr int N = decltype(count)::value;
-          float x[N];
-          int bin[N];
-          bool any = false;
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const int i = i0 + 32 * k;
-            x[k] = i < row.n ? to_f32(row.x[i]) : -INFINITY;
-            bin[k] = i < row.n && kept(order_key(x[k]), row.base + i, least, last) ? bin_of(x[k], s) : BINS;
-            any |= bin[k] <= bin1;
-          }
-          if (!__any_sync(0xffffffffu, any)) return 0;
-          u64 sum = 0, wx[N];
-#pragma unroll
-          for (int k = 0; k < N; ++k) wx[k] = weight(x[k], s, tab);
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            if (bin[k] < bin0)
-              sum += wx[k];
-            else if (bin[k] <= bin1)
-              add_bin(&sh.hist[(high - order_key(x[k])) >> shift], wx[k], true);
-          }
-          return sum;
-        });
+        const u64 sum = sum_wanted(
+            buf, row,
+            [&](int i, float x) {
+              const int bin = bin_of(x, s);
+              return (behind ? bin >= bin0 : bin <= bin1) && kept(order_key(x), row.base + i, least, last);
+            },
+            [&](float x, bool in) -> u64 {
+              const u64 wx = weight(x, s, tab);
+              if (!in) return 0;
+              const int bin = bin_of(x, s);
+              const bool border = bin >= bin0 && bin <= bin1;
+              if (border) add_bin(&sh.hist[(high - order_key(x)) >> shift], wx, true);
+              return behind || !border ? wx : 0;
+            });
+        had = behind ? whole - sum : sum;
+        if (lane == 0) sh.find.sums[warp] = had;
         __syncthreads();
         cluster_barrier();
         const u64 before = total_of(sh.find, ctas);
-        had = lane == 0 ? sh.find.sums[tid >> 5] : 0;
         merge_bins(sh, ctas, tokens, w);
         find_bin(sh, tokens, w, true, 0xffffffffu, 0);  // all of them
         const uint32_t in_n = sh.before_n + sh.in_n;
@@ -1001,20 +1045,25 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
         }
         bin0 = 0;  // (not reached: the bounds hold but for roundings that they allow for)
         bin1 = BINS - 1;
+        behind = false;
       }
       certain = min_key <= sh.least;
       if (certain) {  // and the kept ones of the border's bins
         const uint32_t new_least = sh.least;
         const int new_last = sh.last;
         __syncthreads();
-        sum_spans(sh.find, row.n, [&](auto count, int i0) -> u64 {
-          return weights(count, i0, s, tab, [&](int i, float& x) {
-            x = i < row.n ? to_f32(row.x[i]) : -INFINITY;
-            const int bin = bin_of(x, s);
-            return i < row.n && bin >= bin0 && bin <= bin1 && kept(order_key(x), row.base + i, new_least, new_last);
-          });
-        });
-        if (lane == 0) sh.find.sums[tid >> 5] += had;
+        cluster_barrier();  // (the lists are read no more)
+        const u64 sum = sum_wanted(
+            buf, row,
+            [&](int i, float x) {
+              const int bin = bin_of(x, s);
+              return bin >= bin0 && bin <= bin1 && kept(order_key(x), row.base + i, new_least, new_last);
+            },
+            [&](float x, bool in) -> u64 {
+              const u64 wx = weight(x, s, tab);
+              return in ? wx : 0;
+            });
+        if (lane == 0) sh.find.sums[warp] = had + sum;
       }
     }
   }
