@@ -58,6 +58,7 @@ struct Args {
 struct Shared {
   union {
     uint4 hist[BINS];    // count, and three 16-bit parts of the weights
+    uint32_t counts[BINS];  // counts alone (side by side: 32 banks, not 8)
     struct {
       u64 all[LIST];     // the cluster's list
       u64 weight[LIST];
@@ -208,6 +209,13 @@ __device__ __forceinline__ void merge_bins(Shared& sh, int ctas, uint32_t& n, u6
   }
 }
 
+// Of counts alone.
+__device__ __forceinline__ uint32_t merge_counts(Shared& sh, int ctas) {
+  uint32_t n = 0;
+  for (int c = 0; c < ctas; ++c) n += ctas > 1 ? remote_u32(&sh.counts[threadIdx.x], c) : sh.counts[threadIdx.x];
+  return n;
+}
+
 // Finds the first bin at which the running count reaches `want_n` (by_count), or the running weight
 // want_w, and what lies before and in it (into sh; the last bin if none does).
 __device__ __forceinline__ void find_bin(Shared& sh, uint32_t n, u64 w, bool by_count, uint32_t want_n,
@@ -251,16 +259,14 @@ __device__ uint32_t border_key(Shared& sh, int ctas, const uint32_t (&key)[PER],
     const int shift = key_shift(low, high);
     __syncthreads();
     if (ctas > 1) cluster_barrier();  // (the bins are read no more)
-    sh.hist[tid].x = 0;
+    sh.counts[tid] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (key[i] && key[i] >= low && key[i] <= high) atomicAdd(&sh.hist[(high - key[i]) >> shift].x, 1u);
+      if (key[i] && key[i] >= low && key[i] <= high) atomicAdd(&sh.counts[(high - key[i]) >> shift], 1u);
     __syncthreads();
     if (ctas > 1) cluster_barrier();
-    uint32_t n = 0;
-    for (int c = 0; c < ctas; ++c) n += ctas > 1 ? remote_u32(&sh.hist[tid].x, c) : sh.hist[tid].x;
-    find_bin(sh, n, 0, true, k - before, 0);
+    find_bin(sh, merge_counts(sh, ctas), 0, true, k - before, 0);
     if (before + sh.before_n + sh.in_n < k) break;
     before += sh.before_n;
     high -= (uint32_t)sh.bin << shift;
@@ -892,7 +898,7 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           x[k] = i0 + 32 * k < row.n ? to_f32(row.x[i0 + 32 * k]) : -INFINITY;
-          if (i0 + 32 * k < row.n) atomicAdd(&sh.hist[bin_of(x[k], s)].x, 1u);
+          if (i0 + 32 * k < row.n) atomicAdd(&sh.counts[bin_of(x[k], s)], 1u);
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) sum += weight(x[k], s, tab);
@@ -901,7 +907,7 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
       __syncthreads();
       cluster_barrier();
       mass = total_of(sh.find, ctas);
-      merge_bins(sh, ctas, tokens, w);
+      tokens = merge_counts(sh, ctas);
       want = part_of(top_p, mass);
       border_bins(sh, tokens, (float)want * exp2f((float)-frac), (float)(mass - want) * exp2f((float)-frac));
       const int bin1 = sh.bin1;
@@ -962,13 +968,13 @@ __device__ __forceinline__ void sample_together(const Args& a, Shared& sh, uint4
     }
     // long
     if (by_k) {
-      sh.hist[tid] = make_uint4(0, 0, 0, 0);
+      sh.counts[tid] = 0;
       __syncthreads();
 #pragma unroll 4
-      for (int i = tid; i < row.n; i += THREADS) atomicAdd(&sh.hist[bin_of(to_f32(row.x[i]), s)].x, 1u);
+      for (int i = tid; i < row.n; i += THREADS) atomicAdd(&sh.counts[bin_of(to_f32(row.x[i]), s)], 1u);
       __syncthreads();
       cluster_barrier();
-      merge_bins(sh, ctas, tokens, w);
+      tokens = merge_counts(sh, ctas);
       find_bin(sh, tokens, 0, true, (uint32_t)top_k, 0);
       const int bin = sh.bin;
       const uint32_t before = sh.before_n;
