@@ -14,18 +14,19 @@
 //   long    Otherwise the border is found over the whole row.  The bins that it can be in are divided by
 //           the logits' own order, counts and weights (in 16-bit parts, so that 32-bit additions hold)
 //           summed over the cluster, until RANK tokens are left, which are ranked; what lies before
-//           those bins is added up on the way for each warp's span of the row, and the span in which
-//           u S falls is divided again.
+//           those bins is added up on the way for each warp's span of the row (itself, or as the rest of
+//           what lies behind them), and the span in which u S falls is divided again.
 // With top-k and more rows than run at once, a cluster takes as many rows as it has CTAs: a row passes by one
 // CTA, which keeps its first tokens only, and the cluster then takes the rows for which that is not enough.
 // Sums are whole numbers (sample.cuh), so nothing depends on their order.
 //
 // What bounds it.  A few rows: the chain of a cluster's steps (4 rows of 4096 with top-k: 14 us; 8 rows of 32000
-// with top-p: 20).  Rows without top-k: the instructions of a weight, 60 to 75 a logit (16 fp32 rows of 201088 at
-// temperature 1.6 with top-p: 94 us, issue bound).  Many rows with top-k: instructions again, the list and
-// about 60 for 16 bytes a thread (288 bf16 rows of 201088, top-k 100: 41 us, 116 MB, 17 at the rate of a copy;
-// 61 % of issue slots, DRAM 31 %).  Kept in the shared memory of clusters of 4, 199 such rows with top-k 50 take 56
-// us, passing by 39, and 512 fp32 rows of 32000 took 77 for 50.
+// with top-p: 18).  Rows without top-k: the instructions, 60 to 75 a weight, of which the first pass wants one
+// of every logit and the later ones of those at the border and on its smaller side (16 fp32 rows of 201088 at
+// temperature 1.6 with top-p: 80 us; 94 with every weight in every pass).  Many rows with top-k: instructions again,
+// the list and about 60 for 16 bytes a thread (288 bf16 rows of 201088, top-k 100: 41 us, 116 MB, 17 at the rate of a
+// copy; 61 % of issue slots, DRAM 31 %).  Kept in the shared memory of clusters of 4, 199 such rows with top-k 50 take
+// 56 us, passing by 39, and 512 fp32 rows of 32000 took 77 for 50.
 #include "sample.cuh"
 
 namespace peagle {
