@@ -11,8 +11,10 @@
 // has 8 rows; for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
 // shared memory), for the outputs head_dim / 32 dims.  What bounds it is shared memory: as many
 // wavefronts of loads as cycles of products.  (2 requests of 10 rows x 2 kv heads of 64 over 128 shared and 16
-// own slots: 13.8 us in two launches, of which no more than 4 are the work.)
+// own slots: 13.4 us in two launches, of which no more than 4 are the work.)  With fewer than 25 rows some of a CTA's
+// warps only load: one row of 2 requests over 65536 slots of 8 heads of 128 takes 282 us for 537 MB.
 #include "shared_attn.cuh"
+#include "tc_ptx.cuh"
 
 namespace peagle {
 namespace sha {
@@ -36,6 +38,7 @@ template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS) simt_kernel(Args a, Pieces pc) {
   constexpr int KS = HD + 4, DL = HD / 32;
   extern __shared__ float smem[];
+  tc::pdl_launch_dependents();
   float* sq = smem;                // [ROWS][HD]
   float* sk = sq + ROWS * HD;      // [KEYS][KS]
   float* sv = sk + KEYS * KS;      // [KEYS][HD]
@@ -178,10 +181,12 @@ __global__ void __launch_bounds__(SIMT_THREADS) simt_kernel(Args a, Pieces pc) {
   }
 }
 
-// Joins the pieces of a row and head; a warp each.
+// Joins the pieces of a row and head; a warp each.  What bounds it is the latency of its loads: eight pieces at once
+// (8 requests of 4 rows over 20000 slots: 122 us for the call with one after another, 65 so).
 template <int HD>
 __global__ void __launch_bounds__(256) simt_join_kernel(Args a, Pieces pc) {
   constexpr int DL = HD / 32;
+  tc::pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t x = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int row = (int)(x / a.nq), head = (int)(x % a.nq);
@@ -193,14 +198,35 @@ __global__ void __launch_bounds__(256) simt_join_kernel(Args a, Pieces pc) {
   const Stat* stat = reinterpret_cast<const Stat*>(a.part);
   const float* sums = a.part + 2 * part_at(a, pc.shared + pc.own, 0, 0);
   float m = -INFINITY, l = 0.f, o[DL] = {};
-  for (int p = 0; p < pc.shared + pc.own; ++p) {
-    const size_t i = part_at(a, p, row, head);
-    const Stat s = stat[i];
-    if (s.l == 0.f) continue;
-    const float top = fmaxf(m, s.m), c = exp2f(m - top), w = exp2f(s.m - top);
-    l = l * c + s.l * w;
+  constexpr int AT_ONCE = 8;  // (loads in flight)
+  const int n = pc.shared + pc.own;
+  for (int p0 = 0; p0 < n; p0 += AT_ONCE) {
+    Stat s[AT_ONCE];
+    float y[AT_ONCE][DL], top = m;
 #pragma unroll
-    for (int d = 0; d < DL; ++d) o[d] = fmaf(o[d], c, w * sums[i * HD + lane * DL + d]);
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const size_t i = part_at(a, min(p0 + k, n - 1), row, head);
+      s[k] = stat[i];
+#pragma unroll
+      for (int d = 0; d < DL; ++d) y[k][d] = sums[i * HD + lane * DL + d];
+    }
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      if (p0 + k >= n) s[k] = {-INFINITY, 0.f};
+      top = fmaxf(top, s[k].m);
+    }
+    const float ref = top == -INFINITY ? 0.f : top, c = exp2f(m - ref);
+    l *= c;
+#pragma unroll
+    for (int d = 0; d < DL; ++d) o[d] *= c;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const float w = exp2f(s[k].m - ref);
+      if (s[k].l == 0.f) continue;  // (it saw no slot)
+      l = fmaf(s[k].l, w, l);
+#pragma unroll
+      for (int d = 0; d < DL; ++d) o[d] = fmaf(w, y[k][d], o[d]);
+    }
     m = top;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -230,8 +256,10 @@ int launch_simt(const Args& a, cudaStream_t st) {
                        (int64_t)a.batch * cdiv(a.K * a.G, ROWS) * pc.own;
   simt_kernel<HD><<<dim3((unsigned)ctas, a.nkv), SIMT_THREADS, smem, st>>>(a, pc);
   const int64_t warps = (int64_t)a.batch * a.K * a.nq;
-  simt_join_kernel<HD><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a, pc);
-  return cudaGetLastError() == cudaSuccess ? PEAGLE_OK : PEAGLE_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
+  return launch_pdl(simt_join_kernel<HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a, pc) == cudaSuccess
+             ? PEAGLE_OK
+             : PEAGLE_ERR_CUDA;
 }
 
 int64_t workspace(int dtype, int64_t batch, int K, int nq, int nkv, int hd, int pcap, int cap) {
