@@ -7,12 +7,12 @@
 // part is cut along its slots into pieces, each with its own reference and sum, and a second
 // kernel joins a row's pieces.
 //
-// fp32 (fma): a CTA takes 32 rows of a kv head and a piece of the slots, in tiles of 64.  A warp
-// has 8 rows; for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
+// fp32 (fma): a CTA takes 32 rows of a kv head (or 16, or 8) and a piece of the slots, in tiles of 64.
+// A warp has 8 rows (4, 2); for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
 // shared memory), for the outputs head_dim / 32 dims.  What bounds it is shared memory: as many
 // wavefronts of loads as cycles of products.  (2 requests of 10 rows x 2 kv heads of 64 over 128 shared and 16
-// own slots: 13.4 us in two launches, of which no more than 4 are the work.)  With fewer than 25 rows some of a CTA's
-// warps only load: one row of 2 requests over 65536 slots of 8 heads of 128 takes 282 us for 537 MB.
+// own slots: 13 us in two launches, of which no more than 4 are the work.)  A tile's loads are overlapped
+// by other CTAs of the SM only: one row of 2 requests over 65536 slots of 8 heads of 128, 252 us for 537 MB.
 #include "shared_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -21,7 +21,12 @@ namespace sha {
 
 namespace {
 
-constexpr int ROWS = 32, KEYS = 64, SIMT_THREADS = 128, RW = 8;  // RW: rows a warp
+constexpr int KEYS = 64, SIMT_THREADS = 128;
+// Rows a warp, RW: 8, or as many as give each of the four warps some where the whole batch has few rows of a kv
+// head (with 8 the other warps only load: one request's row of 2 heads over 133 slots 11.8 us for 6.7, 8 rows over
+// 4096 20.5 for 15.9, over 65536 of 8 heads of 128 281 for 252; and 16 rows there with 2 a warp, the slots read
+// twice, 404 for 330).
+inline int rows_a_warp(int64_t all) { return all <= 8 ? 2 : all <= 16 ? 4 : 8; }
 constexpr float LOG2E = 1.44269504f;
 
 // Pieces of a row: `shared` of the prefix, then `own`.
@@ -34,9 +39,9 @@ __device__ __forceinline__ size_t part_at(const Args& a, int piece, int row, int
   return ((size_t)piece * a.batch * a.K + row) * a.nq + head;
 }
 
-template <int HD>
+template <int HD, int RW>
 __global__ void __launch_bounds__(SIMT_THREADS) simt_kernel(Args a, Pieces pc) {
-  constexpr int KS = HD + 4, DL = HD / 32;
+  constexpr int KS = HD + 4, DL = HD / 32, ROWS = SIMT_THREADS / 32 * RW;
   extern __shared__ float smem[];
   tc::pdl_launch_dependents();
   float* sq = smem;                // [ROWS][HD]
@@ -238,28 +243,37 @@ __global__ void __launch_bounds__(256) simt_join_kernel(Args a, Pieces pc) {
 
 // Pieces, so that the CTAs fill the GPU's 304 places a few times, of at least two tiles each.
 Pieces simt_pieces(int batch, int K, int G, int nkv, int pcap, int cap) {
+  const int rows = SIMT_THREADS / 32 * rows_a_warp((int64_t)batch * K * G);
   const auto cut = [](int64_t ctas, int slots) {
     const int64_t most = slots / (2 * KEYS) + 1, want = (4 * 304 + ctas - 1) / ctas;
     return (int)(want < most ? want : most);
   };
-  const int64_t shared = (int64_t)cdiv(batch * K * G, ROWS) * nkv;
-  const int64_t own = (int64_t)batch * cdiv(K * G, ROWS) * nkv;
+  const int64_t shared = (int64_t)cdiv(batch * K * G, rows) * nkv;
+  const int64_t own = (int64_t)batch * cdiv(K * G, rows) * nkv;
   return {cut(shared, pcap), cut(own, cap)};
 }
 
-template <int HD>
-int launch_simt(const Args& a, cudaStream_t st) {
+template <int HD, int RW>
+int launch_simt_rows(const Args& a, cudaStream_t st) {
+  constexpr int ROWS = SIMT_THREADS / 32 * RW;
   const Pieces pc = simt_pieces(a.batch, a.K, a.G, a.nkv, a.pcap, a.cap);
   const size_t smem = (ROWS * HD + KEYS * (HD + 4) + KEYS * HD + ROWS * KEYS) * sizeof(float);
-  if (smem_optin((const void*)simt_kernel<HD>, smem) != cudaSuccess) return PEAGLE_ERR_CUDA;
+  if (smem_optin((const void*)simt_kernel<HD, RW>, smem) != cudaSuccess) return PEAGLE_ERR_CUDA;
   const int64_t ctas = (int64_t)cdiv(a.batch * a.K * a.G, ROWS) * pc.shared +
                        (int64_t)a.batch * cdiv(a.K * a.G, ROWS) * pc.own;
-  simt_kernel<HD><<<dim3((unsigned)ctas, a.nkv), SIMT_THREADS, smem, st>>>(a, pc);
+  simt_kernel<HD, RW><<<dim3((unsigned)ctas, a.nkv), SIMT_THREADS, smem, st>>>(a, pc);
   const int64_t warps = (int64_t)a.batch * a.K * a.nq;
   if (cudaGetLastError() != cudaSuccess) return PEAGLE_ERR_CUDA;
   return launch_pdl(simt_join_kernel<HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, a, pc) == cudaSuccess
              ? PEAGLE_OK
              : PEAGLE_ERR_CUDA;
+}
+template <int HD>
+int launch_simt(const Args& a, cudaStream_t st) {
+  const int rows = rows_a_warp((int64_t)a.batch * a.K * a.G);
+  return rows == 2   ? launch_simt_rows<HD, 2>(a, st)
+         : rows == 4 ? launch_simt_rows<HD, 4>(a, st)
+                     : launch_simt_rows<HD, 8>(a, st);
 }
 
 int64_t workspace(int dtype, int64_t batch, int K, int nq, int nkv, int hd, int pcap, int cap) {
