@@ -10,8 +10,8 @@
 // fp32 (fma): a CTA takes 32 rows of a kv head (or 16, or 8) and a piece of the slots, in tiles of 64.
 // A warp has 8 rows (4, 2); for the scores a lane has two slots (8 x 2 sums, the rows' queries broadcast from
 // shared memory), for the outputs head_dim / 32 dims.  What bounds it is shared memory: as many
-// wavefronts of loads as cycles of products.  (2 requests of 10 rows x 2 kv heads of 64 over 128 shared and 16
-// own slots: 13 us in two launches, of which no more than 4 are the work.)  A tile's loads are overlapped
+// wavefronts of loads as cycles of products.  (2 requests of 8 rows x 2 kv heads of 64 over 128 shared and 5 to 16
+// own slots: 8.8 us in two launches; 13.4 before every warp had rows.)  A tile's loads are overlapped
 // by other CTAs of the SM only: one row of 2 requests over 65536 slots of 8 heads of 128, 252 us for 537 MB.
 #include "shared_attn.cuh"
 #include "tc_ptx.cuh"
